@@ -529,7 +529,7 @@ herald_status herald_debug_status(uint32_t* code) {
 #ifdef HERALD_DEBUG
   HERALD_TRY_CUDA(cudaDeviceSynchronize(), "device synchronize");
   *code = debug_take_select() | debug_take_tc() | debug_take_move() | debug_take_blocks() |
-          debug_take_flash();
+          debug_take_flash() | debug_take_kv4_move() | debug_take_kv4_attn();
 #endif
   return HERALD_OK;
 }
@@ -631,6 +631,161 @@ herald_status herald_select_exact(herald_dims dims, const uint16_t* q_block,
   HERALD_TRY_CUDA(launch_topk_union(dims, ctx_len, cand, n_cand, s, 1, K, K, sink, local, P_max,
                                     idx, n_sel, st),
                   "union launch");
+  return HERALD_OK;
+}
+
+// The rules of herald_kv4 and its device form.
+static herald_status check_kv4(const herald_dims& dm, const herald_kv4* c, Kv4Dev* out) {
+  if (!c) return fail(HERALD_ERR_INVALID_ARG, "cache is NULL");
+  int log2 = 4;
+  while (log2 < 7 && (1 << log2) != c->page) ++log2;
+  if ((1 << log2) != c->page)
+    return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "page %d not in {16, 32, 64, 128}", c->page);
+  if (c->n_pages < 1 || c->max_pages < 1)
+    return fail(HERALD_ERR_INVALID_ARG, "n_pages=%d, max_pages=%d must be >= 1", c->n_pages,
+                c->max_pages);
+  if ((long long)c->max_pages * c->page < dm.L_max)
+    return fail(HERALD_ERR_INVALID_ARG, "max_pages*page = %lld < L_max=%d",
+                (long long)c->max_pages * c->page, dm.L_max);
+  HERALD_CHECK_PTR(c->table);
+  HERALD_CHECK_PTR(c->k_codes);
+  HERALD_CHECK_PTR(c->k_scales);
+  HERALD_CHECK_PTR(c->v_codes);
+  HERALD_CHECK_PTR(c->v_scales);
+  const float lo = 0x1p-60f, hi = 0x1p60f;
+  if (!(c->k_scale >= lo && c->k_scale <= hi && c->v_scale >= lo && c->v_scale <= hi))
+    return fail(HERALD_ERR_INVALID_ARG, "k_scale=%g, v_scale=%g outside [2^-60, 2^60]",
+                double(c->k_scale), double(c->v_scale));
+  *out = Kv4Dev{c->table, c->k_codes, c->k_scales, c->v_codes, c->v_scales,
+                log2,     c->max_pages, c->n_pages, c->k_scale, c->v_scale};
+  return HERALD_OK;
+}
+
+static herald_status check_kv4_dims(const herald_dims& dm) {
+  HERALD_RET_IF(check_dims(dm));
+  if ((long long)dm.N * dm.Hkv > 65535)
+    return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "N*Hkv = %lld > 65535", (long long)dm.N * dm.Hkv);
+  return HERALD_OK;
+}
+
+// A token stride: 0 = dense, else a multiple of 8 that holds a token's row.
+static herald_status check_ld(const char* name, int64_t* ld, int64_t row) {
+  if (*ld == 0) *ld = row;
+  if (*ld < row || *ld % 8 != 0)
+    return fail(HERALD_ERR_INVALID_ARG, "%s=%lld must be 0 or a multiple of 8 >= %lld", name,
+                (long long)*ld, (long long)row);
+  return HERALD_OK;
+}
+
+herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, const uint16_t* q,
+                                int64_t q_ld, const uint16_t* k, int64_t k_ld, const uint16_t* v,
+                                int64_t v_ld, const herald_rope* rope, int32_t* ctx_len,
+                                const herald_kv4* cache, uint16_t* q_rot, uint16_t* k_rot,
+                                float* pooled, int Bk, unsigned flags, void* stream) {
+  g_err[0] = 0;
+  HERALD_RET_IF(check_kv4_dims(dims));
+  if (T < 1) return fail(HERALD_ERR_INVALID_ARG, "T=%d must be >= 1", T);
+  if ((long long)dims.N * T >= (1ll << 31))
+    return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "N*T too large");
+  if (flags & ~HERALD_KV4_ADVANCE) return fail(HERALD_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  if (!q && !k) return fail(HERALD_ERR_INVALID_ARG, "q and k are both NULL");
+  HERALD_CHECK_PTR(ctx_len);
+  if (n_tok) HERALD_CHECK_PTR(n_tok);
+  if (q) {
+    HERALD_CHECK_PTR(q);
+    HERALD_CHECK_PTR(q_rot);
+    HERALD_RET_IF(check_ld("q_ld", &q_ld, int64_t(dims.Hq) * dims.d));
+    if (q == q_rot && q_ld != int64_t(dims.Hq) * dims.d)
+      return fail(HERALD_ERR_INVALID_ARG, "q_rot may be q only when q is dense");
+  }
+  if (k) {
+    HERALD_CHECK_PTR(k);
+    if (k_rot || !cache) HERALD_CHECK_PTR(k_rot);
+    HERALD_RET_IF(check_ld("k_ld", &k_ld, int64_t(dims.Hkv) * dims.d));
+    if (k == k_rot && k_ld != int64_t(dims.Hkv) * dims.d)
+      return fail(HERALD_ERR_INVALID_ARG, "k_rot may be k only when k is dense");
+  }
+  Kv4Dev c{};
+  if (cache) {
+    if (!k) return fail(HERALD_ERR_INVALID_ARG, "k is NULL with a cache");
+    HERALD_CHECK_PTR(v);
+    HERALD_RET_IF(check_ld("v_ld", &v_ld, int64_t(dims.Hkv) * dims.d));
+    HERALD_RET_IF(check_kv4(dims, cache, &c));
+  } else if (pooled || flags) {
+    return fail(HERALD_ERR_INVALID_ARG, "pooled and HERALD_KV4_ADVANCE need a cache");
+  }
+  if (pooled) {
+    HERALD_CHECK_PTR(pooled);
+    if (Bk < 1 || Bk > dims.L_max)
+      return fail(HERALD_ERR_INVALID_ARG, "Bk=%d outside [1, L_max=%d]", Bk, dims.L_max);
+  }
+  if (rope) {
+    HERALD_CHECK_PTR(rope->cos_sin);
+    if (rope->rot < 32 || rope->rot > dims.d || rope->rot % 32 != 0)
+      return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "rot=%d not a multiple of 32 in [32, d=%d]",
+                  rope->rot, dims.d);
+    if (rope->n_pos < dims.L_max)
+      return fail(HERALD_ERR_INVALID_ARG, "n_pos=%d < L_max=%d", rope->n_pos, dims.L_max);
+    if (rope->interleaved != 0 && rope->interleaved != 1)
+      return fail(HERALD_ERR_INVALID_ARG, "interleaved=%d not 0 or 1", rope->interleaved);
+  }
+  HERALD_TRY_CUDA(launch_kv4_append(dims, T, n_tok, q, q_ld, k, k_ld, v, v_ld, rope, ctx_len,
+                                    cache ? &c : nullptr, q_rot, k_rot, pooled, Bk,
+                                    (flags & HERALD_KV4_ADVANCE) != 0,
+                                    static_cast<cudaStream_t>(stream)),
+                  "kv4 append launch");
+  return HERALD_OK;
+}
+
+size_t herald_workspace_size_kv4(herald_dims dims) {
+  return check_kv4_dims(dims) == HERALD_OK ? kv4_attn_workspace(dims) : 0;
+}
+
+herald_status herald_kv4_attn(herald_dims dims, const uint16_t* q, const herald_kv4* cache,
+                              const int32_t* ctx_len, const uint16_t* block_k,
+                              const uint16_t* block_v, uint16_t* out, float scale, void* ws,
+                              size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  HERALD_RET_IF(check_kv4_dims(dims));
+  HERALD_CHECK_PTR(q);
+  HERALD_CHECK_PTR(ctx_len);
+  HERALD_CHECK_PTR(out);
+  HERALD_CHECK_PTR(ws);
+  Kv4Dev c{};
+  HERALD_RET_IF(check_kv4(dims, cache, &c));
+  if ((block_k == nullptr) != (block_v == nullptr))
+    return fail(HERALD_ERR_INVALID_ARG, "block_k and block_v: both or neither");
+  if (block_k) {
+    HERALD_CHECK_PTR(block_k);
+    HERALD_CHECK_PTR(block_v);
+  }
+  if (!(scale >= 0.f) || !isfinite(scale))
+    return fail(HERALD_ERR_INVALID_ARG, "scale=%g must be finite and >= 0", double(scale));
+  const size_t need = kv4_attn_workspace(dims);
+  if (ws_bytes < need)
+    return fail(HERALD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  HERALD_TRY_CUDA(launch_kv4_attn(dims, q, c, ctx_len, block_k, block_v, out,
+                                  scale > 0.f ? scale : 1.f / sqrtf(float(dims.d)), ws, sm_count(),
+                                  static_cast<cudaStream_t>(stream)),
+                  "kv4 attention launch");
+  return HERALD_OK;
+}
+
+herald_status herald_kv4_gather(herald_dims dims, const int32_t* idx, const int32_t* n_sel,
+                                int P_max, const herald_kv4* cache, uint16_t* pool_k,
+                                uint16_t* pool_v, void* stream) {
+  g_err[0] = 0;
+  HERALD_RET_IF(check_kv4_dims(dims));
+  HERALD_RET_IF(check_pmax(dims, P_max));
+  HERALD_CHECK_PTR(idx);
+  HERALD_CHECK_PTR(n_sel);
+  HERALD_CHECK_PTR(pool_k);
+  if (pool_v) HERALD_CHECK_PTR(pool_v);
+  Kv4Dev c{};
+  HERALD_RET_IF(check_kv4(dims, cache, &c));
+  HERALD_TRY_CUDA(launch_kv4_gather(dims, idx, n_sel, P_max, c, pool_k, pool_v,
+                                    static_cast<cudaStream_t>(stream)),
+                  "kv4 gather launch");
   return HERALD_OK;
 }
 

@@ -127,6 +127,8 @@ uint32_t debug_take_tc();
 uint32_t debug_take_move();
 uint32_t debug_take_blocks();
 uint32_t debug_take_flash();
+uint32_t debug_take_kv4_move();
+uint32_t debug_take_kv4_attn();
 
 // A launch failure injected on the host (herald_inject_launch_failure, a
 // test hook of the error paths): returns the injected error for the launch
@@ -311,6 +313,30 @@ cudaError_t launch_block_scan(const herald_dims& dm, const float* pooled, const 
 cudaError_t launch_expand_blocks(const herald_dims& dm, const int32_t* cand_b,
                                  const int32_t* n_cand_b, const int32_t* ctx, int Bk,
                                  int C_blocks, int32_t* cand, int32_t* n_cand, cudaStream_t st);
+
+// ---- the paged 4-bit cache (kv4_move.cu, kv4_attn.cu; kv4.cuh)
+// The cache as the kernels take it (herald_kv4 with the page size as a shift).
+struct Kv4Dev {
+  const int32_t* table;  // [N][max_pages]
+  uint8_t *kc, *ks, *vc, *vs;
+  int page_log2, max_pages, n_pages;
+  float k_scale, v_scale;
+};
+constexpr int kKv4MaxCtas = 608;  // most attention CTAs per row tile (workspace slots)
+// q, k, v rows of one token are q_ld, k_ld, v_ld elements apart; q, k, cache
+// and the outputs may be null as herald_kv4_append allows.
+cudaError_t launch_kv4_append(const herald_dims& dm, int T, const int32_t* n_tok,
+                              const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld,
+                              const uint16_t* v, int64_t v_ld, const herald_rope* rope,
+                              int32_t* ctx, const Kv4Dev* cache, uint16_t* q_rot, uint16_t* k_rot,
+                              float* pooled, int Bk, bool advance, cudaStream_t st);
+cudaError_t launch_kv4_gather(const herald_dims& dm, const int32_t* idx, const int32_t* n_sel,
+                              int P_max, const Kv4Dev& c, uint16_t* pk, uint16_t* pv,
+                              cudaStream_t st);
+size_t kv4_attn_workspace(const herald_dims& dm);
+cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4Dev& c,
+                            const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
+                            uint16_t* out, float scale, void* ws, int num_sms, cudaStream_t st);
 
 // The append of a decoded block, done inside another kernel: the rows of
 // block[n][b][g] (bf16, [N][B][Hkv][d]) go to cache[n][g][L0 + b], rows at or

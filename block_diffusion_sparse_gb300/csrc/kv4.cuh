@@ -1,0 +1,123 @@
+// kv4.cuh -- the paged 4-bit KV cache on the device: its addresses, its
+// number formats, and how the attention kernels share out its keys.
+//
+// A row of d channels (one position of one KV head) is held as d/2 bytes of
+// e2m1 codes, two per byte with the even channel in the low half, and d/16
+// e4m3 scales, one per 16 consecutive channels:
+//   value = code * scale * (k_scale | v_scale).
+// A code has 2 and a scale 4 significant bits, so code * scale has at most 6
+// and lies in [2^-10, 2688]: it is exact in fp16.
+#pragma once
+#include "internal.cuh"
+#include "ptx.cuh"
+
+namespace herald {
+
+// The page of logical page lp of sequence n, or -1 where the table has no
+// page in range (such positions are never read or written).
+HERALD_DEV int kv4_page(const Kv4Dev& c, int n, int lp) {
+  const int p = c.table[size_t(n) * c.max_pages + lp];
+  return p >= 0 && p < c.n_pages ? p : -1;
+}
+// Row index of position pos in page `phys` (64 bits: a long cache has more
+// bytes than 32 bits count).
+HERALD_DEV size_t kv4_row(const Kv4Dev& c, int phys, int Hkv, int g, int pos) {
+  return ((size_t(phys) * Hkv + g) << c.page_log2) + (pos & ((1 << c.page_log2) - 1));
+}
+
+// Two codes (one byte in bits 0-7 of b) -> fp16 pair, low half first.
+HERALD_DEV uint32_t e2m1x2_to_half2(uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t, u0, u1, u2;\n\t"
+      "mov.b32 {t, u0, u1, u2}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+      : "=r"(r)
+      : "r"(b));
+  return r;
+}
+// The four bytes of a word of codes -> four fp16 pairs.
+HERALD_DEV void e2m1x8_to_half2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t"
+      "mov.b32 {t0, t1, t2, t3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, t0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, t1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, t2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, t3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Two scales (bits 0-15) -> fp16 pair (exact: 4 significant bits).
+HERALD_DEV uint32_t e4m3x2_to_half2(uint32_t b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(b)));
+  return r;
+}
+HERALD_DEV float e4m3_to_float(uint32_t b) {
+  const uint32_t h = e4m3x2_to_half2(b & 0xFFu);
+  return __low2float(*reinterpret_cast<const __half2*>(&h));
+}
+HERALD_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// ---- how attention CTAs share the keys
+// The keys of every (sequence, KV head) segment, in units of `unit` cache
+// positions followed by the block's own keys, are laid end to end, segments in
+// order; CTA c takes units [c*share, (c+1)*share).  Equal shares keep ragged
+// batches balanced; a CTA's range may cover the end of one segment, whole
+// segments, and the start of another (its pieces).  Piece (c, segment s) has
+// partial slot c + s: from one piece to the next c or s grows.
+struct Kv4Split {
+  int64_t total;  // units of all segments
+  int64_t share;  // units per CTA
+};
+HERALD_DEV int kv4_units(int ctx, int L_max, int unit, int blk_units) {
+  return (min(max(ctx, 0), L_max) + unit - 1) / unit + blk_units;
+}
+// Sum over the sequences of their units (per KV head); every lane of a warp
+// calls it and gets the total.
+HERALD_DEV int64_t kv4_total_units(const int32_t* ctx, int N, int L_max, int unit, int blk_units) {
+  int64_t sum = 0;
+  for (int n = int(threadIdx.x & 31); n < N; n += 32)
+    sum += kv4_units(ctx[n], L_max, unit, blk_units);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+HERALD_DEV Kv4Split kv4_split(int64_t per_head, int Hkv, int ctas, int min_share) {
+  Kv4Split s;
+  s.total = per_head * Hkv;
+  s.share = max((s.total + ctas - 1) / ctas, int64_t(min_share));
+  return s;
+}
+// The sequence that holds unit `at` (of all segments, at < total) and the
+// first unit of that sequence's first segment; called by a whole warp.
+HERALD_DEV void kv4_find(const int32_t* ctx, int N, int L_max, int unit, int blk_units, int Hkv,
+                         int64_t at, int* n_out, int64_t* first_out) {
+  const int lane = threadIdx.x & 31;
+  int64_t base = 0;
+  for (int n0 = 0; n0 < N; n0 += 32) {
+    const int n = n0 + lane;
+    const int64_t own = n < N ? int64_t(Hkv) * kv4_units(ctx[n], L_max, unit, blk_units) : 0;
+    int64_t inc = own;  // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > at);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      *n_out = n0 + l;
+      *first_out = base + __shfl_sync(0xffffffffu, inc - own, l);
+      return;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  *n_out = N;
+  *first_out = base;
+}
+
+}  // namespace herald

@@ -1,0 +1,345 @@
+// kv4_move.cu -- rows in and out of the paged 4-bit KV cache:
+//   append  rotates a block's (or a prompt's) queries and keys by their
+//           positions, quantises keys and values and writes them into the
+//           sequences' pages
+//   pool    the means of the key blocks an append touched (the block-granular
+//           stage 1's input), from the rows as the cache holds them
+//   gather  held rows at given positions as bf16 (sparse pool, candidates)
+#include "kv4.cuh"
+
+namespace herald {
+
+// max of two numbers, NaN if either is one
+HERALD_DEV float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+// fp32 -> e4m3, to nearest even, past the largest to the largest, NaN stays
+HERALD_DEV uint32_t float_to_e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+  return r & 0xFFu;
+}
+// fp32 pair -> e2m1 codes of one byte (lo in the low half), to nearest even,
+// past 6 to 6
+HERALD_DEV uint32_t float2_to_e2m1(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r;
+}
+
+// One group of 16 channels to codes and scale.  Each step is one IEEE fp32
+// operation, so the result is defined to the bit: scale = e4m3(max|x| /
+// (6 scale0)), code = e2m1(x / (scale scale0)); c6 = 6 scale0.  A quotient
+// rounds to a midpoint of two codes only when it is one (scale and midpoints
+// have few bits), so the division's rounding never moves a code.
+HERALD_DEV void quantise16(const float (&x)[16], float scale0, float c6, uint2* codes,
+                           uint32_t* scale) {
+  float a = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < 16; ++i) a = max_nan(a, fabsf(x[i]));
+  *scale = float_to_e4m3(__fdiv_rn(a, c6));
+  const float S = __fmul_rn(e4m3_to_float(*scale), scale0);
+  uint32_t w[2] = {0, 0};
+  if (S > 0.f) {  // (a zero or NaN scale: codes 0)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i >> 2] |= float2_to_e2m1(__fdiv_rn(x[2 * i], S), __fdiv_rn(x[2 * i + 1], S))
+                   << (8 * (i & 3));
+  }
+  *codes = make_uint2(w[0], w[1]);
+}
+
+constexpr int kKv4MoveThreads = 256;
+
+// A row of D channels is handled by D/16 neighbouring lanes, one group of 16
+// channels each.  An item is one token and `per` consecutive heads of it
+// (query heads, then key heads, then value heads), so a lane keeps its
+// angles in registers for all of them; items run over the tokens of one
+// sequence (blockIdx.y).
+struct Kv4AppendArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_ld, k_ld, v_ld;
+  const int32_t *n_tok, *ctx;
+  const float* cos_sin;  // [n_pos][rot/2][2]
+  int rot, interleaved;
+  uint16_t *q_rot, *k_rot;
+  int Hq, Hkv, T, L_max, heads, per, chunks;
+  int has_cache;
+  Kv4Dev c;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kKv4MoveThreads)
+    kv4_append_kernel(const Kv4AppendArgs a) {
+  constexpr int LPR = D / 16;
+  griddep_enter();
+  const int n = blockIdx.y, lane = threadIdx.x & 31;
+  const int c = lane % LPR;  // this lane's group of 16 channels
+  const int ctx_raw = a.ctx[n];
+  debug_flag(threadIdx.x == 0 && (ctx_raw < 0 || ctx_raw > a.L_max), DEV_BAD_COUNT);
+  const int L0 = min(max(ctx_raw, 0), a.L_max);
+  int toks = a.T;
+  if (a.n_tok) {
+    const int raw = a.n_tok[n];
+    debug_flag(threadIdx.x == 0 && (raw < 0 || raw > a.T), DEV_BAD_COUNT);
+    toks = min(max(raw, 0), a.T);
+  }
+  toks = min(toks, a.L_max - L0);  // tokens at or past L_max are ignored
+  const int64_t item = (int64_t(blockIdx.x) * kKv4MoveThreads + threadIdx.x) / LPR;
+  const int t = int(item / a.chunks), chunk = int(item - int64_t(t) * a.chunks);
+  const bool live = t < toks;
+  // (a warp whose items are all past the tokens leaves together; the others
+  // keep every lane for the exchanges below)
+  if (!__any_sync(0xffffffffu, live)) return;
+  const int pos = live ? L0 + t : 0;
+  const int h0 = chunk * a.per, h1 = min(h0 + a.per, a.heads);
+
+  // angles: in the half-split form channel i < rot/2 pairs with i + rot/2
+  // (the same group of the lane rot/32 groups on), else 2i pairs with 2i+1
+  const bool turns = c * 16 < a.rot;
+  const int RG2 = a.rot / 32;  // groups per half
+  const bool first = c < RG2;
+  const int partner = (lane - c) + (a.interleaved || !turns ? c : first ? c + RG2 : c - RG2);
+  float cs[16], sn[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+  }
+  if (turns && h0 < a.Hq + a.Hkv) {
+    const float* p = a.cos_sin + size_t(pos) * a.rot;
+    if (a.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float4 w = *reinterpret_cast<const float4*>(p + (c * 8 + i) * 2);
+        cs[i] = w.x, sn[i] = w.y, cs[i + 1] = w.z, sn[i + 1] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float4 w =
+            *reinterpret_cast<const float4*>(p + ((first ? c : c - RG2) * 16 + i) * 2);
+        cs[i] = w.x, sn[i] = w.y, cs[i + 1] = w.z, sn[i + 1] = w.w;
+      }
+    }
+  }
+  int phys = -1;
+  if (a.has_cache && live && h1 > a.Hq) {
+    phys = kv4_page(a.c, n, pos >> a.c.page_log2);
+    debug_flag(phys < 0, DEV_BAD_INDEX);  // a token without a page
+  }
+  const int64_t tok = int64_t(n) * a.T + t;
+  for (int h = h0; h < h0 + a.per; ++h) {
+    const bool on = live && h < h1;
+    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+    const int hh = is_q ? h : is_k ? h - a.Hq : h - a.Hq - a.Hkv;
+    uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+    if (on) {
+      const uint16_t* src = (is_q ? a.q + tok * a.q_ld : is_k ? a.k + tok * a.k_ld
+                                                              : a.v + tok * a.v_ld) +
+                            hh * D + c * 16;
+      u0 = *reinterpret_cast<const uint4*>(src);
+      u1 = *reinterpret_cast<const uint4*>(src + 8);
+    }
+    const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[2 * i] = bf16lo(w[i]);
+      x[2 * i + 1] = bf16hi(w[i]);
+    }
+    // products and sums rounded one by one, as the definition has them
+    if (a.interleaved) {
+      if (turns && (is_q || is_k)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float e = x[2 * i], o = x[2 * i + 1];
+          x[2 * i] = __fsub_rn(__fmul_rn(e, cs[i]), __fmul_rn(o, sn[i]));
+          x[2 * i + 1] = __fadd_rn(__fmul_rn(o, cs[i]), __fmul_rn(e, sn[i]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t pw = __shfl_sync(0xffffffffu, w[i], partner);
+        if (turns && (is_q || is_k)) {
+          const float p0 = __fmul_rn(bf16lo(pw), sn[2 * i]),
+                      p1 = __fmul_rn(bf16hi(pw), sn[2 * i + 1]);
+          const float y0 = __fmul_rn(x[2 * i], cs[2 * i]),
+                      y1 = __fmul_rn(x[2 * i + 1], cs[2 * i + 1]);
+          x[2 * i] = first ? __fsub_rn(y0, p0) : __fadd_rn(y0, p0);
+          x[2 * i + 1] = first ? __fsub_rn(y1, p1) : __fadd_rn(y1, p1);
+        }
+      }
+    }
+    if (!on) continue;
+    uint16_t* rot = is_q ? a.q_rot : is_k ? a.k_rot : nullptr;
+    if (rot) {
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+      uint4* dst = reinterpret_cast<uint4*>(rot + (tok * (is_q ? a.Hq : a.Hkv) + hh) * D + c * 16);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+    if (!is_q && phys >= 0) {
+      const float s0 = is_k ? a.c.k_scale : a.c.v_scale;
+      uint2 codes;
+      uint32_t scale;
+      quantise16(x, s0, __fmul_rn(6.f, s0), &codes, &scale);
+      const size_t row = kv4_row(a.c, phys, a.Hkv, hh, pos);
+      *reinterpret_cast<uint2*>((is_k ? a.c.kc : a.c.vc) + row * (D / 2) + c * 8) = codes;
+      (is_k ? a.c.ks : a.c.vs)[row * LPR + c] = uint8_t(scale);
+    }
+  }
+}
+
+// grid (blocks, N*Hkv), block D: the means of the blocks that tokens [ctx,
+// ctx + tokens) fall into, over the rows below ctx + tokens; thread e sums
+// channel e.  A row without a page counts as zeros.
+__global__ void kv4_pool_kernel(const Kv4Dev c, const int32_t* __restrict__ ctx,
+                                const int32_t* __restrict__ n_tok, int T, int Hkv, int d, int L_max,
+                                int Bk, int nb_max, float* __restrict__ pooled) {
+  griddep_enter();
+  const int seg = blockIdx.y, n = seg / Hkv, g = seg - n * Hkv, e = threadIdx.x;
+  const int L0 = min(max(ctx[n], 0), L_max);
+  const int end = min(L0 + (n_tok ? min(max(n_tok[n], 0), T) : T), L_max);
+  const int b = L0 / Bk + int(blockIdx.x);
+  if (end == L0 || b * int64_t(Bk) >= end) return;
+  const int r0 = b * Bk, r1 = min(end, r0 + min(Bk, L_max - r0));
+  float acc = 0.f;
+  for (int r = r0; r < r1; ++r) {
+    const int phys = kv4_page(c, n, r >> c.page_log2);
+    if (phys < 0) {
+      debug_flag(true, DEV_BAD_INDEX);
+      continue;
+    }
+    const size_t row = kv4_row(c, phys, Hkv, g, r);
+    const uint32_t code = c.kc[row * (d / 2) + (e >> 1)] >> (4 * (e & 1));
+    const uint32_t h = e2m1x2_to_half2(code & 0xFu);
+    acc += __low2float(*reinterpret_cast<const __half2*>(&h)) *
+           e4m3_to_float(c.ks[row * (d / 16) + (e >> 4)]);
+  }
+  pooled[(size_t(seg) * nb_max + b) * d + e] = acc * c.k_scale / float(r1 - r0);
+}
+
+__global__ void kv4_advance_kernel(int32_t* ctx, const int32_t* n_tok, int N, int T, int L_max) {
+  griddep_enter();
+  const int n = blockIdx.x * blockDim.x + threadIdx.x;
+  if (n >= N) return;
+  const int L0 = min(max(ctx[n], 0), L_max);
+  ctx[n] = min(L0 + min(n_tok ? min(max(n_tok[n], 0), T) : T, L_max - L0), L_max);
+}
+
+// grid (row groups, N*Hkv): D/16 lanes per row, each 16 channels: 8 bytes of
+// codes and one scale in, 32 bytes of bf16 out.
+template <int D>
+__global__ void __launch_bounds__(kKv4MoveThreads)
+    kv4_gather_kernel(const Kv4Dev c, const int32_t* __restrict__ idx,
+                      const int32_t* __restrict__ n_sel, int P_max, int Hkv, int L_max,
+                      uint16_t* __restrict__ pk, uint16_t* __restrict__ pv) {
+  constexpr int LPR = D / 16, RPC = kKv4MoveThreads / LPR;
+  griddep_enter();
+  const int seg = blockIdx.y, n = seg / Hkv, g = seg - n * Hkv;
+  const int ch = threadIdx.x % LPR, r = blockIdx.x * RPC + threadIdx.x / LPR;
+  if (r >= P_max) return;
+  const int pos = idx[size_t(seg) * P_max + r];
+  const int ns = n_sel[seg];
+  debug_flag(ns < 0 || ns > P_max, DEV_BAD_COUNT);
+  int phys = -1;
+  if (r < ns) {
+    if (pos >= 0 && pos < L_max) phys = kv4_page(c, n, pos >> c.page_log2);
+    debug_flag(phys < 0, DEV_BAD_INDEX);  // a selected row outside the cache
+  }
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    uint16_t* out = kv ? pv : pk;
+    if (!out) continue;
+    uint32_t o[8] = {};
+    if (phys >= 0) {
+      const size_t row = kv4_row(c, phys, Hkv, g, pos);
+      const uint2 w = *reinterpret_cast<const uint2*>((kv ? c.vc : c.kc) + row * (D / 2) + ch * 8);
+      const float s = e4m3_to_float((kv ? c.vs : c.ks)[row * LPR + ch]);
+      const float s0 = kv ? c.v_scale : c.k_scale;
+      uint32_t h[8];
+      e2m1x8_to_half2(w.x, *reinterpret_cast<uint32_t(*)[4]>(h));
+      e2m1x8_to_half2(w.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        // code * scale is exact; one rounding by s0 in fp32, one to bf16
+        o[i] = pack_bf16(f.x * s * s0, f.y * s * s0);
+      }
+    }
+    uint4* dst = reinterpret_cast<uint4*>(out + (size_t(seg) * P_max + r) * D + ch * 16);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+cudaError_t launch_kv4_append(const herald_dims& dm, int T, const int32_t* n_tok,
+                              const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld,
+                              const uint16_t* v, int64_t v_ld, const herald_rope* rope,
+                              int32_t* ctx, const Kv4Dev* cache, uint16_t* q_rot, uint16_t* k_rot,
+                              float* pooled, int Bk, bool advance, cudaStream_t st) {
+  Kv4AppendArgs a{};
+  a.q = q, a.k = k, a.v = v;
+  a.q_ld = q_ld, a.k_ld = k_ld, a.v_ld = v_ld;
+  a.n_tok = n_tok, a.ctx = ctx;
+  if (rope) a.cos_sin = rope->cos_sin, a.rot = rope->rot, a.interleaved = rope->interleaved;
+  a.q_rot = q_rot, a.k_rot = k_rot;
+  a.Hq = q ? dm.Hq : 0, a.Hkv = dm.Hkv, a.T = T, a.L_max = dm.L_max;
+  a.heads = a.Hq + (k ? dm.Hkv : 0) + (cache ? dm.Hkv : 0);
+  if (!k) a.Hkv = 0;
+  a.has_cache = cache != nullptr;
+  if (cache) a.c = *cache;
+  // heads per item: 1 while the items of single heads do not fill the GPU
+  const int lpr = dm.d / 16;
+  const int64_t rows = int64_t(dm.N) * T * a.heads;
+  a.per = rows * lpr <= 152 * 2048 ? 1 : 6;
+  a.chunks = cdiv(a.heads, a.per);
+  const int64_t threads = int64_t(T) * a.chunks * lpr;
+  const dim3 grid(unsigned((threads + kKv4MoveThreads - 1) / kKv4MoveThreads), unsigned(dm.N));
+  if (dm.d == 128)
+    HERALD_CHECK_LAUNCH(launch_k("kv4_append_kernel", kv4_append_kernel<128>, grid,
+                                 dim3(kKv4MoveThreads), 0, st, a));
+  else
+    HERALD_CHECK_LAUNCH(launch_k("kv4_append_kernel", kv4_append_kernel<64>, grid,
+                                 dim3(kKv4MoveThreads), 0, st, a));
+  if (pooled)
+    HERALD_CHECK_LAUNCH(launch_k("kv4_pool_kernel", kv4_pool_kernel,
+                                 dim3(unsigned(cdiv(T - 1, Bk) + 1), unsigned(dm.N * dm.Hkv)),
+                                 dim3(unsigned(dm.d)), 0, st, *cache, ctx, n_tok, T, dm.Hkv, dm.d,
+                                 dm.L_max, Bk, cdiv(dm.L_max, Bk), pooled));
+  if (advance)
+    HERALD_CHECK_LAUNCH(launch_k("kv4_advance_kernel", kv4_advance_kernel,
+                                 dim3(unsigned(cdiv(dm.N, 256))), dim3(256), 0, st, ctx, n_tok,
+                                 dm.N, T, dm.L_max));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_gather(const herald_dims& dm, const int32_t* idx, const int32_t* n_sel,
+                              int P_max, const Kv4Dev& c, uint16_t* pk, uint16_t* pv,
+                              cudaStream_t st) {
+  const int rpc = kKv4MoveThreads / (dm.d / 16);
+  const dim3 grid(unsigned(cdiv(P_max, rpc)), unsigned(dm.N * dm.Hkv));
+  if (dm.d == 128)
+    HERALD_CHECK_LAUNCH(launch_k("kv4_gather_kernel", kv4_gather_kernel<128>, grid,
+                                 dim3(kKv4MoveThreads), 0, st, c, idx, n_sel, P_max, dm.Hkv,
+                                 dm.L_max, pk, pv));
+  else
+    HERALD_CHECK_LAUNCH(launch_k("kv4_gather_kernel", kv4_gather_kernel<64>, grid,
+                                 dim3(kKv4MoveThreads), 0, st, c, idx, n_sel, P_max, dm.Hkv,
+                                 dm.L_max, pk, pv));
+  return cudaGetLastError();
+}
+
+HERALD_DEBUG_WORD_READER(debug_take_kv4_move)
+
+}  // namespace herald

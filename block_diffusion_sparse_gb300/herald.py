@@ -32,6 +32,8 @@ HERALD_ATTN_KERNEL_POOL_CS8, HERALD_ATTN_KERNEL_POOL_CS16, HERALD_ATTN_KERNEL_PO
 # flags of herald_block
 HERALD_BLOCK_ADVANCE = 1
 HERALD_BLOCK_CAND_SETTLED = 2
+# flag of herald_kv4_append
+HERALD_KV4_ADVANCE = 1
 
 
 def HERALD_ATTN_SMS(n: int) -> int:
@@ -51,7 +53,8 @@ EXPORTS = ("herald_workspace_size", "herald_status_string", "herald_last_error",
            "herald_select_stage1_blocks", "herald_stage_candidates",
            "herald_select_stage2_staged", "herald_select_stage2_staged_gather",
            "herald_select_stage2_adaptive", "herald_debug_build", "herald_debug_status",
-           "herald_inject_launch_failure", "herald_block")
+           "herald_inject_launch_failure", "herald_block", "herald_kv4_append",
+           "herald_kv4_attn", "herald_kv4_gather", "herald_workspace_size_kv4")
 
 
 class HeraldError(RuntimeError):
@@ -76,6 +79,54 @@ class BlockBufs(C.Structure):
                 ("n_sel", C.c_void_p), ("pool_k", C.c_void_p * 2), ("pool_v", C.c_void_p * 2),
                 ("ws_den", C.c_void_p), ("ws_sel", C.c_void_p), ("ws_bytes", C.c_size_t),
                 ("sel_stream", C.c_void_p), ("ev_fork", C.c_void_p), ("ev_join", C.c_void_p)]
+
+
+class Kv4(C.Structure):
+    """herald_kv4: a paged 4-bit cache (made by kv4())."""
+    _fields_ = [("page", C.c_int), ("n_pages", C.c_int), ("max_pages", C.c_int),
+                ("table", C.c_void_p), ("k_codes", C.c_void_p), ("k_scales", C.c_void_p),
+                ("v_codes", C.c_void_p), ("v_scales", C.c_void_p), ("k_scale", C.c_float),
+                ("v_scale", C.c_float)]
+
+
+class Rope(C.Structure):
+    """herald_rope: the position rotation (made by rope())."""
+    _fields_ = [("cos_sin", C.c_void_p), ("n_pos", C.c_int), ("rot", C.c_int),
+                ("interleaved", C.c_int)]
+
+
+def kv4(page, table, k_codes, k_scales, v_codes, v_scales, k_scale=1.0, v_scale=1.0) -> Kv4:
+    """The Kv4 of contiguous tensors: table [N, max_pages] int32, codes
+    [n_pages, Hkv, page, d/2] and scales [n_pages, Hkv, page, d/16] of one byte
+    each.  The struct keeps the tensors alive."""
+    arrays = (k_codes, k_scales, v_codes, v_scales)
+    n_pages = int(k_codes.shape[0])
+    for x in arrays:
+        if x.element_size() != 1 or x.dim() != 4 or not x.is_contiguous():
+            raise ValueError("codes and scales must be contiguous [n_pages, Hkv, page, .] bytes")
+        if int(x.shape[0]) != n_pages or int(x.shape[1]) != int(k_codes.shape[1]) \
+                or int(x.shape[2]) != int(page):
+            raise ValueError("codes and scales must agree in n_pages, Hkv and page")
+    if k_codes.shape != v_codes.shape or k_scales.shape != v_scales.shape \
+            or int(k_codes.shape[3]) != 8 * int(k_scales.shape[3]):
+        raise ValueError("codes must be [.., d/2] and scales [.., d/16], alike for K and V")
+    if table.dim() != 2 or table.element_size() != 4 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous [N, max_pages] int32 tensor")
+    s = Kv4(int(page), n_pages, int(table.shape[1]), _p(table), *(_p(x) for x in arrays),
+            float(k_scale), float(v_scale))
+    s._keep = (table, arrays)
+    return s
+
+
+def rope(cos_sin, rot, interleaved=False) -> Rope:
+    """The Rope of a contiguous fp32 tensor cos_sin [n_pos, rot/2, 2], which the
+    struct keeps alive."""
+    if cos_sin.dim() != 3 or tuple(cos_sin.shape[1:]) != (int(rot) // 2, 2) \
+            or cos_sin.element_size() != 4 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous [n_pos, rot/2, 2] fp32 tensor")
+    s = Rope(_p(cos_sin), int(cos_sin.shape[0]), int(rot), int(bool(interleaved)))
+    s._keep = cos_sin
+    return s
 
 
 def dims(N, Hq, Hkv, d, B, L_max) -> Dims:
@@ -145,13 +196,21 @@ def lib() -> C.CDLL:
                                                          vp, sz, vp]
         L.herald_select_stage1_blocks.argtypes = [Dims, vp, vp, vp, i32, i32, vp, vp, vp, sz,
                                                   vp]
+        L.herald_kv4_append.argtypes = [Dims, i32, vp, vp, C.c_int64, vp, C.c_int64, vp, C.c_int64,
+                                        C.POINTER(Rope), vp, C.POINTER(Kv4), vp, vp, vp, i32,
+                                        C.c_uint, vp]
+        L.herald_workspace_size_kv4.argtypes = [Dims]
+        L.herald_workspace_size_kv4.restype = sz
+        L.herald_kv4_attn.argtypes = [Dims, vp, C.POINTER(Kv4), vp, vp, vp, vp, C.c_float, vp, sz,
+                                      vp]
+        L.herald_kv4_gather.argtypes = [Dims, vp, vp, i32, C.POINTER(Kv4), vp, vp, vp]
         L.herald_trace_begin.argtypes = [C.POINTER(vp), i32, i32]
         L.herald_trace_end.argtypes = []
         L.herald_trace_name.argtypes = [i32]
         L.herald_trace_name.restype = C.c_char_p
         for name in EXPORTS:
             if name not in ("herald_workspace_size", "herald_workspace_size_exact",
-                            "herald_status_string",
+                            "herald_workspace_size_kv4", "herald_status_string",
                             "herald_last_error", "herald_trace_name"):
                 getattr(L, name).restype = C.c_int
         _lib = L
@@ -389,6 +448,53 @@ def herald_block(d, C_, K, S, W, P_max, T, i, q_steps, block_k, block_v, k_cache
                               _p(q_steps), _p(block_k), _p(block_v), _p(k_cache), _p(v_cache),
                               _p(ctx_len), _p(next_k_cache), _p(out), int(flags), int(scan_sms),
                               C.byref(bufs), _s(stream)))
+
+
+def _token_ld(x, ld, what):
+    """Elements from token to token of [N, T, heads, d]: given, or a tensor's."""
+    if ld is not None:
+        return int(ld)
+    if x is None or isinstance(x, int):
+        return 0
+    s, shape = x.stride(), x.shape
+    if x.dim() != 4 or s[3] != 1 or (shape[2] > 1 and s[2] != shape[3]):
+        raise ValueError(f"{what}: heads and channels of a token must be contiguous")
+    # (the stride of an axis of one entry says nothing: take the other's)
+    step = s[1] if shape[1] > 1 else s[0] if shape[0] > 1 else shape[2] * shape[3]
+    if shape[0] > 1 and s[0] != shape[1] * step:
+        raise ValueError(f"{what}: sequences must follow each other at T token strides")
+    return int(step)
+
+
+def herald_kv4_append(d, T, q, k, v, ctx_len, cache, q_rot, k_rot, rope=None, n_tok=None,
+                      pooled=None, Bk=0, flags=0, q_ld=None, k_ld=None, v_ld=None, stream=None):
+    """cache: a Kv4 or None (rotate only); rope: a Rope or None.  The token
+    strides of q, k, v [N, T, heads, d] are taken from the tensors (views of a
+    fused projection's output) unless given."""
+    _check(lib().herald_kv4_append(
+        d, int(T), _p(n_tok), _p(q), _token_ld(q, q_ld, "q"), _p(k), _token_ld(k, k_ld, "k"),
+        _p(v), _token_ld(v, v_ld, "v"), None if rope is None else C.byref(rope), _p(ctx_len),
+        None if cache is None else C.byref(cache), _p(q_rot), _p(k_rot), _p(pooled), int(Bk),
+        int(flags), _s(stream)))
+
+
+def herald_workspace_size_kv4(d: Dims) -> int:
+    return int(lib().herald_workspace_size_kv4(d))
+
+
+def herald_kv4_attn(d, q, cache, ctx_len, block_k, block_v, out, scale=0.0, ws=None,
+                    ws_bytes=None, stream=None):
+    """Attention over a paged 4-bit cache (a Kv4) and, unless both are None,
+    the block's own keys and values."""
+    _check(lib().herald_kv4_attn(d, _p(q), None if cache is None else C.byref(cache), _p(ctx_len),
+                                 _p(block_k), _p(block_v), _p(out), float(scale), _p(ws),
+                                 _nbytes(ws, ws_bytes), _s(stream)))
+
+
+def herald_kv4_gather(d, idx, n_sel, P_max, cache, pool_k, pool_v=None, stream=None):
+    _check(lib().herald_kv4_gather(d, _p(idx), _p(n_sel), int(P_max),
+                                   None if cache is None else C.byref(cache), _p(pool_k),
+                                   _p(pool_v), _s(stream)))
 
 
 class Trace:

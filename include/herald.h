@@ -475,6 +475,108 @@ herald_status herald_select_exact(herald_dims dims, const uint16_t *q_block,
                                   int sink, int local, int P_max, int32_t *idx, int32_t *n_sel,
                                   void *ws, size_t ws_bytes, void *stream);
 
+/* A paged KV cache held in 4 bits (the pages have no counterpart; it stands
+ * beside the contiguous bf16 cache of the calls above).  A row -- one position
+ * of one KV head, d channels -- is d/2 bytes of e2m1 codes, two per byte with
+ * the even channel in the low half, and d/16 e4m3 scales, one per 16
+ * consecutive channels:
+ *   value = code * scale * k_scale      (keys; v_scale for values)
+ * 4.5 bits per value.  Position p of sequence n is row p % page of page
+ * table[n][p / page]; table entries outside [0, n_pages) have no page: such
+ * positions are neither read (they count as masked) nor written.  Sequences
+ * may share pages that are only read.
+ *   page               positions per page: 16, 32, 64 or 128
+ *   n_pages            pages in the arrays, >= 1
+ *   max_pages          table entries per sequence, max_pages*page >= dims.L_max
+ *   table              [N][max_pages] int32 device
+ *   k_codes, v_codes   [n_pages][Hkv][page][d/2] device
+ *   k_scales, v_scales [n_pages][Hkv][page][d/16] device
+ *   k_scale, v_scale   one factor for all keys and one for all values, in
+ *                      [2^-60, 2^60] (1 suits keys of order 1; a power of two
+ *                      near max|x| / 2688 or above keeps small values out of
+ *                      e4m3's subnormals, whose step is 2^-9) */
+typedef struct {
+  int page, n_pages, max_pages;
+  const int32_t *table;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  float k_scale, v_scale;
+} herald_kv4;
+
+/* The position rotation: pair i of a position p's channels is turned by the
+ * angle whose cosine and sine are cos_sin[p][i].
+ *   cos_sin      [n_pos][rot/2][2] fp32 device, n_pos >= dims.L_max
+ *   rot          channels that turn, a multiple of 32 in [32, d]; the others
+ *                stay as they are
+ *   interleaved  0: pair i = channels i and i + rot/2; 1: 2i and 2i + 1 */
+typedef struct {
+  const float *cos_sin;
+  int n_pos, rot, interleaved;
+} herald_rope;
+
+#define HERALD_KV4_ADVANCE 1u /* ctx_len[n] += the tokens appended */
+
+/* Rotates queries and keys and appends keys and values to a paged 4-bit
+ * cache in one pass.  Token t of sequence n stands at position p = ctx_len[n]
+ * + t; only tokens t < n_tok[n] (t < T without n_tok) with p < L_max are
+ * touched: no output row of another token is written.
+ *   x'_a = x_a cos - x_b sin, x'_b = x_b cos + x_a sin for every pair (a, b),
+ *   each product and sum rounded to fp32; q_rot, k_rot = x' rounded to bf16;
+ *   the cache takes k' (fp32) and v per group of 16 channels as
+ *     scale = e4m3(max|x| / (6 k_scale)), code = e2m1(x / (scale k_scale)),
+ *   fp32 divisions, to nearest even, past the largest to the largest (an
+ *   infinity is held as 2688 k_scale; a NaN makes its group NaN; a scale
+ *   that rounds to zero, zeros): the held bytes are defined to the bit.
+ *   T        tokens per sequence in the arrays (>= 1; any length)
+ *   n_tok    [N] int32 device, tokens that count (clamped to [0, T]), or NULL
+ *   q        [N][T] rows of Hq*d bf16, q_ld elements from token to token (a
+ *            multiple of 8, >= Hq*d, or 0 = dense: a slice of a fused
+ *            projection's output has its width here); NULL: no queries
+ *   k, v     likewise [N][T] rows of Hkv*d, k_ld, v_ld
+ *   rope     NULL: no rotation
+ *   cache    NULL: rotate only (the earlier denoising steps of a block); v
+ *            and ctx_len are then not written.  k is required with it, v too
+ *   q_rot    [N][T][Hq][d] bf16 device out, required with q (may be q itself
+ *            when q is dense)
+ *   k_rot    [N][T][Hkv][d] bf16 device out (may be k itself when k is
+ *            dense); may be NULL with a cache
+ *   pooled   NULL, or fp32 [N][Hkv][ceil(L_max/Bk)][d] device: the means of
+ *            herald_pool_keys over the keys as held, refreshed for the
+ *            blocks the tokens fall into (herald_select_stage1_blocks reads
+ *            them); Bk in [1, L_max].  Rows without a page count as zeros
+ *   flags    HERALD_KV4_ADVANCE (needs the cache)
+ * dims.B is not used beyond its own checks.  N*Hkv <= 65535. */
+herald_status herald_kv4_append(herald_dims dims, int T, const int32_t *n_tok, const uint16_t *q,
+                                int64_t q_ld, const uint16_t *k, int64_t k_ld, const uint16_t *v,
+                                int64_t v_ld, const herald_rope *rope, int32_t *ctx_len,
+                                const herald_kv4 *cache, uint16_t *q_rot, uint16_t *k_rot,
+                                float *pooled, int Bk, unsigned flags, void *stream);
+
+/* Full attention of a block's queries over a paged 4-bit cache: every query
+ * (n, b, h) attends, without a mask, to the cache positions below
+ * ctx_len[n] of KV head h/G and, where given, the block's own B keys in bf16
+ * (bidirectional inside the block, as herald_denoise_attn).  A query without
+ * any key gets zeros.  B = 1 is single-token decoding.
+ *   q        [N][B][Hq][d] bf16 device     out  [N][B][Hq][d] bf16 device out
+ *   ctx_len  [N] int32 device
+ *   block_k, block_v  [N][B][Hkv][d] bf16 device, or both NULL
+ *   scale    softmax scale; 0 selects 1/sqrt(d)
+ *   ws       herald_workspace_size_kv4(dims) bytes (0 = unsupported shape)
+ * N*Hkv <= 65535.  Results do not depend on other calls or on timing. */
+size_t herald_workspace_size_kv4(herald_dims dims);
+herald_status herald_kv4_attn(herald_dims dims, const uint16_t *q, const herald_kv4 *cache,
+                              const int32_t *ctx_len, const uint16_t *block_k,
+                              const uint16_t *block_v, uint16_t *out, float scale, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/* Rows of a paged 4-bit cache as bf16: herald_gather's pool, or the candidate
+ * rows of herald_stage_candidates (idx = cand, n_sel = n_cand, P_max = C):
+ *   pool[n][g][s] = bf16(value of row idx[n][g][s]) for s < n_sel,
+ * zero rows for n_sel <= s < P_max and for positions outside [0, L_max) or
+ * without a page.  pool_v may be NULL (keys only).  N*Hkv <= 65535. */
+herald_status herald_kv4_gather(herald_dims dims, const int32_t *idx, const int32_t *n_sel,
+                                int P_max, const herald_kv4 *cache, uint16_t *pool_k,
+                                uint16_t *pool_v, void *stream);
+
 /* Self-test of the device-side failure path (the pages have no
  * counterpart).  Every wait inside the library's kernels gives up after
  * about one second, records a code in the workspace's error word and lets
