@@ -529,7 +529,8 @@ herald_status herald_debug_status(uint32_t* code) {
 #ifdef HERALD_DEBUG
   HERALD_TRY_CUDA(cudaDeviceSynchronize(), "device synchronize");
   *code = debug_take_select() | debug_take_tc() | debug_take_move() | debug_take_blocks() |
-          debug_take_flash() | debug_take_kv4_move() | debug_take_kv4_attn();
+          debug_take_flash() | debug_take_kv4_move() | debug_take_kv4_attn() |
+          debug_take_kv4_attn_tc();
 #endif
   return HERALD_OK;
 }

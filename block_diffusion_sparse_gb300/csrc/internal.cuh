@@ -129,6 +129,7 @@ uint32_t debug_take_blocks();
 uint32_t debug_take_flash();
 uint32_t debug_take_kv4_move();
 uint32_t debug_take_kv4_attn();
+uint32_t debug_take_kv4_attn_tc();
 
 // A launch failure injected on the host (herald_inject_launch_failure, a
 // test hook of the error paths): returns the injected error for the launch

@@ -8,6 +8,8 @@
 // A code has 2 and a scale 4 significant bits, so code * scale has at most 6
 // and lies in [2^-10, 2688]: it is exact in fp16.
 #pragma once
+#include <float.h>
+
 #include "internal.cuh"
 #include "ptx.cuh"
 
@@ -61,6 +63,35 @@ HERALD_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+
+// A query row as fp16: values are multiplied by *up, the power of two that
+// brings the row's largest magnitude mx to [2^14, 2^15), and *f turns a product
+// with the codes * scales of a key into a log2-unit score; sc = the softmax scale
+// times k_scale.  (mx below 2^-112 counts as that, infinities as 2^127; *f stays
+// positive and finite: a masked score of -inf times 0, or a zero score times
+// inf, would be NaN.)
+HERALD_DEV void kv4_query_scale(float mx, float sc, float* up, float* f) {
+  const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -112), 127);
+  *up = __uint_as_float(uint32_t(14 - e + 127) << 23);
+  *f = fminf(fmaxf(sc * 1.4426950408889634f * exp2f(float(e - 14)), FLT_MIN), FLT_MAX);
+}
+
+// ---- attention arguments shared by its kernels
+struct Kv4AttnArgs {
+  const uint16_t *q, *bk, *bv;
+  const int32_t* ctx;
+  uint16_t* out;
+  float* opart;  // [slots][R16][D]
+  float2* ml;    // [slots][R16]
+  float scale;
+  int N, Hq, Hkv, B, L_max, R16, ctas;
+  Kv4Dev c;
+};
+constexpr int kKv4TcKeys = 128;  // keys per tile of the tensor-core kernel
+// The tensor-core kernel (kv4_attn_tc.cu) for `rows` <= 256 query rows per KV
+// head; with rows <= 128 each piece has two partials (slots 2p and 2p+1).
+cudaError_t launch_kv4_attn_tc(int d, int rows, const Kv4AttnArgs& a, uint32_t* err,
+                               cudaStream_t st);
 
 // ---- how attention CTAs share the keys
 // The keys of every (sequence, KV head) segment, in units of `unit` cache

@@ -28,6 +28,8 @@
 // stays while no score exceeds it by 15: P lies in fp16's [0, 2^15], weights
 // down to 2^-25 of the largest keep 11 bits, and most units need one vote and
 // no exchange between lanes.
+#include <float.h>
+
 #include "kv4.cuh"
 
 namespace herald {
@@ -36,6 +38,7 @@ constexpr int kKv4Warps = 8;
 constexpr int kKv4Threads = kKv4Warps * 32;
 constexpr int kKv4Unit = 16;        // keys per unit
 constexpr int kKv4MinShare = kKv4Warps;  // units per CTA: at least one per warp
+constexpr int kKv4MmaRows = 16;     // most rows per KV head of this kernel
 constexpr float kKv4Below = 11.f, kKv4Above = 15.f;  // exponent base, log2 units
 
 
@@ -70,72 +73,44 @@ struct Kv4Raw {
   uint32_t v[4][D / 64];  // keys 2t, 2t+1, 2t+8, 2t+9: D/8 codes each
   uint32_t ks[2];         // their scales (D/64 bytes)
   uint32_t vs[4];
-  int valid;              // keys of the unit below the length (0: no page)
 };
 
-struct Kv4AttnArgs {
-  const uint16_t *q, *bk, *bv;
-  const int32_t* ctx;
-  uint16_t* out;
-  float* opart;  // [slots][R16][D]
-  float2* ml;    // [slots][R16]
-  float scale;
-  int N, Hq, Hkv, B, L_max, R16, ctas;
-  Kv4Dev c;
-};
-
+// Loads the unit at cache row `row` (kv4_row of its first key).  One address
+// per array, the keys at constant offsets from it.
 template <int D>
-HERALD_DEV void kv4_load(Kv4Raw<D>& r, const Kv4Dev& c, int phys, int Hkv, int g, int pos0,
-                         int ctx, int lane) {
+HERALD_DEV void kv4_load(Kv4Raw<D>& r, const Kv4Dev& c, size_t row, int lane) {
+  constexpr int C = D / 2, S = D / 16;  // bytes of a row's codes and scales
   const int lg = lane >> 2, lt = lane & 3;
-  r.valid = phys >= 0 ? min(ctx - pos0, kKv4Unit) : 0;
-  if (phys < 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      r.ks[i] = 0;
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) r.k[i][w] = 0;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.vs[i] = 0;
-#pragma unroll
-      for (int w = 0; w < D / 64; ++w) r.v[i][w] = 0;
-    }
-    return;
-  }
-  // (a page holds a whole number of units: rows past the length exist)
-  const size_t row = kv4_row(c, phys, Hkv, g, pos0);
+  const uint8_t* kc = c.kc + (row + lg) * C + lt * (C / 4);
+  const uint8_t* ks = c.ks + (row + lg) * S + lt * (S / 4);
+  const uint8_t* vc = c.vc + (row + 2 * lt) * C + lg * (C / 8);
+  const uint8_t* vs = c.vs + (row + 2 * lt) * S + lg * S / 8;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const size_t rr = row + lg + 8 * i;
-    const uint8_t* p = c.kc + rr * (D / 2) + lt * (D / 8);
     if constexpr (D == 128) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(kc + i * 8 * C));
       r.k[i][0] = w.x, r.k[i][1] = w.y, r.k[i][2] = w.z, r.k[i][3] = w.w;
-      r.ks[i] = __ldg(reinterpret_cast<const uint16_t*>(c.ks + rr * (D / 16) + lt * 2));
+      r.ks[i] = __ldg(reinterpret_cast<const uint16_t*>(ks + i * 8 * S));
     } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(kc + i * 8 * C));
       r.k[i][0] = w.x, r.k[i][1] = w.y;
-      r.ks[i] = __ldg(c.ks + rr * (D / 16) + lt);
+      r.ks[i] = __ldg(ks + i * 8 * S);
     }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const size_t rr = row + 2 * lt + (i & 1) + 8 * (i >> 1);
-    const uint8_t* p = c.vc + rr * (D / 2) + lg * (D / 16);
+    const int o = (i & 1) + 8 * (i >> 1);
     if constexpr (D == 128) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(vc + o * C));
       r.v[i][0] = w.x, r.v[i][1] = w.y;
-      r.vs[i] = __ldg(c.vs + rr * (D / 16) + lg);
     } else {
-      r.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-      r.vs[i] = __ldg(c.vs + rr * (D / 16) + (lg >> 1));
+      r.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(vc + o * C));
     }
+    r.vs[i] = __ldg(vs + o * S);
   }
 }
 
-// grid (ctas, row tiles of 8*NT rows)
+// at most 8*NT query rows per KV head
 template <int D, int NT>
 __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
     kv4_attn_kernel(const Kv4AttnArgs a) {
@@ -145,7 +120,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
   __shared__ float red_m[kKv4Warps][RT], red_l[kKv4Warps][RT];
   griddep_enter();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
-  const int G = a.Hq / a.Hkv, R = a.B * G, r_base = int(blockIdx.y) * RT;
+  const int G = a.Hq / a.Hkv, R = a.B * G;
   const int blk_units = a.bk ? (a.B + kKv4Unit - 1) / kKv4Unit : 0;
   const Kv4Split split =
       kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, kKv4Unit, blk_units), a.Hkv, a.ctas,
@@ -171,6 +146,13 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
     const int64_t seg0 = first + int64_t(g) * units;
     const int u0 = int(at - seg0), u1 = int(min(int64_t(units), end - seg0));
     const int seg = n * a.Hkv + g;
+    const int cu1 = min(u1, cache_units);
+    auto page_of = [&](int u) {
+      if (u >= cu1) return -1;
+      const int p = kv4_page(a.c, n, (u * kKv4Unit) >> a.c.page_log2);
+      debug_flag(p < 0, DEV_BAD_INDEX);  // positions below the length without a page
+      return p;
+    };
 
     // queries: B fragments (lane: row lg of each 8-row tile), fp16 scaled by
     // a power of two per row; rs[nt][2] undo it for the rows this lane's
@@ -179,7 +161,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
     float rs[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = r_base + nt * 8 + lg;
+      const int r = nt * 8 + lg;
       const bool on = r < R;
       const uint16_t* qp =
           a.q + ((size_t(n) * a.B + (on ? r / G : 0)) * a.Hq + g * G + (on ? r % G : 0)) * D +
@@ -196,16 +178,13 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // exponent of the largest value; 2^(14 - e), both factors normal fp32
-      const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -112), 127);
-      const float up = __uint_as_float(uint32_t(14 - e + 127) << 23);
-      const float down = exp2f(float(e - 14));
+      float up, f;
+      kv4_query_scale(mx, a.scale * a.c.k_scale, &up, &f);
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           qf[nt][s][i] = pack_half2(bf16lo(qf[nt][s][i]) * up, bf16hi(qf[nt][s][i]) * up);
-      const float f = a.scale * a.c.k_scale * 1.4426950408889634f * down;
       rs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * lt);      // lane of row 2 lt
       rs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * lt + 4);  // lane of row 2 lt + 1
     }
@@ -215,68 +194,55 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[nt][i] = -INFINITY, l[nt][i] = 0.f;
+      for (int i = 0; i < 2; ++i) m[nt][i] = -FLT_MAX, l[nt][i] = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[nt][k][i] = 0.f;
     }
-    // scores in log2 units -> probabilities; moves the base where needed
-    auto probabilities = [&](float (&s)[NT][4]) {
+    // raw scores -> probabilities 2^(s f - m); moves the base where a score
+    // stands more than kKv4Above over it
+    auto probabilities = [&](float (&s)[NT][4], const float (&f)[NT][2]) {
+      float x[NT][4];
       bool move = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float b = m[nt][i & 1];
-          move |= b == -INFINITY ? s[nt][i] > -INFINITY : s[nt][i] > b + kKv4Above;
-        }
+        for (int i = 0; i < 4; ++i) x[nt][i] = fmaf(s[nt][i], f[nt][i & 1], -m[nt][i & 1]);
+        move |= fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])) > kKv4Above;
+      }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float x = fmaxf(s[nt][i], s[nt][i + 2]);
+            float b = fmaxf(s[nt][i] * f[nt][i], s[nt][i + 2] * f[nt][i]);
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            const float b = fmaxf(m[nt][i], x - kKv4Below);
-            const float f = m[nt][i] == -INFINITY ? 0.f : fast_exp2(m[nt][i] - b);
+            for (int d = 4; d < 32; d <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
+            b = fmaxf(m[nt][i], b - kKv4Below);
+            const float w = fast_exp2(m[nt][i] - b);
             m[nt][i] = b;
-            l[nt][i] *= f;
+            l[nt][i] *= w;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-              o[nt][k][i] *= f;
-              o[nt][k][i + 2] *= f;
+              o[nt][k][i] *= w;
+              o[nt][k][i + 2] *= w;
             }
+            x[nt][i] = fmaf(s[nt][i], f[nt][i], -b);
+            x[nt][i + 2] = fmaf(s[nt][i + 2], f[nt][i], -b);
           }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float b = m[nt][i & 1];
-          s[nt][i] = fast_exp2(s[nt][i] - (b == -INFINITY ? 0.f : b));
+          s[nt][i] = fast_exp2(x[nt][i]);
           l[nt][i & 1] += s[nt][i];
         }
     };
 
     // ------------------------------------------------------ cache units
-    const int cu1 = min(u1, cache_units);
-    auto page_of = [&](int u) {
-      if (u >= cu1) return -1;
-      const int p = kv4_page(a.c, n, (u * kKv4Unit) >> a.c.page_log2);
-      debug_flag(p < 0, DEV_BAD_INDEX);  // positions below the length without a page
-      return p;
-    };
-    int u = u0 + warp;
-    Kv4Raw<D> raw;
-    if (u < cu1) kv4_load<D>(raw, a.c, page_of(u), a.Hkv, g, u * kKv4Unit, ctx, lane);
-    int page_next = page_of(u + kKv4Warps);
-    for (; u < cu1; u += kKv4Warps) {
-      const Kv4Raw<D> cur = raw;
-      if (u + kKv4Warps < cu1)
-        kv4_load<D>(raw, a.c, page_next, a.Hkv, g, (u + kKv4Warps) * kKv4Unit, ctx, lane);
-      page_next = page_of(u + 2 * kKv4Warps);
+    auto unit = [&](const Kv4Raw<D>& cur, int u, bool paged) {
       float s[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -300,30 +266,25 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
           mma_f16(s[nt], h0[2], h1[2], h0[3], h1[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
         }
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] *= rs[nt][i & 1];
-      if (cur.valid < kKv4Unit) {
+      uint32_t vs[4] = {cur.vs[0], cur.vs[1], cur.vs[2], cur.vs[3]};
+      const int valid = paged ? ctx - u * kKv4Unit : 0;
+      if (valid < kKv4Unit) {  // keys past the length, or without a page
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (lg + 8 * (i >> 1) >= cur.valid) s[nt][i] = -INFINITY;
+            if (lg + 8 * (i >> 1) >= valid) s[nt][i] = -INFINITY;
+        // such a row may hold any bytes: 0 * NaN must not arise
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (2 * lt + (i & 1) + 8 * (i >> 1) >= valid) vs[i] = 0;
       }
-      probabilities(s);
+      probabilities(s, rs);
       uint32_t p0[NT], p1[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         p0[nt] = transpose8x8(pack_half2(s[nt][0], s[nt][1]));
         p1[nt] = transpose8x8(pack_half2(s[nt][2], s[nt][3]));
-      }
-      uint32_t vs[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        vs[i] = cur.vs[i];
-        // a row past the length may hold any bytes: 0 * NaN must not arise
-        if (2 * lt + (i & 1) + 8 * (i >> 1) >= cur.valid) vs[i] = 0;
       }
       const uint32_t f0 = e4m3x2_to_half2(vs[0] | vs[1] << 8),
                      f1 = e4m3x2_to_half2(vs[2] | vs[3] << 8);
@@ -345,6 +306,30 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
             mma_f16(o[nt][w * 4 + i], e0[i], d0[i], e1[i], d1[i], p0[nt], p1[nt]);
         }
       }
+    };
+    // two units in flight: one is computed while the other one's bytes travel,
+    // and the page of the one after is looked up a unit ahead of its load
+    Kv4Raw<D> r0, r1;
+    int u = u0 + warp;
+    int pa = page_of(u), pb = page_of(u + kKv4Warps);
+    auto load = [&](Kv4Raw<D>& r, int phys, int at_unit) {
+      // (without a page: row 0, whose bytes the masks keep out)
+      kv4_load<D>(r, a.c, phys < 0 ? 0 : kv4_row(a.c, phys, a.Hkv, g, at_unit * kKv4Unit), lane);
+    };
+    if (u < cu1) load(r0, pa, u);
+    for (; u < cu1; u += 2 * kKv4Warps) {
+      const int v = u + kKv4Warps;
+      const bool ha = pa >= 0, hb = pb >= 0;
+      pa = page_of(v + kKv4Warps);
+      if (v < cu1) load(r1, pb, v);
+      pb = page_of(v + 2 * kKv4Warps);
+      unit(r0, u, ha);
+      if (v >= cu1) {
+        u = v;
+        break;
+      }
+      if (v + kKv4Warps < cu1) load(r0, pa, v + kKv4Warps);
+      unit(r1, v, hb);
     }
 
     // ------------------------------------- the block's own keys, in bf16
@@ -370,7 +355,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
           w[i] = kp[i] ? *reinterpret_cast<const uint2*>(kp[i] + k * 4) : make_uint2(0, 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int r = r_base + nt * 8 + lg;
+          const int r = nt * 8 + lg;
           uint2 b = make_uint2(0, 0);
           if (r < R)
             b = *reinterpret_cast<const uint2*>(
@@ -379,13 +364,15 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
           mma_bf16(s[nt], w[0].x, w[1].x, w[0].y, w[1].y, b.x, b.y);
         }
       }
-      const float f = a.scale * 1.4426950408889634f;
+      float f[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        f[nt][0] = f[nt][1] = fminf(a.scale * 1.4426950408889634f, FLT_MAX);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          s[nt][i] = j0 + lg + 8 * (i >> 1) < a.B ? s[nt][i] * f : -INFINITY;
-      probabilities(s);
+          if (j0 + lg + 8 * (i >> 1) >= a.B) s[nt][i] = -INFINITY;
+      }
+      probabilities(s, f);
       const float iv = 1.f / a.c.v_scale;
       uint32_t p0[NT], p1[NT];
 #pragma unroll
@@ -433,9 +420,9 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
     const bool whole = u0 == 0 && u1 == units;  // no other piece of this segment
     const int slot = int(blockIdx.x) + seg;
     for (int i = threadIdx.x; i < RT * (D / 4); i += kKv4Threads) {
-      const int rr = i / (D / 4), c4 = i % (D / 4), r = r_base + rr;
+      const int rr = i / (D / 4), c4 = i % (D / 4), r = rr;
       if (r >= R) continue;
-      float M = -INFINITY;
+      float M = -FLT_MAX;
 #pragma unroll
       for (int w = 0; w < kKv4Warps; ++w) M = fmaxf(M, red_m[w][rr]);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -443,7 +430,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
 #pragma unroll
       for (int w = 0; w < kKv4Warps; ++w) {
         const float mw = red_m[w][rr];
-        const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+        const float f = fast_exp2(mw - M);
         const float4 x =
             *reinterpret_cast<const float4*>(red + (size_t(w) * RT + rr) * (D + 4) + c4 * 4);
         L += f * red_l[w][rr];
@@ -465,41 +452,75 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
 }
 
 // Joins the pieces of every segment that has more than one, and writes zeros
-// for segments without keys.  grid (N*Hkv, row groups), block 256: D/4
-// threads per row.
+// for segments without keys.  grid (N*Hkv, R), one CTA per row: D/4 threads
+// hold four channels each, and kKv4JoinThreads / (D/4) groups of them take
+// every such-and-suchth piece, so that the pieces of a long context travel at
+// once; the groups are added in order.  subs: partials per piece (slots subs*p
+// ...); with more than one, single pieces are joined here too.
+constexpr int kKv4JoinThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(256)
-    kv4_join_kernel(const Kv4AttnArgs a, int unit, int blk_units, int min_share) {
+__global__ void __launch_bounds__(kKv4JoinThreads)
+    kv4_join_kernel(const Kv4AttnArgs a, int unit, int blk_units, int min_share, int subs) {
+  constexpr int TPR = D / 4, GR = kKv4JoinThreads / TPR;
+  __shared__ float4 part[GR][TPR];
+  __shared__ float part_m[GR], part_l[GR];
   griddep_enter();
   const int seg = blockIdx.x, n = seg / a.Hkv, g = seg - n * a.Hkv;
-  const int G = a.Hq / a.Hkv, R = a.B * G;
-  const int r = int(blockIdx.y) * (256 / (D / 4)) + threadIdx.x / (D / 4);
-  const int c4 = threadIdx.x % (D / 4);
+  const int G = a.Hq / a.Hkv, r = blockIdx.y;
+  const int c4 = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, unit, blk_units), a.Hkv,
                                    a.ctas, min_share);
   const int units = kv4_units(a.ctx[n], a.L_max, unit, blk_units);
-  int64_t first = int64_t(a.Hkv) * kv4_total_units(a.ctx, n, a.L_max, unit, blk_units) +
-                  int64_t(g) * units;
-  if (r >= R) return;
+  const int64_t first = int64_t(a.Hkv) * kv4_total_units(a.ctx, n, a.L_max, unit, blk_units) +
+                        int64_t(g) * units;
   uint2* out = reinterpret_cast<uint2*>(
       a.out + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c4 * 4);
   if (units == 0) {
-    *out = make_uint2(0, 0);
+    if (grp == 0) *out = make_uint2(0, 0);
     return;
   }
-  const int c0 = int(first / split.share), c1 = int((first + units - 1) / split.share);
-  if (c0 == c1) return;  // one piece: written by the attention kernel
-  float M = -INFINITY;
-  for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.ml[size_t(c + seg) * a.R16 + r].x);
+  int c0 = int(first / split.share), c1 = int((first + units - 1) / split.share);
+  if (c0 == c1 && subs == 1) return;  // one piece: written by the attention kernel
+  c0 = (c0 + seg) * subs, c1 = (c1 + seg) * subs + subs - 1;  // its partials
+  float M = -FLT_MAX, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 p = a.ml[size_t(c + seg) * a.R16 + r];
-    const float4 x =
-        *reinterpret_cast<const float4*>(a.opart + (size_t(c + seg) * a.R16 + r) * D + c4 * 4);
-    const float f = p.x == -INFINITY ? 0.f : fast_exp2(p.x - M);
-    L += f * p.y;
+  constexpr int kFly = 4;
+  for (int c = c0 + grp; c <= c1; c += kFly * GR) {
+    float2 p[kFly];
+    float4 x[kFly];
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int ci = min(c + i * GR, c1);
+      p[i] = a.ml[size_t(ci) * a.R16 + r];
+      x[i] = *reinterpret_cast<const float4*>(a.opart + (size_t(ci) * a.R16 + r) * D + c4 * 4);
+      if (c + i * GR > c1) p[i] = make_float2(-FLT_MAX, 0.f), x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float M1 = M;
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) M1 = fmaxf(M1, p[i].x);
+    const float w = fast_exp2(M - M1);
+    L *= w, acc.x *= w, acc.y *= w, acc.z *= w, acc.w *= w;
+    M = M1;
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const float f = fast_exp2(p[i].x - M);
+      L += f * p[i].y;
+      acc.x += f * x[i].x, acc.y += f * x[i].y, acc.z += f * x[i].z, acc.w += f * x[i].w;
+    }
+  }
+  part[grp][c4] = acc;
+  if (c4 == 0) part_m[grp] = M, part_l[grp] = L;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int i = 0; i < GR; ++i) M = fmaxf(M, part_m[i]);
+  L = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < GR; ++i) {
+    const float f = fast_exp2(part_m[i] - M);
+    const float4 x = part[i][c4];
+    L += f * part_l[i];
     acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
   }
   const float inv = L == 0.f ? 0.f : a.c.v_scale / L;
@@ -509,45 +530,61 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------- host
 
 template <int D, int NT>
-static cudaError_t launch_rows(const Kv4AttnArgs& a, int R, cudaStream_t st) {
+static cudaError_t launch_rows(const Kv4AttnArgs& a, cudaStream_t st) {
   constexpr size_t smem = size_t(kKv4Warps) * 8 * NT * (D + 4) * 4;
   HERALD_CHECK_LAUNCH(ensure_smem(kv4_attn_kernel<D, NT>, smem));
   return launch_k("kv4_attn_kernel", kv4_attn_kernel<D, NT>,
-                  dim3(unsigned(a.ctas), unsigned(cdiv(R, 8 * NT))), dim3(kKv4Threads), smem, st, a);
+                  dim3(unsigned(a.ctas)), dim3(kKv4Threads), smem, st, a);
 }
 
-size_t kv4_attn_workspace(const herald_dims& dm) {
-  const int R16 = cdiv(dm.B * (dm.Hq / dm.Hkv), 16) * 16;
-  const size_t slots = size_t(kKv4MaxCtas) + size_t(dm.N) * dm.Hkv;
-  return 256 + align_up(slots * R16 * 8, 256) + slots * R16 * size_t(dm.d) * 4;
+// Workspace: error word, then (m, l) and O of every partial.
+struct Kv4Ws {
+  size_t ml, opart, total;
+  int R16;
+};
+static Kv4Ws kv4_ws(const herald_dims& dm) {
+  Kv4Ws w;
+  w.R16 = cdiv(dm.B * (dm.Hq / dm.Hkv), 16) * 16;
+  const size_t slots = 2 * (size_t(kKv4MaxCtas) + size_t(dm.N) * dm.Hkv);
+  w.ml = 256;
+  w.opart = align_up(w.ml + slots * w.R16 * 8, 256);
+  w.total = w.opart + slots * w.R16 * size_t(dm.d) * 4;
+  return w;
 }
+size_t kv4_attn_workspace(const herald_dims& dm) { return kv4_ws(dm).total; }
 
 cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4Dev& c,
                             const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
                             uint16_t* out, float scale, void* ws, int num_sms, cudaStream_t st) {
-  const int G = dm.Hq / dm.Hkv, R = dm.B * G, R16 = cdiv(R, 16) * 16;
-  const size_t slots = size_t(kKv4MaxCtas) + size_t(dm.N) * dm.Hkv;
+  const int G = dm.Hq / dm.Hkv, R = dm.B * G;
+  const Kv4Ws w = kv4_ws(dm);
+  char* p = static_cast<char*>(ws);
   Kv4AttnArgs a{};
   a.q = q, a.bk = bk, a.bv = bv, a.ctx = ctx, a.out = out;
-  a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + 256);
-  a.opart = reinterpret_cast<float*>(static_cast<char*>(ws) + 256 + align_up(slots * R16 * 8, 256));
+  a.ml = reinterpret_cast<float2*>(p + w.ml);
+  a.opart = reinterpret_cast<float*>(p + w.opart);
   a.scale = scale;
-  a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max, a.R16 = R16;
+  a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max, a.R16 = w.R16;
   a.c = c;
+  const bool tc = R > kKv4MmaRows;
   const int nt = R <= 8 ? 1 : 2;
-  a.ctas = std::min(kKv4MaxCtas, std::max(1, (nt == 1 ? 2 : 1) * num_sms / cdiv(R, 8 * nt)));
-  if (dm.d == 128)
-    HERALD_CHECK_LAUNCH((nt == 1 ? launch_rows<128, 1>(a, R, st) : launch_rows<128, 2>(a, R, st)));
+  a.ctas = std::min(kKv4MaxCtas, tc ? num_sms : (nt == 1 ? 2 : 1) * num_sms);
+  if (tc)
+    HERALD_CHECK_LAUNCH(launch_kv4_attn_tc(dm.d, R, a, reinterpret_cast<uint32_t*>(p), st));
+  else if (dm.d == 128)
+    HERALD_CHECK_LAUNCH((nt == 1 ? launch_rows<128, 1>(a, st) : launch_rows<128, 2>(a, st)));
   else
-    HERALD_CHECK_LAUNCH((nt == 1 ? launch_rows<64, 1>(a, R, st) : launch_rows<64, 2>(a, R, st)));
-  const int blk_units = bk ? cdiv(dm.B, kKv4Unit) : 0;
-  const dim3 jg(unsigned(dm.N * dm.Hkv), unsigned(cdiv(R, 256 / (dm.d / 4))));
+    HERALD_CHECK_LAUNCH((nt == 1 ? launch_rows<64, 1>(a, st) : launch_rows<64, 2>(a, st)));
+  const int unit = tc ? kKv4TcKeys : kKv4Unit;
+  const int blk_units = bk ? cdiv(dm.B, unit) : 0, min_share = tc ? 1 : kKv4MinShare;
+  const int subs = tc && R <= kTileM ? 2 : 1;
+  const dim3 grid(unsigned(dm.N * dm.Hkv), unsigned(R));
   if (dm.d == 128)
-    HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<128>, jg, dim3(256), 0, st, a,
-                                 kKv4Unit, blk_units, kKv4MinShare));
+    HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<128>, grid,
+                                 dim3(kKv4JoinThreads), 0, st, a, unit, blk_units, min_share, subs));
   else
-    HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<64>, jg, dim3(256), 0, st, a,
-                                 kKv4Unit, blk_units, kKv4MinShare));
+    HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<64>, grid,
+                                 dim3(kKv4JoinThreads), 0, st, a, unit, blk_units, min_share, subs));
   return cudaGetLastError();
 }
 

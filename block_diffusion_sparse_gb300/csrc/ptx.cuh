@@ -29,6 +29,7 @@ enum : uint32_t {
   DEV_K_ATTN_POOL = 6u << 8,
   DEV_K_SCAN = 7u << 8,
   DEV_K_ATTN_FLASH = 8u << 8,
+  DEV_K_KV4_ATTN = 9u << 8,
 };
 
 // Checks of the debug build (compiled with -DHERALD_DEBUG): a kernel compares
@@ -174,6 +175,15 @@ HERALD_DEV void bulk_copy_to_peer(uint32_t dst_cluster, const void* src, uint32_
       "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes"
       " [%0], [%1], %2, [%3];" ::"r"(dst_cluster),
       "r"(smem_u32(src)), "r"(bytes), "r"(mbar_cluster)
+      : "memory");
+}
+// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) from
+// global to this CTA's shared memory, completing on its mbarrier.
+HERALD_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
 HERALD_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }

@@ -82,7 +82,14 @@ ATTN = [
     (3, 16, 4, 128, 32, 16, [0, 1, 2047], False),  # 128 rows
     (1, 5, 5, 64, 256, 32, [77], True),        # one head a group, 256 tokens
     (40, 2, 1, 64, 2, 16, list(range(40)), True),
-    (1, 32, 8, 128, 17, 64, [130], True),      # 68 rows
+    (1, 32, 8, 128, 17, 64, [130], True),     # 68 rows
+    # several tiles and segments per CTA of the tensor-core kernel
+    (8, 32, 8, 128, 32, 128, [1024, 0, 900, 1, 128, 1000, 640, 777], True),
+    (8, 32, 8, 128, 32, 128, [1024, 0, 900, 1, 128, 1000, 640, 777], False),
+    (6, 28, 4, 128, 32, 64, [1600, 0, 1200, 1, 1500, 1111], True),
+    (9, 16, 8, 64, 20, 16, [1000, 0, 900, 1, 128, 1000, 640, 777, 130], True),
+    (2, 8, 8, 128, 200, 32, [2000, 1300], True),  # two block tiles
+    (30, 40, 8, 64, 8, 32, [int(x) for x in range(0, 1500, 50)], True),
 ]
 
 
