@@ -81,7 +81,7 @@ struct Kv4AttnArgs {
   const uint16_t *q, *bk, *bv;
   const int32_t* ctx;
   uint16_t* out;
-  float* opart;  // [slots][R16][D]
+  float* opart;  // [slots][D/4][R16][4]
   float2* ml;    // [slots][R16]
   float scale;
   int N, Hq, Hkv, B, L_max, R16, ctas;

@@ -420,7 +420,9 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
     const bool whole = u0 == 0 && u1 == units;  // no other piece of this segment
     const int slot = int(blockIdx.x) + seg;
     for (int i = threadIdx.x; i < RT * (D / 4); i += kKv4Threads) {
-      const int rr = i / (D / 4), c4 = i % (D / 4), r = rr;
+      // (neighbouring threads write neighbouring channels of out, rows of a partial)
+      const int rr = whole ? i / (D / 4) : i % RT, c4 = whole ? i % (D / 4) : i / RT;
+      const int r = rr;
       if (r >= R) continue;
       float M = -FLT_MAX;
 #pragma unroll
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
                                   c4 * 4) =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
       } else {
-        *reinterpret_cast<float4*>(a.opart + (size_t(slot) * a.R16 + r) * D + c4 * 4) = acc;
+        reinterpret_cast<float4*>(a.opart)[(size_t(slot) * (D / 4) + c4) * a.R16 + r] = acc;
         if (c4 == 0) a.ml[size_t(slot) * a.R16 + r] = make_float2(M, L);
       }
     }
@@ -452,36 +454,40 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
 }
 
 // Joins the pieces of every segment that has more than one, and writes zeros
-// for segments without keys.  grid (N*Hkv, R), one CTA per row: D/4 threads
-// hold four channels each, and kKv4JoinThreads / (D/4) groups of them take
-// every such-and-suchth piece, so that the pieces of a long context travel at
-// once; the groups are added in order.  subs: partials per piece (slots subs*p
-// ...); with more than one, single pieces are joined here too.
-constexpr int kKv4JoinThreads = 256;
+// for segments without keys.  grid (N*Hkv, ceil(R / 8)), 1024 threads: eight
+// rows' chunks of four channels per D/4 * 8 threads, and kKv4JoinThreads over
+// that many groups, each with every such-and-suchth partial, four in flight, so
+// that the pieces of a long context travel at once; the groups are added in
+// order.  subs: partials per piece (slots subs*p ...); with more than one,
+// single pieces are joined here too.
+constexpr int kKv4JoinThreads = 1024, kKv4JoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(kKv4JoinThreads)
     kv4_join_kernel(const Kv4AttnArgs a, int unit, int blk_units, int min_share, int subs) {
-  constexpr int TPR = D / 4, GR = kKv4JoinThreads / TPR;
-  __shared__ float4 part[GR][TPR];
-  __shared__ float part_m[GR], part_l[GR];
+  constexpr int TPG = kKv4JoinRows * (D / 4), GR = kKv4JoinThreads / TPG;
+  __shared__ float4 part[GR][TPG];
+  __shared__ float part_m[GR][kKv4JoinRows], part_l[GR][kKv4JoinRows];
   griddep_enter();
   const int seg = blockIdx.x, n = seg / a.Hkv, g = seg - n * a.Hkv;
-  const int G = a.Hq / a.Hkv, r = blockIdx.y;
-  const int c4 = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const int G = a.Hq / a.Hkv, R = a.B * G;
+  const int grp = threadIdx.x / TPG, item = threadIdx.x % TPG;
+  const int rr = item % kKv4JoinRows, c4 = item / kKv4JoinRows;
+  const int r = int(blockIdx.y) * kKv4JoinRows + rr, rc = min(r, R - 1);
   const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, unit, blk_units), a.Hkv,
                                    a.ctas, min_share);
   const int units = kv4_units(a.ctx[n], a.L_max, unit, blk_units);
   const int64_t first = int64_t(a.Hkv) * kv4_total_units(a.ctx, n, a.L_max, unit, blk_units) +
                         int64_t(g) * units;
   uint2* out = reinterpret_cast<uint2*>(
-      a.out + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c4 * 4);
+      a.out + ((size_t(n) * a.B + rc / G) * a.Hq + g * G + rc % G) * D + c4 * 4);
   if (units == 0) {
-    if (grp == 0) *out = make_uint2(0, 0);
+    if (grp == 0 && r < R) *out = make_uint2(0, 0);
     return;
   }
   int c0 = int(first / split.share), c1 = int((first + units - 1) / split.share);
   if (c0 == c1 && subs == 1) return;  // one piece: written by the attention kernel
   c0 = (c0 + seg) * subs, c1 = (c1 + seg) * subs + subs - 1;  // its partials
+  const float4* op = reinterpret_cast<const float4*>(a.opart) + size_t(c4) * a.R16 + rc;
   float M = -FLT_MAX, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kFly = 4;
@@ -491,8 +497,8 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
 #pragma unroll
     for (int i = 0; i < kFly; ++i) {
       const int ci = min(c + i * GR, c1);
-      p[i] = a.ml[size_t(ci) * a.R16 + r];
-      x[i] = *reinterpret_cast<const float4*>(a.opart + (size_t(ci) * a.R16 + r) * D + c4 * 4);
+      p[i] = a.ml[size_t(ci) * a.R16 + rc];
+      x[i] = op[size_t(ci) * (D / 4) * a.R16];
       if (c + i * GR > c1) p[i] = make_float2(-FLT_MAX, 0.f), x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float M1 = M;
@@ -508,19 +514,19 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
       acc.x += f * x[i].x, acc.y += f * x[i].y, acc.z += f * x[i].z, acc.w += f * x[i].w;
     }
   }
-  part[grp][c4] = acc;
-  if (c4 == 0) part_m[grp] = M, part_l[grp] = L;
+  part[grp][item] = acc;
+  if (c4 == 0) part_m[grp][rr] = M, part_l[grp][rr] = L;
   __syncthreads();
-  if (grp != 0) return;
+  if (grp != 0 || r >= R) return;
 #pragma unroll
-  for (int i = 0; i < GR; ++i) M = fmaxf(M, part_m[i]);
+  for (int i = 0; i < GR; ++i) M = fmaxf(M, part_m[i][rr]);
   L = 0.f;
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < GR; ++i) {
-    const float f = fast_exp2(part_m[i] - M);
-    const float4 x = part[i][c4];
-    L += f * part_l[i];
+    const float f = fast_exp2(part_m[i][rr] - M);
+    const float4 x = part[i][item];
+    L += f * part_l[i][rr];
     acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
   }
   const float inv = L == 0.f ? 0.f : a.c.v_scale / L;
@@ -578,7 +584,7 @@ cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4D
   const int unit = tc ? kKv4TcKeys : kKv4Unit;
   const int blk_units = bk ? cdiv(dm.B, unit) : 0, min_share = tc ? 1 : kKv4MinShare;
   const int subs = tc && R <= kTileM ? 2 : 1;
-  const dim3 grid(unsigned(dm.N * dm.Hkv), unsigned(R));
+  const dim3 grid(unsigned(dm.N * dm.Hkv), unsigned(cdiv(R, kKv4JoinRows)));
   if (dm.d == 128)
     HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<128>, grid,
                                  dim3(kKv4JoinThreads), 0, st, a, unit, blk_units, min_share, subs));

@@ -7,21 +7,22 @@
 // 128 keys, a segment's block keys first):
 //   warp 17      copies the codes and scales of a tile's pages into a raw ring
 //                (bulk copies; the pages of a tile in parallel lanes)
-//   warps 8-15   turn raw items (the K or the V half of a tile) into fp16
-//                128-byte-swizzled operand buffers; stage the queries
-//   warps 16, 18 one tcgen05.mma issuer per stream: S = Q K^T into the stream's
-//                scores, O += P V with P read from tensor memory
-//   warps 0-3, 4-7 one softmax warpgroup per stream, a thread per query row
-// Two streams, each with 128 TMEM columns of scores (P, fp16, overlays them)
-// and 128 of output, run side by side so that one stream's products fill the
-// other's softmax: with more than 128 rows a stream is a row tile and takes
-// every key tile, else both streams have the same rows and take alternate key
-// tiles (their partial outputs are joined like those of two CTAs).
+//   warps 8-11, 12-15 turn the K and the V items (halves of a tile) of the raw
+//                ring into fp16 128-byte-swizzled operand buffers; together
+//                they stage the queries
+//   warps 16, 18 one tcgen05.mma issuer per stream: S = Q K^T into a score
+//                buffer, O += P V with P read from tensor memory
+//   warps 0-3, 4-7 softmax of a stream, a thread per query row
+// Two streams run side by side: with more than 128 rows a stream is a row tile
+// and takes every key tile, else both streams have the same rows and take
+// alternate key tiles (their partial outputs are joined like those of two
+// CTAs).  A stream goes in steps of 64 keys through two score buffers of 64
+// TMEM columns (P, fp16, overlays the scores), so the scores of a step are
+// there when the softmax of the step before is done; O takes 128 columns: the
+// two streams fill the 512.
 //
-// The softmax is optimistic: probabilities are formed with the row's present
-// exponent base in the pass that finds the row's maximum, and only a maximum
-// more than 15 (log2) above the base repeats the pass after moving the base to
-// 11 below it (P stays in fp16's range, see kv4_attn.cu).
+// A row's exponent base moves only when its maximum stands more than 15 (log2)
+// above it, to 11 below the maximum (P stays in fp16's range, see kv4_attn.cu).
 //
 // The block's own keys are bf16: their tiles come first in a segment, with
 // the queries staged as bf16 (an mma's operands have one type), then the
@@ -34,6 +35,7 @@
 namespace herald {
 
 constexpr int kTcKeys = kKv4TcKeys;        // keys per tile
+constexpr int kTcStep = 64;                // keys per step of a stream
 constexpr int kTcBufs = 4;                 // operand buffers (128 keys of K or V)
 constexpr int kTcRaw = 3;                  // raw items
 constexpr int kTcMasks = 8;                // tiles whose key masks are kept
@@ -54,10 +56,10 @@ enum : uint32_t {
 // starts no copy or product any more), and the kernel returns.
 struct TcWait {
   volatile uint32_t* failed;  // shared: the wait that ran out first
-  HERALD_DEV bool operator()(uint64_t* bar, uint32_t parity, uint32_t which) const {
-    if (mbar_try_wait(bar, parity)) return true;
+  HERALD_DEV bool slow(uint64_t* bar, uint32_t parity, uint32_t which) const {
     const uint64_t t0 = globaltimer_ns();
     while (true) {
+#pragma unroll 1
       for (int i = 0; i < 64; ++i)
         if (mbar_try_wait(bar, parity)) return true;
       if (*failed) return false;
@@ -67,11 +69,11 @@ struct TcWait {
       }
     }
   }
-  // The same answer for a whole warp, which leaves converged: lanes may see a
+  // The answer for a whole warp, which leaves converged: lanes may see a
   // barrier complete in different polls, and the tensor-memory instructions
   // that follow (.sync.aligned) want the warp in one piece.
-  HERALD_DEV bool warp(uint64_t* bar, uint32_t parity, uint32_t which) const {
-    const bool ok = (*this)(bar, parity, which);
+  HERALD_DEV bool operator()(uint64_t* bar, uint32_t parity, uint32_t which) const {
+    const bool ok = mbar_try_wait(bar, parity) || slow(bar, parity, which);
     return __all_sync(0xffffffffu, ok);
   }
 };
@@ -108,7 +110,78 @@ HERALD_DEV void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-HERALD_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for this thread's tensor-memory loads; r (loaded before) counts as
+// written here, so that no use of it moves above the wait.
+HERALD_DEV void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                 "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])
+               :
+               : "memory");
+}
+
+// Scores of keys that do not count become -inf: those without a bit in msk (two
+// words), or, without msk, all but the first nk of the 64.
+HERALD_DEV void mask_scores(uint32_t ts, const uint32_t* msk, int nk) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const int left = nk - 32 * c;
+    const uint32_t k = msk ? msk[c] : left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+    if (k == ~0u) continue;
+    uint32_t r[32];
+    tmem_ld32_nowait(ts + uint32_t(c) * 32u, r);
+    tmem_wait_ld(r);
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = (k >> i & 1) ? __uint_as_float(r[i]) : -INFINITY;
+    tmem_st32(ts + uint32_t(c) * 32u, v);
+  }
+  tmem_wait_st();
+}
+
+// 32 scores -> probabilities 2^(s f - m), summed into *sum.
+HERALD_DEV void exp32(uint32_t (&x)[32], uint64_t f2, uint64_t nm2, uint64_t* sum) {
+  uint64_t sa = *sum, sb = f2_pack(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float t0, t1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2, nm2), t0, t1);
+    const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+    if (i & 2)
+      sa = f2_add(sa, f2_pack(p0, p1));
+    else
+      sb = f2_add(sb, f2_pack(p0, p1));
+    x[i] = __float_as_uint(p0);
+    x[i + 1] = __float_as_uint(p1);
+  }
+  *sum = f2_add(sa, sb);
+}
+// 32 probabilities -> 16 packed columns at ts.  blk: bf16, times iv (P in units
+// of v_scale: O has one unit for all keys), else fp16.
+HERALD_DEV void store_p32(uint32_t ts, const uint32_t (&x)[32], bool blk, float iv) {
+  uint32_t pk[16];
+  if (blk) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      pk[i] = pack_bf16(__uint_as_float(x[2 * i]) * iv, __uint_as_float(x[2 * i + 1]) * iv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      pk[i] = pack_half2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+  }
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(ts),
+      "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]),
+      "r"(pk[7]), "r"(pk[8]), "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]),
+      "r"(pk[14]), "r"(pk[15])
+      : "memory");
+}
 
 template <int D, int MT>
 __global__ void __launch_bounds__(kTcThreadsAll, 1)
@@ -118,10 +191,16 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   constexpr int kRowC = D / 2, kRowS = D / 16;           // raw bytes of a row
   constexpr uint32_t kRawBytes = kTcKeys * (kRowC + kRowS);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t raw_full[kTcRaw], raw_free[kTcRaw], buf_full[kTcBufs], buf_free[kTcBufs];
-  __shared__ uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2], all_done[2], mask_full[kTcMasks];
+  // [K or V][tile % kTcRaw]: each side of the conversion waits for every phase of
+  // its own barriers (a slot serves K and V items in turn)
+  __shared__ uint64_t raw_full[2][kTcRaw], raw_free[2][kTcRaw];
+  __shared__ uint64_t buf_full[kTcBufs], buf_free[kTcBufs];
+  __shared__ uint64_t q_full, q_free, s_full[2][2], p_full[2][2], pv_done[2], o_done[2];
+  __shared__ uint64_t all_done[2];
+  __shared__ uint64_t mask_full[kTcMasks];
   __shared__ uint32_t tmem_base;
   __shared__ uint32_t failed;
+  __shared__ uint32_t missing;                      // a position below a length had no page
   __shared__ float row_f[2 * kTileM];               // score factors of the rows (cache tiles)
   __shared__ uint32_t key_mask[kTcMasks][4];        // bit: the key counts
   const TcSmem L = tc_smem(D, MT);
@@ -129,15 +208,18 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   uint8_t *Qs = base + L.q, *Bs = base + L.buf, *Rs = base + L.raw;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kTcRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 8);
-    for (int i = 0; i < kTcBufs; ++i) mbar_init(&buf_full[i], 8), mbar_init(&buf_free[i], MT);
+    for (int i = 0; i < 2 * kTcRaw; ++i)
+      mbar_init(&raw_full[i & 1][i >> 1], 1), mbar_init(&raw_free[i & 1][i >> 1], 4);
+    for (int i = 0; i < kTcBufs; ++i) mbar_init(&buf_full[i], 4), mbar_init(&buf_free[i], MT);
     for (int i = 0; i < kTcMasks; ++i) mbar_init(&mask_full[i], 1);
     mbar_init(&q_full, 8);
     mbar_init(&q_free, 2 + kTcSoft);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&pv_done[i], 1),
+      mbar_init(&s_full[i][0], 1), mbar_init(&s_full[i][1], 1), mbar_init(&p_full[i][0], 128),
+          mbar_init(&p_full[i][1], 128), mbar_init(&pv_done[i], 1), mbar_init(&o_done[i], 1),
           mbar_init(&all_done[i], 1);
     failed = 0;
+    missing = 0;
     fence_mbar_init();
   }
   tmem_setup(&tmem_base, 512);
@@ -176,6 +258,10 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
       at = seg0 + u1;
     }
   };
+  // keys of tile u that can count
+  auto tile_keys = [&](int u, int ctx) {
+    return min(kTcKeys, u < blk_units ? a.B - u * kTcKeys : ctx - (u - blk_units) * kTcKeys);
+  };
 
   // registers: 640 threads launch with 96 each (61,440); 256 x 120 + 256 x 80 +
   // 128 x 64 = 59,392.  Each role's branch begins with its own setmaxnreg, so
@@ -188,131 +274,116 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
     const int row = (MT == 2 ? w * kTileM : 0) + lrow;
     const bool idle = (MT == 2 ? w * kTileM : 0) + (warp & 3) * 32 >= R;  // the warp has no rows
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t ts = tm + lanes + uint32_t(w) * 128u, to = tm + lanes + 256u + uint32_t(w) * 128u;
-    uint32_t tile = 0, ns = 0, mt = 0, phase = 0;  // tiles of the CTA, of this stream, masks
+    const uint32_t ts0 = tm + lanes + uint32_t(w) * 128u, to = ts0 + 256u;
+    const float iv = 1.f / a.c.v_scale;
+    uint32_t tile = 0, ns = 0, mt = 0, phase = 0;  // tiles of the CTA, steps of the stream, masks
+    uint32_t no = 0;                               // pieces with a step of this stream
     pieces([&](int n, int g, int seg, int ctx, int units, int u0, int u1) -> bool {
       debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
       float m = -FLT_MAX, l = 0.f;
-      bool any = false;  // this stream has had a tile of the piece
+      bool any = false;  // this stream has had a step of the piece
       int u = u0;
       while (u < u1) {  // a phase: block tiles, or cache tiles
         const bool blk = u < blk_units;
         const int pe = blk ? min(u1, blk_units) : u1;
-        // the phase's queries are staged (so this stream's arrivals on q_free
-        // below never run into an earlier phase, with or without tiles here)
-        if (!wait.warp(&q_full, phase & 1, W_Q_FULL)) return false;
+        // the phase's queries are staged (so this thread's arrival on q_free
+        // below never runs into an earlier phase, with or without tiles here)
+        if (!wait(&q_full, phase & 1, W_Q_FULL)) return false;
         const float f = blk ? fminf(a.scale * 1.4426950408889634f, FLT_MAX)
                             : *(volatile float*)&row_f[row];
+        const uint64_t f2 = f2_pack(f, f);
         for (; u < pe; ++u, ++tile) {
           const uint32_t mask_no = mt;
           if (!blk) ++mt;
           if (MT == 1 && int(tile & 1) != w) continue;
-          if (!wait.warp(&s_full[w], ns & 1, W_S_FULL)) return false;
-          tc_fence_after();
-          uint32_t msk[4] = {~0u, ~0u, ~0u, ~0u};
-          if (!blk) {
-            const uint32_t i = mask_no % kTcMasks;
-            if (!wait.warp(&mask_full[i], (mask_no / kTcMasks) & 1, W_MASK)) return false;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) msk[c] = *(volatile uint32_t*)&key_mask[i][c];
-          } else {
-            const int nk = a.B - u * kTcKeys;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              msk[c] = nk >= 32 * c + 32 ? ~0u : nk <= 32 * c ? 0u : (1u << (nk - 32 * c)) - 1u;
-          }
-          const bool part = (msk[0] & msk[1] & msk[2] & msk[3]) != ~0u;
-          if (!idle) {
-            uint32_t pk[64];
-            while (true) {
-              float mx = -INFINITY;
-              uint64_t sum2 = f2_pack(0.f, 0.f);
-              const uint64_t f2 = f2_pack(f, f), nm2 = f2_pack(-m, -m);
-              const float iv = 1.f / a.c.v_scale;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint32_t r[32];
-                tmem_ld32_nowait(ts + uint32_t(c) * 32u, r);
-                tmem_wait_ld();
-                if (part) {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    if (!(msk[c] >> i & 1)) r[i] = __float_as_uint(-INFINITY);
+          const int keys = tile_keys(u, ctx);
+#pragma unroll 1
+          for (int k0 = 0; k0 < keys; k0 += kTcStep, ++ns) {
+            const uint32_t b = ns & 1, ts = ts0 + b * 64u;
+            if (!wait(&s_full[w][b], (ns >> 1) & 1, W_S_FULL)) return false;
+            tc_fence_after();
+            if (!idle) {
+              if (keys < k0 + kTcStep || (!blk && *(volatile uint32_t*)&missing)) {
+                const uint32_t* msk = nullptr;
+                if (!blk) {
+                  const uint32_t i = mask_no % kTcMasks;
+                  if (!wait(&mask_full[i], (mask_no / kTcMasks) & 1, W_MASK)) return false;
+                  msk = key_mask[i] + k0 / 32;
                 }
-#pragma unroll
-                for (int i = 0; i < 32; i += 2)
-                  mx = fmax3f(mx, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  float x0, x1;
-                  f2_unpack(f2_fma(f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
-                                   f2, nm2),
-                            x0, x1);
-                  const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                  sum2 = f2_add(sum2, f2_pack(p0, p1));
-                  // (block tiles: P in units of v_scale, O has one unit for all keys)
-                  pk[c * 16 + i] = blk ? pack_bf16(p0 * iv, p1 * iv) : pack_half2(p0, p1);
-                }
+                mask_scores(ts, msk, keys - k0);
               }
+              uint32_t x[2][32];
+              tmem_ld32_nowait(ts, x[0]);
+              tmem_ld32_nowait(ts + 32u, x[1]);
+              tmem_wait_ld(x[0]);
+              tmem_wait_ld(x[1]);
+              float mx = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                mx = fmax3f(mx, __uint_as_float(x[0][i]), __uint_as_float(x[0][i + 1]));
+                mx1 = fmax3f(mx1, __uint_as_float(x[1][i]), __uint_as_float(x[1][i + 1]));
+              }
+              mx = fmaxf(mx, mx1);
               const bool move = mx * f - m > kTcAbove;
-              if (!__any_sync(0xffffffffu, move)) {
-                float s0, s1;
-                f2_unpack(sum2, s0, s1);
-                l += s0 + s1;
-                break;
-              }
-              float k = 1.f;
-              if (move) {
-                const float b = mx * f - kTcBelow;
-                k = fast_exp2(m - b);
-                m = b;
-                l *= k;
-              }
-              __syncwarp();
-              if (any) {  // (every earlier P V of the stream is done: S was issued after it)
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                  uint32_t r[32];
-                  tmem_ld32_nowait(to + uint32_t(c) * 32u, r);
-                  tmem_wait_ld();
-                  float v[32];
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * k;
-                  tmem_st32(to + uint32_t(c) * 32u, v);
+              if (__any_sync(0xffffffffu, move)) {
+                float k = 1.f;
+                if (move) {
+                  const float nb = mx * f - kTcBelow;
+                  k = fast_exp2(m - nb);
+                  m = nb;
+                  l *= k;
                 }
-                tmem_wait_st();
+                // O so far, once the P V of the step before is in it (that of two
+                // steps before is: this step's scores took its buffer)
+                if (any) {
+                  if (!wait(&pv_done[w], (ns - 1) & 1, W_O_DONE)) return false;
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32_nowait(to + uint32_t(c) * 32u, r);
+                    tmem_wait_ld(r);
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * k;
+                    tmem_st32(to + uint32_t(c) * 32u, v);
+                  }
+                  tmem_wait_st();
+                }
               }
-            }
-            {
-              float v[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(pk[i]);
-              tmem_st32(ts, v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(pk[32 + i]);
-              tmem_st32(ts + 32u, v);
+              const uint64_t nm2 = f2_pack(-m, -m);
+              uint64_t sum = f2_pack(0.f, 0.f);
+              exp32(x[0], f2, nm2, &sum);
+              store_p32(ts, x[0], blk, iv);
+              exp32(x[1], f2, nm2, &sum);
+              store_p32(ts + 16u, x[1], blk, iv);
+              float s0, s1;
+              f2_unpack(sum, s0, s1);
+              l += s0 + s1;
               tmem_wait_st();
             }
+            tc_fence_before();
+            // (one barrier per buffer: a warp may be a step ahead of another)
+            mbar_arrive(&p_full[w][b]);
+            any = true;
           }
-          tc_fence_before();
-          mbar_arrive(&p_full[w]);
-          any = true;
-          ++ns;
         }
         mbar_arrive(&q_free);  // (this thread has read its factor of the phase)
         ++phase;
       }
-      // the piece's rows: O once the last P V is done
+      // the piece's rows: O once the last P V is done (pv_done would not tell:
+      // the last two may both be under way)
       if (any) {
-        if (!wait.warp(&pv_done[w], (ns - 1) & 1, W_O_DONE)) return false;
+        if (!wait(&o_done[w], no & 1, W_O_DONE)) return false;
         tc_fence_after();
+        ++no;
       }
       if (!idle) {
         const bool whole = MT == 2 && u0 == 0 && u1 == units;
         const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
         const int slot = MT == 2 ? int(blockIdx.x) + seg : 2 * (int(blockIdx.x) + seg) + w;
         const bool on = row < R;
-        float* part = a.opart + (size_t(slot) * a.R16 + row) * D;
+        float4* part = reinterpret_cast<float4*>(a.opart) + size_t(slot) * (D / 4) * a.R16 + row;
         uint16_t* out =
             a.out + ((size_t(n) * a.B + (on ? row / G : 0)) * a.Hq + g * G + (on ? row % G : 0)) * D;
 #pragma unroll 1
@@ -320,7 +391,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
           uint32_t r[32];
           if (any) {
             tmem_ld32_nowait(to + uint32_t(c) * 32u, r);
-            tmem_wait_ld();
+            tmem_wait_ld(r);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) r[i] = 0;
@@ -333,11 +404,12 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                   pack_bf16(__uint_as_float(r[i + 2]) * inv, __uint_as_float(r[i + 3]) * inv),
                   pack_bf16(__uint_as_float(r[i + 4]) * inv, __uint_as_float(r[i + 5]) * inv),
                   pack_bf16(__uint_as_float(r[i + 6]) * inv, __uint_as_float(r[i + 7]) * inv));
-          } else if (on) {
+          } else if (on) {  // neighbouring rows of a warp are neighbours in memory
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(part + c * 32 + i) =
-                  make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+              part[size_t(c * 8 + i / 4) * a.R16] =
+                  make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
+                              __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
           }
           __syncwarp();
         }
@@ -350,20 +422,20 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     // --------------------------------------- queries, operand conversion
-    const int ct = threadIdx.x - kTcSoft, cw = warp - 8;
-    uint32_t item = 0, raw_no = 0, mt = 0, phase = 0;
+    const int ct = threadIdx.x - kTcSoft;
+    const int kv = (warp - 8) >> 2, cw = warp & 3;  // K or V items; warp of the four
+    uint32_t tile = 0, mt = 0, phase = 0;
     auto publish = [&](uint64_t* bar) {  // this warp's writes are ready for the tensor cores
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    pieces([&](int n, int g, int, int ctx, int, int u0, int u1) -> bool {
-      (void)ctx;
+    pieces([&](int n, int g, int, int, int, int u0, int u1) -> bool {
       int u = u0;
       while (u < u1) {
         const bool blk = u < blk_units;
         const int pe = blk ? min(u1, blk_units) : u1;
-        if (phase > 0 && !wait.warp(&q_free, (phase - 1) & 1, W_Q_FREE)) return false;
+        if (phase > 0 && !wait(&q_free, (phase - 1) & 1, W_Q_FREE)) return false;
         // queries: D/16 lanes per row, 16 channels each
         constexpr int LPR = D / 16;
         for (int r0 = ct / LPR; r0 < MT * kTileM; r0 += kTcConv / LPR) {
@@ -397,76 +469,83 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
         }
         publish(&q_full);
         ++phase;
-        for (; u < pe; ++u) {
-          const uint32_t mask_no = mt;
-          if (!blk) ++mt;
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++item) {
-            const uint32_t b = item % kTcBufs;
+        for (; u < pe; ++u, ++tile) {
+          const uint32_t item = 2 * tile + uint32_t(kv), b = item % kTcBufs;
+          uint8_t* dst = Bs + b * kTile;
+          if (blk) {  // bf16 rows of the block, zeros after them
             if (item >= uint32_t(kTcBufs) &&
-                !wait.warp(&buf_free[b], (item / kTcBufs - 1) & 1, W_BUF_FREE))
+                !wait(&buf_free[b], (item / kTcBufs - 1) & 1, W_BUF_FREE))
               return false;
-            uint8_t* dst = Bs + b * kTile;
-            if (blk) {  // bf16 rows of the block, zeros after them
-              const uint16_t* src = kv ? a.bv : a.bk;
-              constexpr int CPR = D / 8;  // 16-byte chunks of a row
-#pragma unroll 4
-              for (int i = ct; i < kTcKeys * CPR; i += kTcConv) {
-                const int r = i / CPR, c = i % CPR, j = u * kTcKeys + r;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (j < a.B)
-                  v = *reinterpret_cast<const uint4*>(
-                      src + ((size_t(n) * a.B + j) * a.Hkv + g) * D + c * 8);
-                *reinterpret_cast<uint4*>(dst + uint32_t(c >> 3) * 16384u +
-                                          sw128_off(uint32_t(r), uint32_t(c & 7))) = v;
-              }
-            } else {
-              const uint32_t rb = raw_no % kTcRaw;
-              if (!wait.warp(&raw_full[rb], (raw_no / kTcRaw) & 1, W_RAW_FULL)) return false;
-              const uint8_t* rc = Rs + rb * kRawBytes;
-              const uint8_t* rsc = rc + kTcKeys * kRowC;
-              // A lane turns chunks of 16 bytes (32 channels): chunk j of row
-              // r.  Rows and chunks are dealt so that the eight lanes of a
-              // shared-memory phase read eight different 16-byte bank groups
-              // ((r&1)*4 + j for d = 128, (r&3)*2 + j for 64) and write eight
-              // (the swizzle's XOR of r&7 with the chunk).
-              constexpr int kTasks = kTcKeys * (kRowC / 16) / kTcConv;
-#pragma unroll
-              for (int s = 0; s < kTasks; ++s) {
-                int r, j;
-                if constexpr (D == 128) {
-                  const int j1 = (lane >> 2) & 1;
-                  j = ((lane >> 1) & 1) + 2 * j1;
-                  r = cw * 16 + (lane >> 3) * 4 + (lane & 1) + 2 * (j1 ^ s);
-                } else {
-                  j = lane & 1;
-                  r = cw * 16 + (lane >> 1);
-                }
-                const uint4 cw4 = *reinterpret_cast<const uint4*>(rc + r * kRowC + j * 16);
-                uint32_t sc = *reinterpret_cast<const uint16_t*>(rsc + r * kRowS + j * 2);
-                // a value row that does not count may hold any bytes: 0 * NaN must not arise
-                if (kv && !(*(volatile uint32_t*)&key_mask[mask_no % kTcMasks][r >> 5] >> (r & 31) & 1))
-                  sc = 0;
-                const uint32_t s2 = e4m3x2_to_half2(sc);
-                const uint32_t words[4] = {cw4.x, cw4.y, cw4.z, cw4.w};
-                uint8_t* half = dst + uint32_t(D == 128 ? j >> 1 : 0) * 16384u;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  uint32_t h[4];
-                  e2m1x8_to_half2(words[k], h);
-                  const uint32_t fs = __byte_perm(s2, 0, k < 2 ? 0x1010 : 0x3232);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) h[i] = hmul2(h[i], fs);
-                  *reinterpret_cast<uint4*>(half + sw128_off(uint32_t(r), uint32_t((j & 1) * 4 + k))) =
-                      make_uint4(h[0], h[1], h[2], h[3]);
-                }
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&raw_free[rb]);
-              ++raw_no;
+            const uint16_t* src = kv ? a.bv : a.bk;
+            constexpr int CPR = D / 8;  // 16-byte chunks of a row
+#pragma unroll 1
+            for (int i = ct & 127; i < kTcKeys * CPR; i += 128) {
+              const int r = i / CPR, c = i % CPR, j = u * kTcKeys + r;
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (j < a.B)
+                v = *reinterpret_cast<const uint4*>(
+                    src + ((size_t(n) * a.B + j) * a.Hkv + g) * D + c * 8);
+              *reinterpret_cast<uint4*>(dst + uint32_t(c >> 3) * 16384u +
+                                        sw128_off(uint32_t(r), uint32_t(c & 7))) = v;
             }
-            publish(&buf_full[b]);
+          } else {
+            const uint32_t rm = mt % kTcRaw;
+            if (!wait(&raw_full[kv][rm], (mt / kTcRaw) & 1, W_RAW_FULL)) return false;
+            const uint8_t* rc = Rs + (2 * mt + uint32_t(kv)) % kTcRaw * kRawBytes;
+            const uint8_t* rsc = rc + kTcKeys * kRowC;
+            // A lane turns chunks of 16 bytes (32 channels): chunk j of row r.
+            // Rows and chunks are dealt so that the eight lanes of a
+            // shared-memory phase read eight different 16-byte bank groups
+            // ((r&1)*4 + j for d = 128, (r&3)*2 + j for 64) and write eight (the
+            // swizzle's XOR of r&7 with the chunk).  All raw bytes are taken
+            // first: the copies of a later item start while these are turned.
+            constexpr int kTasks = kTcKeys * (kRowC / 16) / 128;
+            uint4 code[kTasks];
+            uint32_t sc[kTasks];
+            const int j1 = (lane >> 2) & 1;
+            const int j = D == 128 ? ((lane >> 1) & 1) + 2 * j1 : lane & 1;
+            auto row_of = [&](int s) {
+              return D == 128 ? cw * 32 + (s >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) +
+                                    2 * (j1 ^ (s & 1))
+                              : cw * 32 + s * 16 + (lane >> 1);
+            };
+#pragma unroll
+            for (int s = 0; s < kTasks; ++s) {
+              const int r = row_of(s);
+              code[s] = *reinterpret_cast<const uint4*>(rc + r * kRowC + j * 16);
+              sc[s] = *reinterpret_cast<const uint16_t*>(rsc + r * kRowS + j * 2);
+            }
+            if (kv) {  // a value row that does not count may hold any bytes: no 0 * NaN
+              const uint32_t m = *(volatile uint32_t*)&key_mask[mt % kTcMasks][cw];
+#pragma unroll
+              for (int s = 0; s < kTasks; ++s)
+                if (!(m >> (row_of(s) & 31) & 1)) sc[s] = 0;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_free[kv][rm]);
+            if (item >= uint32_t(kTcBufs) &&
+                !wait(&buf_free[b], (item / kTcBufs - 1) & 1, W_BUF_FREE))
+              return false;
+            uint8_t* half = dst + uint32_t(D == 128 ? j >> 1 : 0) * 16384u;
+#pragma unroll
+            for (int s = 0; s < kTasks; ++s) {
+              const uint32_t r = uint32_t(row_of(s));
+              const uint32_t s2 = e4m3x2_to_half2(sc[s]);
+              const uint32_t words[4] = {code[s].x, code[s].y, code[s].z, code[s].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t h[4];
+                e2m1x8_to_half2(words[k], h);
+                const uint32_t fs = __byte_perm(s2, 0, k < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = hmul2(h[i], fs);
+                *reinterpret_cast<uint4*>(half + sw128_off(r, uint32_t((j & 1) * 4 + k))) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+              }
+            }
+            ++mt;
           }
+          publish(&buf_full[b]);
         }
       }
       return true;
@@ -487,17 +566,20 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
             debug_flag(phys < 0, DEV_BAD_INDEX);
             if (phys >= 0) keys = min(sub, ctx - pos);
           }
+          if (pos < ctx && k0 < kTcKeys && phys < 0) *(volatile uint32_t*)&missing = 1;
           const size_t row = phys >= 0 ? kv4_row(a.c, phys, a.Hkv, g, pos) : 0;
           const uint32_t rows = uint32_t(keys + 15) & ~15u;  // whole groups of 16: inside the page
           uint32_t total = rows;
-  #pragma unroll
+#pragma unroll
           for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  #pragma unroll 1
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++raw_no) {
-            const uint32_t rb = raw_no % kTcRaw;
+            const uint32_t rb = raw_no % kTcRaw;  // the slot held item raw_no - kTcRaw
+            const uint32_t was = raw_no - uint32_t(kTcRaw);
             if (raw_no >= uint32_t(kTcRaw) &&
-                !wait.warp(&raw_free[rb], (raw_no / kTcRaw - 1) & 1, W_RAW_FREE))
+                !wait(&raw_free[was & 1][(was >> 1) % kTcRaw], ((was >> 1) / kTcRaw) & 1, W_RAW_FREE))
               return false;
+            uint64_t* full = &raw_full[kv][mt % kTcRaw];
             if (kv == 0) {
               // (the masks of kTcMasks tiles back have been read: their V item
               // has left the operand ring, which is shorter)
@@ -510,14 +592,14 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(&mask_full[mt % kTcMasks]);
             }
-            if (lane == 0) mbar_arrive_expect_tx(&raw_full[rb], total * uint32_t(kRowC + kRowS));
+            if (lane == 0) mbar_arrive_expect_tx(full, total * uint32_t(kRowC + kRowS));
             __syncwarp();
             if (rows) {
               uint8_t* dst = Rs + rb * kRawBytes;
               bulk_load(dst + k0 * kRowC, (kv ? a.c.vc : a.c.kc) + row * kRowC, rows * kRowC,
-                        &raw_full[rb]);
+                        full);
               bulk_load(dst + kTcKeys * kRowC + k0 * kRowS, (kv ? a.c.vs : a.c.ks) + row * kRowS,
-                        rows * kRowS, &raw_full[rb]);
+                        rows * kRowS, full);
             }
           }
         }
@@ -527,65 +609,94 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
       // wait can one still be under way)
       if (*(volatile uint32_t*)&failed)
         for (uint32_t i = raw_no > uint32_t(kTcRaw) ? raw_no - kTcRaw : 0; i < raw_no; ++i)
-          mbar_wait(&raw_full[i % kTcRaw], (i / kTcRaw) & 1);
-    } else if (warp != kTcIdleWarp && lane == 0) {
+          mbar_wait(&raw_full[i & 1][(i >> 1) % kTcRaw], ((i >> 1) / kTcRaw) & 1);
+    } else if (warp != kTcIdleWarp) {
       // ------------------------------------------------------ MMA issuers
+      // (the whole warp walks the loops, lane 0 issues)
       const int w = warp == kTcMmaWarp0 ? 0 : 1;
-      const uint32_t ts = tm + uint32_t(w) * 128u, to = tm + 256u + uint32_t(w) * 128u;
-      const uint32_t qa = smem_u32(Qs) + (MT == 2 ? uint32_t(w) * kTile : 0u);
-      const uint32_t ba = smem_u32(Bs);
-      uint32_t tile = 0, ns = 0, phase = 0;
-      bool issued = false;
-      pieces([&](int, int, int, int, int, int u0, int u1) -> bool {
+      const uint32_t ts = tm + uint32_t(w) * 128u, to = ts + 256u;
+      // descriptors of buffer 0; other tiles and steps add to the address field
+      // (which never carries: 14 bits hold all of shared memory)
+      const uint64_t qd =
+          make_sdesc_sw128(smem_u32(Qs) + (MT == 2 ? uint32_t(w) * kTile : 0u), 16, 1024);
+      const uint64_t kd = make_sdesc_sw128(smem_u32(Bs), 16, 1024);
+      const uint64_t vd = make_sdesc_sw128(smem_u32(Bs), 16384u, 1024);
+      uint32_t tile0 = 0, np = 0, nsc = 0, phase = 0;  // tiles before the phase, P V, S issued
+      pieces([&](int, int, int, int ctx, int, int u0, int u1) -> bool {
         bool any = false;
         int u = u0;
         while (u < u1) {
           const bool blk = u < blk_units;
           const int pe = blk ? min(u1, blk_units) : u1;
-          const uint32_t ids =
-              blk ? make_idesc_bf16(kTileM, kTcKeys, false, false) : make_idesc_f16(kTileM, kTcKeys, false);
-          const uint32_t ido = blk ? make_idesc_bf16(kTileM, D, false, true) : make_idesc_f16(kTileM, D, true);
+          const uint32_t ids = blk ? make_idesc_bf16(kTileM, kTcStep, false, false)
+                                   : make_idesc_f16(kTileM, kTcStep, false);
+          const uint32_t ido =
+              blk ? make_idesc_bf16(kTileM, D, false, true) : make_idesc_f16(kTileM, D, true);
           if (!wait(&q_full, phase & 1, W_Q_FULL)) return false;
-          const uint32_t ns0 = ns;
-          for (; u < pe; ++u, ++tile) {
-            if (MT == 1 && int(tile & 1) != w) continue;
-            const uint32_t ki = 2 * tile, vi = ki + 1, kb = ki % kTcBufs, vb = vi % kTcBufs;
-            if (!wait(&buf_full[kb], (ki / kTcBufs) & 1, W_K_FULL)) return false;
-            // P of the stream's previous tile has been read
-            if (ns > 0 && !wait(&pv_done[w], (ns - 1) & 1, W_PV_DONE)) return false;
+          // a step: 64 keys of tile u + du, from key k0 on; this stream's tiles
+          const int stride = MT == 1 ? 2 : 1;
+          const int du0 = MT == 1 ? int((tile0 ^ uint32_t(w)) & 1u) : 0;
+          int sd = du0, sk = 0;  // the next S
+          auto issue_s = [&]() -> bool {
+            if (u + sd >= pe) return true;
+            const uint32_t ki = 2 * (tile0 + uint32_t(sd)), kb = ki % kTcBufs;
+            if (sk == 0 && !wait(&buf_full[kb], (ki / kTcBufs) & 1, W_K_FULL)) return false;
             tc_fence_after();
+            const uint64_t kt = kd + ((kb * kTile + uint32_t(sk) * 128u) >> 4);
+            const uint32_t sb = nsc & 1, td = ts + sb * 64u;
+            const bool last = sk + kTcStep >= tile_keys(u + sd, ctx);
+            if (lane == 0) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = uint32_t(ks >> 2) * 16384u + uint32_t(ks & 3) * 32u;
-              umma_bf16(ts, make_sdesc_sw128(qa + off, 16, 1024),
-                        make_sdesc_sw128(ba + kb * kTile + off, 16, 1024), ids, ks > 0 ? 1u : 0u);
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = (uint32_t(ks >> 2) * 16384u + uint32_t(ks & 3) * 32u) >> 4;
+                umma_bf16(td, qd + off, kt + off, ids, ks > 0 ? 1u : 0u);
+              }
+              umma_commit(&s_full[w][sb]);
+              if (last) umma_commit(&buf_free[kb]);
             }
-            issued = true;
-            umma_commit(&s_full[w]);
-            umma_commit(&buf_free[kb]);
-            if (!wait(&p_full[w], ns & 1, W_P_FULL)) return false;
-            if (!wait(&buf_full[vb], (vi / kTcBufs) & 1, W_V_FULL)) return false;
-            tc_fence_after();
+            __syncwarp();
+            ++nsc;
+            sk = last ? 0 : sk + kTcStep;
+            if (last) sd += stride;
+            return true;
+          };
+          if (!issue_s() || !issue_s()) return false;
+          for (int d = du0; u + d < pe; d += stride) {
+            const uint32_t vi = 2 * (tile0 + uint32_t(d)) + 1, vb = vi % kTcBufs;
+            const int keys = tile_keys(u + d, ctx);
+            for (int k0 = 0; k0 < keys; k0 += kTcStep) {
+              if (!wait(&p_full[w][np & 1], (np >> 1) & 1, W_P_FULL)) return false;
+              if (k0 == 0 && !wait(&buf_full[vb], (vi / kTcBufs) & 1, W_V_FULL)) return false;
+              tc_fence_after();
+              const uint64_t vt = vd + ((vb * kTile + uint32_t(k0) * 128u) >> 4);
+              const uint32_t tp = ts + (np & 1) * 64u, acc = any ? 1u : 0u;
+              if (lane == 0) {
 #pragma unroll
-            for (int ks = 0; ks < kTcKeys / 16; ++ks)
-              umma_bf16_ts(to, ts + uint32_t(ks) * 8u,
-                           make_sdesc_sw128(ba + vb * kTile + uint32_t(ks) * 2048u, 16384u, 1024),
-                           ido, any || ks > 0 ? 1u : 0u);
-            umma_commit(&pv_done[w]);
-            umma_commit(&buf_free[vb]);
-            any = true;
-            ++ns;
+                for (int ks = 0; ks < kTcStep / 16; ++ks)
+                  umma_bf16_ts(to, tp + uint32_t(ks) * 8u, vt + uint32_t(ks) * 128u, ido,
+                               ks > 0 ? 1u : acc);
+                umma_commit(&pv_done[w]);
+                if (k0 + kTcStep >= keys) umma_commit(&buf_free[vb]);
+              }
+              __syncwarp();
+              any = true;
+              // P has been read: its buffer takes the scores of two steps on
+              if (!wait(&pv_done[w], np & 1, W_PV_DONE)) return false;
+              ++np;
+              if (!issue_s()) return false;
+            }
           }
-          if (ns > ns0)
-            umma_commit(&q_free);
-          else
-            mbar_arrive(&q_free);  // no product of this stream read the phase's queries
+          // every product of the phase is done (the last P V was waited for)
+          if (lane == 0) mbar_arrive(&q_free);
           ++phase;
+          tile0 += uint32_t(pe - u);
+          u = pe;
         }
+        if (any && lane == 0) mbar_arrive(&o_done[w]);
         return true;
       });
       // every product and commit is done before the tensor memory is given back
-      if (issued) {
+      if (nsc > 0 && lane == 0) {
         umma_commit(&all_done[w]);
         mbar_wait(&all_done[w], 0);
       }
