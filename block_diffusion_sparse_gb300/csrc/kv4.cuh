@@ -100,42 +100,46 @@ cudaError_t launch_kv4_attn_tc(int d, int rows, const Kv4AttnArgs& a, uint32_t* 
 // batches balanced; a CTA's range may cover the end of one segment, whole
 // segments, and the start of another (its pieces).  Piece (c, segment s) has
 // partial slot c + s: from one piece to the next c or s grows.
+// All counts fit 31 bits (N*Hkv*L_max < 2^31, units of 16 keys or more).  The
+// results are handed to every lane from one, which tells the compiler that what
+// follows from them is the same for the whole warp.
 struct Kv4Split {
-  int64_t total;  // units of all segments
-  int64_t share;  // units per CTA
+  int total;  // units of all segments
+  int share;  // units per CTA
 };
+HERALD_DEV int warp_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 HERALD_DEV int kv4_units(int ctx, int L_max, int unit, int blk_units) {
   return (min(max(ctx, 0), L_max) + unit - 1) / unit + blk_units;
 }
 // Sum over the sequences of their units (per KV head); every lane of a warp
 // calls it and gets the total.
-HERALD_DEV int64_t kv4_total_units(const int32_t* ctx, int N, int L_max, int unit, int blk_units) {
-  int64_t sum = 0;
+HERALD_DEV int kv4_total_units(const int32_t* ctx, int N, int L_max, int unit, int blk_units) {
+  int sum = 0;
   for (int n = int(threadIdx.x & 31); n < N; n += 32)
     sum += kv4_units(ctx[n], L_max, unit, blk_units);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
+  return warp_same(sum);
 }
-HERALD_DEV Kv4Split kv4_split(int64_t per_head, int Hkv, int ctas, int min_share) {
+HERALD_DEV Kv4Split kv4_split(int per_head, int Hkv, int ctas, int min_share) {
   Kv4Split s;
   s.total = per_head * Hkv;
-  s.share = max((s.total + ctas - 1) / ctas, int64_t(min_share));
+  s.share = max((s.total + ctas - 1) / ctas, min_share);
   return s;
 }
 // The sequence that holds unit `at` (of all segments, at < total) and the
 // first unit of that sequence's first segment; called by a whole warp.
 HERALD_DEV void kv4_find(const int32_t* ctx, int N, int L_max, int unit, int blk_units, int Hkv,
-                         int64_t at, int* n_out, int64_t* first_out) {
+                         int at, int* n_out, int* first_out) {
   const int lane = threadIdx.x & 31;
-  int64_t base = 0;
+  int base = 0;
   for (int n0 = 0; n0 < N; n0 += 32) {
     const int n = n0 + lane;
-    const int64_t own = n < N ? int64_t(Hkv) * kv4_units(ctx[n], L_max, unit, blk_units) : 0;
-    int64_t inc = own;  // inclusive scan
+    const int own = n < N ? Hkv * kv4_units(ctx[n], L_max, unit, blk_units) : 0;
+    int inc = own;  // inclusive scan
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      const int up = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += up;
     }
     const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > at);

@@ -125,11 +125,11 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
   const Kv4Split split =
       kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, kKv4Unit, blk_units), a.Hkv, a.ctas,
                 kKv4MinShare);
-  int64_t at = int64_t(blockIdx.x) * split.share;
-  const int64_t end = min(at + split.share, split.total);
+  int at = int(blockIdx.x) * split.share;
+  const int end = min(at + split.share, split.total);
   if (at >= end) return;
   int n;
-  int64_t first;  // first unit of sequence n's first segment
+  int first;  // first unit of sequence n's first segment
   kv4_find(a.ctx, a.N, a.L_max, kKv4Unit, blk_units, a.Hkv, at, &n, &first);
 
   while (at < end) {
@@ -137,14 +137,14 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
     debug_flag(threadIdx.x == 0 && (ctx_raw < 0 || ctx_raw > a.L_max), DEV_BAD_COUNT);
     const int ctx = min(max(ctx_raw, 0), a.L_max);
     const int cache_units = (ctx + kKv4Unit - 1) / kKv4Unit, units = cache_units + blk_units;
-    if (units == 0 || at >= first + int64_t(a.Hkv) * units) {  // the next sequence
-      first += int64_t(a.Hkv) * units;
+    if (units == 0 || at >= first + a.Hkv * units) {  // the next sequence
+      first += a.Hkv * units;
       ++n;
       continue;
     }
-    const int g = int((at - first) / units);
-    const int64_t seg0 = first + int64_t(g) * units;
-    const int u0 = int(at - seg0), u1 = int(min(int64_t(units), end - seg0));
+    const int g = (at - first) / units;
+    const int seg0 = first + g * units;
+    const int u0 = at - seg0, u1 = min(units, end - seg0);
     const int seg = n * a.Hkv + g;
     const int cu1 = min(u1, cache_units);
     auto page_of = [&](int u) {
@@ -476,15 +476,15 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
   const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, unit, blk_units), a.Hkv,
                                    a.ctas, min_share);
   const int units = kv4_units(a.ctx[n], a.L_max, unit, blk_units);
-  const int64_t first = int64_t(a.Hkv) * kv4_total_units(a.ctx, n, a.L_max, unit, blk_units) +
-                        int64_t(g) * units;
+  const int first =
+      a.Hkv * kv4_total_units(a.ctx, n, a.L_max, unit, blk_units) + g * units;
   uint2* out = reinterpret_cast<uint2*>(
       a.out + ((size_t(n) * a.B + rc / G) * a.Hq + g * G + rc % G) * D + c4 * 4);
   if (units == 0) {
     if (grp == 0 && r < R) *out = make_uint2(0, 0);
     return;
   }
-  int c0 = int(first / split.share), c1 = int((first + units - 1) / split.share);
+  int c0 = first / split.share, c1 = (first + units - 1) / split.share;
   if (c0 == c1 && subs == 1) return;  // one piece: written by the attention kernel
   c0 = (c0 + seg) * subs, c1 = (c1 + seg) * subs + subs - 1;  // its partials
   const float4* op = reinterpret_cast<const float4*>(a.opart) + size_t(c4) * a.R16 + rc;

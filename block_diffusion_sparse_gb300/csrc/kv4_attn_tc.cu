@@ -37,7 +37,8 @@ namespace herald {
 constexpr int kTcKeys = kKv4TcKeys;        // keys per tile
 constexpr int kTcStep = 64;                // keys per step of a stream
 constexpr int kTcBufs = 4;                 // operand buffers (128 keys of K or V)
-constexpr int kTcRaw = 3;                  // raw items
+// raw items: as many as fit beside the operands
+__host__ __device__ constexpr int tc_raw(int MT) { return MT == 2 ? 3 : 6; }
 constexpr int kTcMasks = 8;                // tiles whose key masks are kept
 constexpr int kTcSoft = 256, kTcConv = 256;  // softmax and conversion threads
 constexpr int kTcThreadsAll = 640;         // 8 + 8 + 4 warps (warp 19 only fills its warpgroup)
@@ -87,7 +88,7 @@ __host__ __device__ inline TcSmem tc_smem(int D, int MT) {
   s.q = 0;
   s.buf = s.q + uint32_t(MT) * tile;
   s.raw = s.buf + uint32_t(kTcBufs) * tile;
-  s.total = s.raw + uint32_t(kTcRaw) * uint32_t(kTcKeys * (D / 2 + D / 16)) + 1024u;
+  s.total = s.raw + uint32_t(tc_raw(MT)) * uint32_t(kTcKeys * (D / 2 + D / 16)) + 1024u;
   return s;
 }
 
@@ -186,7 +187,7 @@ HERALD_DEV void store_p32(uint32_t ts, const uint32_t (&x)[32], bool blk, float 
 template <int D, int MT>
 __global__ void __launch_bounds__(kTcThreadsAll, 1)
     kv4_attn_tc_kernel(const Kv4AttnArgs a, uint32_t* err) {
-  constexpr int H = D / 64;
+  constexpr int H = D / 64, kTcRaw = tc_raw(MT);
   constexpr uint32_t kTile = uint32_t(H) * 16384u;
   constexpr int kRowC = D / 2, kRowS = D / 16;           // raw bytes of a row
   constexpr uint32_t kRawBytes = kTcKeys * (kRowC + kRowS);
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   const TcSmem L = tc_smem(D, MT);
   uint8_t* base = align1024(smem_raw);
   uint8_t *Qs = base + L.q, *Bs = base + L.buf, *Rs = base + L.raw;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * kTcRaw; ++i)
       mbar_init(&raw_full[i & 1][i >> 1], 1), mbar_init(&raw_free[i & 1][i >> 1], 4);
@@ -231,29 +232,29 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   const int blk_units = a.bk ? (a.B + kTcKeys - 1) / kTcKeys : 0;
   const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, kTcKeys, blk_units), a.Hkv,
                                    a.ctas, 1);
-  const int64_t at0 = int64_t(blockIdx.x) * split.share;
-  const int64_t end = min(at0 + split.share, split.total);
+  const int at0 = int(blockIdx.x) * split.share;
+  const int end = min(at0 + split.share, split.total);
   int n_first = 0;
-  int64_t first0 = 0;
+  int first0 = 0;
   if (at0 < end) kv4_find(a.ctx, a.N, a.L_max, kTcKeys, blk_units, a.Hkv, at0, &n_first, &first0);
 
   // Every role walks the same pieces: body(n, g, seg, ctx, units, u0, u1) with
   // tiles u0 <= u < u1 of the segment, the first blk_units of them block tiles;
   // it returns false to leave (a wait ran out).
   auto pieces = [&](auto&& body) {
-    int64_t at = at0, first = first0;
+    int at = at0, first = first0;
     int n = n_first;
     while (at < end) {
-      const int ctx = min(max(a.ctx[n], 0), a.L_max);
+      const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
       const int units = kv4_units(ctx, a.L_max, kTcKeys, blk_units);
-      if (units == 0 || at >= first + int64_t(a.Hkv) * units) {
-        first += int64_t(a.Hkv) * units;
+      if (units == 0 || at >= first + a.Hkv * units) {
+        first += a.Hkv * units;
         ++n;
         continue;
       }
-      const int g = int((at - first) / units);
-      const int64_t seg0 = first + int64_t(g) * units;
-      const int u0 = int(at - seg0), u1 = int(min(int64_t(units), end - seg0));
+      const int g = (at - first) / units;
+      const int seg0 = first + g * units;
+      const int u0 = at - seg0, u1 = min(units, end - seg0);
       if (!body(n, g, n * a.Hkv + g, ctx, units, u0, u1)) return;
       at = seg0 + u1;
     }
@@ -438,34 +439,47 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
         if (phase > 0 && !wait(&q_free, (phase - 1) & 1, W_Q_FREE)) return false;
         // queries: D/16 lanes per row, 16 channels each
         constexpr int LPR = D / 16;
-        for (int r0 = ct / LPR; r0 < MT * kTileM; r0 += kTcConv / LPR) {
-          const int c = ct % LPR;
-          uint32_t x[8] = {};
-          if (r0 < R) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                a.q + ((size_t(n) * a.B + r0 / G) * a.Hq + g * G + r0 % G) * D + c * 16);
-            const uint4 x0 = src[0], x1 = src[1];
-            x[0] = x0.x, x[1] = x0.y, x[2] = x0.z, x[3] = x0.w;
-            x[4] = x1.x, x[5] = x1.y, x[6] = x1.z, x[7] = x1.w;
+        constexpr int kPass = kTcConv / LPR, kRows = kTileM / kPass;  // rows per pass and tile
+        const int c = ct % LPR;
+#pragma unroll 1
+        for (int mt2 = 0; mt2 < MT; ++mt2) {
+          uint4 x4[kRows][2];  // (every load of a tile first)
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const int r = mt2 * kTileM + i * kPass + ct / LPR;
+            x4[i][0] = x4[i][1] = make_uint4(0, 0, 0, 0);
+            if (r < R) {
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c * 16);
+              x4[i][0] = src[0];
+              x4[i][1] = src[1];
+            }
           }
-          if (!blk) {  // fp16 scaled per row by a power of two (see kv4_attn.cu)
-            float mx = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              mx = fmaxf(mx, fmaxf(fabsf(bf16lo(x[i])), fabsf(bf16hi(x[i]))));
+          for (int i = 0; i < kRows; ++i) {
+            const int rr = i * kPass + ct / LPR;
+            uint32_t x[8] = {x4[i][0].x, x4[i][0].y, x4[i][0].z, x4[i][0].w,
+                             x4[i][1].x, x4[i][1].y, x4[i][1].z, x4[i][1].w};
+            if (!blk) {  // fp16 scaled per row by a power of two (see kv4_attn.cu)
+              float mx = 0.f;
 #pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            float up, f;
-            kv4_query_scale(mx, a.scale * a.c.k_scale, &up, &f);
+              for (int k = 0; k < 8; ++k)
+                mx = fmaxf(mx, fmaxf(fabsf(bf16lo(x[k])), fabsf(bf16hi(x[k]))));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = pack_half2(bf16lo(x[i]) * up, bf16hi(x[i]) * up);
-            if (c == 0) row_f[r0] = f;
+              for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              float up, f;
+              kv4_query_scale(mx, a.scale * a.c.k_scale, &up, &f);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = pack_half2(bf16lo(x[k]) * up, bf16hi(x[k]) * up);
+              if (c == 0) row_f[mt2 * kTileM + rr] = f;
+            }
+            uint8_t* dst = Qs + uint32_t(mt2) * kTile + uint32_t(c >> 2) * 16384u;
+            const uint32_t c8 = uint32_t(c & 3) * 2u;
+            *reinterpret_cast<uint4*>(dst + sw128_off(uint32_t(rr), c8)) =
+                make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(dst + sw128_off(uint32_t(rr), c8 + 1)) =
+                make_uint4(x[4], x[5], x[6], x[7]);
           }
-          uint8_t* dst = Qs + uint32_t(r0 / kTileM) * kTile + uint32_t(c >> 2) * 16384u;
-          const uint32_t rr = uint32_t(r0 % kTileM), c8 = uint32_t(c & 3) * 2u;
-          *reinterpret_cast<uint4*>(dst + sw128_off(rr, c8)) = make_uint4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<uint4*>(dst + sw128_off(rr, c8 + 1)) =
-              make_uint4(x[4], x[5], x[6], x[7]);
         }
         publish(&q_full);
         ++phase;
