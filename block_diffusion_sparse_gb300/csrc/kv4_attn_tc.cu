@@ -61,8 +61,8 @@ struct TcWait {
     const uint64_t t0 = globaltimer_ns();
     while (true) {
 #pragma unroll 1
-      for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
+      for (int i = 0; i < 8; ++i)
+        if (mbar_try_wait_for(bar, parity, 20000u)) return true;
       if (*failed) return false;
       if (globaltimer_ns() - t0 > kWaitLimitNs) {
         *failed = which;
@@ -78,6 +78,26 @@ struct TcWait {
     return __all_sync(0xffffffffu, ok);
   }
 };
+
+// Shared memory by 32-bit address (the aligned base of the dynamic part is a
+// generic pointer to the compiler).
+HERALD_DEV uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+HERALD_DEV uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+HERALD_DEV void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
 
 struct TcSmem {
   uint32_t q, buf, raw, total;
@@ -207,6 +227,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   const TcSmem L = tc_smem(D, MT);
   uint8_t* base = align1024(smem_raw);
   uint8_t *Qs = base + L.q, *Bs = base + L.buf, *Rs = base + L.raw;
+  const uint32_t qs = smem_u32(Qs), bs = smem_u32(Bs), raw_s = smem_u32(Rs);
   const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * kTcRaw; ++i)
@@ -473,19 +494,17 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               for (int k = 0; k < 8; ++k) x[k] = pack_half2(bf16lo(x[k]) * up, bf16hi(x[k]) * up);
               if (c == 0) row_f[mt2 * kTileM + rr] = f;
             }
-            uint8_t* dst = Qs + uint32_t(mt2) * kTile + uint32_t(c >> 2) * 16384u;
+            const uint32_t dst = qs + uint32_t(mt2) * kTile + uint32_t(c >> 2) * 16384u;
             const uint32_t c8 = uint32_t(c & 3) * 2u;
-            *reinterpret_cast<uint4*>(dst + sw128_off(uint32_t(rr), c8)) =
-                make_uint4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<uint4*>(dst + sw128_off(uint32_t(rr), c8 + 1)) =
-                make_uint4(x[4], x[5], x[6], x[7]);
+            sts128(dst + sw128_off(uint32_t(rr), c8), x[0], x[1], x[2], x[3]);
+            sts128(dst + sw128_off(uint32_t(rr), c8 + 1), x[4], x[5], x[6], x[7]);
           }
         }
         publish(&q_full);
         ++phase;
         for (; u < pe; ++u, ++tile) {
           const uint32_t item = 2 * tile + uint32_t(kv), b = item % kTcBufs;
-          uint8_t* dst = Bs + b * kTile;
+          const uint32_t dst = bs + b * kTile;
           if (blk) {  // bf16 rows of the block, zeros after them
             if (item >= uint32_t(kTcBufs) &&
                 !wait(&buf_free[b], (item / kTcBufs - 1) & 1, W_BUF_FREE))
@@ -499,14 +518,14 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               if (j < a.B)
                 v = *reinterpret_cast<const uint4*>(
                     src + ((size_t(n) * a.B + j) * a.Hkv + g) * D + c * 8);
-              *reinterpret_cast<uint4*>(dst + uint32_t(c >> 3) * 16384u +
-                                        sw128_off(uint32_t(r), uint32_t(c & 7))) = v;
+              sts128(dst + uint32_t(c >> 3) * 16384u + sw128_off(uint32_t(r), uint32_t(c & 7)), v.x,
+                     v.y, v.z, v.w);
             }
           } else {
             const uint32_t rm = mt % kTcRaw;
             if (!wait(&raw_full[kv][rm], (mt / kTcRaw) & 1, W_RAW_FULL)) return false;
-            const uint8_t* rc = Rs + (2 * mt + uint32_t(kv)) % kTcRaw * kRawBytes;
-            const uint8_t* rsc = rc + kTcKeys * kRowC;
+            const uint32_t rc = raw_s + (2 * mt + uint32_t(kv)) % kTcRaw * kRawBytes;
+            const uint32_t rsc = rc + uint32_t(kTcKeys * kRowC);
             // A lane turns chunks of 16 bytes (32 channels): chunk j of row r.
             // Rows and chunks are dealt so that the eight lanes of a
             // shared-memory phase read eight different 16-byte bank groups
@@ -526,8 +545,8 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
 #pragma unroll
             for (int s = 0; s < kTasks; ++s) {
               const int r = row_of(s);
-              code[s] = *reinterpret_cast<const uint4*>(rc + r * kRowC + j * 16);
-              sc[s] = *reinterpret_cast<const uint16_t*>(rsc + r * kRowS + j * 2);
+              code[s] = lds128(rc + uint32_t(r * kRowC + j * 16));
+              sc[s] = lds_u16(rsc + uint32_t(r * kRowS + j * 2));
             }
             if (kv) {  // a value row that does not count may hold any bytes: no 0 * NaN
               const uint32_t m = *(volatile uint32_t*)&key_mask[mt % kTcMasks][cw];
@@ -540,10 +559,12 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
             if (item >= uint32_t(kTcBufs) &&
                 !wait(&buf_free[b], (item / kTcBufs - 1) & 1, W_BUF_FREE))
               return false;
-            uint8_t* half = dst + uint32_t(D == 128 ? j >> 1 : 0) * 16384u;
 #pragma unroll
             for (int s = 0; s < kTasks; ++s) {
               const uint32_t r = uint32_t(row_of(s));
+              // chunk (j&1)*4 + k of the row: its place is the first one's, XOR k
+              const uint32_t at = dst + uint32_t(D == 128 ? j >> 1 : 0) * 16384u +
+                                  sw128_off(r, uint32_t((j & 1) * 4));
               const uint32_t s2 = e4m3x2_to_half2(sc[s]);
               const uint32_t words[4] = {code[s].x, code[s].y, code[s].z, code[s].w};
 #pragma unroll
@@ -553,8 +574,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                 const uint32_t fs = __byte_perm(s2, 0, k < 2 ? 0x1010 : 0x3232);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = hmul2(h[i], fs);
-                *reinterpret_cast<uint4*>(half + sw128_off(r, uint32_t((j & 1) * 4 + k))) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
+                sts128(at ^ uint32_t(k << 4), h[0], h[1], h[2], h[3]);
               }
             }
             ++mt;
@@ -571,21 +591,28 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
       uint32_t raw_no = 0, mt = 0;
       pieces([&](int n, int g, int, int ctx, int, int u0, int u1) -> bool {
         const int sub = min(1 << a.c.page_log2, kTcKeys);  // keys of a tile in one page
+        const int k0 = lane * sub;  // lane i: sub-chunk i of the tile
+        auto page_of = [&](int u) {
+          const int pos = (u - blk_units) * kTcKeys + k0;
+          return u < u1 && k0 < kTcKeys && pos < ctx ? kv4_page(a.c, n, pos >> a.c.page_log2) : -1;
+        };
+        int next = page_of(max(u0, blk_units));  // (looked up a tile ahead)
         for (int u = max(u0, blk_units); u < u1; ++u, ++mt) {
-          // lane i: the tile's sub-chunk i
-          const int k0 = lane * sub, pos = (u - blk_units) * kTcKeys + k0;
-          int keys = 0, phys = -1;
+          const int pos = (u - blk_units) * kTcKeys + k0;
+          const int phys = next;
+          next = page_of(u + 1);
+          int keys = 0;
           if (k0 < kTcKeys && pos < ctx) {
-            phys = kv4_page(a.c, n, pos >> a.c.page_log2);
-            debug_flag(phys < 0, DEV_BAD_INDEX);
             if (phys >= 0) keys = min(sub, ctx - pos);
+            else *(volatile uint32_t*)&missing = 1;
+            debug_flag(phys < 0, DEV_BAD_INDEX);
           }
-          if (pos < ctx && k0 < kTcKeys && phys < 0) *(volatile uint32_t*)&missing = 1;
           const size_t row = phys >= 0 ? kv4_row(a.c, phys, a.Hkv, g, pos) : 0;
           const uint32_t rows = uint32_t(keys + 15) & ~15u;  // whole groups of 16: inside the page
-          uint32_t total = rows;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+          const uint32_t total = __reduce_add_sync(0xffffffffu, rows);
+          // lane i < 8: which of keys 16 i .. 16 i + 15 count
+          const int mine = __shfl_sync(0xffffffffu, keys, lane * 16 / sub) - lane * 16 % sub;
+          const uint32_t bits = (1u << min(max(mine, 0), 16)) - 1u;
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++raw_no) {
             const uint32_t rb = raw_no % kTcRaw;  // the slot held item raw_no - kTcRaw
@@ -595,14 +622,10 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               return false;
             uint64_t* full = &raw_full[kv][mt % kTcRaw];
             if (kv == 0) {
-              // (the masks of kTcMasks tiles back have been read: their V item
-              // has left the operand ring, which is shorter)
-              if (k0 < kTcKeys)
-                for (int i = 0; i < sub / 16; ++i) {
-                  const int v = min(max(keys - 16 * i, 0), 16);
-                  reinterpret_cast<volatile uint16_t*>(key_mask[mt % kTcMasks])[k0 / 16 + i] =
-                      uint16_t((1u << v) - 1u);
-                }
+              // (the masks of kTcMasks tiles back have been read: their V items
+              // have left the operand ring, which is shorter)
+              if (lane < 8)
+                reinterpret_cast<volatile uint16_t*>(key_mask[mt % kTcMasks])[lane] = uint16_t(bits);
               __syncwarp();
               if (lane == 0) mbar_arrive(&mask_full[mt % kTcMasks]);
             }
@@ -610,8 +633,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
             __syncwarp();
             if (rows) {
               uint8_t* dst = Rs + rb * kRawBytes;
-              bulk_load(dst + k0 * kRowC, (kv ? a.c.vc : a.c.kc) + row * kRowC, rows * kRowC,
-                        full);
+              bulk_load(dst + k0 * kRowC, (kv ? a.c.vc : a.c.kc) + row * kRowC, rows * kRowC, full);
               bulk_load(dst + kTcKeys * kRowC + k0 * kRowS, (kv ? a.c.vs : a.c.ks) + row * kRowS,
                         rows * kRowS, full);
             }
@@ -632,9 +654,9 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
       // descriptors of buffer 0; other tiles and steps add to the address field
       // (which never carries: 14 bits hold all of shared memory)
       const uint64_t qd =
-          make_sdesc_sw128(smem_u32(Qs) + (MT == 2 ? uint32_t(w) * kTile : 0u), 16, 1024);
-      const uint64_t kd = make_sdesc_sw128(smem_u32(Bs), 16, 1024);
-      const uint64_t vd = make_sdesc_sw128(smem_u32(Bs), 16384u, 1024);
+          make_sdesc_sw128(qs + (MT == 2 ? uint32_t(w) * kTile : 0u), 16, 1024);
+      const uint64_t kd = make_sdesc_sw128(bs, 16, 1024);
+      const uint64_t vd = make_sdesc_sw128(bs, 16384u, 1024);
       uint32_t tile0 = 0, np = 0, nsc = 0, phase = 0;  // tiles before the phase, P V, S issued
       pieces([&](int, int, int, int ctx, int, int u0, int u1) -> bool {
         bool any = false;
