@@ -5,13 +5,15 @@
 // turned into fp16 there (exact, kv4.cuh), once per 128-key tile for up to 256
 // query rows.  One CTA per SM walks its share of the keys (kv4_split, units of
 // 128 keys, a segment's block keys first):
-//   warp 17      copies the codes and scales of a tile's pages into a raw ring
-//                (bulk copies; the pages of a tile in parallel lanes)
-//   warps 8-11, 12-15 turn the K and the V items (halves of a tile) of the raw
-//                ring into fp16 128-byte-swizzled operand buffers; together
-//                they stage the queries
-//   warps 16, 18 one tcgen05.mma issuer per stream: S = Q K^T into a score
-//                buffer, O += P V with P read from tensor memory
+//   warps 17, 19 copy the codes and scales of a tile's K and V rows from its pages
+//                into raw slots (bulk copies; the pages of a tile in parallel
+//                lanes)
+//   warps 8-11, 12-15 turn the K and the V slots into fp16 128-byte-swizzled
+//                operand buffers; together they stage the queries
+//   warps 16, 18 a tcgen05.mma issuer per stream of S = Q K^T into a score buffer
+//   warps 20, 21 one per stream of O += P V with P read from tensor memory
+//                (issuing an mma takes a warp about a hundred cycles: with one
+//                warp per stream for both products that was the longest chain)
 //   warps 0-3, 4-7 softmax of a stream, a thread per query row
 // Two streams run side by side: with more than 128 rows a stream is a row tile
 // and takes every key tile, else both streams have the same rows and take
@@ -37,12 +39,16 @@ namespace herald {
 constexpr int kTcKeys = kKv4TcKeys;        // keys per tile
 constexpr int kTcStep = 64;                // keys per step of a stream
 constexpr int kTcBufs = 4;                 // operand buffers (128 keys of K or V)
-// raw items: as many as fit beside the operands
-__host__ __device__ constexpr int tc_raw(int MT) { return MT == 2 ? 3 : 6; }
-constexpr int kTcMasks = 8;                // tiles whose key masks are kept
+// Raw slots of K and of V tiles: as many as fit beside the operands.
+__host__ __device__ constexpr int tc_raw_k(int MT) { return MT == 2 ? 2 : 3; }
+__host__ __device__ constexpr int tc_raw_v(int MT) { return MT == 2 ? 1 : 3; }
+// Tiles whose key masks are kept.  A K copy runs at most three slots and two
+// operand buffers ahead of the scores, and the scores two steps ahead of P: the
+// mask of 16 tiles back has been read by everybody.
+constexpr int kTcMasks = 16;
 constexpr int kTcSoft = 256, kTcConv = 256;  // softmax and conversion threads
-constexpr int kTcThreadsAll = 640;         // 8 + 8 + 4 warps (warp 19 only fills its warpgroup)
-constexpr int kTcMmaWarp0 = 16, kTcCopyWarp = 17, kTcIdleWarp = 19;  // (18: the other issuer)
+constexpr int kTcThreadsAll = 768;         // 8 + 8 + 8 warps (22, 23 only fill a warpgroup)
+constexpr int kTcSWarp = 16, kTcCopyWarp = 17, kTcPvWarp = 20;  // S 16, 18; copies 17, 19; P V 20, 21
 constexpr float kTcBelow = 11.f, kTcAbove = 15.f;
 
 // Waits of the kernel (bits 16-31 of the error word).
@@ -108,7 +114,7 @@ __host__ __device__ inline TcSmem tc_smem(int D, int MT) {
   s.q = 0;
   s.buf = s.q + uint32_t(MT) * tile;
   s.raw = s.buf + uint32_t(kTcBufs) * tile;
-  s.total = s.raw + uint32_t(tc_raw(MT)) * uint32_t(kTcKeys * (D / 2 + D / 16)) + 1024u;
+  s.total = s.raw + uint32_t(tc_raw_k(MT) + tc_raw_v(MT)) * uint32_t(kTcKeys * (D / 2 + D / 16)) + 1024u;
   return s;
 }
 
@@ -207,17 +213,15 @@ HERALD_DEV void store_p32(uint32_t ts, const uint32_t (&x)[32], bool blk, float 
 template <int D, int MT>
 __global__ void __launch_bounds__(kTcThreadsAll, 1)
     kv4_attn_tc_kernel(const Kv4AttnArgs a, uint32_t* err) {
-  constexpr int H = D / 64, kTcRaw = tc_raw(MT);
+  constexpr int H = D / 64, kRawK = tc_raw_k(MT), kRawV = tc_raw_v(MT);
   constexpr uint32_t kTile = uint32_t(H) * 16384u;
   constexpr int kRowC = D / 2, kRowS = D / 16;           // raw bytes of a row
   constexpr uint32_t kRawBytes = kTcKeys * (kRowC + kRowS);
   extern __shared__ uint8_t smem_raw[];
-  // [K or V][tile % kTcRaw]: each side of the conversion waits for every phase of
-  // its own barriers (a slot serves K and V items in turn)
-  __shared__ uint64_t raw_full[2][kTcRaw], raw_free[2][kTcRaw];
+  __shared__ uint64_t raw_full[2][kRawK], raw_free[2][kRawK];  // [K or V][slot]
   __shared__ uint64_t buf_full[kTcBufs], buf_free[kTcBufs];
-  __shared__ uint64_t q_full, q_free, s_full[2][2], p_full[2][2], pv_done[2], o_done[2];
-  __shared__ uint64_t all_done[2];
+  __shared__ uint64_t q_full, q_free, s_full[2][2], p_full[2][2], pv_done[2][2], o_done[2];
+  __shared__ uint64_t all_done[4];
   __shared__ uint64_t mask_full[kTcMasks];
   __shared__ uint32_t tmem_base;
   __shared__ uint32_t failed;
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   const uint32_t qs = smem_u32(Qs), bs = smem_u32(Bs), raw_s = smem_u32(Rs);
   const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * kTcRaw; ++i)
+    for (int i = 0; i < 2 * kRawK; ++i)
       mbar_init(&raw_full[i & 1][i >> 1], 1), mbar_init(&raw_free[i & 1][i >> 1], 4);
     for (int i = 0; i < kTcBufs; ++i) mbar_init(&buf_full[i], 4), mbar_init(&buf_free[i], MT);
     for (int i = 0; i < kTcMasks; ++i) mbar_init(&mask_full[i], 1);
@@ -238,8 +242,9 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
     mbar_init(&q_free, 2 + kTcSoft);
     for (int i = 0; i < 2; ++i)
       mbar_init(&s_full[i][0], 1), mbar_init(&s_full[i][1], 1), mbar_init(&p_full[i][0], 128),
-          mbar_init(&p_full[i][1], 128), mbar_init(&pv_done[i], 1), mbar_init(&o_done[i], 1),
-          mbar_init(&all_done[i], 1);
+          mbar_init(&p_full[i][1], 128), mbar_init(&pv_done[i][0], 1),
+          mbar_init(&pv_done[i][1], 1), mbar_init(&o_done[i], 1), mbar_init(&all_done[i], 1),
+          mbar_init(&all_done[2 + i], 1);
     failed = 0;
     missing = 0;
     fence_mbar_init();
@@ -285,11 +290,11 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
     return min(kTcKeys, u < blk_units ? a.B - u * kTcKeys : ctx - (u - blk_units) * kTcKeys);
   };
 
-  // registers: 640 threads launch with 96 each (61,440); 256 x 120 + 256 x 80 +
-  // 128 x 64 = 59,392.  Each role's branch begins with its own setmaxnreg, so
-  // that the compiler knows the limit of the code that follows.
+  // registers: 768 threads launch with 80 each (61,440) = 256 x (112 + 80 + 48).
+  // Each role's branch begins with its own setmaxnreg, so that the compiler
+  // knows the limit of the code that follows.
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     // ------------------------------------------------------------ softmax
     const int w = warp >> 2;                  // stream
     const int lrow = (warp & 3) * 32 + lane;  // TMEM lane
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                 // O so far, once the P V of the step before is in it (that of two
                 // steps before is: this step's scores took its buffer)
                 if (any) {
-                  if (!wait(&pv_done[w], (ns - 1) & 1, W_O_DONE)) return false;
+                  if (!wait(&pv_done[w][b ^ 1], ((ns - 1) >> 1) & 1, W_O_DONE)) return false;
                   tc_fence_after();
 #pragma unroll 1
                   for (int c = 0; c < D / 32; ++c) {
@@ -522,9 +527,9 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                      v.y, v.z, v.w);
             }
           } else {
-            const uint32_t rm = mt % kTcRaw;
-            if (!wait(&raw_full[kv][rm], (mt / kTcRaw) & 1, W_RAW_FULL)) return false;
-            const uint32_t rc = raw_s + (2 * mt + uint32_t(kv)) % kTcRaw * kRawBytes;
+            const uint32_t slots = kv ? kRawV : kRawK, rm = mt % slots;
+            if (!wait(&raw_full[kv][rm], (mt / slots) & 1, W_RAW_FULL)) return false;
+            const uint32_t rc = raw_s + (rm + (kv ? kRawK : 0)) * kRawBytes;
             const uint32_t rsc = rc + uint32_t(kTcKeys * kRowC);
             // A lane turns chunks of 16 bytes (32 channels): chunk j of row r.
             // Rows and chunks are dealt so that the eight lanes of a
@@ -549,6 +554,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               sc[s] = lds_u16(rsc + uint32_t(r * kRowS + j * 2));
             }
             if (kv) {  // a value row that does not count may hold any bytes: no 0 * NaN
+              if (!wait(&mask_full[mt % kTcMasks], (mt / kTcMasks) & 1, W_MASK)) return false;
               const uint32_t m = *(volatile uint32_t*)&key_mask[mt % kTcMasks][cw];
 #pragma unroll
               for (int s = 0; s < kTasks; ++s)
@@ -585,58 +591,54 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
       return true;
     });
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == kTcCopyWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kTcCopyWarp || warp == kTcCopyWarp + 2) {
       // ------------------------------------------------------- raw copies
-      uint32_t raw_no = 0, mt = 0;
+      const int kv = (warp - kTcCopyWarp) >> 1;
+      const uint32_t slots = kv ? kRawV : kRawK;
+      const uint8_t* codes = kv ? a.c.vc : a.c.kc;
+      const uint8_t* scales = kv ? a.c.vs : a.c.ks;
+      const int sub = min(1 << a.c.page_log2, kTcKeys);  // keys of a tile in one page
+      const int k0 = lane * sub;                         // lane i: sub-chunk i of the tile
+      const uint32_t dst_c = uint32_t(k0 * kRowC), dst_s = uint32_t(kTcKeys * kRowC + k0 * kRowS);
+      uint32_t mt = 0;
       pieces([&](int n, int g, int, int ctx, int, int u0, int u1) -> bool {
-        const int sub = min(1 << a.c.page_log2, kTcKeys);  // keys of a tile in one page
-        const int k0 = lane * sub;  // lane i: sub-chunk i of the tile
-        auto page_of = [&](int u) {
-          const int pos = (u - blk_units) * kTcKeys + k0;
-          return u < u1 && k0 < kTcKeys && pos < ctx ? kv4_page(a.c, n, pos >> a.c.page_log2) : -1;
-        };
-        int next = page_of(max(u0, blk_units));  // (looked up a tile ahead)
-        for (int u = max(u0, blk_units); u < u1; ++u, ++mt) {
-          const int pos = (u - blk_units) * kTcKeys + k0;
+        const int32_t* table = a.c.table + size_t(n) * a.c.max_pages;
+        int pos = (max(u0, blk_units) - blk_units) * kTcKeys + k0;
+        const int stop = k0 < kTcKeys ? min(ctx, (u1 - blk_units) * kTcKeys) : 0;
+        // the table's entry is read a tile ahead
+        int next = pos < stop ? table[pos >> a.c.page_log2] : -1;
+        for (int u = max(u0, blk_units); u < u1; ++u, ++mt, pos += kTcKeys) {
           const int phys = next;
-          next = page_of(u + 1);
-          int keys = 0;
-          if (k0 < kTcKeys && pos < ctx) {
-            if (phys >= 0) keys = min(sub, ctx - pos);
-            else *(volatile uint32_t*)&missing = 1;
-            debug_flag(phys < 0, DEV_BAD_INDEX);
-          }
-          const size_t row = phys >= 0 ? kv4_row(a.c, phys, a.Hkv, g, pos) : 0;
+          if (pos + kTcKeys < stop) next = table[(pos + kTcKeys) >> a.c.page_log2];
+          const bool on = pos < stop, have = on && phys >= 0 && phys < a.c.n_pages;
+          const int keys = have ? min(sub, ctx - pos) : 0;
+          debug_flag(on && !have, DEV_BAD_INDEX);
           const uint32_t rows = uint32_t(keys + 15) & ~15u;  // whole groups of 16: inside the page
           const uint32_t total = __reduce_add_sync(0xffffffffu, rows);
-          // lane i < 8: which of keys 16 i .. 16 i + 15 count
-          const int mine = __shfl_sync(0xffffffffu, keys, lane * 16 / sub) - lane * 16 % sub;
-          const uint32_t bits = (1u << min(max(mine, 0), 16)) - 1u;
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++raw_no) {
-            const uint32_t rb = raw_no % kTcRaw;  // the slot held item raw_no - kTcRaw
-            const uint32_t was = raw_no - uint32_t(kTcRaw);
-            if (raw_no >= uint32_t(kTcRaw) &&
-                !wait(&raw_free[was & 1][(was >> 1) % kTcRaw], ((was >> 1) / kTcRaw) & 1, W_RAW_FREE))
-              return false;
-            uint64_t* full = &raw_full[kv][mt % kTcRaw];
-            if (kv == 0) {
-              // (the masks of kTcMasks tiles back have been read: their V items
-              // have left the operand ring, which is shorter)
-              if (lane < 8)
-                reinterpret_cast<volatile uint16_t*>(key_mask[mt % kTcMasks])[lane] = uint16_t(bits);
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&mask_full[mt % kTcMasks]);
-            }
-            if (lane == 0) mbar_arrive_expect_tx(full, total * uint32_t(kRowC + kRowS));
+          const uint32_t slot = mt % slots;
+          uint64_t* full = &raw_full[kv][slot];
+          if (mt >= slots && !wait(&raw_free[kv][slot], (mt / slots - 1) & 1, W_RAW_FREE))
+            return false;
+          if (kv == 0) {
+            // lane i < 8: which of keys 16 i .. 16 i + 15 count
+            const int mine = __shfl_sync(0xffffffffu, keys, lane * 16 / sub) - lane * 16 % sub;
+            if (lane < 8)
+              reinterpret_cast<volatile uint16_t*>(key_mask[mt % kTcMasks])[lane] =
+                  uint16_t((1u << min(max(mine, 0), 16)) - 1u);
+            if (on && !have) *(volatile uint32_t*)&missing = 1;
             __syncwarp();
-            if (rows) {
-              uint8_t* dst = Rs + rb * kRawBytes;
-              bulk_load(dst + k0 * kRowC, (kv ? a.c.vc : a.c.kc) + row * kRowC, rows * kRowC, full);
-              bulk_load(dst + kTcKeys * kRowC + k0 * kRowS, (kv ? a.c.vs : a.c.ks) + row * kRowS,
-                        rows * kRowS, full);
-            }
+          }
+          if (lane == 0) {
+            if (kv == 0) mbar_arrive(&mask_full[mt % kTcMasks]);
+            mbar_arrive_expect_tx(full, total * uint32_t(kRowC + kRowS));
+          }
+          __syncwarp();
+          if (rows) {
+            const size_t row = kv4_row(a.c, phys, a.Hkv, g, pos);
+            uint8_t* dst = Rs + (slot + (kv ? kRawK : 0)) * kRawBytes;
+            bulk_load(dst + dst_c, codes + row * kRowC, rows * kRowC, full);
+            bulk_load(dst + dst_s, scales + row * kRowS, rows * kRowS, full);
           }
         }
         return true;
@@ -644,97 +646,104 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
       // every copy has landed before the CTA may leave (only after a failed
       // wait can one still be under way)
       if (*(volatile uint32_t*)&failed)
-        for (uint32_t i = raw_no > uint32_t(kTcRaw) ? raw_no - kTcRaw : 0; i < raw_no; ++i)
-          mbar_wait(&raw_full[i & 1][(i >> 1) % kTcRaw], ((i >> 1) / kTcRaw) & 1);
-    } else if (warp != kTcIdleWarp) {
-      // ------------------------------------------------------ MMA issuers
+        for (uint32_t i = mt > slots ? mt - slots : 0; i < mt; ++i)
+          mbar_wait(&raw_full[kv][i % slots], (i / slots) & 1);
+    } else if (warp == kTcSWarp || warp == kTcSWarp + 2) {
+      // ------------------------------------------------------ S issuers
       // (the whole warp walks the loops, lane 0 issues)
-      const int w = warp == kTcMmaWarp0 ? 0 : 1;
-      const uint32_t ts = tm + uint32_t(w) * 128u, to = ts + 256u;
+      const int w = (warp - kTcSWarp) >> 1;
+      const uint32_t ts = tm + uint32_t(w) * 128u;
       // descriptors of buffer 0; other tiles and steps add to the address field
       // (which never carries: 14 bits hold all of shared memory)
-      const uint64_t qd =
-          make_sdesc_sw128(qs + (MT == 2 ? uint32_t(w) * kTile : 0u), 16, 1024);
+      const uint64_t qd = make_sdesc_sw128(qs + (MT == 2 ? uint32_t(w) * kTile : 0u), 16, 1024);
       const uint64_t kd = make_sdesc_sw128(bs, 16, 1024);
-      const uint64_t vd = make_sdesc_sw128(bs, 16384u, 1024);
-      uint32_t tile0 = 0, np = 0, nsc = 0, phase = 0;  // tiles before the phase, P V, S issued
+      uint32_t tile = 0, ns = 0, phase = 0;  // tiles of the CTA, steps of the stream
       pieces([&](int, int, int, int ctx, int, int u0, int u1) -> bool {
-        bool any = false;
         int u = u0;
         while (u < u1) {
           const bool blk = u < blk_units;
           const int pe = blk ? min(u1, blk_units) : u1;
           const uint32_t ids = blk ? make_idesc_bf16(kTileM, kTcStep, false, false)
                                    : make_idesc_f16(kTileM, kTcStep, false);
-          const uint32_t ido =
-              blk ? make_idesc_bf16(kTileM, D, false, true) : make_idesc_f16(kTileM, D, true);
           if (!wait(&q_full, phase & 1, W_Q_FULL)) return false;
-          // a step: 64 keys of tile u + du, from key k0 on; this stream's tiles
-          const int stride = MT == 1 ? 2 : 1;
-          const int du0 = MT == 1 ? int((tile0 ^ uint32_t(w)) & 1u) : 0;
-          int sd = du0, sk = 0;  // the next S
-          auto issue_s = [&]() -> bool {
-            if (u + sd >= pe) return true;
-            const uint32_t ki = 2 * (tile0 + uint32_t(sd)), kb = ki % kTcBufs;
-            if (sk == 0 && !wait(&buf_full[kb], (ki / kTcBufs) & 1, W_K_FULL)) return false;
-            tc_fence_after();
-            const uint64_t kt = kd + ((kb * kTile + uint32_t(sk) * 128u) >> 4);
-            const uint32_t sb = nsc & 1, td = ts + sb * 64u;
-            const bool last = sk + kTcStep >= tile_keys(u + sd, ctx);
-            if (lane == 0) {
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = (uint32_t(ks >> 2) * 16384u + uint32_t(ks & 3) * 32u) >> 4;
-                umma_bf16(td, qd + off, kt + off, ids, ks > 0 ? 1u : 0u);
-              }
-              umma_commit(&s_full[w][sb]);
-              if (last) umma_commit(&buf_free[kb]);
-            }
-            __syncwarp();
-            ++nsc;
-            sk = last ? 0 : sk + kTcStep;
-            if (last) sd += stride;
-            return true;
-          };
-          if (!issue_s() || !issue_s()) return false;
-          for (int d = du0; u + d < pe; d += stride) {
-            const uint32_t vi = 2 * (tile0 + uint32_t(d)) + 1, vb = vi % kTcBufs;
-            const int keys = tile_keys(u + d, ctx);
-            for (int k0 = 0; k0 < keys; k0 += kTcStep) {
-              if (!wait(&p_full[w][np & 1], (np >> 1) & 1, W_P_FULL)) return false;
-              if (k0 == 0 && !wait(&buf_full[vb], (vi / kTcBufs) & 1, W_V_FULL)) return false;
+          const uint32_t ns0 = ns;
+          for (; u < pe; ++u, ++tile) {
+            if (MT == 1 && int(tile & 1) != w) continue;
+            const uint32_t ki = 2 * tile, kb = ki % kTcBufs;
+            if (!wait(&buf_full[kb], (ki / kTcBufs) & 1, W_K_FULL)) return false;
+            const int keys = tile_keys(u, ctx);
+            for (int k0 = 0; k0 < keys; k0 += kTcStep, ++ns) {
+              // P of two steps before has been read: its buffer is free
+              const uint32_t b = ns & 1;
+              if (ns >= 2 && !wait(&pv_done[w][b], ((ns >> 1) - 1) & 1, W_PV_DONE)) return false;
               tc_fence_after();
-              const uint64_t vt = vd + ((vb * kTile + uint32_t(k0) * 128u) >> 4);
-              const uint32_t tp = ts + (np & 1) * 64u, acc = any ? 1u : 0u;
+              const uint64_t kt = kd + ((kb * kTile + uint32_t(k0) * 128u) >> 4);
               if (lane == 0) {
 #pragma unroll
-                for (int ks = 0; ks < kTcStep / 16; ++ks)
-                  umma_bf16_ts(to, tp + uint32_t(ks) * 8u, vt + uint32_t(ks) * 128u, ido,
-                               ks > 0 ? 1u : acc);
-                umma_commit(&pv_done[w]);
-                if (k0 + kTcStep >= keys) umma_commit(&buf_free[vb]);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                  const uint32_t off = (uint32_t(ks >> 2) * 16384u + uint32_t(ks & 3) * 32u) >> 4;
+                  umma_bf16(ts + b * 64u, qd + off, kt + off, ids, ks > 0 ? 1u : 0u);
+                }
+                umma_commit(&s_full[w][b]);
+                if (k0 + kTcStep >= keys) umma_commit(&buf_free[kb]);
               }
               __syncwarp();
-              any = true;
-              // P has been read: its buffer takes the scores of two steps on
-              if (!wait(&pv_done[w], np & 1, W_PV_DONE)) return false;
-              ++np;
-              if (!issue_s()) return false;
             }
           }
-          // every product of the phase is done (the last P V was waited for)
-          if (lane == 0) mbar_arrive(&q_free);
+          if (lane == 0) {
+            if (ns > ns0)
+              umma_commit(&q_free);
+            else
+              mbar_arrive(&q_free);  // no product of this stream read the phase's queries
+          }
           ++phase;
-          tile0 += uint32_t(pe - u);
-          u = pe;
         }
-        if (any && lane == 0) mbar_arrive(&o_done[w]);
         return true;
       });
       // every product and commit is done before the tensor memory is given back
-      if (nsc > 0 && lane == 0) {
+      if (ns > 0 && lane == 0) {
         umma_commit(&all_done[w]);
         mbar_wait(&all_done[w], 0);
+      }
+    } else if (warp == kTcPvWarp || warp == kTcPvWarp + 1) {
+      // ---------------------------------------------------- P V issuers
+      const int w = warp - kTcPvWarp;
+      const uint32_t ts = tm + uint32_t(w) * 128u, to = ts + 256u;
+      const uint64_t vd = make_sdesc_sw128(bs, 16384u, 1024);
+      uint32_t tile = 0, ns = 0;
+      pieces([&](int, int, int, int ctx, int, int u0, int u1) -> bool {
+        const uint32_t ns0 = ns;
+        for (int u = u0; u < u1; ++u, ++tile) {
+          if (MT == 1 && int(tile & 1) != w) continue;
+          const uint32_t ido = u < blk_units ? make_idesc_bf16(kTileM, D, false, true)
+                                             : make_idesc_f16(kTileM, D, true);
+          const uint32_t vi = 2 * tile + 1, vb = vi % kTcBufs;
+          if (!wait(&buf_full[vb], (vi / kTcBufs) & 1, W_V_FULL)) return false;
+          const int keys = tile_keys(u, ctx);
+          for (int k0 = 0; k0 < keys; k0 += kTcStep, ++ns) {
+            const uint32_t b = ns & 1;
+            if (!wait(&p_full[w][b], (ns >> 1) & 1, W_P_FULL)) return false;
+            tc_fence_after();
+            const uint64_t vt = vd + ((vb * kTile + uint32_t(k0) * 128u) >> 4);
+            const uint32_t acc = ns > ns0 ? 1u : 0u;
+            if (lane == 0) {
+#pragma unroll
+              for (int ks = 0; ks < kTcStep / 16; ++ks)
+                umma_bf16_ts(to, ts + b * 64u + uint32_t(ks) * 8u, vt + uint32_t(ks) * 128u, ido,
+                             ks > 0 ? 1u : acc);
+              umma_commit(&pv_done[w][b]);
+              if (k0 + kTcStep >= keys) umma_commit(&buf_free[vb]);
+            }
+            __syncwarp();
+          }
+        }
+        if (ns > ns0 && lane == 0) umma_commit(&o_done[w]);
+        __syncwarp();
+        return true;
+      });
+      if (ns > 0 && lane == 0) {
+        umma_commit(&all_done[2 + w]);
+        mbar_wait(&all_done[2 + w], 0);
       }
     }
     __syncwarp();
