@@ -87,55 +87,119 @@ struct Kv4AttnArgs {
   int N, Hq, Hkv, B, L_max, R16, ctas;
   Kv4Dev c;
 };
-constexpr int kKv4TcKeys = 128;  // keys per tile of the tensor-core kernel
+constexpr int kKv4Tile = 128;  // keys per tile of the attention kernels
 // The tensor-core kernel (kv4_attn_tc.cu) for `rows` <= 256 query rows per KV
 // head; with rows <= 128 each piece has two partials (slots 2p and 2p+1).
 cudaError_t launch_kv4_attn_tc(int d, int rows, const Kv4AttnArgs& a, uint32_t* err,
                                cudaStream_t st);
 
+// Shared memory by 32-bit address (the aligned base of the dynamic part is a
+// generic pointer to the compiler).
+HERALD_DEV uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+HERALD_DEV uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+HERALD_DEV uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+HERALD_DEV uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+HERALD_DEV uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+HERALD_DEV void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// Bounded wait; false when it ran out, or when another wait of the CTA has: the
+// roles then stop copying and issuing and the kernel returns.
+struct Kv4Wait {
+  volatile uint32_t* failed;  // shared: the wait that ran out first
+  HERALD_DEV bool slow(uint64_t* bar, uint32_t parity, uint32_t which) const {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i)
+        if (mbar_try_wait_for(bar, parity, 20000u)) return true;
+      if (*failed) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *failed = which;
+        return false;
+      }
+    }
+  }
+  // The answer for a whole warp, which leaves converged: lanes may see a
+  // barrier complete in different polls, and the tensor-memory instructions
+  // that follow (.sync.aligned) want the warp in one piece.
+  HERALD_DEV bool operator()(uint64_t* bar, uint32_t parity, uint32_t which) const {
+    const bool ok = mbar_try_wait(bar, parity) || slow(bar, parity, which);
+    return __all_sync(0xffffffffu, ok);
+  }
+};
+
 // ---- how attention CTAs share the keys
-// The keys of every (sequence, KV head) segment, in units of `unit` cache
-// positions followed by the block's own keys, are laid end to end, segments in
-// order; CTA c takes units [c*share, (c+1)*share).  Equal shares keep ragged
-// batches balanced; a CTA's range may cover the end of one segment, whole
-// segments, and the start of another (its pieces).  Piece (c, segment s) has
-// partial slot c + s: from one piece to the next c or s grows.
-// All counts fit 31 bits (N*Hkv*L_max < 2^31, units of 16 keys or more).  The
-// results are handed to every lane from one, which tells the compiler that what
-// follows from them is the same for the whole warp.
+// The keys of every (sequence, KV head) segment, in tiles of 128 cache positions,
+// are laid end to end, segments in order, and the block's own keys with them:
+// blk_units tiles of their own per segment, or (blk_units = kKv4BlkJoined) as
+// part of the segment's first tile, which then exists without cache keys too.
+// CTA c takes tiles [c*share, (c+1)*share).  Equal shares keep ragged batches
+// balanced; a CTA's range may cover the end of one segment, whole segments, and
+// the start of another (its pieces).  Piece (c, segment s) has partial slot c +
+// s: from one piece to the next c or s grows.  All counts fit 31 bits
+// (N*Hkv*L_max < 2^31).  The results are handed to every lane from one, which
+// tells the compiler that what follows from them is the same for the whole warp.
+constexpr int kKv4BlkJoined = -1;
 struct Kv4Split {
-  int total;  // units of all segments
-  int share;  // units per CTA
+  int total;  // tiles of all segments
+  int share;  // tiles per CTA
 };
 HERALD_DEV int warp_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-HERALD_DEV int kv4_units(int ctx, int L_max, int unit, int blk_units) {
-  return (min(max(ctx, 0), L_max) + unit - 1) / unit + blk_units;
+HERALD_DEV int kv4_units(int ctx, int L_max, int blk_units) {
+  const int t = (min(max(ctx, 0), L_max) + kKv4Tile - 1) / kKv4Tile;
+  return blk_units == kKv4BlkJoined ? max(t, 1) : t + blk_units;
 }
-// Sum over the sequences of their units (per KV head); every lane of a warp
+// Sum over the sequences of their tiles (per KV head); every lane of a warp
 // calls it and gets the total.
-HERALD_DEV int kv4_total_units(const int32_t* ctx, int N, int L_max, int unit, int blk_units) {
+HERALD_DEV int kv4_total_units(const int32_t* ctx, int N, int L_max, int blk_units) {
   int sum = 0;
   for (int n = int(threadIdx.x & 31); n < N; n += 32)
-    sum += kv4_units(ctx[n], L_max, unit, blk_units);
+    sum += kv4_units(ctx[n], L_max, blk_units);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return warp_same(sum);
 }
-HERALD_DEV Kv4Split kv4_split(int per_head, int Hkv, int ctas, int min_share) {
+HERALD_DEV Kv4Split kv4_split(int per_head, int Hkv, int ctas) {
   Kv4Split s;
   s.total = per_head * Hkv;
-  s.share = max((s.total + ctas - 1) / ctas, min_share);
+  s.share = max((s.total + ctas - 1) / ctas, 1);
   return s;
 }
-// The sequence that holds unit `at` (of all segments, at < total) and the
-// first unit of that sequence's first segment; called by a whole warp.
-HERALD_DEV void kv4_find(const int32_t* ctx, int N, int L_max, int unit, int blk_units, int Hkv,
-                         int at, int* n_out, int* first_out) {
+// The sequence that holds tile `at` (of all segments, at < total) and the
+// first tile of that sequence's first segment; called by a whole warp.
+HERALD_DEV void kv4_find(const int32_t* ctx, int N, int L_max, int blk_units, int Hkv, int at,
+                         int* n_out, int* first_out) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   for (int n0 = 0; n0 < N; n0 += 32) {
     const int n = n0 + lane;
-    const int own = n < N ? Hkv * kv4_units(ctx[n], L_max, unit, blk_units) : 0;
+    const int own = n < N ? Hkv * kv4_units(ctx[n], L_max, blk_units) : 0;
     int inc = own;  // inclusive scan
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

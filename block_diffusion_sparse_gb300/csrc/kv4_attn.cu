@@ -1,22 +1,27 @@
 // kv4_attn.cu -- attention of a block's queries over the whole paged 4-bit
 // cache and the block's own bf16 keys, for few query rows per KV head (one
-// token, a short draft): bound by the cache's bytes, so the codes go from
-// global memory through registers straight into matrix-instruction operands.
+// token, a short draft): bound by the cache's bytes and by the instructions that
+// turn codes into numbers.
 //
-// A warp takes units of 16 keys.  With rows = the group's query rows,
+// A CTA walks its share of the keys (kv4_split) in tiles of 128.  Its ninth warp
+// copies each tile's codes and scales from the pages into a ring of stages (bulk
+// copies, the tile's pages in parallel lanes); each of the other eight takes 16
+// of the tile's keys.  With rows = the group's query rows,
 //   S^T [16 keys x 8 rows] = K [16 x d] Q^T [d x 8]        (mma m16n8k16)
 //   O^T [d x 8 rows]      += V^T [d x 16 keys] P^T [16 x 8] (mma m16n8k16)
 // The keys are the M side of both products, so eight query rows fill an
 // instruction (with the queries as M, half of every instruction would be
 // padding).  The contraction index of an mma may be permuted as long as
-// both operands agree, and so may the M rows of O^T, so each lane's share of
-// a key row is a run of consecutive codes in memory:
-//   K: lane (g = lane/4, t = lane%4) holds channels [t d/4, (t+1) d/4) of
-//      keys g and g+8, as the A fragments of d/16 steps;
-//   V: lane (g, t) holds channels [g d/8, (g+1) d/8) of keys 2t, 2t+1, 2t+8,
-//      2t+9.  A V^T fragment pairs two keys in a register, so the nibbles of
-//      two keys' words are interleaved (two AND-ORs per eight codes) and one
+// both operands agree, and so may the M rows, so each lane's share of a key row
+// is a run of consecutive codes and dequantised registers are operands at once:
+//   K: lane (g = lane/4, t = lane%4) holds channels [t d/4, (t+1) d/4) of two
+//      keys, as the A fragments of d/16 steps;
+//   V: lane (g, t) holds channels [g d/8, (g+1) d/8) of four keys.  A V^T
+//      fragment pairs two keys in a register, so the nibbles of two keys'
+//      words are interleaved (a shift and a bit select per four codes) and one
 //      conversion yields the pair.
+// The mma's key index j = 8h + 2t + o stands for key 8h + 4o + (t ^ o) of the 16:
+// then neither the K nor the V reads meet more than two-way bank conflicts.
 // code * scale is exact in fp16 (kv4.cuh).  Queries become fp16 scaled per
 // row by a power of two that brings the row's largest value to [2^14, 2^15):
 // exact for every value within 2^-32 of the largest (below, off by less than
@@ -26,7 +31,7 @@
 //
 // A row's exponent base is set 11 (log2) below its largest score so far and
 // stays while no score exceeds it by 15: P lies in fp16's [0, 2^15], weights
-// down to 2^-25 of the largest keep 11 bits, and most units need one vote and
+// down to 2^-25 of the largest keep 11 bits, and most tiles need one vote and
 // no exchange between lanes.
 #include <float.h>
 
@@ -35,12 +40,10 @@
 namespace herald {
 
 constexpr int kKv4Warps = 8;
-constexpr int kKv4Threads = kKv4Warps * 32;
-constexpr int kKv4Unit = 16;        // keys per unit
-constexpr int kKv4MinShare = kKv4Warps;  // units per CTA: at least one per warp
+constexpr int kKv4Threads = (kKv4Warps + 1) * 32;
+constexpr int kKv4Unit = 16;        // keys per warp and tile
 constexpr int kKv4MmaRows = 16;     // most rows per KV head of this kernel
 constexpr float kKv4Below = 11.f, kKv4Above = 15.f;  // exponent base, log2 units
-
 
 HERALD_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                         uint32_t b0, uint32_t b1) {
@@ -66,391 +69,451 @@ HERALD_DEV uint32_t bcast16(uint32_t x, int half) {
   return half ? __byte_perm(x, 0, 0x3232) : __byte_perm(x, 0, 0x1010);
 }
 
-// One unit of cache keys as it comes from memory.
-template <int D>
-struct Kv4Raw {
-  uint32_t k[2][D / 32];  // keys g, g+8: D/4 codes (D/32 words) each
-  uint32_t v[4][D / 64];  // keys 2t, 2t+1, 2t+8, 2t+9: D/8 codes each
-  uint32_t ks[2];         // their scales (D/64 bytes)
-  uint32_t vs[4];
-};
-
-// Loads the unit at cache row `row` (kv4_row of its first key).  One address
-// per array, the keys at constant offsets from it.
-template <int D>
-HERALD_DEV void kv4_load(Kv4Raw<D>& r, const Kv4Dev& c, size_t row, int lane) {
-  constexpr int C = D / 2, S = D / 16;  // bytes of a row's codes and scales
-  const int lg = lane >> 2, lt = lane & 3;
-  const uint8_t* kc = c.kc + (row + lg) * C + lt * (C / 4);
-  const uint8_t* ks = c.ks + (row + lg) * S + lt * (S / 4);
-  const uint8_t* vc = c.vc + (row + 2 * lt) * C + lg * (C / 8);
-  const uint8_t* vs = c.vs + (row + 2 * lt) * S + lg * S / 8;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if constexpr (D == 128) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(kc + i * 8 * C));
-      r.k[i][0] = w.x, r.k[i][1] = w.y, r.k[i][2] = w.z, r.k[i][3] = w.w;
-      r.ks[i] = __ldg(reinterpret_cast<const uint16_t*>(ks + i * 8 * S));
-    } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(kc + i * 8 * C));
-      r.k[i][0] = w.x, r.k[i][1] = w.y;
-      r.ks[i] = __ldg(ks + i * 8 * S);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int o = (i & 1) + 8 * (i >> 1);
-    if constexpr (D == 128) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(vc + o * C));
-      r.v[i][0] = w.x, r.v[i][1] = w.y;
-    } else {
-      r.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(vc + o * C));
-    }
-    r.vs[i] = __ldg(vs + o * S);
-  }
+HERALD_DEV void product_bar() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kKv4Warps * 32) : "memory");
 }
+
+// Waits of the kernel (bits 16-31 of the error word).
+enum : uint32_t { W_STAGE_FREE = 1, W_STAGE_FULL = 2 };
+
+// Dynamic shared memory: the ring of stages (codes and scales of 128 keys and
+// values), then the warps' partial outputs.
+template <int D, int NT>
+struct RowsSmem {
+  static constexpr int kStages = NT == 1 ? 3 : 5;
+  static constexpr int kCodes = kKv4Tile * D / 2, kScales = kKv4Tile * D / 16;
+  static constexpr int kStage = 2 * (kCodes + kScales);
+  static constexpr int kRed = kStages * kStage;
+  static constexpr int kTotal = kRed + kKv4Warps * 8 * NT * (D + 4) * 4;
+};
 
 // at most 8*NT query rows per KV head
 template <int D, int NT>
 __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
-    kv4_attn_kernel(const Kv4AttnArgs a) {
+    kv4_attn_kernel(const Kv4AttnArgs a, uint32_t* err) {
+  using S = RowsSmem<D, NT>;
   constexpr int KS = D / 16;  // k steps of S, and M tiles of O^T
   constexpr int RT = 8 * NT;  // rows of a tile
-  extern __shared__ float red[];  // [warps][RT][D + 4]
+  constexpr int kRowC = D / 2, kRowS = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[S::kStages], empty[S::kStages];
+  __shared__ uint32_t failed;
+  __shared__ uint8_t counts[S::kStages][kKv4Warps];  // keys of each 16 that count
   __shared__ float red_m[kKv4Warps][RT], red_l[kKv4Warps][RT];
+  float* red = reinterpret_cast<float*>(smem + S::kRed);  // [warps][RT][D + 4]
+  const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  const int lg = lane >> 2, lt = lane & 3;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kKv4Warps);
+    failed = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
   griddep_enter();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
+  const Kv4Wait wait{&failed};
   const int G = a.Hq / a.Hkv, R = a.B * G;
-  const int blk_units = a.bk ? (a.B + kKv4Unit - 1) / kKv4Unit : 0;
+  const int blk_units = a.bk ? kKv4BlkJoined : 0;
   const Kv4Split split =
-      kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, kKv4Unit, blk_units), a.Hkv, a.ctas,
-                kKv4MinShare);
-  int at = int(blockIdx.x) * split.share;
-  const int end = min(at + split.share, split.total);
-  if (at >= end) return;
-  int n;
-  int first;  // first unit of sequence n's first segment
-  kv4_find(a.ctx, a.N, a.L_max, kKv4Unit, blk_units, a.Hkv, at, &n, &first);
+      kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, blk_units), a.Hkv, a.ctas);
+  const int at0 = int(blockIdx.x) * split.share;
+  const int end = min(at0 + split.share, split.total);
+  if (at0 >= end) return;
+  int n0, first0;
+  kv4_find(a.ctx, a.N, a.L_max, blk_units, a.Hkv, at0, &n0, &first0);
 
-  while (at < end) {
-    const int ctx_raw = a.ctx[n];
-    debug_flag(threadIdx.x == 0 && (ctx_raw < 0 || ctx_raw > a.L_max), DEV_BAD_COUNT);
-    const int ctx = min(max(ctx_raw, 0), a.L_max);
-    const int cache_units = (ctx + kKv4Unit - 1) / kKv4Unit, units = cache_units + blk_units;
-    if (units == 0 || at >= first + a.Hkv * units) {  // the next sequence
-      first += a.Hkv * units;
-      ++n;
-      continue;
-    }
-    const int g = (at - first) / units;
-    const int seg0 = first + g * units;
-    const int u0 = at - seg0, u1 = min(units, end - seg0);
-    const int seg = n * a.Hkv + g;
-    const int cu1 = min(u1, cache_units);
-    auto page_of = [&](int u) {
-      if (u >= cu1) return -1;
-      const int p = kv4_page(a.c, n, (u * kKv4Unit) >> a.c.page_log2);
-      debug_flag(p < 0, DEV_BAD_INDEX);  // positions below the length without a page
-      return p;
-    };
-
-    // queries: B fragments (lane: row lg of each 8-row tile), fp16 scaled by
-    // a power of two per row; rs[nt][2] undo it for the rows this lane's
-    // scores belong to (2 lt, 2 lt + 1)
-    uint32_t qf[NT][KS][2];
-    float rs[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + lg;
-      const bool on = r < R;
-      const uint16_t* qp =
-          a.q + ((size_t(n) * a.B + (on ? r / G : 0)) * a.Hq + g * G + (on ? r % G : 0)) * D +
-          lt * (D / 4);
-      float mx = 0.f;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        uint2 w = make_uint2(0, 0);
-        if (on) w = *reinterpret_cast<const uint2*>(qp + s * 4);
-        qf[nt][s][0] = w.x;
-        qf[nt][s][1] = w.y;
-        mx = fmaxf(fmaxf(mx, fmaxf(fabsf(bf16lo(w.x)), fabsf(bf16hi(w.x)))),
-                   fmaxf(fabsf(bf16lo(w.y)), fabsf(bf16hi(w.y))));
+  // Both roles walk the same pieces: body(n, g, seg, ctx, units, u0, u1), cache
+  // tiles u0 <= u < min(u1, tiles of ctx), the block's keys with tile 0.
+  auto pieces = [&](auto&& body) {
+    int at = at0, first = first0, n = n0;
+    while (at < end) {
+      const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
+      const int units = kv4_units(ctx, a.L_max, blk_units);
+      if (units == 0 || at >= first + a.Hkv * units) {  // the next sequence
+        first += a.Hkv * units;
+        ++n;
+        continue;
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      float up, f;
-      kv4_query_scale(mx, a.scale * a.c.k_scale, &up, &f);
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          qf[nt][s][i] = pack_half2(bf16lo(qf[nt][s][i]) * up, bf16hi(qf[nt][s][i]) * up);
-      rs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * lt);      // lane of row 2 lt
-      rs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * lt + 4);  // lane of row 2 lt + 1
+      const int g = (at - first) / units;
+      const int seg0 = first + g * units;
+      const int u0 = at - seg0, u1 = min(units, end - seg0);
+      body(n, g, n * a.Hkv + g, ctx, units, u0, u1);
+      at = seg0 + u1;
     }
+  };
 
-    float o[NT][KS][4];
-    float m[NT][2], l[NT][2];
+  if (warp == kKv4Warps) {
+    // ------------------------------------------------------------ copies
+    const int sub = min(1 << a.c.page_log2, kKv4Tile);  // keys of a tile in one page
+    const int k0 = lane * sub;                          // lane i: sub-chunk i of the tile
+    uint32_t t = 0;
+    bool ok = true;
+    pieces([&](int n, int g, int, int ctx, int, int u0, int u1) {
+      debug_flag(lane == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
+      const int32_t* table = a.c.table + size_t(n) * a.c.max_pages;
+      int pos = u0 * kKv4Tile + k0;
+      const int stop = k0 < kKv4Tile ? min(ctx, u1 * kKv4Tile) : 0;
+      // the table's entry is read a tile ahead
+      int next = pos < stop ? table[pos >> a.c.page_log2] : -1;
+      const int tiles = min(u1, (ctx + kKv4Tile - 1) / kKv4Tile);
+      for (int u = u0; u < tiles && ok; ++u, ++t, pos += kKv4Tile) {
+        const int phys = next;
+        if (pos + kKv4Tile < stop) next = table[(pos + kKv4Tile) >> a.c.page_log2];
+        const bool on = pos < stop, have = on && phys >= 0 && phys < a.c.n_pages;
+        debug_flag(on && !have, DEV_BAD_INDEX);  // positions below the length without a page
+        const int keys = have ? min(sub, ctx - pos) : 0;
+        const uint32_t rows = uint32_t(keys + 15) & ~15u;  // whole groups of 16: inside the page
+        const uint32_t total = __reduce_add_sync(0xffffffffu, rows);
+        const int mine = __shfl_sync(0xffffffffu, keys, lane * 16 / sub) - lane * 16 % sub;
+        const uint32_t st = t % S::kStages;
+        ok = t < uint32_t(S::kStages) || wait(&empty[st], (t / S::kStages - 1) & 1, W_STAGE_FREE);
+        if (!ok) break;
+        if (lane < kKv4Warps)
+          *(volatile uint8_t*)&counts[st][lane] = uint8_t(min(max(mine, 0), kKv4Unit));
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], total * uint32_t(2 * (kRowC + kRowS)));
+        __syncwarp();
+        if (rows) {
+          const size_t row = kv4_row(a.c, phys, a.Hkv, g, pos);
+          uint8_t* d = smem + st * S::kStage;
+          bulk_load(d + k0 * kRowC, a.c.kc + row * kRowC, rows * kRowC, &full[st]);
+          bulk_load(d + S::kCodes + k0 * kRowC, a.c.vc + row * kRowC, rows * kRowC, &full[st]);
+          bulk_load(d + 2 * S::kCodes + k0 * kRowS, a.c.ks + row * kRowS, rows * kRowS, &full[st]);
+          bulk_load(d + 2 * S::kCodes + S::kScales + k0 * kRowS, a.c.vs + row * kRowS,
+                    rows * kRowS, &full[st]);
+        }
+      }
+    });
+    if (!ok)  // the copies under way land before the CTA may leave
+      for (uint32_t i = t > uint32_t(S::kStages) ? t - S::kStages : 0; i < t; ++i)
+        mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1);
+  } else {
+    // ------------------------------------------------------------ products
+    // (after a failed wait the warps go on without waiting: their barriers
+    // below stay in step, the results are worthless and the error is recorded)
+    uint32_t t = 0;
+    const uint32_t base = smem_u32(smem);
+    // this lane's keys of the warp's 16: the two of its scores, the four of V
+    const int key_s = 4 * (lg & 1) + ((lg >> 1) ^ (lg & 1));  // and + 8
+    auto key_v = [&](int i) { return 8 * (i >> 1) + 4 * (i & 1) + (lt ^ (i & 1)); };
+    pieces([&](int n, int g, int seg, int ctx, int units, int u0, int u1) {
+      // queries: B fragments (lane: row lg of each 8-row tile), fp16 scaled by
+      // a power of two per row; rs[nt][2] undo it for the rows this lane's
+      // scores belong to (2 lt, 2 lt + 1)
+      uint32_t qf[NT][KS][2];
+      float rs[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + lg;
+        const bool on = r < R;
+        const uint16_t* qp =
+            a.q + ((size_t(n) * a.B + (on ? r / G : 0)) * a.Hq + g * G + (on ? r % G : 0)) * D +
+            lt * (D / 4);
+        float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[nt][i] = -FLT_MAX, l[nt][i] = 0.f;
+        for (int s = 0; s < KS; s += 2) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (on) w = *reinterpret_cast<const uint4*>(qp + s * 4);
+          qf[nt][s][0] = w.x, qf[nt][s][1] = w.y, qf[nt][s + 1][0] = w.z, qf[nt][s + 1][1] = w.w;
+        }
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[nt][k][i] = 0.f;
-    }
-    // raw scores -> probabilities 2^(s f - m); moves the base where a score
-    // stands more than kKv4Above over it
-    auto probabilities = [&](float (&s)[NT][4], const float (&f)[NT][2]) {
-      float x[NT][4];
-      bool move = false;
+          for (int i = 0; i < 2; ++i)
+            mx = fmaxf(mx, fmaxf(fabsf(bf16lo(qf[nt][s][i])), fabsf(bf16hi(qf[nt][s][i]))));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        float up, f;
+        kv4_query_scale(mx, a.scale * a.c.k_scale, &up, &f);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qf[nt][s][i] = pack_half2(bf16lo(qf[nt][s][i]) * up, bf16hi(qf[nt][s][i]) * up);
+        rs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * lt);      // lane of row 2 lt
+        rs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * lt + 4);  // lane of row 2 lt + 1
+      }
+
+      float o[NT][KS][4];
+      float m[NT][2], l[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[nt][i] = fmaf(s[nt][i], f[nt][i & 1], -m[nt][i & 1]);
-        move |= fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])) > kKv4Above;
+        for (int i = 0; i < 2; ++i) m[nt][i] = -FLT_MAX, l[nt][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[nt][k][i] = 0.f;
       }
-      if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float b = fmaxf(s[nt][i] * f[nt][i], s[nt][i + 2] * f[nt][i]);
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
-            b = fmaxf(m[nt][i], b - kKv4Below);
-            const float w = fast_exp2(m[nt][i] - b);
-            m[nt][i] = b;
-            l[nt][i] *= w;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              o[nt][k][i] *= w;
-              o[nt][k][i + 2] *= w;
-            }
-            x[nt][i] = fmaf(s[nt][i], f[nt][i], -b);
-            x[nt][i + 2] = fmaf(s[nt][i + 2], f[nt][i], -b);
-          }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[nt][i] = fast_exp2(x[nt][i]);
-          l[nt][i & 1] += s[nt][i];
-        }
-    };
-
-    // ------------------------------------------------------ cache units
-    auto unit = [&](const Kv4Raw<D>& cur, int u, bool paged) {
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-      const uint32_t s0 = e4m3x2_to_half2(cur.ks[0]), s1 = e4m3x2_to_half2(cur.ks[1]);
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {  // a word of codes per key: two k steps
-        uint32_t h0[4], h1[4];
-        e2m1x8_to_half2(cur.k[0][w], h0);
-        e2m1x8_to_half2(cur.k[1][w], h1);
-        const uint32_t f0 = bcast16(s0, w >> 1), f1 = bcast16(s1, w >> 1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h0[i] = hmul2(h0[i], f0);
-          h1[i] = hmul2(h1[i], f1);
-        }
+      // raw scores -> probabilities 2^(s f - m); moves the base where a score
+      // stands more than kKv4Above over it
+      auto probabilities = [&](float (&s)[NT][4], const float (&f)[NT][2]) {
+        float x[NT][4];
+        bool move = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(s[nt], h0[0], h1[0], h0[1], h1[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
-          mma_f16(s[nt], h0[2], h1[2], h0[3], h1[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[nt][i] = fmaf(s[nt][i], f[nt][i & 1], -m[nt][i & 1]);
+          move |= fmaxf(fmax3f(x[nt][0], x[nt][1], x[nt][2]), x[nt][3]) > kKv4Above;
         }
-      }
-      uint32_t vs[4] = {cur.vs[0], cur.vs[1], cur.vs[2], cur.vs[3]};
-      const int valid = paged ? ctx - u * kKv4Unit : 0;
-      if (valid < kKv4Unit) {  // keys past the length, or without a page
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (lg + 8 * (i >> 1) >= valid) s[nt][i] = -INFINITY;
-        // such a row may hold any bytes: 0 * NaN must not arise
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (2 * lt + (i & 1) + 8 * (i >> 1) >= valid) vs[i] = 0;
-      }
-      probabilities(s, rs);
-      uint32_t p0[NT], p1[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        p0[nt] = transpose8x8(pack_half2(s[nt][0], s[nt][1]));
-        p1[nt] = transpose8x8(pack_half2(s[nt][2], s[nt][3]));
-      }
-      const uint32_t f0 = e4m3x2_to_half2(vs[0] | vs[1] << 8),
-                     f1 = e4m3x2_to_half2(vs[2] | vs[3] << 8);
-#pragma unroll
-      for (int w = 0; w < D / 64; ++w) {
-        uint32_t e0[4], d0[4], e1[4], d1[4];  // even, odd channels of the two key pairs
-        e2m1x8_to_half2((cur.v[0][w] & 0x0F0F0F0Fu) | ((cur.v[1][w] << 4) & 0xF0F0F0F0u), e0);
-        e2m1x8_to_half2(((cur.v[0][w] >> 4) & 0x0F0F0F0Fu) | (cur.v[1][w] & 0xF0F0F0F0u), d0);
-        e2m1x8_to_half2((cur.v[2][w] & 0x0F0F0F0Fu) | ((cur.v[3][w] << 4) & 0xF0F0F0F0u), e1);
-        e2m1x8_to_half2(((cur.v[2][w] >> 4) & 0x0F0F0F0Fu) | (cur.v[3][w] & 0xF0F0F0F0u), d1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e0[i] = hmul2(e0[i], f0);
-          d0[i] = hmul2(d0[i], f0);
-          e1[i] = hmul2(e1[i], f1);
-          d1[i] = hmul2(d1[i], f1);
+        if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma_f16(o[nt][w * 4 + i], e0[i], d0[i], e1[i], d1[i], p0[nt], p1[nt]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float b = fmaxf(s[nt][i] * f[nt][i], s[nt][i + 2] * f[nt][i]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
+              b = fmaxf(m[nt][i], b - kKv4Below);
+              const float w = fast_exp2(m[nt][i] - b);
+              m[nt][i] = b;
+              l[nt][i] *= w;
+#pragma unroll
+              for (int k = 0; k < KS; ++k) {
+                o[nt][k][i] *= w;
+                o[nt][k][i + 2] *= w;
+              }
+              x[nt][i] = fmaf(s[nt][i], f[nt][i], -b);
+              x[nt][i + 2] = fmaf(s[nt][i + 2], f[nt][i], -b);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[nt][i] = fast_exp2(x[nt][i]);
+            l[nt][i & 1] += s[nt][i];
+          }
+      };
+
+      // ---------------- the block's own keys, in bf16 (at most 16), one warp
+      // (P in units of v_scale so that O has one unit for all keys)
+      if (a.bk && u0 == 0 && warp == 0) {
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+        const uint16_t* kp[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j = key_s + 8 * i;
+          kp[i] = j < a.B ? a.bk + ((size_t(n) * a.B + j) * a.Hkv + g) * D + lt * (D / 4) : nullptr;
+        }
+#pragma unroll 2
+        for (int k = 0; k < KS; ++k) {
+          uint2 w[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            w[i] = kp[i] ? *reinterpret_cast<const uint2*>(kp[i] + k * 4) : make_uint2(0, 0);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + lg;
+            uint2 b = make_uint2(0, 0);
+            if (r < R)
+              b = *reinterpret_cast<const uint2*>(
+                  a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + lt * (D / 4) +
+                  k * 4);
+            mma_bf16(s[nt], w[0].x, w[1].x, w[0].y, w[1].y, b.x, b.y);
+          }
+        }
+        float f[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          f[nt][0] = f[nt][1] = fminf(a.scale * 1.4426950408889634f, FLT_MAX);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key_s + 8 * (i >> 1) >= a.B) s[nt][i] = -INFINITY;
+        }
+        probabilities(s, f);
+        const float iv = 1.f / a.c.v_scale;
+        uint32_t p0[NT], p1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          p0[nt] = transpose8x8(pack_bf16(s[nt][0] * iv, s[nt][1] * iv));
+          p1[nt] = transpose8x8(pack_bf16(s[nt][2] * iv, s[nt][3] * iv));
+        }
+        const uint16_t* vp[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = key_v(i);
+          vp[i] = j < a.B ? a.bv + ((size_t(n) * a.B + j) * a.Hkv + g) * D + lg * (D / 8) : nullptr;
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {  // channels lg*D/8 + 2k, + 2k+1 of each key
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = vp[i] ? *reinterpret_cast<const uint32_t*>(vp[i] + 2 * k) : 0u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_bf16(o[nt][k], __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+                     __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632), p0[nt],
+                     p1[nt]);
         }
       }
-    };
-    // two units in flight: one is computed while the other one's bytes travel,
-    // and the page of the one after is looked up a unit ahead of its load
-    Kv4Raw<D> r0, r1;
-    int u = u0 + warp;
-    int pa = page_of(u), pb = page_of(u + kKv4Warps);
-    auto load = [&](Kv4Raw<D>& r, int phys, int at_unit) {
-      // (without a page: row 0, whose bytes the masks keep out)
-      kv4_load<D>(r, a.c, phys < 0 ? 0 : kv4_row(a.c, phys, a.Hkv, g, at_unit * kKv4Unit), lane);
-    };
-    if (u < cu1) load(r0, pa, u);
-    for (; u < cu1; u += 2 * kKv4Warps) {
-      const int v = u + kKv4Warps;
-      const bool ha = pa >= 0, hb = pb >= 0;
-      pa = page_of(v + kKv4Warps);
-      if (v < cu1) load(r1, pb, v);
-      pb = page_of(v + 2 * kKv4Warps);
-      unit(r0, u, ha);
-      if (v >= cu1) {
-        u = v;
-        break;
-      }
-      if (v + kKv4Warps < cu1) load(r0, pa, v + kKv4Warps);
-      unit(r1, v, hb);
-    }
 
-    // ------------------------------------- the block's own keys, in bf16
-    // (P in units of v_scale so that O has one unit for all keys)
-    for (; u < u1; u += kKv4Warps) {
-      const int j0 = (u - cache_units) * kKv4Unit;
-      float s[NT][4];
+      // ------------------------------------------------------ cache tiles
+      const int tiles = min(u1, (ctx + kKv4Tile - 1) / kKv4Tile);
+#pragma unroll 1
+      for (int u = u0; u < tiles; ++u, ++t) {
+        const uint32_t st = t % S::kStages, sm = base + st * uint32_t(S::kStage);
+        wait(&full[st], (t / S::kStages) & 1, W_STAGE_FULL);
+        const int valid = warp_same(int(*(volatile uint8_t*)&counts[st][warp]));
+        if (valid > 0) {
+          const uint32_t row0 = uint32_t(warp * kKv4Unit);
+          const uint32_t ka = sm + (row0 + uint32_t(key_s)) * kRowC + uint32_t(lt) * (kRowC / 4);
+          const uint32_t ksa = sm + uint32_t(2 * S::kCodes) + (row0 + uint32_t(key_s)) * kRowS +
+                               uint32_t(lt) * (kRowS / 4);
+          uint32_t kw[2][D / 32], ksc[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (D == 128) {
+              const uint4 w = lds128(ka + uint32_t(i * 8 * kRowC));
+              kw[i][0] = w.x, kw[i][1] = w.y, kw[i][2] = w.z, kw[i][3] = w.w;
+              ksc[i] = lds_u16(ksa + uint32_t(i * 8 * kRowS));
+            } else {
+              const uint2 w = lds64(ka + uint32_t(i * 8 * kRowC));
+              kw[i][0] = w.x, kw[i][1] = w.y;
+              ksc[i] = lds_u8(ksa + uint32_t(i * 8 * kRowS));
+            }
+          }
+          uint32_t vw[4][D / 64], vsc[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t r = row0 + uint32_t(key_v(i));
+            const uint32_t va = sm + uint32_t(S::kCodes) + r * kRowC + uint32_t(lg) * (kRowC / 8);
+            if constexpr (D == 128) {
+              const uint2 w = lds64(va);
+              vw[i][0] = w.x, vw[i][1] = w.y;
+            } else {
+              vw[i][0] = lds32(va);
+            }
+            vsc[i] = lds_u8(sm + uint32_t(2 * S::kCodes + S::kScales) + r * kRowS +
+                            uint32_t(lg) * kRowS / 8);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[st]);
+
+          float s[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+          const uint32_t s0 = e4m3x2_to_half2(ksc[0]), s1 = e4m3x2_to_half2(ksc[1]);
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) {  // a word of codes per key: two k steps
+            uint32_t h0[4], h1[4];
+            e2m1x8_to_half2(kw[0][w], h0);
+            e2m1x8_to_half2(kw[1][w], h1);
+            const uint32_t f0 = bcast16(s0, w >> 1), f1 = bcast16(s1, w >> 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              h0[i] = hmul2(h0[i], f0);
+              h1[i] = hmul2(h1[i], f1);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(s[nt], h0[0], h1[0], h0[1], h1[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
+              mma_f16(s[nt], h0[2], h1[2], h0[3], h1[3], qf[nt][2 * w + 1][0],
+                      qf[nt][2 * w + 1][1]);
+            }
+          }
+          if (valid < kKv4Unit) {  // keys past the length
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (key_s + 8 * (i >> 1) >= valid) s[nt][i] = -INFINITY;
+            // such a row may hold any bytes: 0 * NaN must not arise
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key_v(i) >= valid) vsc[i] = 0;
+          }
+          probabilities(s, rs);
+          uint32_t p0[NT], p1[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            p0[nt] = transpose8x8(pack_half2(s[nt][0], s[nt][1]));
+            p1[nt] = transpose8x8(pack_half2(s[nt][2], s[nt][3]));
+          }
+          const uint32_t f0 = e4m3x2_to_half2(vsc[0] | vsc[1] << 8),
+                         f1 = e4m3x2_to_half2(vsc[2] | vsc[3] << 8);
+#pragma unroll
+          for (int w = 0; w < D / 64; ++w) {
+            uint32_t e0[4], d0[4], e1[4], d1[4];  // even, odd channels of the two key pairs
+            e2m1x8_to_half2((vw[0][w] & 0x0F0F0F0Fu) | ((vw[1][w] << 4) & 0xF0F0F0F0u), e0);
+            e2m1x8_to_half2(((vw[0][w] >> 4) & 0x0F0F0F0Fu) | (vw[1][w] & 0xF0F0F0F0u), d0);
+            e2m1x8_to_half2((vw[2][w] & 0x0F0F0F0Fu) | ((vw[3][w] << 4) & 0xF0F0F0F0u), e1);
+            e2m1x8_to_half2(((vw[2][w] >> 4) & 0x0F0F0F0Fu) | (vw[3][w] & 0xF0F0F0F0u), d1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e0[i] = hmul2(e0[i], f0);
+              d0[i] = hmul2(d0[i], f0);
+              e1[i] = hmul2(e1[i], f1);
+              d1[i] = hmul2(d1[i], f1);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(o[nt][w * 4 + i], e0[i], d0[i], e1[i], d1[i], p0[nt], p1[nt]);
+            }
+          }
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[st]);
+        }
+      }
+
+      // ------------------------------------------------- join the warps
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-      const uint16_t* kp[2];
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = j0 + lg + 8 * i;
-        kp[i] = j < a.B ? a.bk + ((size_t(n) * a.B + j) * a.Hkv + g) * D + lt * (D / 4) : nullptr;
-      }
+          for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
+          if (lg == 0) {
+            red_m[warp][nt * 8 + 2 * lt + i] = m[nt][i];
+            red_l[warp][nt * 8 + 2 * lt + i] = l[nt][i];
+          }
+          float* dst = red + (warp * RT + nt * 8 + 2 * lt + i) * (D + 4) + lg * (D / 8);
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint2 w[2];
+          for (int k = 0; k < KS; ++k)  // channels 2k, 2k+1 of this lane's run
+            *reinterpret_cast<float2*>(dst + 2 * k) = make_float2(o[nt][k][i], o[nt][k][i + 2]);
+        }
+      product_bar();
+      const bool whole = u0 == 0 && u1 == units;  // no other piece of this segment
+      const int slot = int(blockIdx.x) + seg;
+      for (int i = threadIdx.x; i < RT * (D / 4); i += kKv4Warps * 32) {
+        // (neighbouring threads write neighbouring channels of out, rows of a partial)
+        const int r = whole ? i / (D / 4) : i % RT, c4 = whole ? i % (D / 4) : i / RT;
+        if (r >= R) continue;
+        float M = -FLT_MAX;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          w[i] = kp[i] ? *reinterpret_cast<const uint2*>(kp[i] + k * 4) : make_uint2(0, 0);
+        for (int w = 0; w < kKv4Warps; ++w) M = fmaxf(M, red_m[w][r]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int r = nt * 8 + lg;
-          uint2 b = make_uint2(0, 0);
-          if (r < R)
-            b = *reinterpret_cast<const uint2*>(
-                a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + lt * (D / 4) +
-                k * 4);
-          mma_bf16(s[nt], w[0].x, w[1].x, w[0].y, w[1].y, b.x, b.y);
+        for (int w = 0; w < kKv4Warps; ++w) {
+          const float f = fast_exp2(red_m[w][r] - M);
+          const float4 x =
+              *reinterpret_cast<const float4*>(red + (w * RT + r) * (D + 4) + c4 * 4);
+          L += f * red_l[w][r];
+          acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+        }
+        if (whole) {
+          const float inv = L == 0.f ? 0.f : a.c.v_scale / L;
+          *reinterpret_cast<uint2*>(
+              a.out + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c4 * 4) =
+              make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        } else {
+          reinterpret_cast<float4*>(a.opart)[(size_t(slot) * (D / 4) + c4) * a.R16 + r] = acc;
+          if (c4 == 0) a.ml[size_t(slot) * a.R16 + r] = make_float2(M, L);
         }
       }
-      float f[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        f[nt][0] = f[nt][1] = fminf(a.scale * 1.4426950408889634f, FLT_MAX);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j0 + lg + 8 * (i >> 1) >= a.B) s[nt][i] = -INFINITY;
-      }
-      probabilities(s, f);
-      const float iv = 1.f / a.c.v_scale;
-      uint32_t p0[NT], p1[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        p0[nt] = transpose8x8(pack_bf16(s[nt][0] * iv, s[nt][1] * iv));
-        p1[nt] = transpose8x8(pack_bf16(s[nt][2] * iv, s[nt][3] * iv));
-      }
-      const uint16_t* vp[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = j0 + 2 * lt + (i & 1) + 8 * (i >> 1);
-        vp[i] = j < a.B ? a.bv + ((size_t(n) * a.B + j) * a.Hkv + g) * D + lg * (D / 8) : nullptr;
-      }
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {  // channels lg*D/8 + 2k, + 2k+1 of each key
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = vp[i] ? *reinterpret_cast<const uint32_t*>(vp[i] + 2 * k) : 0u;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_bf16(o[nt][k], __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
-                   __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632), p0[nt],
-                   p1[nt]);
-      }
-    }
-
-    // ------------------------------------------------- join the warps
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
-        if (lg == 0) {
-          red_m[warp][nt * 8 + 2 * lt + i] = m[nt][i];
-          red_l[warp][nt * 8 + 2 * lt + i] = l[nt][i];
-        }
-        float* dst = red + (size_t(warp) * RT + nt * 8 + 2 * lt + i) * (D + 4) + lg * (D / 8);
-#pragma unroll
-        for (int k = 0; k < KS; ++k)  // channels 2k, 2k+1 of this lane's run
-          *reinterpret_cast<float2*>(dst + 2 * k) = make_float2(o[nt][k][i], o[nt][k][i + 2]);
-      }
-    __syncthreads();
-    const bool whole = u0 == 0 && u1 == units;  // no other piece of this segment
-    const int slot = int(blockIdx.x) + seg;
-    for (int i = threadIdx.x; i < RT * (D / 4); i += kKv4Threads) {
-      // (neighbouring threads write neighbouring channels of out, rows of a partial)
-      const int rr = whole ? i / (D / 4) : i % RT, c4 = whole ? i % (D / 4) : i / RT;
-      const int r = rr;
-      if (r >= R) continue;
-      float M = -FLT_MAX;
-#pragma unroll
-      for (int w = 0; w < kKv4Warps; ++w) M = fmaxf(M, red_m[w][rr]);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float L = 0.f;
-#pragma unroll
-      for (int w = 0; w < kKv4Warps; ++w) {
-        const float mw = red_m[w][rr];
-        const float f = fast_exp2(mw - M);
-        const float4 x =
-            *reinterpret_cast<const float4*>(red + (size_t(w) * RT + rr) * (D + 4) + c4 * 4);
-        L += f * red_l[w][rr];
-        acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
-      }
-      if (whole) {
-        const float inv = L == 0.f ? 0.f : a.c.v_scale / L;
-        *reinterpret_cast<uint2*>(a.out + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D +
-                                  c4 * 4) =
-            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-      } else {
-        reinterpret_cast<float4*>(a.opart)[(size_t(slot) * (D / 4) + c4) * a.R16 + r] = acc;
-        if (c4 == 0) a.ml[size_t(slot) * a.R16 + r] = make_float2(M, L);
-      }
-    }
-    __syncthreads();  // the reduction buffers are free for the next piece
-    at = seg0 + u1;
+      product_bar();  // the reduction buffers are free for the next piece
+    });
   }
+  __syncthreads();
+  if (threadIdx.x == 0 && failed)
+    record_error(err, DEV_TIMEOUT_TMA | DEV_K_KV4_ROWS | (failed << 16));
 }
 
 // Joins the pieces of every segment that has more than one, and writes zeros
@@ -463,7 +526,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
 constexpr int kKv4JoinThreads = 1024, kKv4JoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(kKv4JoinThreads)
-    kv4_join_kernel(const Kv4AttnArgs a, int unit, int blk_units, int min_share, int subs) {
+    kv4_join_kernel(const Kv4AttnArgs a, int blk_units, int subs) {
   constexpr int TPG = kKv4JoinRows * (D / 4), GR = kKv4JoinThreads / TPG;
   __shared__ float4 part[GR][TPG];
   __shared__ float part_m[GR][kKv4JoinRows], part_l[GR][kKv4JoinRows];
@@ -473,11 +536,10 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
   const int grp = threadIdx.x / TPG, item = threadIdx.x % TPG;
   const int rr = item % kKv4JoinRows, c4 = item / kKv4JoinRows;
   const int r = int(blockIdx.y) * kKv4JoinRows + rr, rc = min(r, R - 1);
-  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, unit, blk_units), a.Hkv,
-                                   a.ctas, min_share);
-  const int units = kv4_units(a.ctx[n], a.L_max, unit, blk_units);
+  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, blk_units), a.Hkv, a.ctas);
+  const int units = kv4_units(a.ctx[n], a.L_max, blk_units);
   const int first =
-      a.Hkv * kv4_total_units(a.ctx, n, a.L_max, unit, blk_units) + g * units;
+      a.Hkv * kv4_total_units(a.ctx, n, a.L_max, blk_units) + g * units;
   uint2* out = reinterpret_cast<uint2*>(
       a.out + ((size_t(n) * a.B + rc / G) * a.Hq + g * G + rc % G) * D + c4 * 4);
   if (units == 0) {
@@ -536,11 +598,11 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
 // ------------------------------------------------------------------- host
 
 template <int D, int NT>
-static cudaError_t launch_rows(const Kv4AttnArgs& a, cudaStream_t st) {
-  constexpr size_t smem = size_t(kKv4Warps) * 8 * NT * (D + 4) * 4;
+static cudaError_t launch_rows(const Kv4AttnArgs& a, uint32_t* err, cudaStream_t st) {
+  const size_t smem = RowsSmem<D, NT>::kTotal;
   HERALD_CHECK_LAUNCH(ensure_smem(kv4_attn_kernel<D, NT>, smem));
-  return launch_k("kv4_attn_kernel", kv4_attn_kernel<D, NT>,
-                  dim3(unsigned(a.ctas)), dim3(kKv4Threads), smem, st, a);
+  return launch_k("kv4_attn_kernel", kv4_attn_kernel<D, NT>, dim3(unsigned(a.ctas)),
+                  dim3(kKv4Threads), smem, st, a, err);
 }
 
 // Workspace: error word, then (m, l) and O of every partial.
@@ -573,24 +635,24 @@ cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4D
   a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max, a.R16 = w.R16;
   a.c = c;
   const bool tc = R > kKv4MmaRows;
-  const int nt = R <= 8 ? 1 : 2;
-  a.ctas = std::min(kKv4MaxCtas, tc ? num_sms : (nt == 1 ? 2 : 1) * num_sms);
+  uint32_t* err = reinterpret_cast<uint32_t*>(p);
+  a.ctas = std::min(kKv4MaxCtas, (!tc && R <= 8 ? 2 : 1) * num_sms);
   if (tc)
-    HERALD_CHECK_LAUNCH(launch_kv4_attn_tc(dm.d, R, a, reinterpret_cast<uint32_t*>(p), st));
+    HERALD_CHECK_LAUNCH(launch_kv4_attn_tc(dm.d, R, a, err, st));
   else if (dm.d == 128)
-    HERALD_CHECK_LAUNCH((nt == 1 ? launch_rows<128, 1>(a, st) : launch_rows<128, 2>(a, st)));
+    HERALD_CHECK_LAUNCH(
+        (R <= 8 ? launch_rows<128, 1>(a, err, st) : launch_rows<128, 2>(a, err, st)));
   else
-    HERALD_CHECK_LAUNCH((nt == 1 ? launch_rows<64, 1>(a, st) : launch_rows<64, 2>(a, st)));
-  const int unit = tc ? kKv4TcKeys : kKv4Unit;
-  const int blk_units = bk ? cdiv(dm.B, unit) : 0, min_share = tc ? 1 : kKv4MinShare;
+    HERALD_CHECK_LAUNCH((R <= 8 ? launch_rows<64, 1>(a, err, st) : launch_rows<64, 2>(a, err, st)));
+  const int blk_units = !bk ? 0 : tc ? cdiv(dm.B, kKv4Tile) : kKv4BlkJoined;
   const int subs = tc && R <= kTileM ? 2 : 1;
   const dim3 grid(unsigned(dm.N * dm.Hkv), unsigned(cdiv(R, kKv4JoinRows)));
   if (dm.d == 128)
     HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<128>, grid,
-                                 dim3(kKv4JoinThreads), 0, st, a, unit, blk_units, min_share, subs));
+                                 dim3(kKv4JoinThreads), 0, st, a, blk_units, subs));
   else
     HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<64>, grid,
-                                 dim3(kKv4JoinThreads), 0, st, a, unit, blk_units, min_share, subs));
+                                 dim3(kKv4JoinThreads), 0, st, a, blk_units, subs));
   return cudaGetLastError();
 }
 

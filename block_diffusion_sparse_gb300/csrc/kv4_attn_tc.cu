@@ -3,7 +3,7 @@
 //
 // The tensor cores take fp16 operands from shared memory, so the codes are
 // turned into fp16 there (exact, kv4.cuh), once per 128-key tile for up to 256
-// query rows.  One CTA per SM walks its share of the keys (kv4_split, units of
+// query rows.  One CTA per SM walks its share of the keys (kv4_split, tiles of
 // 128 keys, a segment's block keys first):
 //   warps 17, 19 copy the codes and scales of a tile's K and V rows from its pages
 //                into raw slots (bulk copies; the pages of a tile in parallel
@@ -36,7 +36,7 @@
 
 namespace herald {
 
-constexpr int kTcKeys = kKv4TcKeys;        // keys per tile
+constexpr int kTcKeys = kKv4Tile;          // keys per tile
 constexpr int kTcStep = 64;                // keys per step of a stream
 constexpr int kTcBufs = 4;                 // operand buffers (128 keys of K or V)
 // Raw slots of K and of V tiles: as many as fit beside the operands.
@@ -57,53 +57,6 @@ enum : uint32_t {
   W_P_FULL = 0x40, W_V_FULL = 0x80, W_PV_DONE = 0x100, W_S_FULL = 0x200, W_MASK = 0x400,
   W_O_DONE = 0x800
 };
-
-// Bounded wait; false when it ran out, or when another wait of the CTA has: a
-// role that gets false leaves its loops at once (it touches no barrier and
-// starts no copy or product any more), and the kernel returns.
-struct TcWait {
-  volatile uint32_t* failed;  // shared: the wait that ran out first
-  HERALD_DEV bool slow(uint64_t* bar, uint32_t parity, uint32_t which) const {
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i)
-        if (mbar_try_wait_for(bar, parity, 20000u)) return true;
-      if (*failed) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        *failed = which;
-        return false;
-      }
-    }
-  }
-  // The answer for a whole warp, which leaves converged: lanes may see a
-  // barrier complete in different polls, and the tensor-memory instructions
-  // that follow (.sync.aligned) want the warp in one piece.
-  HERALD_DEV bool operator()(uint64_t* bar, uint32_t parity, uint32_t which) const {
-    const bool ok = mbar_try_wait(bar, parity) || slow(bar, parity, which);
-    return __all_sync(0xffffffffu, ok);
-  }
-};
-
-// Shared memory by 32-bit address (the aligned base of the dynamic part is a
-// generic pointer to the compiler).
-HERALD_DEV uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-HERALD_DEV uint32_t lds_u16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-  return v;
-}
-HERALD_DEV void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
-}
 
 struct TcSmem {
   uint32_t q, buf, raw, total;
@@ -252,17 +205,16 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   tmem_setup(&tmem_base, 512);
   const uint32_t tm = tmem_base;
   griddep_enter();
-  const TcWait wait{&failed};
+  const Kv4Wait wait{&failed};
 
   const int G = a.Hq / a.Hkv, R = a.B * G;
   const int blk_units = a.bk ? (a.B + kTcKeys - 1) / kTcKeys : 0;
-  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, kTcKeys, blk_units), a.Hkv,
-                                   a.ctas, 1);
+  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, blk_units), a.Hkv, a.ctas);
   const int at0 = int(blockIdx.x) * split.share;
   const int end = min(at0 + split.share, split.total);
   int n_first = 0;
   int first0 = 0;
-  if (at0 < end) kv4_find(a.ctx, a.N, a.L_max, kTcKeys, blk_units, a.Hkv, at0, &n_first, &first0);
+  if (at0 < end) kv4_find(a.ctx, a.N, a.L_max, blk_units, a.Hkv, at0, &n_first, &first0);
 
   // Every role walks the same pieces: body(n, g, seg, ctx, units, u0, u1) with
   // tiles u0 <= u < u1 of the segment, the first blk_units of them block tiles;
@@ -272,7 +224,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
     int n = n_first;
     while (at < end) {
       const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
-      const int units = kv4_units(ctx, a.L_max, kTcKeys, blk_units);
+      const int units = kv4_units(ctx, a.L_max, blk_units);
       if (units == 0 || at >= first + a.Hkv * units) {
         first += a.Hkv * units;
         ++n;
@@ -339,18 +291,20 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                 }
                 mask_scores(ts, msk, keys - k0);
               }
-              uint32_t x[2][32];
-              tmem_ld32_nowait(ts, x[0]);
-              tmem_ld32_nowait(ts + 32u, x[1]);
-              tmem_wait_ld(x[0]);
-              tmem_wait_ld(x[1]);
-              float mx = -INFINITY, mx1 = -INFINITY;
+              float mx = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < 64; c += 32) {
+                uint32_t x[32];
+                tmem_ld32_nowait(ts + uint32_t(c), x);
+                tmem_wait_ld(x);
+                float m1 = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                mx = fmax3f(mx, __uint_as_float(x[0][i]), __uint_as_float(x[0][i + 1]));
-                mx1 = fmax3f(mx1, __uint_as_float(x[1][i]), __uint_as_float(x[1][i + 1]));
+                for (int i = 0; i < 32; i += 4) {
+                  mx = fmax3f(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                  m1 = fmax3f(m1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+                }
+                mx = fmaxf(mx, m1);
               }
-              mx = fmaxf(mx, mx1);
               const bool move = mx * f - m > kTcAbove;
               if (__any_sync(0xffffffffu, move)) {
                 float k = 1.f;
@@ -380,10 +334,14 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               }
               const uint64_t nm2 = f2_pack(-m, -m);
               uint64_t sum = f2_pack(0.f, 0.f);
-              exp32(x[0], f2, nm2, &sum);
-              store_p32(ts, x[0], blk, iv);
-              exp32(x[1], f2, nm2, &sum);
-              store_p32(ts + 16u, x[1], blk, iv);
+#pragma unroll 1
+              for (int c = 0; c < 64; c += 32) {
+                uint32_t x[32];
+                tmem_ld32_nowait(ts + uint32_t(c), x);
+                tmem_wait_ld(x);
+                exp32(x, f2, nm2, &sum);
+                store_p32(ts + uint32_t(c / 2), x, blk, iv);
+              }
               float s0, s1;
               f2_unpack(sum, s0, s1);
               l += s0 + s1;
@@ -535,11 +493,9 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
             // Rows and chunks are dealt so that the eight lanes of a
             // shared-memory phase read eight different 16-byte bank groups
             // ((r&1)*4 + j for d = 128, (r&3)*2 + j for 64) and write eight (the
-            // swizzle's XOR of r&7 with the chunk).  All raw bytes are taken
-            // first: the copies of a later item start while these are turned.
+            // swizzle's XOR of r&7 with the chunk).  The loop is kept rolled, the
+            // next chunk's bytes read ahead: the roles share the instruction cache.
             constexpr int kTasks = kTcKeys * (kRowC / 16) / 128;
-            uint4 code[kTasks];
-            uint32_t sc[kTasks];
             const int j1 = (lane >> 2) & 1;
             const int j = D == 128 ? ((lane >> 1) & 1) + 2 * j1 : lane & 1;
             auto row_of = [&](int s) {
@@ -547,32 +503,29 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                                     2 * (j1 ^ (s & 1))
                               : cw * 32 + s * 16 + (lane >> 1);
             };
-#pragma unroll
-            for (int s = 0; s < kTasks; ++s) {
-              const int r = row_of(s);
-              code[s] = lds128(rc + uint32_t(r * kRowC + j * 16));
-              sc[s] = lds_u16(rsc + uint32_t(r * kRowS + j * 2));
-            }
+            uint32_t counts = ~0u;  // keys of this warp's rows that count
             if (kv) {  // a value row that does not count may hold any bytes: no 0 * NaN
               if (!wait(&mask_full[mt % kTcMasks], (mt / kTcMasks) & 1, W_MASK)) return false;
-              const uint32_t m = *(volatile uint32_t*)&key_mask[mt % kTcMasks][cw];
-#pragma unroll
-              for (int s = 0; s < kTasks; ++s)
-                if (!(m >> (row_of(s) & 31) & 1)) sc[s] = 0;
+              counts = *(volatile uint32_t*)&key_mask[mt % kTcMasks][cw];
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&raw_free[kv][rm]);
             if (item >= uint32_t(kTcBufs) &&
                 !wait(&buf_free[b], (item / kTcBufs - 1) & 1, W_BUF_FREE))
               return false;
-#pragma unroll
+            const uint32_t dh = dst + uint32_t(D == 128 ? j >> 1 : 0) * 16384u;
+            int r = row_of(0);
+            uint4 code = lds128(rc + uint32_t(r * kRowC + j * 16));
+            uint32_t sc = lds_u16(rsc + uint32_t(r * kRowS + j * 2));
+#pragma unroll 1
             for (int s = 0; s < kTasks; ++s) {
-              const uint32_t r = uint32_t(row_of(s));
+              const uint32_t words[4] = {code.x, code.y, code.z, code.w};
+              const uint32_t s2 = (counts >> (r & 31) & 1) ? e4m3x2_to_half2(sc) : 0u;
               // chunk (j&1)*4 + k of the row: its place is the first one's, XOR k
-              const uint32_t at = dst + uint32_t(D == 128 ? j >> 1 : 0) * 16384u +
-                                  sw128_off(r, uint32_t((j & 1) * 4));
-              const uint32_t s2 = e4m3x2_to_half2(sc[s]);
-              const uint32_t words[4] = {code[s].x, code[s].y, code[s].z, code[s].w};
+              const uint32_t at = dh + sw128_off(uint32_t(r), uint32_t((j & 1) * 4));
+              if (s + 1 < kTasks) {
+                r = row_of(s + 1);
+                code = lds128(rc + uint32_t(r * kRowC + j * 16));
+                sc = lds_u16(rsc + uint32_t(r * kRowS + j * 2));
+              }
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint32_t h[4];
@@ -583,6 +536,8 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                 sts128(at ^ uint32_t(k << 4), h[0], h[1], h[2], h[3]);
               }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_free[kv][rm]);
             ++mt;
           }
           publish(&buf_full[b]);

@@ -198,33 +198,57 @@ __global__ void __launch_bounds__(kKv4MoveThreads)
   }
 }
 
-// grid (blocks, N*Hkv), block D: the means of the blocks that tokens [ctx,
-// ctx + tokens) fall into, over the rows below ctx + tokens; thread e sums
-// channel e.  A row without a page counts as zeros.
-__global__ void kv4_pool_kernel(const Kv4Dev c, const int32_t* __restrict__ ctx,
-                                const int32_t* __restrict__ n_tok, int T, int Hkv, int d, int L_max,
-                                int Bk, int nb_max, float* __restrict__ pooled) {
+// grid (blocks, N*Hkv): the means of the blocks that tokens [ctx, ctx + tokens)
+// fall into, over the rows below ctx + tokens.  D/16 lanes per row (16 channels
+// each), the block's rows dealt over the rest of the CTA; the threads' sums are
+// added in a fixed tree.  A row without a page counts as zeros.  (One thread per
+// channel walking the rows, a page lookup and two byte loads per row, took 17 us
+// for one block of 64; this 3 us.)
+template <int D>
+__global__ void __launch_bounds__(kKv4MoveThreads)
+    kv4_pool_kernel(const Kv4Dev c, const int32_t* __restrict__ ctx,
+                    const int32_t* __restrict__ n_tok, int T, int Hkv, int L_max, int Bk,
+                    int nb_max, float* __restrict__ pooled) {
+  constexpr int LPR = D / 16, RPC = kKv4MoveThreads / LPR;
+  __shared__ float sums[RPC][D + 4];
   griddep_enter();
-  const int seg = blockIdx.y, n = seg / Hkv, g = seg - n * Hkv, e = threadIdx.x;
+  const int seg = blockIdx.y, n = seg / Hkv, g = seg - n * Hkv;
   const int L0 = min(max(ctx[n], 0), L_max);
   const int end = min(L0 + (n_tok ? min(max(n_tok[n], 0), T) : T), L_max);
   const int b = L0 / Bk + int(blockIdx.x);
   if (end == L0 || b * int64_t(Bk) >= end) return;
   const int r0 = b * Bk, r1 = min(end, r0 + min(Bk, L_max - r0));
-  float acc = 0.f;
-  for (int r = r0; r < r1; ++r) {
+  const int ch = threadIdx.x % LPR, rr = threadIdx.x / LPR;
+  float acc[16] = {};
+  for (int r = r0 + rr; r < r1; r += RPC) {
     const int phys = kv4_page(c, n, r >> c.page_log2);
     if (phys < 0) {
       debug_flag(true, DEV_BAD_INDEX);
       continue;
     }
     const size_t row = kv4_row(c, phys, Hkv, g, r);
-    const uint32_t code = c.kc[row * (d / 2) + (e >> 1)] >> (4 * (e & 1));
-    const uint32_t h = e2m1x2_to_half2(code & 0xFu);
-    acc += __low2float(*reinterpret_cast<const __half2*>(&h)) *
-           e4m3_to_float(c.ks[row * (d / 16) + (e >> 4)]);
+    const uint2 w = *reinterpret_cast<const uint2*>(c.kc + row * (D / 2) + ch * 8);
+    const float s = e4m3_to_float(c.ks[row * LPR + ch]);
+    uint32_t h[8];
+    e2m1x8_to_half2(w.x, *reinterpret_cast<uint32_t(*)[4]>(h));
+    e2m1x8_to_half2(w.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      acc[2 * i] += f.x * s;
+      acc[2 * i + 1] += f.y * s;
+    }
   }
-  pooled[(size_t(seg) * nb_max + b) * d + e] = acc * c.k_scale / float(r1 - r0);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sums[rr][ch * 16 + i] = acc[i];
+  for (int half = RPC / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < half * D; i += kKv4MoveThreads)
+      sums[i / D][i % D] += sums[i / D + half][i % D];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < D; e += kKv4MoveThreads)
+    pooled[(size_t(seg) * nb_max + b) * D + e] = sums[0][e] * c.k_scale / float(r1 - r0);
 }
 
 __global__ void kv4_advance_kernel(int32_t* ctx, const int32_t* n_tok, int N, int T, int L_max) {
@@ -312,11 +336,17 @@ cudaError_t launch_kv4_append(const herald_dims& dm, int T, const int32_t* n_tok
   else
     HERALD_CHECK_LAUNCH(launch_k("kv4_append_kernel", kv4_append_kernel<64>, grid,
                                  dim3(kKv4MoveThreads), 0, st, a));
-  if (pooled)
-    HERALD_CHECK_LAUNCH(launch_k("kv4_pool_kernel", kv4_pool_kernel,
-                                 dim3(unsigned(cdiv(T - 1, Bk) + 1), unsigned(dm.N * dm.Hkv)),
-                                 dim3(unsigned(dm.d)), 0, st, *cache, ctx, n_tok, T, dm.Hkv, dm.d,
-                                 dm.L_max, Bk, cdiv(dm.L_max, Bk), pooled));
+  if (pooled) {
+    const dim3 pg(unsigned(cdiv(T - 1, Bk) + 1), unsigned(dm.N * dm.Hkv));
+    if (dm.d == 128)
+      HERALD_CHECK_LAUNCH(launch_k("kv4_pool_kernel", kv4_pool_kernel<128>, pg,
+                                   dim3(kKv4MoveThreads), 0, st, *cache, ctx, n_tok, T, dm.Hkv,
+                                   dm.L_max, Bk, cdiv(dm.L_max, Bk), pooled));
+    else
+      HERALD_CHECK_LAUNCH(launch_k("kv4_pool_kernel", kv4_pool_kernel<64>, pg,
+                                   dim3(kKv4MoveThreads), 0, st, *cache, ctx, n_tok, T, dm.Hkv,
+                                   dm.L_max, Bk, cdiv(dm.L_max, Bk), pooled));
+  }
   if (advance)
     HERALD_CHECK_LAUNCH(launch_k("kv4_advance_kernel", kv4_advance_kernel,
                                  dim3(unsigned(cdiv(dm.N, 256))), dim3(256), 0, st, ctx, n_tok,

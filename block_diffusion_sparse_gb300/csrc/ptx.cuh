@@ -30,6 +30,7 @@ enum : uint32_t {
   DEV_K_SCAN = 7u << 8,
   DEV_K_ATTN_FLASH = 8u << 8,
   DEV_K_KV4_ATTN = 9u << 8,
+  DEV_K_KV4_ROWS = 10u << 8,
 };
 
 // Checks of the debug build (compiled with -DHERALD_DEBUG): a kernel compares

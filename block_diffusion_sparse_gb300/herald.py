@@ -218,22 +218,20 @@ def lib() -> C.CDLL:
 
 
 def _p(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x
     raise TypeError(f"expected a tensor or an address, got {type(x)}")
 
 
 def _s(stream):
-    if stream is None:
-        return None
-    if isinstance(stream, int):
-        return stream
-    if hasattr(stream, "cuda_stream"):
+    try:
         return stream.cuda_stream
+    except AttributeError:
+        if stream is None or isinstance(stream, int):
+            return stream
     raise TypeError(f"expected a stream, got {type(stream)}")
 
 
@@ -456,14 +454,16 @@ def _token_ld(x, ld, what):
         return int(ld)
     if x is None or isinstance(x, int):
         return 0
-    s, shape = x.stride(), x.shape
-    if x.dim() != 4 or s[3] != 1 or (shape[2] > 1 and s[2] != shape[3]):
+    if x.dim() != 4:
+        raise ValueError(f"{what}: expected [N, T, heads, d]")
+    (n, t, h, d), (sn, st, sh, sd) = x.shape, x.stride()
+    if sd != 1 or (h > 1 and sh != d):
         raise ValueError(f"{what}: heads and channels of a token must be contiguous")
     # (the stride of an axis of one entry says nothing: take the other's)
-    step = s[1] if shape[1] > 1 else s[0] if shape[0] > 1 else shape[2] * shape[3]
-    if shape[0] > 1 and s[0] != shape[1] * step:
+    step = st if t > 1 else sn if n > 1 else h * d
+    if n > 1 and sn != t * step:
         raise ValueError(f"{what}: sequences must follow each other at T token strides")
-    return int(step)
+    return step
 
 
 def herald_kv4_append(d, T, q, k, v, ctx_len, cache, q_rot, k_rot, rope=None, n_tok=None,

@@ -107,7 +107,8 @@ herald_status herald_inject_launch_failure(int after, int cuda_error);
  * out first (1 = a copy wait, 2 = a tensor-core or pipeline-stage wait);
  * bits 8-15: the kernel (1 refine pass 1, 2 refine pass 2, 3 fused refine,
  * 4 split attention, 5 cluster attention, 6 pool attention, 7 stage-1 scan,
- * 8 pipelined attention, 9 attention over a paged 4-bit cache);
+ * 8 pipelined attention, 9 and 10 attention over a paged 4-bit cache, many
+ * and few rows);
  * bits 16-31: which of the kernel's waits (the
  * pipelined attention: 0x1 K ring slot, 0x2 V ring slot, 0x4 query tile,
  * 0x8 K tile, 0x10 S buffer free, 0x20 P ready, 0x40 V tile, 0x80 S ready,
@@ -115,7 +116,8 @@ herald_status herald_inject_launch_failure(int after, int cuda_error);
  * partials, 0x800 the previous tile's P V done; the attention over a paged
  * 4-bit cache: 0x1 raw slot, 0x2 raw codes, 0x4 operand buffer free, 0x8
  * queries free, 0x10 queries staged, 0x20 K ready, 0x40 P ready, 0x80 V ready,
- * 0x100 P V done, 0x200 S ready, 0x400 key masks, 0x800 O ready).
+ * 0x100 P V done, 0x200 S ready, 0x400 key masks, 0x800 O ready; with few rows
+ * 0x1 stage free, 0x2 stage full).
  * Synchronises `stream` first. */
 herald_status herald_workspace_error(void *ws, void *stream, uint32_t *code);
 
