@@ -175,15 +175,12 @@ HERALD_DEV int kv4_units(int ctx, int L_max, int blk_units) {
   const int t = (min(max(ctx, 0), L_max) + kKv4Tile - 1) / kKv4Tile;
   return blk_units == kKv4BlkJoined ? max(t, 1) : t + blk_units;
 }
-// Sum over the sequences of their tiles (per KV head); every lane of a warp
-// calls it and gets the total.
+// Sum over the first N sequences of their tiles (per KV head); called by a
+// whole warp.
 HERALD_DEV int kv4_total_units(const int32_t* ctx, int N, int L_max, int blk_units) {
   int sum = 0;
-  for (int n = int(threadIdx.x & 31); n < N; n += 32)
-    sum += kv4_units(ctx[n], L_max, blk_units);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return warp_same(sum);
+  for (int n = int(threadIdx.x & 31); n < N; n += 32) sum += kv4_units(ctx[n], L_max, blk_units);
+  return warp_same(__reduce_add_sync(0xffffffffu, sum));
 }
 HERALD_DEV Kv4Split kv4_split(int per_head, int Hkv, int ctas) {
   Kv4Split s;
@@ -191,32 +188,45 @@ HERALD_DEV Kv4Split kv4_split(int per_head, int Hkv, int ctas) {
   s.share = max((s.total + ctas - 1) / ctas, 1);
   return s;
 }
-// The sequence that holds tile `at` (of all segments, at < total) and the
-// first tile of that sequence's first segment; called by a whole warp.
-HERALD_DEV void kv4_find(const int32_t* ctx, int N, int L_max, int blk_units, int Hkv, int at,
-                         int* n_out, int* first_out) {
+// A CTA's share: tiles [at, end); with at < end, n is the sequence that holds
+// tile `at` and first the first tile of that sequence's first segment.  Called
+// by a whole warp.
+struct Kv4Share {
+  int at, end, n, first;
+};
+HERALD_DEV Kv4Share kv4_share(const int32_t* ctx, int N, int L_max, int blk_units, int Hkv,
+                              int ctas, int cta) {
   const int lane = threadIdx.x & 31;
+  // (the lengths of the first 32 sequences are loaded once)
+  const int own0 = lane < N ? kv4_units(ctx[lane], L_max, blk_units) : 0;
+  int sum = own0;
+  for (int n = lane + 32; n < N; n += 32) sum += kv4_units(ctx[n], L_max, blk_units);
+  const Kv4Split split = kv4_split(int(__reduce_add_sync(0xffffffffu, sum)), Hkv, ctas);
+  Kv4Share r;
+  r.at = warp_same(cta * split.share);
+  r.end = warp_same(min(r.at + split.share, split.total));
+  r.n = r.first = 0;
+  if (r.at >= r.end) return r;
   int base = 0;
   for (int n0 = 0; n0 < N; n0 += 32) {
     const int n = n0 + lane;
-    const int own = n < N ? Hkv * kv4_units(ctx[n], L_max, blk_units) : 0;
+    const int own = Hkv * (n0 == 0 ? own0 : n < N ? kv4_units(ctx[n], L_max, blk_units) : 0);
     int inc = own;  // inclusive scan
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += up;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > at);
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > r.at);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      *n_out = n0 + l;
-      *first_out = base + __shfl_sync(0xffffffffu, inc - own, l);
-      return;
+      r.n = warp_same(n0 + l);
+      r.first = base + __shfl_sync(0xffffffffu, inc - own, l);
+      return r;
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  *n_out = N;
-  *first_out = base;
+  return r;
 }
 
 }  // namespace herald

@@ -113,18 +113,15 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
   const Kv4Wait wait{&failed};
   const int G = a.Hq / a.Hkv, R = a.B * G;
   const int blk_units = a.bk ? kKv4BlkJoined : 0;
-  const Kv4Split split =
-      kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, blk_units), a.Hkv, a.ctas);
-  const int at0 = int(blockIdx.x) * split.share;
-  const int end = min(at0 + split.share, split.total);
-  if (at0 >= end) return;
-  int n0, first0;
-  kv4_find(a.ctx, a.N, a.L_max, blk_units, a.Hkv, at0, &n0, &first0);
+  const Kv4Share sh =
+      kv4_share(a.ctx, a.N, a.L_max, blk_units, a.Hkv, a.ctas, int(blockIdx.x));
+  const int end = sh.end;
+  if (sh.at >= end) return;
 
   // Both roles walk the same pieces: body(n, g, seg, ctx, units, u0, u1), cache
   // tiles u0 <= u < min(u1, tiles of ctx), the block's keys with tile 0.
   auto pieces = [&](auto&& body) {
-    int at = at0, first = first0, n = n0;
+    int at = sh.at, first = sh.first, n = sh.n;
     while (at < end) {
       const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
       const int units = kv4_units(ctx, a.L_max, blk_units);
@@ -530,7 +527,6 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
   constexpr int TPG = kKv4JoinRows * (D / 4), GR = kKv4JoinThreads / TPG;
   __shared__ float4 part[GR][TPG];
   __shared__ float part_m[GR][kKv4JoinRows], part_l[GR][kKv4JoinRows];
-  griddep_enter();
   const int seg = blockIdx.x, n = seg / a.Hkv, g = seg - n * a.Hkv;
   const int G = a.Hq / a.Hkv, R = a.B * G;
   const int grp = threadIdx.x / TPG, item = threadIdx.x % TPG;
@@ -540,6 +536,10 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
   const int units = kv4_units(a.ctx[n], a.L_max, blk_units);
   const int first =
       a.Hkv * kv4_total_units(a.ctx, n, a.L_max, blk_units) + g * units;
+  // The lengths were read before the grid-dependency wait: they were written
+  // before the attention kernel's own wait ended, and it lets this kernel start
+  // only after that.
+  griddep_enter();
   uint2* out = reinterpret_cast<uint2*>(
       a.out + ((size_t(n) * a.B + rc / G) * a.Hq + g * G + rc % G) * D + c4 * 4);
   if (units == 0) {

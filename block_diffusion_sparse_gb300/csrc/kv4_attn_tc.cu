@@ -9,12 +9,13 @@
 //                into raw slots (bulk copies; the pages of a tile in parallel
 //                lanes)
 //   warps 8-11, 12-15 turn the K and the V slots into fp16 128-byte-swizzled
-//                operand buffers; together they stage the queries
+//                operand buffers
 //   warps 16, 18 a tcgen05.mma issuer per stream of S = Q K^T into a score buffer
 //   warps 20, 21 one per stream of O += P V with P read from tensor memory
 //                (issuing an mma takes a warp about a hundred cycles: with one
 //                warp per stream for both products that was the longest chain)
-//   warps 0-3, 4-7 softmax of a stream, a thread per query row
+//   warps 0-3, 4-7 softmax of a stream, a thread per query row; together they stage
+//                the queries
 // Two streams run side by side: with more than 128 rows a stream is a row tile
 // and takes every key tile, else both streams have the same rows and take
 // alternate key tiles (their partial outputs are joined like those of two
@@ -209,19 +210,15 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
 
   const int G = a.Hq / a.Hkv, R = a.B * G;
   const int blk_units = a.bk ? (a.B + kTcKeys - 1) / kTcKeys : 0;
-  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, blk_units), a.Hkv, a.ctas);
-  const int at0 = int(blockIdx.x) * split.share;
-  const int end = min(at0 + split.share, split.total);
-  int n_first = 0;
-  int first0 = 0;
-  if (at0 < end) kv4_find(a.ctx, a.N, a.L_max, blk_units, a.Hkv, at0, &n_first, &first0);
+  const Kv4Share sh =
+      kv4_share(a.ctx, a.N, a.L_max, blk_units, a.Hkv, a.ctas, int(blockIdx.x));
+  const int end = sh.end;
 
   // Every role walks the same pieces: body(n, g, seg, ctx, units, u0, u1) with
   // tiles u0 <= u < u1 of the segment, the first blk_units of them block tiles;
   // it returns false to leave (a wait ran out).
   auto pieces = [&](auto&& body) {
-    int at = at0, first = first0;
-    int n = n_first;
+    int at = sh.at, first = sh.first, n = sh.n;
     while (at < end) {
       const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
       const int units = kv4_units(ctx, a.L_max, blk_units);
@@ -265,12 +262,61 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
       while (u < u1) {  // a phase: block tiles, or cache tiles
         const bool blk = u < blk_units;
         const int pe = blk ? min(u1, blk_units) : u1;
-        // the phase's queries are staged (so this thread's arrival on q_free
-        // below never runs into an earlier phase, with or without tiles here)
+        // the phase's queries: staged by these warps (the conversion starts on
+        // the keys meanwhile) once the scores and factors of the phase before are
+        // done with
+        if (phase > 0 && !wait(&q_free, (phase - 1) & 1, W_Q_FREE)) return false;
+        // queries: D/16 lanes per row, 16 channels each
+        constexpr int LPR = D / 16;
+        constexpr int kPass = kTcSoft / LPR, kRows = kTileM / kPass;  // rows per pass and tile
+        const int c = int(threadIdx.x) % LPR;
+#pragma unroll 1
+        for (int mt2 = 0; mt2 < MT; ++mt2) {
+          uint4 x4[kRows][2];  // (every load of a tile first)
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const int r = mt2 * kTileM + i * kPass + int(threadIdx.x) / LPR;
+            x4[i][0] = x4[i][1] = make_uint4(0, 0, 0, 0);
+            if (r < R) {
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c * 16);
+              x4[i][0] = src[0];
+              x4[i][1] = src[1];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const int rr = i * kPass + int(threadIdx.x) / LPR;
+            uint32_t x[8] = {x4[i][0].x, x4[i][0].y, x4[i][0].z, x4[i][0].w,
+                             x4[i][1].x, x4[i][1].y, x4[i][1].z, x4[i][1].w};
+            if (!blk) {  // fp16 scaled per row by a power of two (see kv4_attn.cu)
+              float mx = 0.f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mx = fmaxf(mx, fmaxf(fabsf(bf16lo(x[k])), fabsf(bf16hi(x[k]))));
+#pragma unroll
+              for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              float up, f;
+              kv4_query_scale(mx, a.scale * a.c.k_scale, &up, &f);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = pack_half2(bf16lo(x[k]) * up, bf16hi(x[k]) * up);
+              if (c == 0) row_f[mt2 * kTileM + rr] = f;
+            }
+            const uint32_t dst = qs + uint32_t(mt2) * kTile + uint32_t(c >> 2) * 16384u;
+            const uint32_t c8 = uint32_t(c & 3) * 2u;
+            sts128(dst + sw128_off(uint32_t(rr), c8), x[0], x[1], x[2], x[3]);
+            sts128(dst + sw128_off(uint32_t(rr), c8 + 1), x[4], x[5], x[6], x[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
         if (!wait(&q_full, phase & 1, W_Q_FULL)) return false;
         const float f = blk ? fminf(a.scale * 1.4426950408889634f, FLT_MAX)
                             : *(volatile float*)&row_f[row];
         const uint64_t f2 = f2_pack(f, f);
+        mbar_arrive(&q_free);  // (this thread has read its factor of the phase)
+        ++phase;
         for (; u < pe; ++u, ++tile) {
           const uint32_t mask_no = mt;
           if (!blk) ++mt;
@@ -353,8 +399,6 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
             any = true;
           }
         }
-        mbar_arrive(&q_free);  // (this thread has read its factor of the phase)
-        ++phase;
       }
       // the piece's rows: O once the last P V is done (pv_done would not tell:
       // the last two may both be under way)
@@ -406,10 +450,10 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
     });
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    // --------------------------------------- queries, operand conversion
+    // ------------------------------------------------ operand conversion
     const int ct = threadIdx.x - kTcSoft;
     const int kv = (warp - 8) >> 2, cw = warp & 3;  // K or V items; warp of the four
-    uint32_t tile = 0, mt = 0, phase = 0;
+    uint32_t tile = 0, mt = 0;
     auto publish = [&](uint64_t* bar) {  // this warp's writes are ready for the tensor cores
       fence_proxy_async_smem();
       __syncwarp();
@@ -420,51 +464,6 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
       while (u < u1) {
         const bool blk = u < blk_units;
         const int pe = blk ? min(u1, blk_units) : u1;
-        if (phase > 0 && !wait(&q_free, (phase - 1) & 1, W_Q_FREE)) return false;
-        // queries: D/16 lanes per row, 16 channels each
-        constexpr int LPR = D / 16;
-        constexpr int kPass = kTcConv / LPR, kRows = kTileM / kPass;  // rows per pass and tile
-        const int c = ct % LPR;
-#pragma unroll 1
-        for (int mt2 = 0; mt2 < MT; ++mt2) {
-          uint4 x4[kRows][2];  // (every load of a tile first)
-#pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            const int r = mt2 * kTileM + i * kPass + ct / LPR;
-            x4[i][0] = x4[i][1] = make_uint4(0, 0, 0, 0);
-            if (r < R) {
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c * 16);
-              x4[i][0] = src[0];
-              x4[i][1] = src[1];
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            const int rr = i * kPass + ct / LPR;
-            uint32_t x[8] = {x4[i][0].x, x4[i][0].y, x4[i][0].z, x4[i][0].w,
-                             x4[i][1].x, x4[i][1].y, x4[i][1].z, x4[i][1].w};
-            if (!blk) {  // fp16 scaled per row by a power of two (see kv4_attn.cu)
-              float mx = 0.f;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mx = fmaxf(mx, fmaxf(fabsf(bf16lo(x[k])), fabsf(bf16hi(x[k]))));
-#pragma unroll
-              for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              float up, f;
-              kv4_query_scale(mx, a.scale * a.c.k_scale, &up, &f);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) x[k] = pack_half2(bf16lo(x[k]) * up, bf16hi(x[k]) * up);
-              if (c == 0) row_f[mt2 * kTileM + rr] = f;
-            }
-            const uint32_t dst = qs + uint32_t(mt2) * kTile + uint32_t(c >> 2) * 16384u;
-            const uint32_t c8 = uint32_t(c & 3) * 2u;
-            sts128(dst + sw128_off(uint32_t(rr), c8), x[0], x[1], x[2], x[3]);
-            sts128(dst + sw128_off(uint32_t(rr), c8 + 1), x[4], x[5], x[6], x[7]);
-          }
-        }
-        publish(&q_full);
-        ++phase;
         for (; u < pe; ++u, ++tile) {
           const uint32_t item = 2 * tile + uint32_t(kv), b = item % kTcBufs;
           const uint32_t dst = bs + b * kTile;
