@@ -270,12 +270,11 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
         constexpr int LPR = D / 16;
         constexpr int kPass = kTcSoft / LPR, kRows = kTileM / kPass;  // rows per pass and tile
         const int c = int(threadIdx.x) % LPR;
-#pragma unroll 1
-        for (int mt2 = 0; mt2 < MT; ++mt2) {
-          uint4 x4[kRows][2];  // (every load of a tile first)
+        uint4 x4[MT * kRows][2];  // (every load first)
+        {
 #pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            const int r = mt2 * kTileM + i * kPass + int(threadIdx.x) / LPR;
+          for (int i = 0; i < MT * kRows; ++i) {
+            const int r = i * kPass + int(threadIdx.x) / LPR;
             x4[i][0] = x4[i][1] = make_uint4(0, 0, 0, 0);
             if (r < R) {
               const uint4* src = reinterpret_cast<const uint4*>(
@@ -285,8 +284,8 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
             }
           }
 #pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            const int rr = i * kPass + int(threadIdx.x) / LPR;
+          for (int i = 0; i < MT * kRows; ++i) {
+            const int mt2 = i / kRows, rr = i % kRows * kPass + int(threadIdx.x) / LPR;
             uint32_t x[8] = {x4[i][0].x, x4[i][0].y, x4[i][0].z, x4[i][0].w,
                              x4[i][1].x, x4[i][1].y, x4[i][1].z, x4[i][1].w};
             if (!blk) {  // fp16 scaled per row by a power of two (see kv4_attn.cu)
