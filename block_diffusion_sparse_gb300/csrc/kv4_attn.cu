@@ -3,10 +3,12 @@
 // token, a short draft): bound by the cache's bytes and by the instructions that
 // turn codes into numbers.
 //
-// A CTA walks its share of the keys (kv4_split) in tiles of 128.  Its ninth warp
+// A CTA walks its share of the keys (kv4_split) in tiles of 128.  Its last warp
 // copies each tile's codes and scales from the pages into a ring of stages (bulk
-// copies, the tile's pages in parallel lanes); each of the other eight takes 16
-// of the tile's keys.  With rows = the group's query rows,
+// copies, the tile's pages in parallel lanes); each of the first eight takes 16
+// of the tile's keys, and the ninth the block's own keys, beside them (with one
+// of the eight doing that first, a ragged batch of single tokens took 114 us
+// instead of 91: the ring waited for it).  With rows = the group's query rows,
 //   S^T [16 keys x 8 rows] = K [16 x d] Q^T [d x 8]        (mma m16n8k16)
 //   O^T [d x 8 rows]      += V^T [d x 16 keys] P^T [16 x 8] (mma m16n8k16)
 // The keys are the M side of both products, so eight query rows fill an
@@ -39,8 +41,9 @@
 
 namespace herald {
 
-constexpr int kKv4Warps = 8;
-constexpr int kKv4Threads = (kKv4Warps + 1) * 32;
+constexpr int kKv4Warps = 8;        // warps of cache keys
+constexpr int kKv4Parts = kKv4Warps + 1;  // and one of the block's keys
+constexpr int kKv4Threads = (kKv4Parts + 1) * 32;
 constexpr int kKv4Unit = 16;        // keys per warp and tile
 constexpr int kKv4MmaRows = 16;     // most rows per KV head of this kernel
 constexpr float kKv4Below = 11.f, kKv4Above = 15.f;  // exponent base, log2 units
@@ -70,7 +73,7 @@ HERALD_DEV uint32_t bcast16(uint32_t x, int half) {
 }
 
 HERALD_DEV void product_bar() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kKv4Warps * 32) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kKv4Parts * 32) : "memory");
 }
 
 // Waits of the kernel (bits 16-31 of the error word).
@@ -84,7 +87,7 @@ struct RowsSmem {
   static constexpr int kCodes = kKv4Tile * D / 2, kScales = kKv4Tile * D / 16;
   static constexpr int kStage = 2 * (kCodes + kScales);
   static constexpr int kRed = kStages * kStage;
-  static constexpr int kTotal = kRed + kKv4Warps * 8 * NT * (D + 4) * 4;
+  static constexpr int kTotal = kRed + kKv4Parts * 8 * NT * (D + 4) * 4;
 };
 
 // at most 8*NT query rows per KV head
@@ -99,8 +102,8 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
   __shared__ uint64_t full[S::kStages], empty[S::kStages];
   __shared__ uint32_t failed;
   __shared__ uint8_t counts[S::kStages][kKv4Warps];  // keys of each 16 that count
-  __shared__ float red_m[kKv4Warps][RT], red_l[kKv4Warps][RT];
-  float* red = reinterpret_cast<float*>(smem + S::kRed);  // [warps][RT][D + 4]
+  __shared__ float red_m[kKv4Parts][RT], red_l[kKv4Parts][RT];
+  float* red = reinterpret_cast<float*>(smem + S::kRed);  // [parts][RT][D + 4]
   const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
   const int lg = lane >> 2, lt = lane & 3;
   if (threadIdx.x == 0) {
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
     }
   };
 
-  if (warp == kKv4Warps) {
+  if (warp == kKv4Parts) {
     // ------------------------------------------------------------ copies
     const int sub = min(1 << a.c.page_log2, kKv4Tile);  // keys of a tile in one page
     const int k0 = lane * sub;                          // lane i: sub-chunk i of the tile
@@ -282,36 +285,47 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
           }
       };
 
-      // ---------------- the block's own keys, in bf16 (at most 16), one warp
+      // ---------------- the block's own keys, in bf16 (at most 16): the ninth warp
       // (P in units of v_scale so that O has one unit for all keys)
-      if (a.bk && u0 == 0 && warp == 0) {
+      if (a.bk && u0 == 0 && warp == kKv4Warps) {
         float s[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-        const uint16_t* kp[2];
+        // every load first: the lane's runs of its two keys, its four values
+        uint32_t kw[2][KS][2], vw[4][KS];
+        auto run = [&](const uint16_t* base, int j, int off, uint32_t* to, int chunks) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int j = key_s + 8 * i;
-          kp[i] = j < a.B ? a.bk + ((size_t(n) * a.B + j) * a.Hkv + g) * D + lt * (D / 4) : nullptr;
-        }
-#pragma unroll 2
-        for (int k = 0; k < KS; ++k) {
-          uint2 w[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            w[i] = kp[i] ? *reinterpret_cast<const uint2*>(kp[i] + k * 4) : make_uint2(0, 0);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 8 + lg;
-            uint2 b = make_uint2(0, 0);
-            if (r < R)
-              b = *reinterpret_cast<const uint2*>(
-                  a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + lt * (D / 4) +
-                  k * 4);
-            mma_bf16(s[nt], w[0].x, w[1].x, w[0].y, w[1].y, b.x, b.y);
+          for (int i = 0; i < 4; ++i) {
+            if (i >= chunks) break;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (j < a.B)
+              w = *reinterpret_cast<const uint4*>(base + ((size_t(n) * a.B + j) * a.Hkv + g) * D +
+                                                  off + i * 8);
+            to[4 * i] = w.x, to[4 * i + 1] = w.y, to[4 * i + 2] = w.z, to[4 * i + 3] = w.w;
           }
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) run(a.bk, key_s + 8 * i, lt * (D / 4), &kw[i][0][0], D / 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) run(a.bv, key_v(i), lg * (D / 8), vw[i], D / 64);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = nt * 8 + lg;
+          const uint16_t* qp =
+              a.q + ((size_t(n) * a.B + (r < R ? r / G : 0)) * a.Hq + g * G + (r < R ? r % G : 0)) * D +
+              lt * (D / 4);
+          uint32_t qb[KS][2];
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < R) w = *reinterpret_cast<const uint4*>(qp + k * 4);
+            qb[k][0] = w.x, qb[k][1] = w.y, qb[k + 1][0] = w.z, qb[k + 1][1] = w.w;
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            mma_bf16(s[nt], kw[0][k][0], kw[1][k][0], kw[0][k][1], kw[1][k][1], qb[k][0], qb[k][1]);
         }
         float f[NT][2];
 #pragma unroll
@@ -329,30 +343,20 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
           p0[nt] = transpose8x8(pack_bf16(s[nt][0] * iv, s[nt][1] * iv));
           p1[nt] = transpose8x8(pack_bf16(s[nt][2] * iv, s[nt][3] * iv));
         }
-        const uint16_t* vp[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = key_v(i);
-          vp[i] = j < a.B ? a.bv + ((size_t(n) * a.B + j) * a.Hkv + g) * D + lg * (D / 8) : nullptr;
-        }
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {  // channels lg*D/8 + 2k, + 2k+1 of each key
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = vp[i] ? *reinterpret_cast<const uint32_t*>(vp[i] + 2 * k) : 0u;
+        for (int k = 0; k < KS; ++k)  // channels lg*D/8 + 2k, + 2k+1 of each key
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma_bf16(o[nt][k], __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
-                     __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632), p0[nt],
-                     p1[nt]);
-        }
+            mma_bf16(o[nt][k], __byte_perm(vw[0][k], vw[1][k], 0x5410),
+                     __byte_perm(vw[0][k], vw[1][k], 0x7632),
+                     __byte_perm(vw[2][k], vw[3][k], 0x5410),
+                     __byte_perm(vw[2][k], vw[3][k], 0x7632), p0[nt], p1[nt]);
       }
 
       // ------------------------------------------------------ cache tiles
       const int tiles = min(u1, (ctx + kKv4Tile - 1) / kKv4Tile);
 #pragma unroll 1
-      for (int u = u0; u < tiles; ++u, ++t) {
+      for (int u = u0; u < tiles && warp < kKv4Warps; ++u, ++t) {
         const uint32_t st = t % S::kStages, sm = base + st * uint32_t(S::kStage);
         wait(&full[st], (t / S::kStages) & 1, W_STAGE_FULL);
         const int valid = warp_same(int(*(volatile uint8_t*)&counts[st][warp]));
@@ -478,17 +482,17 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
       product_bar();
       const bool whole = u0 == 0 && u1 == units;  // no other piece of this segment
       const int slot = int(blockIdx.x) + seg;
-      for (int i = threadIdx.x; i < RT * (D / 4); i += kKv4Warps * 32) {
+      for (int i = threadIdx.x; i < RT * (D / 4); i += kKv4Parts * 32) {
         // (neighbouring threads write neighbouring channels of out, rows of a partial)
         const int r = whole ? i / (D / 4) : i % RT, c4 = whole ? i % (D / 4) : i / RT;
         if (r >= R) continue;
         float M = -FLT_MAX;
 #pragma unroll
-        for (int w = 0; w < kKv4Warps; ++w) M = fmaxf(M, red_m[w][r]);
+        for (int w = 0; w < kKv4Parts; ++w) M = fmaxf(M, red_m[w][r]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kKv4Warps; ++w) {
+        for (int w = 0; w < kKv4Parts; ++w) {
           const float f = fast_exp2(red_m[w][r] - M);
           const float4 x =
               *reinterpret_cast<const float4*>(red + (w * RT + r) * (D + 4) + c4 * 4);
