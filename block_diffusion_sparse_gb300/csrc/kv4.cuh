@@ -85,6 +85,7 @@ struct Kv4AttnArgs {
   float2* ml;    // [slots][R16]
   float scale;
   int N, Hq, Hkv, B, L_max, R16, ctas;
+  int pad;       // what a piece costs beside its tiles, in tiles (kv4_units)
   Kv4Dev c;
 };
 constexpr int kKv4Tile = 128;  // keys per tile of the attention kernels
@@ -159,7 +160,9 @@ struct Kv4Wait {
 // are laid end to end, segments in order, and the block's own keys with them:
 // blk_units tiles of their own per segment, or (blk_units = kKv4BlkJoined) as
 // part of the segment's first tile, which then exists without cache keys too.
-// CTA c takes tiles [c*share, (c+1)*share).  Equal shares keep ragged batches
+// Every segment with keys also has `pad` units in front of its tiles that stand
+// for the cost of starting on it (queries, the first copies, the piece's end).
+// CTA c takes units [c*share, (c+1)*share).  Equal shares keep ragged batches
 // balanced; a CTA's range may cover the end of one segment, whole segments, and
 // the start of another (its pieces).  Piece (c, segment s) has partial slot c +
 // s: from one piece to the next c or s grows.  All counts fit 31 bits
@@ -167,19 +170,21 @@ struct Kv4Wait {
 // tells the compiler that what follows from them is the same for the whole warp.
 constexpr int kKv4BlkJoined = -1;
 struct Kv4Split {
-  int total;  // tiles of all segments
-  int share;  // tiles per CTA
+  int total;  // units of all segments
+  int share;  // units per CTA
 };
 HERALD_DEV int warp_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-HERALD_DEV int kv4_units(int ctx, int L_max, int blk_units) {
-  const int t = (min(max(ctx, 0), L_max) + kKv4Tile - 1) / kKv4Tile;
-  return blk_units == kKv4BlkJoined ? max(t, 1) : t + blk_units;
+HERALD_DEV int kv4_units(int ctx, int L_max, int blk_units, int pad) {
+  int t = (min(max(ctx, 0), L_max) + kKv4Tile - 1) / kKv4Tile;
+  t = blk_units == kKv4BlkJoined ? max(t, 1) : t + blk_units;
+  return t > 0 ? t + pad : 0;
 }
-// Sum over the first N sequences of their tiles (per KV head); called by a
+// Sum over the first N sequences of their units (per KV head); called by a
 // whole warp.
-HERALD_DEV int kv4_total_units(const int32_t* ctx, int N, int L_max, int blk_units) {
+HERALD_DEV int kv4_total_units(const int32_t* ctx, int N, int L_max, int blk_units, int pad) {
   int sum = 0;
-  for (int n = int(threadIdx.x & 31); n < N; n += 32) sum += kv4_units(ctx[n], L_max, blk_units);
+  for (int n = int(threadIdx.x & 31); n < N; n += 32)
+    sum += kv4_units(ctx[n], L_max, blk_units, pad);
   return warp_same(__reduce_add_sync(0xffffffffu, sum));
 }
 HERALD_DEV Kv4Split kv4_split(int per_head, int Hkv, int ctas) {
@@ -188,20 +193,21 @@ HERALD_DEV Kv4Split kv4_split(int per_head, int Hkv, int ctas) {
   s.share = max((s.total + ctas - 1) / ctas, 1);
   return s;
 }
-// A CTA's share: tiles [at, end); with at < end, n is the sequence that holds
-// tile `at` and first the first tile of that sequence's first segment.  Called
+// A CTA's share: units [at, end); with at < end, n is the sequence that holds
+// unit `at` and first the first unit of that sequence's first segment.  Called
 // by a whole warp.
 struct Kv4Share {
   int at, end, n, first;
 };
-HERALD_DEV Kv4Share kv4_share(const int32_t* ctx, int N, int L_max, int blk_units, int Hkv,
-                              int ctas, int cta) {
+HERALD_DEV Kv4Share kv4_share(const Kv4AttnArgs& a, int blk_units, int cta) {
+  const int32_t* ctx = a.ctx;
+  const int N = a.N, L_max = a.L_max, Hkv = a.Hkv, pad = a.pad;
   const int lane = threadIdx.x & 31;
   // (the lengths of the first 32 sequences are loaded once)
-  const int own0 = lane < N ? kv4_units(ctx[lane], L_max, blk_units) : 0;
+  const int own0 = lane < N ? kv4_units(ctx[lane], L_max, blk_units, pad) : 0;
   int sum = own0;
-  for (int n = lane + 32; n < N; n += 32) sum += kv4_units(ctx[n], L_max, blk_units);
-  const Kv4Split split = kv4_split(int(__reduce_add_sync(0xffffffffu, sum)), Hkv, ctas);
+  for (int n = lane + 32; n < N; n += 32) sum += kv4_units(ctx[n], L_max, blk_units, pad);
+  const Kv4Split split = kv4_split(int(__reduce_add_sync(0xffffffffu, sum)), Hkv, a.ctas);
   Kv4Share r;
   r.at = warp_same(cta * split.share);
   r.end = warp_same(min(r.at + split.share, split.total));
@@ -210,7 +216,7 @@ HERALD_DEV Kv4Share kv4_share(const int32_t* ctx, int N, int L_max, int blk_unit
   int base = 0;
   for (int n0 = 0; n0 < N; n0 += 32) {
     const int n = n0 + lane;
-    const int own = Hkv * (n0 == 0 ? own0 : n < N ? kv4_units(ctx[n], L_max, blk_units) : 0);
+    const int own = Hkv * (n0 == 0 ? own0 : n < N ? kv4_units(ctx[n], L_max, blk_units, pad) : 0);
     int inc = own;  // inclusive scan
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

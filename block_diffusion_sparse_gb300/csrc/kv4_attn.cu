@@ -46,6 +46,11 @@ constexpr int kKv4Parts = kKv4Warps + 1;  // and one of the block's keys
 constexpr int kKv4Threads = (kKv4Parts + 1) * 32;
 constexpr int kKv4Unit = 16;        // keys per warp and tile
 constexpr int kKv4MmaRows = 16;     // most rows per KV head of this kernel
+// What a piece costs beside its tiles, in tiles (kv4_units).  Ragged batch of 64
+// single tokens: 98 us without, 94 / 86 / 83 / 84 with 1 / 2 / 3 / 4; tensor-core
+// kernel, 32 tokens at 32K: 37 us without, 30 with 2, 4 or 6; drafts of 5: 26, 25,
+// 23.6, 23.6; 32 tokens at 4 x 64K: 150, 149, 147, 146.
+constexpr int kKv4PadRows = 3, kKv4PadTc = 6;
 constexpr float kKv4Below = 11.f, kKv4Above = 15.f;  // exponent base, log2 units
 
 HERALD_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -116,8 +121,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
   const Kv4Wait wait{&failed};
   const int G = a.Hq / a.Hkv, R = a.B * G;
   const int blk_units = a.bk ? kKv4BlkJoined : 0;
-  const Kv4Share sh =
-      kv4_share(a.ctx, a.N, a.L_max, blk_units, a.Hkv, a.ctas, int(blockIdx.x));
+  const Kv4Share sh = kv4_share(a, blk_units, int(blockIdx.x));
   const int end = sh.end;
   if (sh.at >= end) return;
 
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
     int at = sh.at, first = sh.first, n = sh.n;
     while (at < end) {
       const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
-      const int units = kv4_units(ctx, a.L_max, blk_units);
+      const int units = kv4_units(ctx, a.L_max, blk_units, a.pad);
       if (units == 0 || at >= first + a.Hkv * units) {  // the next sequence
         first += a.Hkv * units;
         ++n;
@@ -135,9 +139,9 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
       }
       const int g = (at - first) / units;
       const int seg0 = first + g * units;
-      const int u0 = at - seg0, u1 = min(units, end - seg0);
-      body(n, g, n * a.Hkv + g, ctx, units, u0, u1);
-      at = seg0 + u1;
+      const int u0 = max(at - seg0 - a.pad, 0), u1 = min(units, end - seg0) - a.pad;
+      if (u1 > 0) body(n, g, n * a.Hkv + g, ctx, units - a.pad, u0, u1);
+      at = seg0 + a.pad + u1;
     }
   };
 
@@ -536,10 +540,10 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
   const int grp = threadIdx.x / TPG, item = threadIdx.x % TPG;
   const int rr = item % kKv4JoinRows, c4 = item / kKv4JoinRows;
   const int r = int(blockIdx.y) * kKv4JoinRows + rr, rc = min(r, R - 1);
-  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, blk_units), a.Hkv, a.ctas);
-  const int units = kv4_units(a.ctx[n], a.L_max, blk_units);
+  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, blk_units, a.pad), a.Hkv, a.ctas);
+  const int units = kv4_units(a.ctx[n], a.L_max, blk_units, a.pad);
   const int first =
-      a.Hkv * kv4_total_units(a.ctx, n, a.L_max, blk_units) + g * units;
+      a.Hkv * kv4_total_units(a.ctx, n, a.L_max, blk_units, a.pad) + g * units;
   // The lengths were read before the grid-dependency wait: they were written
   // before the attention kernel's own wait ended, and it lets this kernel start
   // only after that.
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
     if (grp == 0 && r < R) *out = make_uint2(0, 0);
     return;
   }
-  int c0 = first / split.share, c1 = (first + units - 1) / split.share;
+  int c0 = (first + a.pad) / split.share, c1 = (first + units - 1) / split.share;
   if (c0 == c1 && subs == 1) return;  // one piece: written by the attention kernel
   c0 = (c0 + seg) * subs, c1 = (c1 + seg) * subs + subs - 1;  // its partials
   const float4* op = reinterpret_cast<const float4*>(a.opart) + size_t(c4) * a.R16 + rc;
@@ -641,6 +645,7 @@ cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4D
   const bool tc = R > kKv4MmaRows;
   uint32_t* err = reinterpret_cast<uint32_t*>(p);
   a.ctas = std::min(kKv4MaxCtas, (!tc && R <= 8 ? 2 : 1) * num_sms);
+  a.pad = tc ? kKv4PadTc : kKv4PadRows;
   if (tc)
     HERALD_CHECK_LAUNCH(launch_kv4_attn_tc(dm.d, R, a, err, st));
   else if (dm.d == 128)

@@ -210,8 +210,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
 
   const int G = a.Hq / a.Hkv, R = a.B * G;
   const int blk_units = a.bk ? (a.B + kTcKeys - 1) / kTcKeys : 0;
-  const Kv4Share sh =
-      kv4_share(a.ctx, a.N, a.L_max, blk_units, a.Hkv, a.ctas, int(blockIdx.x));
+  const Kv4Share sh = kv4_share(a, blk_units, int(blockIdx.x));
   const int end = sh.end;
 
   // Every role walks the same pieces: body(n, g, seg, ctx, units, u0, u1) with
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
     int at = sh.at, first = sh.first, n = sh.n;
     while (at < end) {
       const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
-      const int units = kv4_units(ctx, a.L_max, blk_units);
+      const int units = kv4_units(ctx, a.L_max, blk_units, a.pad);
       if (units == 0 || at >= first + a.Hkv * units) {
         first += a.Hkv * units;
         ++n;
@@ -229,9 +228,9 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
       }
       const int g = (at - first) / units;
       const int seg0 = first + g * units;
-      const int u0 = at - seg0, u1 = min(units, end - seg0);
-      if (!body(n, g, n * a.Hkv + g, ctx, units, u0, u1)) return;
-      at = seg0 + u1;
+      const int u0 = max(at - seg0 - a.pad, 0), u1 = min(units, end - seg0) - a.pad;
+      if (u1 > 0 && !body(n, g, n * a.Hkv + g, ctx, units - a.pad, u0, u1)) return;
+      at = seg0 + a.pad + u1;
     }
   };
   // keys of tile u that can count
