@@ -31,54 +31,70 @@ HERALD_DEV uint32_t float2_to_e2m1(float lo, float hi) {
   return r;
 }
 
-// One group of 16 channels to codes and scale.  Each step is one IEEE fp32
-// operation, so the result is defined to the bit: scale = e4m3(max|x| /
-// (6 scale0)), code = e2m1(x / (scale scale0)); c6 = 6 scale0.  A quotient
-// rounds to a midpoint of two codes only when it is one (scale and midpoints
-// have few bits), so the division's rounding never moves a code.
-HERALD_DEV void quantise16(const float (&x)[16], float scale0, float c6, uint2* codes,
-                           uint32_t* scale) {
-  float a = fabsf(x[0]);
-#pragma unroll
-  for (int i = 1; i < 16; ++i) a = max_nan(a, fabsf(x[i]));
+// Eight channels of a group of 16 to codes and scale, the other eight in the
+// neighbouring lane (a: the max of both).  Each step is one IEEE fp32 operation,
+// so the result is defined to the bit: scale = e4m3(max|x| / (6 scale0)), code =
+// e2m1(x / S) with S = scale scale0; c6 = 6 scale0.  The quotients are taken
+// without dividing: with inv = 1/S rounded, q = x inv is off by an ulp or two,
+// x - q S is exact in one fma, and q + (x - q S) inv is then the rounded
+// quotient (P. Markstein, IBM J. Res. Dev. 34, 1990).  (The remainder's sign is
+// turned so that a negative zero stays one.)  scale0 lies
+// in [2^-60, 2^60], so S and 1/S are normal; a group past the largest scale, whose
+// quotients may not be, divides.  (Dividing throughout made the prompts' append 7 us
+// longer.)
+HERALD_DEV void quantise8(const float (&x)[8], float a, float scale0, float c6, uint32_t* codes,
+                          uint32_t* scale) {
   *scale = float_to_e4m3(__fdiv_rn(a, c6));
   const float S = __fmul_rn(e4m3_to_float(*scale), scale0);
-  uint32_t w[2] = {0, 0};
-  if (S > 0.f) {  // (a zero or NaN scale: codes 0)
+  uint32_t w = 0;
+  if (a < 16.f * S) {
+    const float inv = __frcp_rn(S);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= float2_to_e2m1(__fdiv_rn(x[2 * i], S), __fdiv_rn(x[2 * i + 1], S))
-                   << (8 * (i & 3));
+    for (int i = 0; i < 4; ++i) {
+      float q[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float q0 = __fmul_rn(x[2 * i + j], inv);
+        q[j] = __fmaf_rn(__fmaf_rn(q0, S, -x[2 * i + j]), -inv, q0);
+      }
+      w |= float2_to_e2m1(q[0], q[1]) << (8 * i);
+    }
+  } else if (S > 0.f) {  // (a zero or NaN scale: codes 0)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w |= float2_to_e2m1(__fdiv_rn(x[2 * i], S), __fdiv_rn(x[2 * i + 1], S)) << (8 * i);
   }
-  *codes = make_uint2(w[0], w[1]);
+  *codes = w;
 }
 
 constexpr int kKv4MoveThreads = 256;
 
-// A row of D channels is handled by D/16 neighbouring lanes, one group of 16
-// channels each.  An item is one token and `per` consecutive heads of it
-// (query heads, then key heads, then value heads), so a lane keeps its
-// angles in registers for all of them; items run over the tokens of one
-// sequence (blockIdx.y).
+// A row of D channels is handled by D/8 neighbouring lanes, eight channels (16
+// bytes) each; an item is one token and Per consecutive heads of its queries, keys
+// or values (a chunk).  A CTA holds `toks` = 2^tok_log2 tokens by kRows / toks
+// chunks; grid (tokens, sequences, chunks).  Bound by memory for prompts (ragged
+// 4 x 4096 tokens of 32 + 2 x 8 heads: 39 us, 83% of the copy rate) and by latency
+// below some hundred tokens.  What counts is that an item loads its heads before it
+// works on any, that queries, keys and values do not share warps (one loop over all
+// three kinds: 64 us) and that no lane divides for its place.
 struct Kv4AppendArgs {
   const uint16_t *q, *k, *v;
   int64_t q_ld, k_ld, v_ld;
   const int32_t *n_tok, *ctx;
   const float* cos_sin;  // [n_pos][rot/2][2]
-  int rot, interleaved;
+  int rot;
   uint16_t *q_rot, *k_rot;
-  int Hq, Hkv, T, L_max, heads, per, chunks;
-  int has_cache;
+  int Hq, Hkv, T, L_max, q_chunks, k_chunks, chunks, tok_log2;
   Kv4Dev c;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kKv4MoveThreads)
+template <int D, bool Interleaved, int Per>
+__global__ void __launch_bounds__(kKv4MoveThreads, 3)
     kv4_append_kernel(const Kv4AppendArgs a) {
-  constexpr int LPR = D / 16;
+  constexpr int LPR = D / 8;
   griddep_enter();
-  const int n = blockIdx.y, lane = threadIdx.x & 31;
-  const int c = lane % LPR;  // this lane's group of 16 channels
+  const int n = blockIdx.y, lane = threadIdx.x & 31, row = threadIdx.x / LPR;
+  const int c = lane % LPR;  // this lane's eight channels
   const int ctx_raw = a.ctx[n];
   debug_flag(threadIdx.x == 0 && (ctx_raw < 0 || ctx_raw > a.L_max), DEV_BAD_COUNT);
   const int L0 = min(max(ctx_raw, 0), a.L_max);
@@ -89,111 +105,111 @@ __global__ void __launch_bounds__(kKv4MoveThreads)
     toks = min(max(raw, 0), a.T);
   }
   toks = min(toks, a.L_max - L0);  // tokens at or past L_max are ignored
-  const int64_t item = (int64_t(blockIdx.x) * kKv4MoveThreads + threadIdx.x) / LPR;
-  const int t = int(item / a.chunks), chunk = int(item - int64_t(t) * a.chunks);
-  const bool live = t < toks;
-  // (a warp whose items are all past the tokens leaves together; the others
-  // keep every lane for the exchanges below)
+  const int t = (int(blockIdx.x) << a.tok_log2) + (row & ((1 << a.tok_log2) - 1));
+  int chunk = int(blockIdx.z) * ((kKv4MoveThreads / LPR) >> a.tok_log2) + (row >> a.tok_log2);
+  const bool live = t < toks && chunk < a.chunks;
+  // (a warp without an item leaves whole; the others keep every lane for the
+  // exchanges below)
   if (!__any_sync(0xffffffffu, live)) return;
   const int pos = live ? L0 + t : 0;
-  const int h0 = chunk * a.per, h1 = min(h0 + a.per, a.heads);
+  const bool is_q = chunk < a.q_chunks;
+  if (!is_q) chunk -= a.q_chunks;
+  const bool is_k = !is_q && chunk < a.k_chunks;
+  if (!is_q && !is_k) chunk -= a.k_chunks;
+  const int H = is_q ? a.Hq : a.Hkv, h0 = chunk * Per;
+  const int64_t tok = int64_t(n) * a.T + t;
 
-  // angles: in the half-split form channel i < rot/2 pairs with i + rot/2
-  // (the same group of the lane rot/32 groups on), else 2i pairs with 2i+1
-  const bool turns = c * 16 < a.rot;
-  const int RG2 = a.rot / 32;  // groups per half
-  const bool first = c < RG2;
-  const int partner = (lane - c) + (a.interleaved || !turns ? c : first ? c + RG2 : c - RG2);
-  float cs[16], sn[16];
+  uint4 u[Per];  // every load of the item first
+  {
+    const uint16_t* src = (is_q ? a.q + tok * a.q_ld : is_k ? a.k + tok * a.k_ld
+                                                            : a.v + tok * a.v_ld) +
+                          h0 * D + c * 8;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < Per; ++i)
+      u[i] = live && h0 + i < H ? *reinterpret_cast<const uint4*>(src + i * D)
+                                : make_uint4(0, 0, 0, 0);
+  }
+  // angles: in the half-split form channel i < rot/2 pairs with i + rot/2
+  // (the same channels of the lane rot/16 lanes on), else 2i pairs with 2i+1
+  const bool turns = c * 8 < a.rot && (is_q || is_k);
+  const int half = a.rot / 16;  // lanes per half
+  const bool first = c < half;
+  const int partner = (lane - c) + (c * 8 >= a.rot ? c : first ? c + half : c - half);
+  constexpr int A = Interleaved ? 4 : 8;  // angles of a lane
+  float cs[A], sn[A];
+#pragma unroll
+  for (int i = 0; i < A; ++i) {
     cs[i] = 1.f;
     sn[i] = 0.f;
   }
-  if (turns && h0 < a.Hq + a.Hkv) {
-    const float* p = a.cos_sin + size_t(pos) * a.rot;
-    if (a.interleaved) {
+  if (turns) {
+    const float* p =
+        a.cos_sin + size_t(pos) * a.rot + (Interleaved || first ? c : c - half) * (2 * A);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float4 w = *reinterpret_cast<const float4*>(p + (c * 8 + i) * 2);
-        cs[i] = w.x, sn[i] = w.y, cs[i + 1] = w.z, sn[i + 1] = w.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float4 w =
-            *reinterpret_cast<const float4*>(p + ((first ? c : c - RG2) * 16 + i) * 2);
-        cs[i] = w.x, sn[i] = w.y, cs[i + 1] = w.z, sn[i + 1] = w.w;
-      }
+    for (int i = 0; i < A; i += 2) {
+      const float4 w = *reinterpret_cast<const float4*>(p + 2 * i);
+      cs[i] = w.x, sn[i] = w.y, cs[i + 1] = w.z, sn[i + 1] = w.w;
     }
   }
   int phys = -1;
-  if (a.has_cache && live && h1 > a.Hq) {
+  if (!is_q && a.c.kc && live) {
     phys = kv4_page(a.c, n, pos >> a.c.page_log2);
     debug_flag(phys < 0, DEV_BAD_INDEX);  // a token without a page
   }
-  const int64_t tok = int64_t(n) * a.T + t;
-  for (int h = h0; h < h0 + a.per; ++h) {
-    const bool on = live && h < h1;
-    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
-    const int hh = is_q ? h : is_k ? h - a.Hq : h - a.Hq - a.Hkv;
-    uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-    if (on) {
-      const uint16_t* src = (is_q ? a.q + tok * a.q_ld : is_k ? a.k + tok * a.k_ld
-                                                              : a.v + tok * a.v_ld) +
-                            hh * D + c * 16;
-      u0 = *reinterpret_cast<const uint4*>(src);
-      u1 = *reinterpret_cast<const uint4*>(src + 8);
-    }
-    const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-    float x[16];
+  uint16_t* rot = is_q ? a.q_rot : is_k ? a.k_rot : nullptr;
+  if (rot) rot += (tok * H + h0) * D + c * 8;
+  const float s0 = is_k ? a.c.k_scale : a.c.v_scale, c6 = __fmul_rn(6.f, s0);
+  const size_t held = kv4_row(a.c, max(phys, 0), a.Hkv, h0, pos);
+  uint8_t* codes = (is_k ? a.c.kc : a.c.vc) + held * (D / 2) + c * 4;
+  uint8_t* scales = (is_k ? a.c.ks : a.c.vs) + held * (D / 16) + c / 2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[2 * i] = bf16lo(w[i]);
-      x[2 * i + 1] = bf16hi(w[i]);
+  for (int i = 0; i < Per; ++i) {
+    const bool on = live && h0 + i < H;
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = bf16lo(w[j]);
+      x[2 * j + 1] = bf16hi(w[j]);
     }
     // products and sums rounded one by one, as the definition has them
-    if (a.interleaved) {
-      if (turns && (is_q || is_k)) {
+    if constexpr (Interleaved) {
+      if (turns) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float e = x[2 * i], o = x[2 * i + 1];
-          x[2 * i] = __fsub_rn(__fmul_rn(e, cs[i]), __fmul_rn(o, sn[i]));
-          x[2 * i + 1] = __fadd_rn(__fmul_rn(o, cs[i]), __fmul_rn(e, sn[i]));
+        for (int j = 0; j < 4; ++j) {
+          const float e = x[2 * j], o = x[2 * j + 1];
+          x[2 * j] = __fsub_rn(__fmul_rn(e, cs[j]), __fmul_rn(o, sn[j]));
+          x[2 * j + 1] = __fadd_rn(__fmul_rn(o, cs[j]), __fmul_rn(e, sn[j]));
         }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t pw = __shfl_sync(0xffffffffu, w[i], partner);
-        if (turns && (is_q || is_k)) {
-          const float p0 = __fmul_rn(bf16lo(pw), sn[2 * i]),
-                      p1 = __fmul_rn(bf16hi(pw), sn[2 * i + 1]);
-          const float y0 = __fmul_rn(x[2 * i], cs[2 * i]),
-                      y1 = __fmul_rn(x[2 * i + 1], cs[2 * i + 1]);
-          x[2 * i] = first ? __fsub_rn(y0, p0) : __fadd_rn(y0, p0);
-          x[2 * i + 1] = first ? __fsub_rn(y1, p1) : __fadd_rn(y1, p1);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t pw = __shfl_sync(0xffffffffu, w[j], partner);
+        if (turns) {
+          const float p0 = __fmul_rn(bf16lo(pw), sn[2 * j]),
+                      p1 = __fmul_rn(bf16hi(pw), sn[2 * j + 1]);
+          const float y0 = __fmul_rn(x[2 * j], cs[2 * j]),
+                      y1 = __fmul_rn(x[2 * j + 1], cs[2 * j + 1]);
+          x[2 * j] = first ? __fsub_rn(y0, p0) : __fadd_rn(y0, p0);
+          x[2 * j + 1] = first ? __fsub_rn(y1, p1) : __fadd_rn(y1, p1);
         }
       }
     }
-    if (!on) continue;
-    uint16_t* rot = is_q ? a.q_rot : is_k ? a.k_rot : nullptr;
-    if (rot) {
-      uint32_t o[8];
+    if (rot && on)
+      *reinterpret_cast<uint4*>(rot + i * D) =
+          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                     pack_bf16(x[6], x[7]));
+    if (__all_sync(0xffffffffu, is_q)) continue;
+    float top = fabsf(x[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-      uint4* dst = reinterpret_cast<uint4*>(rot + (tok * (is_q ? a.Hq : a.Hkv) + hh) * D + c * 16);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
-    if (!is_q && phys >= 0) {
-      const float s0 = is_k ? a.c.k_scale : a.c.v_scale;
-      uint2 codes;
-      uint32_t scale;
-      quantise16(x, s0, __fmul_rn(6.f, s0), &codes, &scale);
-      const size_t row = kv4_row(a.c, phys, a.Hkv, hh, pos);
-      *reinterpret_cast<uint2*>((is_k ? a.c.kc : a.c.vc) + row * (D / 2) + c * 8) = codes;
-      (is_k ? a.c.ks : a.c.vs)[row * LPR + c] = uint8_t(scale);
+    for (int j = 1; j < 8; ++j) top = max_nan(top, fabsf(x[j]));
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    if (on && phys >= 0) {
+      uint32_t w8, scale;
+      quantise8(x, top, s0, c6, &w8, &scale);
+      *reinterpret_cast<uint32_t*>(codes + (size_t(i) << a.c.page_log2) * (D / 2)) = w8;
+      if (!(c & 1)) scales[(size_t(i) << a.c.page_log2) * (D / 16)] = uint8_t(scale);
     }
   }
 }
@@ -316,26 +332,33 @@ cudaError_t launch_kv4_append(const herald_dims& dm, int T, const int32_t* n_tok
   a.q = q, a.k = k, a.v = v;
   a.q_ld = q_ld, a.k_ld = k_ld, a.v_ld = v_ld;
   a.n_tok = n_tok, a.ctx = ctx;
-  if (rope) a.cos_sin = rope->cos_sin, a.rot = rope->rot, a.interleaved = rope->interleaved;
+  if (rope) a.cos_sin = rope->cos_sin, a.rot = rope->rot;
   a.q_rot = q_rot, a.k_rot = k_rot;
-  a.Hq = q ? dm.Hq : 0, a.Hkv = dm.Hkv, a.T = T, a.L_max = dm.L_max;
-  a.heads = a.Hq + (k ? dm.Hkv : 0) + (cache ? dm.Hkv : 0);
-  if (!k) a.Hkv = 0;
-  a.has_cache = cache != nullptr;
+  a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.T = T, a.L_max = dm.L_max;
   if (cache) a.c = *cache;
-  // heads per item: 1 while the items of single heads do not fill the GPU
-  const int lpr = dm.d / 16;
-  const int64_t rows = int64_t(dm.N) * T * a.heads;
-  a.per = rows * lpr <= 152 * 2048 ? 1 : 6;
-  a.chunks = cdiv(a.heads, a.per);
-  const int64_t threads = int64_t(T) * a.chunks * lpr;
-  const dim3 grid(unsigned((threads + kKv4MoveThreads - 1) / kKv4MoveThreads), unsigned(dm.N));
-  if (dm.d == 128)
-    HERALD_CHECK_LAUNCH(launch_k("kv4_append_kernel", kv4_append_kernel<128>, grid,
-                                 dim3(kKv4MoveThreads), 0, st, a));
-  else
-    HERALD_CHECK_LAUNCH(launch_k("kv4_append_kernel", kv4_append_kernel<64>, grid,
-                                 dim3(kKv4MoveThreads), 0, st, a));
+  const int hq = q ? dm.Hq : 0, hk = k ? dm.Hkv : 0, hv = cache ? dm.Hkv : 0;
+  const int rpc = kKv4MoveThreads / (dm.d / 8);  // rows per CTA
+  const int64_t rows = int64_t(dm.N) * T * (hq + hk + hv);
+  // heads per item: 4 share a lane's angles and keep four loads in flight, 1 makes
+  // more warps of a small call.  Us with 1 and 4, 48 heads: 1 x 64 tokens 2.5 and
+  // 3.7, 256 tokens 3.8 and 4.1, 384 tokens 4.6 and 4.3, 1024 tokens 9.3 and 6.7
+  const int per = rows <= 152 * 6 * rpc ? 1 : 4;
+  a.q_chunks = cdiv(hq, per), a.k_chunks = cdiv(hk, per);
+  a.chunks = a.q_chunks + a.k_chunks + cdiv(hv, per);
+  while ((1 << a.tok_log2) < T && (2 << a.tok_log2) <= rpc) ++a.tok_log2;
+  const dim3 grid(unsigned(cdiv(T, 1 << a.tok_log2)), unsigned(dm.N),
+                  unsigned(cdiv(a.chunks, rpc >> a.tok_log2)));
+  auto pick = [&](auto d, auto il) {
+    return per == 1 ? kv4_append_kernel<d.value, il.value, 1>
+                    : kv4_append_kernel<d.value, il.value, 4>;
+  };
+  constexpr std::integral_constant<int, 128> d128{};
+  constexpr std::integral_constant<int, 64> d64{};
+  const bool il = rope && rope->interleaved;
+  auto* kernel = dm.d == 128 ? (il ? pick(d128, std::true_type{}) : pick(d128, std::false_type{}))
+                             : (il ? pick(d64, std::true_type{}) : pick(d64, std::false_type{}));
+  HERALD_CHECK_LAUNCH(
+      launch_k("kv4_append_kernel", kernel, grid, dim3(kKv4MoveThreads), 0, st, a));
   if (pooled) {
     const dim3 pg(unsigned(cdiv(T - 1, Bk) + 1), unsigned(dm.N * dm.Hkv));
     if (dm.d == 128)

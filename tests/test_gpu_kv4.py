@@ -366,6 +366,36 @@ def test_rotation_alone():
                 assert (bits(k_rot) == 0).all()
 
 
+@pytest.mark.parametrize("scale0", [1.0, 0.3, 2.0 ** -14, 7e17, 1e-18, 2.0 ** 60, 2.0 ** -60])
+@pytest.mark.parametrize("inter", [0, 1])
+def test_append_codes_to_the_bit(scale0, inter):
+    """Codes, their zeros' signs and scales over every magnitude, quotients at the
+    midpoints of two codes among them."""
+    H = _h()
+    rng = np.random.default_rng(17)
+    N, Hkv, d, page, T = 1, 2, 64, 64, 1024
+    c = make_cache(rng, N, Hkv, d, page, [T], k_scale=scale0, v_scale=scale0)
+    g = OnGpu(c)
+    unit = np.exp2(rng.integers(-12, 10, (2, N, T, Hkv, d // 16, 1)))
+    x = rng.standard_normal((2, N, T, Hkv, d // 16, 16)) * np.exp2(rng.integers(-3, 1, (16,)))
+    at_mids = rng.choice([0, -0.0, .25, .5, .75, 1.25, 1.75, 2.5, 3.5, 5, -.25, -1.25, -5, 6], x.shape)
+    x = np.where(np.arange(T)[:, None, None, None] % 2 == 0, at_mids, x) * unit
+    with np.errstate(over="ignore"):
+        x = np.clip(x * np.float64(np.float32(scale0)), -3e38, 3e38)
+    x[0, 0, 0] = np.where(rng.random(x[0, 0, 0].shape) < 0.5, -0.0, 0.0)
+    x[1, 0, 1, :, :, 5] = 3e38                   # past the largest scale
+    k, v = ref.bf16(x.astype(np.float32).reshape(2, N, T, Hkv, d))
+    cs = ref.angles(T, d)
+    dctx = torch.tensor([0], dtype=torch.int32, device="cuda")
+    H.herald_kv4_append(H.dims(N, Hkv, Hkv, d, 1, T), T, None, dev(k), dev(v), dctx, g.kv4, None, None,
+                        H.rope(dev(cs), d, inter))
+    torch.cuda.synchronize()
+    rk = ref.rotate32(ref.f64(k[0]), cs, np.arange(T), d, inter)
+    c.write(0, np.arange(T), rk, ref.f64(v[0]).astype(np.float32))
+    assert np.array_equal(g.scales.cpu().numpy(), c.scales)
+    assert np.array_equal(g.codes.cpu().numpy(), c.codes)
+
+
 def test_append_odd_values():
     """Infinities saturate, a NaN makes its group NaN, tiny groups become zeros,
     tokens without a page are dropped; neighbours stay as they were."""
