@@ -73,7 +73,8 @@ HERALD_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
 HERALD_DEV void kv4_query_scale(float mx, float sc, float* up, float* f) {
   const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -112), 127);
   *up = __uint_as_float(uint32_t(14 - e + 127) << 23);
-  *f = fminf(fmaxf(sc * 1.4426950408889634f * exp2f(float(e - 14)), FLT_MIN), FLT_MAX);
+  const float down = __uint_as_float(uint32_t(e - 14 + 127) << 23);
+  *f = fminf(fmaxf(sc * 1.4426950408889634f * down, FLT_MIN), FLT_MAX);
 }
 
 // ---- attention arguments shared by its kernels
@@ -90,7 +91,7 @@ struct Kv4AttnArgs {
 };
 constexpr int kKv4Tile = 128;  // keys per tile of the attention kernels
 // The tensor-core kernel (kv4_attn_tc.cu) for `rows` <= 256 query rows per KV
-// head; with rows <= 128 each piece has two partials (slots 2p and 2p+1).
+// head.
 cudaError_t launch_kv4_attn_tc(int d, int rows, const Kv4AttnArgs& a, uint32_t* err,
                                cudaStream_t st);
 

@@ -526,12 +526,11 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
 // rows' chunks of four channels per D/4 * 8 threads, and kKv4JoinThreads over
 // that many groups, each with every such-and-suchth partial, four in flight, so
 // that the pieces of a long context travel at once; the groups are added in
-// order.  subs: partials per piece (slots subs*p ...); with more than one,
-// single pieces are joined here too.
+// order.
 constexpr int kKv4JoinThreads = 1024, kKv4JoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(kKv4JoinThreads)
-    kv4_join_kernel(const Kv4AttnArgs a, int blk_units, int subs) {
+    kv4_join_kernel(const Kv4AttnArgs a, int blk_units) {
   constexpr int TPG = kKv4JoinRows * (D / 4), GR = kKv4JoinThreads / TPG;
   __shared__ float4 part[GR][TPG];
   __shared__ float part_m[GR][kKv4JoinRows], part_l[GR][kKv4JoinRows];
@@ -555,8 +554,8 @@ __global__ void __launch_bounds__(kKv4JoinThreads)
     return;
   }
   int c0 = (first + a.pad) / split.share, c1 = (first + units - 1) / split.share;
-  if (c0 == c1 && subs == 1) return;  // one piece: written by the attention kernel
-  c0 = (c0 + seg) * subs, c1 = (c1 + seg) * subs + subs - 1;  // its partials
+  if (c0 == c1) return;  // one piece: written by the attention kernel
+  c0 += seg, c1 += seg;  // its partials
   const float4* op = reinterpret_cast<const float4*>(a.opart) + size_t(c4) * a.R16 + rc;
   float M = -FLT_MAX, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -621,7 +620,7 @@ struct Kv4Ws {
 static Kv4Ws kv4_ws(const herald_dims& dm) {
   Kv4Ws w;
   w.R16 = cdiv(dm.B * (dm.Hq / dm.Hkv), 16) * 16;
-  const size_t slots = 2 * (size_t(kKv4MaxCtas) + size_t(dm.N) * dm.Hkv);
+  const size_t slots = size_t(kKv4MaxCtas) + size_t(dm.N) * dm.Hkv;
   w.ml = 256;
   w.opart = align_up(w.ml + slots * w.R16 * 8, 256);
   w.total = w.opart + slots * w.R16 * size_t(dm.d) * 4;
@@ -654,14 +653,13 @@ cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4D
   else
     HERALD_CHECK_LAUNCH((R <= 8 ? launch_rows<64, 1>(a, err, st) : launch_rows<64, 2>(a, err, st)));
   const int blk_units = !bk ? 0 : tc ? cdiv(dm.B, kKv4Tile) : kKv4BlkJoined;
-  const int subs = tc && R <= kTileM ? 2 : 1;
   const dim3 grid(unsigned(dm.N * dm.Hkv), unsigned(cdiv(R, kKv4JoinRows)));
   if (dm.d == 128)
     HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<128>, grid,
-                                 dim3(kKv4JoinThreads), 0, st, a, blk_units, subs));
+                                 dim3(kKv4JoinThreads), 0, st, a, blk_units));
   else
     HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<64>, grid,
-                                 dim3(kKv4JoinThreads), 0, st, a, blk_units, subs));
+                                 dim3(kKv4JoinThreads), 0, st, a, blk_units));
   return cudaGetLastError();
 }
 

@@ -18,14 +18,20 @@
 //                the queries
 // Two streams run side by side: with more than 128 rows a stream is a row tile
 // and takes every key tile, else both streams have the same rows and take
-// alternate key tiles (their partial outputs are joined like those of two
-// CTAs).  A stream goes in steps of 64 keys through two score buffers of 64
+// alternate key tiles (at a piece's end each adds both outputs for half of the
+// channels).  A stream goes in steps of 64 keys through two score buffers of 64
 // TMEM columns (P, fp16, overlays the scores), so the scores of a step are
 // there when the softmax of the step before is done; O takes 128 columns: the
 // two streams fill the 512.
 //
-// A row's exponent base moves only when its maximum stands more than 15 (log2)
-// above it, to 11 below the maximum (P stays in fp16's range, see kv4_attn.cu).
+// A step's scores are read once: with the base m of the row as it is, P =
+// 2^(s - m) stays in fp16 as long as the row's 64 of them sum to less than 60000.
+// Where a sum does not (and at a piece's first step), the scores are looked at for
+// their maximum, m is set 5 below it, O and l follow, and the step is done again:
+// 64 P of a new base sum to 2^11 at most, and the scores must rise by 5 to 11
+// (log2) before it happens again.  (Looking for the maximum in every step, as
+// kv4_attn.cu does: 4 x 64K 146 us instead of 139.  With the base 9 below: 149,
+// the CTAs whose keys rise late doing more steps twice than the others.)
 //
 // The block's own keys are bf16: their tiles come first in a segment, with
 // the queries staged as bf16 (an mma's operands have one type), then the
@@ -50,13 +56,13 @@ constexpr int kTcMasks = 16;
 constexpr int kTcSoft = 256, kTcConv = 256;  // softmax and conversion threads
 constexpr int kTcThreadsAll = 768;         // 8 + 8 + 8 warps (22, 23 only fill a warpgroup)
 constexpr int kTcSWarp = 16, kTcCopyWarp = 17, kTcPvWarp = 20;  // S 16, 18; copies 17, 19; P V 20, 21
-constexpr float kTcBelow = 11.f, kTcAbove = 15.f;
+constexpr float kTcBelow = 5.f, kTcTop = 60000.f;  // base of P and largest sum (see above)
 
 // Waits of the kernel (bits 16-31 of the error word).
 enum : uint32_t {
   W_RAW_FREE = 1, W_RAW_FULL = 2, W_BUF_FREE = 4, W_Q_FREE = 8, W_Q_FULL = 0x10, W_K_FULL = 0x20,
   W_P_FULL = 0x40, W_V_FULL = 0x80, W_PV_DONE = 0x100, W_S_FULL = 0x200, W_MASK = 0x400,
-  W_O_DONE = 0x800
+  W_O_DONE = 0x800, W_O_READ = 0x1000
 };
 
 struct TcSmem {
@@ -142,10 +148,9 @@ HERALD_DEV void exp32(uint32_t (&x)[32], uint64_t f2, uint64_t nm2, uint64_t* su
   }
   *sum = f2_add(sa, sb);
 }
-// 32 probabilities -> 16 packed columns at ts.  blk: bf16, times iv (P in units
-// of v_scale: O has one unit for all keys), else fp16.
-HERALD_DEV void store_p32(uint32_t ts, const uint32_t (&x)[32], bool blk, float iv) {
-  uint32_t pk[16];
+// 32 probabilities -> 16 packed columns.  blk: bf16, times iv (P in units of
+// v_scale: O has one unit for all keys), else fp16.
+HERALD_DEV void pack_p32(uint32_t* pk, const uint32_t (&x)[32], bool blk, float iv) {
   if (blk) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -155,13 +160,20 @@ HERALD_DEV void store_p32(uint32_t ts, const uint32_t (&x)[32], bool blk, float 
     for (int i = 0; i < 16; ++i)
       pk[i] = pack_half2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
   }
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(ts),
-      "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]),
-      "r"(pk[7]), "r"(pk[8]), "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]),
-      "r"(pk[14]), "r"(pk[15])
-      : "memory");
+}
+
+// Largest magnitude of 16 bf16 (a NaN does not count).
+HERALD_DEV uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+HERALD_DEV float absmax16(const uint4& a, const uint4& b) {
+  constexpr uint32_t k = 0x7FFF7FFFu;
+  const uint32_t m = max_bf16x2(
+      max_bf16x2(max_bf16x2(a.x & k, a.y & k), max_bf16x2(a.z & k, a.w & k)),
+      max_bf16x2(max_bf16x2(b.x & k, b.y & k), max_bf16x2(b.z & k, b.w & k)));
+  return fmaxf(bf16lo(m), bf16hi(m));
 }
 
 template <int D, int MT>
@@ -175,7 +187,8 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   __shared__ uint64_t raw_full[2][kRawK], raw_free[2][kRawK];  // [K or V][slot]
   __shared__ uint64_t buf_full[kTcBufs], buf_free[kTcBufs];
   __shared__ uint64_t q_full, q_free, s_full[2][2], p_full[2][2], pv_done[2][2], o_done[2];
-  __shared__ uint64_t all_done[4];
+  __shared__ uint64_t all_done[4], ml_full, o_read;
+  __shared__ float2 row_ml[2][kTileM];              // a piece's (m, l) of both streams
   __shared__ uint64_t mask_full[kTcMasks];
   __shared__ uint32_t tmem_base;
   __shared__ uint32_t failed;
@@ -193,6 +206,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
     for (int i = 0; i < kTcBufs; ++i) mbar_init(&buf_full[i], 4), mbar_init(&buf_free[i], MT);
     for (int i = 0; i < kTcMasks; ++i) mbar_init(&mask_full[i], 1);
     mbar_init(&q_full, 8);
+    mbar_init(&ml_full, 8), mbar_init(&o_read, 8);
     mbar_init(&q_free, 2 + kTcSoft);
     for (int i = 0; i < 2; ++i)
       mbar_init(&s_full[i][0], 1), mbar_init(&s_full[i][1], 1), mbar_init(&p_full[i][0], 128),
@@ -252,9 +266,10 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
     const uint32_t ts0 = tm + lanes + uint32_t(w) * 128u, to = ts0 + 256u;
     const float iv = 1.f / a.c.v_scale;
     uint32_t tile = 0, ns = 0, mt = 0, phase = 0;  // tiles of the CTA, steps of the stream, masks
-    uint32_t no = 0;                               // pieces with a step of this stream
+    uint32_t no = 0, np = 0;  // bit x: parity of the pieces with a step of stream x; pieces
     pieces([&](int n, int g, int seg, int ctx, int units, int u0, int u1) -> bool {
       debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
+      const uint32_t first_tile = tile;
       float m = -FLT_MAX, l = 0.f;
       bool any = false;  // this stream has had a step of the piece
       int u = u0;
@@ -282,20 +297,24 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               x4[i][1] = src[1];
             }
           }
+float mx[MT * kRows];  // (the rows' maxima side by side: their steps wait on one another)
+          if (!blk) {
+#pragma unroll
+            for (int i = 0; i < MT * kRows; ++i) mx[i] = absmax16(x4[i][0], x4[i][1]);
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+              for (int i = 0; i < MT * kRows; ++i)
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+          }
 #pragma unroll
           for (int i = 0; i < MT * kRows; ++i) {
             const int mt2 = i / kRows, rr = i % kRows * kPass + int(threadIdx.x) / LPR;
             uint32_t x[8] = {x4[i][0].x, x4[i][0].y, x4[i][0].z, x4[i][0].w,
                              x4[i][1].x, x4[i][1].y, x4[i][1].z, x4[i][1].w};
             if (!blk) {  // fp16 scaled per row by a power of two (see kv4_attn.cu)
-              float mx = 0.f;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mx = fmaxf(mx, fmaxf(fabsf(bf16lo(x[k])), fabsf(bf16hi(x[k]))));
-#pragma unroll
-              for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
               float up, f;
-              kv4_query_scale(mx, a.scale * a.c.k_scale, &up, &f);
+              kv4_query_scale(mx[i], a.scale * a.c.k_scale, &up, &f);
 #pragma unroll
               for (int k = 0; k < 8; ++k) x[k] = pack_half2(bf16lo(x[k]) * up, bf16hi(x[k]) * up);
               if (c == 0) row_f[mt2 * kTileM + rr] = f;
@@ -335,24 +354,39 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                 }
                 mask_scores(ts, msk, keys - k0);
               }
-              float mx = -INFINITY;
-#pragma unroll 1
-              for (int c = 0; c < 64; c += 32) {
-                uint32_t x[32];
-                tmem_ld32_nowait(ts + uint32_t(c), x);
-                tmem_wait_ld(x);
-                float m1 = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  mx = fmax3f(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                  m1 = fmax3f(m1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+              float p[32], s0, s1;
+              bool again = false;
+              while (true) {
+                bool high = true;
+                if (any || again) {  // (a piece's first step has no base yet)
+                  const uint64_t nm2 = f2_pack(-m, -m);
+                  uint64_t sum = f2_pack(0.f, 0.f);
+                  uint32_t x[32], y[32];
+                  tmem_ld32_nowait(ts, x);
+                  tmem_ld32_nowait(ts + 32u, y);
+                  tmem_wait_ld(x);
+                  tmem_wait_ld(y);
+                  exp32(x, f2, nm2, &sum);
+                  pack_p32(reinterpret_cast<uint32_t*>(p), x, blk, iv);
+                  exp32(y, f2, nm2, &sum);
+                  pack_p32(reinterpret_cast<uint32_t*>(p) + 16, y, blk, iv);
+                  f2_unpack(sum, s0, s1);
+                  high = !(s0 + s1 <= kTcTop);
+                  if (again || !__any_sync(0xffffffffu, high)) break;
                 }
-                mx = fmaxf(mx, m1);
-              }
-              const bool move = mx * f - m > kTcAbove;
-              if (__any_sync(0xffffffffu, move)) {
+                again = true;
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                  uint32_t x[32];
+                  tmem_ld32_nowait(ts + uint32_t(c) * 32u, x);
+                  tmem_wait_ld(x);
+#pragma unroll
+                  for (int i = 0; i < 32; i += 2)
+                    mx = fmax3f(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                }
                 float k = 1.f;
-                if (move) {
+                if (high && mx * f - m > kTcBelow) {
                   const float nb = mx * f - kTcBelow;
                   k = fast_exp2(m - nb);
                   m = nb;
@@ -376,18 +410,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                   tmem_wait_st();
                 }
               }
-              const uint64_t nm2 = f2_pack(-m, -m);
-              uint64_t sum = f2_pack(0.f, 0.f);
-#pragma unroll 1
-              for (int c = 0; c < 64; c += 32) {
-                uint32_t x[32];
-                tmem_ld32_nowait(ts + uint32_t(c), x);
-                tmem_wait_ld(x);
-                exp32(x, f2, nm2, &sum);
-                store_p32(ts + uint32_t(c / 2), x, blk, iv);
-              }
-              float s0, s1;
-              f2_unpack(sum, s0, s1);
+              tmem_st32(ts, p);
               l += s0 + s1;
               tmem_wait_st();
             }
@@ -398,51 +421,88 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
           }
         }
       }
-      // the piece's rows: O once the last P V is done (pv_done would not tell:
-      // the last two may both be under way)
-      if (any) {
-        if (!wait(&o_done[w], no & 1, W_O_DONE)) return false;
-        tc_fence_after();
-        ++no;
+      // the piece's rows: O once the last P V is done (pv_done would not tell: the
+      // last two may both be under way).  With one row tile a row has an O in each
+      // stream: both streams read both, half the channels each, and write their sum.
+      const int some = MT == 1 && u1 - u0 == 1 ? 1 << (first_tile & 1) : 3;  // streams with a step
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if ((MT == 2 && x != w) || !(some >> x & 1)) continue;
+        if (!wait(&o_done[x], no >> x & 1, W_O_DONE)) return false;
+      }
+      no ^= uint32_t(some);
+      tc_fence_after();
+      float w0 = 1.f, w1 = 0.f;  // weights of this stream's O and of the other's
+      if (MT == 1) {
+        if (!any) m = -FLT_MAX, l = 0.f;
+        row_ml[w][lrow] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ml_full);
+        if (!wait(&ml_full, np & 1, W_O_READ)) return false;
+        const float2 o = row_ml[w ^ 1][lrow];
+        const float mm = fmaxf(m, o.x);
+        w0 = any ? fast_exp2(m - mm) : 0.f;
+        w1 = some >> (w ^ 1) & 1 ? fast_exp2(o.x - mm) : 0.f;
+        l = w0 * l + w1 * o.y;
+        m = mm;
       }
       if (!idle) {
-        const bool whole = MT == 2 && u0 == 0 && u1 == units;
+        const bool whole = u0 == 0 && u1 == units;
         const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
-        const int slot = MT == 2 ? int(blockIdx.x) + seg : 2 * (int(blockIdx.x) + seg) + w;
+        const int slot = int(blockIdx.x) + seg;
         const bool on = row < R;
         float4* part = reinterpret_cast<float4*>(a.opart) + size_t(slot) * (D / 4) * a.R16 + row;
         uint16_t* out =
             a.out + ((size_t(n) * a.B + (on ? row / G : 0)) * a.Hq + g * G + (on ? row % G : 0)) * D;
+        const uint32_t to2 = tm + lanes + 256u + uint32_t(w ^ 1) * 128u;
+        constexpr int kParts = MT == 1 ? D / 64 : D / 32;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int cc = 0; cc < kParts; ++cc) {
+          const int c = MT == 1 ? w * kParts + cc : cc;
           uint32_t r[32];
-          if (any) {
+          float v[32];
+          if (MT == 2 || any) {
             tmem_ld32_nowait(to + uint32_t(c) * 32u, r);
             tmem_wait_ld(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * w0;
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = 0;
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
+          if (MT == 1 && (some >> (w ^ 1) & 1)) {
+            tmem_ld32_nowait(to2 + uint32_t(c) * 32u, r);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(r[i]), w1, v[i]);
           }
           if (on && whole) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(out + c * 32 + i) = make_uint4(
-                  pack_bf16(__uint_as_float(r[i]) * inv, __uint_as_float(r[i + 1]) * inv),
-                  pack_bf16(__uint_as_float(r[i + 2]) * inv, __uint_as_float(r[i + 3]) * inv),
-                  pack_bf16(__uint_as_float(r[i + 4]) * inv, __uint_as_float(r[i + 5]) * inv),
-                  pack_bf16(__uint_as_float(r[i + 6]) * inv, __uint_as_float(r[i + 7]) * inv));
+              *reinterpret_cast<uint4*>(out + c * 32 + i) =
+                  make_uint4(pack_bf16(v[i] * inv, v[i + 1] * inv),
+                             pack_bf16(v[i + 2] * inv, v[i + 3] * inv),
+                             pack_bf16(v[i + 4] * inv, v[i + 5] * inv),
+                             pack_bf16(v[i + 6] * inv, v[i + 7] * inv));
           } else if (on) {  // neighbouring rows of a warp are neighbours in memory
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
               part[size_t(c * 8 + i / 4) * a.R16] =
-                  make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
-                              __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
           __syncwarp();
         }
-        if (on && !whole) a.ml[size_t(slot) * a.R16 + row] = make_float2(m, l);
+        if (on && !whole && (MT == 2 || w == 0))
+          a.ml[size_t(slot) * a.R16 + row] = make_float2(m, l);
         __syncwarp();
         tc_fence_before();
+      }
+      if (MT == 1) {  // O and (m, l) have been read: the next piece may begin
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_read);
+        if (!wait(&o_read, np & 1, W_O_READ)) return false;
+        ++np;
+        tc_fence_after();
       }
       return true;
     });

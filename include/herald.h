@@ -116,7 +116,7 @@ herald_status herald_inject_launch_failure(int after, int cuda_error);
  * partials, 0x800 the previous tile's P V done; the attention over a paged
  * 4-bit cache: 0x1 raw slot, 0x2 raw codes, 0x4 operand buffer free, 0x8
  * queries free, 0x10 queries staged, 0x20 K ready, 0x40 P ready, 0x80 V ready,
- * 0x100 P V done, 0x200 S ready, 0x400 key masks, 0x800 O ready; with few rows
+ * 0x100 P V done, 0x200 S ready, 0x400 key masks, 0x800 O ready, 0x1000 O read; with few rows
  * 0x1 stage free, 0x2 stage full).
  * Synchronises `stream` first. */
 herald_status herald_workspace_error(void *ws, void *stream, uint32_t *code);

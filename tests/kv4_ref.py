@@ -137,12 +137,13 @@ def attention(q, cache, lengths, bk=None, bv=None, scale=None):
                                        products and a few fp32 roundings of the
                                        score) + 2^-21 (exp2)
       2^-13 (A_c + A_b)                fp32 sums over up to 2^10 matrix steps
-      2^-36 sum_c |v_j|                P below fp16's 2^-14 is off by half a
+      2^-30 sum_c |v_j|                P below fp16's 2^-14 is off by half a
                                        subnormal step, 2^-25, whatever its size;
-                                       the row's largest P is at least 2^11 (its
+                                       the row's largest P is at least 2^5 (its
                                        exponent base is set 11 below the largest
-                                       score) and the row sum no less, so each
-                                       cache key adds at most 2^-25 / 2^11 |v_j|
+                                       score with few rows, 5 below it with many)
+                                       and the row sum no less, so each cache key
+                                       adds at most 2^-25 / 2^5 |v_j|
     Returns (out, bound)."""
     N, B, Hq, d = q.shape
     Hkv = cache.Hkv
@@ -171,5 +172,5 @@ def attention(q, cache, lengths, bk=None, bv=None, scale=None):
             Ac, Ab = p[:, :m] @ np.abs(vv[:m]), p[:, m:] @ np.abs(vv[m:])
             delta = (d + 8) * 2.0 ** -24 * (np.abs(qq) @ np.abs(kk).T).max(-1) * scale + 2.0 ** -21
             tol[n, :, h] = 2.0 ** -8 * np.abs(out[n, :, h]) + 2.0 ** -11 * Ac + 2.0 ** -8 * Ab \
-                + (2 * delta[:, None] + 2.0 ** -13) * (Ac + Ab) + 2.0 ** -36 * np.abs(vv[:m]).sum(0)
+                + (2 * delta[:, None] + 2.0 ** -13) * (Ac + Ab) + 2.0 ** -30 * np.abs(vv[:m]).sum(0)
     return out, tol
