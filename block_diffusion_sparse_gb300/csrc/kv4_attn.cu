@@ -47,10 +47,11 @@ constexpr int kKv4Threads = (kKv4Parts + 1) * 32;
 constexpr int kKv4Unit = 16;        // keys per warp and tile
 constexpr int kKv4MmaRows = 16;     // most rows per KV head of this kernel
 // What a piece costs beside its tiles, in tiles (kv4_units).  Ragged batch of 64
-// single tokens: 98 us without, 94 / 86 / 83 / 84 with 1 / 2 / 3 / 4; tensor-core
-// kernel, 32 tokens at 32K: 37 us without, 30 with 2, 4 or 6; drafts of 5: 26, 25,
-// 23.6, 23.6; 32 tokens at 4 x 64K: 150, 149, 147, 146.
-constexpr int kKv4PadRows = 3, kKv4PadTc = 6;
+// single tokens: 98 us without, 94 / 86 / 83 / 84 with 1 / 2 / 3 / 4.  Tensor-core
+// kernel with 3 / 6 / 7 / 8 / 11: 32 tokens at 64K 45.5 / 43.0 / 42.3 / 41.6 / 41.1,
+// drafts of 5 24.1 / 22.7 / 23.0 / 23.4 / 23.4, 12 ragged blocks of 64 tokens 170 /
+// 166 / - / 167 / 171.
+constexpr int kKv4PadRows = 3, kKv4PadTc = 7;
 constexpr float kKv4Below = 11.f, kKv4Above = 15.f;  // exponent base, log2 units
 
 HERALD_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -522,23 +523,21 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
 }
 
 // Joins the pieces of every segment that has more than one, and writes zeros
-// for segments without keys.  grid (N*Hkv, ceil(R / 8)), 1024 threads: eight
-// rows' chunks of four channels per D/4 * 8 threads, and kKv4JoinThreads over
-// that many groups, each with every such-and-suchth partial, four in flight, so
-// that the pieces of a long context travel at once; the groups are added in
-// order.
-constexpr int kKv4JoinThreads = 1024, kKv4JoinRows = 8;
-template <int D>
-__global__ void __launch_bounds__(kKv4JoinThreads)
+// for segments without keys.  grid (N*Hkv, ceil(R / Rows)): Rows rows' chunks of
+// four channels per D/4 * Rows threads, and Threads over that many groups, each with
+// every such-and-suchth partial, four in flight, so that the pieces of a long
+// context travel at once; the groups are added in order.
+template <int D, int Rows, int Threads>
+__global__ void __launch_bounds__(Threads)
     kv4_join_kernel(const Kv4AttnArgs a, int blk_units) {
-  constexpr int TPG = kKv4JoinRows * (D / 4), GR = kKv4JoinThreads / TPG;
+  constexpr int TPG = Rows * (D / 4), GR = Threads / TPG;
   __shared__ float4 part[GR][TPG];
-  __shared__ float part_m[GR][kKv4JoinRows], part_l[GR][kKv4JoinRows];
+  __shared__ float part_m[GR][Rows], part_l[GR][Rows];
   const int seg = blockIdx.x, n = seg / a.Hkv, g = seg - n * a.Hkv;
   const int G = a.Hq / a.Hkv, R = a.B * G;
   const int grp = threadIdx.x / TPG, item = threadIdx.x % TPG;
-  const int rr = item % kKv4JoinRows, c4 = item / kKv4JoinRows;
-  const int r = int(blockIdx.y) * kKv4JoinRows + rr, rc = min(r, R - 1);
+  const int rr = item % Rows, c4 = item / Rows;
+  const int r = int(blockIdx.y) * Rows + rr, rc = min(r, R - 1);
   const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, blk_units, a.pad), a.Hkv, a.ctas);
   const int units = kv4_units(a.ctx[n], a.L_max, blk_units, a.pad);
   const int first =
@@ -612,6 +611,24 @@ static cudaError_t launch_rows(const Kv4AttnArgs& a, uint32_t* err, cudaStream_t
                   dim3(kKv4Threads), smem, st, a, err);
 }
 
+template <int D>
+static cudaError_t launch_join(const Kv4AttnArgs& a, int blk_units, int R, int num_sms,
+                               cudaStream_t st) {
+  auto go = [&](auto* kernel, int rows, int threads) {
+    return launch_k("kv4_join_kernel", kernel, dim3(unsigned(a.N * a.Hkv), unsigned(cdiv(R, rows))),
+                    dim3(unsigned(threads)), 0, st, a, blk_units);
+  };
+  const int64_t segs = int64_t(a.N) * a.Hkv;
+  // While one wave holds them, CTAs of 1024 threads keep more partials of a row in
+  // flight; more CTAs than that want small ones, several to an SM.  Us per call with
+  // only (4, 1024) and (8, 1024) / as chosen / only (8, 256): token at 128K 39 / 38.6
+  // / 41.6, 32 tokens at 32K 29 / 29 / 39, 64 ragged tokens 83 / 77 / 77, 32 tokens at
+  // 4 x 64K 134 / 127 / 128, 12 ragged blocks of 64 167 / 119 / 120.
+  if (segs * cdiv(R, 4) <= num_sms) return go(kv4_join_kernel<D, 4, 1024>, 4, 1024);
+  if (segs * cdiv(R, 8) <= num_sms) return go(kv4_join_kernel<D, 8, 1024>, 8, 1024);
+  return go(kv4_join_kernel<D, 8, 256>, 8, 256);
+}
+
 // Workspace: error word, then (m, l) and O of every partial.
 struct Kv4Ws {
   size_t ml, opart, total;
@@ -653,13 +670,8 @@ cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4D
   else
     HERALD_CHECK_LAUNCH((R <= 8 ? launch_rows<64, 1>(a, err, st) : launch_rows<64, 2>(a, err, st)));
   const int blk_units = !bk ? 0 : tc ? cdiv(dm.B, kKv4Tile) : kKv4BlkJoined;
-  const dim3 grid(unsigned(dm.N * dm.Hkv), unsigned(cdiv(R, kKv4JoinRows)));
-  if (dm.d == 128)
-    HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<128>, grid,
-                                 dim3(kKv4JoinThreads), 0, st, a, blk_units));
-  else
-    HERALD_CHECK_LAUNCH(launch_k("kv4_join_kernel", kv4_join_kernel<64>, grid,
-                                 dim3(kKv4JoinThreads), 0, st, a, blk_units));
+  HERALD_CHECK_LAUNCH(dm.d == 128 ? launch_join<128>(a, blk_units, R, num_sms, st)
+                                  : launch_join<64>(a, blk_units, R, num_sms, st));
   return cudaGetLastError();
 }
 
