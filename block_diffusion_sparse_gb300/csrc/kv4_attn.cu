@@ -200,6 +200,17 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
     // this lane's keys of the warp's 16: the two of its scores, the four of V
     const int key_s = 4 * (lg & 1) + ((lg >> 1) ^ (lg & 1));  // and + 8
     auto key_v = [&](int i) { return 8 * (i >> 1) + 4 * (i & 1) + (lt ^ (i & 1)); };
+    // where they start in a stage
+    const uint32_t row_s = uint32_t(warp * kKv4Unit + key_s);
+    const uint32_t k_off = row_s * kRowC + uint32_t(lt) * (kRowC / 4);
+    const uint32_t ks_off = uint32_t(2 * S::kCodes) + row_s * kRowS + uint32_t(lt) * (kRowS / 4);
+    uint32_t v_off[2], vs_off[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t r = uint32_t(warp * kKv4Unit + key_v(i));
+      v_off[i] = uint32_t(S::kCodes) + r * kRowC + uint32_t(lg) * (kRowC / 8);
+      vs_off[i] = uint32_t(2 * S::kCodes + S::kScales) + r * kRowS + uint32_t(lg) * kRowS / 8;
+    }
     pieces([&](int n, int g, int seg, int ctx, int units, int u0, int u1) {
       // queries: B fragments (lane: row lg of each 8-row tile), fp16 scaled by
       // a power of two per row; rs[nt][2] undo it for the rows this lane's
@@ -364,42 +375,39 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
       for (int u = u0; u < tiles && warp < kKv4Warps; ++u, ++t) {
         const uint32_t st = t % S::kStages, sm = base + st * uint32_t(S::kStage);
         wait(&full[st], (t / S::kStages) & 1, W_STAGE_FULL);
-        const int valid = warp_same(int(*(volatile uint8_t*)&counts[st][warp]));
+        // (every read first, not after the count: a tile of which the warp has no key
+        // is rare)
+        const int valid_lane = int(*(volatile uint8_t*)&counts[st][warp]);
+        const uint32_t ka = sm + k_off, ksa = sm + ks_off;
+        uint32_t kw[2][D / 32], ksc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (D == 128) {
+            const uint4 w = lds128(ka + uint32_t(i * 8 * kRowC));
+            kw[i][0] = w.x, kw[i][1] = w.y, kw[i][2] = w.z, kw[i][3] = w.w;
+            ksc[i] = lds_u16(ksa + uint32_t(i * 8 * kRowS));
+          } else {
+            const uint2 w = lds64(ka + uint32_t(i * 8 * kRowC));
+            kw[i][0] = w.x, kw[i][1] = w.y;
+            ksc[i] = lds_u8(ksa + uint32_t(i * 8 * kRowS));
+          }
+        }
+        uint32_t vw[4][D / 64], vsc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t va = sm + v_off[i & 1] + uint32_t((i >> 1) * 8 * kRowC);
+          if constexpr (D == 128) {
+            const uint2 w = lds64(va);
+            vw[i][0] = w.x, vw[i][1] = w.y;
+          } else {
+            vw[i][0] = lds32(va);
+          }
+          vsc[i] = lds_u8(sm + vs_off[i & 1] + uint32_t((i >> 1) * 8 * kRowS));
+        }
+        const int valid = warp_same(valid_lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
         if (valid > 0) {
-          const uint32_t row0 = uint32_t(warp * kKv4Unit);
-          const uint32_t ka = sm + (row0 + uint32_t(key_s)) * kRowC + uint32_t(lt) * (kRowC / 4);
-          const uint32_t ksa = sm + uint32_t(2 * S::kCodes) + (row0 + uint32_t(key_s)) * kRowS +
-                               uint32_t(lt) * (kRowS / 4);
-          uint32_t kw[2][D / 32], ksc[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if constexpr (D == 128) {
-              const uint4 w = lds128(ka + uint32_t(i * 8 * kRowC));
-              kw[i][0] = w.x, kw[i][1] = w.y, kw[i][2] = w.z, kw[i][3] = w.w;
-              ksc[i] = lds_u16(ksa + uint32_t(i * 8 * kRowS));
-            } else {
-              const uint2 w = lds64(ka + uint32_t(i * 8 * kRowC));
-              kw[i][0] = w.x, kw[i][1] = w.y;
-              ksc[i] = lds_u8(ksa + uint32_t(i * 8 * kRowS));
-            }
-          }
-          uint32_t vw[4][D / 64], vsc[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t r = row0 + uint32_t(key_v(i));
-            const uint32_t va = sm + uint32_t(S::kCodes) + r * kRowC + uint32_t(lg) * (kRowC / 8);
-            if constexpr (D == 128) {
-              const uint2 w = lds64(va);
-              vw[i][0] = w.x, vw[i][1] = w.y;
-            } else {
-              vw[i][0] = lds32(va);
-            }
-            vsc[i] = lds_u8(sm + uint32_t(2 * S::kCodes + S::kScales) + r * kRowS +
-                            uint32_t(lg) * kRowS / 8);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[st]);
-
           float s[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -462,9 +470,6 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
                 mma_f16(o[nt][w * 4 + i], e0[i], d0[i], e1[i], d1[i], p0[nt], p1[nt]);
             }
           }
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[st]);
         }
       }
 
