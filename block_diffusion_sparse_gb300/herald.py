@@ -218,10 +218,12 @@ def lib() -> C.CDLL:
 
 
 def _p(x):
+    if x is None:
+        return None
     try:
         return x.data_ptr()
     except AttributeError:
-        if x is None or isinstance(x, int):
+        if isinstance(x, int):
             return x
     raise TypeError(f"expected a tensor or an address, got {type(x)}")
 
@@ -238,9 +240,10 @@ def _s(stream):
 def _nbytes(ws, ws_bytes):
     if ws_bytes is not None:
         return int(ws_bytes)
-    if hasattr(ws, "numel"):
+    try:
         return ws.numel() * ws.element_size()
-    raise ValueError("ws_bytes is required for a raw workspace address")
+    except AttributeError:
+        raise ValueError("ws_bytes is required for a raw workspace address") from None
 
 
 def _check(status: int):
