@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
 // Joins the pieces of every segment that has more than one, and writes zeros
 // for segments without keys.  grid (N*Hkv, ceil(R / Rows)): Rows rows' chunks of
 // four channels per D/4 * Rows threads, and Threads over that many groups, each with
-// every such-and-suchth partial, four in flight, so that the pieces of a long
+// every such-and-suchth partial, five in flight, so that the pieces of a long
 // context travel at once; the groups are added in order.
 template <int D, int Rows, int Threads>
 __global__ void __launch_bounds__(Threads)
@@ -568,16 +568,18 @@ __global__ void __launch_bounds__(Threads)
   const float4* op = reinterpret_cast<const float4*>(a.opart) + size_t(c4) * a.R16 + rc;
   float M = -FLT_MAX, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kFly = 4;
+  constexpr int kFly = 5;
   for (int c = c0 + grp; c <= c1; c += kFly * GR) {
     float2 p[kFly];
     float4 x[kFly];
 #pragma unroll
     for (int i = 0; i < kFly; ++i) {
-      const int ci = min(c + i * GR, c1);
-      p[i] = a.ml[size_t(ci) * a.R16 + rc];
-      x[i] = op[size_t(ci) * (D / 4) * a.R16];
-      if (c + i * GR > c1) p[i] = make_float2(-FLT_MAX, 0.f), x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int ci = c + i * GR;
+      p[i] = make_float2(-FLT_MAX, 0.f), x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ci <= c1) {
+        p[i] = a.ml[size_t(ci) * a.R16 + rc];
+        x[i] = op[size_t(ci) * (D / 4) * a.R16];
+      }
     }
     float M1 = M;
 #pragma unroll

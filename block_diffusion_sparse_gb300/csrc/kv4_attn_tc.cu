@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               x4[i][1] = src[1];
             }
           }
-float mx[MT * kRows];  // (the rows' maxima side by side: their steps wait on one another)
+          float mx[MT * kRows];  // (the rows' maxima side by side: their steps wait on one another)
           if (!blk) {
 #pragma unroll
             for (int i = 0; i < MT * kRows; ++i) mx[i] = absmax16(x4[i][0], x4[i][1]);
