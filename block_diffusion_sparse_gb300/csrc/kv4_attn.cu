@@ -193,14 +193,16 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
         }
       }
     });
-    if (!ok)  // the copies under way land before the CTA may leave
-      for (uint32_t i = t > uint32_t(S::kStages) ? t - S::kStages : 0; i < t; ++i)
-        mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1);
+    // every copy has landed before the CTA may leave (where a wait has run out, nobody
+    // else waits for it)
+    for (uint32_t i = t > uint32_t(S::kStages) ? t - S::kStages : 0; i < t; ++i)
+      mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1);
   } else {
     // ------------------------------------------------------------ products
     // (after a failed wait the warps go on without waiting: their barriers
     // below stay in step, the results are worthless and the error is recorded)
     uint32_t t = 0;
+    bool lost = false;  // a wait has run out
     const uint32_t base = smem_u32(smem);
     // this lane's keys of the warp's 16: the two of its scores, the four of V
     const int key_s = 4 * (lg & 1) + ((lg >> 1) ^ (lg & 1));  // and + 8
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
 #pragma unroll 1
       for (int u = u0; u < tiles && warp < kKv4Warps; ++u, ++t) {
         const uint32_t st = t % S::kStages, sm = base + st * uint32_t(S::kStage);
-        wait(&full[st], (t / S::kStages) & 1, W_STAGE_FULL);
+        if (!lost) lost = !wait(&full[st], (t / S::kStages) & 1, W_STAGE_FULL);
         // (every read first, not after the count: a tile of which the warp has no key
         // is rare)
         const int valid_lane = int(*(volatile uint8_t*)&counts[st][warp]);

@@ -661,11 +661,10 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
         }
         return true;
       });
-      // every copy has landed before the CTA may leave (only after a failed
-      // wait can one still be under way)
-      if (*(volatile uint32_t*)&failed)
-        for (uint32_t i = mt > slots ? mt - slots : 0; i < mt; ++i)
-          mbar_wait(&raw_full[kv][i % slots], (i / slots) & 1);
+      // every copy has landed before the CTA may leave (where a wait has run out,
+      // nobody else waits for it)
+      for (uint32_t i = mt > slots ? mt - slots : 0; i < mt; ++i)
+        mbar_wait(&raw_full[kv][i % slots], (i / slots) & 1);
     } else if (warp == kTcSWarp || warp == kTcSWarp + 2) {
       // ------------------------------------------------------ S issuers
       // (the whole warp walks the loops, lane 0 issues)
