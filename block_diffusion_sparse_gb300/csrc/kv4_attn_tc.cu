@@ -55,7 +55,7 @@ constexpr int kTcBufs = 4;                 // operand buffers (128 keys of K or 
 // Raw slots of K and of V tiles: as many as fit beside the operands.
 __host__ __device__ constexpr int tc_raw_k(int MT) { return MT == 2 ? 2 : 3; }
 __host__ __device__ constexpr int tc_raw_v(int MT) { return MT == 2 ? 1 : 3; }
-// Tiles whose key masks are kept.  A K copy runs at most three slots and two
+// Tiles whose key masks are kept for the softmax.  A K copy runs at most three slots and two
 // operand buffers ahead of the scores, and the scores two steps ahead of P: the
 // mask of 16 tiles back has been read by everybody.
 constexpr int kTcMasks = 16;
@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
   __shared__ uint32_t missing;                      // a position below a length had no page
   __shared__ float row_f[2 * kTileM];               // score factors of the rows (cache tiles)
   __shared__ uint32_t key_mask[kTcMasks][4];        // bit: the key counts
+  __shared__ uint32_t val_mask[kRawV][4];           // the same, for the rows of a raw V slot
   const TcSmem L = tc_smem(D, MT);
   uint8_t* base = align1024(smem_raw);
   uint8_t *Qs = base + L.q, *Bs = base + L.buf, *Rs = base + L.raw;
@@ -340,10 +341,10 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
         const uint64_t f2 = f2_pack(f, f);
         mbar_arrive(&q_free);  // (this thread has read its factor of the phase)
         ++phase;
-        for (; u < pe; ++u, ++tile) {
-          const uint32_t mask_no = mt;
-          if (!blk) ++mt;
-          if (MT == 1 && int(tile & 1) != w) continue;
+        const int ue = u;
+        if (MT == 1 && int(tile & 1) != w) ++u;
+        for (; u < pe; u += 3 - MT) {
+          const uint32_t mask_no = mt + uint32_t(u - ue);
           const int keys = tile_keys(u, ctx);
 #pragma unroll 1
           for (int k0 = 0; k0 < keys; k0 += kTcStep, ++ns) {
@@ -426,6 +427,9 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
             any = true;
           }
         }
+        tile += uint32_t(pe - ue);
+        if (!blk) mt += uint32_t(pe - ue);
+        u = pe;
       }
       // the piece's rows: O once the last P V is done (pv_done would not tell: the
       // last two may both be under way).  With one row tile a row has an O in each
@@ -567,10 +571,8 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                               : cw * 32 + s * 16 + (lane >> 1);
             };
             uint32_t counts = ~0u;  // keys of this warp's rows that count
-            if (kv) {  // a value row that does not count may hold any bytes: no 0 * NaN
-              if (!wait(&mask_full[mt % kTcMasks], (mt / kTcMasks) & 1, W_MASK)) return false;
-              counts = *(volatile uint32_t*)&key_mask[mt % kTcMasks][cw];
-            }
+            // (a value row that does not count may hold any bytes: no 0 * NaN)
+            if (kv) counts = *(volatile uint32_t*)&val_mask[rm][cw];
             if (item >= uint32_t(kTcBufs) &&
                 !wait(&buf_free[b], (item / kTcBufs - 1) & 1, W_BUF_FREE))
               return false;
@@ -638,15 +640,14 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
           uint64_t* full = &raw_full[kv][slot];
           if (mt >= slots && !wait(&raw_free[kv][slot], (mt / slots - 1) & 1, W_RAW_FREE))
             return false;
-          if (kv == 0) {
-            // lane i < 8: which of keys 16 i .. 16 i + 15 count
-            const int mine = __shfl_sync(0xffffffffu, keys, lane * 16 / sub) - lane * 16 % sub;
-            if (lane < 8)
-              reinterpret_cast<volatile uint16_t*>(key_mask[mt % kTcMasks])[lane] =
-                  uint16_t((1u << min(max(mine, 0), 16)) - 1u);
-            if (on && !have) *(volatile uint32_t*)&missing = 1;
-            __syncwarp();
-          }
+          // lane i < 8: which of keys 16 i .. 16 i + 15 count
+          const int mine = __shfl_sync(0xffffffffu, keys, lane * 16 / sub) - lane * 16 % sub;
+          uint32_t* mask = kv ? val_mask[slot] : key_mask[mt % kTcMasks];
+          if (lane < 8)
+            reinterpret_cast<volatile uint16_t*>(mask)[lane] =
+                uint16_t((1u << min(max(mine, 0), 16)) - 1u);
+          if (on && !have) *(volatile uint32_t*)&missing = 1;
+          __syncwarp();
           if (lane == 0) {
             if (kv == 0) mbar_arrive(&mask_full[mt % kTcMasks]);
             mbar_arrive_expect_tx(full, total * uint32_t(kRowC + kRowS));
@@ -684,9 +685,10 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                                    : make_idesc_f16(kTileM, kTcStep, false);
           if (!wait(&q_full, phase & 1, W_Q_FULL)) return false;
           const uint32_t ns0 = ns;
-          for (; u < pe; ++u, ++tile) {
-            if (MT == 1 && int(tile & 1) != w) continue;
-            const uint32_t ki = 2 * tile, kb = ki % kTcBufs;
+          const int ue = u;
+          if (MT == 1 && int(tile & 1) != w) ++u;
+          for (; u < pe; u += 3 - MT) {
+            const uint32_t ki = 2 * (tile + uint32_t(u - ue)), kb = ki % kTcBufs;
             if (!wait(&buf_full[kb], (ki / kTcBufs) & 1, W_K_FULL)) return false;
             const int keys = tile_keys(u, ctx);
             for (int k0 = 0; k0 < keys; k0 += kTcStep, ++ns) {
@@ -707,6 +709,8 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               __syncwarp();
             }
           }
+          tile += uint32_t(pe - ue);
+          u = pe;
           if (lane == 0) {
             if (ns > ns0)
               umma_commit(&q_free);
