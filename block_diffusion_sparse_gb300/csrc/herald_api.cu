@@ -666,6 +666,8 @@ static herald_status check_kv4_dims(const herald_dims& dm) {
   HERALD_RET_IF(check_dims(dm));
   if ((long long)dm.N * dm.Hkv > 65535)
     return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "N*Hkv = %lld > 65535", (long long)dm.N * dm.Hkv);
+  if (dm.L_max > 1 << 30)  // a position plus a tile stays within 31 bits
+    return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "L_max=%d > 2^30", dm.L_max);
   return HERALD_OK;
 }
 
@@ -686,8 +688,11 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
   g_err[0] = 0;
   HERALD_RET_IF(check_kv4_dims(dims));
   if (T < 1) return fail(HERALD_ERR_INVALID_ARG, "T=%d must be >= 1", T);
-  if ((long long)dims.N * T >= (1ll << 31))
+  if ((long long)dims.N * T >= (1ll << 31) || T > 1 << 30)
     return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "N*T too large");
+  if ((long long)dims.Hq + 2ll * dims.Hkv > 65535)
+    return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "Hq + 2*Hkv = %lld > 65535",
+                (long long)dims.Hq + 2ll * dims.Hkv);
   if (flags & ~HERALD_KV4_ADVANCE) return fail(HERALD_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
   if (!q && !k) return fail(HERALD_ERR_INVALID_ARG, "q and k are both NULL");
   HERALD_CHECK_PTR(ctx_len);

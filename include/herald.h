@@ -550,7 +550,8 @@ typedef struct {
  *            blocks the tokens fall into (herald_select_stage1_blocks reads
  *            them); Bk in [1, L_max].  Rows without a page count as zeros
  *   flags    HERALD_KV4_ADVANCE (needs the cache)
- * dims.B is not used beyond its own checks.  N*Hkv <= 65535. */
+ * dims.B is not used beyond its own checks.  N*Hkv <= 65535, Hq + 2*Hkv <=
+ * 65535, N*T < 2^31, T and L_max <= 2^30. */
 herald_status herald_kv4_append(herald_dims dims, int T, const int32_t *n_tok, const uint16_t *q,
                                 int64_t q_ld, const uint16_t *k, int64_t k_ld, const uint16_t *v,
                                 int64_t v_ld, const herald_rope *rope, int32_t *ctx_len,
@@ -567,7 +568,7 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t *n_tok, c
  *   block_k, block_v  [N][B][Hkv][d] bf16 device, or both NULL
  *   scale    softmax scale; 0 selects 1/sqrt(d)
  *   ws       herald_workspace_size_kv4(dims) bytes (0 = unsupported shape)
- * N*Hkv <= 65535.  Results do not depend on other calls or on timing. */
+ * N*Hkv <= 65535, L_max <= 2^30.  Results do not depend on other calls or on timing. */
 size_t herald_workspace_size_kv4(herald_dims dims);
 herald_status herald_kv4_attn(herald_dims dims, const uint16_t *q, const herald_kv4 *cache,
                               const int32_t *ctx_len, const uint16_t *block_k,
@@ -578,7 +579,8 @@ herald_status herald_kv4_attn(herald_dims dims, const uint16_t *q, const herald_
  * rows of herald_stage_candidates (idx = cand, n_sel = n_cand, P_max = C):
  *   pool[n][g][s] = bf16(value of row idx[n][g][s]) for s < n_sel,
  * zero rows for n_sel <= s < P_max and for positions outside [0, L_max) or
- * without a page.  pool_v may be NULL (keys only).  N*Hkv <= 65535. */
+ * without a page.  pool_v may be NULL (keys only).  N*Hkv <= 65535,
+ * L_max <= 2^30. */
 herald_status herald_kv4_gather(herald_dims dims, const int32_t *idx, const int32_t *n_sel,
                                 int P_max, const herald_kv4 *cache, uint16_t *pool_k,
                                 uint16_t *pool_v, void *stream);

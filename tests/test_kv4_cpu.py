@@ -83,7 +83,8 @@ def test_attention_refusals(over, status):
 
 @pytest.mark.parametrize("bad,status", [(dict(d=96), 2), (dict(Hq=9), 2), (dict(Hq=18), 2),
                                         (dict(B=65), 2), (dict(N=0), 1),
-                                        (dict(N=40000, L_max=8), 2)])
+                                        (dict(N=40000, L_max=8), 2),
+                                        (dict(N=1, Hq=1, Hkv=1, L_max=(1 << 30) + 1), 2)])
 def test_shapes_rejected(bad, status):
     _built()
     a = dict(N=2, Hq=8, Hkv=2, d=128, B=4, L_max=2048)
@@ -121,6 +122,17 @@ def test_append_refusals(over, status):
                             a["k_rot"], a["rope"], a["n_tok"], a["pooled"], a["Bk"], a["flags"],
                             a["q_ld"], a["k_ld"], a["v_ld"])
     assert e.value.status == status, e.value
+
+
+def test_append_counts_rejected():
+    """Token positions and head counts that launches or 32-bit positions do not hold."""
+    _built()
+    c = _cache(max_pages=1 << 25)
+    for d, T in ((H.dims(1, 1, 1, 64, 1, 1 << 30), (1 << 30) + 1),
+                 (H.dims(1, 8 * 7000, 7000, 64, 1, 16), 4)):
+        with pytest.raises(H.HeraldError) as e:
+            H.herald_kv4_append(d, T, OK, OK * 2, OK * 3, OK, c, OK * 4, OK * 5)
+        assert e.value.status == 2, e.value
 
 
 @pytest.mark.parametrize("over,status", [(dict(idx=0), 1), (dict(n_sel=OK + 4), 1), (dict(P=0), 1),
