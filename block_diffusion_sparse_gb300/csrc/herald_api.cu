@@ -711,6 +711,9 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
     if (k == k_rot && k_ld != int64_t(dims.Hkv) * dims.d)
       return fail(HERALD_ERR_INVALID_ARG, "k_rot may be k only when k is dense");
   }
+  if ((q && (q_rot == k || (cache && q_rot == v) || q_rot == k_rot)) ||
+      (k_rot && (k_rot == q || (cache && k_rot == v))))
+    return fail(HERALD_ERR_INVALID_ARG, "q_rot and k_rot may lie over q and k only, each over its own");
   Kv4Dev c{};
   if (cache) {
     if (!k) return fail(HERALD_ERR_INVALID_ARG, "k is NULL with a cache");

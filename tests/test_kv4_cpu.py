@@ -124,6 +124,20 @@ def test_append_refusals(over, status):
     assert e.value.status == status, e.value
 
 
+@pytest.mark.parametrize("over", [dict(q_rot=2), dict(q_rot=3), dict(q_rot=5), dict(k_rot=1),
+                                  dict(k_rot=3)])
+def test_append_outputs_over_other_inputs_rejected(over):
+    """A rotated output may lie over its own input, not over one that others still read."""
+    _built()
+    d = H.dims(2, 8, 2, 128, 4, 2048)
+    a = dict(q=1, k=2, v=3, q_rot=4, k_rot=5)
+    a.update(over)
+    q, k, v, q_rot, k_rot = (OK * x for x in a.values())
+    with pytest.raises(H.HeraldError) as e:
+        H.herald_kv4_append(d, 4, q, k, v, OK * 7, _cache(), q_rot, k_rot)
+    assert e.value.status == 1, e.value
+
+
 def test_append_counts_rejected():
     """Token positions and head counts that launches or 32-bit positions do not hold."""
     _built()
