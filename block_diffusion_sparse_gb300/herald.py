@@ -469,11 +469,21 @@ def _token_ld(x, ld, what):
     return step
 
 
+def _check_tokens(x, n, t, what):
+    """A tensor of tokens must hold [n, t] of them (one sequence: at least t)."""
+    if x is not None and not isinstance(x, int):
+        if x.shape[0] != n or (x.shape[1] != t if n > 1 else x.shape[1] < t):
+            raise ValueError(f"{what}: {tuple(x.shape[:2])} tokens, the call has {(n, t)}")
+
+
 def herald_kv4_append(d, T, q, k, v, ctx_len, cache, q_rot, k_rot, rope=None, n_tok=None,
                       pooled=None, Bk=0, flags=0, q_ld=None, k_ld=None, v_ld=None, stream=None):
     """cache: a Kv4 or None (rotate only); rope: a Rope or None.  The token
     strides of q, k, v [N, T, heads, d] are taken from the tensors (views of a
     fused projection's output) unless given."""
+    for x, ld, what in ((q, q_ld, "q"), (k, k_ld, "k"), (v, v_ld, "v")):
+        if ld is None:
+            _check_tokens(x, d.N, T, what)
     _check(lib().herald_kv4_append(
         d, int(T), _p(n_tok), _p(q), _token_ld(q, q_ld, "q"), _p(k), _token_ld(k, k_ld, "k"),
         _p(v), _token_ld(v, v_ld, "v"), None if rope is None else C.byref(rope), _p(ctx_len),

@@ -185,6 +185,21 @@ def test_binding_checks_tensors():
             H._token_ld(bad, None, "q")
 
 
+def test_binding_checks_token_counts():
+    """Tensors of another N or T than the call's would be read at wrong strides."""
+    torch = pytest.importorskip("torch")
+    _built()
+    d = H.dims(2, 4, 2, 64, 1, 64)
+    x = torch.zeros(2, 6, 2, 64, dtype=torch.bfloat16)
+    cache = _cache(max_pages=4, page=16)
+    for T, k in ((5, x), (7, x), (6, x[:1])):
+        with pytest.raises(ValueError):
+            H.herald_kv4_append(d, T, None, k, k, OK, cache, None, None)
+    one = H.dims(1, 4, 2, 64, 1, 64)
+    with pytest.raises(ValueError):
+        H.herald_kv4_append(one, 7, None, x[:1], x[:1], OK, cache, None, None)
+
+
 @pytest.mark.gpu
 def test_launch_failures_are_reported():
     torch = pytest.importorskip("torch")
