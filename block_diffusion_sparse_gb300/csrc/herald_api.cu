@@ -711,9 +711,6 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
     if (k == k_rot && k_ld != int64_t(dims.Hkv) * dims.d)
       return fail(HERALD_ERR_INVALID_ARG, "k_rot may be k only when k is dense");
   }
-  if ((q && (q_rot == k || (cache && q_rot == v) || q_rot == k_rot)) ||
-      (k_rot && (k_rot == q || (cache && k_rot == v))))
-    return fail(HERALD_ERR_INVALID_ARG, "q_rot and k_rot may lie over q and k only, each over its own");
   Kv4Dev c{};
   if (cache) {
     if (!k) return fail(HERALD_ERR_INVALID_ARG, "k is NULL with a cache");
@@ -738,6 +735,10 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
     if (rope->interleaved != 0 && rope->interleaved != 1)
       return fail(HERALD_ERR_INVALID_ARG, "interleaved=%d not 0 or 1", rope->interleaved);
   }
+  if ((q && (q_rot == k || (cache && q_rot == v) || q_rot == k_rot)) ||
+      (k_rot && (k_rot == q || (cache && k_rot == v))))
+    return fail(HERALD_ERR_INVALID_ARG,
+                "q_rot and k_rot may lie over q and k only, each over its own");
   HERALD_TRY_CUDA(launch_kv4_append(dims, T, n_tok, q, q_ld, k, k_ld, v, v_ld, rope, ctx_len,
                                     cache ? &c : nullptr, q_rot, k_rot, pooled, Bk,
                                     (flags & HERALD_KV4_ADVANCE) != 0,
