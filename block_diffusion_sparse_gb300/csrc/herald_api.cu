@@ -722,8 +722,8 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
   }
   if (pooled) {
     HERALD_CHECK_PTR(pooled);
-    if (Bk < 1 || Bk > dims.L_max)
-      return fail(HERALD_ERR_INVALID_ARG, "Bk=%d outside [1, L_max=%d]", Bk, dims.L_max);
+    if (Bk < 1 || Bk > 1 << 30)
+      return fail(HERALD_ERR_INVALID_ARG, "Bk=%d outside [1, 2^30]", Bk);
   }
   if (rope) {
     HERALD_CHECK_PTR(rope->cos_sin);

@@ -548,7 +548,8 @@ typedef struct {
  *   pooled   NULL, or fp32 [N][Hkv][ceil(L_max/Bk)][d] device: the means of
  *            herald_pool_keys over the keys as held, refreshed for the
  *            blocks the tokens fall into (herald_select_stage1_blocks reads
- *            them); Bk in [1, L_max].  Rows without a page count as zeros
+ *            them); Bk >= 1 (a block may be longer than the cache), <= 2^30.
+ *            Rows without a page count as zeros
  *   flags    HERALD_KV4_ADVANCE (needs the cache)
  * dims.B is not used beyond its own checks.  N*Hkv <= 65535, Hq + 2*Hkv <=
  * 65535, N*T < 2^31, T and L_max <= 2^30. */

@@ -267,6 +267,7 @@ APPEND = [
     (2, 16, 2, 128, 9, 16, [3, 55], None, 0, 0, False, 64),
     (2, 8, 2, 128, 600, 64, [0, 33], [600, 590], 128, 0, True, 64),
     (1, 8, 1, 128, 20, 16, [90], None, 128, 0, False, 64),  # runs into L_max = 100
+    (2, 4, 2, 64, 5, 16, [3, 10], [5, 2], 64, 0, True, 64),  # one block longer than the cache
 ]
 
 

@@ -101,7 +101,7 @@ def test_shapes_rejected(bad, status):
     (dict(q_rot=None), 1), (dict(cache=None, k_rot=None), 1), (dict(k=None), 1),
     (dict(v=None), 1), (dict(ctx=None), 1), (dict(n_tok=OK + 4), 1), (dict(flags=2), 1),
     (dict(cache=None, flags=1), 1), (dict(cache=None, pooled=OK, Bk=64), 1),
-    (dict(pooled=OK, Bk=0), 1), (dict(pooled=OK, Bk=4096), 1), (dict(pooled=OK + 8, Bk=64), 1),
+    (dict(pooled=OK, Bk=0), 1), (dict(pooled=OK, Bk=(1 << 30) + 1), 1), (dict(pooled=OK + 8, Bk=64), 1),
     (dict(q_ld=1000), 1), (dict(k_ld=257), 1), (dict(v_ld=-8), 1),
     (dict(q=OK, q_rot=OK, q_ld=2048), 1), (dict(k=OK, k_rot=OK, k_ld=2048), 1),
     (dict(rope=dict(cos_sin=0)), 1), (dict(rope=dict(rot=48)), 2), (dict(rope=dict(rot=0)), 2),
