@@ -1,10 +1,10 @@
 // kv4_attn.cu -- attention of a block's queries over the whole paged 4-bit
 // cache and the block's own bf16 keys, for few query rows per KV head (one
 // token, a short draft): bound by the cache's bytes and by the instructions that
-// turn codes into numbers.  One token over 128K (8 KV heads, 151 MB) takes 38 us, of
+// turn codes into numbers.  One token over 128K (8 KV heads, 151 MB) takes 37 us, of
 // which it streams for 29 at 5.2 TB/s; its copies alone, without a product, 31.  Per
 // 16 keys a warp issues some 340 instructions, 64 of them conversions and 64 products
-// with scales, each at half rate.  64 ragged tokens of up to 8K (327 MB): 76 us.
+// with scales, each at half rate.  64 ragged tokens of up to 8K (327 MB): 75 us.
 //
 // A CTA walks its share of the keys (kv4_split) in tiles of 128.  Its last warp
 // copies each tile's codes and scales from the pages into a ring of stages (bulk
