@@ -49,13 +49,13 @@ constexpr int kKv4Parts = kKv4Warps + 1;  // and one of the block's keys
 constexpr int kKv4Threads = (kKv4Parts + 1) * 32;
 constexpr int kKv4Unit = 16;        // keys per warp and tile
 // Most rows per KV head of this kernel.  16 rows here and on the tensor cores'
-// 128-row products: 19.3 and 25.8 us at 1 x 32K, 57 and 76 us at 16 x 8K (8 KV heads).
+// 128-row products: 18.3 and 24.5 us at 1 x 32K, 53 and 68 us at 16 x 8K (8 KV heads).
 constexpr int kKv4MmaRows = 16;
-// What a piece costs beside its tiles, in tiles (kv4_units).  Ragged batch of 64
-// single tokens: 98 us without, 94 / 86 / 83 / 84 with 1 / 2 / 3 / 4.  Tensor-core
-// kernel with 3 / 6 / 7 / 8 / 11: 32 tokens at 64K 45.5 / 43.0 / 42.3 / 41.6 / 41.1,
-// drafts of 5 24.1 / 22.7 / 23.0 / 23.4 / 23.4, 12 ragged blocks of 64 tokens 170 /
-// 166 / - / 167 / 171.
+// What a piece costs beside its tiles, in tiles (kv4_units).  64 ragged tokens with 0 /
+// 2 / 3 / 4 / 5: 88.7 / 78.7 / 74.7 / 75.7 / 76.4 us.  Tensor-core kernel with 0 / 3 / 5 /
+// 7 / 9 / 12: drafts of 5 25.6 / 23.2 / 22.0 / 22.1 / 22.9 / 22.9, 32 tokens at 32K 35.1 /
+// 29.2 / 28.2 / 28.0 / 27.7 / 28.9, 12 ragged blocks of 32 tokens 115 / 84 / 71.6 / 70.3 /
+// 70.7 / 71.5.
 constexpr int kKv4PadRows = 3, kKv4PadTc = 7;
 constexpr float kKv4Below = 11.f, kKv4Above = 15.f;  // exponent base, log2 units
 
