@@ -50,6 +50,7 @@ constexpr int kKv4Threads = (kKv4Parts + 1) * 32;
 constexpr int kKv4Unit = 16;        // keys per warp and tile
 // Most rows per KV head of this kernel.  16 rows here and on the tensor cores'
 // 128-row products: 18.3 and 24.5 us at 1 x 32K, 53 and 68 us at 16 x 8K (8 KV heads).
+// (24 here spill: 32 and 99 us where the tensor cores take 25 and 68.)
 constexpr int kKv4MmaRows = 16;
 // What a piece costs beside its tiles, in tiles (kv4_units).  64 ragged tokens with 0 /
 // 2 / 3 / 4 / 5: 88.7 / 78.7 / 74.7 / 75.7 / 76.4 us.  Tensor-core kernel with 0 / 3 / 5 /
