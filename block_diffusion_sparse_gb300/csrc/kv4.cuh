@@ -27,17 +27,7 @@ HERALD_DEV size_t kv4_row(const Kv4Dev& c, int phys, int Hkv, int g, int pos) {
   return ((size_t(phys) * Hkv + g) << c.page_log2) + (pos & ((1 << c.page_log2) - 1));
 }
 
-// Two codes (one byte in bits 0-7 of b) -> fp16 pair, low half first.
-HERALD_DEV uint32_t e2m1x2_to_half2(uint32_t b) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t, u0, u1, u2;\n\t"
-      "mov.b32 {t, u0, u1, u2}, %1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
-      : "=r"(r)
-      : "r"(b));
-  return r;
-}
-// The four bytes of a word of codes -> four fp16 pairs.
+// The four bytes of a word of codes -> four fp16 pairs, a byte's low half first.
 HERALD_DEV void e2m1x8_to_half2(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t"
       "mov.b32 {t0, t1, t2, t3}, %4;\n\t"

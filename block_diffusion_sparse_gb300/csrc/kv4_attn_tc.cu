@@ -59,7 +59,7 @@ __host__ __device__ constexpr int tc_raw_v(int MT) { return MT == 2 ? 1 : 3; }
 // operand buffers ahead of the scores, and the scores two steps ahead of P: the
 // mask of 16 tiles back has been read by everybody.
 constexpr int kTcMasks = 16;
-constexpr int kTcSoft = 256, kTcConv = 256;  // softmax and conversion threads
+constexpr int kTcSoft = 256;               // softmax threads
 constexpr int kTcThreadsAll = 768;         // 8 + 8 + 8 warps (22, 23 only fill a warpgroup)
 constexpr int kTcSWarp = 16, kTcCopyWarp = 17, kTcPvWarp = 20;  // S 16, 18; copies 17, 19; P V 20, 21
 constexpr float kTcBelow = 5.f, kTcTop = 60000.f;  // base of P and largest sum (see above)
@@ -168,12 +168,12 @@ HERALD_DEV void pack_p32(uint32_t* pk, const uint32_t (&x)[32], bool blk, float 
   }
 }
 
-// Largest magnitude of 16 bf16 (a NaN does not count).
 HERALD_DEV uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// Largest magnitude of 16 bf16 (a NaN does not count).
 HERALD_DEV float absmax16(const uint4& a, const uint4& b) {
   constexpr uint32_t k = 0x7FFF7FFFu;
   const uint32_t m = max_bf16x2(
