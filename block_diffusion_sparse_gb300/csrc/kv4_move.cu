@@ -276,7 +276,9 @@ __global__ void kv4_advance_kernel(int32_t* ctx, const int32_t* n_tok, int N, in
 }
 
 // grid (row groups, N*Hkv): D/16 lanes per row, each 16 channels: 8 bytes of
-// codes and one scale in, 32 bytes of bf16 out.
+// codes and one scale in, 32 bytes of bf16 out.  Bound by memory (32 x 4096 candidate
+// keys 8.8 us, 74% of the copy rate; with two rows per thread 9.7), by its chain of
+// three loads when small (4 x 1344 rows of K and V 2.7 us, with two 3.1).
 template <int D>
 __global__ void __launch_bounds__(kKv4MoveThreads)
     kv4_gather_kernel(const Kv4Dev c, const int32_t* __restrict__ idx,
