@@ -466,6 +466,8 @@ def _token_ld(x, ld, what):
     step = st if t > 1 else sn if n > 1 else h * d
     if n > 1 and sn != t * step:
         raise ValueError(f"{what}: sequences must follow each other at T token strides")
+    if step < h * d:  # (0 would mean dense to the call)
+        raise ValueError(f"{what}: tokens overlap (broadcast views are not taken)")
     return step
 
 

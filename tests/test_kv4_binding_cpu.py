@@ -1,0 +1,29 @@
+"""What the binding of the paged 4-bit cache's calls refuses before any of
+them reaches the library: tensors that would be read or written elsewhere than
+where they lie."""
+import pytest
+
+from block_diffusion_sparse_gb300 import herald as H
+
+torch = pytest.importorskip("torch")
+
+OK = 1 << 12  # an aligned address that these paths never follow
+
+
+@pytest.mark.parametrize("shape", [(3, 1, 2, 64), (3, 4, 2, 64), (1, 9, 2, 64)], ids=str)
+def test_broadcast_tokens_are_refused(shape):
+    """A token stride of 0 means dense to the call: a broadcast view would be
+    read past its only row."""
+    x = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16).expand(*shape)
+    N, T = shape[:2]
+    d = H.dims(N, 2, 2, 64, 1, 64)
+    with pytest.raises(ValueError, match="broadcast"):
+        H.herald_kv4_append(d, T, None, x, x, OK, None, None, OK)
+    with pytest.raises(ValueError, match="broadcast"):
+        H.herald_kv4_append(d, T, x, None, None, OK, None, OK, None)
+
+
+def test_overlapping_tokens_are_refused():
+    x = torch.zeros(4096, dtype=torch.bfloat16).as_strided((1, 4, 2, 64), (512, 64, 64, 1))
+    with pytest.raises(ValueError, match="overlap"):
+        H.herald_kv4_append(H.dims(1, 2, 2, 64, 1, 64), 4, x, None, None, OK, None, OK, None)
