@@ -27,3 +27,16 @@ def test_overlapping_tokens_are_refused():
     x = torch.zeros(4096, dtype=torch.bfloat16).as_strided((1, 4, 2, 64), (512, 64, 64, 1))
     with pytest.raises(ValueError, match="overlap"):
         H.herald_kv4_append(H.dims(1, 2, 2, 64, 1, 64), 4, x, None, None, OK, None, OK, None)
+
+
+def test_addresses_cross_without_a_failed_look_up():
+    """Raw addresses and streams are taken as they are: looking for a tensor's
+    attribute on each made a call of a dozen addresses 5 us longer."""
+    class Address(int):
+        def __getattr__(self, name):
+            raise AssertionError(f"looked for {name}")
+
+    assert H._p(Address(OK)) == OK and H._s(Address(7)) == 7 and H._s(None) is None
+    for f in (H._p, H._s):
+        with pytest.raises(TypeError):
+            f(1.5)
