@@ -115,6 +115,7 @@ def kv4(page, table, k_codes, k_scales, v_codes, v_scales, k_scale=1.0, v_scale=
     s = Kv4(int(page), n_pages, int(table.shape[1]), _p(table), *(_p(x) for x in arrays),
             float(k_scale), float(v_scale))
     s._keep = (table, arrays)
+    s._shape = (int(table.shape[0]), int(k_codes.shape[1]), 2 * int(k_codes.shape[3]))
     return s
 
 
@@ -478,6 +479,17 @@ def _check_tokens(x, n, t, what):
             raise ValueError(f"{what}: {tuple(x.shape[:2])} tokens, the call has {(n, t)}")
 
 
+def _kv4_arg(cache, d):
+    """A cache made by kv4() must be one of the call's shape: with another Hkv,
+    d or a shorter table the kernels would reach past its arrays."""
+    if cache is None:
+        return None
+    n, hkv, ch = getattr(cache, "_shape", (d.N, d.Hkv, d.d))
+    if n < d.N or hkv != d.Hkv or ch != d.d:
+        raise ValueError(f"cache: made for N={n}, Hkv={hkv}, d={ch}, the call has {d}")
+    return C.byref(cache)
+
+
 def herald_kv4_append(d, T, q, k, v, ctx_len, cache, q_rot, k_rot, rope=None, n_tok=None,
                       pooled=None, Bk=0, flags=0, q_ld=None, k_ld=None, v_ld=None, stream=None):
     """cache: a Kv4 or None (rotate only); rope: a Rope or None.  The token
@@ -489,8 +501,7 @@ def herald_kv4_append(d, T, q, k, v, ctx_len, cache, q_rot, k_rot, rope=None, n_
     _check(lib().herald_kv4_append(
         d, int(T), _p(n_tok), _p(q), _token_ld(q, q_ld, "q"), _p(k), _token_ld(k, k_ld, "k"),
         _p(v), _token_ld(v, v_ld, "v"), None if rope is None else C.byref(rope), _p(ctx_len),
-        None if cache is None else C.byref(cache), _p(q_rot), _p(k_rot), _p(pooled), int(Bk),
-        int(flags), _s(stream)))
+        _kv4_arg(cache, d), _p(q_rot), _p(k_rot), _p(pooled), int(Bk), int(flags), _s(stream)))
 
 
 def herald_workspace_size_kv4(d: Dims) -> int:
@@ -501,15 +512,14 @@ def herald_kv4_attn(d, q, cache, ctx_len, block_k, block_v, out, scale=0.0, ws=N
                     ws_bytes=None, stream=None):
     """Attention over a paged 4-bit cache (a Kv4) and, unless both are None,
     the block's own keys and values."""
-    _check(lib().herald_kv4_attn(d, _p(q), None if cache is None else C.byref(cache), _p(ctx_len),
-                                 _p(block_k), _p(block_v), _p(out), float(scale), _p(ws),
-                                 _nbytes(ws, ws_bytes), _s(stream)))
+    _check(lib().herald_kv4_attn(d, _p(q), _kv4_arg(cache, d), _p(ctx_len), _p(block_k),
+                                 _p(block_v), _p(out), float(scale), _p(ws), _nbytes(ws, ws_bytes),
+                                 _s(stream)))
 
 
 def herald_kv4_gather(d, idx, n_sel, P_max, cache, pool_k, pool_v=None, stream=None):
-    _check(lib().herald_kv4_gather(d, _p(idx), _p(n_sel), int(P_max),
-                                   None if cache is None else C.byref(cache), _p(pool_k),
-                                   _p(pool_v), _s(stream)))
+    _check(lib().herald_kv4_gather(d, _p(idx), _p(n_sel), int(P_max), _kv4_arg(cache, d),
+                                   _p(pool_k), _p(pool_v), _s(stream)))
 
 
 class Trace:

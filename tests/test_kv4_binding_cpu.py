@@ -40,3 +40,23 @@ def test_addresses_cross_without_a_failed_look_up():
     for f in (H._p, H._s):
         with pytest.raises(TypeError):
             f(1.5)
+
+
+def _cache(N=2, Hkv=2, d=64, page=16, max_pages=4):
+    u8 = dict(dtype=torch.uint8)
+    c, s = torch.zeros(3, Hkv, page, d // 2, **u8), torch.zeros(3, Hkv, page, d // 16, **u8)
+    return H.kv4(page, torch.zeros(N, max_pages, dtype=torch.int32), c, s, c.clone(), s.clone())
+
+
+@pytest.mark.parametrize("other", [dict(Hkv=4), dict(Hkv=1), dict(d=128), dict(N=3)], ids=str)
+def test_caches_of_another_shape_are_refused(other):
+    """A cache of fewer heads, channels or sequences than the call's would be
+    reached past its end; one of more would be read at wrong rows."""
+    a = dict(N=2, Hq=8, Hkv=2, d=64, B=1, L_max=64)
+    a.update(other)
+    d, c = H.dims(**a), _cache()
+    for call in (lambda: H.herald_kv4_append(d, 4, OK, OK * 9, OK * 17, OK, c, OK * 25, OK * 33),
+                 lambda: H.herald_kv4_attn(d, OK, c, OK, None, None, OK, ws=OK, ws_bytes=1 << 40),
+                 lambda: H.herald_kv4_gather(d, OK, OK, 8, c, OK)):
+        with pytest.raises(ValueError, match="cache"):
+            call()
