@@ -472,11 +472,42 @@ def _token_ld(x, ld, what):
     return step
 
 
-def _check_tokens(x, n, t, what):
-    """A tensor of tokens must hold [n, t] of them (one sequence: at least t)."""
+def _arr(x, shape, size, what):
+    """The address of a dense array [shape] of `size`-byte elements, or the raw
+    address given.  The kernels take no strides: a view of another layout, or a
+    tensor of another shape, would be read or written elsewhere."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.shape != shape or not x.is_contiguous() or x.element_size() != size:
+        _check_layout(x, shape, size, what)
+    return x.data_ptr()
+
+
+def _check_layout(x, shape, size, what):
+    """A tensor that is not simply [shape] may be flat, longer along its first axis
+    (past axes of one entry), or have axes split or merged before the last."""
+    need = 1
+    for n in shape:
+        need *= n
+    rank, lead = x.dim(), next((i for i, n in enumerate(shape) if n != 1), len(shape) - 1)
+    longer = rank == len(shape) and x.shape[:lead] == shape[:lead] \
+        and x.shape[lead + 1:] == shape[lead + 1:]
+    regrouped = rank != len(shape) and x.numel() == need and x.shape[-1:] == shape[-1:]
+    if not x.is_contiguous() or x.element_size() != size or x.numel() < need \
+            or not (rank <= 1 or longer or regrouped):
+        raise ValueError(f"{what}: expected a contiguous {shape} of {size}-byte elements, got "
+                         f"{tuple(x.shape)} with strides {x.stride()}, {x.element_size()} bytes each")
+
+
+def _check_tokens(x, n, t, h, d, what):
+    """A tensor of tokens must hold [n, t] of them (one sequence: at least t) of h
+    heads of d bf16 channels."""
     if x is not None and not isinstance(x, int):
         if x.shape[0] != n or (x.shape[1] != t if n > 1 else x.shape[1] < t):
             raise ValueError(f"{what}: {tuple(x.shape[:2])} tokens, the call has {(n, t)}")
+        if x.shape[2:] != (h, d) or x.element_size() != 2:
+            raise ValueError(f"{what}: tokens of {tuple(x.shape[2:])}, {x.element_size()} bytes each, "
+                             f"the call has {(h, d)} of 2")
 
 
 def _kv4_arg(cache, d):
@@ -495,13 +526,21 @@ def herald_kv4_append(d, T, q, k, v, ctx_len, cache, q_rot, k_rot, rope=None, n_
     """cache: a Kv4 or None (rotate only); rope: a Rope or None.  The token
     strides of q, k, v [N, T, heads, d] are taken from the tensors (views of a
     fused projection's output) unless given."""
-    for x, ld, what in ((q, q_ld, "q"), (k, k_ld, "k"), (v, v_ld, "v")):
-        if ld is None:
-            _check_tokens(x, d.N, T, what)
+    N, T, Hq, Hkv, ch = d.N, int(T), d.Hq, d.Hkv, d.d
+    if q_ld is None:
+        _check_tokens(q, N, T, Hq, ch, "q")
+    if k_ld is None:
+        _check_tokens(k, N, T, Hkv, ch, "k")
+    if v_ld is None:
+        _check_tokens(v, N, T, Hkv, ch, "v")
+    if pooled is not None and Bk > 0:
+        pooled = _arr(pooled, (N, Hkv, -(-d.L_max // int(Bk)), ch), 4, "pooled")
     _check(lib().herald_kv4_append(
-        d, int(T), _p(n_tok), _p(q), _token_ld(q, q_ld, "q"), _p(k), _token_ld(k, k_ld, "k"),
-        _p(v), _token_ld(v, v_ld, "v"), None if rope is None else C.byref(rope), _p(ctx_len),
-        _kv4_arg(cache, d), _p(q_rot), _p(k_rot), _p(pooled), int(Bk), int(flags), _s(stream)))
+        d, T, _arr(n_tok, (N,), 4, "n_tok"), _p(q), _token_ld(q, q_ld, "q"), _p(k),
+        _token_ld(k, k_ld, "k"), _p(v), _token_ld(v, v_ld, "v"),
+        None if rope is None else C.byref(rope), _arr(ctx_len, (N,), 4, "ctx_len"),
+        _kv4_arg(cache, d), _arr(q_rot, (N, T, Hq, ch), 2, "q_rot"),
+        _arr(k_rot, (N, T, Hkv, ch), 2, "k_rot"), _p(pooled), int(Bk), int(flags), _s(stream)))
 
 
 def herald_workspace_size_kv4(d: Dims) -> int:
@@ -511,15 +550,21 @@ def herald_workspace_size_kv4(d: Dims) -> int:
 def herald_kv4_attn(d, q, cache, ctx_len, block_k, block_v, out, scale=0.0, ws=None,
                     ws_bytes=None, stream=None):
     """Attention over a paged 4-bit cache (a Kv4) and, unless both are None,
-    the block's own keys and values."""
-    _check(lib().herald_kv4_attn(d, _p(q), _kv4_arg(cache, d), _p(ctx_len), _p(block_k),
-                                 _p(block_v), _p(out), float(scale), _p(ws), _nbytes(ws, ws_bytes),
-                                 _s(stream)))
+    the block's own keys and values; every tensor dense, as in include/herald.h."""
+    N, B, Hkv, ch = d.N, d.B, d.Hkv, d.d
+    queries, keys = (N, B, d.Hq, ch), (N, B, Hkv, ch)
+    _check(lib().herald_kv4_attn(d, _arr(q, queries, 2, "q"), _kv4_arg(cache, d),
+                                 _arr(ctx_len, (N,), 4, "ctx_len"), _arr(block_k, keys, 2, "block_k"),
+                                 _arr(block_v, keys, 2, "block_v"), _arr(out, queries, 2, "out"),
+                                 float(scale), _p(ws), _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def herald_kv4_gather(d, idx, n_sel, P_max, cache, pool_k, pool_v=None, stream=None):
-    _check(lib().herald_kv4_gather(d, _p(idx), _p(n_sel), int(P_max), _kv4_arg(cache, d),
-                                   _p(pool_k), _p(pool_v), _s(stream)))
+    rows = (d.N, d.Hkv, int(P_max))
+    pool = rows + (d.d,)
+    _check(lib().herald_kv4_gather(d, _arr(idx, rows, 4, "idx"), _arr(n_sel, rows[:2], 4, "n_sel"),
+                                   int(P_max), _kv4_arg(cache, d), _arr(pool_k, pool, 2, "pool_k"),
+                                   _arr(pool_v, pool, 2, "pool_v"), _s(stream)))
 
 
 class Trace:

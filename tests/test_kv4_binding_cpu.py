@@ -1,6 +1,8 @@
 """What the binding of the paged 4-bit cache's calls refuses before any of
 them reaches the library: tensors that would be read or written elsewhere than
 where they lie."""
+import os
+
 import pytest
 
 from block_diffusion_sparse_gb300 import herald as H
@@ -60,3 +62,82 @@ def test_caches_of_another_shape_are_refused(other):
                  lambda: H.herald_kv4_gather(d, OK, OK, 8, c, OK)):
         with pytest.raises(ValueError, match="cache"):
             call()
+
+
+def _bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def _i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def _attn(**over):
+    d = H.dims(2, 8, 2, 64, 3, 64)
+    a = dict(q=_bf16(2, 3, 8, 64), ctx=_i32(2), bk=_bf16(2, 3, 2, 64), bv=_bf16(2, 3, 2, 64),
+             out=_bf16(2, 3, 8, 64))
+    a.update(over)
+    # (no workspace: what passes the binding is refused by the library)
+    H.herald_kv4_attn(d, a["q"], _cache(), a["ctx"], a["bk"], a["bv"], a["out"], ws=0, ws_bytes=0)
+
+
+def _gather(**over):
+    a = dict(idx=_i32(2, 2, 5), n_sel=_i32(2, 2), pk=_bf16(2, 2, 5, 64), pv=_bf16(2, 2, 5, 64))
+    a.update(over)
+    H.herald_kv4_gather(H.dims(2, 8, 2, 64, 1, 1 << 20), a["idx"], a["n_sel"], 5, _cache(), a["pk"], a["pv"])
+
+
+def _append(**over):
+    a = dict(q=_bf16(2, 3, 8, 64), k=_bf16(2, 3, 2, 64), v=_bf16(2, 3, 2, 64), ctx=_i32(2),
+             n_tok=_i32(2), q_rot=_bf16(2, 3, 8, 64), k_rot=_bf16(2, 3, 2, 64),
+             pooled=torch.zeros(2, 2, 4, 64))
+    a.update(over)
+    H.herald_kv4_append(H.dims(2, 8, 2, 64, 1, 64), 3, a["q"], a["k"], a["v"], a["ctx"], _cache(),
+                        a["q_rot"], a["k_rot"], None, a["n_tok"], a["pooled"], 16, flags=1 << 9)
+
+
+_qkv = _bf16(2, 3, 12, 64)  # a fused projection's output
+MISFITS = [
+    (_attn, dict(q=_qkv[:, :, :8])), (_attn, dict(bv=_qkv[:, :, 10:])),
+    (_attn, dict(bk=_qkv[:, :, 8:10])), (_attn, dict(q=_bf16(2, 8, 3, 64))),
+    (_attn, dict(q=_bf16(2, 3, 8, 64).float())), (_attn, dict(out=_bf16(2, 3, 4, 64))),
+    (_attn, dict(bk=_bf16(2, 1, 2, 64).expand(2, 3, 2, 64))), (_attn, dict(ctx=_i32(1))),
+    (_attn, dict(ctx=_i32(2).long())), (_attn, dict(out=_bf16(2, 8, 3, 64).transpose(1, 2))),
+    (_gather, dict(idx=_i32(2, 2, 4))), (_gather, dict(idx=_i32(2, 2, 6))),
+    (_gather, dict(n_sel=_i32(2))), (_gather, dict(pk=_bf16(2, 2, 5, 128))),
+    (_gather, dict(pv=_bf16(2, 2, 10, 64)[:, :, ::2])), (_gather, dict(idx=_i32(2, 2, 5).long())),
+    (_append, dict(q_rot=_qkv[:, :, :8])), (_append, dict(k_rot=_bf16(2, 2, 3, 64))),
+    (_append, dict(q=_qkv[:, :, :7])), (_append, dict(k=_qkv[:, :, 8:])),
+    (_append, dict(v=_bf16(2, 3, 2, 64).float())), (_append, dict(n_tok=_i32(1))),
+    (_append, dict(ctx=_i32(1))), (_append, dict(pooled=torch.zeros(2, 2, 3, 64))),
+    (_append, dict(pooled=_bf16(2, 2, 4, 64))), (_append, dict(q_rot=_bf16(2, 2, 8, 64))),
+]
+
+
+@pytest.mark.parametrize("call,over", MISFITS,
+                         ids=[f"{c.__name__}-{next(iter(o))}-{i}" for i, (c, o) in enumerate(MISFITS)])
+def test_tensors_of_another_layout_are_refused(call, over):
+    """The kernels take dense arrays of the call's shape; anything else would be
+    read or written elsewhere than where it lies."""
+    with pytest.raises(ValueError, match=next(iter(over)).replace("bk", "block_k").replace("bv", "block_v")
+                       .replace("pk", "pool_k").replace("pv", "pool_v")):
+        call(**over)
+
+
+@pytest.mark.parametrize("call,over", [
+    (_attn, {}), (_gather, {}), (_append, {}), (_attn, dict(q=OK, bk=OK, bv=OK, out=OK, ctx=OK)),
+    (_attn, dict(q=_bf16(6, 8, 64), out=_bf16(2, 3, 2, 4, 64))),   # axes merged, axes split
+    (_attn, dict(q=_bf16(5000), ctx=_i32(7))),                     # flat and longer
+    (_attn, dict(out=_bf16(3, 3, 8, 64), bk=None, bv=None)),       # more sequences behind
+    (_gather, dict(pv=None, n_sel=_i32(4))),
+    (_append, dict(q=_qkv[:, :, :8], k=_qkv[:, :, 8:10], v=_qkv[:, :, 10:], n_tok=None, pooled=None)),
+], ids=str)
+def test_dense_tensors_and_addresses_reach_the_library(call, over):
+    """What has the call's layout passes the binding; the library then refuses the
+    missing workspace, the short table or the unknown flag."""
+    if not os.path.exists(H.LIB_PATH):
+        from block_diffusion_sparse_gb300 import build
+        build.build()
+    with pytest.raises(H.HeraldError) as e:
+        call(**over)
+    assert e.value.status == 1 and any(w in str(e.value) for w in ("ws", "max_pages", "flags")), e.value
