@@ -680,6 +680,16 @@ static herald_status check_ld(const char* name, int64_t* ld, int64_t row) {
   return HERALD_OK;
 }
 
+// The bytes that `toks` rows of `width` bf16 elements, `ld` elements apart, lie in.
+struct Span {
+  uintptr_t begin, end;
+};
+static Span rows_span(const uint16_t* p, int64_t toks, int64_t ld, int64_t width) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return p ? Span{a, a + uintptr_t((toks - 1) * ld + width) * 2} : Span{0, 0};
+}
+static bool overlap(const Span& a, const Span& b) { return a.begin < b.end && b.begin < a.end; }
+
 herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, const uint16_t* q,
                                 int64_t q_ld, const uint16_t* k, int64_t k_ld, const uint16_t* v,
                                 int64_t v_ld, const herald_rope* rope, int32_t* ctx_len,
@@ -735,8 +745,16 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
     if (rope->interleaved != 0 && rope->interleaved != 1)
       return fail(HERALD_ERR_INVALID_ARG, "interleaved=%d not 0 or 1", rope->interleaved);
   }
-  if ((q && (q_rot == k || (cache && q_rot == v) || q_rot == k_rot)) ||
-      (k_rot && (k_rot == q || (cache && k_rot == v))))
+  // An output may be its own input, row for row; lying over anything else that the
+  // call reads or writes it would change rows that others have yet to read.
+  const int64_t toks = int64_t(dims.N) * T, qw = int64_t(dims.Hq) * dims.d,
+                kw = int64_t(dims.Hkv) * dims.d;
+  const Span sq = rows_span(q, toks, q_ld, qw), sk = rows_span(k, toks, k_ld, kw),
+             sv = rows_span(cache ? v : nullptr, toks, v_ld, kw),
+             oq = rows_span(q ? q_rot : nullptr, toks, qw, qw),
+             ok = rows_span(k ? k_rot : nullptr, toks, kw, kw);
+  if ((q != q_rot && overlap(oq, sq)) || overlap(oq, sk) || overlap(oq, sv) || overlap(oq, ok) ||
+      (k != k_rot && overlap(ok, sk)) || overlap(ok, sq) || overlap(ok, sv))
     return fail(HERALD_ERR_INVALID_ARG,
                 "q_rot and k_rot may lie over q and k only, each over its own");
   HERALD_TRY_CUDA(launch_kv4_append(dims, T, n_tok, q, q_ld, k, k_ld, v, v_ld, rope, ctx_len,

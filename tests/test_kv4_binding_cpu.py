@@ -141,3 +141,25 @@ def test_dense_tensors_and_addresses_reach_the_library(call, over):
     with pytest.raises(H.HeraldError) as e:
         call(**over)
     assert e.value.status == 1 and any(w in str(e.value) for w in ("ws", "max_pages", "flags")), e.value
+
+
+@pytest.mark.parametrize("over", [
+    dict(q_rot=lambda a: a["q"] + 256), dict(q_rot=lambda a: a["q"] - 256),
+    dict(q_rot=lambda a: a["k"] + 256), dict(q_rot=lambda a: a["v"] - 16),
+    dict(k_rot=lambda a: a["k"] + 16), dict(k_rot=lambda a: a["q"] + 512),
+    dict(k_rot=lambda a: a["v"] - 16), dict(q_rot=lambda a: a["k_rot"] - 16),
+    dict(q_rot=lambda a: a["k_rot"] + 16),
+    # slices of one buffer: queries of the last token end behind the first keys
+    dict(k=lambda a: a["q"] + 2048, v=lambda a: a["q"] + 2560, q_ld=1536, k_ld=1536, v_ld=1536,
+         k_rot=lambda a: a["q"] + 4096)], ids=lambda o: "-".join(o))
+def test_append_outputs_partly_over_other_arrays_are_refused(over):
+    """Not only equal addresses: a rotated output that begins inside an array the
+    call reads would change rows before they are read."""
+    a = dict(q=1 << 20, k=2 << 20, v=3 << 20, q_rot=4 << 20, k_rot=5 << 20, q_ld=0, k_ld=0, v_ld=0)
+    for name, at in over.items():
+        a[name] = at(a) if callable(at) else at
+    cache = H.Kv4(64, 40, 32, OK, OK, OK, OK, OK, 1.0, 1.0)
+    with pytest.raises(H.HeraldError, match="q_rot and k_rot") as e:
+        H.herald_kv4_append(H.dims(2, 8, 2, 128, 4, 2048), 4, a["q"], a["k"], a["v"], OK, cache,
+                            a["q_rot"], a["k_rot"], q_ld=a["q_ld"], k_ld=a["k_ld"], v_ld=a["v_ld"])
+    assert e.value.status == 1
