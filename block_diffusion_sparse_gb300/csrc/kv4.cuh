@@ -67,6 +67,15 @@ HERALD_DEV void kv4_query_scale(float mx, float sc, float* up, float* f) {
   *f = fminf(fmaxf(sc * 1.4426950408889634f * down, FLT_MIN), FLT_MAX);
 }
 
+// Scores s f whose fp32 steps are no longer small beside the distance of a base m
+// from its row's largest score (log2 units).  2^(s f - m) takes the product exactly
+// (one fma), but m stands on the fp32 grid: rounded to nearest it may lie steps above
+// every score (all weights 0) or far enough below for P to pass fp16's range.
+// Past this size the base is rounded down and 2^(s f - m) ends at P's largest value:
+// keys within a step or so of the largest score, which fp32 holds to no more than
+// that, weigh alike.  (Without it scores past 2^26 gave NaN.)
+constexpr float kKv4Far = 0x1p20f;
+
 // ---- attention arguments shared by its kernels
 struct Kv4AttnArgs {
   const uint16_t *q, *bk, *bv;

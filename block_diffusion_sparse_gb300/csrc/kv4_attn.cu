@@ -284,10 +284,12 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float b = fmaxf(s[nt][i] * f[nt][i], s[nt][i + 2] * f[nt][i]);
+              float mx = fmaxf(s[nt][i], s[nt][i + 2]);
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
-              b = fmaxf(m[nt][i], b - kKv4Below);
+              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              float b = mx * f[nt][i];
+              b = fabsf(b) > kKv4Far ? __fadd_rd(__fmul_rd(mx, f[nt][i]), -kKv4Below) : b - kKv4Below;
+              b = fmaxf(m[nt][i], b);
               const float w = fast_exp2(m[nt][i] - b);
               m[nt][i] = b;
               l[nt][i] *= w;
@@ -296,8 +298,11 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
                 o[nt][k][i] *= w;
                 o[nt][k][i + 2] *= w;
               }
-              x[nt][i] = fmaf(s[nt][i], f[nt][i], -b);
-              x[nt][i + 2] = fmaf(s[nt][i + 2], f[nt][i], -b);
+#pragma unroll
+              for (int j = i; j < 4; j += 2) {
+                x[nt][j] = fmaf(s[nt][j], f[nt][i], -b);
+                if (x[nt][j] > kKv4Above) x[nt][j] = kKv4Above;  // (kKv4Far; a NaN stays)
+              }
             }
         }
 #pragma unroll

@@ -63,6 +63,7 @@ constexpr int kTcSoft = 256;               // softmax threads
 constexpr int kTcThreadsAll = 768;         // 8 + 8 + 8 warps (22, 23 only fill a warpgroup)
 constexpr int kTcSWarp = 16, kTcCopyWarp = 17, kTcPvWarp = 20;  // S 16, 18; copies 17, 19; P V 20, 21
 constexpr float kTcBelow = 5.f, kTcTop = 60000.f;  // base of P and largest sum (see above)
+constexpr float kTcTopLog2 = 15.8727f;
 
 // Waits of the kernel (bits 16-31 of the error word).
 enum : uint32_t {
@@ -362,20 +363,20 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                 mask_scores(ts, msk, keys - k0);
               }
               float p[32], s0, s1;
+              uint64_t fx = f2, nmx = f2_pack(-m, -m);  // P = 2^(score fx + nmx)
               bool again = false;
               while (true) {
                 bool high = true;
                 if (any || again) {  // (a piece's first step has no base yet)
-                  const uint64_t nm2 = f2_pack(-m, -m);
                   uint64_t sum = f2_pack(0.f, 0.f);
                   uint32_t x[32], y[32];
                   tmem_ld32_nowait(ts, x);
                   tmem_ld32_nowait(ts + 32u, y);
                   tmem_wait_ld(x);
                   tmem_wait_ld(y);
-                  exp32(x, f2, nm2, &sum);
+                  exp32(x, fx, nmx, &sum);
                   pack_p32(reinterpret_cast<uint32_t*>(p), x, blk, iv);
-                  exp32(y, f2, nm2, &sum);
+                  exp32(y, fx, nmx, &sum);
                   pack_p32(reinterpret_cast<uint32_t*>(p) + 16, y, blk, iv);
                   f2_unpack(sum, s0, s1);
                   high = !(s0 + s1 <= kTcTop);
@@ -393,11 +394,32 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                     mx = fmax3f(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                 }
                 float k = 1.f;
+                const bool far = fabsf(mx * f) > kKv4Far;
                 if (high && mx * f - m > kTcBelow) {
-                  const float nb = mx * f - kTcBelow;
+                  const float nb =
+                      far ? __fadd_rd(__fmul_rd(mx, f), -kTcBelow) : mx * f - kTcBelow;
                   k = fast_exp2(m - nb);
                   m = nb;
                   l *= k;
+                }
+                nmx = f2_pack(-m, -m);
+                if (__any_sync(0xffffffffu, far)) {  // exponents in the scores' place (kKv4Far)
+#pragma unroll 1
+                  for (int c = 0; c < 2; ++c) {
+                    uint32_t x[32];
+                    tmem_ld32_nowait(ts + uint32_t(c) * 32u, x);
+                    tmem_wait_ld(x);
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                      v[i] = __uint_as_float(x[i]);
+                      const float t = fmaf(v[i], f, -m);
+                      if (far) v[i] = t > kTcTopLog2 ? kTcTopLog2 : t;  // (a NaN stays)
+                    }
+                    tmem_st32(ts + uint32_t(c) * 32u, v);
+                  }
+                  tmem_wait_st();
+                  if (far) fx = f2_pack(1.f, 1.f), nmx = f2_pack(0.f, 0.f);
                 }
                 // O so far, once the P V of the step before is in it (that of two
                 // steps before is: this step's scores took its buffer)

@@ -1,6 +1,7 @@
-"""The paged 4-bit cache's attention where its keys have holes or NaN: missing
-pages beside block keys and NaN scales, in every kernel variant (query rows per
-KV head up to 8, 16, 128, 256)."""
+"""The paged 4-bit cache's attention where its numbers are extreme or its keys
+have holes: scores past what fp32 resolves, NaN values, missing pages beside
+block keys, and every kernel variant (query rows per KV head up to 8, 16, 128,
+256)."""
 import numpy as np
 import pytest
 
@@ -63,3 +64,73 @@ def test_nan_scales_reach_their_head_only(B, kv):
     if kv == 0:
         bad[0, :, 4:] = True
     assert np.isnan(got[bad]).all() and np.isfinite(got[~bad]).all()
+
+
+def rows_of_sign(rng, L, Hkv, d, top, high):
+    """Keys c w per position (w of +-1 per head): c = 6 at the positions `top`
+    (of 1/4 where not `high`), else one of 1 to 4.  Returns keys [L, Hkv, d] and w."""
+    w = rng.choice([-1.0, 1.0], (Hkv, d)).astype(np.float32)
+    c = rng.integers(1, 5, L).astype(np.float32)
+    c[top] = 6 if high else 0.25
+    return c[:, None, None] * w, w
+
+
+@pytest.mark.parametrize("B", BLOCKS)
+@pytest.mark.parametrize("size", [2.0 ** 14, 2.0 ** 22, 2.0 ** 28, 2.0 ** 34])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_past_what_fp32_resolves(B, size, sign):
+    """Scores up to 2^41, whose fp32 steps are 2^17: two equal keys far above all
+    others, in different tiles, share the weight; rows of ordinary queries beside
+    them and the sign of the scores change nothing.  The others' weights are zero
+    (the next score is at least 0.3 of the largest below it); the two have bitwise
+    equal scores, so that the result is the mean of their values: off by its own
+    rounding (2^-8), P's in fp16 against the row sum (2^-11) and fp32 sums (2^-13)."""
+    rng = np.random.default_rng(int(np.log2(size)) + B)
+    N, Hq, Hkv, d, L = 2, 8, 2, 128, 1500
+    top = [77, 1203]
+    c = ref.Cache(rng, N, Hkv, d, 64, [L, L])
+    v = rng.standard_normal((N, L, Hkv, d)).astype(np.float32)
+    ws = []
+    for n in range(N):
+        k, w = rows_of_sign(rng, L, Hkv, d, top, sign > 0)
+        c.write(n, np.arange(L), k, v[n])
+        ws.append(w)
+    q = rng.standard_normal((N, B, Hq, d)).astype(np.float32)
+    huge = rng.random((N, B, Hq)) < 0.5
+    huge[0, 0, 0], huge[1, -1, -1] = True, False
+    far = np.repeat(np.stack(ws), Hq // Hkv, 1)[:, None] * np.float32(sign * size)
+    q = np.where(huge[..., None], far, q)
+    q = ref.bf16(q)
+    want, tol = ref.attention(q, c, [L, L])
+    for n in range(N):
+        rows = c.rows(1, n, top)              # [Hkv, 2, d]
+        mean = np.repeat(rows.mean(1), Hq // Hkv, 0)
+        mag = np.repeat(np.abs(rows).mean(1), Hq // Hkv, 0)
+        for h in range(Hq):
+            at = huge[n, :, h]
+            want[n, at, h] = mean[h]
+            tol[n, at, h] = 2.0 ** -8 * np.abs(mean[h]) + (2.0 ** -11 + 2.0 ** -13) * mag[h]
+    check(run_attn(c, q, [L, L], B, L), want, tol, f"size {size} sign {sign}")
+
+
+@pytest.mark.parametrize("B", BLOCKS)
+@pytest.mark.parametrize("size", [2.0 ** 14, 2.0 ** 24, 2.0 ** 30])
+def test_block_scores_past_what_fp32_resolves(B, size):
+    """The same where a key of the block stands above all others."""
+    rng = np.random.default_rng(int(np.log2(size)) + B)
+    N, Hq, Hkv, d, L = 2, 8, 2, 128, 700
+    c = ref.Cache(rng, N, Hkv, d, 64, [L, L], v_scale=0.25)
+    q = np.zeros((N, B, Hq, d), np.float32)
+    bk, bv = np.zeros((N, B, Hkv, d), np.float32), rng.standard_normal((N, B, Hkv, d))
+    at = B // 2
+    for n in range(N):
+        k, w = rows_of_sign(rng, L, Hkv, d, [], True)
+        c.write(n, np.arange(L), k, rng.standard_normal((L, Hkv, d)).astype(np.float32))
+        q[n] = np.repeat(w, Hq // Hkv, 0) * np.float32(size)
+        bk[n] = w * rng.integers(1, 5, B)[:, None, None]
+        bk[n, at] = w * 8
+    bv = ref.bf16(bv)
+    got = run_attn(c, ref.bf16(q), [L, L], B, L, ref.bf16(bk), bv)
+    want = np.broadcast_to(np.repeat(ref.f64(bv)[:, at], Hq // Hkv, 1)[:, None], got.shape)
+    # its own rounding; P in bf16 (2^-8) against the row sum
+    check(got, want, (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -13) * np.abs(want), f"size {size}")
