@@ -787,8 +787,8 @@ herald_status herald_kv4_attn(herald_dims dims, const uint16_t* q, const herald_
     HERALD_CHECK_PTR(block_k);
     HERALD_CHECK_PTR(block_v);
   }
-  if (!(scale >= 0.f) || !isfinite(scale))
-    return fail(HERALD_ERR_INVALID_ARG, "scale=%g must be finite and >= 0", double(scale));
+  if (!(scale >= 0.f && scale <= 0x1p127f))  // (times log2(e) it has to be finite)
+    return fail(HERALD_ERR_INVALID_ARG, "scale=%g outside [0, 2^127]", double(scale));
   const size_t need = kv4_attn_workspace(dims);
   if (ws_bytes < need)
     return fail(HERALD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);

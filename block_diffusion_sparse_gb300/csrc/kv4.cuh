@@ -56,15 +56,15 @@ HERALD_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
 
 // A query row as fp16: values are multiplied by *up, the power of two that
 // brings the row's largest magnitude mx to [2^14, 2^15), and *f turns a product
-// with the codes * scales of a key into a log2-unit score; sc = the softmax scale
-// times k_scale.  (mx below 2^-112 counts as that, infinities as 2^127; *f stays
-// positive and finite: a masked score of -inf times 0, or a zero score times
-// inf, would be NaN.)
-HERALD_DEV void kv4_query_scale(float mx, float sc, float* up, float* f) {
+// with the codes * scales of a key into a log2-unit score; the softmax scale times
+// k_scale times log2(e) is sc 2^sc_e with sc in [1, 2) (its own exponent: either
+// factor may be near the ends of fp32 where the scores are not).  (mx below 2^-112
+// counts as that, infinities as 2^127; *f stays positive and finite: a masked score
+// of -inf times 0, or a zero score times inf, would be NaN.)
+HERALD_DEV void kv4_query_scale(float mx, float sc, int sc_e, float* up, float* f) {
   const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -112), 127);
   *up = __uint_as_float(uint32_t(14 - e + 127) << 23);
-  const float down = __uint_as_float(uint32_t(e - 14 + 127) << 23);
-  *f = fminf(fmaxf(sc * 1.4426950408889634f * down, FLT_MIN), FLT_MAX);
+  *f = sc * __uint_as_float(uint32_t(min(max(sc_e + e - 14, -126), 127) + 127) << 23);
 }
 
 // Scores s f whose fp32 steps are no longer small beside the distance of a base m
@@ -83,7 +83,9 @@ struct Kv4AttnArgs {
   uint16_t* out;
   float* opart;  // [slots][D/4][R16][4]
   float2* ml;    // [slots][R16]
-  float scale;
+  float scale;   // of the block's keys' scores
+  float sc;      // of the cache's keys' (kv4_query_scale)
+  int sc_e;
   int N, Hq, Hkv, B, L_max, R16, ctas;
   int pad;       // what a piece costs beside its tiles, in tiles (kv4_units)
   Kv4Dev c;

@@ -39,6 +39,7 @@
 // down to 2^-25 of the largest keep 11 bits, and most tiles need one vote and
 // no exchange between lanes.
 #include <float.h>
+#include <math.h>
 
 #include "kv4.cuh"
 
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         float up, f;
-        kv4_query_scale(mx, a.scale * a.c.k_scale, &up, &f);
+        kv4_query_scale(mx, a.sc, a.sc_e, &up, &f);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
         float f[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          f[nt][0] = f[nt][1] = fminf(a.scale * 1.4426950408889634f, FLT_MAX);
+          f[nt][0] = f[nt][1] = a.scale * 1.4426950408889634f;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (key_s + 8 * (i >> 1) >= a.B) s[nt][i] = -INFINITY;
@@ -676,6 +677,10 @@ cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4D
   a.ml = reinterpret_cast<float2*>(p + w.ml);
   a.opart = reinterpret_cast<float*>(p + w.opart);
   a.scale = scale;
+  int es, ek, ep;
+  const float ms = frexpf(scale, &es), mk = frexpf(c.k_scale, &ek);
+  a.sc = 2.f * frexpf(ms * mk * 1.4426950408889634f, &ep);
+  a.sc_e = es + ek + ep - 1;
   a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max, a.R16 = w.R16;
   a.c = c;
   const bool tc = R > kKv4MmaRows;

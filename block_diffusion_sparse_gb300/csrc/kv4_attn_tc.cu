@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                              x4[i][1].x, x4[i][1].y, x4[i][1].z, x4[i][1].w};
             if (!blk) {  // fp16 scaled per row by a power of two (see kv4_attn.cu)
               float up, f;
-              kv4_query_scale(mx[i], a.scale * a.c.k_scale, &up, &f);
+              kv4_query_scale(mx[i], a.sc, a.sc_e, &up, &f);
 #pragma unroll
               for (int k = 0; k < 8; ++k) x[k] = pack_half2(bf16lo(x[k]) * up, bf16hi(x[k]) * up);
               if (c == 0) row_f[mt2 * kTileM + rr] = f;
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full);
         if (!wait(&q_full, phase & 1, W_Q_FULL)) return false;
-        const float f = blk ? fminf(a.scale * 1.4426950408889634f, FLT_MAX)
+        const float f = blk ? a.scale * 1.4426950408889634f
                             : *(volatile float*)&row_f[row];
         const uint64_t f2 = f2_pack(f, f);
         mbar_arrive(&q_free);  // (this thread has read its factor of the phase)

@@ -568,7 +568,7 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t *n_tok, c
  *   q        [N][B][Hq][d] bf16 device     out  [N][B][Hq][d] bf16 device out
  *   ctx_len  [N] int32 device
  *   block_k, block_v  [N][B][Hkv][d] bf16 device, or both NULL
- *   scale    softmax scale; 0 selects 1/sqrt(d)
+ *   scale    softmax scale, at most 2^127; 0 selects 1/sqrt(d)
  *   ws       herald_workspace_size_kv4(dims) bytes (0 = unsupported shape)
  * N*Hkv <= 65535, L_max <= 2^30.  Results do not depend on other calls or on timing. */
 size_t herald_workspace_size_kv4(herald_dims dims);

@@ -134,3 +134,18 @@ def test_block_scores_past_what_fp32_resolves(B, size):
     want = np.broadcast_to(np.repeat(ref.f64(bv)[:, at], Hq // Hkv, 1)[:, None], got.shape)
     # its own rounding; P in bf16 (2^-8) against the row sum
     check(got, want, (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -13) * np.abs(want), f"size {size}")
+
+
+@pytest.mark.parametrize("B", BLOCKS)
+def test_scale_and_cache_factor_past_fp32_together(B):
+    """The softmax scale times the cache's factor is past fp32's largest number, the
+    scores are ordinary."""
+    rng = np.random.default_rng(50 + B)
+    N, Hq, Hkv, d, L = 1, 8, 2, 128, 500
+    c = ref.Cache(rng, N, Hkv, d, 64, [L], k_scale=2.0 ** 60)
+    k = rng.standard_normal((L, Hkv, d)) * 2.0 ** 53
+    c.write(0, np.arange(L), k.astype(np.float32), rng.standard_normal((L, Hkv, d)).astype(np.float32))
+    q = ref.bf16((rng.standard_normal((N, B, Hq, d)) * 2.0 ** -124).astype(np.float32))
+    want, tol = ref.attention(q, c, [L], scale=2.0 ** 69)
+    assert np.abs(want - c.rows(1, 0, np.arange(L)).mean(1).repeat(4, 0)).max() > 0.1  # not uniform
+    check(run_attn(c, q, [L], B, L, scale=2.0 ** 69), want, tol, "scales")

@@ -163,3 +163,11 @@ def test_append_outputs_partly_over_other_arrays_are_refused(over):
         H.herald_kv4_append(H.dims(2, 8, 2, 128, 4, 2048), 4, a["q"], a["k"], a["v"], OK, cache,
                             a["q_rot"], a["k_rot"], q_ld=a["q_ld"], k_ld=a["k_ld"], v_ld=a["v_ld"])
     assert e.value.status == 1
+
+
+def test_scales_without_a_finite_base_2_form_are_refused():
+    d = H.dims(2, 8, 2, 128, 4, 2048)
+    cache = H.Kv4(64, 40, 32, OK, OK, OK, OK, OK, 1.0, 1.0)
+    with pytest.raises(H.HeraldError, match="scale") as e:
+        H.herald_kv4_attn(d, OK, cache, OK, None, None, OK, 3e38, OK, H.herald_workspace_size_kv4(d))
+    assert e.value.status == 1
