@@ -363,20 +363,21 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                 mask_scores(ts, msk, keys - k0);
               }
               float p[32], s0, s1;
-              uint64_t fx = f2, nmx = f2_pack(-m, -m);  // P = 2^(score fx + nmx)
+              float nm = -m;  // P = 2^(score f + nm)
               bool again = false;
               while (true) {
                 bool high = true;
                 if (any || again) {  // (a piece's first step has no base yet)
+                  const uint64_t nm2 = f2_pack(nm, nm);
                   uint64_t sum = f2_pack(0.f, 0.f);
                   uint32_t x[32], y[32];
                   tmem_ld32_nowait(ts, x);
                   tmem_ld32_nowait(ts + 32u, y);
                   tmem_wait_ld(x);
                   tmem_wait_ld(y);
-                  exp32(x, fx, nmx, &sum);
+                  exp32(x, f2, nm2, &sum);
                   pack_p32(reinterpret_cast<uint32_t*>(p), x, blk, iv);
-                  exp32(y, fx, nmx, &sum);
+                  exp32(y, f2, nm2, &sum);
                   pack_p32(reinterpret_cast<uint32_t*>(p) + 16, y, blk, iv);
                   f2_unpack(sum, s0, s1);
                   high = !(s0 + s1 <= kTcTop);
@@ -402,8 +403,9 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                   m = nb;
                   l *= k;
                 }
-                nmx = f2_pack(-m, -m);
-                if (__any_sync(0xffffffffu, far)) {  // exponents in the scores' place (kKv4Far)
+                nm = -m;
+                if (__any_sync(0xffffffffu, far)) {  // P's exponents over f as scores (kKv4Far)
+                  const float per_f = 1.f / f;
 #pragma unroll 1
                   for (int c = 0; c < 2; ++c) {
                     uint32_t x[32];
@@ -414,12 +416,12 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                     for (int i = 0; i < 32; ++i) {
                       v[i] = __uint_as_float(x[i]);
                       const float t = fmaf(v[i], f, -m);
-                      if (far) v[i] = t > kTcTopLog2 ? kTcTopLog2 : t;  // (a NaN stays)
+                      if (far) v[i] = (t > kTcTopLog2 ? kTcTopLog2 : t) * per_f;  // (a NaN stays)
                     }
                     tmem_st32(ts + uint32_t(c) * 32u, v);
                   }
                   tmem_wait_st();
-                  if (far) fx = f2_pack(1.f, 1.f), nmx = f2_pack(0.f, 0.f);
+                  if (far) nm = 0.f;
                 }
                 // O so far, once the P V of the step before is in it (that of two
                 // steps before is: this step's scores took its buffer)
