@@ -67,6 +67,17 @@ HERALD_DEV void kv4_query_scale(float mx, float sc, int sc_e, float* up, float* 
   *f = sc * __uint_as_float(uint32_t(min(max(sc_e + e - 14, -126), 127) + 127) << 23);
 }
 
+// Weights of the block's own keys.  Their values are bf16 and an mma's operands have
+// one type, so P is bf16 too, as the sum of two numbers (the second what the first
+// left: 16 bits in all, beside fp16's 11 over the cache), each multiplied with V: with
+// one, 8 bits, a short context's output was off by up to 2^-8 of its weighted |values|
+// before its own rounding.
+HERALD_DEV uint32_t take_bf16(float& a, float& b) {  // a, b: left with the remainders
+  const uint32_t w = pack_bf16(a, b);
+  a -= bf16lo(w), b -= bf16hi(w);
+  return w;
+}
+
 // Scores s f whose fp32 steps are no longer small beside the distance of a base m
 // from its row's largest score (log2 units).  2^(s f - m) takes the product exactly
 // (one fma), but m stands on the fp32 grid: rounded to nearest it may lie steps above

@@ -367,20 +367,27 @@ __global__ void __launch_bounds__(kKv4Threads, NT == 1 ? 2 : 1)
         }
         probabilities(s, f);
         const float iv = 1.f / a.c.v_scale;
-        uint32_t p0[NT], p1[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          p0[nt] = transpose8x8(pack_bf16(s[nt][0] * iv, s[nt][1] * iv));
-          p1[nt] = transpose8x8(pack_bf16(s[nt][2] * iv, s[nt][3] * iv));
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i] *= iv;
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {  // P as the sum of two bf16 numbers
+          uint32_t p0[NT], p1[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            p0[nt] = transpose8x8(take_bf16(s[nt][0], s[nt][1]));
+            p1[nt] = transpose8x8(take_bf16(s[nt][2], s[nt][3]));
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k)  // channels lg*D/8 + 2k, + 2k+1 of each key
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_bf16(o[nt][k], __byte_perm(vw[0][k], vw[1][k], 0x5410),
+                       __byte_perm(vw[0][k], vw[1][k], 0x7632),
+                       __byte_perm(vw[2][k], vw[3][k], 0x5410),
+                       __byte_perm(vw[2][k], vw[3][k], 0x7632), p0[nt], p1[nt]);
         }
-#pragma unroll
-        for (int k = 0; k < KS; ++k)  // channels lg*D/8 + 2k, + 2k+1 of each key
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_bf16(o[nt][k], __byte_perm(vw[0][k], vw[1][k], 0x5410),
-                     __byte_perm(vw[0][k], vw[1][k], 0x7632),
-                     __byte_perm(vw[2][k], vw[3][k], 0x5410),
-                     __byte_perm(vw[2][k], vw[3][k], 0x7632), p0[nt], p1[nt]);
       }
 
       // ------------------------------------------------------ cache tiles

@@ -41,7 +41,8 @@
 //
 // The block's own keys are bf16: their tiles come first in a segment, with
 // the queries staged as bf16 (an mma's operands have one type), then the
-// queries are staged again as fp16 for the cache.
+// queries are staged again as fp16 for the cache.  P is bf16 there as well, two
+// numbers a weight (take_bf16): the scores' 64 columns have room for both.
 #include <float.h>
 
 #include "kv4.cuh"
@@ -156,7 +157,8 @@ HERALD_DEV void exp32(uint32_t (&x)[32], uint64_t f2, uint64_t nm2, uint64_t* su
   *sum = f2_add(sa, sb);
 }
 // 32 probabilities -> 16 packed columns.  blk: bf16, times iv (P in units of
-// v_scale: O has one unit for all keys), else fp16.
+// v_scale: O has one unit for all keys; the weights' first numbers, rest_of_p has
+// the second), else fp16.
 HERALD_DEV void pack_p32(uint32_t* pk, const uint32_t (&x)[32], bool blk, float iv) {
   if (blk) {
 #pragma unroll
@@ -166,6 +168,38 @@ HERALD_DEV void pack_p32(uint32_t* pk, const uint32_t (&x)[32], bool blk, float 
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       pk[i] = pack_half2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+  }
+}
+
+HERALD_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// The second numbers of a block step's weights, from its scores at ts once more, into
+// columns 32-63 (the second half's first: its own scores lie there; none without keys,
+// nk, in it).  Block steps are few:
+// kept beside P in the steps' common code these spilled registers, and blocks took 29.1
+// us at 32K and 120 at 4 x 64K instead of 28.5 and 118.4.  (With one number a weight
+// 27.9 and 117.1.)
+HERALD_DEV void rest_of_p(uint32_t ts, uint64_t f2, uint64_t nm2, float iv, int nk) {
+#pragma unroll 1
+  for (int c = nk > 32 ? 1 : 0; c >= 0; --c) {
+    uint32_t x[32], rest[16];
+    uint64_t sum = f2_pack(0.f, 0.f);
+    tmem_ld32_nowait(ts + uint32_t(c) * 32u, x);
+    tmem_wait_ld(x);
+    exp32(x, f2, nm2, &sum);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float a = __uint_as_float(x[2 * i]) * iv, b = __uint_as_float(x[2 * i + 1]) * iv;
+      take_bf16(a, b);
+      rest[i] = pack_bf16(a, b);
+    }
+    tmem_st16(ts + 32u + uint32_t(c) * 16u, rest);
   }
 }
 
@@ -441,6 +475,7 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
                   tmem_wait_st();
                 }
               }
+              if (blk) rest_of_p(ts, f2, f2_pack(nm, nm), iv, keys - k0);
               tmem_st32(ts, p);
               l += s0 + s1;
               tmem_wait_st();
@@ -776,6 +811,12 @@ __global__ void __launch_bounds__(kTcThreadsAll, 1)
               for (int ks = 0; ks < kTcStep / 16; ++ks)
                 umma_bf16_ts(to, ts + b * 64u + uint32_t(ks) * 8u, vt + uint32_t(ks) * 128u, ido,
                              ks > 0 ? 1u : acc);
+              if (u < blk_units) {  // P's second numbers, of the 32-key halves with keys
+#pragma unroll 1
+                for (int ks = 0; ks < (keys - k0 > 32 ? 4 : 2); ++ks)
+                  umma_bf16_ts(to, ts + b * 64u + 32u + uint32_t(ks) * 8u,
+                               vt + uint32_t(ks) * 128u, ido, 1u);
+              }
               umma_commit(&pv_done[w][b]);
               if (k0 + kTcStep >= keys) umma_commit(&buf_free[vb]);
             }

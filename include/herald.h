@@ -570,6 +570,8 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t *n_tok, c
  *   block_k, block_v  [N][B][Hkv][d] bf16 device, or both NULL
  *   scale    softmax scale, at most 2^127; 0 selects 1/sqrt(d)
  *   ws       herald_workspace_size_kv4(dims) bytes (0 = unsupported shape)
+ * Scores, sums and partial outputs are fp32; a weight is rounded to fp16 (11 bits)
+ * over the cache and to 16 bits over the block's own keys, the output to bf16.
  * N*Hkv <= 65535, L_max <= 2^30.  Results do not depend on other calls or on timing. */
 size_t herald_workspace_size_kv4(herald_dims dims);
 herald_status herald_kv4_attn(herald_dims dims, const uint16_t *q, const herald_kv4 *cache,

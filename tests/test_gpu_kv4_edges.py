@@ -149,3 +149,28 @@ def test_scale_and_cache_factor_past_fp32_together(B):
     want, tol = ref.attention(q, c, [L], scale=2.0 ** 69)
     assert np.abs(want - c.rows(1, 0, np.arange(L)).mean(1).repeat(4, 0)).max() > 0.1  # not uniform
     check(run_attn(c, q, [L], B, L, scale=2.0 ** 69), want, tol, "scales")
+
+
+@pytest.mark.parametrize("B", BLOCKS)
+@pytest.mark.parametrize("lengths", [[0, 1], [128, 7]], ids=str)
+def test_weights_of_the_blocks_keys_keep_16_bits(B, lengths):
+    """Short contexts, where the block's own keys carry most of the weight: their
+    weights are held as precisely as the cache's, not in bf16's 8 bits.  The bound
+    is ref.attention's with 2^-16 A_b (a weight as the sum of two bf16 numbers) in
+    the place of 2^-8 A_b, and 2^-23 A_b for the product with 1/v_scale."""
+    rng = np.random.default_rng(60 + B + sum(lengths))
+    N, Hq, Hkv, d = 2, 8, 2, 128
+    c = make_cache(rng, N, Hkv, d, 64, lengths, v_scale=0.3)
+    q = ref.bf16(rng.standard_normal((N, B, Hq, d)))
+    bk, bv = (ref.bf16(rng.standard_normal((N, B, Hkv, d))) for _ in range(2))
+    want, tol = ref.attention(q, c, lengths, bk, bv)
+    for n in range(N):
+        at = np.arange(lengths[n])
+        for h in range(Hq):
+            keys = np.concatenate((c.rows(0, n, at)[h // 4], ref.f64(bk)[n, :, h // 4]))
+            s = ref.f64(q)[n, :, h] @ keys.T / np.sqrt(d)
+            p = np.exp(s - s.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            Ab = p[:, lengths[n]:] @ np.abs(ref.f64(bv)[n, :, h // 4])
+            tol[n, :, h] -= (2.0 ** -8 - 2.0 ** -16 - 2.0 ** -23) * Ab
+    check(run_attn(c, q, lengths, B, max(lengths), bk, bv), want, tol, f"B {B} {lengths}")
