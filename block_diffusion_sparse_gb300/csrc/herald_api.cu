@@ -829,6 +829,17 @@ herald_status herald_selftest_wait_timeout(uint64_t limit_ns, void* ws, void* st
   return HERALD_OK;
 }
 
+herald_status herald_selftest_kv4_wait(int tries, void* ws, void* stream) {
+  g_err[0] = 0;
+  HERALD_CHECK_PTR(ws);
+  if (tries < 1 || tries > int(kKv4Tries))
+    return fail(HERALD_ERR_INVALID_ARG, "tries=%d outside [1, %d]", tries, int(kKv4Tries));
+  HERALD_TRY_CUDA(launch_kv4_wait(uint32_t(tries), static_cast<uint32_t*>(ws),
+                                  static_cast<cudaStream_t>(stream)),
+                  "kv4 wait self-test launch");
+  return HERALD_OK;
+}
+
 herald_status herald_select_stage1(herald_dims dims, const uint16_t* q_merge,
                                    const uint16_t* k_cache, const int32_t* ctx_len, int C,
                                    int32_t* cand, int32_t* n_cand, void* ws, size_t ws_bytes,

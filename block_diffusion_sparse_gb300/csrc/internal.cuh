@@ -323,6 +323,7 @@ struct Kv4Dev {
   int page_log2, max_pages, n_pages;
   float k_scale, v_scale;
 };
+constexpr uint32_t kKv4Tries = 250000;  // of a wait: 4 us each (measured: 3.95), a second in all
 constexpr int kKv4MaxCtas = 608;  // most attention CTAs per row tile (workspace slots)
 // q, k, v rows of one token are q_ld, k_ld, v_ld elements apart; q, k, cache
 // and the outputs may be null as herald_kv4_append allows.
@@ -335,6 +336,7 @@ cudaError_t launch_kv4_gather(const herald_dims& dm, const int32_t* idx, const i
                               int P_max, const Kv4Dev& c, uint16_t* pk, uint16_t* pv,
                               cudaStream_t st);
 size_t kv4_attn_workspace(const herald_dims& dm);
+cudaError_t launch_kv4_wait(uint32_t tries, uint32_t* err, cudaStream_t st);
 cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4Dev& c,
                             const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
                             uint16_t* out, float scale, void* ws, int num_sms, cudaStream_t st);

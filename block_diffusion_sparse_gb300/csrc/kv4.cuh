@@ -149,7 +149,7 @@ HERALD_DEV void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t 
 // the others' failures in each, 4 x 64K blocks took 127 us instead of 120.
 struct Kv4Wait {
   uint32_t* failed;  // shared: the waits that ran out
-  static constexpr uint32_t kTries = 250000;  // of 4 us each (measured: 3.95), a second in all
+  uint32_t limit = kKv4Tries;
   // The answer for a whole warp, which leaves converged: lanes may see a
   // barrier complete in different polls, and the tensor-memory instructions
   // that follow (.sync.aligned) want the warp in one piece.
@@ -159,7 +159,7 @@ struct Kv4Wait {
       uint32_t tries = 0;
 #pragma unroll 1
       do ok = mbar_try_wait_for(bar, parity, 4000u);
-      while (!ok && ++tries < kTries);
+      while (!ok && ++tries < limit);
     }
     if (__all_sync(0xffffffffu, ok)) return true;
     atomicOr(failed, which);

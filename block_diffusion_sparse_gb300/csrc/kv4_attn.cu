@@ -629,7 +629,32 @@ __global__ void __launch_bounds__(Threads)
   *out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
+// Self-test of Kv4Wait: a warp waits on a completed barrier, then on one that nothing
+// completes, and reports as the attention kernels do.
+__global__ void kv4_wait_kernel(uint32_t tries, uint32_t* err) {
+  __shared__ uint64_t done, open;
+  __shared__ uint32_t failed;
+  if (threadIdx.x == 0) {
+    mbar_init(&done, 1);
+    mbar_init(&open, 1);
+    failed = 0;
+    fence_mbar_init();
+    mbar_arrive(&done);
+  }
+  __syncthreads();
+  const Kv4Wait wait{&failed, tries};
+  if (wait(&done, 0, W_STAGE_FREE)) wait(&open, 0, W_STAGE_FULL);
+  __syncthreads();
+  if (threadIdx.x == 0 && failed)
+    record_error(err, DEV_TIMEOUT_TMA | DEV_K_KV4_ROWS | (failed << 16));
+}
+
 // ------------------------------------------------------------------- host
+
+cudaError_t launch_kv4_wait(uint32_t tries, uint32_t* err, cudaStream_t st) {
+  kv4_wait_kernel<<<1, 32, 0, st>>>(tries, err);
+  return cudaGetLastError();
+}
 
 template <int D, int NT>
 static cudaError_t launch_rows(const Kv4AttnArgs& a, uint32_t* err, cudaStream_t st) {

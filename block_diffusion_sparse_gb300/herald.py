@@ -54,7 +54,8 @@ EXPORTS = ("herald_workspace_size", "herald_status_string", "herald_last_error",
            "herald_select_stage2_staged", "herald_select_stage2_staged_gather",
            "herald_select_stage2_adaptive", "herald_debug_build", "herald_debug_status",
            "herald_inject_launch_failure", "herald_block", "herald_kv4_append",
-           "herald_kv4_attn", "herald_kv4_gather", "herald_workspace_size_kv4")
+           "herald_kv4_attn", "herald_kv4_gather", "herald_workspace_size_kv4",
+           "herald_selftest_kv4_wait")
 
 
 class HeraldError(RuntimeError):
@@ -177,6 +178,7 @@ def lib() -> C.CDLL:
         L.herald_select_stage2_noalloc.argtypes = [Dims, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                                    i32, vp, vp, vp]
         L.herald_selftest_wait_timeout.argtypes = [C.c_uint64, vp, vp]
+        L.herald_selftest_kv4_wait.argtypes = [i32, vp, vp]
         L.herald_workspace_size_exact.argtypes = [Dims, i32, i32]
         L.herald_workspace_size_exact.restype = sz
         L.herald_select_exact.argtypes = [Dims, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz,
@@ -360,6 +362,11 @@ def herald_select_exact(d, q_block, k_cache, ctx_len, K, sink, local, P_max, idx
 def herald_selftest_wait_timeout(limit_ns, ws, stream=None):
     """Runs one bounded wait that nothing completes (see include/herald.h)."""
     _check(lib().herald_selftest_wait_timeout(int(limit_ns), _p(ws), _s(stream)))
+
+
+def herald_selftest_kv4_wait(tries, ws, stream=None):
+    """Runs one wait of herald_kv4_attn's that nothing completes (see include/herald.h)."""
+    _check(lib().herald_selftest_kv4_wait(int(tries), _p(ws), _s(stream)))
 
 
 def herald_select_stage2_gather(d, q_block, k_cache, v_cache, ctx_len, cand, n_cand, C, K, sink,

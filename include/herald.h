@@ -600,6 +600,13 @@ herald_status herald_kv4_gather(herald_dims dims, const int32_t *idx, const int3
  * first 4 bytes are the error word). */
 herald_status herald_selftest_wait_timeout(uint64_t limit_ns, void *ws, void *stream);
 
+/* The same for the waits of herald_kv4_attn, which are bounded by a count of
+ * tries of about 4 us instead of a timer: one warp waits on a completed barrier,
+ * then `tries` tries (1 to 250000, the kernels' own count) on one that nothing
+ * completes; herald_workspace_error() then reads 0x20a01 (a copy wait of
+ * kernel 10, its stage-full wait). */
+herald_status herald_selftest_kv4_wait(int tries, void *ws, void *stream);
+
 /* Kernel tracing, a profiling aid that is off by default.  While enabled on
  * the calling host thread, every kernel the library launches is bracketed
  * by two caller-created CUDA events (cudaEvent_t, timing enabled) recorded
