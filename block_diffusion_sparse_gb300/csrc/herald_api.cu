@@ -759,7 +759,7 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
                 "q_rot and k_rot may lie over q and k only, each over its own");
   HERALD_TRY_CUDA(launch_kv4_append(dims, T, n_tok, q, q_ld, k, k_ld, v, v_ld, rope, ctx_len,
                                     cache ? &c : nullptr, q_rot, k_rot, pooled, Bk,
-                                    (flags & HERALD_KV4_ADVANCE) != 0,
+                                    (flags & HERALD_KV4_ADVANCE) != 0, sm_count(),
                                     static_cast<cudaStream_t>(stream)),
                   "kv4 append launch");
   return HERALD_OK;

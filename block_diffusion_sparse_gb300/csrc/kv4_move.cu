@@ -329,7 +329,7 @@ cudaError_t launch_kv4_append(const herald_dims& dm, int T, const int32_t* n_tok
                               const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld,
                               const uint16_t* v, int64_t v_ld, const herald_rope* rope,
                               int32_t* ctx, const Kv4Dev* cache, uint16_t* q_rot, uint16_t* k_rot,
-                              float* pooled, int Bk, bool advance, cudaStream_t st) {
+                              float* pooled, int Bk, bool advance, int num_sms, cudaStream_t st) {
   Kv4AppendArgs a{};
   a.q = q, a.k = k, a.v = v;
   a.q_ld = q_ld, a.k_ld = k_ld, a.v_ld = v_ld;
@@ -344,7 +344,7 @@ cudaError_t launch_kv4_append(const herald_dims& dm, int T, const int32_t* n_tok
   // heads per item: 4 share a lane's angles and keep four loads in flight, 1 makes
   // more warps of a small call.  Us with 1 and 4, 48 heads: 1 x 64 tokens 2.5 and
   // 3.7, 256 tokens 3.8 and 4.1, 384 tokens 4.6 and 4.3, 1024 tokens 9.3 and 6.7
-  const int per = rows <= 152 * 6 * rpc ? 1 : 4;
+  const int per = rows <= int64_t(num_sms) * 6 * rpc ? 1 : 4;
   a.q_chunks = cdiv(hq, per), a.k_chunks = cdiv(hk, per);
   a.chunks = a.q_chunks + a.k_chunks + cdiv(hv, per);
   while ((1 << a.tok_log2) < T && (2 << a.tok_log2) <= rpc) ++a.tok_log2;
