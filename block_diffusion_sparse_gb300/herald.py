@@ -244,7 +244,7 @@ def _nbytes(ws, ws_bytes):
     if ws_bytes is not None:
         return int(ws_bytes)
     try:
-        return ws.numel() * ws.element_size()
+        return ws.nbytes
     except AttributeError:
         raise ValueError("ws_bytes is required for a raw workspace address") from None
 
@@ -479,15 +479,27 @@ def _token_ld(x, ld, what):
     return step
 
 
-def _arr(x, shape, size, what):
-    """The address of a dense array [shape] of `size`-byte elements, or the raw
-    address given.  The kernels take no strides: a view of another layout, or a
-    tensor of another shape, would be read or written elsewhere."""
-    if x is None or isinstance(x, int):
+def _arr(x, nbytes, shape, size, what):
+    """The address of a dense array [shape] of `size`-byte elements (nbytes in all),
+    or the raw address given.  The kernels take no strides: a view of another layout,
+    or a tensor of another shape, would be read or written elsewhere.  (Bytes and
+    contiguity tell what fits at a third of the cost of comparing shapes: calls of
+    one token are bound by the host.  Where the order of axes matters _axis asks.)"""
+    if x is None or type(x) is int:
         return x
-    if x.shape != shape or not x.is_contiguous() or x.element_size() != size:
-        _check_layout(x, shape, size, what)
+    try:
+        if x.nbytes == nbytes and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        return _p(x)
+    _check_layout(x, shape, size, what)
     return x.data_ptr()
+
+
+def _axis(x, second, shape, size, what):
+    """Refuses a tensor of [shape]'s bytes whose axes stand in another order."""
+    if x is not None and not isinstance(x, int) and (x.dim() < 2 or x.size(1) != second):
+        _check_layout(x, shape, size, what)
 
 
 def _check_layout(x, shape, size, what):
@@ -517,14 +529,29 @@ def _check_tokens(x, n, t, h, d, what):
                              f"the call has {(h, d)} of 2")
 
 
-def _kv4_arg(cache, d):
+def _tokens(x, ld, n, t, h, d, what):
+    """Address and token stride (0: dense) of tokens [n, t, h, d], checked unless the
+    stride is given."""
+    if x is None or ld is not None or isinstance(x, int):
+        return _p(x), int(ld or 0)
+    if x.shape == (n, t, h, d) and x.element_size() == 2:
+        sn, st, sh, sd = x.stride()
+        step = st if t > 1 else sn if n > 1 else h * d
+        if sd == 1 and (sh == d or h == 1) and (sn == t * step or n == 1) and step >= h * d:
+            return x.data_ptr(), step
+    _check_tokens(x, n, t, h, d, what)
+    return _p(x), _token_ld(x, ld, what)
+
+
+def _kv4_arg(cache, d, n, hkv, ch):
     """A cache made by kv4() must be one of the call's shape: with another Hkv,
     d or a shorter table the kernels would reach past its arrays."""
     if cache is None:
         return None
-    n, hkv, ch = getattr(cache, "_shape", (d.N, d.Hkv, d.d))
-    if n < d.N or hkv != d.Hkv or ch != d.d:
-        raise ValueError(f"cache: made for N={n}, Hkv={hkv}, d={ch}, the call has {d}")
+    shape = getattr(cache, "_shape", None)
+    if shape and (shape[0] < n or shape[1] != hkv or shape[2] != ch):
+        raise ValueError(f"cache: made for N={shape[0]}, Hkv={shape[1]}, d={shape[2]}, "
+                         f"the call has {d}")
     return C.byref(cache)
 
 
@@ -534,20 +561,22 @@ def herald_kv4_append(d, T, q, k, v, ctx_len, cache, q_rot, k_rot, rope=None, n_
     strides of q, k, v [N, T, heads, d] are taken from the tensors (views of a
     fused projection's output) unless given."""
     N, T, Hq, Hkv, ch = d.N, int(T), d.Hq, d.Hkv, d.d
-    if q_ld is None:
-        _check_tokens(q, N, T, Hq, ch, "q")
-    if k_ld is None:
-        _check_tokens(k, N, T, Hkv, ch, "k")
-    if v_ld is None:
-        _check_tokens(v, N, T, Hkv, ch, "v")
     if pooled is not None and Bk > 0:
-        pooled = _arr(pooled, (N, Hkv, -(-d.L_max // int(Bk)), ch), 4, "pooled")
-    _check(lib().herald_kv4_append(
-        d, T, _arr(n_tok, (N,), 4, "n_tok"), _p(q), _token_ld(q, q_ld, "q"), _p(k),
-        _token_ld(k, k_ld, "k"), _p(v), _token_ld(v, v_ld, "v"),
-        None if rope is None else C.byref(rope), _arr(ctx_len, (N,), 4, "ctx_len"),
-        _kv4_arg(cache, d), _arr(q_rot, (N, T, Hq, ch), 2, "q_rot"),
-        _arr(k_rot, (N, T, Hkv, ch), 2, "k_rot"), _p(pooled), int(Bk), int(flags), _s(stream)))
+        blocks = -(-d.L_max // int(Bk))
+        pooled = _arr(pooled, N * Hkv * blocks * ch * 4, (N, Hkv, blocks, ch), 4, "pooled")
+    toks = N * T * ch * 2
+    if T > 1:
+        _axis(q_rot, T, (N, T, Hq, ch), 2, "q_rot")
+        _axis(k_rot, T, (N, T, Hkv, ch), 2, "k_rot")
+    q, q_ld = _tokens(q, q_ld, N, T, Hq, ch, "q")
+    k, k_ld = _tokens(k, k_ld, N, T, Hkv, ch, "k")
+    v, v_ld = _tokens(v, v_ld, N, T, Hkv, ch, "v")
+    _check((_lib or lib()).herald_kv4_append(
+        d, T, _arr(n_tok, 4 * N, (N,), 4, "n_tok"), q, q_ld, k, k_ld, v, v_ld,
+        None if rope is None else C.byref(rope), _arr(ctx_len, 4 * N, (N,), 4, "ctx_len"),
+        _kv4_arg(cache, d, N, Hkv, ch), _arr(q_rot, toks * Hq, (N, T, Hq, ch), 2, "q_rot"),
+        _arr(k_rot, toks * Hkv, (N, T, Hkv, ch), 2, "k_rot"), _p(pooled), int(Bk), int(flags),
+        _s(stream)))
 
 
 def herald_workspace_size_kv4(d: Dims) -> int:
@@ -558,20 +587,31 @@ def herald_kv4_attn(d, q, cache, ctx_len, block_k, block_v, out, scale=0.0, ws=N
                     ws_bytes=None, stream=None):
     """Attention over a paged 4-bit cache (a Kv4) and, unless both are None,
     the block's own keys and values; every tensor dense, as in include/herald.h."""
-    N, B, Hkv, ch = d.N, d.B, d.Hkv, d.d
-    queries, keys = (N, B, d.Hq, ch), (N, B, Hkv, ch)
-    _check(lib().herald_kv4_attn(d, _arr(q, queries, 2, "q"), _kv4_arg(cache, d),
-                                 _arr(ctx_len, (N,), 4, "ctx_len"), _arr(block_k, keys, 2, "block_k"),
-                                 _arr(block_v, keys, 2, "block_v"), _arr(out, queries, 2, "out"),
-                                 float(scale), _p(ws), _nbytes(ws, ws_bytes), _s(stream)))
+    N, B, Hq, Hkv, ch = d.N, d.B, d.Hq, d.Hkv, d.d
+    toks = N * B * ch * 2
+    if B > 1:
+        for x, h, what in (q, Hq, "q"), (block_k, Hkv, "block_k"), (block_v, Hkv, "block_v"), \
+                (out, Hq, "out"):
+            _axis(x, B, (N, B, h, ch), 2, what)
+    _check((_lib or lib()).herald_kv4_attn(
+        d, _arr(q, toks * Hq, (N, B, Hq, ch), 2, "q"), _kv4_arg(cache, d, N, Hkv, ch),
+        _arr(ctx_len, 4 * N, (N,), 4, "ctx_len"),
+        _arr(block_k, toks * Hkv, (N, B, Hkv, ch), 2, "block_k"),
+        _arr(block_v, toks * Hkv, (N, B, Hkv, ch), 2, "block_v"),
+        _arr(out, toks * Hq, (N, B, Hq, ch), 2, "out"), float(scale), _p(ws),
+        _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def herald_kv4_gather(d, idx, n_sel, P_max, cache, pool_k, pool_v=None, stream=None):
-    rows = (d.N, d.Hkv, int(P_max))
-    pool = rows + (d.d,)
-    _check(lib().herald_kv4_gather(d, _arr(idx, rows, 4, "idx"), _arr(n_sel, rows[:2], 4, "n_sel"),
-                                   int(P_max), _kv4_arg(cache, d), _arr(pool_k, pool, 2, "pool_k"),
-                                   _arr(pool_v, pool, 2, "pool_v"), _s(stream)))
+    N, Hkv, ch, P = d.N, d.Hkv, d.d, int(P_max)
+    rows = N * Hkv * P
+    if Hkv > 1:
+        _axis(pool_k, Hkv, (N, Hkv, P, ch), 2, "pool_k")
+    _check((_lib or lib()).herald_kv4_gather(
+        d, _arr(idx, rows * 4, (N, Hkv, P), 4, "idx"),
+        _arr(n_sel, N * Hkv * 4, (N, Hkv), 4, "n_sel"), P, _kv4_arg(cache, d, N, Hkv, ch),
+        _arr(pool_k, rows * ch * 2, (N, Hkv, P, ch), 2, "pool_k"),
+        _arr(pool_v, rows * ch * 2, (N, Hkv, P, ch), 2, "pool_v"), _s(stream)))
 
 
 class Trace:
