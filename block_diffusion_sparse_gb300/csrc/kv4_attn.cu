@@ -3,15 +3,16 @@
 // token, a short draft): bound by the cache's bytes and by the instructions that
 // turn codes into numbers.  One token over 128K (8 KV heads, 151 MB) takes 37 us, of
 // which it streams for 29 at 5.2 TB/s; its copies alone, without a product, 31.  Per
-// 16 keys a warp issues some 340 instructions, 64 of them conversions and 64 products
-// with scales, each at half rate.  64 ragged tokens of up to 8K (327 MB): 75 us.
+// 16 keys a warp issues some 345 instructions, 64 of them conversions and 64 products
+// with scales, each at half rate; at 96 registers (two CTAs an SM) d = 128 spills 10
+// bytes.  64 ragged tokens of up to 8K (327 MB): 75 us.
 //
 // A CTA walks its share of the keys (kv4_split) in tiles of 128.  Its last warp
 // copies each tile's codes and scales from the pages into a ring of stages (bulk
 // copies, the tile's pages in parallel lanes); each of the first eight takes 16
 // of the tile's keys, and the ninth the block's own keys, beside them (with one
 // of the eight doing that first, a ragged batch of single tokens took 114 us
-// instead of 91: the ring waited for it).  With rows = the group's query rows,
+// instead of 97: the ring waited for it).  With rows = the group's query rows,
 //   S^T [16 keys x 8 rows] = K [16 x d] Q^T [d x 8]        (mma m16n8k16)
 //   O^T [d x 8 rows]      += V^T [d x 16 keys] P^T [16 x 8] (mma m16n8k16)
 // The keys are the M side of both products, so eight query rows fill an
@@ -29,9 +30,10 @@
 // then neither the K nor the V reads meet more than two-way bank conflicts.
 // code * scale is exact in fp16 (kv4.cuh).  Queries become fp16 scaled per
 // row by a power of two that brings the row's largest value to [2^14, 2^15):
-// exact for every value within 2^-32 of the largest (below, off by less than
-// 2^-40 of the largest), the power undone in the fp32 scores.  P is fp16 (11
-// bits against bf16's 8); scores, row sums and O are fp32.  P^T needs the
+// exact for every value within 2^-31 of the largest (below, off by at most
+// 2^-39 of the largest), the power undone in the fp32 scores.  P is fp16 (11
+// bits against bf16's 8; over the block's keys two bf16 numbers, take_bf16);
+// scores, row sums and O are fp32.  P^T needs the
 // scores transposed: one movmatrix per 8x8 tile.
 //
 // A row's exponent base is set 11 (log2) below its largest score so far and

@@ -24,9 +24,9 @@
 // there when the softmax of the step before is done; O takes 128 columns: the
 // two streams fill the 512.
 //
-// A block of 32 tokens over 4 x 64K (128 rows, 8 KV heads) takes 118 us: 305 MB, 137
+// A block of 32 tokens over 4 x 64K (128 rows, 8 KV heads) takes 119 us: 305 MB, 137
 // GFLOP.  No unit bounds it: the tensor pipe is active for 48% of the time, memory for
-// a third; 0.7 of the issue slots are taken by 5,600 warp instructions a tile, and the
+// a third; 0.7 of the issue slots are taken by 5,650 warp instructions a tile, and the
 // roles crowd the instruction cache: code that is unrolled more runs slower (the
 // conversion by two chunks: 136 us where it was 127).
 //

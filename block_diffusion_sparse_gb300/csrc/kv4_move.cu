@@ -72,9 +72,11 @@ constexpr int kKv4MoveThreads = 256;
 // A row of D channels is handled by D/8 neighbouring lanes, eight channels (16
 // bytes) each; an item is one token and Per consecutive heads of its queries, keys
 // or values (a chunk).  A CTA holds `toks` = 2^tok_log2 tokens by kRows / toks
-// chunks; grid (tokens, sequences, chunks).  Bound by memory for prompts (ragged
-// 4 x 4096 tokens of 32 + 2 x 8 heads: 39 us, 83% of the copy rate) and by latency
-// below some hundred tokens.  What counts is that an item loads its heads before it
+// chunks; grid (tokens, sequences, chunks).  Bound by memory for interleaved prompts
+// (ragged 4 x 4096 tokens of 32 + 2 x 8 heads: 39 us, 82% of the copy rate; 42 with
+// inputs that change from call to call, past L2), by instructions as well for
+// half-split ones (50 and 53 us: four shuffles a head, 72 registers for 61), and by
+// latency below some hundred tokens.  What counts is that an item loads its heads before it
 // works on any, that queries, keys and values do not share warps (one loop over all
 // three kinds: 64 us) and that no lane divides for its place.
 struct Kv4AppendArgs {
@@ -276,9 +278,11 @@ __global__ void kv4_advance_kernel(int32_t* ctx, const int32_t* n_tok, int N, in
 }
 
 // grid (row groups, N*Hkv): D/16 lanes per row, each 16 channels: 8 bytes of
-// codes and one scale in, 32 bytes of bf16 out.  Bound by memory (32 x 4096 candidate
-// keys 8.8 us, 74% of the copy rate; with two rows per thread 9.7), by its chain of
-// three loads when small (4 x 1344 rows of K and V 2.7 us, with two 3.1).
+// codes and one scale in, 32 bytes of bf16 out.  Bound by its chain of three loads,
+// 13 bytes a thread in flight: 32 x 4096 candidate keys 12.9 us, half of the copy rate,
+// with inputs that change from call to call, 8.9 where the same 43.5 MB stay in L2;
+// 4 x 1344 rows of K and V 3.8 and 2.8.  (Two rows per thread, on data in L2: 9.7 and
+// 3.1.)
 template <int D>
 __global__ void __launch_bounds__(kKv4MoveThreads)
     kv4_gather_kernel(const Kv4Dev c, const int32_t* __restrict__ idx,
