@@ -745,8 +745,8 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
     if (rope->interleaved != 0 && rope->interleaved != 1)
       return fail(HERALD_ERR_INVALID_ARG, "interleaved=%d not 0 or 1", rope->interleaved);
   }
-  // An output may be its own input, row for row; lying over anything else that the
-  // call reads or writes it would change rows that others have yet to read.
+  // An output may be its own input, row for row; lying over another of these arrays it
+  // would change rows that others have yet to read.
   const int64_t toks = int64_t(dims.N) * T, qw = int64_t(dims.Hq) * dims.d,
                 kw = int64_t(dims.Hkv) * dims.d;
   const Span sq = rows_span(q, toks, q_ld, qw), sk = rows_span(k, toks, k_ld, kw),

@@ -64,7 +64,7 @@ constexpr int kTcSoft = 256;               // softmax threads
 constexpr int kTcThreadsAll = 768;         // 8 + 8 + 8 warps (22, 23 only fill a warpgroup)
 constexpr int kTcSWarp = 16, kTcCopyWarp = 17, kTcPvWarp = 20;  // S 16, 18; copies 17, 19; P V 20, 21
 constexpr float kTcBelow = 5.f, kTcTop = 60000.f;  // base of P and largest sum (see above)
-constexpr float kTcTopLog2 = 15.8727f;
+constexpr float kTcTopLog2 = 15.8727f;                // log2 of kTcTop
 
 // Waits of the kernel (bits 16-31 of the error word).
 enum : uint32_t {
@@ -181,10 +181,9 @@ HERALD_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
 }
 // The second numbers of a block step's weights, from its scores at ts once more, into
 // columns 32-63 (the second half's first: its own scores lie there; none without keys,
-// nk, in it).  Block steps are few:
-// kept beside P in the steps' common code these spilled registers, and blocks took 29.1
-// us at 32K and 120 at 4 x 64K instead of 28.5 and 118.4.  (With one number a weight
-// 27.9 and 117.1.)
+// nk, in it).  Block steps are few: kept beside P in the steps' common code these
+// numbers spilled registers, and blocks took 29.1 us at 32K and 120 at 4 x 64K instead
+// of 28.5 and 118.4.  (With one number a weight 27.9 and 117.1.)
 HERALD_DEV void rest_of_p(uint32_t ts, uint64_t f2, uint64_t nm2, float iv, int nk) {
 #pragma unroll 1
   for (int c = nk > 32 ? 1 : 0; c >= 0; --c) {

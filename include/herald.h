@@ -544,8 +544,8 @@ typedef struct {
  *   q_rot    [N][T][Hq][d] bf16 device out, required with q (may be q itself
  *            when q is dense)
  *   k_rot    [N][T][Hkv][d] bf16 device out (may be k itself when k is
- *            dense); may be NULL with a cache.  Neither may lie, even in part,
- *            over anything else that the call reads or writes
+ *            dense); may be NULL with a cache.  Neither output may lie, even in
+ *            part, over the other or over another input of q, k, v
  *   pooled   NULL, or fp32 [N][Hkv][ceil(L_max/Bk)][d] device: the means of
  *            herald_pool_keys over the keys as held, refreshed for the
  *            blocks the tokens fall into (herald_select_stage1_blocks reads
