@@ -530,7 +530,7 @@ herald_status herald_debug_status(uint32_t* code) {
   HERALD_TRY_CUDA(cudaDeviceSynchronize(), "device synchronize");
   *code = debug_take_select() | debug_take_tc() | debug_take_move() | debug_take_blocks() |
           debug_take_flash() | debug_take_kv4_move() | debug_take_kv4_attn() |
-          debug_take_kv4_attn_tc();
+          debug_take_kv4_attn_tc() | debug_take_kv8_move() | debug_take_kv8_attn();
 #endif
   return HERALD_OK;
 }
@@ -690,13 +690,14 @@ static Span rows_span(const uint16_t* p, int64_t toks, int64_t ld, int64_t width
 }
 static bool overlap(const Span& a, const Span& b) { return a.begin < b.end && b.begin < a.end; }
 
-herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, const uint16_t* q,
-                                int64_t q_ld, const uint16_t* k, int64_t k_ld, const uint16_t* v,
-                                int64_t v_ld, const herald_rope* rope, int32_t* ctx_len,
-                                const herald_kv4* cache, uint16_t* q_rot, uint16_t* k_rot,
-                                float* pooled, int Bk, unsigned flags, void* stream) {
-  g_err[0] = 0;
-  HERALD_RET_IF(check_kv4_dims(dims));
+// What herald_kv4_append and herald_kv8_append check alike, all but their caches; the
+// token strides leave with their values (0 = dense resolved).
+static herald_status check_append(const herald_dims& dims, int T, const int32_t* n_tok,
+                                  const uint16_t* q, int64_t* q_ld, const uint16_t* k,
+                                  int64_t* k_ld, const uint16_t* v, int64_t* v_ld,
+                                  const int32_t* ctx_len, bool cache, const uint16_t* q_rot,
+                                  const uint16_t* k_rot, unsigned flags) {
+  static_assert(HERALD_KV4_ADVANCE == HERALD_KV8_ADVANCE, "one flag");
   if (T < 1) return fail(HERALD_ERR_INVALID_ARG, "T=%d must be >= 1", T);
   if ((long long)dims.N * T >= (1ll << 31) || T > 1 << 30)
     return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "N*T too large");
@@ -710,26 +711,32 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
   if (q) {
     HERALD_CHECK_PTR(q);
     HERALD_CHECK_PTR(q_rot);
-    HERALD_RET_IF(check_ld("q_ld", &q_ld, int64_t(dims.Hq) * dims.d));
-    if (q == q_rot && q_ld != int64_t(dims.Hq) * dims.d)
+    HERALD_RET_IF(check_ld("q_ld", q_ld, int64_t(dims.Hq) * dims.d));
+    if (q == q_rot && *q_ld != int64_t(dims.Hq) * dims.d)
       return fail(HERALD_ERR_INVALID_ARG, "q_rot may be q only when q is dense");
   }
   if (k) {
     HERALD_CHECK_PTR(k);
     if (k_rot || !cache) HERALD_CHECK_PTR(k_rot);
-    HERALD_RET_IF(check_ld("k_ld", &k_ld, int64_t(dims.Hkv) * dims.d));
-    if (k == k_rot && k_ld != int64_t(dims.Hkv) * dims.d)
+    HERALD_RET_IF(check_ld("k_ld", k_ld, int64_t(dims.Hkv) * dims.d));
+    if (k == k_rot && *k_ld != int64_t(dims.Hkv) * dims.d)
       return fail(HERALD_ERR_INVALID_ARG, "k_rot may be k only when k is dense");
   }
-  Kv4Dev c{};
   if (cache) {
     if (!k) return fail(HERALD_ERR_INVALID_ARG, "k is NULL with a cache");
     HERALD_CHECK_PTR(v);
-    HERALD_RET_IF(check_ld("v_ld", &v_ld, int64_t(dims.Hkv) * dims.d));
-    HERALD_RET_IF(check_kv4(dims, cache, &c));
-  } else if (pooled || flags) {
-    return fail(HERALD_ERR_INVALID_ARG, "pooled and HERALD_KV4_ADVANCE need a cache");
+    HERALD_RET_IF(check_ld("v_ld", v_ld, int64_t(dims.Hkv) * dims.d));
   }
+  return HERALD_OK;
+}
+// The rest of them, which the cache's own checks come before.
+static herald_status check_append_more(const herald_dims& dims, int T, const uint16_t* q,
+                                       int64_t q_ld, const uint16_t* k, int64_t k_ld,
+                                       const uint16_t* v, int64_t v_ld, const herald_rope* rope,
+                                       bool cache, const uint16_t* q_rot, const uint16_t* k_rot,
+                                       const float* pooled, int Bk, unsigned flags) {
+  if (!cache && (pooled || flags))
+    return fail(HERALD_ERR_INVALID_ARG, "pooled and the advance flag need a cache");
   if (pooled) {
     HERALD_CHECK_PTR(pooled);
     if (Bk < 1 || Bk > 1 << 30)
@@ -757,6 +764,22 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, c
       (k != k_rot && overlap(ok, sk)) || overlap(ok, sq) || overlap(ok, sv))
     return fail(HERALD_ERR_INVALID_ARG,
                 "q_rot and k_rot may lie over q and k only, each over its own");
+  return HERALD_OK;
+}
+
+herald_status herald_kv4_append(herald_dims dims, int T, const int32_t* n_tok, const uint16_t* q,
+                                int64_t q_ld, const uint16_t* k, int64_t k_ld, const uint16_t* v,
+                                int64_t v_ld, const herald_rope* rope, int32_t* ctx_len,
+                                const herald_kv4* cache, uint16_t* q_rot, uint16_t* k_rot,
+                                float* pooled, int Bk, unsigned flags, void* stream) {
+  g_err[0] = 0;
+  HERALD_RET_IF(check_kv4_dims(dims));
+  HERALD_RET_IF(check_append(dims, T, n_tok, q, &q_ld, k, &k_ld, v, &v_ld, ctx_len, cache != nullptr,
+                             q_rot, k_rot, flags));
+  Kv4Dev c{};
+  if (cache) HERALD_RET_IF(check_kv4(dims, cache, &c));
+  HERALD_RET_IF(check_append_more(dims, T, q, q_ld, k, k_ld, v, v_ld, rope, cache != nullptr, q_rot,
+                                  k_rot, pooled, Bk, flags));
   HERALD_TRY_CUDA(launch_kv4_append(dims, T, n_tok, q, q_ld, k, k_ld, v, v_ld, rope, ctx_len,
                                     cache ? &c : nullptr, q_rot, k_rot, pooled, Bk,
                                     (flags & HERALD_KV4_ADVANCE) != 0, sm_count(),
@@ -814,6 +837,106 @@ herald_status herald_kv4_gather(herald_dims dims, const int32_t* idx, const int3
   HERALD_TRY_CUDA(launch_kv4_gather(dims, idx, n_sel, P_max, c, pool_k, pool_v,
                                     static_cast<cudaStream_t>(stream)),
                   "kv4 gather launch");
+  return HERALD_OK;
+}
+
+// The rules of herald_kv8 and its device form.
+static herald_status check_kv8(const herald_dims& dm, const herald_kv8* c, Kv8Dev* out) {
+  if (!c) return fail(HERALD_ERR_INVALID_ARG, "cache is NULL");
+  int log2 = 4, blog2 = 4;
+  while (log2 < 7 && (1 << log2) != c->page) ++log2;
+  if ((1 << log2) != c->page)
+    return fail(HERALD_ERR_UNSUPPORTED_SHAPE, "page %d not in {16, 32, 64, 128}", c->page);
+  while (blog2 < log2 && (1 << blog2) != c->block) ++blog2;
+  if ((1 << blog2) != c->block)
+    return fail(HERALD_ERR_UNSUPPORTED_SHAPE,
+                "block %d not in {16, 32, 64, 128} or above page %d", c->block, c->page);
+  if (c->n_pages < 1 || c->max_pages < 1)
+    return fail(HERALD_ERR_INVALID_ARG, "n_pages=%d, max_pages=%d must be >= 1", c->n_pages,
+                c->max_pages);
+  if ((long long)c->max_pages * c->page < dm.L_max)
+    return fail(HERALD_ERR_INVALID_ARG, "max_pages*page = %lld < L_max=%d",
+                (long long)c->max_pages * c->page, dm.L_max);
+  HERALD_CHECK_PTR(c->table);
+  HERALD_CHECK_PTR(c->k_codes);
+  HERALD_CHECK_PTR(c->v_codes);
+  if (!c->k_scales || !c->v_scales)  // (read byte by byte: any alignment)
+    return fail(HERALD_ERR_INVALID_ARG, "k_scales or v_scales is NULL");
+  *out = Kv8Dev{c->table, c->k_codes, c->k_scales,  c->v_codes, c->v_scales,
+                log2,     blog2,      c->max_pages, c->n_pages};
+  return HERALD_OK;
+}
+
+herald_status herald_kv8_append(herald_dims dims, int T, const int32_t* n_tok, const uint16_t* q,
+                                int64_t q_ld, const uint16_t* k, int64_t k_ld, const uint16_t* v,
+                                int64_t v_ld, const herald_rope* rope, int32_t* ctx_len,
+                                const herald_kv8* cache, uint16_t* q_rot, uint16_t* k_rot,
+                                float* pooled, int Bk, unsigned flags, void* stream) {
+  g_err[0] = 0;
+  HERALD_RET_IF(check_kv4_dims(dims));
+  HERALD_RET_IF(check_append(dims, T, n_tok, q, &q_ld, k, &k_ld, v, &v_ld, ctx_len, cache != nullptr,
+                             q_rot, k_rot, flags));
+  Kv8Dev c{};
+  if (cache) HERALD_RET_IF(check_kv8(dims, cache, &c));
+  HERALD_RET_IF(check_append_more(dims, T, q, q_ld, k, k_ld, v, v_ld, rope, cache != nullptr, q_rot,
+                                  k_rot, pooled, Bk, flags));
+  HERALD_TRY_CUDA(launch_kv8_append(dims, T, n_tok, q, q_ld, k, k_ld, v, v_ld, rope, ctx_len,
+                                    cache ? &c : nullptr, q_rot, k_rot, pooled, Bk,
+                                    (flags & HERALD_KV8_ADVANCE) != 0, sm_count(),
+                                    static_cast<cudaStream_t>(stream)),
+                  "kv8 append launch");
+  return HERALD_OK;
+}
+
+size_t herald_workspace_size_kv8(herald_dims dims) {
+  return check_kv4_dims(dims) == HERALD_OK ? kv8_attn_workspace(dims) : 0;
+}
+
+herald_status herald_kv8_attn(herald_dims dims, const uint16_t* q, const herald_kv8* cache,
+                              const int32_t* ctx_len, const uint16_t* block_k,
+                              const uint16_t* block_v, uint16_t* out, float scale, void* ws,
+                              size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  HERALD_RET_IF(check_kv4_dims(dims));
+  HERALD_CHECK_PTR(q);
+  HERALD_CHECK_PTR(ctx_len);
+  HERALD_CHECK_PTR(out);
+  HERALD_CHECK_PTR(ws);
+  Kv8Dev c{};
+  HERALD_RET_IF(check_kv8(dims, cache, &c));
+  if ((block_k == nullptr) != (block_v == nullptr))
+    return fail(HERALD_ERR_INVALID_ARG, "block_k and block_v: both or neither");
+  if (block_k) {
+    HERALD_CHECK_PTR(block_k);
+    HERALD_CHECK_PTR(block_v);
+  }
+  if (!(scale >= 0.f && scale <= 0x1p127f))  // (times log2(e) it has to be finite)
+    return fail(HERALD_ERR_INVALID_ARG, "scale=%g outside [0, 2^127]", double(scale));
+  const size_t need = kv8_attn_workspace(dims);
+  if (ws_bytes < need)
+    return fail(HERALD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  HERALD_TRY_CUDA(launch_kv8_attn(dims, q, c, ctx_len, block_k, block_v, out,
+                                  scale > 0.f ? scale : 1.f / sqrtf(float(dims.d)), ws, sm_count(),
+                                  static_cast<cudaStream_t>(stream)),
+                  "kv8 attention launch");
+  return HERALD_OK;
+}
+
+herald_status herald_kv8_gather(herald_dims dims, const int32_t* idx, const int32_t* n_sel,
+                                int P_max, const herald_kv8* cache, uint16_t* pool_k,
+                                uint16_t* pool_v, void* stream) {
+  g_err[0] = 0;
+  HERALD_RET_IF(check_kv4_dims(dims));
+  HERALD_RET_IF(check_pmax(dims, P_max));
+  HERALD_CHECK_PTR(idx);
+  HERALD_CHECK_PTR(n_sel);
+  HERALD_CHECK_PTR(pool_k);
+  if (pool_v) HERALD_CHECK_PTR(pool_v);
+  Kv8Dev c{};
+  HERALD_RET_IF(check_kv8(dims, cache, &c));
+  HERALD_TRY_CUDA(launch_kv8_gather(dims, idx, n_sel, P_max, c, pool_k, pool_v, sm_count(),
+                                    static_cast<cudaStream_t>(stream)),
+                  "kv8 gather launch");
   return HERALD_OK;
 }
 

@@ -130,6 +130,8 @@ uint32_t debug_take_flash();
 uint32_t debug_take_kv4_move();
 uint32_t debug_take_kv4_attn();
 uint32_t debug_take_kv4_attn_tc();
+uint32_t debug_take_kv8_move();
+uint32_t debug_take_kv8_attn();
 
 // A launch failure injected on the host (herald_inject_launch_failure, a
 // test hook of the error paths): returns the injected error for the launch
@@ -333,12 +335,37 @@ cudaError_t launch_kv4_append(const herald_dims& dm, int T, const int32_t* n_tok
                               int32_t* ctx, const Kv4Dev* cache, uint16_t* q_rot, uint16_t* k_rot,
                               float* pooled, int Bk, bool advance, int num_sms,
                               cudaStream_t st);
+// ctx[n] += the tokens that an append of T (n_tok) wrote
+cudaError_t launch_kv_advance(const herald_dims& dm, int T, const int32_t* n_tok, int32_t* ctx,
+                              cudaStream_t st);
 cudaError_t launch_kv4_gather(const herald_dims& dm, const int32_t* idx, const int32_t* n_sel,
                               int P_max, const Kv4Dev& c, uint16_t* pk, uint16_t* pv,
                               cudaStream_t st);
 size_t kv4_attn_workspace(const herald_dims& dm);
 cudaError_t launch_kv4_wait(uint32_t tries, uint32_t* err, cudaStream_t st);
 cudaError_t launch_kv4_attn(const herald_dims& dm, const uint16_t* q, const Kv4Dev& c,
+                            const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
+                            uint16_t* out, float scale, void* ws, int num_sms, cudaStream_t st);
+
+// ---- the paged 8-bit cache (kv8_move.cu, kv8_attn.cu; kv8.cuh)
+// The cache as the kernels take it (herald_kv8 with its sizes as shifts).
+struct Kv8Dev {
+  const int32_t* table;  // [N][max_pages]
+  uint8_t *kc, *ks, *vc, *vs;
+  int page_log2, block_log2, max_pages, n_pages;
+};
+// as launch_kv4_append
+cudaError_t launch_kv8_append(const herald_dims& dm, int T, const int32_t* n_tok,
+                              const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld,
+                              const uint16_t* v, int64_t v_ld, const herald_rope* rope,
+                              int32_t* ctx, const Kv8Dev* cache, uint16_t* q_rot, uint16_t* k_rot,
+                              float* pooled, int Bk, bool advance, int num_sms,
+                              cudaStream_t st);
+cudaError_t launch_kv8_gather(const herald_dims& dm, const int32_t* idx, const int32_t* n_sel,
+                              int P_max, const Kv8Dev& c, uint16_t* pk, uint16_t* pv, int num_sms,
+                              cudaStream_t st);
+size_t kv8_attn_workspace(const herald_dims& dm);
+cudaError_t launch_kv8_attn(const herald_dims& dm, const uint16_t* q, const Kv8Dev& c,
                             const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
                             uint16_t* out, float scale, void* ws, int num_sms, cudaStream_t st);
 

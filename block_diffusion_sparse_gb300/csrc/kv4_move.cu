@@ -376,11 +376,14 @@ cudaError_t launch_kv4_append(const herald_dims& dm, int T, const int32_t* n_tok
                                    dim3(kKv4MoveThreads), 0, st, *cache, ctx, n_tok, T, dm.Hkv,
                                    dm.L_max, Bk, cdiv(dm.L_max, Bk), pooled));
   }
-  if (advance)
-    HERALD_CHECK_LAUNCH(launch_k("kv4_advance_kernel", kv4_advance_kernel,
-                                 dim3(unsigned(cdiv(dm.N, 256))), dim3(256), 0, st, ctx, n_tok,
-                                 dm.N, T, dm.L_max));
+  if (advance) HERALD_CHECK_LAUNCH(launch_kv_advance(dm, T, n_tok, ctx, st));
   return cudaGetLastError();
+}
+
+cudaError_t launch_kv_advance(const herald_dims& dm, int T, const int32_t* n_tok, int32_t* ctx,
+                              cudaStream_t st) {
+  return launch_k("kv4_advance_kernel", kv4_advance_kernel, dim3(unsigned(cdiv(dm.N, 256))),
+                  dim3(256), 0, st, ctx, n_tok, dm.N, T, dm.L_max);
 }
 
 cudaError_t launch_kv4_gather(const herald_dims& dm, const int32_t* idx, const int32_t* n_sel,

@@ -1,0 +1,83 @@
+// kv8.cuh -- the paged 8-bit KV cache on the device: its addresses, its number
+// format, and the arguments of its attention kernels.
+//
+// A row of d channels (one position of one KV head) is d bytes of e4m3 codes; the
+// rows of `block` consecutive positions of a head share one scale, a power of two
+// whose biased exponent is a byte:  value = code * 2^(byte - 127).
+// A code has 4 significant bits and the scale none, so a value is exact in bf16.
+#pragma once
+#include <float.h>
+
+#include "kv4.cuh"
+
+namespace herald {
+
+constexpr int kKv8MinExp = -32, kKv8MaxExp = 32;  // exponents of the scales
+
+// The page of logical page lp of sequence n, or -1 where the table has no page in
+// range (such positions are never read or written).
+HERALD_DEV int kv8_page(const Kv8Dev& c, int n, int lp) {
+  const int p = c.table[size_t(n) * c.max_pages + lp];
+  return p >= 0 && p < c.n_pages ? p : -1;
+}
+// Row index of position pos in page `phys` (64 bits: a long cache has more bytes
+// than 32 bits count), and the index of its scale.
+HERALD_DEV size_t kv8_row(const Kv8Dev& c, int phys, int Hkv, int g, int pos) {
+  return ((size_t(phys) * Hkv + g) << c.page_log2) + (pos & ((1 << c.page_log2) - 1));
+}
+HERALD_DEV size_t kv8_scale(const Kv8Dev& c, int phys, int Hkv, int g, int pos) {
+  return kv8_row(c, phys, Hkv, g, pos) >> c.block_log2;  // (pages hold whole blocks)
+}
+// Exponent of a scale byte; bytes that no call writes count as the nearer end.
+HERALD_DEV int kv8_exp(uint32_t byte) {
+  return min(max(int(byte) - 127, kKv8MinExp), kKv8MaxExp);
+}
+HERALD_DEV float exp2_int(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }  // -126..127
+
+// The four e4m3 codes of a word -> two fp16 pairs (exact).
+HERALD_DEV void e4m3x4_to_half2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  lo = e4m3x2_to_half2(w & 0xFFFFu);
+  hi = e4m3x2_to_half2(w >> 16);
+}
+// fp32 pair -> e4m3 codes (lo in bits 0-7), to nearest even, past 448 to 448, NaN stays.
+HERALD_DEV uint32_t float2_to_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ---- attention arguments shared by its kernels
+struct Kv8AttnArgs {
+  const uint16_t *q, *bk, *bv;
+  const int32_t* ctx;
+  uint16_t* out;
+  float* opart;  // [slots][R16][D]
+  float2* ml;    // [slots][R16]
+  float scale;   // softmax scale times log2(e): scores are in log2 units
+  int N, Hq, Hkv, B, L_max, R16, ctas;
+  int pad;       // what a piece costs beside its tiles, in tiles (kv4_units)
+  Kv8Dev c;
+};
+
+// The pieces of a CTA's share, in order: body(n, g, seg, ctx, u0, u1) with tiles
+// u0 <= u < u1 of 128 cache positions; it returns false to leave.
+template <typename Body>
+HERALD_DEV void kv8_pieces(const Kv8AttnArgs& a, const Kv4Share& sh, Body&& body) {
+  int at = sh.at, first = sh.first, n = sh.n;
+  while (at < sh.end) {
+    const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
+    const int units = kv4_units(ctx, a.L_max, 0, a.pad);
+    if (units == 0 || at >= first + a.Hkv * units) {  // the next sequence
+      first += a.Hkv * units;
+      ++n;
+      continue;
+    }
+    const int g = (at - first) / units;
+    const int seg0 = first + g * units;
+    const int u0 = max(at - seg0 - a.pad, 0), u1 = min(units, sh.end - seg0) - a.pad;
+    if (u1 > 0 && !body(n, g, n * a.Hkv + g, ctx, u0, u1)) return;
+    at = seg0 + a.pad + u1;
+  }
+}
+
+}  // namespace herald

@@ -32,8 +32,8 @@ HERALD_ATTN_KERNEL_POOL_CS8, HERALD_ATTN_KERNEL_POOL_CS16, HERALD_ATTN_KERNEL_PO
 # flags of herald_block
 HERALD_BLOCK_ADVANCE = 1
 HERALD_BLOCK_CAND_SETTLED = 2
-# flag of herald_kv4_append
-HERALD_KV4_ADVANCE = 1
+# flags of herald_kv4_append and herald_kv8_append
+HERALD_KV4_ADVANCE = HERALD_KV8_ADVANCE = 1
 
 
 def HERALD_ATTN_SMS(n: int) -> int:
@@ -55,7 +55,8 @@ EXPORTS = ("herald_workspace_size", "herald_status_string", "herald_last_error",
            "herald_select_stage2_adaptive", "herald_debug_build", "herald_debug_status",
            "herald_inject_launch_failure", "herald_block", "herald_kv4_append",
            "herald_kv4_attn", "herald_kv4_gather", "herald_workspace_size_kv4",
-           "herald_selftest_kv4_wait")
+           "herald_selftest_kv4_wait", "herald_kv8_append", "herald_kv8_attn",
+           "herald_kv8_gather", "herald_workspace_size_kv8")
 
 
 class HeraldError(RuntimeError):
@@ -90,6 +91,13 @@ class Kv4(C.Structure):
                 ("v_scale", C.c_float)]
 
 
+class Kv8(C.Structure):
+    """herald_kv8: a paged 8-bit cache (made by kv8())."""
+    _fields_ = [("page", C.c_int), ("block", C.c_int), ("n_pages", C.c_int), ("max_pages", C.c_int),
+                ("table", C.c_void_p), ("k_codes", C.c_void_p), ("k_scales", C.c_void_p),
+                ("v_codes", C.c_void_p), ("v_scales", C.c_void_p)]
+
+
 class Rope(C.Structure):
     """herald_rope: the position rotation (made by rope())."""
     _fields_ = [("cos_sin", C.c_void_p), ("n_pos", C.c_int), ("rot", C.c_int),
@@ -117,6 +125,29 @@ def kv4(page, table, k_codes, k_scales, v_codes, v_scales, k_scale=1.0, v_scale=
             float(k_scale), float(v_scale))
     s._keep = (table, arrays)
     s._shape = (int(table.shape[0]), int(k_codes.shape[1]), 2 * int(k_codes.shape[3]))
+    return s
+
+
+def kv8(page, block, table, k_codes, k_scales, v_codes, v_scales) -> Kv8:
+    """The Kv8 of contiguous tensors: table [N, max_pages] int32, codes
+    [n_pages, Hkv, page, d] and scales [n_pages, Hkv, page/block] of one byte
+    each.  The struct keeps the tensors alive."""
+    codes, scales, page, block = (k_codes, v_codes), (k_scales, v_scales), int(page), int(block)
+    for x, rank in (k_codes, 4), (v_codes, 4), (k_scales, 3), (v_scales, 3):
+        if x.element_size() != 1 or x.dim() != rank or not x.is_contiguous():
+            raise ValueError("codes must be contiguous [n_pages, Hkv, page, d], scales contiguous "
+                             "[n_pages, Hkv, page/block] bytes")
+    n_pages, hkv, rows, d = k_codes.shape
+    if block < 1 or rows != page or v_codes.shape != k_codes.shape or page % block != 0 \
+            or any(x.shape != (n_pages, hkv, page // block) for x in scales):
+        raise ValueError("codes and scales must agree in n_pages, Hkv, page and page/block, alike "
+                         "for K and V")
+    if table.dim() != 2 or table.element_size() != 4 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous [N, max_pages] int32 tensor")
+    s = Kv8(page, block, n_pages, int(table.shape[1]), _p(table), _p(k_codes), _p(k_scales),
+            _p(v_codes), _p(v_scales))
+    s._keep = (table, codes, scales)
+    s._shape = (int(table.shape[0]), int(hkv), int(d))
     return s
 
 
@@ -207,13 +238,22 @@ def lib() -> C.CDLL:
         L.herald_kv4_attn.argtypes = [Dims, vp, C.POINTER(Kv4), vp, vp, vp, vp, C.c_float, vp, sz,
                                       vp]
         L.herald_kv4_gather.argtypes = [Dims, vp, vp, i32, C.POINTER(Kv4), vp, vp, vp]
+        L.herald_kv8_append.argtypes = [Dims, i32, vp, vp, C.c_int64, vp, C.c_int64, vp, C.c_int64,
+                                        C.POINTER(Rope), vp, C.POINTER(Kv8), vp, vp, vp, i32,
+                                        C.c_uint, vp]
+        L.herald_workspace_size_kv8.argtypes = [Dims]
+        L.herald_workspace_size_kv8.restype = sz
+        L.herald_kv8_attn.argtypes = [Dims, vp, C.POINTER(Kv8), vp, vp, vp, vp, C.c_float, vp, sz,
+                                      vp]
+        L.herald_kv8_gather.argtypes = [Dims, vp, vp, i32, C.POINTER(Kv8), vp, vp, vp]
         L.herald_trace_begin.argtypes = [C.POINTER(vp), i32, i32]
         L.herald_trace_end.argtypes = []
         L.herald_trace_name.argtypes = [i32]
         L.herald_trace_name.restype = C.c_char_p
         for name in EXPORTS:
             if name not in ("herald_workspace_size", "herald_workspace_size_exact",
-                            "herald_workspace_size_kv4", "herald_status_string",
+                            "herald_workspace_size_kv4", "herald_workspace_size_kv8",
+                            "herald_status_string",
                             "herald_last_error", "herald_trace_name"):
                 getattr(L, name).restype = C.c_int
         _lib = L
@@ -543,8 +583,8 @@ def _tokens(x, ld, n, t, h, d, what):
     return _p(x), _token_ld(x, ld, what)
 
 
-def _kv4_arg(cache, d, n, hkv, ch):
-    """A cache made by kv4() must be one of the call's shape: with another Hkv,
+def _kv_arg(cache, d, n, hkv, ch):
+    """A cache made by kv4() or kv8() must be one of the call's shape: with another Hkv,
     d or a shorter table the kernels would reach past its arrays."""
     if cache is None:
         return None
@@ -555,63 +595,92 @@ def _kv4_arg(cache, d, n, hkv, ch):
     return C.byref(cache)
 
 
-def herald_kv4_append(d, T, q, k, v, ctx_len, cache, q_rot, k_rot, rope=None, n_tok=None,
-                      pooled=None, Bk=0, flags=0, q_ld=None, k_ld=None, v_ld=None, stream=None):
-    """cache: a Kv4 or None (rotate only); rope: a Rope or None.  The token
-    strides of q, k, v [N, T, heads, d] are taken from the tensors (views of a
-    fused projection's output) unless given."""
-    N, T, Hq, Hkv, ch = d.N, int(T), d.Hq, d.Hkv, d.d
-    if pooled is not None and Bk > 0:
-        blocks = -(-d.L_max // int(Bk))
-        pooled = _arr(pooled, N * Hkv * blocks * ch * 4, (N, Hkv, blocks, ch), 4, "pooled")
-    toks = N * T * ch * 2
-    if T > 1:
-        _axis(q_rot, T, (N, T, Hq, ch), 2, "q_rot")
-        _axis(k_rot, T, (N, T, Hkv, ch), 2, "k_rot")
-    q, q_ld = _tokens(q, q_ld, N, T, Hq, ch, "q")
-    k, k_ld = _tokens(k, k_ld, N, T, Hkv, ch, "k")
-    v, v_ld = _tokens(v, v_ld, N, T, Hkv, ch, "v")
-    _check((_lib or lib()).herald_kv4_append(
-        d, T, _arr(n_tok, 4 * N, (N,), 4, "n_tok"), q, q_ld, k, k_ld, v, v_ld,
-        None if rope is None else C.byref(rope), _arr(ctx_len, 4 * N, (N,), 4, "ctx_len"),
-        _kv4_arg(cache, d, N, Hkv, ch), _arr(q_rot, toks * Hq, (N, T, Hq, ch), 2, "q_rot"),
-        _arr(k_rot, toks * Hkv, (N, T, Hkv, ch), 2, "k_rot"), _p(pooled), int(Bk), int(flags),
-        _s(stream)))
+# The calls of the two paged caches, alike but for the cache (a function made for each: a
+# shared one in between would add to calls of one token, which are bound by the host).
+def _kv_append(entry, doc):
+    def call(d, T, q, k, v, ctx_len, cache, q_rot, k_rot, rope=None, n_tok=None, pooled=None, Bk=0,
+             flags=0, q_ld=None, k_ld=None, v_ld=None, stream=None):
+        N, T, Hq, Hkv, ch = d.N, int(T), d.Hq, d.Hkv, d.d
+        if pooled is not None and Bk > 0:
+            blocks = -(-d.L_max // int(Bk))
+            pooled = _arr(pooled, N * Hkv * blocks * ch * 4, (N, Hkv, blocks, ch), 4, "pooled")
+        toks = N * T * ch * 2
+        if T > 1:
+            _axis(q_rot, T, (N, T, Hq, ch), 2, "q_rot")
+            _axis(k_rot, T, (N, T, Hkv, ch), 2, "k_rot")
+        q, q_ld = _tokens(q, q_ld, N, T, Hq, ch, "q")
+        k, k_ld = _tokens(k, k_ld, N, T, Hkv, ch, "k")
+        v, v_ld = _tokens(v, v_ld, N, T, Hkv, ch, "v")
+        _check(getattr(_lib or lib(), entry)(
+            d, T, _arr(n_tok, 4 * N, (N,), 4, "n_tok"), q, q_ld, k, k_ld, v, v_ld,
+            None if rope is None else C.byref(rope), _arr(ctx_len, 4 * N, (N,), 4, "ctx_len"),
+            _kv_arg(cache, d, N, Hkv, ch), _arr(q_rot, toks * Hq, (N, T, Hq, ch), 2, "q_rot"),
+            _arr(k_rot, toks * Hkv, (N, T, Hkv, ch), 2, "k_rot"), _p(pooled), int(Bk), int(flags),
+            _s(stream)))
+
+    call.__name__ = call.__qualname__ = entry
+    call.__doc__ = doc
+    return call
+
+
+def _kv_attn(entry, doc):
+    def call(d, q, cache, ctx_len, block_k, block_v, out, scale=0.0, ws=None, ws_bytes=None,
+             stream=None):
+        N, B, Hq, Hkv, ch = d.N, d.B, d.Hq, d.Hkv, d.d
+        toks = N * B * ch * 2
+        if B > 1:
+            for x, h, what in (q, Hq, "q"), (block_k, Hkv, "block_k"), (block_v, Hkv, "block_v"), \
+                    (out, Hq, "out"):
+                _axis(x, B, (N, B, h, ch), 2, what)
+        _check(getattr(_lib or lib(), entry)(
+            d, _arr(q, toks * Hq, (N, B, Hq, ch), 2, "q"), _kv_arg(cache, d, N, Hkv, ch),
+            _arr(ctx_len, 4 * N, (N,), 4, "ctx_len"),
+            _arr(block_k, toks * Hkv, (N, B, Hkv, ch), 2, "block_k"),
+            _arr(block_v, toks * Hkv, (N, B, Hkv, ch), 2, "block_v"),
+            _arr(out, toks * Hq, (N, B, Hq, ch), 2, "out"), float(scale), _p(ws),
+            _nbytes(ws, ws_bytes), _s(stream)))
+
+    call.__name__ = call.__qualname__ = entry
+    call.__doc__ = doc
+    return call
+
+
+def _kv_gather(entry, doc):
+    def call(d, idx, n_sel, P_max, cache, pool_k, pool_v=None, stream=None):
+        N, Hkv, ch, P = d.N, d.Hkv, d.d, int(P_max)
+        rows = N * Hkv * P
+        if Hkv > 1:
+            _axis(pool_k, Hkv, (N, Hkv, P, ch), 2, "pool_k")
+        _check(getattr(_lib or lib(), entry)(
+            d, _arr(idx, rows * 4, (N, Hkv, P), 4, "idx"),
+            _arr(n_sel, N * Hkv * 4, (N, Hkv), 4, "n_sel"), P, _kv_arg(cache, d, N, Hkv, ch),
+            _arr(pool_k, rows * ch * 2, (N, Hkv, P, ch), 2, "pool_k"),
+            _arr(pool_v, rows * ch * 2, (N, Hkv, P, ch), 2, "pool_v"), _s(stream)))
+
+    call.__name__ = call.__qualname__ = entry
+    call.__doc__ = doc
+    return call
+
+
+herald_kv4_append = _kv_append("herald_kv4_append", """cache: a Kv4 or None (rotate only); rope: a Rope
+    or None.  The token strides of q, k, v [N, T, heads, d] are taken from the tensors (views of a
+    fused projection's output) unless given.""")
+herald_kv8_append = _kv_append("herald_kv8_append", "herald_kv4_append with a Kv8 (or None: rotate only).")
 
 
 def herald_workspace_size_kv4(d: Dims) -> int:
     return int(lib().herald_workspace_size_kv4(d))
 
 
-def herald_kv4_attn(d, q, cache, ctx_len, block_k, block_v, out, scale=0.0, ws=None,
-                    ws_bytes=None, stream=None):
-    """Attention over a paged 4-bit cache (a Kv4) and, unless both are None,
-    the block's own keys and values; every tensor dense, as in include/herald.h."""
-    N, B, Hq, Hkv, ch = d.N, d.B, d.Hq, d.Hkv, d.d
-    toks = N * B * ch * 2
-    if B > 1:
-        for x, h, what in (q, Hq, "q"), (block_k, Hkv, "block_k"), (block_v, Hkv, "block_v"), \
-                (out, Hq, "out"):
-            _axis(x, B, (N, B, h, ch), 2, what)
-    _check((_lib or lib()).herald_kv4_attn(
-        d, _arr(q, toks * Hq, (N, B, Hq, ch), 2, "q"), _kv4_arg(cache, d, N, Hkv, ch),
-        _arr(ctx_len, 4 * N, (N,), 4, "ctx_len"),
-        _arr(block_k, toks * Hkv, (N, B, Hkv, ch), 2, "block_k"),
-        _arr(block_v, toks * Hkv, (N, B, Hkv, ch), 2, "block_v"),
-        _arr(out, toks * Hq, (N, B, Hq, ch), 2, "out"), float(scale), _p(ws),
-        _nbytes(ws, ws_bytes), _s(stream)))
+def herald_workspace_size_kv8(d: Dims) -> int:
+    return int(lib().herald_workspace_size_kv8(d))
 
 
-def herald_kv4_gather(d, idx, n_sel, P_max, cache, pool_k, pool_v=None, stream=None):
-    N, Hkv, ch, P = d.N, d.Hkv, d.d, int(P_max)
-    rows = N * Hkv * P
-    if Hkv > 1:
-        _axis(pool_k, Hkv, (N, Hkv, P, ch), 2, "pool_k")
-    _check((_lib or lib()).herald_kv4_gather(
-        d, _arr(idx, rows * 4, (N, Hkv, P), 4, "idx"),
-        _arr(n_sel, N * Hkv * 4, (N, Hkv), 4, "n_sel"), P, _kv4_arg(cache, d, N, Hkv, ch),
-        _arr(pool_k, rows * ch * 2, (N, Hkv, P, ch), 2, "pool_k"),
-        _arr(pool_v, rows * ch * 2, (N, Hkv, P, ch), 2, "pool_v"), _s(stream)))
+herald_kv4_attn = _kv_attn("herald_kv4_attn", """Attention over a paged 4-bit cache (a Kv4) and, unless
+    both are None, the block's own keys and values; every tensor dense, as in include/herald.h.""")
+herald_kv8_attn = _kv_attn("herald_kv8_attn", "herald_kv4_attn over a paged 8-bit cache (a Kv8).")
+herald_kv4_gather = _kv_gather("herald_kv4_gather", "Rows of a paged 4-bit cache (a Kv4) as bf16.")
+herald_kv8_gather = _kv_gather("herald_kv8_gather", "Rows of a paged 8-bit cache (a Kv8) as bf16.")
 
 
 class Trace:

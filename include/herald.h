@@ -589,6 +589,67 @@ herald_status herald_kv4_gather(herald_dims dims, const int32_t *idx, const int3
                                 int P_max, const herald_kv4 *cache, uint16_t *pool_k,
                                 uint16_t *pool_v, void *stream);
 
+/* A paged KV cache held in 8 bits (the pages have no counterpart; between the
+ * 4-bit cache above and the bf16 rows).  A row -- one position of one KV head --
+ * is d bytes of e4m3 codes; `block` consecutive positions of a KV head share one
+ * power-of-two scale, held as a byte (e8m0: 2^(byte - 127)):
+ *   value = code * 2^(byte - 127).
+ * A code is a float of its own, so a power of two costs it nothing, every held
+ * value is exact in bf16, and rows are held anew under a larger scale without a
+ * loss but for e4m3's subnormals (2^-9 of the scale).  Scale bytes lie in [95, 159]
+ * (2^-32 to 2^32): the calls write no others and read others as the nearer of
+ * the two.  Pages, the table and positions without a page: as in herald_kv4.
+ *   page               positions per page: 16, 32, 64 or 128
+ *   block              positions per scale: 16, 32, 64 or 128, at most page
+ *   n_pages, max_pages, table   as in herald_kv4
+ *   k_codes, v_codes   [n_pages][Hkv][page][d] device
+ *   k_scales, v_scales [n_pages][Hkv][page/block] device, of any alignment */
+typedef struct {
+  int page, block, n_pages, max_pages;
+  const int32_t *table;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+} herald_kv8;
+
+#define HERALD_KV8_ADVANCE 1u /* ctx_len[n] += the tokens appended */
+
+/* Rotates queries and keys and appends keys and values to a paged 8-bit cache
+ * in one pass: herald_kv4_append's arguments, tokens, rotation and rules, with
+ *   q_rot, k_rot = x' rounded to bf16, and the cache takes that k_rot and v.
+ * Per block of positions, KV head, and K or V, with e the block's exponent:
+ *   e    the smallest in [-32, 32] with max|x| <= 448 2^e over the block's new
+ *        rows (infinities and NaNs do not count; -32 for zeros), and not below
+ *        the block's old exponent where it holds rows before ctx_len[n]
+ *   new rows     code = e4m3(x 2^-e), to nearest even, past 448 to 448 (so an
+ *                infinity is held as 448 2^e; a NaN stays one, alone)
+ *   older rows of the block, where e grew: code = e4m3(code 2^(old e - e))
+ * so the held bytes are defined to the bit.  Rows before ctx_len[n] in the
+ * block that token 0 falls into must have been appended before; rows after the
+ * tokens keep their bytes.
+ *   pooled   as there: the means of the rows as held, refreshed for the blocks of
+ *            Bk that the tokens fall into (other blocks' means stay, also where
+ *            their rows are held anew) */
+herald_status herald_kv8_append(herald_dims dims, int T, const int32_t *n_tok, const uint16_t *q,
+                                int64_t q_ld, const uint16_t *k, int64_t k_ld, const uint16_t *v,
+                                int64_t v_ld, const herald_rope *rope, int32_t *ctx_len,
+                                const herald_kv8 *cache, uint16_t *q_rot, uint16_t *k_rot,
+                                float *pooled, int Bk, unsigned flags, void *stream);
+
+/* Full attention of a block's queries over a paged 8-bit cache, and where given
+ * the block's own B keys in bf16: herald_kv4_attn with a herald_kv8.
+ *   ws       herald_workspace_size_kv8(dims) bytes (0 = unsupported shape) */
+size_t herald_workspace_size_kv8(herald_dims dims);
+herald_status herald_kv8_attn(herald_dims dims, const uint16_t *q, const herald_kv8 *cache,
+                              const int32_t *ctx_len, const uint16_t *block_k,
+                              const uint16_t *block_v, uint16_t *out, float scale, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/* Rows of a paged 8-bit cache as bf16, exactly: herald_kv4_gather with a
+ * herald_kv8: the sparse pool, stage 2's candidates, or with idx = 0, 1, 2, ...
+ * the whole cache read back. */
+herald_status herald_kv8_gather(herald_dims dims, const int32_t *idx, const int32_t *n_sel,
+                                int P_max, const herald_kv8 *cache, uint16_t *pool_k,
+                                uint16_t *pool_v, void *stream);
+
 /* Self-test of the device-side failure path (the pages have no
  * counterpart).  Every wait inside the library's kernels gives up after
  * about one second, records a code in the workspace's error word and lets
