@@ -530,7 +530,8 @@ herald_status herald_debug_status(uint32_t* code) {
   HERALD_TRY_CUDA(cudaDeviceSynchronize(), "device synchronize");
   *code = debug_take_select() | debug_take_tc() | debug_take_move() | debug_take_blocks() |
           debug_take_flash() | debug_take_kv4_move() | debug_take_kv4_attn() |
-          debug_take_kv4_attn_tc() | debug_take_kv8_move() | debug_take_kv8_attn();
+          debug_take_kv4_attn_tc() | debug_take_kv8_move() | debug_take_kv8_attn() |
+          debug_take_kv8_rows();
 #endif
   return HERALD_OK;
 }
@@ -867,6 +868,24 @@ static herald_status check_kv8(const herald_dims& dm, const herald_kv8* c, Kv8De
   return HERALD_OK;
 }
 
+// Tensor map of a cache's codes [n_pages][Hkv*page][d] with a box of one page of one head,
+// rows swizzled among themselves as the tensor cores take them.
+static herald_status encode_kv8_map(const uint8_t* codes, const herald_dims& dm,
+                                    const herald_kv8& c, CUtensorMap* map) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(HERALD_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const cuuint64_t ext[3] = {cuuint64_t(dm.d), cuuint64_t(dm.Hkv) * c.page, cuuint64_t(c.n_pages)};
+  const cuuint64_t strides[2] = {ext[0], ext[0] * ext[1]};
+  const cuuint32_t box[3] = {cuuint32_t(dm.d), cuuint32_t(c.page), 1}, one[3] = {1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), ext, strides, box, one,
+         CU_TENSOR_MAP_INTERLEAVE_NONE,
+         dm.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(HERALD_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return HERALD_OK;
+}
+
 herald_status herald_kv8_append(herald_dims dims, int T, const int32_t* n_tok, const uint16_t* q,
                                 int64_t q_ld, const uint16_t* k, int64_t k_ld, const uint16_t* v,
                                 int64_t v_ld, const herald_rope* rope, int32_t* ctx_len,
@@ -915,7 +934,10 @@ herald_status herald_kv8_attn(herald_dims dims, const uint16_t* q, const herald_
   const size_t need = kv8_attn_workspace(dims);
   if (ws_bytes < need)
     return fail(HERALD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
-  HERALD_TRY_CUDA(launch_kv8_attn(dims, q, c, ctx_len, block_k, block_v, out,
+  CUtensorMap kmap, vmap;
+  HERALD_RET_IF(encode_kv8_map(cache->k_codes, dims, *cache, &kmap));
+  HERALD_RET_IF(encode_kv8_map(cache->v_codes, dims, *cache, &vmap));
+  HERALD_TRY_CUDA(launch_kv8_attn(dims, q, c, kmap, vmap, ctx_len, block_k, block_v, out,
                                   scale > 0.f ? scale : 1.f / sqrtf(float(dims.d)), ws, sm_count(),
                                   static_cast<cudaStream_t>(stream)),
                   "kv8 attention launch");

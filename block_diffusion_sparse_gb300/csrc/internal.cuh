@@ -132,6 +132,7 @@ uint32_t debug_take_kv4_attn();
 uint32_t debug_take_kv4_attn_tc();
 uint32_t debug_take_kv8_move();
 uint32_t debug_take_kv8_attn();
+uint32_t debug_take_kv8_rows();
 
 // A launch failure injected on the host (herald_inject_launch_failure, a
 // test hook of the error paths): returns the injected error for the launch
@@ -365,8 +366,9 @@ cudaError_t launch_kv8_gather(const herald_dims& dm, const int32_t* idx, const i
                               int P_max, const Kv8Dev& c, uint16_t* pk, uint16_t* pv, int num_sms,
                               cudaStream_t st);
 size_t kv8_attn_workspace(const herald_dims& dm);
+// kmap, vmap: the codes as [n_pages][Hkv*page][d], box one page of one head
 cudaError_t launch_kv8_attn(const herald_dims& dm, const uint16_t* q, const Kv8Dev& c,
-                            const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
+                            const CUtensorMap& kmap, const CUtensorMap& vmap, const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
                             uint16_t* out, float scale, void* ws, int num_sms, cudaStream_t st);
 
 // The append of a decoded block, done inside another kernel: the rows of

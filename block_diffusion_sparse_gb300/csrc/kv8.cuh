@@ -58,6 +58,10 @@ struct Kv8AttnArgs {
   int pad;       // what a piece costs beside its tiles, in tiles (kv4_units)
   Kv8Dev c;
 };
+// The kernel for `rows` <= kKv8FewRows query rows per KV head (kv8_rows.cu).
+constexpr int kKv8FewRows = 32;
+cudaError_t launch_kv8_rows(int d, int rows, const Kv8AttnArgs& a, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, uint32_t* err, cudaStream_t st);
 
 // The pieces of a CTA's share, in order: body(n, g, seg, ctx, u0, u1) with tiles
 // u0 <= u < u1 of 128 cache positions; it returns false to leave.

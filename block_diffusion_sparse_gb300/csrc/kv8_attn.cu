@@ -240,7 +240,7 @@ static Kv8Ws kv8_ws(const herald_dims& dm) {
 size_t kv8_attn_workspace(const herald_dims& dm) { return kv8_ws(dm).total; }
 
 cudaError_t launch_kv8_attn(const herald_dims& dm, const uint16_t* q, const Kv8Dev& c,
-                            const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
+                            const CUtensorMap& kmap, const CUtensorMap& vmap, const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
                             uint16_t* out, float scale, void* ws, int num_sms, cudaStream_t st) {
   const int G = dm.Hq / dm.Hkv, R = dm.B * G;
   const Kv8Ws w = kv8_ws(dm);
@@ -254,10 +254,16 @@ cudaError_t launch_kv8_attn(const herald_dims& dm, const uint16_t* q, const Kv8D
   a.c = c;
   a.ctas = std::min(kKv8MaxCtas, num_sms);
   a.pad = 0;
-  const size_t smem = size_t(R) * (dm.d + 2) * 4;
-  auto* kernel = dm.d == 128 ? kv8_attn_kernel<128> : kv8_attn_kernel<64>;
-  HERALD_CHECK_LAUNCH(ensure_smem(kernel, smem));
-  HERALD_CHECK_LAUNCH(launch_k("kv8_attn_kernel", kernel, dim3(unsigned(a.ctas)), dim3(128), smem, st, a));
+  uint32_t* err = reinterpret_cast<uint32_t*>(p);
+  if (R <= kKv8FewRows) {
+    HERALD_CHECK_LAUNCH(launch_kv8_rows(dm.d, R, a, kmap, vmap, err, st));
+  } else {
+    const size_t smem = size_t(R) * (dm.d + 2) * 4;
+    auto* kernel = dm.d == 128 ? kv8_attn_kernel<128> : kv8_attn_kernel<64>;
+    HERALD_CHECK_LAUNCH(ensure_smem(kernel, smem));
+    HERALD_CHECK_LAUNCH(
+        launch_k("kv8_attn_kernel", kernel, dim3(unsigned(a.ctas)), dim3(128), smem, st, a));
+  }
   HERALD_CHECK_LAUNCH(dm.d == 128 ? launch_join<128>(a, R, num_sms, st)
                                   : launch_join<64>(a, R, num_sms, st));
   return cudaGetLastError();

@@ -31,6 +31,8 @@ enum : uint32_t {
   DEV_K_ATTN_FLASH = 8u << 8,
   DEV_K_KV4_ATTN = 9u << 8,
   DEV_K_KV4_ROWS = 10u << 8,
+  DEV_K_KV8_ROWS = 11u << 8,
+  DEV_K_KV8_ATTN = 12u << 8,
 };
 
 // Checks of the debug build (compiled with -DHERALD_DEBUG): a kernel compares
@@ -271,6 +273,17 @@ HERALD_DEV void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, 
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs (32 of K an instruction), fp32
+// accumulator.
+HERALD_DEV void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Arrive once on the mbarrier when all previously issued tcgen05.mma of this
 // thread have completed.
 HERALD_DEV void umma_commit(uint64_t* bar) {
@@ -346,6 +359,13 @@ __host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, bool a_mn_m
          (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
+// Instruction descriptor, kind::f8f6f4 with e4m3 A/B (formats 0) and fp32 D.
+__host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N, bool a_mn_major,
+                                                       bool b_mn_major) {
+  return (1u << 4) | (uint32_t(a_mn_major) << 15) | (uint32_t(b_mn_major) << 16) |
+         (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
 // Shared-memory matrix descriptor for a 128-byte-swizzled operand.
 //   [0,14) start address >> 4   [16,30) leading byte offset >> 4
 //   [32,46) stride byte offset >> 4   [46,48) = 1 (descriptor version)
@@ -361,6 +381,22 @@ HERALD_DEV uint64_t make_sdesc_sw128(uint32_t saddr, uint32_t lbo_bytes, uint32_
   d |= uint64_t(1) << 46;
   d |= uint64_t(2) << 61;
   return d;
+}
+
+// The same for rows of Bytes = 32, 64 or 128 swizzled among themselves (layouts 6, 4
+// and 2): 8-row groups are 8 * Bytes apart, K-major and MN-major alike, and no operand
+// is wider than a row.
+template <int Bytes>
+HERALD_DEV uint64_t make_sdesc_rows(uint32_t saddr) {
+  static_assert(Bytes == 32 || Bytes == 64 || Bytes == 128, "row bytes");
+  return uint64_t((saddr >> 4) & 0x3FFFu) | uint64_t(1) << 16 | uint64_t(Bytes / 2) << 32 |
+         uint64_t(1) << 46 | uint64_t(Bytes == 128 ? 2 : Bytes == 64 ? 4 : 6) << 61;
+}
+// Byte offset of 16-byte chunk `c` of row `r` in such rows.
+template <int Bytes>
+HERALD_DEV uint32_t rows_off(uint32_t r, uint32_t c) {
+  const uint32_t x = Bytes == 128 ? r & 7u : Bytes == 64 ? r >> 1 & 3u : r >> 2 & 1u;
+  return r * uint32_t(Bytes) + ((c ^ x) << 4);
 }
 
 // Byte offset of 16-byte chunk `c` (0..7) of row `r` inside a 128B-swizzled

@@ -108,7 +108,7 @@ herald_status herald_inject_launch_failure(int after, int cuda_error);
  * bits 8-15: the kernel (1 refine pass 1, 2 refine pass 2, 3 fused refine,
  * 4 split attention, 5 cluster attention, 6 pool attention, 7 stage-1 scan,
  * 8 pipelined attention, 9 and 10 attention over a paged 4-bit cache, many
- * and few rows);
+ * and few rows, 11 and 12 over a paged 8-bit one, few and many rows);
  * bits 16-31: which of the kernel's waits (the
  * pipelined attention: 0x1 K ring slot, 0x2 V ring slot, 0x4 query tile,
  * 0x8 K tile, 0x10 S buffer free, 0x20 P ready, 0x40 V tile, 0x80 S ready,
