@@ -530,7 +530,7 @@ herald_status herald_debug_status(uint32_t* code) {
   HERALD_TRY_CUDA(cudaDeviceSynchronize(), "device synchronize");
   *code = debug_take_select() | debug_take_tc() | debug_take_move() | debug_take_blocks() |
           debug_take_flash() | debug_take_kv4_move() | debug_take_kv4_attn() |
-          debug_take_kv4_attn_tc() | debug_take_kv8_move() | debug_take_kv8_attn() |
+          debug_take_kv4_attn_tc() | debug_take_kv8_move() | debug_take_kv8_attn_tc() |
           debug_take_kv8_rows();
 #endif
   return HERALD_OK;

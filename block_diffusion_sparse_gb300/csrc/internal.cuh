@@ -131,7 +131,7 @@ uint32_t debug_take_kv4_move();
 uint32_t debug_take_kv4_attn();
 uint32_t debug_take_kv4_attn_tc();
 uint32_t debug_take_kv8_move();
-uint32_t debug_take_kv8_attn();
+uint32_t debug_take_kv8_attn_tc();
 uint32_t debug_take_kv8_rows();
 
 // A launch failure injected on the host (herald_inject_launch_failure, a

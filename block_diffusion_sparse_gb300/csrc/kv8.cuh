@@ -46,6 +46,21 @@ HERALD_DEV uint32_t float2_to_e4m3(float lo, float hi) {
   return r;
 }
 
+// A query row as e4m3 numbers: values are multiplied by *up, the power of two that
+// brings the row's largest magnitude mx to [2^7, 2^8), and *f turns a product with a
+// key's codes into a log2-unit score (`scale` has log2(e) in it).  (mx below 2^-112
+// counts as that, infinities as 2^127; *f stays positive and finite, also times a key's
+// scale: a masked score of -inf times 0, or a zero score times inf, would be NaN.)
+HERALD_DEV void kv8_query_scale(float mx, float scale, float* up, float* f) {
+  const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -112), 127);
+  *up = exp2_int(7 - e);
+  *f = fminf(fmaxf(scale * exp2_int(e - 7), 0x1p-90f), 0x1p90f);
+}
+// One value of it; an infinity becomes a NaN, as inf - inf makes one of its row.
+HERALD_DEV float kv8_query(float x, float up) {
+  return fabsf(x) < INFINITY ? x * up : __uint_as_float(0x7FC00000u);
+}
+
 // ---- attention arguments shared by its kernels
 struct Kv8AttnArgs {
   const uint16_t *q, *bk, *bv;
@@ -55,6 +70,7 @@ struct Kv8AttnArgs {
   float2* ml;    // [slots][R16]
   float scale;   // softmax scale times log2(e): scores are in log2 units
   int N, Hq, Hkv, B, L_max, R16, ctas;
+  int row_tiles; // of 128 rows (1 with few rows): a KV head has that many segments
   int pad;       // what a piece costs beside its tiles, in tiles (kv4_units)
   Kv8Dev c;
 };
@@ -62,24 +78,29 @@ struct Kv8AttnArgs {
 constexpr int kKv8FewRows = 32;
 cudaError_t launch_kv8_rows(int d, int rows, const Kv8AttnArgs& a, const CUtensorMap& kmap,
                             const CUtensorMap& vmap, uint32_t* err, cudaStream_t st);
+// The kernel for more (kv8_attn_tc.cu).
+cudaError_t launch_kv8_attn_tc(int d, const Kv8AttnArgs& a, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, uint32_t* err, cudaStream_t st);
 
-// The pieces of a CTA's share, in order: body(n, g, seg, ctx, u0, u1) with tiles
-// u0 <= u < u1 of 128 cache positions; it returns false to leave.
+// The pieces of a CTA's share, in order: body(n, gt, seg, ctx, u0, u1) with gt = g *
+// row_tiles + row tile, seg = n * Hkv * row_tiles + gt, tiles u0 <= u < u1 of 128 cache
+// positions; it returns false to leave.
 template <typename Body>
 HERALD_DEV void kv8_pieces(const Kv8AttnArgs& a, const Kv4Share& sh, Body&& body) {
+  const int heads = a.Hkv * a.row_tiles;
   int at = sh.at, first = sh.first, n = sh.n;
   while (at < sh.end) {
     const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
     const int units = kv4_units(ctx, a.L_max, 0, a.pad);
-    if (units == 0 || at >= first + a.Hkv * units) {  // the next sequence
-      first += a.Hkv * units;
+    if (units == 0 || at >= first + heads * units) {  // the next sequence
+      first += heads * units;
       ++n;
       continue;
     }
-    const int g = (at - first) / units;
-    const int seg0 = first + g * units;
+    const int gt = (at - first) / units;
+    const int seg0 = first + gt * units;
     const int u0 = max(at - seg0 - a.pad, 0), u1 = min(units, sh.end - seg0) - a.pad;
-    if (u1 > 0 && !body(n, g, n * a.Hkv + g, ctx, u0, u1)) return;
+    if (u1 > 0 && !body(n, gt, n * heads + gt, ctx, u0, u1)) return;
     at = seg0 + a.pad + u1;
   }
 }

@@ -1,7 +1,7 @@
 // kv8_attn.cu -- attention of a block's queries over the whole paged 8-bit cache and
-// the block's own bf16 keys.  One kernel writes partial results over the cache's keys
-// (m, l, O per query row and piece of a segment), the join adds the block's own keys
-// and writes the output.
+// the block's own bf16 keys: a kernel for few or many query rows (kv8_rows.cu,
+// kv8_attn_tc.cu) writes partial results over the cache's keys (m, l, O per query row
+// and piece of a segment), the join here adds the block's own keys and writes the output.
 #include <float.h>
 #include <math.h>
 
@@ -9,81 +9,7 @@
 
 namespace herald {
 
-constexpr int kKv8MaxCtas = 608;  // most attention CTAs (workspace slots)
-
-// One CTA walks its share of the keys in tiles of 128, a thread per key for the
-// scores and per channel for the output; everything in fp32.
-template <int D>
-__global__ void __launch_bounds__(128) kv8_attn_kernel(const Kv8AttnArgs a) {
-  extern __shared__ float sm[];
-  __shared__ float qs[D], ps[128], red[4];
-  __shared__ int rows[128];
-  __shared__ float vsc[128];
-  griddep_enter();
-  const int G = a.Hq / a.Hkv, R = a.B * G, t = threadIdx.x;
-  float *O = sm, *ml = sm + R * D;  // [R][D], [R][2]
-  const Kv4Share sh = kv4_share(a.ctx, a.N, a.L_max, a.Hkv, a.ctas, a.pad, 0, int(blockIdx.x));
-  kv8_pieces(a, sh, [&](int n, int g, int seg, int ctx, int u0, int u1) -> bool {
-    for (int i = t; i < R * D; i += 128) O[i] = 0.f;
-    for (int i = t; i < R; i += 128) ml[2 * i] = -FLT_MAX, ml[2 * i + 1] = 0.f;
-    __syncthreads();
-    for (int u = u0; u < u1; ++u) {
-      const int pos = u * 128 + t;
-      int phys = -1;
-      float ks = 0.f;
-      if (pos < ctx) phys = kv8_page(a.c, n, pos >> a.c.page_log2);
-      debug_flag(pos < ctx && phys < 0, DEV_BAD_INDEX);
-      if (phys >= 0) {
-        const size_t sc = kv8_scale(a.c, phys, a.Hkv, g, pos);
-        ks = exp2_int(kv8_exp(a.c.ks[sc]));
-        vsc[t] = exp2_int(kv8_exp(a.c.vs[sc]));
-      }
-      rows[t] = phys;
-      const uint8_t* kr = a.c.kc + (phys >= 0 ? kv8_row(a.c, phys, a.Hkv, g, pos) * D : 0);
-      for (int r = 0; r < R; ++r) {
-        __syncthreads();
-        if (t < D)
-          qs[t] = bf16lo(a.q[((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + t]);
-        __syncthreads();
-        float s = 0.f;
-        if (phys >= 0)
-          for (int c = 0; c < D; ++c) s = fmaf(qs[c], e4m3_to_float(kr[c]), s);
-        s = phys >= 0 ? s * (ks * a.scale) : -INFINITY;
-        float mx = warp_max(s);
-        if ((t & 31) == 0) red[t >> 5] = mx;
-        __syncthreads();
-        mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float m0 = ml[2 * r], m1 = fmaxf(m0, mx);
-        const float p = exp2f(s - m1);
-        ps[t] = p;
-        const float sum = warp_sum(p);
-        __syncthreads();
-        if ((t & 31) == 0) red[t >> 5] = sum;
-        __syncthreads();
-        const float k = exp2f(m0 - m1);
-        if (t < D) {
-          float o = O[r * D + t] * k;
-          for (int j = 0; j < 128; ++j)
-            if (rows[j] >= 0)
-              o = fmaf(ps[j] * vsc[j],
-                       e4m3_to_float(a.c.vc[kv8_row(a.c, rows[j], a.Hkv, g, u * 128 + j) * D + t]), o);
-          O[r * D + t] = o;
-        }
-        if (t == 0) {
-          ml[2 * r] = m1;
-          ml[2 * r + 1] = ml[2 * r + 1] * k + red[0] + red[1] + red[2] + red[3];
-        }
-      }
-      __syncthreads();
-    }
-    const size_t slot = size_t(blockIdx.x) + seg;
-    for (int i = t; i < R * D; i += 128) a.opart[slot * a.R16 * D + i] = O[i];
-    for (int i = t; i < R; i += 128)
-      a.ml[slot * a.R16 + i] = make_float2(ml[2 * i], ml[2 * i + 1]);
-    __syncthreads();
-    return true;
-  });
-}
+constexpr int kKv8MaxCtas = 304;  // most attention CTAs (workspace slots)
 
 // The output: the pieces of a segment joined, with the block's own keys.  grid (N*Hkv,
 // ceil(R / Rows)); D/4 lanes hold a row's channels, four each, and Threads over Rows
@@ -104,9 +30,10 @@ __global__ void __launch_bounds__(Threads) kv8_join_kernel(const Kv8AttnArgs a) 
   const int c4 = threadIdx.x % TPR, rr = threadIdx.x / TPR % Rows, grp = threadIdx.x / (TPR * Rows);
   const int r = int(blockIdx.y) * Rows + rr, rc = min(r, R - 1);
   const size_t row = (size_t(n) * a.B + rc / G) * a.Hq + g * G + rc % G;
-  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, 0, a.pad), a.Hkv, a.ctas);
-  const int units = kv4_units(a.ctx[n], a.L_max, 0, a.pad);
-  const int first = a.Hkv * kv4_total_units(a.ctx, n, a.L_max, 0, a.pad) + g * units;
+  const int heads = a.Hkv * a.row_tiles, tile = rc / a.R16, rt = rc - tile * a.R16;
+  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, 0, a.pad), heads, a.ctas);
+  const int units = kv4_units(a.ctx[n], a.L_max, 0, a.pad), gt = g * a.row_tiles + tile;
+  const int first = heads * kv4_total_units(a.ctx, n, a.L_max, 0, a.pad) + gt * units;
   float M = -FLT_MAX, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.bk) {
@@ -158,8 +85,9 @@ __global__ void __launch_bounds__(Threads) kv8_join_kernel(const Kv8AttnArgs a) 
   }
   griddep_enter();
   if (units > 0) {
-    const int c0 = (first + a.pad) / split.share + seg, c1 = (first + units - 1) / split.share + seg;
-    const float4* op = reinterpret_cast<const float4*>(a.opart) + size_t(rc) * (D / 4) + c4;
+    const int c0 = (first + a.pad) / split.share + n * heads + gt,
+              c1 = (first + units - 1) / split.share + n * heads + gt;  // slots of its pieces
+    const float4* op = reinterpret_cast<const float4*>(a.opart) + size_t(rt) * (D / 4) + c4;
     constexpr int kFly = 5;
     for (int c = c0 + grp; c <= c1; c += kFly * GR) {
       float2 p[kFly];
@@ -169,7 +97,7 @@ __global__ void __launch_bounds__(Threads) kv8_join_kernel(const Kv8AttnArgs a) 
         const int ci = c + i * GR;
         p[i] = make_float2(-FLT_MAX, 0.f), x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (ci <= c1) {
-          p[i] = a.ml[size_t(ci) * a.R16 + rc];
+          p[i] = a.ml[size_t(ci) * a.R16 + rt];
           x[i] = op[size_t(ci) * a.R16 * (D / 4)];
         }
       }
@@ -226,12 +154,14 @@ static cudaError_t launch_join(const Kv8AttnArgs& a, int R, int num_sms, cudaStr
 // Workspace: error word, then (m, l) and O of every partial.
 struct Kv8Ws {
   size_t ml, opart, total;
-  int R16;
+  int R16, row_tiles;
 };
 static Kv8Ws kv8_ws(const herald_dims& dm) {
   Kv8Ws w;
-  w.R16 = cdiv(dm.B * (dm.Hq / dm.Hkv), 16) * 16;
-  const size_t slots = size_t(kKv8MaxCtas) + size_t(dm.N) * dm.Hkv;
+  const int R = dm.B * (dm.Hq / dm.Hkv);
+  w.row_tiles = cdiv(R, kTileM);
+  w.R16 = std::min(cdiv(R, 16) * 16, kTileM);
+  const size_t slots = size_t(kKv8MaxCtas) + size_t(dm.N) * dm.Hkv * w.row_tiles;
   w.ml = 256;
   w.opart = align_up(w.ml + slots * w.R16 * 8, 256);
   w.total = w.opart + slots * w.R16 * size_t(dm.d) * 4;
@@ -250,25 +180,18 @@ cudaError_t launch_kv8_attn(const herald_dims& dm, const uint16_t* q, const Kv8D
   a.ml = reinterpret_cast<float2*>(p + w.ml);
   a.opart = reinterpret_cast<float*>(p + w.opart);
   a.scale = scale * 1.4426950408889634f;
-  a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max, a.R16 = w.R16;
+  a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max, a.R16 = w.R16, a.row_tiles = w.row_tiles;
   a.c = c;
   a.ctas = std::min(kKv8MaxCtas, num_sms);
   a.pad = 0;
   uint32_t* err = reinterpret_cast<uint32_t*>(p);
-  if (R <= kKv8FewRows) {
+  if (R <= kKv8FewRows)
     HERALD_CHECK_LAUNCH(launch_kv8_rows(dm.d, R, a, kmap, vmap, err, st));
-  } else {
-    const size_t smem = size_t(R) * (dm.d + 2) * 4;
-    auto* kernel = dm.d == 128 ? kv8_attn_kernel<128> : kv8_attn_kernel<64>;
-    HERALD_CHECK_LAUNCH(ensure_smem(kernel, smem));
-    HERALD_CHECK_LAUNCH(
-        launch_k("kv8_attn_kernel", kernel, dim3(unsigned(a.ctas)), dim3(128), smem, st, a));
-  }
+  else
+    HERALD_CHECK_LAUNCH(launch_kv8_attn_tc(dm.d, a, kmap, vmap, err, st));
   HERALD_CHECK_LAUNCH(dm.d == 128 ? launch_join<128>(a, R, num_sms, st)
                                   : launch_join<64>(a, R, num_sms, st));
   return cudaGetLastError();
 }
-
-HERALD_DEBUG_WORD_READER(debug_take_kv8_attn)
 
 }  // namespace herald

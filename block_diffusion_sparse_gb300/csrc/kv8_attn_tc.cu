@@ -1,0 +1,595 @@
+// kv8_attn_tc.cu -- attention over the paged 8-bit cache on the 5th-generation tensor
+// cores for blocks of queries (many rows per KV head).
+//
+// A CTA takes 128 query rows of a KV head (a row tile) and walks its share of the keys
+// in tiles of 128:
+//   S [128 rows x 128 keys] = Q K^T    kind::f8f6f4: K's codes as they are held, Q in
+//                                      tensor memory as two e4m3 numbers a value, q0 +
+//                                      q1 (a bf16 has 8 bits, e4m3 4), one product each
+//   O [128 rows x d]       += P V      kind::f16: P fp16 in tensor memory over the
+//                                      scores, V's codes turned into fp16 (exact)
+// (P as e4m3 numbers, V as it is held, would take no conversion of V, 450 warp
+// instructions a tile, but splitting 128 x 128 weights takes some 1500 more than
+// packing them.)  Q in tensor memory keeps 64 KB a tile off shared memory, whose
+// bandwidth would be the bound: 144 KB a tile as it is (copies 32, K twice 32, V read
+// 16, written 32 and read as fp16 32).
+//   warps 0-3, 4-7  softmax: a thread per row and half of the tile's keys; both halves
+//              of a row share its base m (one vote a tile, exchanged where it moves)
+//   warps 8-11 turn V tiles into fp16
+//   warp 12    copies K and V tiles by TMA, looks up pages and scales four tiles ahead
+//   warps 13, 14  issue S and P V
+// Scales: a key's multiplies its scores.  A value's exponent e_v goes into the weight's
+// own, P = 2^(x + e_v - m), and out of the row's sum again, l += P 2^-e_v, so O has one
+// unit and P fills fp16 whatever the values' scales.
+//
+// P = 2^(x + e_v - m) stays in fp16 as long as a thread's 64 of them sum to less than
+// 60000.  Where a sum does not (and at a piece's first tile) the row's largest exponent
+// is looked up, m set 5 below it, O and l follow, and the tile is done again.
+#include <float.h>
+
+#include "kv8.cuh"
+#include "tc_common.cuh"
+
+namespace herald {
+
+constexpr int kKv8TcThreads = 512;  // 16 warps (15 only fills a warpgroup)
+constexpr int kKv8KStages = 5, kKv8VStages = 4;
+// Tiles whose scales and counts are kept for the softmax: K copies run at most five
+// tiles ahead of the scores, those two ahead of P, and look-ups four ahead of copies.
+constexpr int kKv8Metas = 16;
+constexpr float kKv8Below = 5.f, kKv8Top = 60000.f, kKv8TopLog2 = 15.8f;
+
+// Waits of the kernel (bits 16-31 of the error word).
+enum : uint32_t {
+  X8_K_FREE = 1, X8_V_FREE = 2, X8_K_FULL = 4, X8_V_FULL = 8, X8_META = 0x10, X8_Q_FULL = 0x20,
+  X8_S_FULL = 0x40, X8_P_FULL = 0x80, X8_PV_DONE = 0x100, X8_V16_FREE = 0x200,
+  X8_V16_FULL = 0x400
+};
+
+struct Kv8TileMeta {  // per 16 keys: 2^e_k, e_v, 2^-e_v and how many count
+  float sk[8], ev[8], iv[8];
+  uint32_t keys[8];
+};
+
+template <int D>
+struct Kv8Tc {
+  static constexpr uint32_t kTile = 128u * D;          // bytes of 128 keys as held
+  static constexpr uint32_t kTile16 = uint32_t(D / 64) * 16384u;  // as fp16
+  static constexpr uint32_t kV = kKv8KStages * kTile, kV16 = kV + kKv8VStages * kTile;
+  static constexpr uint32_t kSmem = kV16 + 2 * kTile16 + 1024;
+};
+// Tensor memory: two S (and P) buffers, O, q0, q1.
+constexpr uint32_t kKv8TmO = 256, kKv8TmQ0 = 384, kKv8TmQ1 = 416;
+
+HERALD_DEV void umma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// fp16 A and B (make_idesc_bf16 with formats 0)
+__host__ __device__ constexpr uint32_t make_idesc_half(int M, int N, bool b_mn_major) {
+  return (1u << 4) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(M >> 4) << 24);
+}
+HERALD_DEV void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Waits for this thread's tensor-memory loads; r (loaded before) counts as written
+// here, so that no use of it moves above the wait.
+HERALD_DEV void tmem_ld_done(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                 "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])
+               :
+               : "memory");
+}
+HERALD_DEV void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+
+// 16 scores -> P (fp16 pairs) and their sum; two values an instruction.
+HERALD_DEV float exp16(const uint32_t* x, float f, float nm, uint32_t* pk) {
+  const uint64_t f2 = f2_pack(f, f), nm2 = f2_pack(nm, nm);
+  uint64_t sa = f2_pack(0.f, 0.f), sb = sa;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    float t0, t1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2, nm2), t0, t1);
+    const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+    if (i & 2)
+      sa = f2_add(sa, f2_pack(p0, p1));
+    else
+      sb = f2_add(sb, f2_pack(p0, p1));
+    pk[i / 2] = pack_half2(p0, p1);
+  }
+  float s0, s1;
+  f2_unpack(f2_add(sa, sb), s0, s1);
+  return s0 + s1;
+}
+
+HERALD_DEV bool tc_any(bool x) {  // any of the softmax threads
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(x))
+      : "memory");
+  return r != 0;
+}
+HERALD_DEV void tc_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kKv8TcThreads, 1)
+    kv8_attn_tc_kernel(const Kv8AttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, uint32_t* err) {
+  using S = Kv8Tc<D>;
+  constexpr int KS = kKv8KStages, VS = kKv8VStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t k_full[KS], k_free[KS], v_full[VS], v_free[VS], v16_full[2], v16_free[2],
+      meta_full[kKv8Metas], q_full, s_full[2], p_full[2], pv_done[2], all_done[2];
+  __shared__ uint32_t tmem_base, failed;
+  __shared__ __align__(16) Kv8TileMeta meta[kKv8Metas];
+  __shared__ float row_x[2][128];  // exchanged between the halves of a row
+  uint8_t* base = align1024(smem_raw);
+  const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_free[i], 1);
+    for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_free[i], 4);
+    for (int i = 0; i < kKv8Metas; ++i) mbar_init(&meta_full[i], 1);
+    for (int i = 0; i < 2; ++i)
+      mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 1), mbar_init(&s_full[i], 1),
+          mbar_init(&p_full[i], 8), mbar_init(&pv_done[i], 1), mbar_init(&all_done[i], 1);
+    mbar_init(&q_full, 8);
+    failed = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12 && lane == 0) tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
+  tmem_setup(&tmem_base, 512);
+  const uint32_t tm = tmem_base;
+  griddep_enter();
+  const Kv4Wait wait{&failed};
+  const int G = a.Hq / a.Hkv, R = a.B * G;
+  const Kv4Share sh = kv4_share(a.ctx, a.N, a.L_max, a.Hkv * a.row_tiles, a.ctas, a.pad, 0,
+                                int(blockIdx.x));
+
+  // registers: 512 threads launch with 128 each (65,536) = 256 x (168 + 88)
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    // ------------------------------------------------------------ softmax
+    // (after a failed wait these warps go on without waiting: the barriers among them
+    // stay in step, the results are worthless and the error is recorded)
+    bool lost = false;
+    auto await = [&](uint64_t* bar, uint32_t parity, uint32_t which) {
+      if (!lost) lost = !wait(bar, parity, which);
+    };
+    const int w = warp >> 2, lrow = (warp & 3) * 32 + lane;  // half of the keys, TMEM lane
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    uint32_t t = 0;
+    kv8_pieces(a, sh, [&](int n, int gt, int seg, int ctx, int u0, int u1) -> bool {
+      debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
+      const int g = gt / a.row_tiles, r0 = (gt - g * a.row_tiles) * 128;
+      const bool idle = r0 + (warp & 3) * 32 >= R;  // the warp has no rows
+      const int row = r0 + lrow, rc = min(row, R - 1);
+      // queries: a thread has its row whole; the first half of the warps stores q0, the
+      // other q1.  (The scores of the piece before have been read: nothing reads Q now.)
+      float f = 0.f;
+      if (!idle) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((size_t(n) * a.B + rc / G) * a.Hq + g * G + rc % G) * D);
+        uint4 x[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = src[i];
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx = fmax3f(mx, fabsf(bf16lo(wd[j])), fabsf(bf16hi(wd[j])));
+        }
+        float up;
+        kv8_query_scale(mx, a.scale, &up, &f);
+#pragma unroll
+        for (int i = 0; i < D / 8; i += 4) {  // 32 channels, 8 columns
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t wd[4] = {x[i + k].x, x[i + k].y, x[i + k].z, x[i + k].w};
+            uint32_t c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float v0 = kv8_query(bf16lo(wd[j]), up), v1 = kv8_query(bf16hi(wd[j]), up);
+              c[j] = float2_to_e4m3(v0, v1);
+              if (w == 1) {  // what q0 left
+                const uint32_t h = e4m3x2_to_half2(c[j]);
+                const float2 q0 = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                c[j] = float2_to_e4m3(v0 - q0.x, v1 - q0.y);
+              }
+            }
+            o[2 * k] = c[0] | c[1] << 16;
+            o[2 * k + 1] = c[2] | c[3] << 16;
+          }
+          tmem_st8(tm + lanes + (w ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(i) * 2u, o);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full);
+
+      float m = -FLT_MAX, l = 0.f;
+      for (int u = u0; u < u1; ++u, ++t) {
+        const uint32_t b = t & 1, ts = tm + lanes + b * 128u + uint32_t(w) * 64u;
+        const Kv8TileMeta& mt = meta[t % kKv8Metas];
+        await(&meta_full[t % kKv8Metas], (t / kKv8Metas) & 1, X8_META);
+        await(&s_full[b], (t >> 1) & 1, X8_S_FULL);
+        tc_fence_after();
+        float sk[4], ev[4], iv[4];
+        {
+          const float4 x = *reinterpret_cast<const float4*>(&mt.sk[4 * w]);
+          const float4 y = *reinterpret_cast<const float4*>(&mt.ev[4 * w]);
+          const float4 z = *reinterpret_cast<const float4*>(&mt.iv[4 * w]);
+          sk[0] = f * x.x, sk[1] = f * x.y, sk[2] = f * x.z, sk[3] = f * x.w;
+          ev[0] = y.x, ev[1] = y.y, ev[2] = y.z, ev[3] = y.w;
+          iv[0] = z.x, iv[1] = z.y, iv[2] = z.z, iv[3] = z.w;
+        }
+        if (!idle) {  // keys that do not count: scores of -inf
+          const uint4 k4 = *reinterpret_cast<const uint4*>(&mt.keys[4 * w]);
+          if (min(min(k4.x, k4.y), min(k4.z, k4.w)) < 16u) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const int keys = int(mt.keys[4 * w + c]);
+              if (keys == 16) continue;
+              float v[16];
+              tmem_ld16(ts + uint32_t(c) * 16u, v);
+              uint32_t o[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = i < keys ? __float_as_uint(v[i]) : 0xFF800000u;
+              tmem_st8(ts + uint32_t(c) * 16u, *reinterpret_cast<uint32_t(*)[8]>(o));
+              tmem_st8(ts + uint32_t(c) * 16u + 8u, *reinterpret_cast<uint32_t(*)[8]>(o + 8));
+            }
+            tmem_wait_st();
+          }
+        }
+        uint32_t pk[32];
+        float add = 0.f;
+        bool high = u == u0;  // (a piece's first tile has no base yet)
+        if (!idle && u > u0) {
+          uint32_t x[32], y[32];
+          tmem_ld32_async(ts, x);
+          tmem_ld32_async(ts + 32u, y);
+          tmem_ld_done(x);
+          tmem_ld_done(y);
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float s = exp16((c < 2 ? x : y) + 16 * (c & 1), sk[c], ev[c] - m, pk + 8 * c);
+            sum += s;
+            add = fmaf(s, iv[c], add);
+          }
+          high = !(sum <= kKv8Top);
+        }
+        if (tc_any(high)) {
+          float z = -INFINITY;  // the largest exponent, rounded down: scores may be so large
+          if (!idle) {          // that fp32's steps are no longer small
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float v[16];
+              tmem_ld16(ts + uint32_t(c) * 16u, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                z = fmaxf(z, __fadd_rd(__fmul_rd(v[i], f * mt.sk[4 * w + c]), mt.ev[4 * w + c]));
+            }
+            row_x[w][lrow] = z;
+          }
+          tc_bar();
+          if (!idle) {
+            z = fmaxf(z, row_x[w ^ 1][lrow]);
+            float k = 1.f;
+            if (u == u0 || z - m > kKv8Below) {
+              const float nb = fmaxf(__fadd_rd(z, -kKv8Below), -FLT_MAX);
+              k = fast_exp2(m - nb);
+              m = nb;
+            }
+            l *= k;
+            if (u > u0) {  // O so far, once the products before this tile are in it
+              await(&pv_done[b ^ 1], ((t - 1) >> 1) & 1, X8_PV_DONE);
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 2; c += 32) {
+                const uint32_t to = tm + lanes + kKv8TmO + uint32_t(w) * (D / 2) + uint32_t(c);
+                float o[32];
+                tmem_ld32(to, o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= k;
+                tmem_st32(to, o);
+              }
+            }
+            add = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float v[16];
+              tmem_ld16(ts + uint32_t(c) * 16u, v);
+              const float fk = f * mt.sk[4 * w + c], nm = mt.ev[4 * w + c] - m;
+              float s = 0.f;
+              uint32_t o[8];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float x = fmaf(v[i], fk, nm);
+                v[i] = fast_exp2(x > kKv8TopLog2 ? kKv8TopLog2 : x);  // (a NaN stays)
+                s += v[i];
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+              add = fmaf(s, mt.iv[4 * w + c], add);
+              tmem_st8(ts + uint32_t(c) * 8u, o);  // (over scores that have been read)
+            }
+          }
+          tc_bar();  // (the exponents have been read)
+        } else if (!idle) {
+          tmem_st32(ts, *reinterpret_cast<float(*)[32]>(pk));
+        }
+        l += add;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[b]);
+      }
+      // the piece's partials: O once the last product is done, l of both halves
+      if (!idle) row_x[w][lrow] = l;
+      tc_bar();
+      await(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, X8_PV_DONE);
+      tc_fence_after();
+      const size_t slot = size_t(blockIdx.x) + seg;
+      if (!idle) {
+        if (w == 0 && row < R)
+          a.ml[slot * a.R16 + lrow] = make_float2(m, l + row_x[1][lrow]);
+        float4* out = reinterpret_cast<float4*>(a.opart + (slot * a.R16 + lrow) * D + w * (D / 2));
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+          float o[32];
+          tmem_ld32(tm + lanes + kKv8TmO + uint32_t(w) * (D / 2) + uint32_t(c), o);
+          if (row < R) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              out[(c + i) / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      tc_bar();  // (the sums have been read)
+      return true;
+    });
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp < 12) {
+      // ------------------------------------------------- values to fp16
+      // A lane turns chunks of 16 channels: eight (d = 64: four) lanes read a row, and of
+      // the two chunks that each writes, with d = 128 the lanes of the row's second half
+      // write theirs in the other order, so that the eight lanes of a shared-memory phase
+      // meet eight different groups of banks (with d = 64 they are two rows of them).
+      constexpr int CPR = D / 16, RPW = 32 / CPR, kTasks = 32 / RPW;
+      const int c = lane % CPR, cw = warp - 8;
+      const uint32_t flip = D == 128 ? uint32_t(c >> 2) : 0u;
+      const uint32_t vs = smem_u32(base) + S::kV, v16 = smem_u32(base) + S::kV16;
+      uint32_t t = 0;
+      kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
+        for (int u = u0; u < u1; ++u, ++t) {
+          const uint32_t st = t % VS, b = t & 1;
+          const Kv8TileMeta& mt = meta[t % kKv8Metas];
+          if (!wait(&meta_full[t % kKv8Metas], (t / kKv8Metas) & 1, X8_META)) return false;
+          if (!wait(&v_full[st], (t / VS) & 1, X8_V_FULL)) return false;
+          if (t >= 2 && !wait(&v16_free[b], ((t >> 1) - 1) & 1, X8_V16_FREE)) return false;
+          const uint32_t src = vs + st * S::kTile, dst = v16 + b * S::kTile16;
+          const uint32_t k0 = mt.keys[2 * cw], k1 = mt.keys[2 * cw + 1];  // of this warp's rows
+#pragma unroll 2
+          for (int s = 0; s < kTasks; ++s) {
+            const uint32_t rr = uint32_t(s * RPW + lane / CPR), r = uint32_t(cw * 32) + rr;
+            uint4 x = lds128(src + rows_off<D>(r, uint32_t(c)));
+            // (a row that does not count may hold any bytes: no 0 * NaN)
+            if ((rr & 15u) >= (rr < 16u ? k0 : k1)) x = make_uint4(0, 0, 0, 0);
+            uint32_t h[8];
+            e4m3x4_to_half2(x.x, h[0], h[1]);
+            e4m3x4_to_half2(x.y, h[2], h[3]);
+            e4m3x4_to_half2(x.z, h[4], h[5]);
+            e4m3x4_to_half2(x.w, h[6], h[7]);
+            const uint32_t at = dst + uint32_t(D == 128 ? c >> 2 : 0) * 16384u;
+            const uint32_t c0 = uint32_t(c & 3) * 2u;
+            const uint32_t a0 = at + sw128_off(r, c0 | flip), a1 = at + sw128_off(r, c0 | (flip ^ 1u));
+            if (flip) {
+              sts128(a0, h[4], h[5], h[6], h[7]);
+              sts128(a1, h[0], h[1], h[2], h[3]);
+            } else {
+              sts128(a0, h[0], h[1], h[2], h[3]);
+              sts128(a1, h[4], h[5], h[6], h[7]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_free[st]), mbar_arrive(&v16_full[b]);
+        }
+        return true;
+      });
+    } else if (warp == 12) {
+      // ------------------------------------------------------------ copies
+      const int page = 1 << a.c.page_log2;
+      const int ti = lane >> 3, gr = (lane & 7) * 16;  // this lane's tile of four, its 16 keys
+      uint32_t t = 0, k_issued = 0, v_issued = 0;
+      kv8_pieces(a, sh, [&](int n, int gt, int, int ctx, int u0, int u1) -> bool {
+        const int g = gt / a.row_tiles;
+        const int32_t* table = a.c.table + size_t(n) * a.c.max_pages;
+        const int stop = min(ctx, u1 * 128);
+        int pos = (u0 + ti) * 128 + gr;
+        auto look = [&](int p) { return p < stop ? table[p >> a.c.page_log2] : -1; };
+        auto scales = [&](int p, int phys, int& ek, int& ev) {
+          ek = ev = 127;
+          if (p < stop && phys >= 0 && phys < a.c.n_pages) {
+            const size_t at = kv8_scale(a.c, phys, a.Hkv, g, p);
+            ek = a.c.ks[at], ev = a.c.vs[at];
+          }
+        };
+        int phys = look(pos), ek, ev;
+        scales(pos, phys, ek, ev);
+        for (int u = u0; u < u1; u += 4, pos += 512) {
+          const int next = look(pos + 512);
+          const bool on = pos < stop, have = on && phys >= 0 && phys < a.c.n_pages;
+          debug_flag(on && !have, DEV_BAD_INDEX);
+          const bool head = have && (gr & (page - 1)) == 0;  // this lane copies the page
+          const uint32_t heads = __ballot_sync(0xffffffffu, head);
+          const int tiles = min(4, u1 - u);
+          auto publish = [&](int i) {  // of tile i: its keys and scales
+            const uint32_t x = (t + uint32_t(i)) % kKv8Metas;
+            if (ti == i) {
+              const int e_k = kv8_exp(uint32_t(ek)), e_v = kv8_exp(uint32_t(ev)), j = lane & 7;
+              meta[x].sk[j] = exp2_int(e_k);
+              meta[x].ev[j] = float(e_v);
+              meta[x].iv[j] = exp2_int(-e_v);
+              meta[x].keys[j] = have ? uint32_t(min(16, ctx - pos)) : 0u;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&meta_full[x]);
+          };
+          for (int i = 0; i < tiles; ++i) {
+            const uint32_t x = t + uint32_t(i), ks = x % KS, vst = x % VS;
+            const uint32_t bytes = uint32_t(__popc(heads >> (8 * i) & 0xFFu) * page) * D;
+            if (x >= uint32_t(KS) && !wait(&k_free[ks], (x / KS - 1) & 1, X8_K_FREE)) return false;
+            k_issued = x + 1;
+            if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
+            __syncwarp();
+            if (head && ti == i)
+              tma_load_3d(base + ks * S::kTile + uint32_t(gr) * D, &kmap, &k_full[ks], 0,
+                          g << a.c.page_log2, phys);
+            if (u > u0) publish(i);  // (its scales came while the four before were copied)
+            if (x >= uint32_t(VS) && !wait(&v_free[vst], (x / VS - 1) & 1, X8_V_FREE)) return false;
+            v_issued = x + 1;
+            if (lane == 0) mbar_arrive_expect_tx(&v_full[vst], bytes);
+            __syncwarp();
+            if (head && ti == i)
+              tma_load_3d(base + S::kV + vst * S::kTile + uint32_t(gr) * D, &vmap, &v_full[vst], 0,
+                          g << a.c.page_log2, phys);
+          }
+          if (u == u0)
+            for (int i = 0; i < tiles; ++i) publish(i);
+          phys = next;
+          scales(pos + 512, phys, ek, ev);
+          t += uint32_t(tiles);
+        }
+        return true;
+      });
+      // every copy has landed before the CTA may leave (where a wait has run out, nobody
+      // else waits for it)
+      for (uint32_t i = k_issued > uint32_t(KS) ? k_issued - KS : 0; i < k_issued; ++i)
+        mbar_wait(&k_full[i % KS], (i / KS) & 1);
+      for (uint32_t i = v_issued > uint32_t(VS) ? v_issued - VS : 0; i < v_issued; ++i)
+        mbar_wait(&v_full[i % VS], (i / VS) & 1);
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- S issuer
+      // (the whole warp walks the loops, lane 0 issues)
+      const uint64_t kd = make_sdesc_rows<D>(smem_u32(base));
+      constexpr uint32_t ids = make_idesc_e4m3(128, 128, false, false);
+      uint32_t t = 0, np = 0;
+      kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
+        if (!wait(&q_full, np & 1, X8_Q_FULL)) return false;
+        ++np;
+        for (int u = u0; u < u1; ++u, ++t) {
+          const uint32_t b = t & 1, st = t % KS;
+          if (!wait(&k_full[st], (t / KS) & 1, X8_K_FULL)) return false;
+          // P of two tiles before has been read: its buffer is free
+          if (t >= 2 && !wait(&pv_done[b], ((t >> 1) - 1) & 1, X8_PV_DONE)) return false;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int ks = 0; ks < D / 32; ++ks)
+                umma_e4m3_ts(tm + b * 128u, tm + (part ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(ks) * 8u,
+                             kd + ((st * S::kTile + uint32_t(ks) * 32u) >> 4), ids, part + ks > 0);
+            umma_commit(&s_full[b]);
+            umma_commit(&k_free[st]);
+          }
+          __syncwarp();
+        }
+        return true;
+      });
+      // every product and commit is done before the tensor memory is given back
+      if (t > 0 && lane == 0) {
+        umma_commit(&all_done[0]);
+        mbar_wait(&all_done[0], 0);
+      }
+    } else if (warp == 14) {
+      // -------------------------------------------------------- P V issuer
+      const uint64_t vd = make_sdesc_sw128(smem_u32(base) + S::kV16, 16384u, 1024);
+      constexpr uint32_t ido = make_idesc_half(128, D, true);
+      uint32_t t = 0;
+      kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
+        for (int u = u0; u < u1; ++u, ++t) {
+          const uint32_t b = t & 1;
+          if (!wait(&v16_full[b], (t >> 1) & 1, X8_V16_FULL)) return false;
+          if (!wait(&p_full[b], (t >> 1) & 1, X8_P_FULL)) return false;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)  // P: 32 columns in each half of the scores' place
+              umma_bf16_ts(tm + kKv8TmO, tm + b * 128u + uint32_t(ks >> 2) * 64u + uint32_t(ks & 3) * 8u,
+                           vd + ((b * S::kTile16) >> 4) + uint32_t(ks) * 128u, ido,
+                           u > u0 || ks > 0);
+            umma_commit(&pv_done[b]);
+            umma_commit(&v16_free[b]);
+          }
+          __syncwarp();
+        }
+        return true;
+      });
+      if (t > 0 && lane == 0) {
+        umma_commit(&all_done[1]);
+        mbar_wait(&all_done[1], 0);
+      }
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && failed)
+    record_error(err, DEV_TIMEOUT_MMA | DEV_K_KV8_ATTN | (failed << 16));
+  tmem_teardown(tm, 512);
+}
+
+// ------------------------------------------------------------------- host
+
+template <int D>
+static cudaError_t launch_tc(const Kv8AttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                             uint32_t* err, cudaStream_t st) {
+  constexpr size_t smem = Kv8Tc<D>::kSmem;
+  HERALD_CHECK_LAUNCH(ensure_smem(kv8_attn_tc_kernel<D>, smem));
+  return launch_k("kv8_attn_tc_kernel", kv8_attn_tc_kernel<D>, dim3(unsigned(a.ctas)),
+                  dim3(kKv8TcThreads), smem, st, a, kmap, vmap, err);
+}
+cudaError_t launch_kv8_attn_tc(int d, const Kv8AttnArgs& a, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, uint32_t* err, cudaStream_t st) {
+  return d == 128 ? launch_tc<128>(a, kmap, vmap, err, st) : launch_tc<64>(a, kmap, vmap, err, st);
+}
+
+HERALD_DEBUG_WORD_READER(debug_take_kv8_attn_tc)
+
+}  // namespace herald

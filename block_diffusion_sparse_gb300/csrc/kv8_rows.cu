@@ -430,14 +430,10 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         }
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        // the largest to [2^7, 2^8) (below 2^-112 it counts as that, infinities as 2^127);
-        // the factor that undoes it stays positive and finite, also times a key's scale
-        const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -112), 127);
-        const float up = exp2_int(min(7 - e, 119));
-        const float fac = a.scale * exp2_int(max(e - 7, -119));
+        float up, f;
+        kv8_query_scale(mx, a.scale, &up, &f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)  // (an infinity: NaN, as inf - inf makes of its row)
-          v[i] = fabsf(v[i]) < INFINITY ? v[i] * up : __uint_as_float(0x7FC00000u);
+        for (int i = 0; i < 8; ++i) v[i] = kv8_query(v[i], up);
         uint8_t* dst = Qs + qb * S::kQ;
         const uint32_t half = uint32_t(c & 1) * 8u;
         float q0[8];
@@ -447,7 +443,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         for (int i = 0; i < 8; i += 2) split_e4m3(v[i], v[i + 1]);
         stage_e4m3x8(dst + rows_off<D>(uint32_t(r), uint32_t(c >> 1)) + half, q0);
         stage_e4m3x8(dst + rows_off<D>(uint32_t(RP + r), uint32_t(c >> 1)) + half, v);
-        if (c == 0) row_f[qb][r] = fminf(fmaxf(fac, 0x1p-90f), 0x1p90f);
+        if (c == 0) row_f[qb][r] = f;
       }
       fence_proxy_async_smem();
       __syncwarp();
