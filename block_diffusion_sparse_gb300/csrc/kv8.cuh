@@ -36,8 +36,10 @@ HERALD_DEV float exp2_int(int e) { return __uint_as_float(uint32_t(e + 127) << 2
 
 // The four e4m3 codes of a word -> two fp16 pairs (exact).
 HERALD_DEV void e4m3x4_to_half2(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  lo = e4m3x2_to_half2(w & 0xFFFFu);
-  hi = e4m3x2_to_half2(w >> 16);
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 // fp32 pair -> e4m3 codes (lo in bits 0-7), to nearest even, past 448 to 448, NaN stays.
 HERALD_DEV uint32_t float2_to_e4m3(float lo, float hi) {
@@ -59,6 +61,16 @@ HERALD_DEV void kv8_query_scale(float mx, float scale, float* up, float* f) {
 // One value of it; an infinity becomes a NaN, as inf - inf makes one of its row.
 HERALD_DEV float kv8_query(float x, float up) {
   return fabsf(x) < INFINITY ? x * up : __uint_as_float(0x7FC00000u);
+}
+
+// One lane of a converged warp, the same every time: what it alone issues keeps its
+// operands in uniform registers (with `lane == 0` each mma moved them there anew).
+HERALD_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // ---- attention arguments shared by its kernels

@@ -11,24 +11,153 @@ namespace herald {
 
 constexpr int kKv8MaxCtas = 304;  // most attention CTAs (workspace slots)
 
+HERALD_DEV void join_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <int Words>
+HERALD_DEV void load_run(const uint16_t* p, bool on, uint32_t (&w)[Words]) {
+#pragma unroll
+  for (int i = 0; i < Words; i += 4) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (on) x = *reinterpret_cast<const uint4*>(p + 2 * i);
+    w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+  }
+}
+
+// The block's own keys in the join: up to kOwnWarps warps take 16 keys at a time, for 16
+// query rows (mma m16n8k16 of bf16, fp32 sums; P as two bf16 numbers, take_bf16), and
+// leave (m, l, O) in shared memory.  The contraction's channels may stand in any order
+// that both operands share, so a lane's share of a row is a run of channels: q and k
+// [t D/4, (t+1) D/4) of lane t = lane%4, v [g D/8, (g+1) D/8) of lane group g = lane/4,
+// whose n-th channel goes to column g of the product's n-th tile.
+constexpr int kOwnWarps = 4;
+template <int D>
+struct OwnKeys {
+  static constexpr int kPitch = D / 32 * 36;  // (four floats after 32: runs meet all banks)
+  float o[kOwnWarps][16][kPitch];
+  float m[kOwnWarps][16], l[kOwnWarps][16];
+};
+template <int D>
+HERALD_DEV void own_keys(const Kv8AttnArgs& a, OwnKeys<D>& sm, int n, int g, int r0, int warp,
+                         int lane) {
+  constexpr int KW = D / 8, VW = D / 16;  // words of a lane's run
+  const int G = a.Hq / a.Hkv, R = a.B * G, lg = lane >> 2, lt = lane & 3;
+  uint32_t q[2][KW];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = min(r0 + lg + 8 * i, R - 1);
+    load_run<KW>(a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + lt * (D / 4), true,
+                 q[i]);
+  }
+  float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
+#pragma unroll 1
+  for (int k0 = warp * 16; k0 < a.B; k0 += kOwnWarps * 16) {
+    const size_t ld = size_t(a.Hkv) * D, at = (size_t(n) * a.B + k0) * ld + size_t(g) * D;
+    uint32_t v[4][VW];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 2 * lt + (i & 1) + 8 * (i >> 1);
+      load_run<VW>(a.bv + at + j * ld + lg * (D / 8), k0 + j < a.B, v[i]);
+    }
+    float s[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t k[KW];
+      load_run<KW>(a.bk + at + (lg + 8 * h) * ld + lt * (D / 4), k0 + lg + 8 * h < a.B, k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[h][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KW; i += 2)
+        join_mma(s[h], q[0][i], q[1][i], q[0][i + 1], q[1][i + 1], k[i], k[i + 1]);
+    }
+    float f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // rows lg, lg + 8: scores 2 i, 2 i + 1 of each half
+      float mx = m[i];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& x = s[h][2 * i + e];
+          x = k0 + 8 * h + 2 * lt + e < a.B ? x * a.scale : -INFINITY;
+          mx = fmaxf(mx, x);
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      f[i] = fast_exp2(m[i] - mx);
+      m[i] = mx;
+      l[i] *= f[i];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[h][2 * i + e] = fast_exp2(s[h][2 * i + e] - mx);
+          l[i] += s[h][2 * i + e];
+        }
+    }
+    uint32_t p[2][4];
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) p[part][2 * h + i] = take_bf16(s[h][2 * i], s[h][2 * i + 1]);
+#pragma unroll
+    for (int c = 0; c < VW; c += 2) {  // four channels of a run: four tiles
+      float o[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = c + j / 2;
+        const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+        const uint32_t b0 = __byte_perm(v[0][i], v[1][i], sel), b1 = __byte_perm(v[2][i], v[3][i], sel);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+        join_mma(o[j], p[0][0], p[0][1], p[0][2], p[0][3], b0, b1);
+        join_mma(o[j], p[1][0], p[1][1], p[1][2], p[1][3], b0, b1);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // row lg + 8 (e >> 1), run 2 lt + (e & 1)
+        const int ch = (2 * lt + (e & 1)) * (D / 8) + 2 * c;
+        float4* dst = reinterpret_cast<float4*>(&sm.o[warp][lg + 8 * (e >> 1)][ch + ch / 32 * 4]);
+        float4 x = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
+        if (k0 >= kOwnWarps * 16) {
+          const float4 y = *dst;
+          const float w = f[e >> 1];
+          x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y), x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
+        }
+        *dst = x;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    if (lt == 0) sm.m[warp][lg + 8 * i] = m[i], sm.l[warp][lg + 8 * i] = l[i];
+  }
+}
+
 // The output: the pieces of a segment joined, with the block's own keys.  grid (N*Hkv,
-// ceil(R / Rows)); D/4 lanes hold a row's channels, four each, and Threads over Rows
-// such groups share a row: each takes every such-and-suchth chunk of the block's own
-// keys (a key per lane: q in shared memory, the whole of a dot product in one lane,
-// fp32 throughout) and every such-and-suchth piece, five in flight; the groups are
-// then added in order.  The block's keys come before the grid-dependency wait: they
-// and the lengths were written before the attention kernel's own wait ended, and it
-// lets this kernel start only after that.
-template <int D, int Rows, int Threads>
-__global__ void __launch_bounds__(Threads) kv8_join_kernel(const Kv8AttnArgs a) {
-  constexpr int TPR = D / 4, GR = Threads / (TPR * Rows);
-  __shared__ float qs[Rows][D];
+// ceil(R / Rows)); D/4 lanes hold a row's channels, four each, and GR groups of Rows
+// such rows share the pieces: each group takes every such-and-suchth, five in flight;
+// the groups are then added in order.  The block's keys come before the grid-dependency
+// wait: they and the lengths were written before the attention kernel's own wait
+// ended, and it lets this kernel start only after that.
+template <int D, int Rows, int GR>
+__global__ void __launch_bounds__(D / 4 * Rows * GR) kv8_join_kernel(const Kv8AttnArgs a) {
+  constexpr int TPR = D / 4;
+  static_assert(TPR * Rows * GR >= 32 * kOwnWarps, "warps of the block's keys");
+  __shared__ OwnKeys<D> own;
   __shared__ float4 part[GR][Rows][TPR];
   __shared__ float part_m[GR][Rows], part_l[GR][Rows];
   const int seg = blockIdx.x, n = seg / a.Hkv, g = seg - n * a.Hkv;
   const int G = a.Hq / a.Hkv, R = a.B * G;
   const int c4 = threadIdx.x % TPR, rr = threadIdx.x / TPR % Rows, grp = threadIdx.x / (TPR * Rows);
-  const int r = int(blockIdx.y) * Rows + rr, rc = min(r, R - 1);
+  const int r0 = int(blockIdx.y) * Rows, r = r0 + rr, rc = min(r, R - 1);
   const size_t row = (size_t(n) * a.B + rc / G) * a.Hq + g * G + rc % G;
   const int heads = a.Hkv * a.row_tiles, tile = rc / a.R16, rt = rc - tile * a.R16;
   const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, 0, a.pad), heads, a.ctas);
@@ -37,49 +166,17 @@ __global__ void __launch_bounds__(Threads) kv8_join_kernel(const Kv8AttnArgs a) 
   float M = -FLT_MAX, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.bk) {
-    if (grp == 0) {
-      const uint2 w = *reinterpret_cast<const uint2*>(a.q + row * D + c4 * 4);
-      float4 f = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-      *reinterpret_cast<float4*>(&qs[rr][c4 * 4]) = f;
-    }
+    const int warp = warp_same(int(threadIdx.x) >> 5);
+    if (warp < kOwnWarps) own_keys<D>(a, own, n, g, r0, warp, threadIdx.x & 31);
     __syncthreads();
-    const int chunks = (a.B + TPR - 1) / TPR;
-    for (int ch = grp; ch < chunks; ch += GR) {  // (grp, and so the count, is a warp's own
-      const int j = ch * TPR + c4;               // or, with D = 64, a multiple of it: Rows >= 2)
-      float s = -INFINITY;
-      if (j < a.B) {
-        const uint4* kp =
-            reinterpret_cast<const uint4*>(a.bk + ((size_t(n) * a.B + j) * a.Hkv + g) * D);
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 w = kp[i];
-          const float4 x = *reinterpret_cast<const float4*>(&qs[rr][i * 8]);
-          const float4 y = *reinterpret_cast<const float4*>(&qs[rr][i * 8 + 4]);
-          s0 = fmaf(x.x, bf16lo(w.x), s0), s1 = fmaf(x.y, bf16hi(w.x), s1);
-          s0 = fmaf(x.z, bf16lo(w.y), s0), s1 = fmaf(x.w, bf16hi(w.y), s1);
-          s0 = fmaf(y.x, bf16lo(w.z), s0), s1 = fmaf(y.y, bf16hi(w.z), s1);
-          s0 = fmaf(y.z, bf16lo(w.w), s0), s1 = fmaf(y.w, bf16hi(w.w), s1);
-        }
-        s = (s0 + s1) * a.scale;
-      }
-      float m1 = fmaxf(M, s);
-#pragma unroll
-      for (int o = TPR / 2; o > 0; o >>= 1) m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-      const float k = fast_exp2(M - m1), p = fast_exp2(s - m1);
-      float sum = p;
-#pragma unroll
-      for (int o = TPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      M = m1, L = L * k + sum;
-      acc.x *= k, acc.y *= k, acc.z *= k, acc.w *= k;
-      const int here = min(TPR, a.B - ch * TPR);
-      const uint16_t* vp = a.bv + ((size_t(n) * a.B + ch * TPR) * a.Hkv + g) * D + c4 * 4;
-#pragma unroll 4
-      for (int i = 0; i < here; ++i) {
-        const float pi = __shfl_sync(0xffffffffu, p, i, TPR);
-        const uint2 w = *reinterpret_cast<const uint2*>(vp + size_t(i) * a.Hkv * D);
-        acc.x = fmaf(pi, bf16lo(w.x), acc.x), acc.y = fmaf(pi, bf16hi(w.x), acc.y);
-        acc.z = fmaf(pi, bf16lo(w.y), acc.z), acc.w = fmaf(pi, bf16hi(w.y), acc.w);
+    if (grp == 0) {
+      const int with = min(kOwnWarps, (a.B + 15) / 16);
+      for (int i = 0; i < with; ++i) M = fmaxf(M, own.m[i][rr]);
+      for (int i = 0; i < with; ++i) {
+        const float f = fast_exp2(own.m[i][rr] - M);
+        const float4 x = *reinterpret_cast<const float4*>(&own.o[i][rr][c4 * 4 + c4 / 8 * 4]);
+        L += f * own.l[i][rr];
+        acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
       }
     }
   }
@@ -142,13 +239,14 @@ __global__ void __launch_bounds__(Threads) kv8_join_kernel(const Kv8AttnArgs a) 
 
 template <int D>
 static cudaError_t launch_join(const Kv8AttnArgs& a, int R, int num_sms, cudaStream_t st) {
-  auto go = [&](auto* kernel, int rows, int threads) {
+  auto go = [&](auto* kernel, int rows, int groups) {
     return launch_k("kv8_join_kernel", kernel, dim3(unsigned(a.N * a.Hkv), unsigned(cdiv(R, rows))),
-                    dim3(unsigned(threads)), 0, st, a);
+                    dim3(unsigned(D / 4 * rows * groups)), 0, st, a);
   };
   const int64_t segs = int64_t(a.N) * a.Hkv;
-  if (segs * cdiv(R, 4) <= num_sms) return go(kv8_join_kernel<D, 4, 1024>, 4, 1024);
-  return go(kv8_join_kernel<D, 8, D * 2>, 8, D * 2);
+  if (segs * cdiv(R, 4) <= num_sms) return go(kv8_join_kernel<D, 4, 4>, 4, 4);
+  if (segs * cdiv(R, 8) <= num_sms || R <= 8) return go(kv8_join_kernel<D, 8, 2>, 8, 2);
+  return go(kv8_join_kernel<D, 16, 1>, 16, 1);
 }
 
 // Workspace: error word, then (m, l) and O of every partial.

@@ -13,18 +13,22 @@
 // packing them.)  Q in tensor memory keeps 64 KB a tile off shared memory, whose
 // bandwidth would be the bound: 144 KB a tile as it is (copies 32, K twice 32, V read
 // 16, written 32 and read as fp16 32).
-//   warps 0-3, 4-7  softmax: a thread per row and half of the tile's keys; both halves
-//              of a row share its base m (one vote a tile, exchanged where it moves)
+//   warps 0-3, 4-7  softmax: two streams, a thread per row each, the first with the
+//              first 64 keys of every tile, the second with the others; each has its own
+//              base m, sum l and O, added up at a piece's end
 //   warps 8-11 turn V tiles into fp16
 //   warp 12    copies K and V tiles by TMA, looks up pages and scales four tiles ahead
-//   warps 13, 14  issue S and P V
+//   warp 13    issues S, in steps of 64 keys, the streams' in turn
+//   warps 14, 15  issue P V, one per stream
+// The steps go through three score buffers of 64 TMEM columns (P overlays the scores):
+// with both O and Q these fill the 512.
 // Scales: a key's multiplies its scores.  A value's exponent e_v goes into the weight's
 // own, P = 2^(x + e_v - m), and out of the row's sum again, l += P 2^-e_v, so O has one
 // unit and P fills fp16 whatever the values' scales.
 //
-// P = 2^(x + e_v - m) stays in fp16 as long as a thread's 64 of them sum to less than
-// 60000.  Where a sum does not (and at a piece's first tile) the row's largest exponent
-// is looked up, m set 5 below it, O and l follow, and the tile is done again.
+// P = 2^(x + e_v - m) stays in fp16 as long as a step's 64 of them sum to less than
+// 60000.  Where a sum does not (and at a piece's first step) the row's largest exponent
+// is looked up, m set 5 below it, O and l follow, and the step is done again.
 #include <float.h>
 
 #include "kv8.cuh"
@@ -32,7 +36,7 @@
 
 namespace herald {
 
-constexpr int kKv8TcThreads = 512;  // 16 warps (15 only fills a warpgroup)
+constexpr int kKv8TcThreads = 512;  // 16 warps
 constexpr int kKv8KStages = 5, kKv8VStages = 4;
 // Tiles whose scales and counts are kept for the softmax: K copies run at most five
 // tiles ahead of the scores, those two ahead of P, and look-ups four ahead of copies.
@@ -43,7 +47,7 @@ constexpr float kKv8Below = 5.f, kKv8Top = 60000.f, kKv8TopLog2 = 15.8f;
 enum : uint32_t {
   X8_K_FREE = 1, X8_V_FREE = 2, X8_K_FULL = 4, X8_V_FULL = 8, X8_META = 0x10, X8_Q_FULL = 0x20,
   X8_S_FULL = 0x40, X8_P_FULL = 0x80, X8_PV_DONE = 0x100, X8_V16_FREE = 0x200,
-  X8_V16_FULL = 0x400
+  X8_V16_FULL = 0x400, X8_O_DONE = 0x800
 };
 
 struct Kv8TileMeta {  // per 16 keys: 2^e_k, e_v, 2^-e_v and how many count
@@ -58,8 +62,9 @@ struct Kv8Tc {
   static constexpr uint32_t kV = kKv8KStages * kTile, kV16 = kV + kKv8VStages * kTile;
   static constexpr uint32_t kSmem = kV16 + 2 * kTile16 + 1024;
 };
-// Tensor memory: two S (and P) buffers, O, q0, q1.
-constexpr uint32_t kKv8TmO = 256, kKv8TmQ0 = 384, kKv8TmQ1 = 416;
+constexpr int kKv8Bufs = 3;  // score buffers
+// Tensor memory: the score buffers, q0, q1, both streams' O.
+constexpr uint32_t kKv8TmQ0 = 192, kKv8TmQ1 = 224, kKv8TmO = 256;
 
 HERALD_DEV void umma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                              uint32_t accumulate) {
@@ -128,16 +133,6 @@ HERALD_DEV float exp16(const uint32_t* x, float f, float nm, uint32_t* pk) {
   return s0 + s1;
 }
 
-HERALD_DEV bool tc_any(bool x) {  // any of the softmax threads
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(uint32_t(x))
-      : "memory");
-  return r != 0;
-}
 HERALD_DEV void tc_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <int D>
@@ -148,10 +143,11 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
   constexpr int KS = kKv8KStages, VS = kKv8VStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full[KS], k_free[KS], v_full[VS], v_free[VS], v16_full[2], v16_free[2],
-      meta_full[kKv8Metas], q_full, s_full[2], p_full[2], pv_done[2], all_done[2];
+      meta_full[kKv8Metas], q_full, s_full[2][2], p_full[2][2], pv_done[kKv8Bufs], o_done[2],
+      all_done[3];
   __shared__ uint32_t tmem_base, failed;
   __shared__ __align__(16) Kv8TileMeta meta[kKv8Metas];
-  __shared__ float row_x[2][128];  // exchanged between the halves of a row
+  __shared__ float2 row_ml[2][128];  // a piece's (m, l) of both streams
   uint8_t* base = align1024(smem_raw);
   const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -159,8 +155,10 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_free[i], 4);
     for (int i = 0; i < kKv8Metas; ++i) mbar_init(&meta_full[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 1), mbar_init(&s_full[i], 1),
-          mbar_init(&p_full[i], 8), mbar_init(&pv_done[i], 1), mbar_init(&all_done[i], 1);
+      mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 2), mbar_init(&o_done[i], 1);
+    // (by stream and parity of its steps: whoever waits on a barrier sees its every phase)
+    for (int i = 0; i < 4; ++i) mbar_init(&s_full[i & 1][i >> 1], 1), mbar_init(&p_full[i & 1][i >> 1], 4);
+    for (int i = 0; i < kKv8Bufs; ++i) mbar_init(&pv_done[i], 1), mbar_init(&all_done[i], 1);
     mbar_init(&q_full, 8);
     failed = 0;
     fence_mbar_init();
@@ -184,8 +182,9 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     auto await = [&](uint64_t* bar, uint32_t parity, uint32_t which) {
       if (!lost) lost = !wait(bar, parity, which);
     };
-    const int w = warp >> 2, lrow = (warp & 3) * 32 + lane;  // half of the keys, TMEM lane
+    const int w = warp >> 2, lrow = (warp & 3) * 32 + lane;  // stream, TMEM lane
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t to = tm + lanes + kKv8TmO + uint32_t(w) * 128u, to2 = to ^ 128u;  // O, the other's
     uint32_t t = 0;
     kv8_pieces(a, sh, [&](int n, int gt, int seg, int ctx, int u0, int u1) -> bool {
       debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
@@ -240,10 +239,10 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
 
       float m = -FLT_MAX, l = 0.f;
       for (int u = u0; u < u1; ++u, ++t) {
-        const uint32_t b = t & 1, ts = tm + lanes + b * 128u + uint32_t(w) * 64u;
+        const uint32_t j = 2 * t + uint32_t(w), b = j % kKv8Bufs, ts = tm + lanes + b * 64u;  // the step
         const Kv8TileMeta& mt = meta[t % kKv8Metas];
         await(&meta_full[t % kKv8Metas], (t / kKv8Metas) & 1, X8_META);
-        await(&s_full[b], (t >> 1) & 1, X8_S_FULL);
+        await(&s_full[w][t & 1], (t >> 1) & 1, X8_S_FULL);
         tc_fence_after();
         float sk[4], ev[4], iv[4];
         {
@@ -272,28 +271,28 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
             tmem_wait_st();
           }
         }
-        uint32_t pk[32];
-        float add = 0.f;
-        bool high = u == u0;  // (a piece's first tile has no base yet)
-        if (!idle && u > u0) {
-          uint32_t x[32], y[32];
-          tmem_ld32_async(ts, x);
-          tmem_ld32_async(ts + 32u, y);
-          tmem_ld_done(x);
-          tmem_ld_done(y);
-          float sum = 0.f;
+        if (!idle) {
+          uint32_t pk[32];
+          float add = 0.f;
+          bool high = true;
+          if (u > u0) {  // (a piece's first step has no base yet)
+            uint32_t x[32], y[32];
+            tmem_ld32_async(ts, x);
+            tmem_ld32_async(ts + 32u, y);
+            tmem_ld_done(x);
+            tmem_ld_done(y);
+            float sum = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float s = exp16((c < 2 ? x : y) + 16 * (c & 1), sk[c], ev[c] - m, pk + 8 * c);
-            sum += s;
-            add = fmaf(s, iv[c], add);
+            for (int c = 0; c < 4; ++c) {
+              const float s = exp16((c < 2 ? x : y) + 16 * (c & 1), sk[c], ev[c] - m, pk + 8 * c);
+              sum += s;
+              add = fmaf(s, iv[c], add);
+            }
+            high = !(sum <= kKv8Top);
           }
-          high = !(sum <= kKv8Top);
-        }
-        if (tc_any(high)) {
-          float z = -INFINITY;  // the largest exponent, rounded down: scores may be so large
-          if (!idle) {          // that fp32's steps are no longer small
-#pragma unroll 1
+          if (__any_sync(0xffffffffu, high)) {
+            float z = -INFINITY;  // the largest exponent, rounded down: scores may be so large
+#pragma unroll 1                  // that fp32's steps are no longer small
             for (int c = 0; c < 4; ++c) {
               float v[16];
               tmem_ld16(ts + uint32_t(c) * 16u, v);
@@ -301,11 +300,6 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
               for (int i = 0; i < 16; ++i)
                 z = fmaxf(z, __fadd_rd(__fmul_rd(v[i], f * mt.sk[4 * w + c]), mt.ev[4 * w + c]));
             }
-            row_x[w][lrow] = z;
-          }
-          tc_bar();
-          if (!idle) {
-            z = fmaxf(z, row_x[w ^ 1][lrow]);
             float k = 1.f;
             if (u == u0 || z - m > kKv8Below) {
               const float nb = fmaxf(__fadd_rd(z, -kKv8Below), -FLT_MAX);
@@ -313,25 +307,24 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
               m = nb;
             }
             l *= k;
-            if (u > u0) {  // O so far, once the products before this tile are in it
-              await(&pv_done[b ^ 1], ((t - 1) >> 1) & 1, X8_PV_DONE);
+            if (u > u0) {  // O so far, once the stream's product before is in it
+              await(&o_done[w], (t - 1) & 1, X8_O_DONE);
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D / 2; c += 32) {
-                const uint32_t to = tm + lanes + kKv8TmO + uint32_t(w) * (D / 2) + uint32_t(c);
+              for (uint32_t c = 0; c < D; c += 32) {
                 float o[32];
-                tmem_ld32(to, o);
+                tmem_ld32(to + c, o);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] *= k;
-                tmem_st32(to, o);
+                tmem_st32(to + c, o);
               }
             }
             add = 0.f;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
+              const float fk = f * mt.sk[4 * w + c], nm = mt.ev[4 * w + c] - m;
               float v[16];
               tmem_ld16(ts + uint32_t(c) * 16u, v);
-              const float fk = f * mt.sk[4 * w + c], nm = mt.ev[4 * w + c] - m;
               float s = 0.f;
               uint32_t o[8];
 #pragma unroll
@@ -345,41 +338,46 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
               add = fmaf(s, mt.iv[4 * w + c], add);
               tmem_st8(ts + uint32_t(c) * 8u, o);  // (over scores that have been read)
             }
+          } else {
+            tmem_st32(ts, *reinterpret_cast<float(*)[32]>(pk));
           }
-          tc_bar();  // (the exponents have been read)
-        } else if (!idle) {
-          tmem_st32(ts, *reinterpret_cast<float(*)[32]>(pk));
+          l += add;
+          tmem_wait_st();
         }
-        l += add;
-        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[b]);
+        if (lane == 0) mbar_arrive(&p_full[w][t & 1]);
       }
-      // the piece's partials: O once the last product is done, l of both halves
-      if (!idle) row_x[w][lrow] = l;
+      // the piece's partials, once both streams' last products are done: each stream
+      // reads both O for half of the channels and writes their sum
+      row_ml[w][lrow] = make_float2(m, l);
       tc_bar();
-      await(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, X8_PV_DONE);
+      await(&o_done[w], (t - 1) & 1, X8_O_DONE);
+      await(&o_done[w ^ 1], (t - 1) & 1, X8_O_DONE);
       tc_fence_after();
       const size_t slot = size_t(blockIdx.x) + seg;
       if (!idle) {
-        if (w == 0 && row < R)
-          a.ml[slot * a.R16 + lrow] = make_float2(m, l + row_x[1][lrow]);
+        const float2 o2 = row_ml[w ^ 1][lrow];
+        const float mm = fmaxf(m, o2.x), w0 = fast_exp2(m - mm), w1 = fast_exp2(o2.x - mm);
+        if (w == 0 && row < R) a.ml[slot * a.R16 + lrow] = make_float2(mm, w0 * l + w1 * o2.y);
         float4* out = reinterpret_cast<float4*>(a.opart + (slot * a.R16 + lrow) * D + w * (D / 2));
 #pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
-          float o[32];
-          tmem_ld32(tm + lanes + kKv8TmO + uint32_t(w) * (D / 2) + uint32_t(c), o);
+        for (uint32_t c = 0; c < D / 2; c += 32) {
+          float o[32], p[32];
+          tmem_ld32(to + uint32_t(w) * (D / 2) + c, o);
+          tmem_ld32(to2 + uint32_t(w) * (D / 2) + c, p);
           if (row < R) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              out[(c + i) / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              out[(c + i) / 4] =
+                  make_float4(fmaf(p[i], w1, o[i] * w0), fmaf(p[i + 1], w1, o[i + 1] * w0),
+                              fmaf(p[i + 2], w1, o[i + 2] * w0), fmaf(p[i + 3], w1, o[i + 3] * w0));
           }
           __syncwarp();
         }
       }
       tc_fence_before();
-      tc_bar();  // (the sums have been read)
+      tc_bar();  // (O and row_ml have been read: the next piece may begin)
       return true;
     });
   } else {
@@ -390,10 +388,20 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       // the two chunks that each writes, with d = 128 the lanes of the row's second half
       // write theirs in the other order, so that the eight lanes of a shared-memory phase
       // meet eight different groups of banks (with d = 64 they are two rows of them).
-      constexpr int CPR = D / 16, RPW = 32 / CPR, kTasks = 32 / RPW;
-      const int c = lane % CPR, cw = warp - 8;
+      // Every load of a tile first: with two chunks under way at a time a tile took
+      // 1,500 cycles, which was the longest of all roles.
+      constexpr int CPR = D / 16, RPW = 32 / CPR, kTasks = 32 / RPW, kPar = 8 / RPW;
+      const int c = lane % CPR, cw = warp - 8, sub = lane / CPR;
       const uint32_t flip = D == 128 ? uint32_t(c >> 2) : 0u;
       const uint32_t vs = smem_u32(base) + S::kV, v16 = smem_u32(base) + S::kV16;
+      // places of the lane's first chunks; the others are eight rows on, and on
+      uint32_t from[kPar], to[kPar];
+#pragma unroll
+      for (int i = 0; i < kPar; ++i) {
+        const uint32_t r = uint32_t(cw * 32 + i * RPW + sub);
+        from[i] = rows_off<D>(r, uint32_t(c));
+        to[i] = uint32_t(D == 128 ? c >> 2 : 0) * 16384u + sw128_off(r, uint32_t(c & 3) * 2u | flip);
+      }
       uint32_t t = 0;
       kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
         for (int u = u0; u < u1; ++u, ++t) {
@@ -403,27 +411,32 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           if (!wait(&v_full[st], (t / VS) & 1, X8_V_FULL)) return false;
           if (t >= 2 && !wait(&v16_free[b], ((t >> 1) - 1) & 1, X8_V16_FREE)) return false;
           const uint32_t src = vs + st * S::kTile, dst = v16 + b * S::kTile16;
+          uint4 x[kTasks];
+#pragma unroll
+          for (int s = 0; s < kTasks; ++s)
+            x[s] = lds128(src + from[s % kPar] + uint32_t(s / kPar) * (8u * D));
           const uint32_t k0 = mt.keys[2 * cw], k1 = mt.keys[2 * cw + 1];  // of this warp's rows
-#pragma unroll 2
+          if (min(k0, k1) < 16u) {  // rows that do not count may hold any bytes: no 0 * NaN
+#pragma unroll
+            for (int s = 0; s < kTasks; ++s) {
+              const uint32_t r = uint32_t(s * RPW + sub);
+              if ((r & 15u) >= (r < 16u ? k0 : k1)) x[s] = make_uint4(0, 0, 0, 0);
+            }
+          }
+#pragma unroll
           for (int s = 0; s < kTasks; ++s) {
-            const uint32_t rr = uint32_t(s * RPW + lane / CPR), r = uint32_t(cw * 32) + rr;
-            uint4 x = lds128(src + rows_off<D>(r, uint32_t(c)));
-            // (a row that does not count may hold any bytes: no 0 * NaN)
-            if ((rr & 15u) >= (rr < 16u ? k0 : k1)) x = make_uint4(0, 0, 0, 0);
             uint32_t h[8];
-            e4m3x4_to_half2(x.x, h[0], h[1]);
-            e4m3x4_to_half2(x.y, h[2], h[3]);
-            e4m3x4_to_half2(x.z, h[4], h[5]);
-            e4m3x4_to_half2(x.w, h[6], h[7]);
-            const uint32_t at = dst + uint32_t(D == 128 ? c >> 2 : 0) * 16384u;
-            const uint32_t c0 = uint32_t(c & 3) * 2u;
-            const uint32_t a0 = at + sw128_off(r, c0 | flip), a1 = at + sw128_off(r, c0 | (flip ^ 1u));
+            e4m3x4_to_half2(x[s].x, h[0], h[1]);
+            e4m3x4_to_half2(x[s].y, h[2], h[3]);
+            e4m3x4_to_half2(x[s].z, h[4], h[5]);
+            e4m3x4_to_half2(x[s].w, h[6], h[7]);
+            const uint32_t at = dst + to[s % kPar] + uint32_t(s / kPar) * 1024u;
             if (flip) {
-              sts128(a0, h[4], h[5], h[6], h[7]);
-              sts128(a1, h[0], h[1], h[2], h[3]);
+              sts128(at, h[4], h[5], h[6], h[7]);
+              sts128(at ^ 16u, h[0], h[1], h[2], h[3]);
             } else {
-              sts128(a0, h[0], h[1], h[2], h[3]);
-              sts128(a1, h[4], h[5], h[6], h[7]);
+              sts128(at, h[0], h[1], h[2], h[3]);
+              sts128(at ^ 16u, h[4], h[5], h[6], h[7]);
             }
           }
           fence_proxy_async_smem();
@@ -450,10 +463,13 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
             ek = a.c.ks[at], ev = a.c.vs[at];
           }
         };
-        int phys = look(pos), ek, ev;
+        // (the table is read two groups of four tiles ahead, the scales one)
+        int phys = look(pos), next = look(pos + 512), ek, ev;
         scales(pos, phys, ek, ev);
         for (int u = u0; u < u1; u += 4, pos += 512) {
-          const int next = look(pos + 512);
+          const int after = look(pos + 1024);
+          int ek1, ev1;
+          scales(pos + 512, next, ek1, ev1);
           const bool on = pos < stop, have = on && phys >= 0 && phys < a.c.n_pages;
           debug_flag(on && !have, DEV_BAD_INDEX);
           const bool head = have && (gr & (page - 1)) == 0;  // this lane copies the page
@@ -492,8 +508,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           }
           if (u == u0)
             for (int i = 0; i < tiles; ++i) publish(i);
-          phys = next;
-          scales(pos + 512, phys, ek, ev);
+          phys = next, next = after, ek = ek1, ev = ev1;
           t += uint32_t(tiles);
         }
         return true;
@@ -508,63 +523,70 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       // ---------------------------------------------------------- S issuer
       // (the whole warp walks the loops, lane 0 issues)
       const uint64_t kd = make_sdesc_rows<D>(smem_u32(base));
-      constexpr uint32_t ids = make_idesc_e4m3(128, 128, false, false);
+      constexpr uint32_t ids = make_idesc_e4m3(128, 64, false, false);
       uint32_t t = 0, np = 0;
       kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
         if (!wait(&q_full, np & 1, X8_Q_FULL)) return false;
         ++np;
         for (int u = u0; u < u1; ++u, ++t) {
-          const uint32_t b = t & 1, st = t % KS;
+          const uint32_t st = t % KS;
           if (!wait(&k_full[st], (t / KS) & 1, X8_K_FULL)) return false;
-          // P of two tiles before has been read: its buffer is free
-          if (t >= 2 && !wait(&pv_done[b], ((t >> 1) - 1) & 1, X8_PV_DONE)) return false;
-          tc_fence_after();
-          if (lane == 0) {
+#pragma unroll 1
+          for (uint32_t w = 0; w < 2; ++w) {
+            // P of three steps before has been read: its buffer is free
+            const uint32_t j = 2 * t + w, b = j % kKv8Bufs;
+            if (j >= kKv8Bufs && !wait(&pv_done[b], (j / kKv8Bufs - 1) & 1, X8_PV_DONE)) return false;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-              for (int ks = 0; ks < D / 32; ++ks)
-                umma_e4m3_ts(tm + b * 128u, tm + (part ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(ks) * 8u,
-                             kd + ((st * S::kTile + uint32_t(ks) * 32u) >> 4), ids, part + ks > 0);
-            umma_commit(&s_full[b]);
-            umma_commit(&k_free[st]);
+                for (int ks = 0; ks < D / 32; ++ks)
+                  umma_e4m3_ts(tm + b * 64u, tm + (part ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(ks) * 8u,
+                               kd + ((st * S::kTile + w * (64u * D) + uint32_t(ks) * 32u) >> 4), ids,
+                               part + ks > 0);
+              umma_commit(&s_full[w][t & 1]);
+              if (w == 1) umma_commit(&k_free[st]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
         return true;
       });
       // every product and commit is done before the tensor memory is given back
-      if (t > 0 && lane == 0) {
+      if (t > 0 && elect_one()) {
         umma_commit(&all_done[0]);
         mbar_wait(&all_done[0], 0);
       }
-    } else if (warp == 14) {
-      // -------------------------------------------------------- P V issuer
+    } else {
+      // ------------------------------------------------------- P V issuers
+      const uint32_t w = uint32_t(warp - 14);
       const uint64_t vd = make_sdesc_sw128(smem_u32(base) + S::kV16, 16384u, 1024);
       constexpr uint32_t ido = make_idesc_half(128, D, true);
       uint32_t t = 0;
       kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
         for (int u = u0; u < u1; ++u, ++t) {
-          const uint32_t b = t & 1;
-          if (!wait(&v16_full[b], (t >> 1) & 1, X8_V16_FULL)) return false;
-          if (!wait(&p_full[b], (t >> 1) & 1, X8_P_FULL)) return false;
+          const uint32_t vb = t & 1, j = 2 * t + w, b = j % kKv8Bufs;
+          if (!wait(&v16_full[vb], (t >> 1) & 1, X8_V16_FULL)) return false;
+          if (!wait(&p_full[w][vb], (t >> 1) & 1, X8_P_FULL)) return false;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)  // P: 32 columns in each half of the scores' place
-              umma_bf16_ts(tm + kKv8TmO, tm + b * 128u + uint32_t(ks >> 2) * 64u + uint32_t(ks & 3) * 8u,
-                           vd + ((b * S::kTile16) >> 4) + uint32_t(ks) * 128u, ido,
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16_ts(tm + kKv8TmO + w * 128u, tm + b * 64u + uint32_t(ks) * 8u,
+                           vd + ((vb * S::kTile16 + w * 8192u) >> 4) + uint32_t(ks) * 128u, ido,
                            u > u0 || ks > 0);
             umma_commit(&pv_done[b]);
-            umma_commit(&v16_free[b]);
+            umma_commit(&o_done[w]);
+            umma_commit(&v16_free[vb]);
           }
           __syncwarp();
         }
         return true;
       });
-      if (t > 0 && lane == 0) {
-        umma_commit(&all_done[1]);
-        mbar_wait(&all_done[1], 0);
+      if (t > 0 && elect_one()) {
+        umma_commit(&all_done[1 + w]);
+        mbar_wait(&all_done[1 + w], 0);
       }
     }
     __syncwarp();

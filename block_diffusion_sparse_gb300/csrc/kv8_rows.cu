@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
       const uint32_t b = x & 1, st = x % ST;
       if (!wait(&p_full[b], (x >> 1) & 1, W8_P_FULL)) return false;
       tc_fence_after();
-      if (lane == 0) {
+      if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           umma_e4m3(to, vd + ((st * S::kStage + uint32_t(ks) * 32u * D) >> 4),
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         const uint32_t st = t % ST;
         if (!wait(&full[st], (t / ST) & 1, W8_STAGE_FULL)) return false;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 32; ++ks)
             umma_e4m3(tm + (t & 1) * NS, kd + ((st * S::kStage + uint32_t(ks) * 32u) >> 4),
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
       return true;
     });
     // every product and commit is done before the tensor memory is given back
-    if (t > 0 && lane == 0) {
+    if (t > 0 && elect_one()) {
       umma_commit(&all_done);
       mbar_wait(&all_done, 0);
     }
@@ -354,10 +354,13 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
           ek = a.c.ks[at], ev = a.c.vs[at];
         }
       };
-      int phys = look(pos), ek, ev;
+      // (the table is read two groups of four tiles ahead, the scales one)
+      int phys = look(pos), next = look(pos + 512), ek, ev;
       scales(pos, phys, ek, ev);
       for (int u = u0; u < u1; u += 4, pos += 512) {
-        const int next = look(pos + 512);
+        const int after = look(pos + 1024);
+        int ek1, ev1;
+        scales(pos + 512, next, ek1, ev1);
         const bool on = pos < stop, have = on && phys >= 0 && phys < a.c.n_pages;
         debug_flag(on && !have, DEV_BAD_INDEX);
         const bool head = have && (gr & (page - 1)) == 0;  // this lane copies the page
@@ -391,8 +394,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         }
         if (u == u0)
           for (int i = 0; i < tiles; ++i) publish(i);
-        phys = next;
-        scales(pos + 512, phys, ek, ev);
+        phys = next, next = after, ek = ek1, ev = ev1;
         t += uint32_t(tiles);
       }
       return true;
