@@ -20,8 +20,11 @@
 //   warp 12    copies K and V tiles by TMA, looks up pages and scales four tiles ahead
 //   warp 13    issues S, in steps of 64 keys, the streams' in turn
 //   warps 14, 15  issue P V, one per stream
-// The steps go through three score buffers of 64 TMEM columns (P overlays the scores):
-// with both O and Q these fill the 512.
+// Tensor memory holds, for each stream, one step's scores (64 columns), its P (32) and O
+// (128), and Q (64): 512.  A step's scores are in registers before anything is done
+// with them, so the next step's product runs beside its softmax.  (With P over the
+// scores and three such buffers for both streams, each step waited for the product
+// before it: 1,800 cycles a tile.)
 // Scales: a key's multiplies its scores.  A value's exponent e_v goes into the weight's
 // own, P = 2^(x + e_v - m), and out of the row's sum again, l += P 2^-e_v, so O has one
 // unit and P fills fp16 whatever the values' scales.
@@ -46,7 +49,7 @@ constexpr float kKv8Below = 5.f, kKv8Top = 60000.f, kKv8TopLog2 = 15.8f;
 // Waits of the kernel (bits 16-31 of the error word).
 enum : uint32_t {
   X8_K_FREE = 1, X8_V_FREE = 2, X8_K_FULL = 4, X8_V_FULL = 8, X8_META = 0x10, X8_Q_FULL = 0x20,
-  X8_S_FULL = 0x40, X8_P_FULL = 0x80, X8_PV_DONE = 0x100, X8_V16_FREE = 0x200,
+  X8_S_FULL = 0x40, X8_P_FULL = 0x80, X8_S_READ = 0x100, X8_V16_FREE = 0x200,
   X8_V16_FULL = 0x400, X8_O_DONE = 0x800
 };
 
@@ -62,9 +65,8 @@ struct Kv8Tc {
   static constexpr uint32_t kV = kKv8KStages * kTile, kV16 = kV + kKv8VStages * kTile;
   static constexpr uint32_t kSmem = kV16 + 2 * kTile16 + 1024;
 };
-constexpr int kKv8Bufs = 3;  // score buffers
-// Tensor memory: the score buffers, q0, q1, both streams' O.
-constexpr uint32_t kKv8TmQ0 = 192, kKv8TmQ1 = 224, kKv8TmO = 256;
+// Tensor memory: both streams' scores, P, then q0, q1, both streams' O.
+constexpr uint32_t kKv8TmP = 128, kKv8TmQ0 = 192, kKv8TmQ1 = 224, kKv8TmO = 256;
 
 HERALD_DEV void umma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                              uint32_t accumulate) {
@@ -143,8 +145,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
   constexpr int KS = kKv8KStages, VS = kKv8VStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full[KS], k_free[KS], v_full[VS], v_free[VS], v16_full[2], v16_free[2],
-      meta_full[kKv8Metas], q_full, s_full[2][2], p_full[2][2], pv_done[kKv8Bufs], o_done[2],
-      all_done[3];
+      meta_full[kKv8Metas], q_full, s_full[2], s_read[2], p_full[2], o_done[2], all_done[3];
   __shared__ uint32_t tmem_base, failed;
   __shared__ __align__(16) Kv8TileMeta meta[kKv8Metas];
   __shared__ float2 row_ml[2][128];  // a piece's (m, l) of both streams
@@ -155,10 +156,9 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_free[i], 4);
     for (int i = 0; i < kKv8Metas; ++i) mbar_init(&meta_full[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 2), mbar_init(&o_done[i], 1);
-    // (by stream and parity of its steps: whoever waits on a barrier sees its every phase)
-    for (int i = 0; i < 4; ++i) mbar_init(&s_full[i & 1][i >> 1], 1), mbar_init(&p_full[i & 1][i >> 1], 4);
-    for (int i = 0; i < kKv8Bufs; ++i) mbar_init(&pv_done[i], 1), mbar_init(&all_done[i], 1);
+      mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 2), mbar_init(&o_done[i], 1),
+          mbar_init(&s_full[i], 1), mbar_init(&s_read[i], 4), mbar_init(&p_full[i], 4);
+    for (int i = 0; i < 3; ++i) mbar_init(&all_done[i], 1);
     mbar_init(&q_full, 8);
     failed = 0;
     fence_mbar_init();
@@ -172,9 +172,9 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
   const Kv4Share sh = kv4_share(a.ctx, a.N, a.L_max, a.Hkv * a.row_tiles, a.ctas, a.pad, 0,
                                 int(blockIdx.x));
 
-  // registers: 512 threads launch with 128 each (65,536) = 256 x (168 + 88)
+  // registers: 512 threads launch with 128 each (65,536) = 256 x (184 + 72)
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ------------------------------------------------------------ softmax
     // (after a failed wait these warps go on without waiting: the barriers among them
     // stay in step, the results are worthless and the error is recorded)
@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     };
     const int w = warp >> 2, lrow = (warp & 3) * 32 + lane;  // stream, TMEM lane
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t ts = tm + lanes + uint32_t(w) * 64u, tp = tm + lanes + kKv8TmP + uint32_t(w) * 32u;
     const uint32_t to = tm + lanes + kKv8TmO + uint32_t(w) * 128u, to2 = to ^ 128u;  // O, the other's
     uint32_t t = 0;
     kv8_pieces(a, sh, [&](int n, int gt, int seg, int ctx, int u0, int u1) -> bool {
@@ -239,10 +240,9 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
 
       float m = -FLT_MAX, l = 0.f;
       for (int u = u0; u < u1; ++u, ++t) {
-        const uint32_t j = 2 * t + uint32_t(w), b = j % kKv8Bufs, ts = tm + lanes + b * 64u;  // the step
         const Kv8TileMeta& mt = meta[t % kKv8Metas];
         await(&meta_full[t % kKv8Metas], (t / kKv8Metas) & 1, X8_META);
-        await(&s_full[w][t & 1], (t >> 1) & 1, X8_S_FULL);
+        await(&s_full[w], t & 1, X8_S_FULL);
         tc_fence_after();
         float sk[4], ev[4], iv[4];
         {
@@ -253,100 +253,85 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           ev[0] = y.x, ev[1] = y.y, ev[2] = y.z, ev[3] = y.w;
           iv[0] = z.x, iv[1] = z.y, iv[2] = z.z, iv[3] = z.w;
         }
-        if (!idle) {  // keys that do not count: scores of -inf
-          const uint4 k4 = *reinterpret_cast<const uint4*>(&mt.keys[4 * w]);
-          if (min(min(k4.x, k4.y), min(k4.z, k4.w)) < 16u) {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const int keys = int(mt.keys[4 * w + c]);
-              if (keys == 16) continue;
-              float v[16];
-              tmem_ld16(ts + uint32_t(c) * 16u, v);
-              uint32_t o[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = i < keys ? __float_as_uint(v[i]) : 0xFF800000u;
-              tmem_st8(ts + uint32_t(c) * 16u, *reinterpret_cast<uint32_t(*)[8]>(o));
-              tmem_st8(ts + uint32_t(c) * 16u + 8u, *reinterpret_cast<uint32_t(*)[8]>(o + 8));
-            }
-            tmem_wait_st();
-          }
-        }
+        auto await_o = [&] {  // the stream's product before has read P, and is in O
+          if (t > 0) await(&o_done[w], (t - 1) & 1, X8_O_DONE);
+          tc_fence_after();
+        };
+        uint32_t x[64], pk[32];
         if (!idle) {
-          uint32_t pk[32];
-          float add = 0.f;
-          bool high = true;
-          if (u > u0) {  // (a piece's first step has no base yet)
-            uint32_t x[32], y[32];
-            tmem_ld32_async(ts, x);
-            tmem_ld32_async(ts + 32u, y);
-            tmem_ld_done(x);
-            tmem_ld_done(y);
-            float sum = 0.f;
+          tmem_ld32_async(ts, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld32_async(ts + 32u, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+          tmem_ld_done(*reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld_done(*reinterpret_cast<uint32_t(*)[32]>(x + 32));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_read[w]);
+        if (!idle) {
+          const uint4 k4 = *reinterpret_cast<const uint4*>(&mt.keys[4 * w]);
+          if (min(min(k4.x, k4.y), min(k4.z, k4.w)) < 16u) {  // keys that do not count
+            const uint32_t keys[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float s = exp16((c < 2 ? x : y) + 16 * (c & 1), sk[c], ev[c] - m, pk + 8 * c);
-              sum += s;
-              add = fmaf(s, iv[c], add);
-            }
-            high = !(sum <= kKv8Top);
+            for (int i = 0; i < 64; ++i)
+              if (uint32_t(i & 15) >= keys[i / 16]) x[i] = 0xFF800000u;  // -inf
           }
-          if (__any_sync(0xffffffffu, high)) {
-            float z = -INFINITY;  // the largest exponent, rounded down: scores may be so large
-#pragma unroll 1                  // that fp32's steps are no longer small
-            for (int c = 0; c < 4; ++c) {
-              float v[16];
-              tmem_ld16(ts + uint32_t(c) * 16u, v);
+          float add = 0.f, sum = 0.f;
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                z = fmaxf(z, __fadd_rd(__fmul_rd(v[i], f * mt.sk[4 * w + c]), mt.ev[4 * w + c]));
-            }
-            float k = 1.f;
+          for (int c = 0; c < 4; ++c) {
+            const float s = exp16(x + 16 * c, sk[c], ev[c] - m, pk + 8 * c);
+            sum += s;
+            add = fmaf(s, iv[c], add);
+          }
+          const bool high = u == u0 || !(sum <= kKv8Top);  // (a piece's first step has no base yet)
+          const bool move = __any_sync(0xffffffffu, high);
+          float k = 1.f;
+          if (move) {
+            float z = -INFINITY;  // the largest exponent, rounded down: scores may be so large
+#pragma unroll                    // that fp32's steps are no longer small
+            for (int i = 0; i < 64; ++i)
+              z = fmaxf(z, __fadd_rd(__fmul_rd(__uint_as_float(x[i]), sk[i / 16]), ev[i / 16]));
             if (u == u0 || z - m > kKv8Below) {
               const float nb = fmaxf(__fadd_rd(z, -kKv8Below), -FLT_MAX);
               k = fast_exp2(m - nb);
               m = nb;
             }
             l *= k;
-            if (u > u0) {  // O so far, once the stream's product before is in it
-              await(&o_done[w], (t - 1) & 1, X8_O_DONE);
-              tc_fence_after();
-#pragma unroll 1
-              for (uint32_t c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(to + c, o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= k;
-                tmem_st32(to + c, o);
-              }
-            }
             add = 0.f;
-#pragma unroll 1
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const float fk = f * mt.sk[4 * w + c], nm = mt.ev[4 * w + c] - m;
-              float v[16];
-              tmem_ld16(ts + uint32_t(c) * 16u, v);
               float s = 0.f;
-              uint32_t o[8];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float x = fmaf(v[i], fk, nm);
-                v[i] = fast_exp2(x > kKv8TopLog2 ? kKv8TopLog2 : x);  // (a NaN stays)
-                s += v[i];
+              for (int i = 16 * c; i < 16 * c + 16; i += 2) {
+                float t0 = fmaf(__uint_as_float(x[i]), sk[c], ev[c] - m);
+                float t1 = fmaf(__uint_as_float(x[i + 1]), sk[c], ev[c] - m);
+                t0 = fast_exp2(t0 > kKv8TopLog2 ? kKv8TopLog2 : t0);  // (a NaN stays)
+                t1 = fast_exp2(t1 > kKv8TopLog2 ? kKv8TopLog2 : t1);
+                s += t0 + t1;
+                pk[i / 2] = pack_half2(t0, t1);
               }
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] = pack_half2(v[2 * i], v[2 * i + 1]);
-              add = fmaf(s, mt.iv[4 * w + c], add);
-              tmem_st8(ts + uint32_t(c) * 8u, o);  // (over scores that have been read)
+              add = fmaf(s, iv[c], add);
             }
-          } else {
-            tmem_st32(ts, *reinterpret_cast<float(*)[32]>(pk));
           }
           l += add;
+          await_o();
+          if (move && u > u0) {
+#pragma unroll 1
+            for (uint32_t c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(to + c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= k;
+              tmem_st32(to + c, o);
+            }
+          }
+          tmem_st32(tp, *reinterpret_cast<float(*)[32]>(pk));
           tmem_wait_st();
+        } else {
+          await_o();  // (no warp arrives twice in one phase of the barrier below)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w][t & 1]);
+        if (lane == 0) mbar_arrive(&p_full[w]);
       }
       // the piece's partials, once both streams' last products are done: each stream
       // reads both O for half of the channels and writes their sum
@@ -381,7 +366,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       return true;
     });
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < 12) {
       // ------------------------------------------------- values to fp16
       // A lane turns chunks of 16 channels: eight (d = 64: four) lanes read a row, and of
@@ -533,19 +518,18 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           if (!wait(&k_full[st], (t / KS) & 1, X8_K_FULL)) return false;
 #pragma unroll 1
           for (uint32_t w = 0; w < 2; ++w) {
-            // P of three steps before has been read: its buffer is free
-            const uint32_t j = 2 * t + w, b = j % kKv8Bufs;
-            if (j >= kKv8Bufs && !wait(&pv_done[b], (j / kKv8Bufs - 1) & 1, X8_PV_DONE)) return false;
+            // the stream's scores of the step before have been read
+            if (t > 0 && !wait(&s_read[w], (t - 1) & 1, X8_S_READ)) return false;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
               for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int ks = 0; ks < D / 32; ++ks)
-                  umma_e4m3_ts(tm + b * 64u, tm + (part ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(ks) * 8u,
+                  umma_e4m3_ts(tm + w * 64u, tm + (part ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(ks) * 8u,
                                kd + ((st * S::kTile + w * (64u * D) + uint32_t(ks) * 32u) >> 4), ids,
                                part + ks > 0);
-              umma_commit(&s_full[w][t & 1]);
+              umma_commit(&s_full[w]);
               if (w == 1) umma_commit(&k_free[st]);
             }
             __syncwarp();
@@ -566,17 +550,16 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       uint32_t t = 0;
       kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
         for (int u = u0; u < u1; ++u, ++t) {
-          const uint32_t vb = t & 1, j = 2 * t + w, b = j % kKv8Bufs;
+          const uint32_t vb = t & 1;
           if (!wait(&v16_full[vb], (t >> 1) & 1, X8_V16_FULL)) return false;
-          if (!wait(&p_full[w][vb], (t >> 1) & 1, X8_P_FULL)) return false;
+          if (!wait(&p_full[w], t & 1, X8_P_FULL)) return false;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_bf16_ts(tm + kKv8TmO + w * 128u, tm + b * 64u + uint32_t(ks) * 8u,
+              umma_bf16_ts(tm + kKv8TmO + w * 128u, tm + kKv8TmP + w * 32u + uint32_t(ks) * 8u,
                            vd + ((vb * S::kTile16 + w * 8192u) >> 4) + uint32_t(ks) * 128u, ido,
                            u > u0 || ks > 0);
-            umma_commit(&pv_done[b]);
             umma_commit(&o_done[w]);
             umma_commit(&v16_free[vb]);
           }
