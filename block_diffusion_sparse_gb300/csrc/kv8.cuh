@@ -51,18 +51,13 @@ HERALD_DEV uint32_t float2_to_e4m3(float lo, float hi) {
 // A query row as e4m3 numbers: values are multiplied by *up, the power of two that
 // brings the row's largest magnitude mx to [2^7, 2^8), and *f turns a product with a
 // key's codes into a log2-unit score (`scale` has log2(e) in it).  (mx below 2^-112
-// counts as that, infinities as 2^127; *f stays positive and finite, also times a key's
-// scale: a masked score of -inf times 0, or a zero score times inf, would be NaN.)
+// counts as that; with an infinity *up is a NaN, as inf - inf makes the row; *f stays
+// positive and finite, also times a key's scale: a zero score times inf would be NaN.)
 HERALD_DEV void kv8_query_scale(float mx, float scale, float* up, float* f) {
   const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -112), 127);
-  *up = exp2_int(7 - e);
+  *up = mx < INFINITY ? exp2_int(7 - e) : __uint_as_float(0x7FC00000u);
   *f = fminf(fmaxf(scale * exp2_int(e - 7), 0x1p-90f), 0x1p90f);
 }
-// One value of it; an infinity becomes a NaN, as inf - inf makes one of its row.
-HERALD_DEV float kv8_query(float x, float up) {
-  return fabsf(x) < INFINITY ? x * up : __uint_as_float(0x7FC00000u);
-}
-
 // One lane of a converged warp, the same every time: what it alone issues keeps its
 // operands in uniform registers (with `lane == 0` each mma moved them there anew).
 HERALD_DEV bool elect_one() {
@@ -71,6 +66,25 @@ HERALD_DEV bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r));
   return r != 0;
+}
+
+// fp16 pair -> e4m3 codes, as float2_to_e4m3 (a query goes through fp16, whose step below
+// 2^-14 is far under e4m3's)
+HERALD_DEV uint32_t half2_to_e4m3(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+HERALD_DEV uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Largest magnitudes so far and of a word of two bf16, as bits (a NaN does not count).
+HERALD_DEV uint32_t max_bf16x2_abs(uint32_t m, uint32_t w) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w & 0x7FFF7FFFu));
+  return d;
 }
 
 // ---- attention arguments shared by its kernels

@@ -142,41 +142,47 @@ HERALD_DEV void own_keys(const Kv8AttnArgs& a, OwnKeys<D>& sm, int n, int g, int
 }
 
 // The output: the pieces of a segment joined, with the block's own keys.  grid (N*Hkv,
-// ceil(R / Rows)); D/4 lanes hold a row's channels, four each, and GR groups of Rows
-// such rows share the pieces: each group takes every such-and-suchth, five in flight;
-// the groups are then added in order.  The block's keys come before the grid-dependency
-// wait: they and the lengths were written before the attention kernel's own wait
-// ended, and it lets this kernel start only after that.
-template <int D, int Rows, int GR>
-__global__ void __launch_bounds__(D / 4 * Rows * GR) kv8_join_kernel(const Kv8AttnArgs a) {
-  constexpr int TPR = D / 4;
-  static_assert(TPR * Rows * GR >= 32 * kOwnWarps, "warps of the block's keys");
+// ceil(R / Rows)); D/4 lanes hold a row's channels, four each, a thread has Per rows, and
+// GR groups of threads share the pieces: each takes every such-and-suchth, kFly rows'
+// worth in flight; the groups are then added in order.  The block's keys come before the
+// grid-dependency wait: they and the lengths were written before the attention
+// kernel's own wait ended, and it lets this kernel start only after that.
+template <int D, int Rows, int Per, int GR>
+__global__ void __launch_bounds__(D / 4 * Rows / Per * GR) kv8_join_kernel(const Kv8AttnArgs a) {
+  constexpr int TPR = D / 4, RS = Rows / Per;  // rows side by side
+  static_assert(TPR * RS * GR >= 32 * kOwnWarps, "warps of the block's keys");
   __shared__ OwnKeys<D> own;
   __shared__ float4 part[GR][Rows][TPR];
   __shared__ float part_m[GR][Rows], part_l[GR][Rows];
   const int seg = blockIdx.x, n = seg / a.Hkv, g = seg - n * a.Hkv;
   const int G = a.Hq / a.Hkv, R = a.B * G;
-  const int c4 = threadIdx.x % TPR, rr = threadIdx.x / TPR % Rows, grp = threadIdx.x / (TPR * Rows);
-  const int r0 = int(blockIdx.y) * Rows, r = r0 + rr, rc = min(r, R - 1);
-  const size_t row = (size_t(n) * a.B + rc / G) * a.Hq + g * G + rc % G;
-  const int heads = a.Hkv * a.row_tiles, tile = rc / a.R16, rt = rc - tile * a.R16;
+  const int c4 = threadIdx.x % TPR, rr = threadIdx.x / TPR % RS, grp = threadIdx.x / (TPR * RS);
+  const int r0 = int(blockIdx.y) * Rows;
+  // (the rows of a CTA lie in one row tile: Rows divides 128)
+  const int heads = a.Hkv * a.row_tiles, tile = r0 / a.R16;
   const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, 0, a.pad), heads, a.ctas);
   const int units = kv4_units(a.ctx[n], a.L_max, 0, a.pad), gt = g * a.row_tiles + tile;
   const int first = heads * kv4_total_units(a.ctx, n, a.L_max, 0, a.pad) + gt * units;
-  float M = -FLT_MAX, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M[Per], L[Per];
+  float4 acc[Per];
+#pragma unroll
+  for (int e = 0; e < Per; ++e) M[e] = -FLT_MAX, L[e] = 0.f, acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.bk) {
     const int warp = warp_same(int(threadIdx.x) >> 5);
     if (warp < kOwnWarps) own_keys<D>(a, own, n, g, r0, warp, threadIdx.x & 31);
     __syncthreads();
     if (grp == 0) {
       const int with = min(kOwnWarps, (a.B + 15) / 16);
-      for (int i = 0; i < with; ++i) M = fmaxf(M, own.m[i][rr]);
-      for (int i = 0; i < with; ++i) {
-        const float f = fast_exp2(own.m[i][rr] - M);
-        const float4 x = *reinterpret_cast<const float4*>(&own.o[i][rr][c4 * 4 + c4 / 8 * 4]);
-        L += f * own.l[i][rr];
-        acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+#pragma unroll
+      for (int e = 0; e < Per; ++e) {
+        const int r = rr + e * RS;
+        for (int i = 0; i < with; ++i) M[e] = fmaxf(M[e], own.m[i][r]);
+        for (int i = 0; i < with; ++i) {
+          const float f = fast_exp2(own.m[i][r] - M[e]);
+          const float4 x = *reinterpret_cast<const float4*>(&own.o[i][r][c4 * 4 + c4 / 8 * 4]);
+          L[e] += f * own.l[i][r];
+          acc[e].x += f * x.x, acc[e].y += f * x.y, acc[e].z += f * x.z, acc[e].w += f * x.w;
+        }
       }
     }
   }
@@ -184,69 +190,82 @@ __global__ void __launch_bounds__(D / 4 * Rows * GR) kv8_join_kernel(const Kv8At
   if (units > 0) {
     const int c0 = (first + a.pad) / split.share + n * heads + gt,
               c1 = (first + units - 1) / split.share + n * heads + gt;  // slots of its pieces
-    const float4* op = reinterpret_cast<const float4*>(a.opart) + size_t(rt) * (D / 4) + c4;
-    constexpr int kFly = 5;
+    const int rt = r0 - tile * a.R16 + rr, top = min(a.R16, R - tile * a.R16) - 1;
+    constexpr int kFly = Per > 1 ? 3 : 5;
     for (int c = c0 + grp; c <= c1; c += kFly * GR) {
-      float2 p[kFly];
-      float4 x[kFly];
+      float2 p[kFly][Per];
+      float4 x[kFly][Per];
 #pragma unroll
-      for (int i = 0; i < kFly; ++i) {
-        const int ci = c + i * GR;
-        p[i] = make_float2(-FLT_MAX, 0.f), x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ci <= c1) {
-          p[i] = a.ml[size_t(ci) * a.R16 + rt];
-          x[i] = op[size_t(ci) * a.R16 * (D / 4)];
+      for (int i = 0; i < kFly; ++i)
+#pragma unroll
+        for (int e = 0; e < Per; ++e) {
+          const int ci = c + i * GR;
+          const size_t at = size_t(ci) * a.R16 + min(rt + e * RS, top);
+          p[i][e] = make_float2(-FLT_MAX, 0.f), x[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (ci <= c1) {
+            p[i][e] = a.ml[at];
+            x[i][e] = reinterpret_cast<const float4*>(a.opart)[at * (D / 4) + c4];
+          }
         }
-      }
-      float M1 = M;
 #pragma unroll
-      for (int i = 0; i < kFly; ++i) M1 = fmaxf(M1, p[i].x);
-      const float w = fast_exp2(M - M1);
-      L *= w, acc.x *= w, acc.y *= w, acc.z *= w, acc.w *= w;
-      M = M1;
+      for (int e = 0; e < Per; ++e) {
+        float M1 = M[e];
 #pragma unroll
-      for (int i = 0; i < kFly; ++i) {
-        const float f = fast_exp2(p[i].x - M);
-        L += f * p[i].y;
-        acc.x += f * x[i].x, acc.y += f * x[i].y, acc.z += f * x[i].z, acc.w += f * x[i].w;
+        for (int i = 0; i < kFly; ++i) M1 = fmaxf(M1, p[i][e].x);
+        const float w = fast_exp2(M[e] - M1);
+        L[e] *= w, acc[e].x *= w, acc[e].y *= w, acc[e].z *= w, acc[e].w *= w;
+        M[e] = M1;
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+          const float f = fast_exp2(p[i][e].x - M1);
+          L[e] += f * p[i][e].y;
+          acc[e].x += f * x[i][e].x, acc[e].y += f * x[i][e].y;
+          acc[e].z += f * x[i][e].z, acc[e].w += f * x[i][e].w;
+        }
       }
     }
   }
   if constexpr (GR > 1) {
-    part[grp][rr][c4] = acc;
-    if (c4 == 0) part_m[grp][rr] = M, part_l[grp][rr] = L;
+    static_assert(Per == 1, "groups of one row a thread");
+    part[grp][rr][c4] = acc[0];
+    if (c4 == 0) part_m[grp][rr] = M[0], part_l[grp][rr] = L[0];
     __syncthreads();
     if (grp != 0) return;
 #pragma unroll
-    for (int i = 0; i < GR; ++i) M = fmaxf(M, part_m[i][rr]);
-    L = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < GR; ++i) M[0] = fmaxf(M[0], part_m[i][rr]);
+    L[0] = 0.f;
+    acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < GR; ++i) {
-      const float f = fast_exp2(part_m[i][rr] - M);
+      const float f = fast_exp2(part_m[i][rr] - M[0]);
       const float4 x = part[i][rr][c4];
-      L += f * part_l[i][rr];
-      acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+      L[0] += f * part_l[i][rr];
+      acc[0].x += f * x.x, acc[0].y += f * x.y, acc[0].z += f * x.z, acc[0].w += f * x.w;
     }
   }
-  if (r >= R) return;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  *reinterpret_cast<uint2*>(a.out + row * D + c4 * 4) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+#pragma unroll
+  for (int e = 0; e < Per; ++e) {
+    const int r = r0 + rr + e * RS;
+    if (r >= R) break;
+    const float inv = L[e] == 0.f ? 0.f : 1.f / L[e];
+    *reinterpret_cast<uint2*>(a.out + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c4 * 4) =
+        make_uint2(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv));
+  }
 }
 
 // ------------------------------------------------------------------- host
 
 template <int D>
 static cudaError_t launch_join(const Kv8AttnArgs& a, int R, int num_sms, cudaStream_t st) {
-  auto go = [&](auto* kernel, int rows, int groups) {
+  auto go = [&](auto* kernel, int rows, int threads) {
     return launch_k("kv8_join_kernel", kernel, dim3(unsigned(a.N * a.Hkv), unsigned(cdiv(R, rows))),
-                    dim3(unsigned(D / 4 * rows * groups)), 0, st, a);
+                    dim3(unsigned(threads)), 0, st, a);
   };
   const int64_t segs = int64_t(a.N) * a.Hkv;
-  if (segs * cdiv(R, 4) <= num_sms) return go(kv8_join_kernel<D, 4, 4>, 4, 4);
-  if (segs * cdiv(R, 8) <= num_sms || R <= 8) return go(kv8_join_kernel<D, 8, 2>, 8, 2);
-  return go(kv8_join_kernel<D, 16, 1>, 16, 1);
+  if (segs * cdiv(R, 4) <= num_sms) return go(kv8_join_kernel<D, 4, 1, 4>, 4, D * 4);
+  if (segs * cdiv(R, 8) <= num_sms) return go(kv8_join_kernel<D, 8, 1, 2>, 8, D * 4);
+  if (R <= 8) return go(kv8_join_kernel<D, 8, 1, 1>, 8, D * 2);
+  return go(kv8_join_kernel<D, 16, 2, 1>, 16, D * 2);
 }
 
 // Workspace: error word, then (m, l) and O of every partial.

@@ -40,9 +40,9 @@
 namespace herald {
 
 constexpr int kKv8TcThreads = 512;  // 16 warps
-constexpr int kKv8KStages = 5, kKv8VStages = 4;
-// Tiles whose scales and counts are kept for the softmax: K copies run at most five
-// tiles ahead of the scores, those two ahead of P, and look-ups four ahead of copies.
+constexpr int kKv8KStages = 4, kKv8VStages = 4;
+// Tiles whose scales and counts are kept for the softmax: K copies run at most four
+// tiles ahead of the scores, and those one ahead of the softmax.
 constexpr int kKv8Metas = 16;
 constexpr float kKv8Below = 5.f, kKv8Top = 60000.f, kKv8TopLog2 = 15.8f;
 
@@ -63,7 +63,8 @@ struct Kv8Tc {
   static constexpr uint32_t kTile = 128u * D;          // bytes of 128 keys as held
   static constexpr uint32_t kTile16 = uint32_t(D / 64) * 16384u;  // as fp16
   static constexpr uint32_t kV = kKv8KStages * kTile, kV16 = kV + kKv8VStages * kTile;
-  static constexpr uint32_t kSmem = kV16 + 2 * kTile16 + 1024;
+  static constexpr uint32_t kX = kV16 + 2 * kTile16;  // 2 KB for each softmax warp's transposes
+  static constexpr uint32_t kSmem = kX + 8 * 2048 + 1024;
 };
 // Tensor memory: both streams' scores, P, then q0, q1, both streams' O.
 constexpr uint32_t kKv8TmP = 128, kKv8TmQ0 = 192, kKv8TmQ1 = 224, kKv8TmO = 256;
@@ -182,56 +183,92 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     auto await = [&](uint64_t* bar, uint32_t parity, uint32_t which) {
       if (!lost) lost = !wait(bar, parity, which);
     };
+    auto await2 = [&](uint64_t* x, uint32_t px, uint64_t* y, uint32_t py) {
+      if (lost) return;
+      const bool a0 = mbar_try_wait(x, px), b0 = mbar_try_wait(y, py);  // (both at once)
+      if (__all_sync(0xffffffffu, a0 && b0)) return;
+      lost = !wait(x, px, X8_META) || !wait(y, py, X8_S_FULL);
+    };
     const int w = warp >> 2, lrow = (warp & 3) * 32 + lane;  // stream, TMEM lane
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tm + lanes + uint32_t(w) * 64u, tp = tm + lanes + kKv8TmP + uint32_t(w) * 32u;
     const uint32_t to = tm + lanes + kKv8TmO + uint32_t(w) * 128u, to2 = to ^ 128u;  // O, the other's
+    uint8_t* xb = base + S::kX + warp * 2048;
+    const int per_g = 65536 / G + 1;  // r / G = r per_g / 2^16 for the rows r < 256
     uint32_t t = 0;
     kv8_pieces(a, sh, [&](int n, int gt, int seg, int ctx, int u0, int u1) -> bool {
       debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
       const int g = gt / a.row_tiles, r0 = (gt - g * a.row_tiles) * 128;
       const bool idle = r0 + (warp & 3) * 32 >= R;  // the warp has no rows
-      const int row = r0 + lrow, rc = min(row, R - 1);
-      // queries: a thread has its row whole; the first half of the warps stores q0, the
-      // other q1.  (The scores of the piece before have been read: nothing reads Q now.)
+      const int row = r0 + lrow;
+      // queries: D/8 lanes load a row, as e4m3 it goes through shared memory to the lane
+      // that has it in tensor memory, 16 rows at a time; the first half of the warps stores
+      // q0, the other q1.  (A lane loading its row by itself touched 32 lines an
+      // instruction: 6 us until the first scores.)  The scores of the piece before have
+      // been read: nothing reads Q now.
       float f = 0.f;
       if (!idle) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((size_t(n) * a.B + rc / G) * a.Hq + g * G + rc % G) * D);
-        uint4 x[D / 8];
+        constexpr int LPR = D / 8, RPP = 32 / LPR, P = 32 / RPP, W = D / 4;
+        const int c = lane % LPR, sub = lane / LPR;
+        const uint16_t* q0 = a.q + (size_t(n) * a.B * a.Hq + g * G) * D + c * 8;
+        uint32_t o[W];  // this lane's row
+        // (in turns of 16 rows: the code of a start comes from far, and is kept short)
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint4 x[P / 2];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = src[i];
-        float mx = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx = fmax3f(mx, fabsf(bf16lo(wd[j])), fabsf(bf16hi(wd[j])));
-        }
-        float up;
-        kv8_query_scale(mx, a.scale, &up, &f);
-#pragma unroll
-        for (int i = 0; i < D / 8; i += 4) {  // 32 channels, 8 columns
-          uint32_t o[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t wd[4] = {x[i + k].x, x[i + k].y, x[i + k].z, x[i + k].w};
-            uint32_t c[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float v0 = kv8_query(bf16lo(wd[j]), up), v1 = kv8_query(bf16hi(wd[j]), up);
-              c[j] = float2_to_e4m3(v0, v1);
-              if (w == 1) {  // what q0 left
-                const uint32_t h = e4m3x2_to_half2(c[j]);
-                const float2 q0 = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                c[j] = float2_to_e4m3(v0 - q0.x, v1 - q0.y);
-              }
-            }
-            o[2 * k] = c[0] | c[1] << 16;
-            o[2 * k + 1] = c[2] | c[3] << 16;
+          for (int p = 0; p < P / 2; ++p) {
+            const int r = min(r0 + (warp & 3) * 32 + h * 16 + p * RPP + sub, R - 1);
+            const int tok = r * per_g >> 16;  // r / G
+            x[p] = *reinterpret_cast<const uint4*>(q0 + (r + tok * (a.Hq - G)) * D);
           }
-          tmem_st8(tm + lanes + (w ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(i) * 2u, o);
+          float mx[P / 2];  // (the rows' maxima side by side: their steps wait on one another)
+#pragma unroll
+          for (int p = 0; p < P / 2; ++p) {
+            const uint32_t m4 = max_bf16x2_abs(
+                max_bf16x2_abs(max_bf16x2_abs(max_bf16x2_abs(0, x[p].x), x[p].y), x[p].z), x[p].w);
+            mx[p] = fmaxf(bf16lo(m4), bf16hi(m4));
+          }
+#pragma unroll
+          for (int i = 1; i < LPR; i <<= 1)
+#pragma unroll
+            for (int p = 0; p < P / 2; ++p)
+              mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], i));
+#pragma unroll
+          for (int p = 0; p < P / 2; ++p) {
+            float up, fp;
+            kv8_query_scale(mx[p], a.scale, &up, &fp);
+            fp = __shfl_sync(0xffffffffu, fp, lane % RPP * LPR);
+            if (lane / RPP == h * (P / 2) + p) f = fp;
+            const uint32_t wd[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t h2 = pack_half2(bf16lo(wd[i]) * up, bf16hi(wd[i]) * up);
+              v[i] = half2_to_e4m3(h2);
+              const uint32_t rest = half2_to_e4m3(hsub2(h2, e4m3x2_to_half2(v[i])));  // what q0 left
+              v[i] = w ? rest : v[i];
+            }
+            const uint32_t r = uint32_t(p * RPP + sub);
+            *reinterpret_cast<uint2*>(xb + r * D + ((uint32_t(c >> 1) ^ (r & (D / 16 - 1))) << 4) +
+                                      (c & 1) * 8) = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+          }
+          __syncwarp();
+          if (lane >> 4 == h) {
+            const uint32_t r = uint32_t(lane) & 15u;
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+              const uint4 y = *reinterpret_cast<const uint4*>(
+                  xb + r * D + ((uint32_t(i) ^ (r & (D / 16 - 1))) << 4));
+              o[4 * i] = y.x, o[4 * i + 1] = y.y, o[4 * i + 2] = y.z, o[4 * i + 3] = y.w;
+            }
+          }
+          __syncwarp();
         }
+#pragma unroll
+        for (int i = 0; i < W; i += 8)
+          tmem_st8(tm + lanes + (w ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(i),
+                   *reinterpret_cast<uint32_t(*)[8]>(o + i));
         tmem_wait_st();
       }
       tc_fence_before();
@@ -239,34 +276,31 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       if (lane == 0) mbar_arrive(&q_full);
 
       float m = -FLT_MAX, l = 0.f;
-      for (int u = u0; u < u1; ++u, ++t) {
-        const Kv8TileMeta& mt = meta[t % kKv8Metas];
-        await(&meta_full[t % kKv8Metas], (t / kKv8Metas) & 1, X8_META);
-        await(&s_full[w], t & 1, X8_S_FULL);
+      uint32_t x[64];
+      // the scores of tile tt, and that they have been read
+      auto begin_load = [&](uint32_t tt) {
+        await2(&meta_full[tt % kKv8Metas], (tt / kKv8Metas) & 1, &s_full[w], tt & 1);
         tc_fence_after();
-        float sk[4], ev[4], iv[4];
-        {
-          const float4 x = *reinterpret_cast<const float4*>(&mt.sk[4 * w]);
-          const float4 y = *reinterpret_cast<const float4*>(&mt.ev[4 * w]);
-          const float4 z = *reinterpret_cast<const float4*>(&mt.iv[4 * w]);
-          sk[0] = f * x.x, sk[1] = f * x.y, sk[2] = f * x.z, sk[3] = f * x.w;
-          ev[0] = y.x, ev[1] = y.y, ev[2] = y.z, ev[3] = y.w;
-          iv[0] = z.x, iv[1] = z.y, iv[2] = z.z, iv[3] = z.w;
-        }
-        auto await_o = [&] {  // the stream's product before has read P, and is in O
-          if (t > 0) await(&o_done[w], (t - 1) & 1, X8_O_DONE);
-          tc_fence_after();
-        };
-        uint32_t x[64], pk[32];
         if (!idle) {
           tmem_ld32_async(ts, *reinterpret_cast<uint32_t(*)[32]>(x));
           tmem_ld32_async(ts + 32u, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
-          tmem_ld_done(*reinterpret_cast<uint32_t(*)[32]>(x));
-          tmem_ld_done(*reinterpret_cast<uint32_t(*)[32]>(x + 32));
         }
+      };
+      auto end_load = [&] {
+        tmem_ld_done(*reinterpret_cast<uint32_t(*)[32]>(x));
+        tmem_ld_done(*reinterpret_cast<uint32_t(*)[32]>(x + 32));
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_read[w]);
+      };
+      begin_load(t);
+      end_load();
+#pragma unroll 1
+      for (int u = u0; u < u1; ++u, ++t) {
+        const Kv8TileMeta& mt = meta[t % kKv8Metas];
+        uint32_t pk[32];
+        float k = 1.f;
+        bool moved = false;
         if (!idle) {
           const uint4 k4 = *reinterpret_cast<const uint4*>(&mt.keys[4 * w]);
           if (min(min(k4.x, k4.y), min(k4.z, k4.w)) < 16u) {  // keys that do not count
@@ -275,63 +309,87 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
             for (int i = 0; i < 64; ++i)
               if (uint32_t(i & 15) >= keys[i / 16]) x[i] = 0xFF800000u;  // -inf
           }
-          float add = 0.f, sum = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float s = exp16(x + 16 * c, sk[c], ev[c] - m, pk + 8 * c);
-            sum += s;
-            add = fmaf(s, iv[c], add);
+          float fk[4], ev[4], iv[4];  // P = 2^(score fk + ev - m)
+          {
+            const float4 a4 = *reinterpret_cast<const float4*>(&mt.sk[4 * w]);
+            const float4 b4 = *reinterpret_cast<const float4*>(&mt.ev[4 * w]);
+            const float4 c4 = *reinterpret_cast<const float4*>(&mt.iv[4 * w]);
+            fk[0] = f * a4.x, fk[1] = f * a4.y, fk[2] = f * a4.z, fk[3] = f * a4.w;
+            ev[0] = b4.x, ev[1] = b4.y, ev[2] = b4.z, ev[3] = b4.w;
+            iv[0] = c4.x, iv[1] = c4.y, iv[2] = c4.z, iv[3] = c4.w;
           }
-          const bool high = u == u0 || !(sum <= kKv8Top);  // (a piece's first step has no base yet)
-          const bool move = __any_sync(0xffffffffu, high);
-          float k = 1.f;
-          if (move) {
-            float z = -INFINITY;  // the largest exponent, rounded down: scores may be so large
-#pragma unroll                    // that fp32's steps are no longer small
-            for (int i = 0; i < 64; ++i)
-              z = fmaxf(z, __fadd_rd(__fmul_rd(__uint_as_float(x[i]), sk[i / 16]), ev[i / 16]));
+          float add;
+          float base = m;
+          while (true) {
+            add = 0.f;
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float s = exp16(x + 16 * c, fk[c], ev[c] - base, pk + 8 * c);
+              sum += s;
+              add = fmaf(s, iv[c], add);
+            }
+            const bool high = u == u0 || !(sum <= kKv8Top);  // (a piece's first step has no base)
+            if (moved || !__any_sync(0xffffffffu, high)) break;
+            moved = true;
+            // the largest exponent, rounded down: scores may be so large that fp32's steps
+            // are no longer small
+            float z = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float mx = -INFINITY;
+#pragma unroll
+              for (int i = 16 * c; i < 16 * c + 16; i += 2)
+                mx = fmax3f(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+              z = fmaxf(z, __fadd_rd(__fmul_rd(mx, fk[c]), ev[c]));
+            }
             if (u == u0 || z - m > kKv8Below) {
               const float nb = fmaxf(__fadd_rd(z, -kKv8Below), -FLT_MAX);
               k = fast_exp2(m - nb);
               m = nb;
             }
             l *= k;
-            add = 0.f;
+            base = m;
+            // P of scores within a step of so large a base may pass fp16: no further than
+            // its largest (the exponents themselves stand for the scores then)
+            if (__any_sync(0xffffffffu, fabsf(m) > kKv4Far && m > -FLT_MAX)) {
+              const bool far = fabsf(m) > kKv4Far && m > -FLT_MAX;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float s = 0.f;
+              for (int c = 0; c < 4; ++c) {
 #pragma unroll
-              for (int i = 16 * c; i < 16 * c + 16; i += 2) {
-                float t0 = fmaf(__uint_as_float(x[i]), sk[c], ev[c] - m);
-                float t1 = fmaf(__uint_as_float(x[i + 1]), sk[c], ev[c] - m);
-                t0 = fast_exp2(t0 > kKv8TopLog2 ? kKv8TopLog2 : t0);  // (a NaN stays)
-                t1 = fast_exp2(t1 > kKv8TopLog2 ? kKv8TopLog2 : t1);
-                s += t0 + t1;
-                pk[i / 2] = pack_half2(t0, t1);
+                for (int i = 16 * c; i < 16 * c + 16; ++i) {
+                  const float e = fmaf(__uint_as_float(x[i]), fk[c], ev[c] - m);
+                  if (far) x[i] = __float_as_uint(e > kKv8TopLog2 ? kKv8TopLog2 : e);  // (a NaN stays)
+                }
+                if (far) fk[c] = 1.f, ev[c] = 0.f;
               }
-              add = fmaf(s, iv[c], add);
+              if (far) base = 0.f;
             }
           }
           l += add;
-          await_o();
-          if (move && u > u0) {
-#pragma unroll 1
-            for (uint32_t c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld32(to + c, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= k;
-              tmem_st32(to + c, o);
-            }
-          }
-          tmem_st32(tp, *reinterpret_cast<float(*)[32]>(pk));
-          tmem_wait_st();
-        } else {
-          await_o();  // (no warp arrives twice in one phase of the barrier below)
         }
+        // the stream's product before has read P, and is in O (idle warps wait too: no
+        // warp arrives twice in one phase of p_full)
+        if (t > 0) await(&o_done[w], (t - 1) & 1, X8_O_DONE);
+        tc_fence_after();
+        if (moved && u > u0) {
+#pragma unroll 1
+          for (uint32_t c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(to + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= k;
+            tmem_st32(to + c, o);
+          }
+        }
+        // the next scores come while P goes
+        if (u + 1 < u1) begin_load(t + 1);
+        if (!idle) tmem_st32(tp, *reinterpret_cast<float(*)[32]>(pk));
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[w]);
+        if (u + 1 < u1) end_load();
       }
       // the piece's partials, once both streams' last products are done: each stream
       // reads both O for half of the channels and writes their sum
@@ -345,21 +403,39 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         const float2 o2 = row_ml[w ^ 1][lrow];
         const float mm = fmaxf(m, o2.x), w0 = fast_exp2(m - mm), w1 = fast_exp2(o2.x - mm);
         if (w == 0 && row < R) a.ml[slot * a.R16 + lrow] = make_float2(mm, w0 * l + w1 * o2.y);
-        float4* out = reinterpret_cast<float4*>(a.opart + (slot * a.R16 + lrow) * D + w * (D / 2));
+        // 16 channels at a time through shared memory, so that a row's 64 bytes are written
+        // by neighbouring lanes (a lane writing its own row took 2.8 us a piece)
 #pragma unroll 1
         for (uint32_t c = 0; c < D / 2; c += 32) {
-          float o[32], p[32];
-          tmem_ld32(to + uint32_t(w) * (D / 2) + c, o);
-          tmem_ld32(to2 + uint32_t(w) * (D / 2) + c, p);
-          if (row < R) {
+          uint32_t o[32], p[32];
+          tmem_ld32_async(to + uint32_t(w) * (D / 2) + c, o);
+          tmem_ld32_async(to2 + uint32_t(w) * (D / 2) + c, p);
+          tmem_ld_done(o);
+          tmem_ld_done(p);
+          float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              out[(c + i) / 4] =
-                  make_float4(fmaf(p[i], w1, o[i] * w0), fmaf(p[i + 1], w1, o[i + 1] * w0),
-                              fmaf(p[i + 2], w1, o[i + 2] * w0), fmaf(p[i + 3], w1, o[i + 3] * w0));
+          for (int i = 0; i < 32; ++i)
+            v[i] = fmaf(__uint_as_float(p[i]), w1, __uint_as_float(o[i]) * w0);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(xb + rows_off<64>(uint32_t(lane), uint32_t(i))) =
+                  make_float4(v[16 * e + 4 * i], v[16 * e + 4 * i + 1], v[16 * e + 4 * i + 2],
+                              v[16 * e + 4 * i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 8 + (lane >> 2), lr = (warp & 3) * 32 + r;
+              if (r0 + lr < R)
+                *reinterpret_cast<float4*>(a.opart + (slot * a.R16 + lr) * D + w * (D / 2) + c + 16 * e +
+                                           (lane & 3) * 4) =
+                    *reinterpret_cast<const float4*>(xb + rows_off<64>(uint32_t(r), uint32_t(lane & 3)));
+            }
           }
-          __syncwarp();
         }
+        __syncwarp();
       }
       tc_fence_before();
       tc_bar();  // (O and row_ml have been read: the next piece may begin)
@@ -369,23 +445,25 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < 12) {
       // ------------------------------------------------- values to fp16
-      // A lane turns chunks of 16 channels: eight (d = 64: four) lanes read a row, and of
-      // the two chunks that each writes, with d = 128 the lanes of the row's second half
-      // write theirs in the other order, so that the eight lanes of a shared-memory phase
-      // meet eight different groups of banks (with d = 64 they are two rows of them).
+      // A lane turns chunks of 16 channels, one of which becomes two: eight (d = 64: four)
+      // neighbouring lanes read eight chunks of one row (two rows).  With d = 128 the lanes
+      // of a row's second half take the row beside it, so that in reads and writes the
+      // eight lanes of a shared-memory phase meet eight different groups of banks.
       // Every load of a tile first: with two chunks under way at a time a tile took
       // 1,500 cycles, which was the longest of all roles.
       constexpr int CPR = D / 16, RPW = 32 / CPR, kTasks = 32 / RPW, kPar = 8 / RPW;
-      const int c = lane % CPR, cw = warp - 8, sub = lane / CPR;
-      const uint32_t flip = D == 128 ? uint32_t(c >> 2) : 0u;
+      const int c = lane % CPR, cw = warp - 8;
+      // row (of the warp's 32) of task s: eight more every kPar tasks
+      auto row_of = [&](int s) {
+        return D == 128 ? (s >> 1) * 8 + (lane >> 3) * 2 + ((s & 1) ^ (c >> 2)) : s * 8 + (lane >> 2);
+      };
       const uint32_t vs = smem_u32(base) + S::kV, v16 = smem_u32(base) + S::kV16;
-      // places of the lane's first chunks; the others are eight rows on, and on
       uint32_t from[kPar], to[kPar];
 #pragma unroll
       for (int i = 0; i < kPar; ++i) {
-        const uint32_t r = uint32_t(cw * 32 + i * RPW + sub);
+        const uint32_t r = uint32_t(cw * 32 + row_of(i));
         from[i] = rows_off<D>(r, uint32_t(c));
-        to[i] = uint32_t(D == 128 ? c >> 2 : 0) * 16384u + sw128_off(r, uint32_t(c & 3) * 2u | flip);
+        to[i] = uint32_t(D == 128 ? c >> 2 : 0) * 16384u + sw128_off(r, uint32_t(c & 3) * 2u);
       }
       uint32_t t = 0;
       kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
@@ -404,7 +482,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           if (min(k0, k1) < 16u) {  // rows that do not count may hold any bytes: no 0 * NaN
 #pragma unroll
             for (int s = 0; s < kTasks; ++s) {
-              const uint32_t r = uint32_t(s * RPW + sub);
+              const uint32_t r = uint32_t(row_of(s));
               if ((r & 15u) >= (r < 16u ? k0 : k1)) x[s] = make_uint4(0, 0, 0, 0);
             }
           }
@@ -416,13 +494,8 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
             e4m3x4_to_half2(x[s].z, h[4], h[5]);
             e4m3x4_to_half2(x[s].w, h[6], h[7]);
             const uint32_t at = dst + to[s % kPar] + uint32_t(s / kPar) * 1024u;
-            if (flip) {
-              sts128(at, h[4], h[5], h[6], h[7]);
-              sts128(at ^ 16u, h[0], h[1], h[2], h[3]);
-            } else {
-              sts128(at, h[0], h[1], h[2], h[3]);
-              sts128(at ^ 16u, h[4], h[5], h[6], h[7]);
-            }
+            sts128(at, h[0], h[1], h[2], h[3]);
+            sts128(at ^ 16u, h[4], h[5], h[6], h[7]);
           }
           fence_proxy_async_smem();
           __syncwarp();

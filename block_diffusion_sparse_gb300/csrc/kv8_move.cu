@@ -11,12 +11,6 @@ namespace herald {
 
 constexpr int kKv8MoveThreads = 256;
 
-// Largest magnitude of a word of two bf16, as bits (a NaN does not count).
-HERALD_DEV uint32_t max_bf16x2_abs(uint32_t m, uint32_t w) {
-  uint32_t d;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w & 0x7FFF7FFFu));
-  return d;
-}
 // The smallest exponent e with top <= 448 2^e (448 = 1.75 2^8), of a bf16 magnitude's
 // bits, within the scales' range.
 HERALD_DEV int kv8_need(uint32_t top) {

@@ -62,11 +62,6 @@ struct Kv8Meta {
   uint8_t keys, pad;
 };
 
-HERALD_DEV void stage_e4m3x8(uint8_t* at, const float (&x)[8]) {
-  *reinterpret_cast<uint2*>(at) =
-      make_uint2(float2_to_e4m3(x[0], x[1]) | float2_to_e4m3(x[2], x[3]) << 16,
-                 float2_to_e4m3(x[4], x[5]) | float2_to_e4m3(x[6], x[7]) << 16);
-}
 // x -> 16 (x - e4m3(x)) for a pair, returning the codes: what the next number holds.
 HERALD_DEV uint32_t split_e4m3(float& a, float& b) {
   const uint32_t w = float2_to_e4m3(a, b);
@@ -420,31 +415,36 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
               a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c * 8);
       }
       if (np >= 2 && !wait(&q_free[qb], ((np >> 1) - 1) & 1, W8_Q_FREE)) return false;
+      float mx[P];  // (the rows' maxima side by side: their steps wait on one another)
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        const int r = p * RPP + sub;
+        const uint32_t m = max_bf16x2_abs(
+            max_bf16x2_abs(max_bf16x2_abs(max_bf16x2_abs(0, x[p].x), x[p].y), x[p].z), x[p].w);
+        mx[p] = fmaxf(bf16lo(m), bf16hi(m));
+      }
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+        for (int p = 0; p < P; ++p) mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], o));
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const uint32_t r = uint32_t(p * RPP + sub), half = uint32_t(c & 1) * 8u;
+        float up, f;
+        kv8_query_scale(mx[p], a.scale, &up, &f);
         const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-        float v[8], mx = 0.f;
+        uint32_t v0[4], v1[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[2 * i] = bf16lo(w[i]), v[2 * i + 1] = bf16hi(w[i]);
-          mx = fmax3f(mx, fabsf(v[2 * i]), fabsf(v[2 * i + 1]));
+          const uint32_t h = pack_half2(bf16lo(w[i]) * up, bf16hi(w[i]) * up);
+          v0[i] = half2_to_e4m3(h);
+          const uint32_t rest = hsub2(h, e4m3x2_to_half2(v0[i]));  // what q0 left, times 16
+          v1[i] = half2_to_e4m3(hmul2(rest, 0x4C004C00u));
         }
-#pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        float up, f;
-        kv8_query_scale(mx, a.scale, &up, &f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = kv8_query(v[i], up);
         uint8_t* dst = Qs + qb * S::kQ;
-        const uint32_t half = uint32_t(c & 1) * 8u;
-        float q0[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q0[i] = v[i];
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) split_e4m3(v[i], v[i + 1]);
-        stage_e4m3x8(dst + rows_off<D>(uint32_t(r), uint32_t(c >> 1)) + half, q0);
-        stage_e4m3x8(dst + rows_off<D>(uint32_t(RP + r), uint32_t(c >> 1)) + half, v);
+        *reinterpret_cast<uint2*>(dst + rows_off<D>(r, uint32_t(c >> 1)) + half) =
+            make_uint2(v0[0] | v0[1] << 16, v0[2] | v0[3] << 16);
+        *reinterpret_cast<uint2*>(dst + rows_off<D>(uint32_t(RP) + r, uint32_t(c >> 1)) + half) =
+            make_uint2(v1[0] | v1[1] << 16, v1[2] | v1[3] << 16);
         if (c == 0) row_f[qb][r] = f;
       }
       fence_proxy_async_smem();
