@@ -146,32 +146,80 @@ HERALD_DEV void own_keys(const Kv8AttnArgs& a, OwnKeys<D>& sm, int n, int g, int
 // GR groups of threads share the pieces: each takes every such-and-suchth, kFly rows'
 // worth in flight; the groups are then added in order.  The block's keys come before the
 // grid-dependency wait: they and the lengths were written before the attention
-// kernel's own wait ended, and it lets this kernel start only after that.
-template <int D, int Rows, int Per, int GR>
-__global__ void __launch_bounds__(D / 4 * Rows / Per * GR) kv8_join_kernel(const Kv8AttnArgs a) {
+// kernel's own wait ended, and it lets this kernel start only after that.  Few of them
+// (not Tc) are taken one after another by the row's lanes, every load first.
+constexpr int kOwnFew = 4;  // block keys at most that the lanes take
+template <int D, int Rows, int Per, int GR, bool Tc>
+__global__ void __launch_bounds__(D / 4 * Rows / Per * GR, Tc && GR == 1 ? 2 : 1)
+    kv8_join_kernel(const Kv8AttnArgs a) {
   constexpr int TPR = D / 4, RS = Rows / Per;  // rows side by side
-  static_assert(TPR * RS * GR >= 32 * kOwnWarps, "warps of the block's keys");
-  __shared__ OwnKeys<D> own;
-  __shared__ float4 part[GR][Rows][TPR];
+  static_assert(!Tc || TPR * RS * GR > 32 * kOwnWarps || GR == 1, "warps of the block's keys");
+  __shared__ OwnKeys<Tc ? D : 32> own;
+  __shared__ float4 part[GR][GR > 1 ? Rows : 1][TPR];
   __shared__ float part_m[GR][Rows], part_l[GR][Rows];
+  __shared__ int pieces[2];
   const int seg = blockIdx.x, n = seg / a.Hkv, g = seg - n * a.Hkv;
   const int G = a.Hq / a.Hkv, R = a.B * G;
   const int c4 = threadIdx.x % TPR, rr = threadIdx.x / TPR % RS, grp = threadIdx.x / (TPR * RS);
-  const int r0 = int(blockIdx.y) * Rows;
+  const int r0 = int(blockIdx.y) * Rows, warp = warp_same(int(threadIdx.x) >> 5);
   // (the rows of a CTA lie in one row tile: Rows divides 128)
   const int heads = a.Hkv * a.row_tiles, tile = r0 / a.R16;
-  const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, 0, a.pad), heads, a.ctas);
-  const int units = kv4_units(a.ctx[n], a.L_max, 0, a.pad), gt = g * a.row_tiles + tile;
-  const int first = heads * kv4_total_units(a.ctx, n, a.L_max, 0, a.pad) + gt * units;
+  if (warp == int(blockDim.x) / 32 - 1) {  // slots of the segment's pieces
+    const Kv4Split split = kv4_split(kv4_total_units(a.ctx, a.N, a.L_max, 0, a.pad), heads, a.ctas);
+    const int units = kv4_units(a.ctx[n], a.L_max, 0, a.pad), gt = g * a.row_tiles + tile;
+    const int first = heads * kv4_total_units(a.ctx, n, a.L_max, 0, a.pad) + gt * units;
+    if ((threadIdx.x & 31) == 0) {
+      pieces[0] = units > 0 ? (first + a.pad) / split.share + n * heads + gt : 0;
+      pieces[1] = units > 0 ? (first + units - 1) / split.share + n * heads + gt : -1;
+    }
+  }
   float M[Per], L[Per];
   float4 acc[Per];
 #pragma unroll
   for (int e = 0; e < Per; ++e) M[e] = -FLT_MAX, L[e] = 0.f, acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (a.bk) {
-    const int warp = warp_same(int(threadIdx.x) >> 5);
-    if (warp < kOwnWarps) own_keys<D>(a, own, n, g, r0, warp, threadIdx.x & 31);
-    __syncthreads();
+  if constexpr (Tc) {
+    if (a.bk && warp < kOwnWarps) own_keys<D>(a, own, n, g, r0, warp, threadIdx.x & 31);
+  } else if (a.bk) {
+    static_assert(Per == 1, "one row a thread");
+    const int r = min(r0 + rr, R - 1);
+    const uint2 qw = *reinterpret_cast<const uint2*>(
+        a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c4 * 4);
+    uint2 kw[kOwnFew], vw[kOwnFew];
+#pragma unroll
+    for (int j = 0; j < kOwnFew; ++j) {
+      const size_t at = ((size_t(n) * a.B + min(j, a.B - 1)) * a.Hkv + g) * D + c4 * 4;
+      kw[j] = *reinterpret_cast<const uint2*>(a.bk + at);
+      vw[j] = *reinterpret_cast<const uint2*>(a.bv + at);
+    }
+    float s[kOwnFew];
+#pragma unroll
+    for (int j = 0; j < kOwnFew; ++j)
+      s[j] = fmaf(bf16lo(qw.x), bf16lo(kw[j].x), bf16hi(qw.x) * bf16hi(kw[j].x)) +
+             fmaf(bf16lo(qw.y), bf16lo(kw[j].y), bf16hi(qw.y) * bf16hi(kw[j].y));
+#pragma unroll
+    for (int o = 1; o < TPR; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < kOwnFew; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
     if (grp == 0) {
+#pragma unroll
+      for (int j = 0; j < kOwnFew; ++j) {
+        s[j] = j < a.B ? s[j] * a.scale : -INFINITY;
+        M[0] = fmaxf(M[0], s[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kOwnFew; ++j) {
+        const float p = fast_exp2(s[j] - M[0]);
+        if (j >= a.B) break;
+        L[0] += p;
+        acc[0].x = fmaf(p, bf16lo(vw[j].x), acc[0].x), acc[0].y = fmaf(p, bf16hi(vw[j].x), acc[0].y);
+        acc[0].z = fmaf(p, bf16lo(vw[j].y), acc[0].z), acc[0].w = fmaf(p, bf16hi(vw[j].y), acc[0].w);
+      }
+    }
+  }
+  __syncthreads();
+  const int c0 = pieces[0], c1 = pieces[1];
+  if constexpr (Tc) {
+    if (a.bk && grp == 0) {
       const int with = min(kOwnWarps, (a.B + 15) / 16);
 #pragma unroll
       for (int e = 0; e < Per; ++e) {
@@ -187,9 +235,7 @@ __global__ void __launch_bounds__(D / 4 * Rows / Per * GR) kv8_join_kernel(const
     }
   }
   griddep_enter();
-  if (units > 0) {
-    const int c0 = (first + a.pad) / split.share + n * heads + gt,
-              c1 = (first + units - 1) / split.share + n * heads + gt;  // slots of its pieces
+  {
     const int rt = r0 - tile * a.R16 + rr, top = min(a.R16, R - tile * a.R16) - 1;
     constexpr int kFly = Per > 1 ? 3 : 5;
     for (int c = c0 + grp; c <= c1; c += kFly * GR) {
@@ -262,10 +308,13 @@ static cudaError_t launch_join(const Kv8AttnArgs& a, int R, int num_sms, cudaStr
                     dim3(unsigned(threads)), 0, st, a);
   };
   const int64_t segs = int64_t(a.N) * a.Hkv;
-  if (segs * cdiv(R, 4) <= num_sms) return go(kv8_join_kernel<D, 4, 1, 4>, 4, D * 4);
-  if (segs * cdiv(R, 8) <= num_sms) return go(kv8_join_kernel<D, 8, 1, 2>, 8, D * 4);
-  if (R <= 8) return go(kv8_join_kernel<D, 8, 1, 1>, 8, D * 2);
-  return go(kv8_join_kernel<D, 16, 2, 1>, 16, D * 2);
+  if (!a.bk || a.B <= kOwnFew) {
+    if (segs * cdiv(R, 4) <= num_sms) return go(kv8_join_kernel<D, 4, 1, 4, false>, 4, D * 4);
+    return go(kv8_join_kernel<D, 8, 1, 1, false>, 8, D * 2);
+  }
+  if (segs * cdiv(R, 4) <= num_sms) return go(kv8_join_kernel<D, 4, 1, 4, true>, 4, D * 4);
+  if (segs * cdiv(R, 8) <= num_sms) return go(kv8_join_kernel<D, 8, 1, 2, true>, 8, D * 4);
+  return go(kv8_join_kernel<D, 16, 2, 1, true>, 16, D * 2);
 }
 
 // Workspace: error word, then (m, l) and O of every partial.
