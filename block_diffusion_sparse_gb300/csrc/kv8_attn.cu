@@ -9,6 +9,8 @@
 
 namespace herald {
 
+// What a piece costs beside its tiles, in tiles (kv4_units).
+constexpr int kKv8PadRows = 3, kKv8PadTc = 9;
 constexpr int kKv8MaxCtas = 304;  // most attention CTAs (workspace slots)
 
 HERALD_DEV void join_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -349,7 +351,7 @@ cudaError_t launch_kv8_attn(const herald_dims& dm, const uint16_t* q, const Kv8D
   a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max, a.R16 = w.R16, a.row_tiles = w.row_tiles;
   a.c = c;
   a.ctas = std::min(kKv8MaxCtas, num_sms);
-  a.pad = 0;
+  a.pad = R <= kKv8FewRows ? kKv8PadRows : kKv8PadTc;
   uint32_t* err = reinterpret_cast<uint32_t*>(p);
   if (R <= kKv8FewRows)
     HERALD_CHECK_LAUNCH(launch_kv8_rows(dm.d, R, a, kmap, vmap, err, st));
