@@ -18,8 +18,8 @@
 //              base m, sum l and O, added up at a piece's end
 //   warps 8-11 turn V tiles into fp16
 //   warp 12    copies K and V tiles by TMA, looks up pages and scales four tiles ahead
-//   warp 13    issues S, in steps of 64 keys, the streams' in turn
-//   warps 14, 15  issue P V, one per stream
+//   warps 13, 14  issue S, one per stream, in steps of 64 keys
+//   warp 15    issues P V, the streams' in turn
 // Tensor memory holds, for each stream, one step's scores (64 columns), its P (32) and O
 // (128), and Q (64): 512.  A step's scores are in registers before anything is done
 // with them, so the next step's product runs beside its softmax.  (With P over the
@@ -153,11 +153,11 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
   uint8_t* base = align1024(smem_raw);
   const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_free[i], 1);
+    for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_free[i], 2);
     for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_free[i], 4);
     for (int i = 0; i < kKv8Metas; ++i) mbar_init(&meta_full[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 2), mbar_init(&o_done[i], 1),
+      mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 1), mbar_init(&o_done[i], 1),
           mbar_init(&s_full[i], 1), mbar_init(&s_read[i], 4), mbar_init(&p_full[i], 4);
     for (int i = 0; i < 3; ++i) mbar_init(&all_done[i], 1);
     mbar_init(&q_full, 8);
@@ -577,10 +577,11 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         mbar_wait(&k_full[i % KS], (i / KS) & 1);
       for (uint32_t i = v_issued > uint32_t(VS) ? v_issued - VS : 0; i < v_issued; ++i)
         mbar_wait(&v_full[i % VS], (i / VS) & 1);
-    } else if (warp == 13) {
-      // ---------------------------------------------------------- S issuer
-      // (the whole warp walks the loops, lane 0 issues)
-      const uint64_t kd = make_sdesc_rows<D>(smem_u32(base));
+    } else if (warp < 15) {
+      // --------------------------------------------------------- S issuers
+      // (the whole warp walks the loops, an elected lane issues)
+      const uint32_t w = uint32_t(warp - 13);
+      const uint64_t kd = make_sdesc_rows<D>(smem_u32(base) + w * (64u * D));
       constexpr uint32_t ids = make_idesc_e4m3(128, 64, false, false);
       uint32_t t = 0, np = 0;
       kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
@@ -589,35 +590,30 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         for (int u = u0; u < u1; ++u, ++t) {
           const uint32_t st = t % KS;
           if (!wait(&k_full[st], (t / KS) & 1, X8_K_FULL)) return false;
-#pragma unroll 1
-          for (uint32_t w = 0; w < 2; ++w) {
-            // the stream's scores of the step before have been read
-            if (t > 0 && !wait(&s_read[w], (t - 1) & 1, X8_S_READ)) return false;
-            tc_fence_after();
-            if (elect_one()) {
+          // the stream's scores of the step before have been read
+          if (t > 0 && !wait(&s_read[w], (t - 1) & 1, X8_S_READ)) return false;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-              for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
-                for (int ks = 0; ks < D / 32; ++ks)
-                  umma_e4m3_ts(tm + w * 64u, tm + (part ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(ks) * 8u,
-                               kd + ((st * S::kTile + w * (64u * D) + uint32_t(ks) * 32u) >> 4), ids,
-                               part + ks > 0);
-              umma_commit(&s_full[w]);
-              if (w == 1) umma_commit(&k_free[st]);
-            }
-            __syncwarp();
+              for (int ks = 0; ks < D / 32; ++ks)
+                umma_e4m3_ts(tm + w * 64u, tm + (part ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(ks) * 8u,
+                             kd + ((st * S::kTile + uint32_t(ks) * 32u) >> 4), ids, part + ks > 0);
+            umma_commit(&s_full[w]);
+            umma_commit(&k_free[st]);
           }
+          __syncwarp();
         }
         return true;
       });
       // every product and commit is done before the tensor memory is given back
       if (t > 0 && elect_one()) {
-        umma_commit(&all_done[0]);
-        mbar_wait(&all_done[0], 0);
+        umma_commit(&all_done[w]);
+        mbar_wait(&all_done[w], 0);
       }
     } else {
-      // ------------------------------------------------------- P V issuers
-      const uint32_t w = uint32_t(warp - 14);
+      // -------------------------------------------------------- P V issuer
       const uint64_t vd = make_sdesc_sw128(smem_u32(base) + S::kV16, 16384u, 1024);
       constexpr uint32_t ido = make_idesc_half(128, D, true);
       uint32_t t = 0;
@@ -625,24 +621,27 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         for (int u = u0; u < u1; ++u, ++t) {
           const uint32_t vb = t & 1;
           if (!wait(&v16_full[vb], (t >> 1) & 1, X8_V16_FULL)) return false;
-          if (!wait(&p_full[w], t & 1, X8_P_FULL)) return false;
-          tc_fence_after();
-          if (elect_one()) {
+#pragma unroll 1
+          for (uint32_t w = 0; w < 2; ++w) {
+            if (!wait(&p_full[w], t & 1, X8_P_FULL)) return false;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_bf16_ts(tm + kKv8TmO + w * 128u, tm + kKv8TmP + w * 32u + uint32_t(ks) * 8u,
-                           vd + ((vb * S::kTile16 + w * 8192u) >> 4) + uint32_t(ks) * 128u, ido,
-                           u > u0 || ks > 0);
-            umma_commit(&o_done[w]);
-            umma_commit(&v16_free[vb]);
+              for (int ks = 0; ks < 4; ++ks)
+                umma_bf16_ts(tm + kKv8TmO + w * 128u, tm + kKv8TmP + w * 32u + uint32_t(ks) * 8u,
+                             vd + ((vb * S::kTile16 + w * 8192u) >> 4) + uint32_t(ks) * 128u, ido,
+                             u > u0 || ks > 0);
+              umma_commit(&o_done[w]);
+              if (w == 1) umma_commit(&v16_free[vb]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
         return true;
       });
       if (t > 0 && elect_one()) {
-        umma_commit(&all_done[1 + w]);
-        mbar_wait(&all_done[1 + w], 0);
+        umma_commit(&all_done[2]);
+        mbar_wait(&all_done[2], 0);
       }
     }
     __syncwarp();
