@@ -211,14 +211,15 @@ HERALD_DEV Kv4Split kv4_split(int per_head, int Hkv, int ctas) {
 struct Kv4Share {
   int at, end, n, first;
 };
-HERALD_DEV Kv4Share kv4_share(const int32_t* ctx, int N, int L_max, int Hkv, int ctas, int pad,
-                              int blk_units, int cta) {
+HERALD_DEV Kv4Share kv4_share(const Kv4AttnArgs& a, int blk_units, int cta) {
+  const int32_t* ctx = a.ctx;
+  const int N = a.N, L_max = a.L_max, Hkv = a.Hkv, pad = a.pad;
   const int lane = threadIdx.x & 31;
   // (the lengths of the first 32 sequences are loaded once)
   const int own0 = lane < N ? kv4_units(ctx[lane], L_max, blk_units, pad) : 0;
   int sum = own0;
   for (int n = lane + 32; n < N; n += 32) sum += kv4_units(ctx[n], L_max, blk_units, pad);
-  const Kv4Split split = kv4_split(int(__reduce_add_sync(0xffffffffu, sum)), Hkv, ctas);
+  const Kv4Split split = kv4_split(int(__reduce_add_sync(0xffffffffu, sum)), Hkv, a.ctas);
   Kv4Share r;
   r.at = warp_same(cta * split.share);
   r.end = warp_same(min(r.at + split.share, split.total));
@@ -244,9 +245,6 @@ HERALD_DEV Kv4Share kv4_share(const int32_t* ctx, int N, int L_max, int Hkv, int
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
   return r;
-}
-HERALD_DEV Kv4Share kv4_share(const Kv4AttnArgs& a, int blk_units, int cta) {
-  return kv4_share(a.ctx, a.N, a.L_max, a.Hkv, a.ctas, a.pad, blk_units, cta);
 }
 
 }  // namespace herald

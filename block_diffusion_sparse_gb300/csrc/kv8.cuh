@@ -108,19 +108,61 @@ cudaError_t launch_kv8_rows(int d, int rows, const Kv8AttnArgs& a, const CUtenso
 cudaError_t launch_kv8_attn_tc(int d, const Kv8AttnArgs& a, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, uint32_t* err, cudaStream_t st);
 
+// A CTA's share of the tiles of 128 keys, as kv4_share's (kv4.cuh) with the segments of
+// heads * row tiles per sequence and no units for block keys: units [at, end); with at <
+// end, n is the sequence that holds unit `at`, first the first unit of its first
+// segment and ctx its length (a load that every role would wait for again).
+struct Kv8Share {
+  int at, end, n, first, ctx;
+};
+HERALD_DEV Kv8Share kv8_share(const Kv8AttnArgs& a, int cta) {
+  const int lane = threadIdx.x & 31, heads = a.Hkv * a.row_tiles;
+  auto length = [&](int n) { return n < a.N ? min(max(a.ctx[n], 0), a.L_max) : 0; };
+  const int ctx0 = length(lane);  // (the lengths of the first 32 sequences are loaded once)
+  int sum = kv4_units(ctx0, a.L_max, 0, a.pad);
+  for (int n = lane + 32; n < a.N; n += 32) sum += kv4_units(length(n), a.L_max, 0, a.pad);
+  const Kv4Split split = kv4_split(int(__reduce_add_sync(0xffffffffu, sum)), heads, a.ctas);
+  Kv8Share r;
+  r.at = warp_same(cta * split.share);
+  r.end = warp_same(min(r.at + split.share, split.total));
+  r.n = r.first = r.ctx = 0;
+  if (r.at >= r.end) return r;
+  int base = 0;
+  for (int n0 = 0; n0 < a.N; n0 += 32) {
+    const int ctx = n0 == 0 ? ctx0 : length(n0 + lane);
+    const int own = heads * kv4_units(ctx, a.L_max, 0, a.pad);
+    int inc = own;  // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > r.at);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      r.n = warp_same(n0 + l);
+      r.first = base + __shfl_sync(0xffffffffu, inc - own, l);
+      r.ctx = __shfl_sync(0xffffffffu, ctx, l);
+      return r;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return r;
+}
+
 // The pieces of a CTA's share, in order: body(n, gt, seg, ctx, u0, u1) with gt = g *
 // row_tiles + row tile, seg = n * Hkv * row_tiles + gt, tiles u0 <= u < u1 of 128 cache
 // positions; it returns false to leave.
 template <typename Body>
-HERALD_DEV void kv8_pieces(const Kv8AttnArgs& a, const Kv4Share& sh, Body&& body) {
+HERALD_DEV void kv8_pieces(const Kv8AttnArgs& a, const Kv8Share& sh, Body&& body) {
   const int heads = a.Hkv * a.row_tiles;
-  int at = sh.at, first = sh.first, n = sh.n;
+  int at = sh.at, first = sh.first, n = sh.n, ctx = sh.ctx;
   while (at < sh.end) {
-    const int ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
     const int units = kv4_units(ctx, a.L_max, 0, a.pad);
     if (units == 0 || at >= first + heads * units) {  // the next sequence
       first += heads * units;
       ++n;
+      ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
       continue;
     }
     const int gt = (at - first) / units;

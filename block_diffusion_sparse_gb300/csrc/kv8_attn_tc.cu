@@ -109,6 +109,23 @@ HERALD_DEV void tmem_ld_done(uint32_t (&r)[32]) {
                :
                : "memory");
 }
+HERALD_DEV void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+HERALD_DEV void tmem_ld16_done(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                 "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 HERALD_DEV void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
@@ -148,8 +165,10 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
   __shared__ uint64_t k_full[KS], k_free[KS], v_full[VS], v_free[VS], v16_full[2], v16_free[2],
       meta_full[kKv8Metas], q_full, s_full[2], s_read[2], p_full[2], o_done[2], all_done[3];
   __shared__ uint32_t tmem_base, failed;
+  __shared__ Kv8Share share;
   __shared__ __align__(16) Kv8TileMeta meta[kKv8Metas];
   __shared__ float2 row_ml[2][128];  // a piece's (m, l) of both streams
+  __shared__ float row_f[128];       // score factors of its rows
   uint8_t* base = align1024(smem_raw);
   const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -169,13 +188,19 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
   const uint32_t tm = tmem_base;
   griddep_enter();
   const Kv4Wait wait{&failed};
-  const int G = a.Hq / a.Hkv, R = a.B * G;
-  const Kv4Share sh = kv4_share(a.ctx, a.N, a.L_max, a.Hkv * a.row_tiles, a.ctas, a.pad, 0,
-                                int(blockIdx.x));
+  // (through shared memory: values that all roles hold from here on would be spilled for
+  // the role with the fewest registers)
+  if (warp == 0) {
+    const Kv8Share mine = kv8_share(a, int(blockIdx.x));
+    if (lane == 0) share = mine;
+  }
+  __syncthreads();
 
-  // registers: 512 threads launch with 128 each (65,536) = 256 x (184 + 72)
+  // registers: 512 threads launch with 128 each (65,536) = 128 x (2 x 200 + 64 + 48).  Each
+  // role's branch begins with its own setmaxnreg, so that the compiler knows the limit
+  // of the code that follows.
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ------------------------------------------------------------ softmax
     // (after a failed wait these warps go on without waiting: the barriers among them
     // stay in step, the results are worthless and the error is recorded)
@@ -194,37 +219,43 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     const uint32_t ts = tm + lanes + uint32_t(w) * 64u, tp = tm + lanes + kKv8TmP + uint32_t(w) * 32u;
     const uint32_t to = tm + lanes + kKv8TmO + uint32_t(w) * 128u, to2 = to ^ 128u;  // O, the other's
     uint8_t* xb = base + S::kX + warp * 2048;
+    const int G = a.Hq / a.Hkv, R = a.B * G;
     const int per_g = 65536 / G + 1;  // r / G = r per_g / 2^16 for the rows r < 256
     uint32_t t = 0;
-    kv8_pieces(a, sh, [&](int n, int gt, int seg, int ctx, int u0, int u1) -> bool {
+    kv8_pieces(a, share, [&](int n, int gt, int seg, int ctx, int u0, int u1) -> bool {
       debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
       const int g = gt / a.row_tiles, r0 = (gt - g * a.row_tiles) * 128;
       const bool idle = r0 + (warp & 3) * 32 >= R;  // the warp has no rows
       const int row = r0 + lrow;
-      // queries: D/8 lanes load a row, as e4m3 it goes through shared memory to the lane
-      // that has it in tensor memory, 16 rows at a time; the first half of the warps stores
-      // q0, the other q1.  (A lane loading its row by itself touched 32 lines an
-      // instruction: 6 us until the first scores.)  The scores of the piece before have
-      // been read: nothing reads Q now.
-      float f = 0.f;
-      if (!idle) {
-        constexpr int LPR = D / 8, RPP = 32 / LPR, P = 32 / RPP, W = D / 4;
-        const int c = lane % LPR, sub = lane / LPR;
-        const uint16_t* q0 = a.q + (size_t(n) * a.B * a.Hq + g * G) * D + c * 8;
-        uint32_t o[W];  // this lane's row
-        // (in turns of 16 rows: the code of a start comes from far, and is kept short)
+      // queries: of a quarter's 32 rows each stream's warp turns 16 into q0 and q1, D/8
+      // lanes a row and 8 rows at a time, and through shared memory the first stream's
+      // lanes take q0 of their rows, the other's q1.  (A lane loading its row by itself
+      // touched 32 lines an instruction: 6 us until the first scores.)  The scores of the
+      // piece before have been read: nothing reads Q now.
+      constexpr int LPR = D / 8, RPP = 32 / LPR, P = 8 / RPP, W = D / 4;
+      const int c = lane % LPR, sub = lane / LPR, q_row = r0 + (warp & 3) * 32 + w * 16 + sub;
+      const uint16_t* q0 = a.q + (size_t(n) * a.B * a.Hq + g * G) * D + c * 8;
+      uint4 next[P];
+      auto load_q = [&](int h) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int r = min(q_row + h * 8 + p * RPP, R - 1), tok = r * per_g >> 16;  // r / G
+          next[p] = *reinterpret_cast<const uint4*>(q0 + (r + tok * (a.Hq - G)) * D);
+        }
+      };
+      if (!idle) load_q(0);
+      uint32_t o[W];  // this lane's row of q0 or q1
+      // (a loop kept rolled: unrolled it crowds the registers of the whole role)
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint4 x[P / 2];
+      for (int h = 0; h < 2; ++h) {
+        if (!idle) {
+          uint4 x[P];
 #pragma unroll
-          for (int p = 0; p < P / 2; ++p) {
-            const int r = min(r0 + (warp & 3) * 32 + h * 16 + p * RPP + sub, R - 1);
-            const int tok = r * per_g >> 16;  // r / G
-            x[p] = *reinterpret_cast<const uint4*>(q0 + (r + tok * (a.Hq - G)) * D);
-          }
-          float mx[P / 2];  // (the rows' maxima side by side: their steps wait on one another)
+          for (int p = 0; p < P; ++p) x[p] = next[p];
+          if (h == 0) load_q(1);
+          float mx[P];  // (the rows' maxima side by side: their steps wait on one another)
 #pragma unroll
-          for (int p = 0; p < P / 2; ++p) {
+          for (int p = 0; p < P; ++p) {
             const uint32_t m4 = max_bf16x2_abs(
                 max_bf16x2_abs(max_bf16x2_abs(max_bf16x2_abs(0, x[p].x), x[p].y), x[p].z), x[p].w);
             mx[p] = fmaxf(bf16lo(m4), bf16hi(m4));
@@ -232,39 +263,42 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
 #pragma unroll
           for (int i = 1; i < LPR; i <<= 1)
 #pragma unroll
-            for (int p = 0; p < P / 2; ++p)
+            for (int p = 0; p < P; ++p)
               mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], i));
 #pragma unroll
-          for (int p = 0; p < P / 2; ++p) {
+          for (int p = 0; p < P; ++p) {
             float up, fp;
             kv8_query_scale(mx[p], a.scale, &up, &fp);
-            fp = __shfl_sync(0xffffffffu, fp, lane % RPP * LPR);
-            if (lane / RPP == h * (P / 2) + p) f = fp;
             const uint32_t wd[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-            uint32_t v[4];
+            uint32_t v0[4], v1[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t h2 = pack_half2(bf16lo(wd[i]) * up, bf16hi(wd[i]) * up);
-              v[i] = half2_to_e4m3(h2);
-              const uint32_t rest = half2_to_e4m3(hsub2(h2, e4m3x2_to_half2(v[i])));  // what q0 left
-              v[i] = w ? rest : v[i];
+              v0[i] = half2_to_e4m3(h2);
+              v1[i] = half2_to_e4m3(hsub2(h2, e4m3x2_to_half2(v0[i])));  // what q0 left
             }
             const uint32_t r = uint32_t(p * RPP + sub);
-            *reinterpret_cast<uint2*>(xb + r * D + ((uint32_t(c >> 1) ^ (r & (D / 16 - 1))) << 4) +
-                                      (c & 1) * 8) = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+            uint8_t* dst = xb + r * D + ((uint32_t(c >> 1) ^ (r & (D / 16 - 1))) << 4) + (c & 1) * 8;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(v0[0] | v0[1] << 16, v0[2] | v0[3] << 16);
+            *reinterpret_cast<uint2*>(dst + 8 * D) = make_uint2(v1[0] | v1[1] << 16, v1[2] | v1[3] << 16);
+            if (c == 0) row_f[(warp & 3) * 32 + w * 16 + h * 8 + int(r)] = fp;
           }
-          __syncwarp();
-          if (lane >> 4 == h) {
-            const uint32_t r = uint32_t(lane) & 15u;
-#pragma unroll
-            for (int i = 0; i < W / 4; ++i) {
-              const uint4 y = *reinterpret_cast<const uint4*>(
-                  xb + r * D + ((uint32_t(i) ^ (r & (D / 16 - 1))) << 4));
-              o[4 * i] = y.x, o[4 * i + 1] = y.y, o[4 * i + 2] = y.z, o[4 * i + 3] = y.w;
-            }
-          }
-          __syncwarp();
         }
+        tc_bar();
+        if (!idle && (lane >> 3 & 1) == h) {
+          const uint32_t r = uint32_t(lane) & 7u;
+          const uint8_t* src = base + S::kX + ((lane >> 4) * 4 + (warp & 3)) * 2048 + w * (8 * D) + r * D;
+#pragma unroll
+          for (int i = 0; i < W / 4; ++i) {
+            const uint4 y = *reinterpret_cast<const uint4*>(src + ((uint32_t(i) ^ (r & (D / 16 - 1))) << 4));
+            o[4 * i] = y.x, o[4 * i + 1] = y.y, o[4 * i + 2] = y.z, o[4 * i + 3] = y.w;
+          }
+        }
+        tc_bar();
+      }
+      float f = 0.f;
+      if (!idle) {
+        f = row_f[lrow];
 #pragma unroll
         for (int i = 0; i < W; i += 8)
           tmem_st8(tm + lanes + (w ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(i),
@@ -406,44 +440,40 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         // 16 channels at a time through shared memory, so that a row's 64 bytes are written
         // by neighbouring lanes (a lane writing its own row took 2.8 us a piece)
 #pragma unroll 1
-        for (uint32_t c = 0; c < D / 2; c += 32) {
-          uint32_t o[32], p[32];
-          tmem_ld32_async(to + uint32_t(w) * (D / 2) + c, o);
-          tmem_ld32_async(to2 + uint32_t(w) * (D / 2) + c, p);
-          tmem_ld_done(o);
-          tmem_ld_done(p);
-          float v[32];
+        for (uint32_t c = 0; c < D / 2; c += 16) {
+          uint32_t v[16], p[16];
+          tmem_ld16_async(to + uint32_t(w) * (D / 2) + c, v);
+          tmem_ld16_async(to2 + uint32_t(w) * (D / 2) + c, p);
+          tmem_ld16_done(v);
+          tmem_ld16_done(p);
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            v[i] = fmaf(__uint_as_float(p[i]), w1, __uint_as_float(o[i]) * w0);
+          for (int i = 0; i < 4; ++i) {
+            float4 y;
+            y.x = fmaf(__uint_as_float(p[4 * i]), w1, __uint_as_float(v[4 * i]) * w0);
+            y.y = fmaf(__uint_as_float(p[4 * i + 1]), w1, __uint_as_float(v[4 * i + 1]) * w0);
+            y.z = fmaf(__uint_as_float(p[4 * i + 2]), w1, __uint_as_float(v[4 * i + 2]) * w0);
+            y.w = fmaf(__uint_as_float(p[4 * i + 3]), w1, __uint_as_float(v[4 * i + 3]) * w0);
+            *reinterpret_cast<float4*>(xb + rows_off<64>(uint32_t(lane), uint32_t(i))) = y;
+          }
+          __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4*>(xb + rows_off<64>(uint32_t(lane), uint32_t(i))) =
-                  make_float4(v[16 * e + 4 * i], v[16 * e + 4 * i + 1], v[16 * e + 4 * i + 2],
-                              v[16 * e + 4 * i + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = i * 8 + (lane >> 2), lr = (warp & 3) * 32 + r;
-              if (r0 + lr < R)
-                *reinterpret_cast<float4*>(a.opart + (slot * a.R16 + lr) * D + w * (D / 2) + c + 16 * e +
-                                           (lane & 3) * 4) =
-                    *reinterpret_cast<const float4*>(xb + rows_off<64>(uint32_t(r), uint32_t(lane & 3)));
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), lr = (warp & 3) * 32 + r;
+            if (r0 + lr < R)
+              *reinterpret_cast<float4*>(a.opart + (slot * a.R16 + lr) * D + w * (D / 2) + c +
+                                         (lane & 3) * 4) =
+                  *reinterpret_cast<const float4*>(xb + rows_off<64>(uint32_t(r), uint32_t(lane & 3)));
           }
         }
-        __syncwarp();
       }
       tc_fence_before();
       tc_bar();  // (O and row_ml have been read: the next piece may begin)
       return true;
     });
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp < 12) {
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    {
       // ------------------------------------------------- values to fp16
       // A lane turns chunks of 16 channels, one of which becomes two: eight (d = 64: four)
       // neighbouring lanes read eight chunks of one row (two rows).  With d = 128 the lanes
@@ -466,7 +496,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         to[i] = uint32_t(D == 128 ? c >> 2 : 0) * 16384u + sw128_off(r, uint32_t(c & 3) * 2u);
       }
       uint32_t t = 0;
-      kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
+      kv8_pieces(a, share, [&](int, int, int, int, int u0, int u1) -> bool {
         for (int u = u0; u < u1; ++u, ++t) {
           const uint32_t st = t % VS, b = t & 1;
           const Kv8TileMeta& mt = meta[t % kKv8Metas];
@@ -503,12 +533,15 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         }
         return true;
       });
-    } else if (warp == 12) {
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 12) {
       // ------------------------------------------------------------ copies
       const int page = 1 << a.c.page_log2;
       const int ti = lane >> 3, gr = (lane & 7) * 16;  // this lane's tile of four, its 16 keys
       uint32_t t = 0, k_issued = 0, v_issued = 0;
-      kv8_pieces(a, sh, [&](int n, int gt, int, int ctx, int u0, int u1) -> bool {
+      kv8_pieces(a, share, [&](int n, int gt, int, int ctx, int u0, int u1) -> bool {
         const int g = gt / a.row_tiles;
         const int32_t* table = a.c.table + size_t(n) * a.c.max_pages;
         const int stop = min(ctx, u1 * 128);
@@ -584,7 +617,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       const uint64_t kd = make_sdesc_rows<D>(smem_u32(base) + w * (64u * D));
       constexpr uint32_t ids = make_idesc_e4m3(128, 64, false, false);
       uint32_t t = 0, np = 0;
-      kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
+      kv8_pieces(a, share, [&](int, int, int, int, int u0, int u1) -> bool {
         if (!wait(&q_full, np & 1, X8_Q_FULL)) return false;
         ++np;
         for (int u = u0; u < u1; ++u, ++t) {
@@ -617,7 +650,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       const uint64_t vd = make_sdesc_sw128(smem_u32(base) + S::kV16, 16384u, 1024);
       constexpr uint32_t ido = make_idesc_half(128, D, true);
       uint32_t t = 0;
-      kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
+      kv8_pieces(a, share, [&](int, int, int, int, int u0, int u1) -> bool {
         for (int u = u0; u < u1; ++u, ++t) {
           const uint32_t vb = t & 1;
           if (!wait(&v16_full[vb], (t >> 1) & 1, X8_V16_FULL)) return false;

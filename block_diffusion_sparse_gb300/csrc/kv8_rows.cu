@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
   griddep_enter();
   const Kv4Wait wait{&failed};
   const int G = a.Hq / a.Hkv, R = a.B * G;
-  const Kv4Share sh = kv4_share(a.ctx, a.N, a.L_max, a.Hkv, a.ctas, a.pad, 0, int(blockIdx.x));
+  const Kv8Share sh = kv8_share(a, int(blockIdx.x));
 
   if (warp < 4) {
     // ------------------------------------------------------------ softmax
