@@ -12,9 +12,10 @@
 // of 4 bits in columns of their own:
 //   q = (q0 + q1/16) 2^x: a bf16 has 8 bits; x brings the row's largest to [2^7, 2^8)
 //   p = p0 + p1/16 + p2/256 + p3/4096 (kKv8Parts), with p at most 2^8
-// and the columns are added in fp32 afterwards.  A key's scale (its block's) multiplies
-// its scores; a value's multiplies its weight before that is split, over the largest
-// such scale so far (the exponent mv).
+// and the columns are added in fp32 afterwards.  A key's scale (its block's) multiplies its
+// scores.  A value's exponent e_v goes into the weight's own, p = 2^(x + e_v - m), and
+// out of the row's sum again, l += p 2^-e_v: O has one unit, and weights keep their bits
+// whatever their values' scales.
 //
 // One CTA per SM walks its share of the keys (kv4_split):
 //   warps 0-3  softmax, a thread per key of the tile (its TMEM lane), rows in registers;
@@ -23,9 +24,9 @@
 //   warp 5     copies tiles into a ring and looks up pages and scales, four tiles of
 //              page table and scales (32 lanes: 8 groups of 16 keys each) ahead
 //   warp 6     stages the queries of the next piece
-// A row's exponent base m stays while no score exceeds it by 2^kAbove; all four warps
-// vote on that in one barrier a tile.  Else the tile's row maxima are exchanged, O is
-// scaled once the products before it are done, and l follows.
+// A row's exponent base m is set 4 below its largest exponent and stays while no p passes
+// 2^8; all four warps vote on that in one barrier a tile.  Else the tile's row maxima are
+// exchanged, O is scaled once the products before it are done, and l follows.
 #include <float.h>
 
 #include "kv8.cuh"
@@ -34,9 +35,8 @@
 namespace herald {
 
 constexpr int kKv8Parts = 4;               // e4m3 numbers of a weight
-constexpr float kKv8Above = 4.f;           // log2: how far scores may rise over the base
+constexpr float kKv8At = 4.f, kKv8Most = 8.f;  // log2 p of a new base's row, and the largest
 constexpr int kKv8RowsThreads = 224;       // 7 warps
-constexpr int kKv8NoScale = -64;           // below every scale's exponent
 
 // Waits of the kernel (bits 16-31 of the error word).
 enum : uint32_t {
@@ -56,10 +56,10 @@ struct Kv8Rows {
   static constexpr uint32_t kCols = RP == 8 ? 64 : RP == 16 ? 128 : 256;  // 2 S + O
 };
 
-// What the softmax needs of 16 keys: scale exponents and how many of them count.
-struct Kv8Meta {
-  int8_t ek, ev;
-  uint8_t keys, pad;
+// What the softmax needs of 16 keys: 2^e_k, e_v, 2^-e_v and how many of them count.
+struct __align__(16) Kv8Meta {
+  float sk, ev, iv;
+  int keys;
 };
 
 // x -> 16 (x - e4m3(x)) for a pair, returning the codes: what the next number holds.
@@ -105,10 +105,10 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
   __shared__ uint64_t full[ST], empty[ST], q_full[2], q_free[2], s_full[2], p_full[2], pv_done[2],
       all_done;
   __shared__ uint32_t tmem_base, failed;
+  __shared__ Kv8Share share;
   __shared__ Kv8Meta meta[ST][8];
   __shared__ __align__(16) float row_f[2][RP];  // score factors of the rows
   __shared__ float red[4][RP];
-  __shared__ int red_e[4];
   uint8_t* base = align1024(smem_raw);
   uint8_t *Qs = base + ST * S::kStage, *Ps = Qs + 2 * S::kQ;
   const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
@@ -127,7 +127,11 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
   griddep_enter();
   const Kv4Wait wait{&failed};
   const int G = a.Hq / a.Hkv, R = a.B * G;
-  const Kv8Share sh = kv8_share(a, int(blockIdx.x));
+  if (warp == 0) {
+    const Kv8Share mine = kv8_share(a, int(blockIdx.x));
+    if (lane == 0) share = mine;
+  }
+  __syncthreads();
 
   if (warp < 4) {
     // ------------------------------------------------------------ softmax
@@ -140,22 +144,26 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
     const int key = int(threadIdx.x);
     const uint32_t lanes = uint32_t(warp * 32) << 16;
     uint32_t t = 0, np = 0;  // tiles and pieces of the CTA
-    kv8_pieces(a, sh, [&](int n, int, int seg, int ctx, int u0, int u1) -> bool {
+    kv8_pieces(a, share, [&](int n, int, int seg, int ctx, int u0, int u1) -> bool {
       debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
       const uint32_t qb = np & 1;
       await(&q_full[qb], (np >> 1) & 1, W8_Q_FULL);
-      float f[RP], m[RP], l[RP];
+      constexpr bool kKeepF = RP < 32;  // (32 factors in registers would spill)
+      float f[kKeepF ? RP : 1] = {}, m[RP], l[RP];
+      if constexpr (kKeepF) {
 #pragma unroll
-      for (int r = 0; r < RP; r += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(&row_f[qb][r]);
-        f[r] = x.x, f[r + 1] = x.y, f[r + 2] = x.z, f[r + 3] = x.w;
+        for (int r = 0; r < RP; r += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(&row_f[qb][r]);
+          f[r] = x.x, f[r + 1] = x.y, f[r + 2] = x.z, f[r + 3] = x.w;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_free[qb]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_free[qb]);
+      auto factor = [&](int r) { return kKeepF ? f[kKeepF ? r : 0] : *(volatile float*)&row_f[qb][r]; };
       ++np;
 #pragma unroll
       for (int r = 0; r < RP; ++r) m[r] = -FLT_MAX, l[r] = 0.f;
-      int mv = kKv8NoScale;
+#pragma unroll 1
       for (int u = u0; u < u1; ++u, ++t) {
         const uint32_t b = t & 1, st = t % ST;
         await(&full[st], (t / ST) & 1, W8_STAGE_FULL);  // (the meta data and V are here)
@@ -163,47 +171,40 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         tc_fence_after();
         const Kv8Meta mt = meta[st][key >> 4];
         const bool on = (key & 15) < mt.keys;
-        const float ek = exp2_int(mt.ek);
-        const int ev = on ? mt.ev : kKv8NoScale;
-        float s[RP];
+        float s[RP], p[RP];
         {
           float x[NS];
           tmem_load<NS>(tm + lanes + b * NS, x);
 #pragma unroll
           for (int r = 0; r < RP; ++r) s[r] = fmaf(x[RP + r], 0.0625f, x[r]);
         }
-        bool move = ev > mv;
-        float p[RP];
+        bool move = false;
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          p[r] = on ? fmaf(s[r], f[r] * ek, -m[r]) : -INFINITY;
-          move |= p[r] > kKv8Above;
+          p[r] = on ? fmaf(s[r], factor(r) * mt.sk, mt.ev - m[r]) : -INFINITY;
+          move |= p[r] > kKv8Most;
         }
         if (soft_any(move)) {
-          // row maxima of the tile, products rounded down: where scores are so large that
-          // fp32's steps are no longer small, a base above them all would leave no weight
+          // row maxima of the tile, rounded down: where scores are so large that fp32's
+          // steps are no longer small, a base above them all would leave no weight
 #pragma unroll
           for (int r = 0; r < RP; ++r) {
-            const float mx = warp_max(on ? __fmul_rd(s[r], f[r] * ek) : -INFINITY);
+            const float z = __fadd_rd(__fmul_rd(s[r], factor(r) * mt.sk), mt.ev);
+            const float mx = warp_max(on ? z : -INFINITY);
             if (lane == 0) red[warp][r] = mx;
           }
-          const int me = __reduce_max_sync(0xffffffffu, ev);
-          if (lane == 0) red_e[warp] = me;
           soft_bar();
-          const int mv1 = max(max(max(red_e[0], red_e[1]), max(red_e[2], red_e[3])), mv);
-          const float ks = exp2_int(max(mv - mv1, -126));
           float k[RP];
 #pragma unroll
           for (int r = 0; r < RP; ++r) {
-            const float m1 = fmaxf(fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r])), m[r]);
+            const float z = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
+            const float m1 = fmaxf(__fadd_rd(z, -kKv8At), m[r]);
             k[r] = fast_exp2(m[r] - m1);
             m[r] = m1;
             l[r] *= k[r];
-            k[r] *= ks;
-            const float x = fmaf(s[r], f[r] * ek, -m1);
-            p[r] = !on ? -INFINITY : x > kKv8Above ? kKv8Above : x;  // (a NaN stays)
+            const float x = fmaf(s[r], factor(r) * mt.sk, mt.ev - m1);
+            p[r] = !on ? -INFINITY : x > kKv8Most ? kKv8Most : x;  // (a NaN stays)
           }
-          mv = mv1;
           if (u > u0) {  // O so far, once the products before this tile are in it
             await(&pv_done[b ^ 1], ((t - 1) >> 1) & 1, W8_PV_DONE);
             tc_fence_after();
@@ -219,12 +220,10 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
           }
           soft_bar();  // (the maxima have been read)
         }
-        const float w = on ? exp2_int(max(ev - mv, -120) + int(8.f - kKv8Above)) : 0.f;
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
           p[r] = fast_exp2(p[r]);
-          l[r] += p[r];
-          p[r] *= w;
+          l[r] = fmaf(p[r], mt.iv, l[r]);
         }
         // P of two tiles before has been read
         if (t >= 2) await(&pv_done[b], ((t >> 1) - 1) & 1, W8_PV_DONE);
@@ -248,6 +247,10 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         tc_fence_before();
         mbar_arrive(&p_full[b]);
       }
+      if constexpr (!kKeepF) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_free[qb]);
+      }
       // the piece's partials: O once the last product is done, l over all keys
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
@@ -265,7 +268,6 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
       // (with d = 64 an M = 64 product's rows lie in the first 16 lanes of each warp's 32)
       const int ch = D == 128 ? key : warp * 16 + lane;
       float* out = a.opart + slot * a.R16 * D + ch;
-      const float unit = exp2_int(max(mv, -32) + int(kKv8Above) - 8);
       float o[NO];
       tmem_load<NO>(to + lanes, o);
       if (D == 128 || lane < 16) {
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
           float x = o[(kKv8Parts - 1) * RP + r];
 #pragma unroll
           for (int i = kKv8Parts - 2; i >= 0; --i) x = fmaf(x, 0.0625f, o[i * RP + r]);
-          if (r < R) out[r * D] = x * unit;
+          if (r < R) out[r * D] = x;
         }
       }
       tc_fence_before();
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
       __syncwarp();
       return true;
     };
-    kv8_pieces(a, sh, [&](int, int, int, int, int u0, int u1) -> bool {
+    kv8_pieces(a, share, [&](int, int, int, int, int u0, int u1) -> bool {
       const uint32_t qb = np & 1;
       if (!wait(&q_full[qb], (np >> 1) & 1, W8_Q_FULL)) return false;
       for (int u = u0; u < u1; ++u, ++t) {
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
     const int page = 1 << a.c.page_log2;
     const int ti = lane >> 3, gr = (lane & 7) * 16;  // this lane's tile of four, its 16 keys
     uint32_t t = 0, issued = 0;
-    kv8_pieces(a, sh, [&](int n, int g, int, int ctx, int u0, int u1) -> bool {
+    kv8_pieces(a, share, [&](int n, int g, int, int ctx, int u0, int u1) -> bool {
       const int32_t* table = a.c.table + size_t(n) * a.c.max_pages;
       const int stop = min(ctx, u1 * 128);
       int pos = (u0 + ti) * 128 + gr;
@@ -365,8 +367,9 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
           const uint32_t x = (t + uint32_t(i)) % ST;
           if (ti == i) {
             Kv8Meta mt;
-            mt.ek = int8_t(kv8_exp(uint32_t(ek))), mt.ev = int8_t(kv8_exp(uint32_t(ev)));
-            mt.keys = uint8_t(have ? min(16, ctx - pos) : 0), mt.pad = 0;
+            const int e_k = kv8_exp(uint32_t(ek)), e_v = kv8_exp(uint32_t(ev));
+            mt.sk = exp2_int(e_k), mt.ev = float(e_v), mt.iv = exp2_int(-e_v);
+            mt.keys = have ? min(16, ctx - pos) : 0;
             meta[x][lane & 7] = mt;
           }
           __syncwarp();
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
     constexpr int LPR = D / 8, RPP = 32 / LPR, P = RP / RPP;
     const int c = lane % LPR, sub = lane / LPR;
     uint32_t np = 0;
-    kv8_pieces(a, sh, [&](int n, int g, int, int, int, int) -> bool {
+    kv8_pieces(a, share, [&](int n, int g, int, int, int, int) -> bool {
       const uint32_t qb = np & 1;
       uint4 x[P];
 #pragma unroll
