@@ -23,10 +23,13 @@ HERALD_DEV int kv8_page(const Kv8Dev& c, int n, int lp) {
 // Row index of position pos in page `phys` (64 bits: a long cache has more bytes
 // than 32 bits count), and the index of its scale.
 HERALD_DEV size_t kv8_row(const Kv8Dev& c, int phys, int Hkv, int g, int pos) {
-  return ((size_t(phys) * Hkv + g) << c.page_log2) + (pos & ((1 << c.page_log2) - 1));
+  return size_t(uint32_t(phys)) * uint32_t(Hkv << c.page_log2) +
+         uint32_t((g << c.page_log2) + (pos & ((1 << c.page_log2) - 1)));
 }
 HERALD_DEV size_t kv8_scale(const Kv8Dev& c, int phys, int Hkv, int g, int pos) {
-  return kv8_row(c, phys, Hkv, g, pos) >> c.block_log2;  // (pages hold whole blocks)
+  const int log2 = c.page_log2 - c.block_log2;  // (pages hold whole blocks)
+  return size_t(uint32_t(phys)) * uint32_t(Hkv << log2) +
+         uint32_t((g << log2) + ((pos & ((1 << c.page_log2) - 1)) >> c.block_log2));
 }
 // Exponent of a scale byte; bytes that no call writes count as the nearer end.
 HERALD_DEV int kv8_exp(uint32_t byte) {

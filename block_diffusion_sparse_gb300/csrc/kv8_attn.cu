@@ -10,7 +10,7 @@
 namespace herald {
 
 // What a piece costs beside its tiles, in tiles (kv4_units).
-constexpr int kKv8PadRows = 3, kKv8PadTc = 9;
+constexpr int kKv8PadRows = 3, kKv8PadTc = 7;
 constexpr int kKv8MaxCtas = 304;  // most attention CTAs (workspace slots)
 
 HERALD_DEV void join_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,

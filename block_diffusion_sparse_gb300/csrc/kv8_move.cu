@@ -262,11 +262,11 @@ HERALD_DEV void held8(const uint2& w, float s, float (&x)[8]) {
   uint32_t h[4];
   e4m3x4_to_half2(w.x, h[0], h[1]);
   e4m3x4_to_half2(w.y, h[2], h[3]);
+  const uint64_t s2 = f2_pack(s, s);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-    x[2 * j] = f.x * s;
-    x[2 * j + 1] = f.y * s;
+    f2_unpack(f2_mul(f2_pack(f.x, f.y), s2), x[2 * j], x[2 * j + 1]);
   }
 }
 
