@@ -41,9 +41,11 @@ namespace herald {
 
 constexpr int kKv8TcThreads = 512;  // 16 warps
 constexpr int kKv8KStages = 4, kKv8VStages = 4;
-// Tiles whose scales and counts are kept for the softmax: K copies run at most four
-// tiles ahead of the scores, and those one ahead of the softmax.
-constexpr int kKv8Metas = 16;
+// Scales and counts of tiles, published by groups of four (fewer at a piece's end) with a
+// barrier each.  The last copied tile t has S(t - 4) done, for which the scores of
+// t - 5 had to be read, whose scales may still be wanted: six groups at most, of one
+// tile each.
+constexpr int kKv8Groups = 8;
 constexpr float kKv8Below = 5.f, kKv8Top = 60000.f, kKv8TopLog2 = 15.8f;
 
 // Waits of the kernel (bits 16-31 of the error word).
@@ -56,6 +58,7 @@ enum : uint32_t {
 struct Kv8TileMeta {  // per 16 keys: 2^e_k, e_v, 2^-e_v and how many count
   float sk[8], ev[8], iv[8];
   uint32_t keys[8];
+  uint32_t whole[4];  // [0]: all of them count
 };
 
 template <int D>
@@ -163,10 +166,10 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
   constexpr int KS = kKv8KStages, VS = kKv8VStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full[KS], k_free[KS], v_full[VS], v_free[VS], v16_full[2], v16_free[2],
-      meta_full[kKv8Metas], q_full, s_full[2], s_read[2], p_full[2], o_done[2], all_done[3];
+      meta_full[kKv8Groups], q_full, s_full[2], s_read[2], p_full[2], o_done[2], all_done[3];
   __shared__ uint32_t tmem_base, failed;
   __shared__ Kv8Share share;
-  __shared__ __align__(16) Kv8TileMeta meta[kKv8Metas];
+  __shared__ __align__(16) Kv8TileMeta meta[kKv8Groups][4];
   __shared__ float2 row_ml[2][128];  // a piece's (m, l) of both streams
   __shared__ float row_f[128];       // score factors of its rows
   uint8_t* base = align1024(smem_raw);
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_free[i], 2);
     for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_free[i], 4);
-    for (int i = 0; i < kKv8Metas; ++i) mbar_init(&meta_full[i], 1);
+    for (int i = 0; i < kKv8Groups; ++i) mbar_init(&meta_full[i], 1);
     for (int i = 0; i < 2; ++i)
       mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 1), mbar_init(&o_done[i], 1),
           mbar_init(&s_full[i], 1), mbar_init(&s_read[i], 4), mbar_init(&p_full[i], 4);
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       if (lost) return;
       const bool a0 = mbar_try_wait(x, px), b0 = mbar_try_wait(y, py);  // (both at once)
       if (__all_sync(0xffffffffu, a0 && b0)) return;
-      lost = !wait(x, px, X8_META) || !wait(y, py, X8_S_FULL);
+      lost = !wait(x, px, X8_O_DONE) || !wait(y, py, X8_S_FULL);
     };
     const int w = warp >> 2, lrow = (warp & 3) * 32 + lane;  // stream, TMEM lane
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     uint8_t* xb = base + S::kX + warp * 2048;
     const int G = a.Hq / a.Hkv, R = a.B * G;
     const int per_g = 65536 / G + 1;  // r / G = r per_g / 2^16 for the rows r < 256
-    uint32_t t = 0;
+    uint32_t t = 0, mg = 0;  // tiles and groups of them
     kv8_pieces(a, share, [&](int n, int gt, int seg, int ctx, int u0, int u1) -> bool {
       debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
       const int g = gt / a.row_tiles, r0 = (gt - g * a.row_tiles) * 128;
@@ -311,10 +314,8 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
 
       float m = -FLT_MAX, l = 0.f;
       uint32_t x[64];
-      // the scores of tile tt, and that they have been read
-      auto begin_load = [&](uint32_t tt) {
-        await2(&meta_full[tt % kKv8Metas], (tt / kKv8Metas) & 1, &s_full[w], tt & 1);
-        tc_fence_after();
+      // the next scores into registers, and that they have been read
+      auto begin_load = [&] {
         if (!idle) {
           tmem_ld32_async(ts, *reinterpret_cast<uint32_t(*)[32]>(x));
           tmem_ld32_async(ts + 32u, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
@@ -327,17 +328,21 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_read[w]);
       };
-      begin_load(t);
+      await(&s_full[w], t & 1, X8_S_FULL);
+      tc_fence_after();
+      begin_load();
       end_load();
 #pragma unroll 1
       for (int u = u0; u < u1; ++u, ++t) {
-        const Kv8TileMeta& mt = meta[t % kKv8Metas];
+        if ((u - u0) % 4 == 0 && u > u0) ++mg;
+        if ((u - u0) % 4 == 0) await(&meta_full[mg % kKv8Groups], (mg / kKv8Groups) & 1, X8_META);
+        const Kv8TileMeta& mt = meta[mg % kKv8Groups][(u - u0) % 4];
         uint32_t pk[32];
         float k = 1.f;
         bool moved = false;
         if (!idle) {
-          const uint4 k4 = *reinterpret_cast<const uint4*>(&mt.keys[4 * w]);
-          if (min(min(k4.x, k4.y), min(k4.z, k4.w)) < 16u) {  // keys that do not count
+          if (!mt.whole[0]) {  // keys that do not count
+            const uint4 k4 = *reinterpret_cast<const uint4*>(&mt.keys[4 * w]);
             const uint32_t keys[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
             for (int i = 0; i < 64; ++i)
@@ -404,7 +409,13 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         }
         // the stream's product before has read P, and is in O (idle warps wait too: no
         // warp arrives twice in one phase of p_full)
-        if (t > 0) await(&o_done[w], (t - 1) & 1, X8_O_DONE);
+        // Beside it, the next scores.
+        if (u + 1 < u1 && t > 0)
+          await2(&o_done[w], (t - 1) & 1, &s_full[w], (t + 1) & 1);
+        else if (u + 1 < u1)
+          await(&s_full[w], (t + 1) & 1, X8_S_FULL);
+        else if (t > 0)
+          await(&o_done[w], (t - 1) & 1, X8_O_DONE);
         tc_fence_after();
         if (moved && u > u0) {
 #pragma unroll 1
@@ -417,7 +428,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           }
         }
         // the next scores come while P goes
-        if (u + 1 < u1) begin_load(t + 1);
+        if (u + 1 < u1) begin_load();
         if (!idle) tmem_st32(tp, *reinterpret_cast<float(*)[32]>(pk));
         tmem_wait_st();
         tc_fence_before();
@@ -425,6 +436,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[w]);
         if (u + 1 < u1) end_load();
       }
+      ++mg;
       // the piece's partials, once both streams' last products are done: each stream
       // reads both O for half of the channels and writes their sum
       row_ml[w][lrow] = make_float2(m, l);
@@ -495,12 +507,14 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         from[i] = rows_off<D>(r, uint32_t(c));
         to[i] = uint32_t(D == 128 ? c >> 2 : 0) * 16384u + sw128_off(r, uint32_t(c & 3) * 2u);
       }
-      uint32_t t = 0;
+      uint32_t t = 0, mg = 0;
       kv8_pieces(a, share, [&](int, int, int, int, int u0, int u1) -> bool {
         for (int u = u0; u < u1; ++u, ++t) {
           const uint32_t st = t % VS, b = t & 1;
-          const Kv8TileMeta& mt = meta[t % kKv8Metas];
-          if (!wait(&meta_full[t % kKv8Metas], (t / kKv8Metas) & 1, X8_META)) return false;
+          if ((u - u0) % 4 == 0 && u > u0) ++mg;
+          if ((u - u0) % 4 == 0 && !wait(&meta_full[mg % kKv8Groups], (mg / kKv8Groups) & 1, X8_META))
+            return false;
+          const Kv8TileMeta& mt = meta[mg % kKv8Groups][(u - u0) % 4];
           if (!wait(&v_full[st], (t / VS) & 1, X8_V_FULL)) return false;
           if (t >= 2 && !wait(&v16_free[b], ((t >> 1) - 1) & 1, X8_V16_FREE)) return false;
           const uint32_t src = vs + st * S::kTile, dst = v16 + b * S::kTile16;
@@ -508,8 +522,8 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
 #pragma unroll
           for (int s = 0; s < kTasks; ++s)
             x[s] = lds128(src + from[s % kPar] + uint32_t(s / kPar) * (8u * D));
-          const uint32_t k0 = mt.keys[2 * cw], k1 = mt.keys[2 * cw + 1];  // of this warp's rows
-          if (min(k0, k1) < 16u) {  // rows that do not count may hold any bytes: no 0 * NaN
+          if (!mt.whole[0]) {  // rows that do not count may hold any bytes: no 0 * NaN
+            const uint32_t k0 = mt.keys[2 * cw], k1 = mt.keys[2 * cw + 1];  // of this warp's rows
 #pragma unroll
             for (int s = 0; s < kTasks; ++s) {
               const uint32_t r = uint32_t(row_of(s));
@@ -531,6 +545,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&v_free[st]), mbar_arrive(&v16_full[b]);
         }
+        ++mg;
         return true;
       });
     }
@@ -540,7 +555,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       // ------------------------------------------------------------ copies
       const int page = 1 << a.c.page_log2;
       const int ti = lane >> 3, gr = (lane & 7) * 16;  // this lane's tile of four, its 16 keys
-      uint32_t t = 0, k_issued = 0, v_issued = 0;
+      uint32_t t = 0, mg = 0, k_issued = 0, v_issued = 0;
       kv8_pieces(a, share, [&](int n, int gt, int, int ctx, int u0, int u1) -> bool {
         const int g = gt / a.row_tiles;
         const int32_t* table = a.c.table + size_t(n) * a.c.max_pages;
@@ -566,18 +581,21 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           const bool head = have && (gr & (page - 1)) == 0;  // this lane copies the page
           const uint32_t heads = __ballot_sync(0xffffffffu, head);
           const int tiles = min(4, u1 - u);
-          auto publish = [&](int i) {  // of tile i: its keys and scales
-            const uint32_t x = (t + uint32_t(i)) % kKv8Metas;
-            if (ti == i) {
-              const int e_k = kv8_exp(uint32_t(ek)), e_v = kv8_exp(uint32_t(ev)), j = lane & 7;
-              meta[x].sk[j] = exp2_int(e_k);
-              meta[x].ev[j] = float(e_v);
-              meta[x].iv[j] = exp2_int(-e_v);
-              meta[x].keys[j] = have ? uint32_t(min(16, ctx - pos)) : 0u;
-            }
+          auto publish = [&] {  // the group's keys and scales
+            const uint32_t x = mg % kKv8Groups;
+            const int e_k = kv8_exp(uint32_t(ek)), e_v = kv8_exp(uint32_t(ev)), j = lane & 7;
+            const int keys = have ? min(16, ctx - pos) : 0;
+            const uint32_t some = __ballot_sync(0xffffffffu, keys < 16);
+            Kv8TileMeta& m = meta[x][ti];
+            m.sk[j] = exp2_int(e_k), m.ev[j] = float(e_v), m.iv[j] = exp2_int(-e_v);
+            m.keys[j] = uint32_t(keys);
+            if (j == 0) m.whole[0] = (some >> (8 * ti) & 0xFFu) == 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(&meta_full[x]);
+            ++mg;
           };
+          // (a piece's first scales are still on their way: its first copies go before them)
+          if (u > u0) publish();
           for (int i = 0; i < tiles; ++i) {
             const uint32_t x = t + uint32_t(i), ks = x % KS, vst = x % VS;
             const uint32_t bytes = uint32_t(__popc(heads >> (8 * i) & 0xFFu) * page) * D;
@@ -588,7 +606,6 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
             if (head && ti == i)
               tma_load_3d(base + ks * S::kTile + uint32_t(gr) * D, &kmap, &k_full[ks], 0,
                           g << a.c.page_log2, phys);
-            if (u > u0) publish(i);  // (its scales came while the four before were copied)
             if (x >= uint32_t(VS) && !wait(&v_free[vst], (x / VS - 1) & 1, X8_V_FREE)) return false;
             v_issued = x + 1;
             if (lane == 0) mbar_arrive_expect_tx(&v_full[vst], bytes);
@@ -597,8 +614,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
               tma_load_3d(base + S::kV + vst * S::kTile + uint32_t(gr) * D, &vmap, &v_full[vst], 0,
                           g << a.c.page_log2, phys);
           }
-          if (u == u0)
-            for (int i = 0; i < tiles; ++i) publish(i);
+          if (u == u0) publish();
           phys = next, next = after, ek = ek1, ev = ev1;
           t += uint32_t(tiles);
         }
