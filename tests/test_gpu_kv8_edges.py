@@ -1,0 +1,92 @@
+"""The paged 8-bit cache's attention over its kernels' variants (query rows per KV head up to
+8, 16, 32, 128, 256; both head sizes), pages and blocks: keys with holes, bytes behind the
+lengths, pieces of every kind, and random cases."""
+import random
+
+import numpy as np
+import pytest
+
+import kv4_ref
+import kv8_ref as ref
+from test_gpu_kv8 import check, make_cache, run_attn
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+# query tokens of 4 heads a group: 4, 16, 32, 128 and 256 rows per KV head
+TOKENS = [1, 4, 8, 32, 64]
+
+
+@pytest.mark.parametrize("B", TOKENS)
+@pytest.mark.parametrize("page,block", [(16, 16), (64, 32), (128, 128)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_missing_pages(B, page, block, d):
+    """Table entries without a page are masked: single pages, whole 128-key tiles, a sequence's
+    first and last, and sequences that have none at all."""
+    rng = np.random.default_rng(page + B)
+    N, Hq, Hkv = 4, 8, 2
+    lengths = [1000, 900, 640, 257]
+    c = make_cache(rng, N, Hkv, d, page, block, lengths)
+    per = 128 // page
+    c.table[0, per:2 * per] = -1             # the second tile of 128 keys
+    c.table[0, 4 * per] = c.n_pages          # past the arrays
+    c.table[0, 5 * per + per // 2] = 2 ** 31 - 1
+    c.table[1, 0] = -1
+    c.table[1, -(-900 // page) - 1] = -7     # the page that holds the last keys
+    c.table[2, :] = -5
+    c.table[3, ::2] = -1
+    q = kv4_ref.bf16(rng.standard_normal((N, B, Hq, d)))
+    r = ref.Cache.__new__(ref.Cache)         # (the reference wants -1 for a missing page)
+    r.__dict__.update(c.__dict__, table=np.where((c.table < 0) | (c.table >= c.n_pages), -1, c.table))
+    want, tol = ref.attention(q, r, lengths)
+    got = run_attn(c, q, lengths, B, 1000)
+    check(got, want, tol, f"B {B} page {page}")
+    assert (got[2] == 0).all()
+
+
+@pytest.mark.parametrize("B", TOKENS)
+def test_bytes_behind_the_lengths(B):
+    """NaN codes and any scales behind a length, inside its block and page, change nothing."""
+    rng = np.random.default_rng(50)
+    N, Hq, Hkv, d, page = 3, 8, 2, 128, 64
+    lengths = [65, 127, 300]
+    c = make_cache(rng, N, Hkv, d, page, 16, lengths)
+    for n, L in enumerate(lengths):
+        ph, r = c.table[n, L // page], L % page
+        c.codes[:, ph, :, r:] = 0x7F
+        c.scales[:, ph, :, -(-r // 16):] = 255
+    q = kv4_ref.bf16(rng.standard_normal((N, B, Hq, d)))
+    want, tol = ref.attention(q, c, lengths)
+    check(run_attn(c, q, lengths, B, 300), want, tol, "behind")
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_cases(seed):
+    r = random.Random(seed)
+    rng = np.random.default_rng(seed)
+    d, Hkv, G = r.choice((64, 128)), r.choice((1, 2, 3, 8)), r.choice((1, 2, 3, 5, 7, 8))
+    page = r.choice((16, 32, 64, 128))
+    block = r.choice([b for b in (16, 32, 64, 128) if b <= page])
+    B = r.choice((1, 1, 2, 3, 4, r.randint(1, 256 // G)))
+    top = r.choice((1, 130, 1000, 5000))
+    N = r.randint(1, max(1, min(24, 60000 // (top * Hkv))))
+    lengths = [r.choice((0, 1, top, r.randint(0, top))) for _ in range(N)]
+    c = make_cache(rng, N, Hkv, d, page, block, lengths)
+    q = kv4_ref.bf16(rng.standard_normal((N, B, Hkv * G, d)))
+    bk = bv = None
+    if r.random() < 0.5:
+        bk, bv = (kv4_ref.bf16(rng.standard_normal((N, B, Hkv, d))) for _ in range(2))
+    want, tol = ref.attention(q, c, lengths, bk, bv)
+    what = f"N {N} Hkv {Hkv} G {G} d {d} B {B} page {page} block {block} top {top} own {bk is not None}"
+    check(run_attn(c, q, lengths, B, max(1, max(lengths)), bk, bv), want, tol, what)
+
+
+@pytest.mark.parametrize("B", TOKENS)
+def test_one_sequence_of_every_length(B):
+    """Lengths around tiles, pages and blocks."""
+    rng = np.random.default_rng(51)
+    for L in (1, 2, 15, 16, 17, 127, 128, 129, 255, 256, 257, 511, 513, 640):
+        c = make_cache(rng, 1, 1, 128, 16, 16, [L])
+        q = kv4_ref.bf16(rng.standard_normal((1, B, 4, 128)))
+        want, tol = ref.attention(q, c, [L])
+        check(run_attn(c, q, [L], B, L), want, tol, f"length {L}")
