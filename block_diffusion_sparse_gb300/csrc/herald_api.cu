@@ -901,7 +901,7 @@ herald_status herald_kv8_append(herald_dims dims, int T, const int32_t* n_tok, c
                                   k_rot, pooled, Bk, flags));
   HERALD_TRY_CUDA(launch_kv8_append(dims, T, n_tok, q, q_ld, k, k_ld, v, v_ld, rope, ctx_len,
                                     cache ? &c : nullptr, q_rot, k_rot, pooled, Bk,
-                                    (flags & HERALD_KV8_ADVANCE) != 0, sm_count(),
+                                    (flags & HERALD_KV8_ADVANCE) != 0,
                                     static_cast<cudaStream_t>(stream)),
                   "kv8 append launch");
   return HERALD_OK;

@@ -360,8 +360,7 @@ cudaError_t launch_kv8_append(const herald_dims& dm, int T, const int32_t* n_tok
                               const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld,
                               const uint16_t* v, int64_t v_ld, const herald_rope* rope,
                               int32_t* ctx, const Kv8Dev* cache, uint16_t* q_rot, uint16_t* k_rot,
-                              float* pooled, int Bk, bool advance, int num_sms,
-                              cudaStream_t st);
+                              float* pooled, int Bk, bool advance, cudaStream_t st);
 cudaError_t launch_kv8_gather(const herald_dims& dm, const int32_t* idx, const int32_t* n_sel,
                               int P_max, const Kv8Dev& c, uint16_t* pk, uint16_t* pv, int num_sms,
                               cudaStream_t st);

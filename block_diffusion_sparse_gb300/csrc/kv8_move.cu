@@ -10,6 +10,10 @@
 namespace herald {
 
 constexpr int kKv8MoveThreads = 256;
+// Query heads of an item: they share a lane's angles, and their loads are in flight
+// together.  Prompts of 4 x 4096 tokens, 32 + 2 x 8 heads, with 2 / 4 / 8: 74 / 63 / 61 us;
+// below 512 tokens the three (and 1) are alike, 5 to 7 us.
+constexpr int kQueryHeads = 8;
 
 // The smallest exponent e with top <= 448 2^e (448 = 1.75 2^8), of a bf16 magnitude's
 // bits, within the scales' range.
@@ -56,7 +60,7 @@ struct Kv8AppendArgs {
   int units;                 // of a sequence: touched blocks x kinds x KV heads
   int kinds;                 // 2: keys and values, 1: keys only
   int block_log2;            // of the units (the cache's, 16 without one)
-  int q_chunks, tok_log2;    // queries: chunks of Per heads, tokens of a CTA
+  int q_chunks, tok_log2;    // queries: chunks of kQueryHeads heads, tokens of a CTA
   Kv8Dev c;                  // (kc null: rotate only)
 };
 
@@ -96,8 +100,13 @@ HERALD_DEV uint4 shfl4(const uint4& x, int src) {
 // warp's (all loads first), so block/16 warps share a unit and its maximum.  Where
 // the first block holds older rows and its scale grows, the same warps hold those
 // anew.  A CTA has the units of neighbouring heads: rows of a token lie side by side.
-template <int D, bool Interleaved, int Per>
-__global__ void __launch_bounds__(kKv8MoveThreads) kv8_append_kernel(const Kv8AppendArgs a) {
+// (Registers: the half-split form has twice the angles; with 64 instead of 84 a lane it takes
+// 14.0 us for 1024 tokens instead of 12.5, the other with 84 instead of 64 64 us for the
+// prompts instead of 61.)
+template <int D, bool Interleaved>
+__global__ void __launch_bounds__(kKv8MoveThreads, Interleaved ? 4 : 3)
+    kv8_append_kernel(const Kv8AppendArgs a) {
+  constexpr int Per = kQueryHeads;
   constexpr int LPR = D / 8, RPP = 32 / LPR, P = 16 / RPP;  // rows per pass of a warp, passes
   __shared__ uint32_t tops[kKv8MoveThreads / 32];
   griddep_enter();
@@ -375,7 +384,7 @@ cudaError_t launch_kv8_append(const herald_dims& dm, int T, const int32_t* n_tok
                               const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld,
                               const uint16_t* v, int64_t v_ld, const herald_rope* rope,
                               int32_t* ctx, const Kv8Dev* cache, uint16_t* q_rot, uint16_t* k_rot,
-                              float* pooled, int Bk, bool advance, int num_sms, cudaStream_t st) {
+                              float* pooled, int Bk, bool advance, cudaStream_t st) {
   Kv8AppendArgs a{};
   a.q = q, a.k = k, a.v = v;
   a.q_ld = q_ld, a.k_ld = k_ld, a.v_ld = v_ld;
@@ -399,23 +408,16 @@ cudaError_t launch_kv8_append(const herald_dims& dm, int T, const int32_t* n_tok
   a.kv_ctas = int(kv_ctas);
   int64_t q_ctas = 0;
   const int rpc = kKv8MoveThreads / (dm.d / 8);  // query rows of a CTA and load
-  const int per = int64_t(dm.N) * T * dm.Hq <= int64_t(num_sms) * 6 * rpc ? 1 : 4;
   if (q) {
-    a.q_chunks = cdiv(dm.Hq, per);
+    a.q_chunks = cdiv(dm.Hq, kQueryHeads);
     while ((1 << a.tok_log2) < T && (2 << a.tok_log2) <= rpc) ++a.tok_log2;
     q_ctas = int64_t(cdiv(T, 1 << a.tok_log2)) * cdiv(a.q_chunks, rpc >> a.tok_log2);
   }
   if (kv_ctas + q_ctas >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
   const dim3 grid(unsigned(kv_ctas + q_ctas), unsigned(dm.N));
-  auto pick = [&](auto d, auto il) {
-    return per == 1 ? kv8_append_kernel<d.value, il.value, 1>
-                    : kv8_append_kernel<d.value, il.value, 4>;
-  };
-  constexpr std::integral_constant<int, 128> d128{};
-  constexpr std::integral_constant<int, 64> d64{};
   const bool il = rope && rope->interleaved;
-  auto* kernel = dm.d == 128 ? (il ? pick(d128, std::true_type{}) : pick(d128, std::false_type{}))
-                             : (il ? pick(d64, std::true_type{}) : pick(d64, std::false_type{}));
+  auto* kernel = dm.d == 128 ? (il ? kv8_append_kernel<128, true> : kv8_append_kernel<128, false>)
+                             : (il ? kv8_append_kernel<64, true> : kv8_append_kernel<64, false>);
   HERALD_CHECK_LAUNCH(
       launch_k("kv8_append_kernel", kernel, grid, dim3(kKv8MoveThreads), 0, st, a));
   if (pooled) {
