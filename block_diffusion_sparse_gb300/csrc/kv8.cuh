@@ -103,8 +103,12 @@ struct Kv8AttnArgs {
   int pad;       // what a piece costs beside its tiles, in tiles (kv4_units)
   Kv8Dev c;
 };
-// The kernel for `rows` <= kKv8FewRows query rows per KV head (kv8_rows.cu).
-constexpr int kKv8FewRows = 32;
+// The kernel for `rows` <= kKv8FewRows query rows per KV head (kv8_rows.cu).  It and the one
+// for more rows, in us over 64 sequences of up to 8K tokens / one of 128K / one of 32K (8 KV
+// heads, d = 128): 16 rows 105 / 48.3 / 18.1 here and 136 / 58.9 / 23.6 there.  Its softmax keeps a
+// row of a key in two registers and more: with 32 rows they would spill (a form of it measured
+// 269 / 102 / 53, the other kernel 145 / 61 / 24).
+constexpr int kKv8FewRows = 16;
 cudaError_t launch_kv8_rows(int d, int rows, const Kv8AttnArgs& a, const CUtensorMap& kmap,
                             const CUtensorMap& vmap, uint32_t* err, cudaStream_t st);
 // The kernel for more (kv8_attn_tc.cu).
@@ -160,12 +164,14 @@ template <typename Body>
 HERALD_DEV void kv8_pieces(const Kv8AttnArgs& a, const Kv8Share& sh, Body&& body) {
   const int heads = a.Hkv * a.row_tiles;
   int at = sh.at, first = sh.first, n = sh.n, ctx = sh.ctx;
+  int next = a.ctx[min(n + 1, a.N - 1)];  // (of the sequence after, before it is asked for)
   while (at < sh.end) {
     const int units = kv4_units(ctx, a.L_max, 0, a.pad);
     if (units == 0 || at >= first + heads * units) {  // the next sequence
       first += heads * units;
       ++n;
-      ctx = warp_same(min(max(a.ctx[n], 0), a.L_max));
+      ctx = warp_same(min(max(next, 0), a.L_max));
+      next = a.ctx[min(n + 1, a.N - 1)];
       continue;
     }
     const int gt = (at - first) / units;

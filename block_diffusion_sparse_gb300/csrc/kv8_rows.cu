@@ -18,15 +18,17 @@
 // whatever their values' scales.
 //
 // One CTA per SM walks its share of the keys (kv4_split):
-//   warps 0-3  softmax, a thread per key of the tile (its TMEM lane), rows in registers;
-//              each keeps the sum of its own keys' weights
-//   warp 4     the issuer of both products, S a tile ahead of P V
-//   warp 5     copies tiles into a ring and looks up pages and scales, four tiles of
-//              page table and scales (32 lanes: 8 groups of 16 keys each) ahead
-//   warp 6     stages the queries of the next piece
+//   warps 0-3, 4-7  softmax: two streams that take the tiles in turn, a thread per key of
+//              the tile (its TMEM lane), rows in registers; each keeps the sum of its own
+//              keys' weights, each stream its own base m and O, added up at a piece's end
+//   warp 8     the issuer of both products, S two tiles ahead of P V
+//   warps 9, 10  copy tiles of keys and of values into a ring each, and look up pages and
+//              scales, four tiles of them (32 lanes: 8 groups of 16 keys each) ahead.  A tile's
+//              keys leave after its scores; its values wait for the weights, some tiles longer
+//   warp 11    stages the queries of the next piece
 // A row's exponent base m is set 4 below its largest exponent and stays while no p passes
-// 2^8; all four warps vote on that in one barrier a tile.  Else the tile's row maxima are
-// exchanged, O is scaled once the products before it are done, and l follows.
+// 2^8; a stream's four warps vote on that in one barrier a tile.  Else the tile's row maxima
+// are exchanged, O is scaled once the products before it are done, and l follows.
 #include <float.h>
 
 #include "kv8.cuh"
@@ -36,12 +38,13 @@ namespace herald {
 
 constexpr int kKv8Parts = 4;               // e4m3 numbers of a weight
 constexpr float kKv8At = 4.f, kKv8Most = 8.f;  // log2 p of a new base's row, and the largest
-constexpr int kKv8RowsThreads = 224;       // 7 warps
+constexpr int kKv8RowsThreads = 384;       // 12 warps
+constexpr int kKv8Metas = 16;              // tiles whose scales are held
 
 // Waits of the kernel (bits 16-31 of the error word).
 enum : uint32_t {
-  W8_STAGE_FREE = 1, W8_STAGE_FULL = 2, W8_Q_FREE = 4, W8_Q_FULL = 8, W8_S_FULL = 0x10,
-  W8_P_FULL = 0x20, W8_PV_DONE = 0x40
+  W8_K_FREE = 1, W8_K_FULL = 2, W8_Q_FREE = 4, W8_Q_FULL = 8, W8_S_FULL = 0x10,
+  W8_P_FULL = 0x20, W8_PV_DONE = 0x40, W8_V_FREE = 0x80, W8_V_FULL = 0x100, W8_META = 0x200
 };
 
 template <int D, int RP>
@@ -49,11 +52,18 @@ struct Kv8Rows {
   static constexpr int kNs = 2 * RP;                // columns of S: q0 rows, q1 rows
   static constexpr int kNo = kKv8Parts * RP;        // columns of O, bytes of a key's P
   static constexpr uint32_t kTile = 128u * D;       // bytes of 128 keys
-  static constexpr uint32_t kStage = 2 * kTile;
-  static constexpr int kStages = D == 64 ? 8 : RP == 32 ? 5 : 6;
+  // Stages of 128 keys and of 128 values.  160 KB in flight an SM: more only makes pages of
+  // other rows meet in DRAM (64 sequences of up to 8K tokens, 1 and 16 rows: 5 and 5 stages
+  // 93.6 and 104.7 us, 4 and 5 93.6 and 105.7, 3 and 4 95.3 and 102.7, 4 and 7 93.4 and 116.1,
+  // 6 and 7 97.9 and, 5 and 7, 112.7; one sequence of 128K 46.9 / 46.8 / 47.8 / 48.0 / 49.6).
+  static constexpr int kKs = D == 64 ? 10 : 5, kVs = kKs;
   static constexpr uint32_t kQ = uint32_t(kNs) * D, kP = 128u * kNo;
-  static constexpr uint32_t kSmem = kStages * kStage + 2 * kQ + 2 * kP + 1024;
-  static constexpr uint32_t kCols = RP == 8 ? 64 : RP == 16 ? 128 : 256;  // 2 S + O
+  static constexpr uint32_t kSmem = (kKs + kVs) * kTile + 2 * kQ + 2 * kP + 1024;
+  static constexpr int kSBufs = 4;
+  static constexpr uint32_t kCols = kSBufs * kNs + 2 * kNo;  // of tensor memory
+  // scales are written with a tile's keys, which wait for the products of kKs before; the
+  // weights of three before those have been made by then
+  static_assert(kKs + 3 <= kKv8Metas, "scales outlive their reader");
 };
 
 // What the softmax needs of 16 keys: 2^e_k, e_v, 2^-e_v and how many of them count.
@@ -72,17 +82,18 @@ HERALD_DEV uint32_t split_e4m3(float& a, float& b) {
   return w;
 }
 
-HERALD_DEV bool soft_any(bool x) {  // any of the softmax threads
+HERALD_DEV bool soft_any(int g, bool x) {  // any of a stream's threads
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.aligned.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(uint32_t(x))
+      : "r"(uint32_t(x)), "r"(1 + g)
       : "memory");
   return r != 0;
 }
-HERALD_DEV void soft_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+HERALD_DEV void soft_bar(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
+HERALD_DEV void both_bar() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 template <int N>
 HERALD_DEV void tmem_load(uint32_t at, float (&v)[N]) {
@@ -95,35 +106,93 @@ HERALD_DEV void tmem_load(uint32_t at, float (&v)[N]) {
   }
 }
 
+// N = 4 or 8 columns of this thread's lane at each of four places.
+HERALD_DEV void tmem_ld_parts(uint32_t at, uint32_t step, uint32_t (&r)[4][4]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%4, %5, %6, %7}, [%17];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%8, %9, %10, %11}, [%18];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%12, %13, %14, %15}, [%19];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[1][0]), "=r"(r[1][1]),
+        "=r"(r[1][2]), "=r"(r[1][3]), "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[2][2]), "=r"(r[2][3]),
+        "=r"(r[3][0]), "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3])
+      : "r"(at), "r"(at + step), "r"(at + 2 * step), "r"(at + 3 * step)
+      : "memory");
+}
+HERALD_DEV void tmem_ld_parts(uint32_t at, uint32_t step, uint32_t (&r)[4][8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[0][4]), "=r"(r[0][5]),
+        "=r"(r[0][6]), "=r"(r[0][7]), "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]),
+        "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]), "=r"(r[2][0]), "=r"(r[2][1]),
+        "=r"(r[2][2]), "=r"(r[2][3]), "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7]),
+        "=r"(r[3][0]), "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3]), "=r"(r[3][4]), "=r"(r[3][5]),
+        "=r"(r[3][6]), "=r"(r[3][7])
+      : "r"(at), "r"(at + step), "r"(at + 2 * step), "r"(at + 3 * step)
+      : "memory");
+}
+
+// All N rows' values over a warp's lanes at once: each step halves the rows a lane holds.
+// Lane i < N returns row i's, as do lanes i + N and so on.
+template <int N, typename Op>
+HERALD_DEV float warp_rows(float (&v)[N], Op&& op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = N / 2; h >= 1; h >>= 1) {
+    const bool up = lane & h;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float give = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, h));
+    }
+  }
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
+}
+
 template <int D, int RP>
 __global__ void __launch_bounds__(kKv8RowsThreads, 1)
     kv8_rows_kernel(const Kv8AttnArgs a, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, uint32_t* err) {
   using S = Kv8Rows<D, RP>;
-  constexpr int NS = S::kNs, NO = S::kNo, ST = S::kStages;
+  constexpr int NS = S::kNs, NO = S::kNo, KS = S::kKs, VS = S::kVs, SB = S::kSBufs;
+  constexpr int MB = kKv8Metas;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[ST], empty[ST], q_full[2], q_free[2], s_full[2], p_full[2], pv_done[2],
-      all_done;
+  __shared__ uint64_t k_full[KS], k_free[KS], v_full[VS], v_free[VS], m_full[MB], q_full[2],
+      q_free[2], s_full[SB], p_full[2], pv_done[2], all_done;
   __shared__ uint32_t tmem_base, failed;
   __shared__ Kv8Share share;
-  __shared__ Kv8Meta meta[ST][8];
+  __shared__ Kv8Meta meta[MB][8];
   __shared__ __align__(16) float row_f[2][RP];  // score factors of the rows
-  __shared__ float red[4][RP];
+  __shared__ float red[2][4][RP];               // row maxima of a stream's warps
+  // a piece's bases and the warps' sums of both streams
+  __shared__ __align__(16) float row_m[2][RP];
+  __shared__ float row_l[2][4][RP];
   uint8_t* base = align1024(smem_raw);
-  uint8_t *Qs = base + ST * S::kStage, *Ps = Qs + 2 * S::kQ;
+  uint8_t *Vs = base + KS * S::kTile, *Qs = Vs + VS * S::kTile, *Ps = Qs + 2 * S::kQ;
   const int warp = warp_same(int(threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; ++i) mbar_init(&full[i], 2), mbar_init(&empty[i], 1);
+    for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_free[i], 1);
+    for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_free[i], 1);
+    for (int i = 0; i < MB; ++i) mbar_init(&m_full[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&q_full[i], 1), mbar_init(&q_free[i], 5), mbar_init(&s_full[i], 1),
-          mbar_init(&p_full[i], 128), mbar_init(&pv_done[i], 1);
+      mbar_init(&q_full[i], 1), mbar_init(&q_free[i], 9), mbar_init(&p_full[i], 4),
+          mbar_init(&pv_done[i], 1);
+    for (int i = 0; i < SB; ++i) mbar_init(&s_full[i], 1);
     mbar_init(&all_done, 1);
     failed = 0;
     fence_mbar_init();
   }
-  if (warp == 5 && lane == 0) tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
+  if (warp == 9 && lane == 0) tma_prefetch_desc(&kmap);
+  if (warp == 10 && lane == 0) tma_prefetch_desc(&vmap);
   tmem_setup(&tmem_base, S::kCols);
-  const uint32_t tm = tmem_base, to = tm + 2 * NS;
+  const uint32_t tm = tmem_base, to = tm + SB * NS;  // S buffers, then both streams' O
   griddep_enter();
   const Kv4Wait wait{&failed};
   const int G = a.Hq / a.Hkv, R = a.B * G;
@@ -133,7 +202,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
   }
   __syncthreads();
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ------------------------------------------------------------ softmax
     // (after a failed wait these warps go on without waiting: the barriers among them
     // stay in step, the results are worthless and the error is recorded)
@@ -141,93 +210,89 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
     auto await = [&](uint64_t* bar, uint32_t parity, uint32_t which) {
       if (!lost) lost = !wait(bar, parity, which);
     };
-    const int key = int(threadIdx.x);
-    const uint32_t lanes = uint32_t(warp * 32) << 16;
-    uint32_t t = 0, np = 0;  // tiles and pieces of the CTA
+    const int w = warp >> 2, wq = warp & 3, key = int(threadIdx.x) & 127;  // stream, quarter, key
+    const uint32_t lanes = uint32_t(wq * 32) << 16, tow = to + lanes + uint32_t(w) * NO;
+    uint32_t t0 = 0, np = 0;  // tiles and pieces of the CTA
     kv8_pieces(a, share, [&](int n, int, int seg, int ctx, int u0, int u1) -> bool {
       debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
       const uint32_t qb = np & 1;
       await(&q_full[qb], (np >> 1) & 1, W8_Q_FULL);
-      constexpr bool kKeepF = RP < 32;  // (32 factors in registers would spill)
-      float f[kKeepF ? RP : 1] = {}, m[RP], l[RP];
-      if constexpr (kKeepF) {
+      float f[RP], m[RP], l[RP];
 #pragma unroll
-        for (int r = 0; r < RP; r += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(&row_f[qb][r]);
-          f[r] = x.x, f[r + 1] = x.y, f[r + 2] = x.z, f[r + 3] = x.w;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_free[qb]);
+      for (int r = 0; r < RP; r += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&row_f[qb][r]);
+        f[r] = x.x, f[r + 1] = x.y, f[r + 2] = x.z, f[r + 3] = x.w;
       }
-      auto factor = [&](int r) { return kKeepF ? f[kKeepF ? r : 0] : *(volatile float*)&row_f[qb][r]; };
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_free[qb]);
       ++np;
 #pragma unroll
       for (int r = 0; r < RP; ++r) m[r] = -FLT_MAX, l[r] = 0.f;
+      const uint32_t t1 = t0 + uint32_t(u1 - u0), mine = t0 + ((t0 ^ uint32_t(w)) & 1);
 #pragma unroll 1
-      for (int u = u0; u < u1; ++u, ++t) {
-        const uint32_t b = t & 1, st = t % ST;
-        await(&full[st], (t / ST) & 1, W8_STAGE_FULL);  // (the meta data and V are here)
-        await(&s_full[b], (t >> 1) & 1, W8_S_FULL);
+      for (uint32_t t = mine; t < t1; t += 2) {
+        await(&m_full[t % MB], (t / MB) & 1, W8_META);
+        await(&s_full[t % SB], (t / SB) & 1, W8_S_FULL);
         tc_fence_after();
-        const Kv8Meta mt = meta[st][key >> 4];
+        const Kv8Meta mt = meta[t % MB][key >> 4];
         const bool on = (key & 15) < mt.keys;
         float s[RP], p[RP];
         {
           float x[NS];
-          tmem_load<NS>(tm + lanes + b * NS, x);
+          tmem_load<NS>(tm + lanes + t % SB * NS, x);
 #pragma unroll
           for (int r = 0; r < RP; ++r) s[r] = fmaf(x[RP + r], 0.0625f, x[r]);
         }
         bool move = false;
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          p[r] = on ? fmaf(s[r], factor(r) * mt.sk, mt.ev - m[r]) : -INFINITY;
+          p[r] = on ? fmaf(s[r], f[r] * mt.sk, mt.ev - m[r]) : -INFINITY;
           move |= p[r] > kKv8Most;
         }
-        if (soft_any(move)) {
+        move = soft_any(w, move);
+        // P of the stream's tile before has been read, and is in O
+        if (t >= 2) await(&pv_done[w], ((t >> 1) - 1) & 1, W8_PV_DONE);
+        if (move) {
           // row maxima of the tile, rounded down: where scores are so large that fp32's
           // steps are no longer small, a base above them all would leave no weight
+          float z[RP];
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            const float z = __fadd_rd(__fmul_rd(s[r], factor(r) * mt.sk), mt.ev);
-            const float mx = warp_max(on ? z : -INFINITY);
-            if (lane == 0) red[warp][r] = mx;
-          }
-          soft_bar();
+          for (int r = 0; r < RP; ++r)
+            z[r] = on ? __fadd_rd(__fmul_rd(s[r], f[r] * mt.sk), mt.ev) : -INFINITY;
+          const float mx = warp_rows(z, [](float x, float y) { return fmaxf(x, y); });
+          if (lane < RP) red[w][wq][lane] = mx;
+          soft_bar(w);
           float k[RP];
 #pragma unroll
           for (int r = 0; r < RP; ++r) {
-            const float z = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
+            const float z = fmaxf(fmaxf(red[w][0][r], red[w][1][r]), fmaxf(red[w][2][r], red[w][3][r]));
             const float m1 = fmaxf(__fadd_rd(z, -kKv8At), m[r]);
             k[r] = fast_exp2(m[r] - m1);
             m[r] = m1;
             l[r] *= k[r];
-            const float x = fmaf(s[r], factor(r) * mt.sk, mt.ev - m1);
+            const float x = fmaf(s[r], f[r] * mt.sk, mt.ev - m1);
             p[r] = !on ? -INFINITY : x > kKv8Most ? kKv8Most : x;  // (a NaN stays)
           }
-          if (u > u0) {  // O so far, once the products before this tile are in it
-            await(&pv_done[b ^ 1], ((t - 1) >> 1) & 1, W8_PV_DONE);
+          if (t > mine) {
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < NO; c += 32) {
               float o[32];
-              tmem_ld32(to + lanes + uint32_t(c), o);
+              tmem_ld32(tow + uint32_t(c), o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] *= k[(c + i) % RP];
-              tmem_st32(to + lanes + uint32_t(c), o);
+              tmem_st32(tow + uint32_t(c), o);
             }
             tmem_wait_st();
           }
-          soft_bar();  // (the maxima have been read)
+          soft_bar(w);  // (the maxima have been read)
         }
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
           p[r] = fast_exp2(p[r]);
           l[r] = fmaf(p[r], mt.iv, l[r]);
         }
-        // P of two tiles before has been read
-        if (t >= 2) await(&pv_done[b], ((t >> 1) - 1) & 1, W8_PV_DONE);
-        uint8_t* dst = Ps + b * S::kP;
+        uint8_t* dst = Ps + uint32_t(w) * S::kP;
         uint32_t pk[NO / 4];
 #pragma unroll
         for (int i = 0; i < kKv8Parts; ++i)
@@ -238,94 +303,119 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         for (int c = 0; c < NO / 16; ++c)
           *reinterpret_cast<uint4*>(dst + rows_off<NO>(uint32_t(key), uint32_t(c))) =
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        if (!on) {  // such a row may hold any bytes: 0 * NaN must not arise
-          uint4* v = reinterpret_cast<uint4*>(base + st * S::kStage + S::kTile + uint32_t(key) * D);
+        if (__any_sync(0xffffffffu, !on)) {  // a row without a key may hold any bytes: 0 * NaN
+          await(&v_full[t % VS], (t / VS) & 1, W8_V_FULL);  // must not arise
+          if (!on) {
+            uint4* v = reinterpret_cast<uint4*>(Vs + t % VS * S::kTile + uint32_t(key) * D);
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&p_full[b]);
-      }
-      if constexpr (!kKeepF) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_free[qb]);
+        if (lane == 0) mbar_arrive(&p_full[w]);
       }
-      // the piece's partials: O once the last product is done, l over all keys
+      // the piece's partials: l over the stream's keys, then, once both streams' last
+      // products are done, each stream adds up both O for half of the rows
+      const float sum = warp_rows(l, [](float x, float y) { return x + y; });
+      if (lane < RP) row_l[w][wq][lane] = sum;
+      if (key == 0)
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        l[r] = warp_sum(l[r]);
-        if (lane == 0) red[warp][r] = l[r];
-      }
-      soft_bar();
-      const size_t slot = size_t(blockIdx.x) + seg;
-#pragma unroll
-      for (int r = 0; r < RP; ++r)
-        if (key == r && r < R)
-          a.ml[slot * a.R16 + r] = make_float2(m[r], red[0][r] + red[1][r] + red[2][r] + red[3][r]);
-      await(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, W8_PV_DONE);
+        for (int r = 0; r < RP; r += 4)
+          *reinterpret_cast<float4*>(&row_m[w][r]) = make_float4(m[r], m[r + 1], m[r + 2], m[r + 3]);
+      both_bar();
+      const bool two = u1 - u0 > 1;  // both streams had a tile; else that of the piece's first
+      await(&pv_done[(t1 - 1) & 1], ((t1 - 1) >> 1) & 1, W8_PV_DONE);
+      if (two) await(&pv_done[t1 & 1], ((t1 - 2) >> 1) & 1, W8_PV_DONE);
       tc_fence_after();
+      const size_t slot = size_t(blockIdx.x) + seg;
       // (with d = 64 an M = 64 product's rows lie in the first 16 lanes of each warp's 32)
-      const int ch = D == 128 ? key : warp * 16 + lane;
-      float* out = a.opart + slot * a.R16 * D + ch;
-      float o[NO];
-      tmem_load<NO>(to + lanes, o);
-      if (D == 128 || lane < 16) {
+      const int ch = D == 128 ? key : wq * 16 + lane;
+      constexpr int RH = RP / 2;
+      float x[2][RH];
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          float x = o[(kKv8Parts - 1) * RP + r];
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int i = kKv8Parts - 2; i >= 0; --i) x = fmaf(x, 0.0625f, o[i * RP + r]);
-          if (r < R) out[r * D] = x;
+        for (int r = 0; r < RH; ++r) x[h][r] = 0.f;
+        if (two || (t0 & 1) == uint32_t(h)) {
+          uint32_t o[4][RH];
+          tmem_ld_parts(to + lanes + uint32_t(h * NO + w * RH), RP, o);
+#pragma unroll
+          for (int i = kKv8Parts - 1; i >= 0; --i)
+#pragma unroll
+            for (int r = 0; r < RH; ++r) x[h][r] = fmaf(x[h][r], 0.0625f, __uint_as_float(o[i][r]));
         }
       }
+      if (key < RH && w * RH + key < R) {
+        const int row = w * RH + key;
+        const float m0 = row_m[0][row], m1 = row_m[1][row], mm = fmaxf(m0, m1);
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l0 += row_l[0][i][row], l1 += row_l[1][i][row];
+        a.ml[slot * a.R16 + row] =
+            make_float2(mm, fast_exp2(m0 - mm) * l0 + fast_exp2(m1 - mm) * l1);
+      }
+#pragma unroll
+      for (int r = 0; r < RH; ++r) {
+        const int row = w * RH + r;
+        const float m0 = row_m[0][row], m1 = row_m[1][row], mm = fmaxf(m0, m1);
+        if (row < R && (D == 128 || lane < 16))
+          a.opart[(slot * a.R16 + row) * D + ch] =
+              fmaf(x[0][r], fast_exp2(m0 - mm), x[1][r] * fast_exp2(m1 - mm));
+      }
       tc_fence_before();
-      soft_bar();  // (the sums have been read)
+      both_bar();  // (O, the sums and maxima have been read)
+      t0 = t1;
       return true;
     });
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ------------------------------------------------------------- products
-    const uint64_t kd = make_sdesc_rows<D>(smem_u32(base)), vd = kd + (S::kTile >> 4);
+    const uint64_t kd = make_sdesc_rows<D>(smem_u32(base)), vd = make_sdesc_rows<D>(smem_u32(Vs));
     const uint64_t qd = make_sdesc_rows<D>(smem_u32(Qs)), pd = make_sdesc_rows<NO>(smem_u32(Ps));
     constexpr uint32_t ids = make_idesc_e4m3(128, NS, false, false);
     constexpr uint32_t ido = make_idesc_e4m3(D, NO, true, true);
     uint32_t t = 0, np = 0;
-    // P V of tile x, the first of its piece or not
+    // P V of tile x, its stream's first in the piece or not
     auto pv = [&](uint32_t x, bool first) -> bool {
-      const uint32_t b = x & 1, st = x % ST;
+      const uint32_t b = x & 1, st = x % VS;
+      if (!wait(&v_full[st], (x / VS) & 1, W8_V_FULL)) return false;
       if (!wait(&p_full[b], (x >> 1) & 1, W8_P_FULL)) return false;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma_e4m3(to, vd + ((st * S::kStage + uint32_t(ks) * 32u * D) >> 4),
+          umma_e4m3(to + b * NO, vd + ((st * S::kTile + uint32_t(ks) * 32u * D) >> 4),
                     pd + ((b * S::kP + uint32_t(ks) * 32u * NO) >> 4), ido, !first || ks > 0);
         umma_commit(&pv_done[b]);
-        umma_commit(&empty[st]);
+        umma_commit(&v_free[st]);
       }
       __syncwarp();
       return true;
     };
     kv8_pieces(a, share, [&](int, int, int, int, int u0, int u1) -> bool {
-      const uint32_t qb = np & 1;
+      const uint32_t qb = np & 1, t1 = t + uint32_t(u1 - u0), t0 = t;
       if (!wait(&q_full[qb], (np >> 1) & 1, W8_Q_FULL)) return false;
-      for (int u = u0; u < u1; ++u, ++t) {
-        // (S of two tiles before has been read: its P was waited for)
-        const uint32_t st = t % ST;
-        if (!wait(&full[st], (t / ST) & 1, W8_STAGE_FULL)) return false;
-        tc_fence_after();
-        if (elect_one()) {
+      for (; t < t1 + 2; ++t) {
+        // (S of four tiles before has been read: its P was waited for)
+        if (t < t1) {
+          const uint32_t st = t % KS;
+          if (!wait(&k_full[st], (t / KS) & 1, W8_K_FULL)) return false;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < D / 32; ++ks)
-            umma_e4m3(tm + (t & 1) * NS, kd + ((st * S::kStage + uint32_t(ks) * 32u) >> 4),
-                      qd + ((qb * S::kQ + uint32_t(ks) * 32u) >> 4), ids, ks > 0);
-          umma_commit(&s_full[t & 1]);
-          if (u + 1 == u1) umma_commit(&q_free[qb]);
+            for (int ks = 0; ks < D / 32; ++ks)
+              umma_e4m3(tm + t % SB * NS, kd + ((st * S::kTile + uint32_t(ks) * 32u) >> 4),
+                        qd + ((qb * S::kQ + uint32_t(ks) * 32u) >> 4), ids, ks > 0);
+            umma_commit(&s_full[t % SB]);
+            umma_commit(&k_free[st]);
+            if (t + 1 == t1) umma_commit(&q_free[qb]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (u > u0 && !pv(t - 1, u == u0 + 1)) return false;
+        if (t >= t0 + 2 && !pv(t - 2, t - 2 < t0 + 2)) return false;
       }
-      if (!pv(t - 1, u1 == u0 + 1)) return false;
+      t = t1;
       ++np;
       return true;
     });
@@ -334,11 +424,17 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
       umma_commit(&all_done);
       mbar_wait(&all_done, 0);
     }
-  } else if (warp == 5) {
+  } else if (warp == 9 || warp == 10) {
     // --------------------------------------------------------------- copies
+    // (a warp for the keys and the scales, another for the values, which wait longer)
+    const bool keys = warp == 9;
     const int page = 1 << a.c.page_log2;
     const int ti = lane >> 3, gr = (lane & 7) * 16;  // this lane's tile of four, its 16 keys
-    uint32_t t = 0, issued = 0;
+    const uint32_t stages = keys ? KS : VS;
+    uint64_t *full = keys ? k_full : v_full, *free = keys ? k_free : v_free;
+    uint8_t* ring = keys ? base : Vs;
+    const CUtensorMap* map = keys ? &kmap : &vmap;
+    uint32_t t = 0, st = 0, round = 0;  // the next tile, its stage and the stage's use
     kv8_pieces(a, share, [&](int n, int g, int, int ctx, int u0, int u1) -> bool {
       const int32_t* table = a.c.table + size_t(n) * a.c.max_pages;
       const int stop = min(ctx, u1 * 128);
@@ -346,7 +442,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
       auto look = [&](int p) { return p < stop ? table[p >> a.c.page_log2] : -1; };
       auto scales = [&](int p, int phys, int& ek, int& ev) {
         ek = ev = 127;
-        if (p < stop && phys >= 0 && phys < a.c.n_pages) {
+        if (keys && p < stop && phys >= 0 && phys < a.c.n_pages) {
           const size_t at = kv8_scale(a.c, phys, a.Hkv, g, p);
           ek = a.c.ks[at], ev = a.c.vs[at];
         }
@@ -364,7 +460,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         const uint32_t heads = __ballot_sync(0xffffffffu, head);
         const int tiles = min(4, u1 - u);
         auto publish = [&](int i) {  // of tile i: its keys and scales
-          const uint32_t x = (t + uint32_t(i)) % ST;
+          const uint32_t x = (t + uint32_t(i)) % MB;
           if (ti == i) {
             Kv8Meta mt;
             const int e_k = kv8_exp(uint32_t(ek)), e_v = kv8_exp(uint32_t(ev));
@@ -373,24 +469,22 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
             meta[x][lane & 7] = mt;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[x]);
+          if (lane == 0) mbar_arrive(&m_full[x]);
         };
         for (int i = 0; i < tiles; ++i) {
-          const uint32_t x = t + uint32_t(i), st = x % ST;
-          if (x >= uint32_t(ST) && !wait(&empty[st], (x / ST - 1) & 1, W8_STAGE_FREE)) return false;
-          issued = x + 1;
+          if (round > 0 && !wait(&free[st], (round - 1) & 1, keys ? W8_K_FREE : W8_V_FREE))
+            return false;
           if (lane == 0)
             mbar_arrive_expect_tx(&full[st],
-                                  uint32_t(__popc(heads >> (8 * i) & 0xFFu) * page) * (2u * D));
+                                  uint32_t(__popc(heads >> (8 * i) & 0xFFu) * page) * D);
           __syncwarp();
-          if (head && ti == i) {
-            uint8_t* dst = base + st * S::kStage + uint32_t(gr) * D;
-            tma_load_3d(dst, &kmap, &full[st], 0, g << a.c.page_log2, phys);
-            tma_load_3d(dst + S::kTile, &vmap, &full[st], 0, g << a.c.page_log2, phys);
-          }
-          if (u > u0) publish(i);  // (its scales came while the four before were copied)
+          if (head && ti == i)
+            tma_load_3d(ring + st * S::kTile + uint32_t(gr) * D, map, &full[st], 0,
+                        g << a.c.page_log2, phys);
+          if (++st == stages) st = 0, ++round;
+          if (keys && u > u0) publish(i);  // (its scales came while the four before were copied)
         }
-        if (u == u0)
+        if (keys && u == u0)
           for (int i = 0; i < tiles; ++i) publish(i);
         phys = next, next = after, ek = ek1, ev = ev1;
         t += uint32_t(tiles);
@@ -399,8 +493,10 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
     });
     // every copy has landed before the CTA may leave (where a wait has run out, nobody
     // else waits for it)
-    for (uint32_t i = issued > uint32_t(ST) ? issued - ST : 0; i < issued; ++i)
-      mbar_wait(&full[i % ST], (i / ST) & 1);
+    for (uint32_t i = 0; i < stages; ++i) {
+      const uint32_t uses = round + (i < st ? 1 : 0);
+      if (uses > 0) mbar_wait(&full[i], (uses - 1) & 1);
+    }
   } else {
     // -------------------------------------------------------------- queries
     constexpr int LPR = D / 8, RPP = 32 / LPR, P = RP / RPP;
@@ -477,11 +573,9 @@ cudaError_t launch_kv8_rows(int d, int rows, const Kv8AttnArgs& a, const CUtenso
                             const CUtensorMap& vmap, uint32_t* err, cudaStream_t st) {
   if (d == 128)
     return rows <= 8    ? launch_rows<128, 8>(a, kmap, vmap, err, st)
-           : rows <= 16 ? launch_rows<128, 16>(a, kmap, vmap, err, st)
-                        : launch_rows<128, 32>(a, kmap, vmap, err, st);
+                        : launch_rows<128, 16>(a, kmap, vmap, err, st);
   return rows <= 8    ? launch_rows<64, 8>(a, kmap, vmap, err, st)
-         : rows <= 16 ? launch_rows<64, 16>(a, kmap, vmap, err, st)
-                      : launch_rows<64, 32>(a, kmap, vmap, err, st);
+                      : launch_rows<64, 16>(a, kmap, vmap, err, st);
 }
 
 HERALD_DEBUG_WORD_READER(debug_take_kv8_rows)

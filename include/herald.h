@@ -117,7 +117,11 @@ herald_status herald_inject_launch_failure(int after, int cuda_error);
  * 4-bit cache: 0x1 raw slot, 0x2 raw codes, 0x4 operand buffer free, 0x8
  * queries free, 0x10 queries staged, 0x20 K ready, 0x40 P ready, 0x80 V ready,
  * 0x100 P V done, 0x200 S ready, 0x400 key masks, 0x800 O ready, 0x1000 O read; with few rows
- * 0x1 stage free, 0x2 stage full).
+ * 0x1 stage free, 0x2 stage full; over a paged 8-bit cache with few rows: 0x1 K stage free,
+ * 0x2 K stage full, 0x4 queries free, 0x8 queries staged, 0x10 S ready, 0x20 P ready, 0x40 P V
+ * done, 0x80 V stage free, 0x100 V stage full, 0x200 scales; with many: 0x1 K stage free, 0x2
+ * V stage free, 0x4 K stage full, 0x8 V stage full, 0x10 scales, 0x20 queries staged, 0x40 S
+ * ready, 0x80 P ready, 0x100 S read, 0x200 fp16 V free, 0x400 fp16 V full, 0x800 P V done).
  * Synchronises `stream` first. */
 herald_status herald_workspace_error(void *ws, void *stream, uint32_t *code);
 

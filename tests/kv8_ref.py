@@ -119,7 +119,7 @@ def attention(q, cache, lengths, bk=None, bv=None, scale=None):
     N, B, Hq, d = q.shape
     G = Hq // cache.Hkv
     scale = 1 / np.sqrt(d) if scale is None else scale
-    qs = 2.0 ** (-21 if B * G <= 32 else -17)
+    qs = 2.0 ** (-21 if B * G <= 16 else -17)
     qf = f64(q)
     out = np.zeros((N, B, Hq, d))
     tol = np.zeros_like(out)
