@@ -931,6 +931,13 @@ herald_status herald_kv8_attn(herald_dims dims, const uint16_t* q, const herald_
   }
   if (!(scale >= 0.f && scale <= 0x1p127f))  // (times log2(e) it has to be finite)
     return fail(HERALD_ERR_INVALID_ARG, "scale=%g outside [0, 2^127]", double(scale));
+  // (the join reads queries and block keys of rows that its other CTAs may have written)
+  const int64_t toks = int64_t(dims.N) * dims.B, qw = int64_t(dims.Hq) * dims.d,
+                kw = int64_t(dims.Hkv) * dims.d;
+  const Span o = rows_span(out, toks, qw, qw);
+  if (overlap(o, rows_span(q, toks, qw, qw)) || overlap(o, rows_span(block_k, toks, kw, kw)) ||
+      overlap(o, rows_span(block_v, toks, kw, kw)))
+    return fail(HERALD_ERR_INVALID_ARG, "out may not lie over q, block_k or block_v");
   const size_t need = kv8_attn_workspace(dims);
   if (ws_bytes < need)
     return fail(HERALD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);

@@ -9,7 +9,12 @@
 
 namespace herald {
 
-// What a piece costs beside its tiles, in tiles (kv4_units).
+// What a piece costs beside its tiles, in tiles (kv4_units): its first scores, its first base
+// and its partials.  Few rows, with 0 / 1 / 2 / 3 / 4: 64 ragged sequences of up to 8K tokens
+// 97.5 / 95.2 / 94.6 / 93.7 / 94.3 us, 16 of them with 4 tokens each 35.4 / 29.7 / 27.0 / 26.1 /
+// 25.9, one of 128K (whose pieces are long) 46.3 / 46.0 / 46.0 / 46.8 / 47.1.  Many, with 5 / 7 / 9 /
+// 11: seven ragged drafts of 35 rows 23.2 / 21.9 / 22.5 / 22.7, a block of 224 rows over 32K 25.9 /
+// 25.5 / 25.5 / 26.2.
 constexpr int kKv8PadRows = 3, kKv8PadTc = 7;
 constexpr int kKv8MaxCtas = 304;  // most attention CTAs (workspace slots)
 
@@ -150,6 +155,7 @@ HERALD_DEV void own_keys(const Kv8AttnArgs& a, OwnKeys<D>& sm, int n, int g, int
 // grid-dependency wait: they and the lengths were written before the attention
 // kernel's own wait ended, and it lets this kernel start only after that.  Few of them
 // (not Tc) are taken one after another by the row's lanes, every load first.
+// (64 sequences of one token: 105 us by lanes and 110 by products, when the whole took that.)
 constexpr int kOwnFew = 4;  // block keys at most that the lanes take
 template <int D, int Rows, int Per, int GR, bool Tc>
 __global__ void __launch_bounds__(D / 4 * Rows / Per * GR, Tc && GR == 1 ? 2 : 1)
@@ -309,6 +315,13 @@ static cudaError_t launch_join(const Kv8AttnArgs& a, int R, int num_sms, cudaStr
     return launch_k("kv8_join_kernel", kernel, dim3(unsigned(a.N * a.Hkv), unsigned(cdiv(R, rows))),
                     dim3(unsigned(threads)), 0, st, a);
   };
+  // Few rows a CTA and its groups of threads side by side on the pieces, as long as every CTA
+  // is resident at once; many CTAs in a row would each pay for the pieces' place and the block's
+  // keys.  The whole call in us, without products (4 rows in 4 groups / 8 in one): one segment of
+  // 2K keys 7.0 / 7.8, eight of 128K 47.2 / 48.3, 512 of up to 8K 97.2 / 93.7, 128 with 16 rows
+  // 29.0 / 26.4.  With products (4 rows in 4 groups / 8 in two / 16 in one): 8 segments of 20 rows
+  // 15.3 / 15.5 / 18.0, 32 of 32 rows 19.8 / 17.1 / 17.0, 4 of 224 rows 28.4 / 25.8 / 28.5, 32 of
+  // 128 rows 131 / 121 / 112.
   const int64_t segs = int64_t(a.N) * a.Hkv;
   if (!a.bk || a.B <= kOwnFew) {
     if (segs * cdiv(R, 4) <= num_sms) return go(kv8_join_kernel<D, 4, 1, 4, false>, 4, D * 4);
@@ -338,8 +351,8 @@ static Kv8Ws kv8_ws(const herald_dims& dm) {
 size_t kv8_attn_workspace(const herald_dims& dm) { return kv8_ws(dm).total; }
 
 cudaError_t launch_kv8_attn(const herald_dims& dm, const uint16_t* q, const Kv8Dev& c,
-                            const CUtensorMap& kmap, const CUtensorMap& vmap, const int32_t* ctx, const uint16_t* bk, const uint16_t* bv,
-                            uint16_t* out, float scale, void* ws, int num_sms, cudaStream_t st) {
+                            const CUtensorMap& kmap, const CUtensorMap& vmap, const int32_t* ctx,
+                            const uint16_t* bk, const uint16_t* bv, uint16_t* out, float scale, void* ws, int num_sms, cudaStream_t st) {
   const int G = dm.Hq / dm.Hkv, R = dm.B * G;
   const Kv8Ws w = kv8_ws(dm);
   char* p = static_cast<char*>(ws);
@@ -348,7 +361,8 @@ cudaError_t launch_kv8_attn(const herald_dims& dm, const uint16_t* q, const Kv8D
   a.ml = reinterpret_cast<float2*>(p + w.ml);
   a.opart = reinterpret_cast<float*>(p + w.opart);
   a.scale = scale * 1.4426950408889634f;
-  a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max, a.R16 = w.R16, a.row_tiles = w.row_tiles;
+  a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max;
+  a.R16 = w.R16, a.row_tiles = w.row_tiles;
   a.c = c;
   a.ctas = std::min(kKv8MaxCtas, num_sms);
   a.pad = R <= kKv8FewRows ? kKv8PadRows : kKv8PadTc;

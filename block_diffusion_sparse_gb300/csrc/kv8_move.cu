@@ -9,6 +9,12 @@
 
 namespace herald {
 
+// All three are bound by memory where there is much to do and by one launch and a chain of
+// dependent loads where there is not.  Measured (per call in a graph, 32 + 2 x 8 heads of 128
+// channels): append of ragged prompts, 4 x <= 4096 tokens, interleaved, 35.7 us for 222 MB (93%
+// of the copy rate); of 64 tokens 3.7; of 32 tokens with block means 8.4, two launches; gather
+// of 4096 rows of 32 heads 8.6 us from L2 (11.8 from DRAM) for 51 MB, of a pool of 4 x 1344 rows
+// 2.0.
 constexpr int kKv8MoveThreads = 256;
 // Query heads of an item: they share a lane's angles, and their loads are in flight
 // together.  Prompts of 4 x 4096 tokens, 32 + 2 x 8 heads, with 2 / 4 / 8: 74 / 63 / 61 us;
@@ -435,6 +441,10 @@ cudaError_t launch_kv8_gather(const herald_dims& dm, const int32_t* idx, const i
                               int P_max, const Kv8Dev& c, uint16_t* pk, uint16_t* pv, int num_sms,
                               cudaStream_t st) {
   const int rpc = kKv8MoveThreads / (dm.d / 8), segs = dm.N * dm.Hkv;
+  // Two rows a thread, all their loads out before any is converted, where that still leaves
+  // four CTAs for every SM.  With one and two, in us: 4096 candidate keys of 8, 16 and 32 heads (2048
+  // to 8192 CTAs of one row a thread) 3.9 / 6.2 / 11.1 and 3.6 / 5.2 / 8.9; pools of 1344 rows of
+  // 4, 16, 32 and 64 heads (336 to 5376 CTAs) 2.3 / 3.7 / 5.7 / 9.7 and 2.4 / 4.1 / 5.4 / 8.9.
   const bool many = int64_t(segs) * cdiv(P_max, rpc) > int64_t(num_sms) * 8;
   const dim3 grid(unsigned(cdiv(P_max, many ? 2 * rpc : rpc)), unsigned(segs));
   auto* kernel = dm.d == 128 ? (many ? kv8_gather_kernel<128, 2> : kv8_gather_kernel<128, 1>)

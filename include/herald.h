@@ -640,7 +640,14 @@ herald_status herald_kv8_append(herald_dims dims, int T, const int32_t *n_tok, c
 
 /* Full attention of a block's queries over a paged 8-bit cache, and where given
  * the block's own B keys in bf16: herald_kv4_attn with a herald_kv8.
- *   ws       herald_workspace_size_kv8(dims) bytes (0 = unsupported shape) */
+ *   out      may not lie, even in part, over q, block_k or block_v
+ *   ws       herald_workspace_size_kv8(dims) bytes (0 = unsupported shape)
+ * Scores, sums and partial outputs are fp32.  A query value enters as the sum of
+ * two e4m3 numbers times its row's power of two (off by at most 2^-17 of the row's
+ * largest value, 2^-21 with up to 16 query rows per KV head), a weight over the
+ * cache as one fp16 number (with up to 16 rows four e4m3 ones), a weight over the
+ * block's own keys as an fp32 or the sum of two bf16 numbers, and the output is
+ * rounded to bf16. */
 size_t herald_workspace_size_kv8(herald_dims dims);
 herald_status herald_kv8_attn(herald_dims dims, const uint16_t *q, const herald_kv8 *cache,
                               const int32_t *ctx_len, const uint16_t *block_k,
@@ -665,7 +672,7 @@ herald_status herald_kv8_gather(herald_dims dims, const int32_t *idx, const int3
  * first 4 bytes are the error word). */
 herald_status herald_selftest_wait_timeout(uint64_t limit_ns, void *ws, void *stream);
 
-/* The same for the waits of herald_kv4_attn, which are bounded by a count of
+/* The same for the waits of herald_kv4_attn and herald_kv8_attn, which are bounded by a count of
  * tries of about 4 us instead of a timer: one warp waits on a completed barrier,
  * then `tries` tries (1 to 250000, the kernels' own count) on one that nothing
  * completes; herald_workspace_error() then reads 0x20a01 (a copy wait of

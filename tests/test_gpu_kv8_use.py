@@ -244,6 +244,22 @@ def test_attention_of_many_sequences(case):
         check(got, want, tol, f"{case}, block {b}")
 
 
+@pytest.mark.parametrize("case", [(300, 8, 4, 64, 1, 16, 420), (250, 16, 4, 128, 4, 32, 300),
+                                  (200, 24, 4, 128, 5, 64, 260), (300, 4, 4, 128, 2, 16, 140)], ids=str)
+def test_attention_of_many_short_pieces(case):
+    """Many segments a CTA, of one, two and three tiles and of none, one after another: each
+    begins and ends on either of the kernel's streams."""
+    N, Hq, Hkv, d, B, page, top = case
+    rng = np.random.default_rng(N + 1)
+    lengths = [int(x) for x in rng.integers(0, top, N)]
+    for i in range(0, N, 7):
+        lengths[i] = (0, 1, 128, 129, 256)[i // 7 % 5] % (top + 1)
+    c = make_cache(rng, N, Hkv, d, page, 16, lengths)
+    q = kv4_ref.bf16(rng.standard_normal((N, B, Hq, d)))
+    want, tol = ref.attention(q, c, lengths)
+    check(run_attn(c, q, lengths, B, max(lengths)), want, tol, f"{case}")
+
+
 def test_offsets_past_32_bits():
     """Pages at the end of arrays of more than 2^32 bytes: append, attention with
     few and with many rows, gather."""

@@ -91,7 +91,8 @@ def test_refused_caches(bad, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
     (dict(ws_bytes=1000), 3), (dict(bk=None), 1), (dict(bv=None), 1), (dict(q=0x6002), 1),
-    (dict(out=None), 1), (dict(bk=0x7008), 1), (dict(d=dims(d=96)), 2), (dict(d=dims(B=65)), 2),
+    (dict(out=None), 1), (dict(out=0x6000), 1), (dict(out=0x6ff0), 1), (dict(out=0x7000), 1),
+    (dict(out=0x8010), 1), (dict(bk=0x7008), 1), (dict(d=dims(d=96)), 2), (dict(d=dims(B=65)), 2),
     (dict(d=dims(N=32768)), 2), (dict(d=dims(L_max=(1 << 30) + 1, N=1, Hkv=1)), 2)], ids=str)
 def test_refused_attention(kw, status):
     with pytest.raises(H.HeraldError) as e:
