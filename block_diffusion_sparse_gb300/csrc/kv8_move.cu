@@ -252,21 +252,25 @@ __global__ void __launch_bounds__(kKv8MoveThreads, Interleaved ? 4 : 3)
   }
   if (pos0 < L0 && e > old) {  // older rows under the larger scale
     const float down = exp2_int(old - e);
-#pragma unroll 1
+    uint2 w[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      if (row0 + p * RPP < L0)
+        w[p] = *reinterpret_cast<const uint2*>(codes + size_t(row0 + p * RPP - pos0) * D);
+#pragma unroll
     for (int p = 0; p < P; ++p) {
       const int pos = row0 + p * RPP;
-      if (pos >= L0) break;
-      uint2* at = reinterpret_cast<uint2*>(codes + size_t(pos - pos0) * D);
-      const uint2 w = *at;
+      if (pos >= L0) continue;
       uint32_t h[4], o[4];
-      e4m3x4_to_half2(w.x, h[0], h[1]);
-      e4m3x4_to_half2(w.y, h[2], h[3]);
+      e4m3x4_to_half2(w[p].x, h[0], h[1]);
+      e4m3x4_to_half2(w[p].y, h[2], h[3]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
         o[j] = float2_to_e4m3(f.x * down, f.y * down);
       }
-      *at = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+      *reinterpret_cast<uint2*>(codes + size_t(pos - pos0) * D) =
+          make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
     }
   }
   if (sub == 0 && lane == 0) (is_v ? a.c.vs : a.c.ks)[scale_at] = uint8_t(e + 127);
@@ -305,17 +309,32 @@ __global__ void __launch_bounds__(kKv8MoveThreads)
   const int r0 = b * Bk, r1 = min(end, r0 + min(Bk, L_max - r0));
   const int ch = threadIdx.x % LPR, rr = threadIdx.x / LPR;
   float acc[8] = {};
-  for (int r = r0 + rr; r < r1; r += RPC) {
-    const int phys = kv8_page(c, n, r >> c.page_log2);
-    if (phys < 0) {
-      debug_flag(true, DEV_BAD_INDEX);
-      continue;
-    }
-    const uint2 w = *reinterpret_cast<const uint2*>(c.kc + kv8_row(c, phys, Hkv, g, r) * D + ch * 8);
-    float x[8];
-    held8(w, exp2_int(kv8_exp(c.ks[kv8_scale(c, phys, Hkv, g, r)])), x);
+  constexpr int F = 4;  // rows in flight
+  for (int r = r0 + rr; r < r1; r += F * RPC) {
+    int phys[F];
+    uint2 w[F];
+    uint32_t s[F];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += x[i];
+    for (int j = 0; j < F; ++j) {
+      const int rj = r + j * RPC;
+      phys[j] = rj < r1 ? kv8_page(c, n, rj >> c.page_log2) : -1;
+      debug_flag(rj < r1 && phys[j] < 0, DEV_BAD_INDEX);
+    }
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+      if (phys[j] >= 0) {
+        const int rj = r + j * RPC;
+        w[j] = *reinterpret_cast<const uint2*>(c.kc + kv8_row(c, phys[j], Hkv, g, rj) * D + ch * 8);
+        s[j] = c.ks[kv8_scale(c, phys[j], Hkv, g, rj)];
+      }
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+      if (phys[j] >= 0) {
+        float x[8];
+        held8(w[j], exp2_int(kv8_exp(s[j])), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += x[i];
+      }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) sums[rr][ch * 8 + i] = acc[i];
