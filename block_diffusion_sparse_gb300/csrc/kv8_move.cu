@@ -12,7 +12,7 @@ namespace herald {
 // All three are bound by memory where there is much to do and by one launch and a chain of
 // dependent loads where there is not.  Measured (per call in a graph, 32 + 2 x 8 heads of 128
 // channels): append of ragged prompts, 4 x <= 4096 tokens, interleaved, 35.7 us for 222 MB (93%
-// of the copy rate); of 64 tokens 3.7; of 32 tokens with block means 8.4, two launches; gather
+// of the copy rate); of 64 tokens 3.7; of 32 tokens with block means 7.6, two launches; gather
 // of 4096 rows of 32 heads 8.6 us from L2 (11.8 from DRAM) for 51 MB, of a pool of 4 x 1344 rows
 // 2.0.
 constexpr int kKv8MoveThreads = 256;
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kKv8MoveThreads, Interleaved ? 4 : 3)
     }
   }
   if (!is_v && a.rot) {
+    // (the angles of a row ahead would spill: 37.2 us for the prompts instead of 35.8)
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int pos = row0 + p * RPP;
