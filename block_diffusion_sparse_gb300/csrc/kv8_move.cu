@@ -13,8 +13,8 @@ namespace herald {
 // dependent loads where there is not.  Measured (per call in a graph, 32 + 2 x 8 heads of 128
 // channels): append of ragged prompts, 4 x <= 4096 tokens, interleaved, 35.7 us for 222 MB (93%
 // of the copy rate); of 64 tokens 3.7; of 32 tokens with block means 7.6, two launches; gather
-// of 4096 rows of 32 heads 8.6 us from L2 (11.8 from DRAM) for 51 MB, of a pool of 4 x 1344 rows
-// 2.0.
+// of 4096 rows of 32 heads 6.9 us from L2 (11.2 from DRAM) for 51 MB (with 8 channels a lane,
+// and so twice the indexes, pages, scales and addresses, 8.9), of a pool of 4 x 1344 rows 2.0.
 constexpr int kKv8MoveThreads = 256;
 // Query heads of an item: they share a lane's angles, and their loads are in flight
 // together.  Prompts of 4 x 4096 tokens, 32 + 2 x 8 heads, with 2 / 4 / 8: 74 / 63 / 61 us;
@@ -349,14 +349,26 @@ __global__ void __launch_bounds__(kKv8MoveThreads)
     pooled[(size_t(seg) * nb_max + b) * D + e] = sums[0][e] / float(r1 - r0);
 }
 
-// grid (row groups, N*Hkv): D/8 lanes per row, eight channels each (8 bytes in, 16 out),
+// 32 bytes of a lane, at once where the array allows it.
+HERALD_DEV void store32(uint16_t* p, const uint32_t (&x)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(p + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// grid (row groups, N*Hkv): D/16 lanes per row, 16 channels each (16 bytes in, 32 out),
 // Rows rows a thread.
 template <int D, int Rows>
 __global__ void __launch_bounds__(kKv8MoveThreads)
     kv8_gather_kernel(const Kv8Dev c, const int32_t* __restrict__ idx,
                       const int32_t* __restrict__ n_sel, int P_max, int Hkv, int L_max,
                       uint16_t* __restrict__ pk, uint16_t* __restrict__ pv) {
-  constexpr int LPR = D / 8, RPC = kKv8MoveThreads / LPR;
+  constexpr int LPR = D / 16, RPC = kKv8MoveThreads / LPR;
   griddep_enter();
   const int seg = blockIdx.y, n = seg / Hkv, g = seg - n * Hkv;
   const int ch = threadIdx.x % LPR, r0 = blockIdx.x * (RPC * Rows) + threadIdx.x / LPR;
@@ -374,16 +386,16 @@ __global__ void __launch_bounds__(kKv8MoveThreads)
     phys[i] = pos[i] >= 0 && pos[i] < L_max ? kv8_page(c, n, pos[i] >> c.page_log2) : -1;
     debug_flag(r0 + i * RPC < min(ns, P_max) && phys[i] < 0, DEV_BAD_INDEX);  // outside the cache
   }
-  uint2 w[2][Rows];
+  uint4 w[2][Rows];
   uint32_t s[2][Rows];
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
     for (int i = 0; i < Rows; ++i) {
-      w[kv][i] = make_uint2(0, 0), s[kv][i] = 0;
+      w[kv][i] = make_uint4(0, 0, 0, 0), s[kv][i] = 0;
       if (phys[i] >= 0 && (kv == 0 || pv)) {
-        w[kv][i] = *reinterpret_cast<const uint2*>(
-            (kv ? c.vc : c.kc) + kv8_row(c, phys[i], Hkv, g, pos[i]) * D + ch * 8);
+        w[kv][i] = *reinterpret_cast<const uint4*>(
+            (kv ? c.vc : c.kc) + kv8_row(c, phys[i], Hkv, g, pos[i]) * D + ch * 16);
         s[kv][i] = (kv ? c.vs : c.ks)[kv8_scale(c, phys[i], Hkv, g, pos[i])];
       }
     }
@@ -391,15 +403,18 @@ __global__ void __launch_bounds__(kKv8MoveThreads)
   for (int kv = 0; kv < 2; ++kv) {
     uint16_t* out = kv ? pv : pk;
     if (!out) continue;
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;  // (arrays are aligned to 16)
 #pragma unroll
     for (int i = 0; i < Rows; ++i) {
       const int r = r0 + i * RPC;
-      float x[8];
-      held8(w[kv][i], exp2_int(kv8_exp(s[kv][i])), x);
-      if (r < P_max)
-        *reinterpret_cast<uint4*>(out + (size_t(seg) * P_max + r) * D + ch * 8) =
-            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                       pack_bf16(x[6], x[7]));
+      const float f = exp2_int(kv8_exp(s[kv][i]));
+      float x[2][8];
+      held8(make_uint2(w[kv][i].x, w[kv][i].y), f, x[0]);
+      held8(make_uint2(w[kv][i].z, w[kv][i].w), f, x[1]);
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = pack_bf16(x[j / 4][2 * (j % 4)], x[j / 4][2 * (j % 4) + 1]);
+      if (r < P_max) store32(out + (size_t(seg) * P_max + r) * D + ch * 16, o, wide);
     }
   }
 }
@@ -460,12 +475,13 @@ cudaError_t launch_kv8_append(const herald_dims& dm, int T, const int32_t* n_tok
 cudaError_t launch_kv8_gather(const herald_dims& dm, const int32_t* idx, const int32_t* n_sel,
                               int P_max, const Kv8Dev& c, uint16_t* pk, uint16_t* pv, int num_sms,
                               cudaStream_t st) {
-  const int rpc = kKv8MoveThreads / (dm.d / 8), segs = dm.N * dm.Hkv;
-  // Two rows a thread, all their loads out before any is converted, where that still leaves
-  // four CTAs for every SM.  With one and two, in us: 4096 candidate keys of 8, 16 and 32 heads (2048
-  // to 8192 CTAs of one row a thread) 3.9 / 6.2 / 11.1 and 3.6 / 5.2 / 8.9; pools of 1344 rows of
-  // 4, 16, 32 and 64 heads (336 to 5376 CTAs) 2.3 / 3.7 / 5.7 / 9.7 and 2.4 / 4.1 / 5.4 / 8.9.
-  const bool many = int64_t(segs) * cdiv(P_max, rpc) > int64_t(num_sms) * 8;
+  const int rpc = kKv8MoveThreads / (dm.d / 16), segs = dm.N * dm.Hkv;
+  // Two rows a thread, both rows' loads out before one is converted, where only keys are read
+  // and the launch is more than one wave; keys and values are two loads already.  With one and
+  // two, in us: 4096 candidate keys of 8, 16 and 32 heads (1024 to 4096 CTAs of one row a thread)
+  // 3.4 / 4.7 / 7.7 and 3.3 / 4.4 / 6.9; pools of 1344 keys and values of 4, 32 and 64 heads 2.4 /
+  // 5.0 / 8.1 and 2.5 / 5.1 / 8.3.
+  const bool many = !pv && int64_t(segs) * cdiv(P_max, rpc) > int64_t(num_sms) * 8;
   const dim3 grid(unsigned(cdiv(P_max, many ? 2 * rpc : rpc)), unsigned(segs));
   auto* kernel = dm.d == 128 ? (many ? kv8_gather_kernel<128, 2> : kv8_gather_kernel<128, 1>)
                              : (many ? kv8_gather_kernel<64, 2> : kv8_gather_kernel<64, 1>);

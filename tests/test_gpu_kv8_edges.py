@@ -8,7 +8,8 @@ import pytest
 
 import kv4_ref
 import kv8_ref as ref
-from test_gpu_kv8 import check, make_cache, run_attn
+from helpers import dev
+from test_gpu_kv8 import OnGpu, _h, bits, check, make_cache, run_attn
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -90,3 +91,33 @@ def test_one_sequence_of_every_length(B):
         q = kv4_ref.bf16(rng.standard_normal((1, B, 4, 128)))
         want, tol = ref.attention(q, c, [L])
         check(run_attn(c, q, [L], B, L), want, tol, f"length {L}")
+
+
+@pytest.mark.parametrize("d,P,values,shift", [(128, 5003, False, 0), (64, 9001, False, 8), (128, 77, True, 8),
+                                              (64, 33, True, 16)])
+def test_gather_layouts(d, P, values, shift):
+    """Launches of more than one wave (two rows a thread), and pools aligned to 16 bytes but not
+    to 32; the whole cache and more: the last rows repeat."""
+    H = _h()
+    rng = np.random.default_rng(P)
+    N, Hkv, page, block = 2, 4, 64, 16
+    lengths = [P - 2, P // 2 + 1]
+    c = make_cache(rng, N, Hkv, d, page, block, lengths)
+    g = OnGpu(c)
+    idx = np.zeros((N, Hkv, P), np.int32)
+    n_sel = np.full((N, Hkv), P, np.int32)
+    for n, L in enumerate(lengths):
+        idx[n] = np.minimum(np.arange(P), L - 1)
+    n_sel[1, 1] = P // 3
+    pools = []
+    for _ in range(2):
+        flat = torch.full((N * Hkv * P * d + shift,), 7, dtype=torch.int16, device="cuda")
+        pools.append(flat[shift:].view(N, Hkv, P, d))
+    H.herald_kv8_gather(H.dims(N, Hkv, Hkv, d, 1, P), dev(idx), dev(n_sel), P, g.kv8, pools[0],
+                        pools[1] if values else None)
+    for i in range(2 if values else 1):
+        want = np.stack([c.rows(i, n, idx[n, 0]) for n in range(N)])
+        want[1, 1, P // 3:] = 0
+        assert np.array_equal(kv4_ref.f64(bits(pools[i])), want)
+    if not values:
+        assert (pools[1] == 7).all()
