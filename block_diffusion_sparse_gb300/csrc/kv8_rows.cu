@@ -25,7 +25,7 @@
 //   warps 9, 10  copy tiles of keys and of values into a ring each, and look up pages and
 //              scales, four tiles of them (32 lanes: 8 groups of 16 keys each) ahead.  A tile's
 //              keys leave after its scores; its values wait for the weights, some tiles longer
-//   warp 11    stages the queries of the next piece
+//   warp 11    stages the queries of the next piece (the first piece's: the softmax warps)
 // A row's exponent base m is set 4 below its largest exponent and stays while no p passes
 // 2^8; a stream's four warps vote on that in one barrier a tile.  Else the tile's row maxima
 // are exchanged, O is scaled once the products before it are done, and l follows.
@@ -163,6 +163,62 @@ HERALD_DEV float warp_rows(float (&v)[N], Op&& op) {
   return v[0];
 }
 
+// Queries of a piece: D/8 lanes hold a row, eight channels each; a warp takes passes of
+// 32 / (D/8) rows.
+template <int D>
+struct Kv8Query {
+  static constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // of a row, of a pass
+  static constexpr int passes(int rows) { return rows / kRows; }
+  uint4 x;
+  HERALD_DEV void load(const Kv8AttnArgs& a, int n, int g, int pass, int lane) {
+    const int G = a.Hq / a.Hkv, r = pass * kRows + lane / kLanes;
+    x = make_uint4(0, 0, 0, 0);
+    if (r < a.B * G)
+      x = *reinterpret_cast<const uint4*>(
+          a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + lane % kLanes * 8);
+  }
+};
+// Passes pass0 to pass0 + P as operands and their score factors.
+template <int D, int RP, int P>
+HERALD_DEV void stage_queries(const Kv8Query<D> (&q)[P], int pass0, int lane, float scale,
+                              uint8_t* dst, float* row_f) {
+  constexpr int LPR = Kv8Query<D>::kLanes;
+  const int c = lane % LPR;
+  float mx[P];  // (the rows' maxima side by side: their steps wait on one another)
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const uint4& x = q[p].x;
+    const uint32_t m = max_bf16x2_abs(
+        max_bf16x2_abs(max_bf16x2_abs(max_bf16x2_abs(0, x.x), x.y), x.z), x.w);
+    mx[p] = fmaxf(bf16lo(m), bf16hi(m));
+  }
+#pragma unroll
+  for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+    for (int p = 0; p < P; ++p) mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], o));
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const uint32_t r = uint32_t((pass0 + p) * Kv8Query<D>::kRows + lane / LPR);
+    const uint32_t half = uint32_t(c & 1) * 8u;
+    float up, f;
+    kv8_query_scale(mx[p], scale, &up, &f);
+    const uint32_t w[4] = {q[p].x.x, q[p].x.y, q[p].x.z, q[p].x.w};
+    uint32_t v0[4], v1[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = pack_half2(bf16lo(w[i]) * up, bf16hi(w[i]) * up);
+      v0[i] = half2_to_e4m3(h);
+      const uint32_t rest = hsub2(h, e4m3x2_to_half2(v0[i]));  // what q0 left, times 16
+      v1[i] = half2_to_e4m3(hmul2(rest, 0x4C004C00u));
+    }
+    *reinterpret_cast<uint2*>(dst + rows_off<D>(r, uint32_t(c >> 1)) + half) =
+        make_uint2(v0[0] | v0[1] << 16, v0[2] | v0[3] << 16);
+    *reinterpret_cast<uint2*>(dst + rows_off<D>(uint32_t(RP) + r, uint32_t(c >> 1)) + half) =
+        make_uint2(v1[0] | v1[1] << 16, v1[2] | v1[3] << 16);
+    if (c == 0) row_f[r] = f;
+  }
+}
+
 template <int D, int RP>
 __global__ void __launch_bounds__(kKv8RowsThreads, 1)
     kv8_rows_kernel(const Kv8AttnArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -177,7 +233,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
   __shared__ Kv8Share share;
   __shared__ Kv8Meta meta[MB][8];
   __shared__ __align__(16) float row_f[2][RP];  // score factors of the rows
-  __shared__ float red[2][4][RP];               // row maxima of a stream's warps
+  __shared__ __align__(16) float red[2][4][RP];  // row maxima of a stream's warps
   // a piece's bases and the warps' sums of both streams
   __shared__ __align__(16) float row_m[2][RP];
   __shared__ float row_l[2][4][RP];
@@ -220,9 +276,19 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
     const int w = warp >> 2, wq = warp & 3, key = int(threadIdx.x) & 127;  // stream, quarter, key
     const uint32_t lanes = uint32_t(wq * 32) << 16, tow = to + lanes + uint32_t(w) * NO;
     uint32_t t0 = 0, np = 0;  // tiles and pieces of the CTA
-    kv8_pieces(a, share, [&](int n, int, int seg, int ctx, int u0, int u1) -> bool {
+    kv8_pieces(a, share, [&](int n, int g, int seg, int ctx, int u0, int u1) -> bool {
       debug_flag(threadIdx.x == 0 && a.ctx[n] != ctx, DEV_BAD_COUNT);
       const uint32_t qb = np & 1;
+      if (np == 0) {  // a pass for each warp: one warp alone takes 4,300 cycles for 16 rows
+        if (warp < Kv8Query<D>::passes(RP)) {
+          Kv8Query<D> x[1];
+          x[0].load(a, n, g, warp, lane);
+          stage_queries<D, RP, 1>(x, warp, lane, a.scale, Qs, row_f[0]);
+          fence_proxy_async_smem();
+        }
+        both_bar();
+        if (threadIdx.x == 0) mbar_arrive(&q_full[0]);
+      }
       await(&q_full[qb], (np >> 1) & 1, W8_Q_FULL);
       float f[RP], m[RP], l[RP];
 #pragma unroll
@@ -271,9 +337,18 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
           soft_bar(w);
           float k[RP];
 #pragma unroll
+          for (int r = 0; r < RP; r += 4) {
+            float4 x = *reinterpret_cast<const float4*>(&red[w][0][r]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+              const float4 y = *reinterpret_cast<const float4*>(&red[w][i][r]);
+              x.x = fmaxf(x.x, y.x), x.y = fmaxf(x.y, y.y), x.z = fmaxf(x.z, y.z), x.w = fmaxf(x.w, y.w);
+            }
+            k[r] = x.x, k[r + 1] = x.y, k[r + 2] = x.z, k[r + 3] = x.w;
+          }
+#pragma unroll
           for (int r = 0; r < RP; ++r) {
-            const float z = fmaxf(fmaxf(red[w][0][r], red[w][1][r]), fmaxf(red[w][2][r], red[w][3][r]));
-            const float m1 = fmaxf(__fadd_rd(z, -kKv8At), m[r]);
+            const float m1 = fmaxf(__fadd_rd(k[r], -kKv8At), m[r]);
             k[r] = fast_exp2(m[r] - m1);
             m[r] = m1;
             l[r] *= k[r];
@@ -340,19 +415,37 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
       // (with d = 64 an M = 64 product's rows lie in the first 16 lanes of each warp's 32)
       const int ch = D == 128 ? key : wq * 16 + lane;
       constexpr int RH = RP / 2;
-      float x[2][RH];
+      float w0[RH], w1[RH];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int r = 0; r < RH; r += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&row_m[0][w * RH + r]);
+        const float4 y = *reinterpret_cast<const float4*>(&row_m[1][w * RH + r]);
+        const float m0[4] = {x.x, x.y, x.z, x.w}, m1[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int r = 0; r < RH; ++r) x[h][r] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const float mm = fmaxf(m0[i], m1[i]);
+          w0[r + i] = fast_exp2(m0[i] - mm), w1[r + i] = fast_exp2(m1[i] - mm);
+        }
+      }
+      float x[RH] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
         if (two || (t0 & 1) == uint32_t(h)) {
           uint32_t o[4][RH];
           tmem_ld_parts(to + lanes + uint32_t(h * NO + w * RH), RP, o);
 #pragma unroll
-          for (int i = kKv8Parts - 1; i >= 0; --i)
+          for (int r = 0; r < RH; ++r) {
+            float y = 0.f;
 #pragma unroll
-            for (int r = 0; r < RH; ++r) x[h][r] = fmaf(x[h][r], 0.0625f, __uint_as_float(o[i][r]));
+            for (int i = kKv8Parts - 1; i >= 0; --i) y = fmaf(y, 0.0625f, __uint_as_float(o[i][r]));
+            x[r] = fmaf(y, h ? w1[r] : w0[r], x[r]);
+          }
         }
+      if (D == 128 || lane < 16) {
+        float* dst = a.opart + (slot * a.R16 + w * RH) * D + ch;
+#pragma unroll
+        for (int r = 0; r < RH; ++r)
+          if (w * RH + r < R) dst[r * D] = x[r];
       }
       if (key < RH && w * RH + key < R) {
         const int row = w * RH + key;
@@ -362,14 +455,6 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         for (int i = 0; i < 4; ++i) l0 += row_l[0][i][row], l1 += row_l[1][i][row];
         a.ml[slot * a.R16 + row] =
             make_float2(mm, fast_exp2(m0 - mm) * l0 + fast_exp2(m1 - mm) * l1);
-      }
-#pragma unroll
-      for (int r = 0; r < RH; ++r) {
-        const int row = w * RH + r;
-        const float m0 = row_m[0][row], m1 = row_m[1][row], mm = fmaxf(m0, m1);
-        if (row < R && (D == 128 || lane < 16))
-          a.opart[(slot * a.R16 + row) * D + ch] =
-              fmaf(x[0][r], fast_exp2(m0 - mm), x[1][r] * fast_exp2(m1 - mm));
       }
       tc_fence_before();
       both_bar();  // (O, the sums and maxima have been read)
@@ -506,56 +591,20 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- queries
-    constexpr int LPR = D / 8, RPP = 32 / LPR, P = RP / RPP;
-    const int c = lane % LPR, sub = lane / LPR;
     uint32_t np = 0;
     kv8_pieces(a, share, [&](int n, int g, int, int, int, int) -> bool {
-      const uint32_t qb = np & 1;
-      uint4 x[P];
+      if (np >= 1) {
+        const uint32_t qb = np & 1;
+        constexpr int P = Kv8Query<D>::passes(RP);
+        Kv8Query<D> x[P];
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int r = p * RPP + sub;
-        x[p] = make_uint4(0, 0, 0, 0);
-        if (r < R)
-          x[p] = *reinterpret_cast<const uint4*>(
-              a.q + ((size_t(n) * a.B + r / G) * a.Hq + g * G + r % G) * D + c * 8);
+        for (int p = 0; p < P; ++p) x[p].load(a, n, g, p, lane);
+        if (np >= 2 && !wait(&q_free[qb], ((np >> 1) - 1) & 1, W8_Q_FREE)) return false;
+        stage_queries<D, RP, P>(x, 0, lane, a.scale, Qs + qb * S::kQ, row_f[qb]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[qb]);
       }
-      if (np >= 2 && !wait(&q_free[qb], ((np >> 1) - 1) & 1, W8_Q_FREE)) return false;
-      float mx[P];  // (the rows' maxima side by side: their steps wait on one another)
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const uint32_t m = max_bf16x2_abs(
-            max_bf16x2_abs(max_bf16x2_abs(max_bf16x2_abs(0, x[p].x), x[p].y), x[p].z), x[p].w);
-        mx[p] = fmaxf(bf16lo(m), bf16hi(m));
-      }
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1)
-#pragma unroll
-        for (int p = 0; p < P; ++p) mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], o));
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const uint32_t r = uint32_t(p * RPP + sub), half = uint32_t(c & 1) * 8u;
-        float up, f;
-        kv8_query_scale(mx[p], a.scale, &up, &f);
-        const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-        uint32_t v0[4], v1[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t h = pack_half2(bf16lo(w[i]) * up, bf16hi(w[i]) * up);
-          v0[i] = half2_to_e4m3(h);
-          const uint32_t rest = hsub2(h, e4m3x2_to_half2(v0[i]));  // what q0 left, times 16
-          v1[i] = half2_to_e4m3(hmul2(rest, 0x4C004C00u));
-        }
-        uint8_t* dst = Qs + qb * S::kQ;
-        *reinterpret_cast<uint2*>(dst + rows_off<D>(r, uint32_t(c >> 1)) + half) =
-            make_uint2(v0[0] | v0[1] << 16, v0[2] | v0[3] << 16);
-        *reinterpret_cast<uint2*>(dst + rows_off<D>(uint32_t(RP) + r, uint32_t(c >> 1)) + half) =
-            make_uint2(v1[0] | v1[1] << 16, v1[2] | v1[3] << 16);
-        if (c == 0) row_f[qb][r] = f;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qb]);
       ++np;
       return true;
     });
