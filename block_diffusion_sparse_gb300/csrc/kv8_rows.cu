@@ -31,10 +31,10 @@
 // are exchanged, O is scaled once the products before it are done, and l follows.
 //
 // What bounds it: with up to 8 rows the cache's bytes; 64 ragged sequences of up to 8K tokens
-// 93.4 us for 580 MB (6.2 TB/s, 93% of the copy rate), one of 128K 47.0 us for 268 MB, of which 7
+// 93.4 us for 580 MB (6.2 TB/s, 93% of the copy rate), one of 128K 46.5 us for 268 MB, of which 6
 // are launch, lengths, the first tile and the join.  With 16 rows a tile's softmax (four
 // conversions and their remainders a weight) takes 1,060 cycles, a little more than its copies,
-// and a piece's start and end 3 us: 105 us.  One stream took 121 there: a thread's steps wait on
+// and a piece's start and end 2 to 3 us: 102 us.  One stream took 121 there: a thread's steps wait on
 // one another, and the two streams fill each other's waits.
 #include <float.h>
 
