@@ -90,6 +90,13 @@ HERALD_DEV uint32_t max_bf16x2_abs(uint32_t m, uint32_t w) {
   return d;
 }
 
+// Eight words at once, a whole sector, to an address of 32 bytes' alignment.
+HERALD_DEV void store8(void* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 // ---- attention arguments shared by its kernels
 struct Kv8AttnArgs {
   const uint16_t *q, *bk, *bv;

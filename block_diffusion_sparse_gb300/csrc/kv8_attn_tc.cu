@@ -18,8 +18,8 @@
 //              base m, sum l and O, added up at a piece's end
 //   warps 8-11 turn V tiles into fp16
 //   warp 12    copies K and V tiles by TMA, looks up pages and scales four tiles ahead
-//   warps 13, 14  issue S, one per stream, in steps of 64 keys
-//   warp 15    issues P V, the streams' in turn
+//   warps 13, 14  issue S and P V, one per stream, in steps of 64 keys (warp 15 idles: registers
+//              are dealt by four warps)
 // Tensor memory holds, for each stream, one step's scores (64 columns), its P (32) and O
 // (128), and Q (64): 512.  A step's scores are in registers before anything is done
 // with them, so the next step's product runs beside its softmax.  (With P over the
@@ -33,12 +33,13 @@
 // 60000.  Where a sum does not (and at a piece's first step) the row's largest exponent
 // is looked up, m set 5 below it, O and l follow, and the step is done again.
 //
-// What bounds it: the dependent steps of a stream's warp, some 2,000 cycles a tile (scores
-// from tensor memory 400, exponentials and packing 950, waiting for products 330, P to tensor
-// memory 350); the tensor pipe is active 52% and DRAM 61% of the time.  Four blocks of 32 over
-// 64K tokens each, 32 heads over 8: 111 us for 539 MB; one over 32K, 28 heads over 4, 25.4 us,
+// What bounds it: the dependent steps of a stream's warp, some 1,950 cycles a tile (scores
+// from tensor memory 400, exponentials and packing 950, waiting for products 250, P to tensor
+// memory 350); the tensor pipe is active 53% and DRAM 62% of the time.  Four blocks of 32 over
+// 64K tokens each, 32 heads over 8: 107 us for 539 MB; one over 32K, 28 heads over 4, 24.4 us,
 // half of it phases that do not grow with the keys (share 0.8 us, queries 2.6, first scores 0.6,
-// partials 2.3, join 3).
+// partials 1.5, join 3).  S and P V from one warp a stream, so that a stream waits once a step:
+// 25.2 to 24.9 us for the latter.
 #include <float.h>
 
 #include "kv8.cuh"
@@ -73,7 +74,7 @@ struct Kv8Tc {
   static constexpr uint32_t kTile = 128u * D;          // bytes of 128 keys as held
   static constexpr uint32_t kTile16 = uint32_t(D / 64) * 16384u;  // as fp16
   static constexpr uint32_t kV = kKv8KStages * kTile, kV16 = kV + kKv8VStages * kTile;
-  static constexpr uint32_t kX = kV16 + 2 * kTile16;  // 2 KB for each softmax warp's transposes
+  static constexpr uint32_t kX = kV16 + 2 * kTile16;  // 2 KB for each softmax warp's queries
   static constexpr uint32_t kSmem = kX + 8 * 2048 + 1024;
 };
 // Tensor memory: both streams' scores, P, then q0, q1, both streams' O.
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
   constexpr int KS = kKv8KStages, VS = kKv8VStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full[KS], k_free[KS], v_full[VS], v_free[VS], v16_full[2], v16_free[2],
-      meta_full[kKv8Groups], q_full, s_full[2], s_read[2], p_full[2], o_done[2], all_done[3];
+      meta_full[kKv8Groups], q_full, s_full[2], s_read[2], p_full[2], o_done[2], all_done[2];
   __shared__ uint32_t tmem_base, failed;
   __shared__ Kv8Share share;
   __shared__ __align__(16) Kv8TileMeta meta[kKv8Groups][4];
@@ -186,9 +187,9 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_free[i], 4);
     for (int i = 0; i < kKv8Groups; ++i) mbar_init(&meta_full[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 1), mbar_init(&o_done[i], 1),
+      mbar_init(&v16_full[i], 4), mbar_init(&v16_free[i], 2), mbar_init(&o_done[i], 1),
           mbar_init(&s_full[i], 1), mbar_init(&s_read[i], 4), mbar_init(&p_full[i], 4);
-    for (int i = 0; i < 3; ++i) mbar_init(&all_done[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&all_done[i], 1);
     mbar_init(&q_full, 8);
     failed = 0;
     fence_mbar_init();
@@ -217,12 +218,6 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
     bool lost = false;
     auto await = [&](uint64_t* bar, uint32_t parity, uint32_t which) {
       if (!lost) lost = !wait(bar, parity, which);
-    };
-    auto await2 = [&](uint64_t* x, uint32_t px, uint64_t* y, uint32_t py) {
-      if (lost) return;
-      const bool a0 = mbar_try_wait(x, px), b0 = mbar_try_wait(y, py);  // (both at once)
-      if (__all_sync(0xffffffffu, a0 && b0)) return;
-      lost = !wait(x, px, X8_O_DONE) || !wait(y, py, X8_S_FULL);
     };
     const int w = warp >> 2, lrow = (warp & 3) * 32 + lane;  // stream, TMEM lane
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -348,6 +343,9 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         float k = 1.f;
         bool moved = false;
         if (!idle) {
+          const float4 a4 = *reinterpret_cast<const float4*>(&mt.sk[4 * w]);
+          const float4 b4 = *reinterpret_cast<const float4*>(&mt.ev[4 * w]);
+          const float4 c4 = *reinterpret_cast<const float4*>(&mt.iv[4 * w]);
           if (!mt.whole[0]) {  // keys that do not count
             const uint4 k4 = *reinterpret_cast<const uint4*>(&mt.keys[4 * w]);
             const uint32_t keys[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -357,9 +355,6 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           }
           float fk[4], ev[4], iv[4];  // P = 2^(score fk + ev - m)
           {
-            const float4 a4 = *reinterpret_cast<const float4*>(&mt.sk[4 * w]);
-            const float4 b4 = *reinterpret_cast<const float4*>(&mt.ev[4 * w]);
-            const float4 c4 = *reinterpret_cast<const float4*>(&mt.iv[4 * w]);
             fk[0] = f * a4.x, fk[1] = f * a4.y, fk[2] = f * a4.z, fk[3] = f * a4.w;
             ev[0] = b4.x, ev[1] = b4.y, ev[2] = b4.z, ev[3] = b4.w;
             iv[0] = c4.x, iv[1] = c4.y, iv[2] = c4.z, iv[3] = c4.w;
@@ -414,12 +409,9 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           }
           l += add;
         }
-        // the stream's product before has read P, and is in O (idle warps wait too: no
-        // warp arrives twice in one phase of p_full)
-        // Beside it, the next scores.
-        if (u + 1 < u1 && t > 0)
-          await2(&o_done[w], (t - 1) & 1, &s_full[w], (t + 1) & 1);
-        else if (u + 1 < u1)
+        // the next scores; they come after the stream's product before, which has then read
+        // P, and is in O (idle warps wait too: no warp arrives twice in one phase of p_full)
+        if (u + 1 < u1)
           await(&s_full[w], (t + 1) & 1, X8_S_FULL);
         else if (t > 0)
           await(&o_done[w], (t - 1) & 1, X8_O_DONE);
@@ -435,8 +427,8 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           }
         }
         // the next scores come while P goes
-        if (u + 1 < u1) begin_load();
         if (!idle) tmem_st32(tp, *reinterpret_cast<float(*)[32]>(pk));
+        if (u + 1 < u1) begin_load();
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -456,8 +448,8 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
         const float2 o2 = row_ml[w ^ 1][lrow];
         const float mm = fmaxf(m, o2.x), w0 = fast_exp2(m - mm), w1 = fast_exp2(o2.x - mm);
         if (w == 0 && row < R) a.ml[slot * a.R16 + lrow] = make_float2(mm, w0 * l + w1 * o2.y);
-        // 16 channels at a time through shared memory, so that a row's 64 bytes are written
-        // by neighbouring lanes (a lane writing its own row took 2.8 us a piece)
+        // (a lane writes whole sectors of its own row: 32 bytes an instruction.  With 16 bytes a
+        // piece took 2.8 us longer, through shared memory by neighbouring lanes 1.2.)
 #pragma unroll 1
         for (uint32_t c = 0; c < D / 2; c += 16) {
           uint32_t v[16], p[16];
@@ -465,24 +457,13 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           tmem_ld16_async(to2 + uint32_t(w) * (D / 2) + c, p);
           tmem_ld16_done(v);
           tmem_ld16_done(p);
-          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float4 y;
-            y.x = fmaf(__uint_as_float(p[4 * i]), w1, __uint_as_float(v[4 * i]) * w0);
-            y.y = fmaf(__uint_as_float(p[4 * i + 1]), w1, __uint_as_float(v[4 * i + 1]) * w0);
-            y.z = fmaf(__uint_as_float(p[4 * i + 2]), w1, __uint_as_float(v[4 * i + 2]) * w0);
-            y.w = fmaf(__uint_as_float(p[4 * i + 3]), w1, __uint_as_float(v[4 * i + 3]) * w0);
-            *reinterpret_cast<float4*>(xb + rows_off<64>(uint32_t(lane), uint32_t(i))) = y;
-          }
-          __syncwarp();
+          for (int i = 0; i < 16; ++i)
+            v[i] = __float_as_uint(fmaf(__uint_as_float(p[i]), w1, __uint_as_float(v[i]) * w0));
+          if (row < R) {
+            float* dst = a.opart + (slot * a.R16 + lrow) * D + w * (D / 2) + c;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2), lr = (warp & 3) * 32 + r;
-            if (r0 + lr < R)
-              *reinterpret_cast<float4*>(a.opart + (slot * a.R16 + lr) * D + w * (D / 2) + c +
-                                         (lane & 3) * 4) =
-                  *reinterpret_cast<const float4*>(xb + rows_off<64>(uint32_t(r), uint32_t(lane & 3)));
+            for (int i = 0; i < 16; i += 8) store8(dst + i, v + i);
           }
         }
       }
@@ -634,32 +615,55 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       for (uint32_t i = v_issued > uint32_t(VS) ? v_issued - VS : 0; i < v_issued; ++i)
         mbar_wait(&v_full[i % VS], (i / VS) & 1);
     } else if (warp < 15) {
-      // --------------------------------------------------------- S issuers
+      // ----------------------------------------------------------- issuers
       // (the whole warp walks the loops, an elected lane issues)
       const uint32_t w = uint32_t(warp - 13);
       const uint64_t kd = make_sdesc_rows<D>(smem_u32(base) + w * (64u * D));
+      const uint64_t vd = make_sdesc_sw128(smem_u32(base) + S::kV16 + w * 8192u, 16384u, 1024);
       constexpr uint32_t ids = make_idesc_e4m3(128, 64, false, false);
+      constexpr uint32_t ido = make_idesc_half(128, D, true);
       uint32_t t = 0, np = 0;
       kv8_pieces(a, share, [&](int, int, int, int, int u0, int u1) -> bool {
         if (!wait(&q_full, np & 1, X8_Q_FULL)) return false;
         ++np;
-        for (int u = u0; u < u1; ++u, ++t) {
-          const uint32_t st = t % KS;
-          if (!wait(&k_full[st], (t / KS) & 1, X8_K_FULL)) return false;
-          // the stream's scores of the step before have been read
-          if (t > 0 && !wait(&s_read[w], (t - 1) & 1, X8_S_READ)) return false;
-          tc_fence_after();
-          if (elect_one()) {
+        // S of tile u, then P V of the one before: the next S comes after that, so whoever
+        // has its scores knows that P has been read
+        for (int u = u0; u <= u1; ++u) {
+          if (u < u1) {
+            const uint32_t st = t % KS;
+            if (!wait(&k_full[st], (t / KS) & 1, X8_K_FULL)) return false;
+            // the stream's scores of the step before have been read
+            if (t > 0 && !wait(&s_read[w], (t - 1) & 1, X8_S_READ)) return false;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-              for (int ks = 0; ks < D / 32; ++ks)
-                umma_e4m3_ts(tm + w * 64u, tm + (part ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(ks) * 8u,
-                             kd + ((st * S::kTile + uint32_t(ks) * 32u) >> 4), ids, part + ks > 0);
-            umma_commit(&s_full[w]);
-            umma_commit(&k_free[st]);
+                for (int ks = 0; ks < D / 32; ++ks)
+                  umma_e4m3_ts(tm + w * 64u, tm + (part ? kKv8TmQ1 : kKv8TmQ0) + uint32_t(ks) * 8u,
+                               kd + ((st * S::kTile + uint32_t(ks) * 32u) >> 4), ids, part + ks > 0);
+              umma_commit(&s_full[w]);
+              umma_commit(&k_free[st]);
+            }
+            __syncwarp();
+            ++t;
           }
-          __syncwarp();
+          if (u > u0) {
+            const uint32_t x = u < u1 ? t - 2 : t - 1, vb = x & 1;
+            if (!wait(&v16_full[vb], (x >> 1) & 1, X8_V16_FULL)) return false;
+            if (!wait(&p_full[w], x & 1, X8_P_FULL)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                umma_bf16_ts(tm + kKv8TmO + w * 128u, tm + kKv8TmP + w * 32u + uint32_t(ks) * 8u,
+                             vd + ((vb * S::kTile16) >> 4) + uint32_t(ks) * 128u, ido,
+                             u - 1 > u0 || ks > 0);
+              umma_commit(&o_done[w]);
+              umma_commit(&v16_free[vb]);
+            }
+            __syncwarp();
+          }
         }
         return true;
       });
@@ -667,37 +671,6 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
       if (t > 0 && elect_one()) {
         umma_commit(&all_done[w]);
         mbar_wait(&all_done[w], 0);
-      }
-    } else {
-      // -------------------------------------------------------- P V issuer
-      const uint64_t vd = make_sdesc_sw128(smem_u32(base) + S::kV16, 16384u, 1024);
-      constexpr uint32_t ido = make_idesc_half(128, D, true);
-      uint32_t t = 0;
-      kv8_pieces(a, share, [&](int, int, int, int, int u0, int u1) -> bool {
-        for (int u = u0; u < u1; ++u, ++t) {
-          const uint32_t vb = t & 1;
-          if (!wait(&v16_full[vb], (t >> 1) & 1, X8_V16_FULL)) return false;
-#pragma unroll 1
-          for (uint32_t w = 0; w < 2; ++w) {
-            if (!wait(&p_full[w], t & 1, X8_P_FULL)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                umma_bf16_ts(tm + kKv8TmO + w * 128u, tm + kKv8TmP + w * 32u + uint32_t(ks) * 8u,
-                             vd + ((vb * S::kTile16 + w * 8192u) >> 4) + uint32_t(ks) * 128u, ido,
-                             u > u0 || ks > 0);
-              umma_commit(&o_done[w]);
-              if (w == 1) umma_commit(&v16_free[vb]);
-            }
-            __syncwarp();
-          }
-        }
-        return true;
-      });
-      if (t > 0 && elect_one()) {
-        umma_commit(&all_done[2]);
-        mbar_wait(&all_done[2], 0);
       }
     }
     __syncwarp();

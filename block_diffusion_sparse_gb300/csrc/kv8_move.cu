@@ -349,18 +349,6 @@ __global__ void __launch_bounds__(kKv8MoveThreads)
     pooled[(size_t(seg) * nb_max + b) * D + e] = sums[0][e] / float(r1 - r0);
 }
 
-// 32 bytes of a lane, at once where the array allows it.
-HERALD_DEV void store32(uint16_t* p, const uint32_t (&x)[8], bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
-                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                 : "memory");
-  } else {
-    *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<uint4*>(p + 8) = make_uint4(x[4], x[5], x[6], x[7]);
-  }
-}
-
 // grid (row groups, N*Hkv): D/16 lanes per row, 16 channels each (16 bytes in, 32 out),
 // Rows rows a thread.
 template <int D, int Rows>
@@ -414,7 +402,14 @@ __global__ void __launch_bounds__(kKv8MoveThreads)
       uint32_t o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = pack_bf16(x[j / 4][2 * (j % 4)], x[j / 4][2 * (j % 4) + 1]);
-      if (r < P_max) store32(out + (size_t(seg) * P_max + r) * D + ch * 16, o, wide);
+      if (r >= P_max) continue;
+      uint16_t* dst = out + (size_t(seg) * P_max + r) * D + ch * 16;
+      if (wide) {
+        store8(dst, o);
+      } else {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
   }
 }
