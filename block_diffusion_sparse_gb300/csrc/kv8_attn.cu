@@ -12,9 +12,9 @@ namespace herald {
 // What a piece costs beside its tiles, in tiles (kv4_units): its first scores, its first base
 // and its partials.  Few rows, with 0 / 1 / 2 / 3 / 4: 64 ragged sequences of up to 8K tokens
 // 97.5 / 95.2 / 94.6 / 93.7 / 94.3 us, 16 of them with 4 tokens each 35.4 / 29.7 / 27.0 / 26.1 /
-// 25.9, one of 128K (whose pieces are long) 46.3 / 46.0 / 46.0 / 46.8 / 47.1.  Many, with 5 / 7 / 9 /
-// 11: seven ragged drafts of 35 rows 23.2 / 21.9 / 22.5 / 22.7, a block of 224 rows over 32K 25.9 /
-// 25.5 / 25.5 / 26.2.
+// 25.9, one of 128K (whose pieces are long) 46.3 / 46.0 / 46.0 / 46.8 / 47.1.  Many, with 5 / 6 / 7 /
+// 8: seven ragged drafts of 35 rows 21.0 / 20.7 / 21.0 / 21.6, 16 ragged sequences of 32 rows 35.1 /
+// 34.3 / 34.4 / 35.1, 64 of 128 rows 184 / 176 / 172 / 168, a block of 224 rows over 32K 24.7 to 24.9.
 constexpr int kKv8PadRows = 3, kKv8PadTc = 7;
 constexpr int kKv8MaxCtas = 304;  // most attention CTAs (workspace slots)
 
