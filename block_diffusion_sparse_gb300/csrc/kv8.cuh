@@ -112,7 +112,7 @@ struct Kv8AttnArgs {
 };
 // The kernel for `rows` <= kKv8FewRows query rows per KV head (kv8_rows.cu).  It and the one
 // for more rows, in us over 64 sequences of up to 8K tokens / one of 128K / one of 32K (8 KV
-// heads, d = 128): 16 rows 103 / 48.8 / 16.3 here and 134 / 58 / 22 there.  Its softmax keeps a
+// heads, d = 128): 16 rows 103 / 48.8 / 16.3 here and 129 / 57.7 / 22.3 there.  Its softmax keeps a
 // row of a key in two registers and more: with 32 rows they would spill (a form of it measured
 // 269 / 102 / 53, the other kernel 134 / 58.5 / 22.3).
 constexpr int kKv8FewRows = 16;
