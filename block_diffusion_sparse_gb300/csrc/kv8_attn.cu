@@ -345,7 +345,8 @@ static Kv8Ws kv8_ws(const herald_dims& dm) {
   const size_t slots = size_t(kKv8MaxCtas) + size_t(dm.N) * dm.Hkv * w.row_tiles;
   w.ml = 256;
   w.opart = align_up(w.ml + slots * w.R16 * 8, 256);
-  w.total = w.opart + slots * w.R16 * size_t(dm.d) * 4;
+  // (O is written by 32 bytes; the workspace itself may be aligned to 16)
+  w.total = w.opart + slots * w.R16 * size_t(dm.d) * 4 + 16;
   return w;
 }
 size_t kv8_attn_workspace(const herald_dims& dm) { return kv8_ws(dm).total; }
@@ -359,7 +360,7 @@ cudaError_t launch_kv8_attn(const herald_dims& dm, const uint16_t* q, const Kv8D
   Kv8AttnArgs a{};
   a.q = q, a.bk = bk, a.bv = bv, a.ctx = ctx, a.out = out;
   a.ml = reinterpret_cast<float2*>(p + w.ml);
-  a.opart = reinterpret_cast<float*>(p + w.opart);
+  a.opart = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(p + w.opart) + 31) & ~uintptr_t(31));
   a.scale = scale * 1.4426950408889634f;
   a.N = dm.N, a.Hq = dm.Hq, a.Hkv = dm.Hkv, a.B = dm.B, a.L_max = dm.L_max;
   a.R16 = w.R16, a.row_tiles = w.row_tiles;

@@ -121,3 +121,26 @@ def test_gather_layouts(d, P, values, shift):
         assert np.array_equal(kv4_ref.f64(bits(pools[i])), want)
     if not values:
         assert (pools[1] == 7).all()
+
+
+@pytest.mark.parametrize("d,B", [(128, 1), (64, 4), (128, 9), (64, 40)])
+@pytest.mark.parametrize("shift", [0, 16])
+def test_workspace_of_16_bytes_alignment(d, B, shift):
+    """A workspace of exactly the size asked for, aligned to 16 bytes only: the same results, and
+    nothing beside it is written."""
+    H = _h()
+    rng = np.random.default_rng(d + B)
+    N, Hq, Hkv, page = 3, 8, 2, 64
+    lengths = [3000, 0, 700]
+    c = make_cache(rng, N, Hkv, d, page, 32, lengths)
+    q = kv4_ref.bf16(rng.standard_normal((N, B, Hq, d)))
+    bk, bv = (kv4_ref.bf16(rng.standard_normal((N, B, Hkv, d))) for _ in range(2))
+    size = H.herald_workspace_size_kv8(H.dims(N, Hq, Hkv, d, B, 3000))
+    room = torch.full((size + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+    ws = room[16 + shift:16 + shift + size]
+    ws[:4] = 0  # (the error word)
+    got = run_attn(c, q, lengths, B, 3000, bk, bv, ws=ws)
+    want, tol = ref.attention(q, c, lengths, bk, bv)
+    check(got, want, tol, "16-byte workspace")
+    assert (room[:16 + shift] == 0x5A).all() and (room[16 + shift + size:] == 0x5A).all()
+    assert np.array_equal(got, run_attn(c, q, lengths, B, 3000, bk, bv))
