@@ -5,6 +5,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "kv8.cuh"
 
 namespace herald {
@@ -35,12 +37,27 @@ HERALD_DEV void load_run(const uint16_t* p, bool on, uint32_t (&w)[Words]) {
   }
 }
 
+// Whether one of two bf16 is an infinity or a NaN shows in a sum of 0 * x: t stays 0 (of
+// either sign) as long as none is.
+HERALD_DEV uint32_t zero_times(uint32_t w, uint32_t t) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(t) : "r"(w), "r"(0u));
+  return t;
+}
+HERALD_DEV uint32_t finite_or_zero(uint32_t w) {  // (of two bf16)
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+  return w;
+}
+
 // The block's own keys in the join: up to kOwnWarps warps take 16 keys at a time, for 16
 // query rows (mma m16n8k16 of bf16, fp32 sums; P as two bf16 numbers, take_bf16), and
 // leave (m, l, O) in shared memory.  The contraction's channels may stand in any order
 // that both operands share, so a lane's share of a row is a run of channels: q and k
 // [t D/4, (t+1) D/4) of lane t = lane%4, v [g D/8, (g+1) D/8) of lane group g = lane/4,
 // whose n-th channel goes to column g of the product's n-th tile.
+// A weight's second number may be 0 or negative, and times an infinite value that is a NaN or
+// the other infinity where the weight times it is not: infinities and NaNs are left to
+// the first number alone (positive, or 0 where the weight is).
 constexpr int kOwnWarps = 4;
 template <int D>
 struct OwnKeys {
@@ -113,32 +130,46 @@ HERALD_DEV void own_keys(const Kv8AttnArgs& a, OwnKeys<D>& sm, int n, int g, int
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 2; ++i) p[part][2 * h + i] = take_bf16(s[h][2 * i], s[h][2 * i + 1]);
+    uint32_t t = 0;
 #pragma unroll
-    for (int c = 0; c < VW; c += 2) {  // four channels of a run: four tiles
-      float o[4][4];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = c + j / 2;
-        const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-        const uint32_t b0 = __byte_perm(v[0][i], v[1][i], sel), b1 = __byte_perm(v[2][i], v[3][i], sel);
+      for (int j = 0; j < VW; ++j) t = zero_times(v[i][j], t);
+    const bool odd = __any_sync(0xffffffffu, (t & 0x7FFF7FFFu) != 0);
+    auto values = [&](auto odd_c) {
+      constexpr bool Odd = decltype(odd_c)::value;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-        join_mma(o[j], p[0][0], p[0][1], p[0][2], p[0][3], b0, b1);
-        join_mma(o[j], p[1][0], p[1][1], p[1][2], p[1][3], b0, b1);
-      }
+      for (int c = 0; c < VW; c += 2) {  // four channels of a run: four tiles
+        float o[4][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {  // row lg + 8 (e >> 1), run 2 lt + (e & 1)
-        const int ch = (2 * lt + (e & 1)) * (D / 8) + 2 * c;
-        float4* dst = reinterpret_cast<float4*>(&sm.o[warp][lg + 8 * (e >> 1)][ch + ch / 32 * 4]);
-        float4 x = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
-        if (k0 >= kOwnWarps * 16) {
-          const float4 y = *dst;
-          const float w = f[e >> 1];
-          x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y), x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
+        for (int j = 0; j < 4; ++j) {
+          const int i = c + j / 2;
+          const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+          uint32_t b0 = __byte_perm(v[0][i], v[1][i], sel), b1 = __byte_perm(v[2][i], v[3][i], sel);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+          join_mma(o[j], p[0][0], p[0][1], p[0][2], p[0][3], b0, b1);
+          if constexpr (Odd) b0 = finite_or_zero(b0), b1 = finite_or_zero(b1);
+          join_mma(o[j], p[1][0], p[1][1], p[1][2], p[1][3], b0, b1);
         }
-        *dst = x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // row lg + 8 (e >> 1), run 2 lt + (e & 1)
+          const int ch = (2 * lt + (e & 1)) * (D / 8) + 2 * c;
+          float4* dst = reinterpret_cast<float4*>(&sm.o[warp][lg + 8 * (e >> 1)][ch + ch / 32 * 4]);
+          float4 x = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
+          if (k0 >= kOwnWarps * 16) {
+            const float4 y = *dst;
+            const float w = f[e >> 1];
+            x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y), x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
+          }
+          *dst = x;
+        }
       }
-    }
+    };
+    if (odd)
+      values(std::true_type{});
+    else
+      values(std::false_type{});
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
