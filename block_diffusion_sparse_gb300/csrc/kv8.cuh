@@ -54,13 +54,20 @@ HERALD_DEV uint32_t float2_to_e4m3(float lo, float hi) {
 // A query row as e4m3 numbers: values are multiplied by *up, the power of two that
 // brings the row's largest magnitude mx to [2^7, 2^8), and *f turns a product with a
 // key's codes into a log2-unit score (`scale` has log2(e) in it).  (mx below 2^-112
-// counts as that; with an infinity *up is a NaN, as inf - inf makes the row; *f stays
-// positive and finite, also times a key's scale: a zero score times inf would be NaN.)
+// counts as that; with an infinity *up is a NaN, as inf - inf makes the row.)
+// *f times a key's scale, 2^-32 to 2^32, must not be 0 or infinite: a masked -inf times 0
+// and a zero score times inf would be NaN.  Below 2^-94 *f counts as that (scores are then
+// under 2^-38: 2^8 * 448 * 128 channels); the other end is the product's, not *f's
+// (kv8_score_factor): with *f held to 2^90 for it, the cache's scores past that shrank
+// beside those of the block's own keys.  2^127 is a row's largest value times the scale of 2^133.
 HERALD_DEV void kv8_query_scale(float mx, float scale, float* up, float* f) {
   const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -112), 127);
   *up = mx < INFINITY ? exp2_int(7 - e) : __uint_as_float(0x7FC00000u);
-  *f = fminf(fmaxf(scale * exp2_int(e - 7), 0x1p-90f), 0x1p90f);
+  *f = fminf(fmaxf(scale * exp2_int(e - 7), 0x1p-94f), 0x1p127f);
 }
+// *f times a key's scale sk, finite.  (Past 2^127 any product of codes but the smallest
+// scores past fp32.)
+HERALD_DEV float kv8_score_factor(float f, float sk) { return fminf(f * sk, 0x1p127f); }
 // One lane of a converged warp, the same every time: what it alone issues keeps its
 // operands in uniform registers (with `lane == 0` each mma moved them there anew).
 HERALD_DEV bool elect_one() {

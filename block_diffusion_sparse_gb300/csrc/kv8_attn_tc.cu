@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(kKv8TcThreads, 1)
           }
           float fk[4], ev[4], iv[4];  // P = 2^(score fk + ev - m)
           {
-            fk[0] = f * a4.x, fk[1] = f * a4.y, fk[2] = f * a4.z, fk[3] = f * a4.w;
+            fk[0] = kv8_score_factor(f, a4.x), fk[1] = kv8_score_factor(f, a4.y);
+            fk[2] = kv8_score_factor(f, a4.z), fk[3] = kv8_score_factor(f, a4.w);
             ev[0] = b4.x, ev[1] = b4.y, ev[2] = b4.z, ev[3] = b4.w;
             iv[0] = c4.x, iv[1] = c4.y, iv[2] = c4.z, iv[3] = c4.w;
           }

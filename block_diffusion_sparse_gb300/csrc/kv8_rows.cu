@@ -313,13 +313,15 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
         {
           float x[NS];
           tmem_load<NS>(tm + lanes + t % SB * NS, x);
+          // (times the key's scale, an exact step, before the row's factor: the two factors'
+          // product might leave fp32 where the score does not)
 #pragma unroll
-          for (int r = 0; r < RP; ++r) s[r] = fmaf(x[RP + r], 0.0625f, x[r]);
+          for (int r = 0; r < RP; ++r) s[r] = fmaf(x[RP + r], 0.0625f, x[r]) * mt.sk;
         }
         bool move = false;
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          p[r] = on ? fmaf(s[r], f[r] * mt.sk, mt.ev - m[r]) : -INFINITY;
+          p[r] = on ? fmaf(s[r], f[r], mt.ev - m[r]) : -INFINITY;
           move |= p[r] > kKv8Most;
         }
         move = soft_any(w, move);
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
           float z[RP];
 #pragma unroll
           for (int r = 0; r < RP; ++r)
-            z[r] = on ? __fadd_rd(__fmul_rd(s[r], f[r] * mt.sk), mt.ev) : -INFINITY;
+            z[r] = on ? __fadd_rd(__fmul_rd(s[r], f[r]), mt.ev) : -INFINITY;
           const float mx = warp_rows(z, [](float x, float y) { return fmaxf(x, y); });
           if (lane < RP) red[w][wq][lane] = mx;
           soft_bar(w);
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
             k[r] = fast_exp2(m[r] - m1);
             m[r] = m1;
             l[r] *= k[r];
-            const float x = fmaf(s[r], f[r] * mt.sk, mt.ev - m1);
+            const float x = fmaf(s[r], f[r], mt.ev - m1);
             p[r] = !on ? -INFINITY : x > kKv8Most ? kKv8Most : x;  // (a NaN stays)
           }
           if (t > mine) {

@@ -641,6 +641,9 @@ herald_status herald_kv8_append(herald_dims dims, int T, const int32_t *n_tok, c
 /* Full attention of a block's queries over a paged 8-bit cache, and where given
  * the block's own B keys in bf16: herald_kv4_attn with a herald_kv8.
  *   out      may not lie, even in part, over q, block_k or block_v
+ *   scale    with it a query row's largest value is at most 2^133, and scores times log2(e)
+ *            are within fp32: larger ones are not told apart over the cache and are NaN
+ *            over the block's own keys
  *   ws       herald_workspace_size_kv8(dims) bytes (0 = unsupported shape)
  * Scores, sums and partial outputs are fp32.  A query value enters as the sum of
  * two e4m3 numbers times its row's power of two (off by at most 2^-17 of the row's
