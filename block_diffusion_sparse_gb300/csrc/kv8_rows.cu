@@ -11,11 +11,15 @@
 // The other operands are made e4m3 too, without losing their bits, as sums of numbers
 // of 4 bits in columns of their own:
 //   q = (q0 + q1/16) 2^x: a bf16 has 8 bits; x brings the row's largest to [2^7, 2^8)
-//   p = p0 + p1/16 + p2/256 + p3/4096 (kKv8Parts), with p at most 2^8
+//   p = p0 + p1/2^5 + p2/2^10 + p3/2^15 (kKv8Parts), with p at most 2^8: what a number leaves
+//   is then at most 2^3, and 2^5 times that 2^8 again; the last one's step is 2^-24 (with
+//   steps of 2^4 between them it was 2^-21, and weights of 2^-26 of a row's largest and less,
+//   many of which may make its output beside a sink without value, were 0)
 // and the columns are added in fp32 afterwards.  A key's scale (its block's) multiplies its
 // scores.  A value's exponent e_v goes into the weight's own, p = 2^(x + e_v - m), and
-// out of the row's sum again, l += p 2^-e_v: O has one unit, and weights keep their bits
-// whatever their values' scales.
+// out of the row's sum again, l += p 2^-e_v: O has one unit.  p's steps end at 2^-24, where
+// a row's largest p is 2^4 at least: keys 2^-29 and less below it (values of so small a
+// scale, or weights) count in the sum only.
 //
 // One CTA per SM walks its share of the keys (kv4_split):
 //   warps 0-3, 4-7  softmax: two streams that take the tiles in turn, a thread per key of
@@ -79,13 +83,13 @@ struct __align__(16) Kv8Meta {
   int keys;
 };
 
-// x -> 16 (x - e4m3(x)) for a pair, returning the codes: what the next number holds.
+// x -> 32 (x - e4m3(x)) for a pair, returning the codes: what the next number holds.
 HERALD_DEV uint32_t split_e4m3(float& a, float& b) {
   const uint32_t w = float2_to_e4m3(a, b);
   const uint32_t h = e4m3x2_to_half2(w);
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  a = fmaf(f.x, -16.f, a * 16.f);
-  b = fmaf(f.y, -16.f, b * 16.f);
+  a = fmaf(f.x, -32.f, a * 32.f);
+  b = fmaf(f.y, -32.f, b * 32.f);
   return w;
 }
 
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(kKv8RowsThreads, 1)
           for (int r = 0; r < RH; ++r) {
             float y = 0.f;
 #pragma unroll
-            for (int i = kKv8Parts - 1; i >= 0; --i) y = fmaf(y, 0.0625f, __uint_as_float(o[i][r]));
+            for (int i = kKv8Parts - 1; i >= 0; --i) y = fmaf(y, 0.03125f, __uint_as_float(o[i][r]));
             x[r] = fmaf(y, h ? w1[r] : w0[r], x[r]);
           }
         }

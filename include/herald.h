@@ -650,7 +650,10 @@ herald_status herald_kv8_append(herald_dims dims, int T, const int32_t *n_tok, c
  * largest value, 2^-21 with up to 16 query rows per KV head), a weight over the
  * cache as one fp16 number (with up to 16 rows four e4m3 ones), a weight over the
  * block's own keys as an fp32 or the sum of two bf16 numbers, and the output is
- * rounded to bf16.  Infinities and NaNs in block_k and block_v give what the formula
+ * rounded to bf16.  Weights over the cache end at a step: a weight times its value's
+ * scale is held to 2^-29 (with up to 16 rows 2^-28) of the row's largest such product
+ * among the keys of a share of the cache, and under half of that counts in the row's sum
+ * only.  Infinities and NaNs in block_k and block_v give what the formula
  * gives (a weight below 2^-126 counts as 0, and 0 * inf is a NaN). */
 size_t herald_workspace_size_kv8(herald_dims dims);
 herald_status herald_kv8_attn(herald_dims dims, const uint16_t *q, const herald_kv8 *cache,
