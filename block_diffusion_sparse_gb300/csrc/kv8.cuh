@@ -119,9 +119,10 @@ struct Kv8AttnArgs {
 };
 // The kernel for `rows` <= kKv8FewRows query rows per KV head (kv8_rows.cu).  It and the one
 // for more rows, in us over 64 sequences of up to 8K tokens / one of 128K / one of 32K (8 KV
-// heads, d = 128): 16 rows 103 / 48.8 / 16.3 here and 129 / 57.7 / 22.3 there.  Its softmax keeps a
-// row of a key in two registers and more: with 32 rows they would spill (a form of it measured
-// 269 / 102 / 53, the other kernel 134 / 58.5 / 22.3).
+// heads, d = 128): 16 rows 103 / 48.8 / 16.3 here and 129 / 57.7 / 22.3 there, a form of it for 32
+// rows 269 / 102 / 53 and the other kernel 134 / 58.5 / 22.3.  Its softmax keeps a row of a key in
+// two registers and more: with 16 rows all 168 that 384 threads can have are in use and 72 bytes
+// are spilled (64 with d = 64), with 8 rows 121 to 123 and none.
 constexpr int kKv8FewRows = 16;
 cudaError_t launch_kv8_rows(int d, int rows, const Kv8AttnArgs& a, const CUtensorMap& kmap,
                             const CUtensorMap& vmap, uint32_t* err, cudaStream_t st);

@@ -6,8 +6,8 @@
 //   S [128 rows x 128 keys] = Q K^T    kind::f8f6f4: K's codes as they are held, Q in
 //                                      tensor memory as two e4m3 numbers a value, q0 +
 //                                      q1 (a bf16 has 8 bits, e4m3 4), one product each
-//   O [128 rows x d]       += P V      kind::f16: P fp16 in tensor memory over the
-//                                      scores, V's codes turned into fp16 (exact)
+//   O [128 rows x d]       += P V      kind::f16: P fp16 in tensor memory, V's codes
+//                                      turned into fp16 (exact)
 // (P as e4m3 numbers, V as it is held, would take no conversion of V, 450 warp
 // instructions a tile, but splitting 128 x 128 weights takes some 1500 more than
 // packing them.)  Q in tensor memory keeps 64 KB a tile off shared memory, whose
@@ -27,11 +27,18 @@
 // before it: 1,800 cycles a tile.)
 // Scales: a key's multiplies its scores.  A value's exponent e_v goes into the weight's
 // own, P = 2^(x + e_v - m), and out of the row's sum again, l += P 2^-e_v, so O has one
-// unit and P fills fp16 whatever the values' scales.
+// unit and P fills fp16 whatever the values' scales.  fp16 ends at 2^-24, where a row's largest
+// P is 2^5 at least: keys 2^-30 and less below it (values of so small a scale, or
+// weights) count in the sum only.
 //
 // P = 2^(x + e_v - m) stays in fp16 as long as a step's 64 of them sum to less than
 // 60000.  Where a sum does not (and at a piece's first step) the row's largest exponent
 // is looked up, m set 5 below it, O and l follow, and the step is done again.
+//
+// fp16 rounds a weight by at most 2^-11 of it.  That shows in an output's last bf16 place now
+// and then (block over 32K: 8e-4 of the outputs' norm beside the same in fp32) and not beside
+// the output's own rounding (1.7e-3 from the exact values either way).  A second number a weight
+// would take half as many products again and columns of tensor memory that d = 128 lacks.
 //
 // What bounds it: the dependent steps of a stream's warp, some 1,950 cycles a tile (scores
 // from tensor memory 400, exponentials and packing 950, waiting for products 250, P to tensor

@@ -106,9 +106,9 @@ HERALD_DEV uint4 shfl4(const uint4& x, int src) {
 // warp's (all loads first), so block/16 warps share a unit and its maximum.  Where
 // the first block holds older rows and its scale grows, the same warps hold those
 // anew.  A CTA has the units of neighbouring heads: rows of a token lie side by side.
-// (Registers: the half-split form has twice the angles; with 64 instead of 84 a lane it takes
-// 14.0 us for 1024 tokens instead of 12.5, the other with 84 instead of 64 64 us for the
-// prompts instead of 61.)
+// (Registers: the half-split form has twice the angles; with four CTAs an SM, 64 registers a
+// lane, it takes 14.0 us for 1024 tokens instead of 12.5 with three, 80 (79 used); the other
+// with three 64 us for the prompts of 4 x 4096 instead of 61 with four.)
 template <int D, bool Interleaved>
 __global__ void __launch_bounds__(kKv8MoveThreads, Interleaved ? 4 : 3)
     kv8_append_kernel(const Kv8AppendArgs a) {

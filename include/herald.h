@@ -576,6 +576,7 @@ herald_status herald_kv4_append(herald_dims dims, int T, const int32_t *n_tok, c
  *   ws       herald_workspace_size_kv4(dims) bytes (0 = unsupported shape)
  * Scores, sums and partial outputs are fp32; a weight is rounded to fp16 (11 bits)
  * over the cache and to 16 bits over the block's own keys, the output to bf16.
+ * Values of the block have to be finite (an infinite one may give a NaN).
  * N*Hkv <= 65535, L_max <= 2^30.  Results do not depend on other calls or on timing. */
 size_t herald_workspace_size_kv4(herald_dims dims);
 herald_status herald_kv4_attn(herald_dims dims, const uint16_t *q, const herald_kv4 *cache,
@@ -628,7 +629,9 @@ typedef struct {
  *   older rows of the block, where e grew: code = e4m3(code 2^(old e - e))
  * so the held bytes are defined to the bit.  Rows before ctx_len[n] in the
  * block that token 0 falls into must have been appended before; rows after the
- * tokens keep their bytes.
+ * tokens keep their bytes.  Unlike herald_kv4_append the call may rewrite those
+ * older rows, codes and scale: nothing may read that block -- attention, a gather,
+ * on another stream or of another sequence -- while it runs.
  *   pooled   as there: the means of the rows as held, refreshed for the blocks of
  *            Bk that the tokens fall into (other blocks' means stay, also where
  *            their rows are held anew) */
