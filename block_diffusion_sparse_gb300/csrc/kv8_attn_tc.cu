@@ -43,7 +43,7 @@
 // What bounds it: the dependent steps of a stream's warp, some 1,950 cycles a tile (scores
 // from tensor memory 400, exponentials and packing 950, waiting for products 250, P to tensor
 // memory 350); the tensor pipe is active 53% and DRAM 62% of the time.  Four blocks of 32 over
-// 64K tokens each, 32 heads over 8: 107 us for 539 MB; one over 32K, 28 heads over 4, 24.4 us,
+// 64K tokens each, 32 heads over 8: 109 us for 539 MB; one over 32K, 28 heads over 4, 24.9 us,
 // half of it phases that do not grow with the keys (share 0.8 us, queries 2.6, first scores 0.6,
 // partials 1.5, join 3).  S and P V from one warp a stream, so that a stream waits once a step:
 // 25.2 to 24.9 us for the latter.
